@@ -204,7 +204,7 @@ def _own(s, c):
         kw = dict(ref_logp=s["ref"], entropy=s["entropy"], cu_seqlens=s["cu"], clip_low=0.2, clip_high=0.25,
                   dual_clip=c["dual"], kl_weight=0.0 if c["kl"] == "none" else 0.05,
                   kl_kind="k3" if c["kl"] == "none" else c["kl"], entropy_weight=0.01 if c["entropy"] else 0.0,
-                  reduction=c["reduction"])
+                  reduction=c["reduction"], per_sequence=c["per_seq"])
         if c["autograd"]:
             loss, stats = kd.policy_loss(s["logp"], s["old"], s["adv"], s["mask"], **kw)
             return dict(stats=stats, dlogp=torch.autograd.grad(loss, s["logp"])[0])
