@@ -26,6 +26,13 @@ from ._binding import (  # noqa: F401
     kd_topk_kl_shard_workspace_size, kd_topk_kl_fwd_shard, kd_topk_kl_shard_combine, kd_topk_kl_bwd_shard,
     kd_full_kl_fwd_shard, kd_full_kl_shard_combine, kd_full_kl_bwd_shard,
 )
+from ._policy_binding import POLICY_EXPORTS  # noqa: F401
+from .policy import (  # noqa: F401
+    clip_grad_norm, clip_grad_norm_, grad_sumsq, policy_loss, policy_loss_backward, policy_loss_forward,
+    policy_loss_forward_backward, preference_loss, preference_loss_backward, preference_loss_forward,
+    preference_loss_forward_backward, token_logp, token_logp_backward, token_logp_forward, token_logp_shard_backward,
+    token_logp_shard_combine, token_logp_shard_forward,
+)
 
 __all__ = [
     "topk_kl", "full_kl", "topk_kl_forward", "topk_kl_backward", "topk_kl_forward_backward", "full_kl_forward",
@@ -39,6 +46,10 @@ __all__ = [
     "kd_topk_kl_fwd_shard", "kd_topk_kl_shard_combine", "kd_topk_kl_bwd_shard",
     "full_kl_shard_forward", "full_kl_shard_combine", "full_kl_shard_backward", "kd_full_kl_fwd_shard",
     "kd_full_kl_shard_combine", "kd_full_kl_bwd_shard",
+    "token_logp", "token_logp_forward", "token_logp_backward", "token_logp_shard_forward", "token_logp_shard_combine",
+    "token_logp_shard_backward", "policy_loss", "policy_loss_forward", "policy_loss_backward",
+    "policy_loss_forward_backward", "preference_loss", "preference_loss_forward", "preference_loss_backward",
+    "preference_loss_forward_backward", "grad_sumsq", "clip_grad_norm", "clip_grad_norm_",
 ]
 
 

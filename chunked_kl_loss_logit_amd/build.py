@@ -78,30 +78,30 @@ def build(verbose: bool = False) -> str:
 # The host code of the C ABI (argument checks, workspace planning, launch
 # sequences) compiled with the address and undefined-behaviour sanitizers,
 # linked with the uninstrumented kernels and a driver that runs the ABI's
-# rejection and workspace-size cases on the CPU (tests/host/abi_driver.cpp).
+# rejection and workspace-size cases on the CPU (tests/host/*_driver.cpp).
 ASAN_DIR = os.path.join(BUILD, "host_sanitizers")
 ASAN_HOST = ["-Xarch_host", "-fsanitize=address", "-Xarch_host", "-fsanitize=undefined",
              "-Xarch_host", "-fno-sanitize-recover=undefined", "-Xarch_host", "-fno-omit-frame-pointer"]
 
 
-def build_host_sanitizer_driver() -> str:
-    """Build the sanitizer-instrumented ABI driver; returns its path.  Needs
+def build_host_sanitizer_driver(name: str = "abi_driver") -> str:
+    """Build a sanitizer-instrumented ABI driver; returns its path.  Needs
     the kernels' objects of a regular build (build() makes them)."""
     os.makedirs(ASAN_DIR, exist_ok=True)
-    api = os.path.join(CSRC, "kd_api.cpp")
+    apis = [s for s in sources() if s.endswith(".cpp")]
     kernels = [os.path.join(BUILD, os.path.basename(s) + ".o") for s in sources() if s.endswith(".hip")]
     missing = [k for k in kernels if not os.path.exists(k)]
     if missing:
         build()
-    api_o = os.path.join(ASAN_DIR, "kd_api.o")
-    drv_src = os.path.join(ROOT, "tests", "host", "abi_driver.cpp")
-    drv_o = os.path.join(ASAN_DIR, "abi_driver.o")
-    exe = os.path.join(ASAN_DIR, "abi_driver")
+    api_os = [os.path.join(ASAN_DIR, os.path.basename(a) + ".o") for a in apis]
+    drv_src = os.path.join(ROOT, "tests", "host", name + ".cpp")
+    drv_o = os.path.join(ASAN_DIR, name + ".o")
+    exe = os.path.join(ASAN_DIR, name)
     flags = [f for f in _flags() if f != "-O3"] + ["-O1", "-g"]
     steps = [
-        [_hipcc(), "-xhip", *flags, *ASAN_HOST, "-c", api, "-o", api_o],
+        *([_hipcc(), "-xhip", *flags, *ASAN_HOST, "-c", a, "-o", o] for a, o in zip(apis, api_os)),
         [_hipcc(), *flags, *ASAN_HOST, "-c", drv_src, "-o", drv_o],
-        [_hipcc(), f"--offload-arch={ARCH}", *ASAN_HOST, "-o", exe, drv_o, api_o, *kernels],
+        [_hipcc(), f"--offload-arch={ARCH}", *ASAN_HOST, "-o", exe, drv_o, *api_os, *kernels],
     ]
     for cmd in steps:
         r = subprocess.run(cmd, capture_output=True, text=True)

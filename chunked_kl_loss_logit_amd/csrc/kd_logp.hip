@@ -1,0 +1,585 @@
+// Token log-probabilities through the output head, their entropy and dZ.
+//
+//   s = z / tau with z = H_t . W, L_t = logsumexp(s), q = softmax(s)
+//   logp_t = s[y_t] - L_t           ent_t = L_t - sum_v q_v s_v
+//   dZ_t   = (1/tau) (g_t [v = y_t] - q_v (g_t + e_t (ent_t + log q_v)))
+//
+// Grid: (256 valid rows) x (vocabulary split).  A workgroup walks the
+// 256-column tiles of its split; the tile's products are accumulated
+// transposed (mma_frags_t), so a lane holds 64 columns of each of four rows
+// and both epilogues work in registers.
+//   forward: per lane and row a running (m, l, e): m the maximum of y = s
+//     log2(e), l = sum 2^(y - m), e = sum 2^(y - m) (y - m).  e is kept
+//     relative to the maximum, so the entropy ln2 (log2 l - e / l) is a
+//     difference of small numbers whatever the size of the logits.  Moving
+//     the maximum by dm <= 0 (old minus new) scales: l' = l 2^dm,
+//     e' = (e + dm l) 2^dm.
+//   backward: each register becomes its dZ.
+// The tile contraction (2 T d V flops) bounds both; without the entropy the
+// extra terms are compiled out.
+#include "kd_gemm.h"
+#include "kd_main.h"
+#include "kd_policy.h"
+
+namespace kd {
+
+namespace {
+
+constexpr int kBN = kTileN;
+constexpr int kStgBytes = 2048;       // per wave: 32 rows x 64 bytes of bf16 dZ
+constexpr int kFstWords = 4 * 4 * 64;  // per wave: (m, l, e, x) of 4 rows x 64 lanes
+
+__device__ inline int tile_n0(int vt, int V) { return V >= kBN ? min(vt * kBN, V - kBN) : 0; }
+
+// Byte position of 8 bytes (half hh of 16-byte chunk j) of row r in a wave's
+// [32][64 B] staging region: chunk and half XOR-swizzled, so the 32 rows that
+// a half-wave writes at once land in distinct bank groups, and so do the
+// 4 x 4 chunks a quarter-wave reads back.
+__device__ inline int stg8(int r, int j, int hh) {
+  return r * 64 + ((j ^ ((r >> 2) & 3)) << 4) + ((hh ^ ((r >> 4) & 1)) << 3);
+}
+
+typedef float f32x2_t __attribute__((ext_vector_type(2)));
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+__device__ inline uint32_t pk_bf16(float lo, float hi) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{lo, hi}, bf16x2_t));
+}
+
+// (m, l, e) parts of one row over two column sets, merged; m = -inf: nothing yet
+template <bool kEnt>
+__device__ inline void merge(float& m, float& l, float& e, float om, float ol, float oe) {
+  const float M = fmaxf(m, om);
+  const float d = m - M, od = om - M;
+  const float f = m == -INFINITY ? 0.f : fast_exp2(d), of = om == -INFINITY ? 0.f : fast_exp2(od);
+  if constexpr (kEnt)
+    e = (m == -INFINITY ? 0.f : f * fmaf(d, l, e)) + (om == -INFINITY ? 0.f : of * fmaf(od, ol, oe));
+  l = l * f + ol * of;
+  m = M;
+}
+
+// One row's update from the lane's 64 values of the tile (register i of
+// block nb: column base + 32 nb + 8 (i / 4) + 4 h + i % 4).  Columns outside
+// [lo, hi) (multiples of 4) are left out unless kFull.
+template <bool kEnt, bool kFull>
+__device__ inline void fwd_row(const f32x16_t (&v)[4], float c2, float* st, int label, int base, int lo, int hi) {
+  const int h = (opaque((int)threadIdx.x) >> 5) & 1;
+  float m = st[0], l = st[64];
+  auto in = [&](int nb, int i) {
+    const int col = base + 32 * nb + 8 * (i >> 2) + 4 * h;
+    return kFull || (col >= lo && col < hi);
+  };
+  float cm = -INFINITY;
+#pragma unroll
+  for (int nb = 0; nb < 4; ++nb)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) cm = in(nb, i) ? fmaxf(cm, v[nb][i]) : cm;
+  const float cmy = cm * c2;
+  float e = 0.f;
+  if constexpr (kEnt) e = st[128];
+  if (cmy > m) {
+    const float f = fast_exp2(m - cmy);  // 2^(-inf) = 0 while nothing is summed yet
+    if constexpr (kEnt) e = l == 0.f ? 0.f : f * fmaf(m - cmy, l, e);
+    l *= f;
+    m = cmy;
+  }
+  float sum = 0.f, es = 0.f;
+#pragma unroll
+  for (int nb = 0; nb < 4; ++nb)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float w = in(nb, i) ? fmaf(v[nb][i], c2, -m) : -1e30f;
+      const float p = fast_exp2(w);
+      sum += p;
+      if constexpr (kEnt) es = fmaf(p, w, es);
+    }
+  st[0] = m;
+  st[64] = l + sum;
+  if constexpr (kEnt) st[128] = e + es;
+  const int dc = label - base;
+  if ((unsigned)dc < 128u && label >= lo && label < hi && ((dc >> 2) & 1) == h) {
+    const int nbl = dc >> 5, at = ((dc >> 3 & 3) << 2) | (dc & 3);
+    float z = 0.f;
+#pragma unroll
+    for (int nb = 0; nb < 4; ++nb)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) z = nb == nbl && i == at ? v[nb][i] : z;
+    st[192] = z;
+  }
+}
+
+// The tile's raw logits of one row (the columns of [lo, hi)), fp32, 16 bytes per store.
+template <int NB, int J>
+__device__ inline void zout4(const f32x16_t (&acc)[4], float* zr, int base, int lo, int hi, int h) {
+  const int col = base + 32 * NB + 8 * J + 4 * h;
+  if (col >= lo && col < hi)
+    *reinterpret_cast<f32x4_t*>(zr + col) =
+        __builtin_shufflevector(acc[NB], acc[NB], 4 * J, 4 * J + 1, 4 * J + 2, 4 * J + 3);
+}
+template <int NB>
+__device__ inline void zout_nb(const f32x16_t (&acc)[4], float* zr, int base, int lo, int hi, int h) {
+  zout4<NB, 0>(acc, zr, base, lo, hi, h);
+  zout4<NB, 1>(acc, zr, base, lo, hi, h);
+  zout4<NB, 2>(acc, zr, base, lo, hi, h);
+  zout4<NB, 3>(acc, zr, base, lo, hi, h);
+}
+
+}  // namespace
+
+// ------------------------------------------------------------------ forward tiles
+template <class Main, class E, bool kEnt, bool kOut>
+__global__ __launch_bounds__(kThreads, 1) void logp_fwd_kernel(LogpFwdArgs a) {
+  __shared__ __attribute__((aligned(16))) char sl_0[kSlotBytes];
+  __shared__ __attribute__((aligned(16))) char sl_1[kSlotBytes];
+  __shared__ __attribute__((aligned(16))) char sl_2[kSlotBytes];
+  __shared__ __attribute__((aligned(16))) char sl_3[kSlotBytes];
+  __shared__ float fst_all[4 * kFstWords];
+  __shared__ int labk[kBM];
+  const Slots sl{sl_0, sl_1, sl_2, sl_3, nullptr};
+
+  const long count = *a.c.count;
+  const long M = min(a.C, count - a.c0);  // valid rows of the chunk
+  if (M <= 0) return;
+  int rb, sp;
+  grouped_coords(xcd_remap(blockIdx.x, gridDim.x), a.nrb, a.S, a.group, rb, sp);
+  const int row0 = rb * kBM;
+  if (row0 >= M) return;
+  const int tb = (int)((long)a.ntiles * sp / a.S);
+  const int te = (int)((long)a.ntiles * (sp + 1) / a.S);
+  const int V = (int)a.V;
+
+  Main mainloop;
+  mainloop.init(
+      a.Hp, [&](int r) -> const char* { return row0 + r < M ? a.Hp + (row0 + r) * kRowB : nullptr; }, a.W,
+      a.V * E::kElem, a.V, a.d, a.C * kRowB);
+
+  const int w = wave_id(), wm = w >> 1, wn = w & 1;
+  const int lane = (int)threadIdx.x & 63;
+  const int trow0 = wm * 128;
+  float* fst = fst_all + w * kFstWords;
+#pragma unroll
+  for (int mb = 0; mb < 4; ++mb) {
+    const int ti = row0 + trow0 + mb * 32 + (lane & 31);
+    if (wn == 0 && lane < 32)
+      labk[trow0 + mb * 32 + lane] = ti < M ? (int)((long)a.tokens[a.c.rows[a.c0 + ti]] - a.v0) : -1;
+    fst[mb * 256 + lane] = -INFINITY;
+    fst[mb * 256 + 64 + lane] = 0.f;
+    fst[mb * 256 + 128 + lane] = 0.f;
+    fst[mb * 256 + 192 + lane] = 0.f;
+  }
+
+  mainloop.template run<true>(
+      sl, te - tb, [&](int i) { return TileAt{0, tile_n0(tb + i, V)}; },
+      [&](int i, const f32x16_t (&acc)[4][4]) {
+        const int vt = tb + i, n0 = tile_n0(vt, V), lo = vt * kBN, hi = min(lo + kBN, V);
+        const int base = n0 + wn * 128;
+        const bool full = n0 == lo && lo + kBN <= hi;
+        const int ln = opaque((int)threadIdx.x) & 63;
+        if constexpr (kOut) {
+          const int zr0 = opaque(row0 + trow0 + (ln & 31)), h = ln >> 5;
+          float* zp = a.zout + (long)zr0 * a.ldz;
+#pragma unroll
+          for (int mb = 0; mb < 4; ++mb)
+            if (zr0 + mb * 32 < M) {
+              float* zr = zp + (long)mb * 32 * a.ldz;
+              zout_nb<0>(acc[mb], zr, base, lo, hi, h);
+              zout_nb<1>(acc[mb], zr, base, lo, hi, h);
+              zout_nb<2>(acc[mb], zr, base, lo, hi, h);
+              zout_nb<3>(acc[mb], zr, base, lo, hi, h);
+            }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+        for (int mb = 0; mb < 4; ++mb) {
+          float* st = fst + mb * 256 + ln;
+          const int label = labk[trow0 + mb * 32 + (ln & 31)];
+          if (full)
+            fwd_row<kEnt, true>(acc[mb], a.c2, st, label, base, lo, hi);
+          else
+            fwd_row<kEnt, false>(acc[mb], a.c2, st, label, base, lo, hi);
+        }
+      });
+
+  // the split's record per row: lane halves, then column halves (wave wn = 1
+  // hands its part to wave wn = 0 through slot 0, free after the ring)
+  __syncthreads();
+  float4* xch = reinterpret_cast<float4*>(sl_0);
+#pragma unroll
+  for (int mb = 0; mb < 4; ++mb) {
+    float m = fst[mb * 256 + lane], l = fst[mb * 256 + 64 + lane], e = fst[mb * 256 + 128 + lane];
+    float x = fst[mb * 256 + 192 + lane];
+    const float om = __shfl_xor(m, 32), ol = __shfl_xor(l, 32), oe = __shfl_xor(e, 32), ox = __shfl_xor(x, 32);
+    if (lane < 32) merge<kEnt>(m, l, e, om, ol, oe);
+    x += ox;
+    if (wn == 1 && lane < 32) xch[trow0 + mb * 32 + lane] = make_float4(m, l, e, x);
+    fst[mb * 256 + lane] = m;
+    fst[mb * 256 + 64 + lane] = l;
+    fst[mb * 256 + 128 + lane] = e;
+    fst[mb * 256 + 192 + lane] = x;
+  }
+  __syncthreads();
+  if (wn == 0 && lane < 32) {
+#pragma unroll
+    for (int mb = 0; mb < 4; ++mb) {
+      const int ti = row0 + trow0 + mb * 32 + lane;
+      if (ti >= M) continue;
+      float m = fst[mb * 256 + lane], l = fst[mb * 256 + 64 + lane], e = fst[mb * 256 + 128 + lane];
+      const float4 o = xch[trow0 + mb * 32 + lane];
+      merge<kEnt>(m, l, e, o.x, o.y, o.z);
+      float4* dst = reinterpret_cast<float4*>(a.part) + (long)sp * a.C + ti;
+      *dst = make_float4(m, l, e, fst[mb * 256 + 192 + lane] + o.w);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ per-row outputs
+namespace {
+
+// S records at stride `stride`, merged in order.
+__device__ inline float4 merge_records(const float4* pp, int S, long stride) {
+  float M = -INFINITY;
+  for (int s = 0; s < S; ++s) M = fmaxf(M, pp[s * stride].x);
+  float l = 0.f, e = 0.f, x = 0.f;
+  for (int s = 0; s < S; ++s) {
+    const float4 q = pp[s * stride];
+    const float dm = q.x - M, f = exp2f(dm);
+    l = fmaf(q.y, f, l);
+    if (q.x != -INFINITY) e = fmaf(f, fmaf(dm, q.y, q.z), e);
+    x += q.w;
+  }
+  return make_float4(M, l, e, x);
+}
+
+// logp = ln2 ((y at the token - m) - log2 l): the maximum goes out first, so
+// only the small log2 l is subtracted from the row's distance to its maximum.
+__device__ inline void finish_row(long t, const float4 r, float c2, const LogpOut& o) {
+  const float ll = log2f(r.y);
+  o.logp[t] = kLn2 * (fmaf(r.w, c2, -r.x) - ll);
+  o.lse[t] = kLn2 * (r.x + ll);
+  if (o.entropy) o.entropy[t] = kLn2 * (ll - r.z / r.y);
+}
+
+__device__ inline void zero_row(long t, const LogpOut& o) {
+  if (o.rec) {
+    o.rec[t] = make_float4(0.f, 0.f, 0.f, 0.f);
+    return;
+  }
+  o.logp[t] = 0.f;
+  o.lse[t] = 0.f;
+  if (o.entropy) o.entropy[t] = 0.f;
+}
+
+}  // namespace
+
+__global__ __launch_bounds__(256) void logp_combine_kernel(const float4* part, int S, Compact c, const uint8_t* mask,
+                                                           const int32_t* tokens, long T, int V, long c0, long C,
+                                                           float c2, LogpOut o, int zero_masked) {
+  const long j = (long)blockIdx.x * blockDim.x + threadIdx.x;
+  if (zero_masked && j < T && mask != nullptr && mask[j] == 0) zero_row(j, o);
+  if (j >= min(C, (long)*c.count - c0)) return;
+  float4 r = merge_records(part + j, S, C);
+  const long t = c.rows[c0 + j];
+  if (o.rec) {
+    o.rec[t] = r;
+    return;
+  }
+  if ((uint32_t)tokens[t] >= (uint32_t)V) r.w = NAN;  // no such token: loud, not a plausible number
+  finish_row(t, r, c2, o);
+}
+
+hipError_t launch_logp_combine(const float* part, int S, Compact c, const uint8_t* mask, const int32_t* tokens,
+                               int64_t T, int64_t V, int64_t c0, int64_t C, float c2, const LogpOut& o,
+                               bool zero_masked, hipStream_t st) {
+  const int64_t n = zero_masked ? T : (T < C ? T : C);
+  hipLaunchKernelGGL(logp_combine_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st,
+                     reinterpret_cast<const float4*>(part), S, c, mask, tokens, (long)T, (int)V, (long)c0, (long)C, c2,
+                     o, zero_masked ? 1 : 0);
+  return hipGetLastError();
+}
+
+__global__ __launch_bounds__(256) void logp_shard_combine_kernel(const float4* rec, int R, long T, const uint8_t* mask,
+                                                                 float c2, LogpOut o) {
+  const long t = (long)blockIdx.x * blockDim.x + threadIdx.x;
+  if (t >= T) return;
+  if (mask != nullptr && mask[t] == 0) {
+    zero_row(t, o);
+    return;
+  }
+  finish_row(t, merge_records(rec + t, R, T), c2, o);
+}
+
+hipError_t launch_logp_shard_combine(const float4* rec, int R, int64_t T, const uint8_t* mask, float c2,
+                                     const LogpOut& o, hipStream_t st) {
+  hipLaunchKernelGGL(logp_shard_combine_kernel, dim3((unsigned)((T + 255) / 256)), dim3(256), 0, st, rec, R, (long)T,
+                     mask, c2, o);
+  return hipGetLastError();
+}
+
+// ------------------------------------------------------------------ dZ tiles
+namespace {
+
+// What dZ of a row needs: L2 = lse log2(e), A = ga + ge ent, B = ge ln2, ga,
+// c2 and the token's column.  Rows past the chunk's valid rows get zeros, c2
+// included, so whatever their products hold their dZ is 0.
+struct DzRow {
+  float4 k;  // (L2, A, B, ga)
+  float c2;
+  int label;
+};
+__device__ inline DzRow dz_row(const LogpDzArgs& a, bool rv, long t) {
+  DzRow r{make_float4(0.f, 0.f, 0.f, 0.f), 0.f, -1};
+  if (!rv) return r;
+  const float ga = a.g ? a.g[t] * a.inv_tau : 0.f;
+  const float gb = a.ge ? a.ge[t] * a.inv_tau : 0.f;
+  r.k = make_float4(a.lse[t] * kLog2e, a.ge ? fmaf(gb, a.ent[t], ga) : ga, gb * kLn2, ga);
+  r.c2 = a.c2;
+  r.label = (int)((long)a.tokens[t] - a.v0);
+  return r;
+}
+// -q (A + B log2 q)
+template <bool kEnt>
+__device__ inline float dz_value(float z, const float4 k, float c2) {
+  const float lq = fmaf(z, c2, -k.x);
+  const float q = fast_exp2(lq);
+  if constexpr (kEnt) return -q * fmaf(k.z, lq, k.y);
+  return -q * k.y;
+}
+
+// One 32 x 32 block: dZ of the lane's row at its 16 columns, to the chunk's
+// panels.  Columns from hi on are zero, columns below lo belong to the
+// previous tile and are not stored.  bf16 goes through a wave-private 2 KB
+// LDS region (LDS accesses of one wave complete in order: no barrier), so
+// that a store instruction writes 16 consecutive rows of one 64-byte piece;
+// fp32 is stored as it lies, 32 bytes of a piece per row.
+template <class E, bool kEnt, bool kFull>
+__device__ inline void dz_block(const f32x16_t& v, const float4 k, float c2, int label, int cb, int lo, int hi,
+                                char* stg, char* dz, long C, long brow0) {
+  const int lane = opaque((int)threadIdx.x) & 63, h = lane >> 5, cl = lane & 31;
+  float o[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const float e = dz_value<kEnt>(v[i], k, c2);
+    o[i] = kFull || cb + 8 * (i >> 2) + 4 * h < hi ? e : 0.f;
+  }
+  const int dc = label - cb;
+  if ((unsigned)dc < 32u && ((dc >> 2) & 1) == h) {
+    const int at = ((dc >> 3) << 2) | (dc & 3);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[i] = i == at ? o[i] + k.w : o[i];
+  }
+  if constexpr (E::kElem == 2) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      *reinterpret_cast<uint2*>(stg + stg8(cl, j, h)) =
+          make_uint2(pk_bf16(o[4 * j], o[4 * j + 1]), pk_bf16(o[4 * j + 2], o[4 * j + 3]));
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+      const int r = kk * 16 + (lane >> 2), j = lane & 3;
+      const uint4 q = *reinterpret_cast<const uint4*>(stg + r * 64 + ((j ^ ((r >> 2) & 3)) << 4));
+      const uint4 x = ((r >> 4) & 1) ? make_uint4(q.z, q.w, q.x, q.y) : q;  // halves stored exchanged
+      const int col = cb + 8 * j;
+      if (kFull || col >= lo) *reinterpret_cast<uint4*>(dz + panel_off(C, brow0 + r, (long)col * 2)) = x;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int col = cb + 8 * j + 4 * h;
+      if (kFull || col >= lo)
+        *reinterpret_cast<float4*>(dz + panel_off(C, brow0 + cl, (long)col * 4)) =
+            make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+    }
+  }
+}
+
+}  // namespace
+
+template <class Main, class E, bool kEnt>
+__global__ __launch_bounds__(kThreads, 1) void logp_dz_kernel(LogpDzArgs a) {
+  __shared__ __attribute__((aligned(16))) char sl_0[kSlotBytes];
+  __shared__ __attribute__((aligned(16))) char sl_1[kSlotBytes];
+  __shared__ __attribute__((aligned(16))) char sl_2[kSlotBytes];
+  __shared__ __attribute__((aligned(16))) char sl_3[kSlotBytes];
+  __shared__ __attribute__((aligned(16))) char stg_all[4 * kStgBytes];
+  __shared__ __attribute__((aligned(16))) float4 rowk[kBM];
+  __shared__ __attribute__((aligned(8))) float2 rowc[kBM];
+  const Slots sl{sl_0, sl_1, sl_2, sl_3, nullptr};
+
+  const long count = *a.c.count;
+  const long M = min(a.C, count - a.c0);
+  if (M <= 0) return;
+  int rb, sp;
+  grouped_coords(xcd_remap(blockIdx.x, gridDim.x), a.nrb, a.S, a.group, rb, sp);
+  const int row0 = rb * kBM;
+  if (row0 >= M) return;
+  const int tb = (int)((long)a.ntiles * sp / a.S);
+  const int te = (int)((long)a.ntiles * (sp + 1) / a.S);
+  const int V = (int)a.V;
+
+  Main mainloop;
+  mainloop.init(
+      a.Hp, [&](int r) -> const char* { return row0 + r < M ? a.Hp + (row0 + r) * kRowB : nullptr; }, a.W,
+      a.V * E::kElem, a.V, a.d, a.C * kRowB);
+
+  {
+    const int i = (int)threadIdx.x;
+    const bool rv = row0 + i < M;
+    const DzRow r = dz_row(a, rv, rv ? a.c.rows[a.c0 + row0 + i] : 0);
+    rowk[i] = r.k;
+    rowc[i] = make_float2(r.c2, __int_as_float(r.label));
+  }
+  __syncthreads();
+  const int w = wave_id(), wm = w >> 1, wn = w & 1;
+  const int trow0 = wm * 128;
+  char* stg = stg_all + w * kStgBytes;
+
+  mainloop.template run<true>(
+      sl, te - tb, [&](int i) { return TileAt{0, tile_n0(tb + i, V)}; },
+      [&](int i, const f32x16_t (&acc)[4][4]) {
+        const int vt = tb + i, n0 = tile_n0(vt, V), lo = vt * kBN, hi = min(lo + kBN, V);
+        const int base = n0 + wn * 128;
+        const bool full = n0 == lo && lo + kBN <= hi;
+        const int ln = opaque((int)threadIdx.x) & 31;
+#pragma unroll
+        for (int mb = 0; mb < 4; ++mb) {
+          const float4 k = rowk[trow0 + mb * 32 + ln];
+          const float2 cc = rowc[trow0 + mb * 32 + ln];
+          const int label = __float_as_int(cc.y);
+#pragma unroll
+          for (int nb = 0; nb < 4; ++nb) {
+            if (full)
+              dz_block<E, kEnt, true>(acc[mb][nb], k, cc.x, label, base + 32 * nb, lo, hi, stg, a.dz, a.C,
+                                      row0 + trow0 + mb * 32);
+            else
+              dz_block<E, kEnt, false>(acc[mb][nb], k, cc.x, label, base + 32 * nb, lo, hi, stg, a.dz, a.C,
+                                       row0 + trow0 + mb * 32);
+          }
+        }
+      });
+}
+
+// ------------------------------------------------------------------ dZ from stored logits
+// A block covers 64 rows and one range of the rows' 64-byte dZ pieces, four
+// threads per piece: a wave writes 16 consecutive rows of a piece, a
+// contiguous kilobyte of the panels.  Rows past the chunk's valid rows, up
+// to the end of the chunk, get zeros.
+constexpr int kFzRows = 64, kFzRanges = 64;
+
+template <class E, bool kEnt>
+__global__ __launch_bounds__(256) void logp_dz_from_z_kernel(LogpDzArgs a) {
+  constexpr int EPT = E::kEpc;
+  constexpr int PC = kRowB / E::kElem;  // columns per piece
+  const long i = (long)blockIdx.y * kFzRows + (threadIdx.x >> 2);
+  const int sub = threadIdx.x & 3;
+  const long np = (a.V * E::kElem + kRowB - 1) / kRowB;
+  const long pb = np * blockIdx.x / gridDim.x, pe = np * (blockIdx.x + 1) / gridDim.x;
+  const long M = min(a.C, (long)*a.c.count - a.c0);
+  const bool rv = i < M;
+  const DzRow r = dz_row(a, rv, rv ? a.c.rows[a.c0 + i] : 0);
+  const float* zr = a.z + i * a.ldz;
+  for (long p = pb; p < pe; ++p) {
+    const long v0 = p * PC + sub * EPT;
+    if (v0 >= a.V) break;
+    float o[EPT];
+#pragma unroll
+    for (int q = 0; q < EPT; ++q) o[q] = 0.f;
+    if (rv) {
+#pragma unroll
+      for (int e = 0; e < EPT; e += 4) {
+        const float4 z4 = *reinterpret_cast<const float4*>(zr + v0 + e);
+        o[e + 0] = dz_value<kEnt>(z4.x, r.k, r.c2);
+        o[e + 1] = dz_value<kEnt>(z4.y, r.k, r.c2);
+        o[e + 2] = dz_value<kEnt>(z4.z, r.k, r.c2);
+        o[e + 3] = dz_value<kEnt>(z4.w, r.k, r.c2);
+      }
+#pragma unroll
+      for (int q = 0; q < EPT; ++q) o[q] = (long)r.label == v0 + q ? o[q] + r.k.w : o[q];
+    }
+    *reinterpret_cast<u32x4_t*>(a.dz + panel_off(a.C, i, v0 * E::kElem)) = pack16<E>(o);
+  }
+}
+
+__global__ __launch_bounds__(256) void to_bf16_kernel(const float* in, uint16_t* out, long n8) {
+  for (long q = (long)blockIdx.x * 256 + threadIdx.x; q < n8; q += (long)gridDim.x * 256) {
+    const float4 x = *reinterpret_cast<const float4*>(in + 8 * q), y = *reinterpret_cast<const float4*>(in + 8 * q + 4);
+    *reinterpret_cast<uint4*>(out + 8 * q) =
+        make_uint4(pk_bf16(x.x, x.y), pk_bf16(x.z, x.w), pk_bf16(y.x, y.y), pk_bf16(y.z, y.w));
+  }
+}
+
+hipError_t launch_to_bf16(const float* in, void* out, int64_t n, hipStream_t st) {
+  const int64_t n8 = n / 8;
+  if (n8 == 0) return hipSuccess;
+  const int64_t blocks = (n8 + 255) / 256;
+  hipLaunchKernelGGL(to_bf16_kernel, dim3((unsigned)(blocks < 8192 ? blocks : 8192)), dim3(256), 0, st, in,
+                     static_cast<uint16_t*>(out), (long)n8);
+  return hipGetLastError();
+}
+
+// ------------------------------------------------------------------ launches
+namespace {
+
+// The direct-load ring needs bf16, a hidden width of whole ring turns, a
+// whole 256-column tile of vocabulary and operands within its 32-bit offsets.
+bool ring_fits(int elem, int64_t C, int64_t d, int64_t V) {
+  return elem == 2 && d % kDmaKMult == 0 && V >= kBN && fits32(C * d * 2) && fits32(d * V * 2);
+}
+
+template <class Main, class E>
+void fwd(const LogpFwdArgs& a, bool entropy, hipStream_t st) {
+  const dim3 grid(a.nrb * a.S), block(kThreads);
+  if (entropy && a.zout)
+    hipLaunchKernelGGL((logp_fwd_kernel<Main, E, true, true>), grid, block, 0, st, a);
+  else if (entropy)
+    hipLaunchKernelGGL((logp_fwd_kernel<Main, E, true, false>), grid, block, 0, st, a);
+  else if (a.zout)
+    hipLaunchKernelGGL((logp_fwd_kernel<Main, E, false, true>), grid, block, 0, st, a);
+  else
+    hipLaunchKernelGGL((logp_fwd_kernel<Main, E, false, false>), grid, block, 0, st, a);
+}
+
+template <class Main, class E>
+void dz(const LogpDzArgs& a, hipStream_t st) {
+  const dim3 grid(a.nrb * a.S), block(kThreads);
+  if (a.ge)
+    hipLaunchKernelGGL((logp_dz_kernel<Main, E, true>), grid, block, 0, st, a);
+  else
+    hipLaunchKernelGGL((logp_dz_kernel<Main, E, false>), grid, block, 0, st, a);
+}
+
+}  // namespace
+
+hipError_t launch_logp_fwd(int elem, const LogpFwdArgs& a, bool entropy, hipStream_t st) {
+  if (ring_fits(elem, a.C, a.d, a.V))
+    fwd<DmaNN<kBN>, Bf16>(a, entropy, st);
+  else if (elem == 2)
+    fwd<GenNN<Bf16, kBN>, Bf16>(a, entropy, st);
+  else
+    fwd<GenNN<F32, kBN>, F32>(a, entropy, st);
+  return hipGetLastError();
+}
+
+hipError_t launch_logp_dz(int elem, const LogpDzArgs& a, hipStream_t st) {
+  if (ring_fits(elem, a.C, a.d, a.V))
+    dz<DmaNN<kBN>, Bf16>(a, st);
+  else if (elem == 2)
+    dz<GenNN<Bf16, kBN>, Bf16>(a, st);
+  else
+    dz<GenNN<F32, kBN>, F32>(a, st);
+  return hipGetLastError();
+}
+
+hipError_t launch_logp_dz_from_z(int elem, const LogpDzArgs& a, hipStream_t st) {
+  const int64_t pieces = (a.V * elem + kRowB - 1) / kRowB;
+  const dim3 grid((unsigned)(pieces < kFzRanges ? pieces : kFzRanges), (unsigned)(a.C / kFzRows)), block(256);
+  if (elem == 2 && a.ge)
+    hipLaunchKernelGGL((logp_dz_from_z_kernel<Bf16, true>), grid, block, 0, st, a);
+  else if (elem == 2)
+    hipLaunchKernelGGL((logp_dz_from_z_kernel<Bf16, false>), grid, block, 0, st, a);
+  else if (a.ge)
+    hipLaunchKernelGGL((logp_dz_from_z_kernel<F32, true>), grid, block, 0, st, a);
+  else
+    hipLaunchKernelGGL((logp_dz_from_z_kernel<F32, false>), grid, block, 0, st, a);
+  return hipGetLastError();
+}
+
+}  // namespace kd

@@ -1,0 +1,139 @@
+// Internal interface of the policy- and preference-training operators: token
+// log-probabilities through the head, the clipped policy loss, the preference
+// loss and gradient clipping.  Every launcher enqueues on the given stream
+// and returns the launch status.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "kd_launch.h"
+
+namespace kd {
+
+// ---------------------------------------------------------------- token log-probabilities
+// One record per (vocabulary split, row): with y = z log2(e) / tau over the
+// split's columns, (m, l, e, x) = (max y, sum 2^(y - m), sum 2^(y - m) (y - m),
+// z at the row's token or 0).
+struct LogpFwdArgs {
+  const char* Hp;         // rows [c0, c0 + C) of H in panels of C rows
+  const char* W;          // [d][V]
+  Compact c;
+  const int32_t* tokens;  // [T]
+  float* part;            // [S][C][4], row p of a split is compacted row c0 + p
+  float* zout;            // nullable: the logits of those rows, fp32 [C][ldz]
+  int64_t ldz;
+  int64_t c0, C, d, V;
+  int32_t v0;             // first column of W in the whole head (tokens are whole-head indices)
+  int nrb, S, ntiles;
+  int group;
+  float c2;               // log2(e) / tau
+};
+hipError_t launch_logp_fwd(int elem, const LogpFwdArgs& a, bool entropy, hipStream_t st);
+
+// Per-row outputs of compacted rows [c0, c0 + C) from the records; with
+// zero_masked, also zeroes the outputs of every masked row.  rec != nullptr:
+// the merged record itself goes out instead (a vocabulary shard).
+struct LogpOut {
+  float* logp;
+  float* lse;
+  float* entropy;  // nullable
+  float4* rec;     // nullable
+};
+hipError_t launch_logp_combine(const float* part, int S, Compact c, const uint8_t* mask, const int32_t* tokens,
+                               int64_t T, int64_t V, int64_t c0, int64_t C, float c2, const LogpOut& o,
+                               bool zero_masked, hipStream_t st);
+// The same outputs from R shards' records rec [R][T].
+hipError_t launch_logp_shard_combine(const float4* rec, int R, int64_t T, const uint8_t* mask, float c2,
+                                     const LogpOut& o, hipStream_t st);
+
+// dZ of one chunk: dZ = ga [v = token] - q (ga + ge (ent + log q)), ga = g / tau, ge = grad_entropy / tau.
+struct LogpDzArgs {
+  const char* Hp;         // rows [c0, c0 + C) of H in panels of C rows (unused with z)
+  const char* W;
+  const float* z;         // nullable: stored logits [C][ldz] of the chunk
+  Compact c;
+  const int32_t* tokens;
+  const float* lse;
+  const float* ent;       // [T], read when ge is set
+  const float* g;         // nullable [T]: gradient of the log-probability
+  const float* ge;        // nullable [T]: gradient of the entropy
+  char* dz;               // [C][ldz] in panels of C rows
+  int64_t ldz, c0, C, d, V;
+  int32_t v0;
+  int nrb, S, ntiles;
+  int group;
+  float c2, inv_tau;
+};
+hipError_t launch_logp_dz(int elem, const LogpDzArgs& a, hipStream_t st);
+hipError_t launch_logp_dz_from_z(int elem, const LogpDzArgs& a, hipStream_t st);
+
+// out[i] = bf16(in[i]) for i < n, n a multiple of 8, both 16-byte aligned
+hipError_t launch_to_bf16(const float* in, void* out, int64_t n, hipStream_t st);
+
+// ---------------------------------------------------------------- clipped policy loss
+struct PolicyArgs {
+  const float* logp;
+  const float* old;
+  const float* adv;
+  const uint8_t* mask;    // nullable
+  const float* ref;       // nullable
+  const float* ent;       // nullable
+  const int32_t* cu;      // nullable [S+1]
+  int32_t T, S;
+  int per_sequence, reduction, kl_kind;
+  double lo, hi, dual, klw, entw;  // lo, hi: 1 - clip_low, 1 + clip_high
+  double* weights;        // [max(S, 1)]
+  const float* grad_total;  // nullable: 1
+  float* total;           // nullable [1]
+  float* stats;           // nullable [6]
+  float* grad_logp;       // nullable [T]
+  float* grad_ent;        // nullable [T]
+  double* part;           // workspace: [policy_blocks(T)][5]
+  int32_t* counts;        // workspace: [policy_counts(T, S)]
+};
+int64_t policy_blocks(int64_t T);
+int64_t policy_counts(int64_t T, int64_t S);
+// weights (and counts), then loss and / or gradients
+hipError_t launch_policy(const PolicyArgs& a, bool make_weights, hipStream_t st);
+
+// ---------------------------------------------------------------- preference loss
+struct PrefArgs {
+  const float* logp;      // not read by the backward
+  const float* ref;       // nullable
+  const int32_t* cu;      // [2P+1]
+  const uint8_t* mask;    // nullable
+  int32_t T, P;
+  int kind, average;
+  double beta, eps, margin;
+  double* sums;           // [2P][2]
+  float* loss;            // [P]
+  float* rewards;         // [2P]
+  const float* grad_loss; // [P]
+  float* grad_logp;       // nullable [T]
+  double* part;           // workspace: [pref_chunks(T)][4]
+};
+int64_t pref_chunks(int64_t T);
+hipError_t launch_pref_fwd(const PrefArgs& a, hipStream_t st);  // sums, loss, rewards
+hipError_t launch_pref_bwd(const PrefArgs& a, hipStream_t st);  // grad_logp from sums
+
+// ---------------------------------------------------------------- gradient norm and clipping
+// One launch's tensors, by value (the kernel argument segment holds 4 KB).
+// Tensor i is covered by blocks [first[i], first[i + 1]), kClipBlock elements each.
+constexpr int kClipTensors = 96;
+constexpr int kClipBlock = 16384;
+struct ClipTable {
+  const void* in[kClipTensors];
+  void* out[kClipTensors];
+  int64_t numel[kClipTensors];
+  int32_t first[kClipTensors + 1];
+  uint8_t in_type[kClipTensors], out_type[kClipTensors];  // KD_F32, KD_BF16, KD_F16
+  int32_t n;
+};
+// partial sums of squares, one per block, from part[0] on
+hipError_t launch_sumsq(const ClipTable& t, double* part, hipStream_t st);
+hipError_t launch_sumsq_total(const double* part, int64_t n, double* sumsq, hipStream_t st);
+hipError_t launch_clip(const ClipTable& t, const double* sumsq, double max_norm, hipStream_t st);
+hipError_t launch_norm(const double* sumsq, float* norm, hipStream_t st);
+
+}  // namespace kd
