@@ -7,6 +7,7 @@ one is given.
 """
 from __future__ import annotations
 
+import array
 import contextlib
 import ctypes
 
@@ -365,24 +366,42 @@ def _dense(t):
 
 
 class TensorTable:
-    """Host arrays of pointers, element counts and types of a list of tensors on one device."""
+    """Host arrays of pointers, element counts and types of a list of tensors on one device.  One pass per attribute:
+    a few hundred tensors are checked in less time than their kernels take."""
 
     def __init__(self, name, tensors):
-        for t in tensors:
-            if not isinstance(t, torch.Tensor):
-                raise TypeError(f"{name} must hold torch.Tensors, got {type(t).__name__}")
-            if t.dtype not in GRAD_TYPES:
-                raise TypeError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
-            if not t.is_cuda:
-                raise ValueError("libkdloss tensors must be on the GPU")
-            if not _dense(t):
-                raise ValueError(f"{name} must be dense in memory, got shape {tuple(t.shape)} with strides {t.stride()}")
-        _one_device(*tensors)
-        n = self.n = len(tensors)
+        try:
+            types = [GRAD_TYPES[t.dtype] for t in tensors]
+        except (KeyError, AttributeError):
+            for t in tensors:
+                if not isinstance(t, torch.Tensor):
+                    raise TypeError(f"{name} must hold torch.Tensors, got {type(t).__name__}") from None
+                if t.dtype not in GRAD_TYPES:
+                    raise TypeError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}") from None
+            raise
+        devices = {t.get_device() for t in tensors}
+        if -1 in devices:
+            raise ValueError("libkdloss tensors must be on the GPU")
+        if len(devices) > 1:
+            _one_device(*tensors)
+        self.contiguous = all([t.is_contiguous() for t in tensors])
+        if not self.contiguous:
+            for t in tensors:
+                if not _dense(t):
+                    raise ValueError(f"{name} must be dense in memory, got shape {tuple(t.shape)} with strides {t.stride()}")
+        self.n = len(tensors)
         self.tensors = tensors
-        self.ptrs = (ctypes.c_void_p * n)(*[t.data_ptr() for t in tensors])
-        self.numel = (ctypes.c_int64 * n)(*[t.numel() for t in tensors])
-        self.types = (ctypes.c_int32 * n)(*[GRAD_TYPES[t.dtype] for t in tensors])
+        self._arrays = (array.array("Q", [t.data_ptr() for t in tensors]),
+                        array.array("q", [t.numel() for t in tensors]), array.array("i", types))
+        self.ptrs, self.numel, self.types = (a.buffer_info()[0] for a in self._arrays)
+
+    def same_layout(self, other):
+        """Whether the two tables' tensors pair up element by element in memory."""
+        if self._arrays[1] != other._arrays[1]:
+            return False
+        if self.contiguous and other.contiguous:
+            return True
+        return all(t.shape == o.shape and t.stride() == o.stride() for t, o in zip(self.tensors, other.tensors))
 
 
 def kd_grad_norm_workspace_size(table) -> int:
@@ -400,9 +419,9 @@ def kd_grad_sumsq(table, sumsq, workspace, stream=None):
 def kd_grad_clip(table, outs, sumsq, max_norm, norm, stream=None):
     """Enqueue the scaling of a TensorTable into another (or itself); norm (one float32) in place."""
     _need("sumsq", sumsq, (1,), _F64)
-    _need("norm", norm, (1,), _F32)
-    if outs is not table and (outs.n != table.n or list(outs.numel) != list(table.numel)):
-        raise ValueError("out must have the tensors' number and sizes")
+    _need("norm", norm, (), _F32)
+    if outs is not table and not table.same_layout(outs):
+        raise ValueError("out must match the tensors' number, sizes and strides")
     _one_device(sumsq, norm, *table.tensors[:1], *outs.tensors[:1])
     _run("kd_grad_clip", sumsq, stream, table.ptrs, table.numel, table.types, table.n, outs.ptrs, outs.types, _ptr(sumsq),
          float(max_norm), _ptr(norm))

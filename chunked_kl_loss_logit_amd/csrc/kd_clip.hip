@@ -18,57 +18,152 @@ namespace kd {
 
 namespace {
 
-constexpr int kClipThreads = 256;
+constexpr int kClipThreads = 512;
 enum { kTypeF32 = 0, kTypeBf16 = 1, kTypeF16 = 2 };
 
+template <int NT>
 __device__ inline double block_sum(double v) {
-  __shared__ double red[kClipThreads / 64];
+  __shared__ double red[NT / 64];
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
   __syncthreads();
   v = 0;
 #pragma unroll
-  for (int i = 0; i < kClipThreads / 64; ++i) v += red[i];
+  for (int i = 0; i < NT / 64; ++i) v += red[i];
   return v;
 }
 
 // the tensor that block b covers
-__device__ inline int tensor_of(const ClipTable& t, int b) {
-  int lo = 0, hi = t.n;  // first index with first > b
+__device__ inline int tensor_of(const int32_t* first, int n, int b) {
+  int lo = 0, hi = n;  // first index with first > b
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
-    if (t.first[mid] <= b) lo = mid + 1; else hi = mid;
+    if (first[mid] <= b) lo = mid + 1; else hi = mid;
   }
   return lo - 1;
 }
 
-template <int TY>
-__device__ inline float load1(const void* p, long i) {
-  if constexpr (TY == kTypeF32) return static_cast<const float*>(p)[i];
-  if constexpr (TY == kTypeBf16) return __uint_as_float((uint32_t)static_cast<const uint16_t*>(p)[i] << 16);
-  if constexpr (TY == kTypeF16) return __half2float(static_cast<const __half*>(p)[i]);
+// 16 bytes at any element-aligned address (the hardware takes unaligned
+// vector accesses; only those that cross a cache line cost more).
+__device__ inline u32x4_t load16(const char* p) {
+  u32x4_t v;
+  __builtin_memcpy(&v, p, 16);
+  return v;
 }
-template <int TY>
-__device__ inline void store1(void* p, long i, float v) {
-  if constexpr (TY == kTypeF32) static_cast<float*>(p)[i] = v;
-  if constexpr (TY == kTypeBf16) static_cast<uint16_t*>(p)[i] = (uint16_t)Bf16::cvt(v);
-  if constexpr (TY == kTypeF16) static_cast<__half*>(p)[i] = __float2half_rn(v);
-}
+__device__ inline void store16(char* p, u32x4_t v) { __builtin_memcpy(p, &v, 16); }
 
 template <int TY>
-__device__ inline double sumsq_range(const void* p, long b, long e) {
-  double s = 0;
-  for (long i = b + threadIdx.x; i < e; i += kClipThreads) {
-    const double x = load1<TY>(p, i);
-    s = fma(x, x, s);
+struct Elem;
+template <>
+struct Elem<kTypeF32> {
+  static constexpr int kBytes = 4;
+  __device__ static inline float get(u32x4_t v, int i) { return __uint_as_float(v[i]); }
+  __device__ static inline float get1(const char* p) { return *reinterpret_cast<const float*>(p); }
+  __device__ static inline void put1(char* p, float x) { *reinterpret_cast<float*>(p) = x; }
+};
+template <>
+struct Elem<kTypeBf16> {
+  static constexpr int kBytes = 2;
+  __device__ static inline float get(u32x4_t v, int i) {
+    return __uint_as_float(i & 1 ? v[i >> 1] & 0xffff0000u : v[i >> 1] << 16);
   }
-  return s;
+  __device__ static inline float get1(const char* p) {
+    return __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t*>(p) << 16);
+  }
+  __device__ static inline void put1(char* p, float x) { *reinterpret_cast<uint16_t*>(p) = (uint16_t)Bf16::cvt(x); }
+  __device__ static inline uint32_t pack(float a, float b) { return Bf16::pack2(a, b); }
+};
+template <>
+struct Elem<kTypeF16> {
+  static constexpr int kBytes = 2;
+  __device__ static inline float get(u32x4_t v, int i) {
+    return __half2float(__ushort_as_half((unsigned short)(v[i >> 1] >> (16 * (i & 1)))));
+  }
+  __device__ static inline float get1(const char* p) { return __half2float(*reinterpret_cast<const __half*>(p)); }
+  __device__ static inline void put1(char* p, float x) { *reinterpret_cast<__half*>(p) = __float2half_rn(x); }
+  __device__ static inline uint32_t pack(float a, float b) {
+    return (uint32_t)__half_as_ushort(__float2half_rn(a)) | ((uint32_t)__half_as_ushort(__float2half_rn(b)) << 16);
+  }
+};
+
+// Elements [b, e) (at most kClipBlock, from a multiple of it) of a tensor:
+// 16-byte pieces, kDeep of a thread's loads in flight at once, then the
+// last few elements one by one.
+constexpr int kDeep = 4;
+
+template <int TY>
+__device__ inline double sumsq_range(const void* base, long b, long e) {
+  using E = Elem<TY>;
+  constexpr int N = 16 / E::kBytes;
+  const char* p = static_cast<const char*>(base) + b * E::kBytes;
+  const int n = (int)(e - b), pieces = n / N;
+  double s[2] = {0, 0};
+  auto add = [&](u32x4_t v) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const double x = E::get(v, i);
+      s[i & 1] = fma(x, x, s[i & 1]);
+    }
+  };
+  int q = threadIdx.x;
+  for (; q + (kDeep - 1) * kClipThreads < pieces; q += kDeep * kClipThreads) {
+    u32x4_t v[kDeep];
+#pragma unroll
+    for (int k = 0; k < kDeep; ++k) v[k] = load16(p + 16 * (q + k * kClipThreads));
+#pragma unroll
+    for (int k = 0; k < kDeep; ++k) add(v[k]);
+  }
+  for (; q < pieces; q += kClipThreads) add(load16(p + 16 * q));
+  const int last = pieces * N + threadIdx.x;
+  if (last < n) {
+    const double x = E::get1(p + last * E::kBytes);
+    s[0] = fma(x, x, s[0]);
+  }
+  return s[0] + s[1];
+}
+
+// One piece of 16 / TI::kBytes elements, scaled, to the output's type: 8, 16 or 32 bytes.
+template <int TI, int TO>
+__device__ inline void scale_piece(u32x4_t v, char* o, float c) {
+  using I = Elem<TI>;
+  using O = Elem<TO>;
+  constexpr int N = 16 / I::kBytes;
+  float x[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) x[i] = I::get(v, i) * c;
+  if constexpr (TO == kTypeF32) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4)
+      store16(o + 4 * i, u32x4_t{__float_as_uint(x[i]), __float_as_uint(x[i + 1]), __float_as_uint(x[i + 2]),
+                                 __float_as_uint(x[i + 3])});
+  } else {
+    uint32_t w[N / 2];
+#pragma unroll
+    for (int i = 0; i < N; i += 2) w[i / 2] = O::pack(x[i], x[i + 1]);
+    __builtin_memcpy(o, w, sizeof w);
+  }
 }
 
 template <int TI, int TO>
-__device__ inline void scale_range(const void* p, void* o, long b, long e, float c) {
-  for (long i = b + threadIdx.x; i < e; i += kClipThreads) store1<TO>(o, i, load1<TI>(p, i) * c);
+__device__ inline void scale_range(const void* base, void* out, long b, long e, float c) {
+  using I = Elem<TI>;
+  using O = Elem<TO>;
+  constexpr int N = 16 / I::kBytes;
+  const char* p = static_cast<const char*>(base) + b * I::kBytes;
+  char* o = static_cast<char*>(out) + b * O::kBytes;
+  const int n = (int)(e - b), pieces = n / N;
+  int q = threadIdx.x;
+  for (; q + (kDeep - 1) * kClipThreads < pieces; q += kDeep * kClipThreads) {
+    u32x4_t v[kDeep];
+#pragma unroll
+    for (int k = 0; k < kDeep; ++k) v[k] = load16(p + 16 * (q + k * kClipThreads));
+#pragma unroll
+    for (int k = 0; k < kDeep; ++k) scale_piece<TI, TO>(v[k], o + N * O::kBytes * (q + k * kClipThreads), c);
+  }
+  for (; q < pieces; q += kClipThreads) scale_piece<TI, TO>(load16(p + 16 * q), o + N * O::kBytes * q, c);
+  const int last = pieces * N + threadIdx.x;
+  if (last < n) O::put1(o + last * O::kBytes, I::get1(p + last * I::kBytes) * c);
 }
 
 template <int TI>
@@ -80,29 +175,36 @@ __device__ inline void scale_to(int to, const void* p, void* o, long b, long e, 
 
 }  // namespace
 
-__global__ __launch_bounds__(kClipThreads) void sumsq_kernel(ClipTable t, double* part) {
-  const int i = tensor_of(t, blockIdx.x);
+__global__ __launch_bounds__(kClipThreads) void sumsq_kernel(SumsqTable t, double* part) {
+  const int i = tensor_of(t.first, t.n, blockIdx.x);
   const long b = (long)(blockIdx.x - t.first[i]) * kClipBlock, e = min(b + kClipBlock, (long)t.numel[i]);
-  const int ty = t.in_type[i];
+  const int ty = t.type[i];
   double s;
   if (ty == kTypeF32) s = sumsq_range<kTypeF32>(t.in[i], b, e);
   else if (ty == kTypeBf16) s = sumsq_range<kTypeBf16>(t.in[i], b, e);
   else s = sumsq_range<kTypeF16>(t.in[i], b, e);
-  s = block_sum(s);
+  s = block_sum<kClipThreads>(s);
   if (threadIdx.x == 0) part[blockIdx.x] = s;
 }
 
-__global__ __launch_bounds__(kClipThreads) void sumsq_total_kernel(const double* part, long n, double* sumsq) {
-  double s = 0;
-  for (long i = threadIdx.x; i < n; i += kClipThreads) s += part[i];
-  s = block_sum(s);
-  if (threadIdx.x == 0) *sumsq = s;
+// One block of 1024; 4 loads of a thread in flight (12 K partials for 400 M elements).
+__global__ __launch_bounds__(1024) void sumsq_total_kernel(const double* part, long n, double* sumsq) {
+  double s[4] = {0, 0, 0, 0};
+  for (long i = threadIdx.x; i < n; i += 4096)
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (i + 1024 * k < n) s[k] += part[i + 1024 * k];
+  const double v = block_sum<1024>((s[0] + s[1]) + (s[2] + s[3]));
+  if (threadIdx.x == 0) *sumsq = v;
 }
 
-__global__ __launch_bounds__(kClipThreads) void clip_kernel(ClipTable t, const double* sumsq, double max_norm) {
-  const int i = tensor_of(t, blockIdx.x);
+__global__ __launch_bounds__(kClipThreads) void clip_kernel(ClipTable t, const double* sumsq, double max_norm,
+                                                            float* norm) {
+  const int i = tensor_of(t.first, t.n, blockIdx.x);
   const long b = (long)(blockIdx.x - t.first[i]) * kClipBlock, e = min(b + kClipBlock, (long)t.numel[i]);
-  const double r = max_norm / (sqrt(*sumsq) + 1e-6);
+  const double n = sqrt(*sumsq);
+  if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)n;
+  const double r = max_norm / (n + 1e-6);
   const float c = r >= 1.0 || max_norm == INFINITY ? 1.f : (float)r;  // a NaN norm stays NaN
   if (c == 1.f && t.in[i] == t.out[i]) return;
   const int ty = t.in_type[i], to = t.out_type[i];
@@ -113,16 +215,16 @@ __global__ __launch_bounds__(kClipThreads) void clip_kernel(ClipTable t, const d
 
 __global__ void norm_kernel(const double* sumsq, float* norm) { *norm = (float)sqrt(*sumsq); }
 
-hipError_t launch_sumsq(const ClipTable& t, double* part, hipStream_t st) {
+hipError_t launch_sumsq(const SumsqTable& t, double* part, hipStream_t st) {
   hipLaunchKernelGGL(sumsq_kernel, dim3(t.first[t.n]), dim3(kClipThreads), 0, st, t, part);
   return hipGetLastError();
 }
 hipError_t launch_sumsq_total(const double* part, int64_t n, double* sumsq, hipStream_t st) {
-  hipLaunchKernelGGL(sumsq_total_kernel, dim3(1), dim3(kClipThreads), 0, st, part, (long)n, sumsq);
+  hipLaunchKernelGGL(sumsq_total_kernel, dim3(1), dim3(1024), 0, st, part, (long)n, sumsq);
   return hipGetLastError();
 }
-hipError_t launch_clip(const ClipTable& t, const double* sumsq, double max_norm, hipStream_t st) {
-  hipLaunchKernelGGL(clip_kernel, dim3(t.first[t.n]), dim3(kClipThreads), 0, st, t, sumsq, max_norm);
+hipError_t launch_clip(const ClipTable& t, const double* sumsq, double max_norm, float* norm, hipStream_t st) {
+  hipLaunchKernelGGL(clip_kernel, dim3(t.first[t.n]), dim3(kClipThreads), 0, st, t, sumsq, max_norm, norm);
   return hipGetLastError();
 }
 hipError_t launch_norm(const double* sumsq, float* norm, hipStream_t st) {

@@ -118,22 +118,33 @@ hipError_t launch_pref_fwd(const PrefArgs& a, hipStream_t st);  // sums, loss, r
 hipError_t launch_pref_bwd(const PrefArgs& a, hipStream_t st);  // grad_logp from sums
 
 // ---------------------------------------------------------------- gradient norm and clipping
-// One launch's tensors, by value (the kernel argument segment holds 4 KB).
-// Tensor i is covered by blocks [first[i], first[i + 1]), kClipBlock elements each.
-constexpr int kClipTensors = 96;
-constexpr int kClipBlock = 16384;
-struct ClipTable {
-  const void* in[kClipTensors];
-  void* out[kClipTensors];
-  int64_t numel[kClipTensors];
-  int32_t first[kClipTensors + 1];
-  uint8_t in_type[kClipTensors], out_type[kClipTensors];  // KD_F32, KD_BF16, KD_F16
+// One launch's tensors, by value (a table stays within a kernel argument
+// segment of 4 KB).  Tensor i is covered by blocks [first[i], first[i + 1]),
+// kClipBlock elements each.
+constexpr int kClipBlock = 32768;
+struct SumsqTable {
+  static constexpr int kTensors = 188;
+  const void* in[kTensors];
+  int64_t numel[kTensors];
+  int32_t first[kTensors + 1];
   int32_t n;
+  uint8_t type[kTensors];  // KD_F32, KD_BF16, KD_F16
 };
+struct ClipTable {
+  static constexpr int kTensors = 132;
+  const void* in[kTensors];
+  void* out[kTensors];
+  int64_t numel[kTensors];
+  int32_t first[kTensors + 1];
+  int32_t n;
+  uint8_t in_type[kTensors], out_type[kTensors];
+};
+static_assert(sizeof(SumsqTable) <= 4000 && sizeof(ClipTable) <= 4000, "kernel arguments");
 // partial sums of squares, one per block, from part[0] on
-hipError_t launch_sumsq(const ClipTable& t, double* part, hipStream_t st);
+hipError_t launch_sumsq(const SumsqTable& t, double* part, hipStream_t st);
 hipError_t launch_sumsq_total(const double* part, int64_t n, double* sumsq, hipStream_t st);
-hipError_t launch_clip(const ClipTable& t, const double* sumsq, double max_norm, hipStream_t st);
+// norm (nullable) is written too
+hipError_t launch_clip(const ClipTable& t, const double* sumsq, double max_norm, float* norm, hipStream_t st);
 hipError_t launch_norm(const double* sumsq, float* norm, hipStream_t st);
 
 }  // namespace kd

@@ -608,25 +608,22 @@ kd_status check_overlap(const void* const* in, const int32_t* ty, void* const* o
   return KD_OK;
 }
 
-// The tensors in tables of at most kClipTensors; f(table, first block of the table).
-template <class F>
-kd_status over_tables(const void* const* in, const int64_t* numel, const int32_t* ty, int64_t n, void* const* out,
-                      const int32_t* oty, F&& f) {
-  kd::ClipTable t;
+// The non-empty tensors in tables of at most Table::kTensors: set(table, slot,
+// i) fills a slot, f(table, first block of the table) launches it.
+template <class Table, class Set, class F>
+kd_status over_tables(const int64_t* numel, int64_t n, Set&& set, F&& f) {
+  Table t;
   int64_t base = 0;
   t.n = 0;
   t.first[0] = 0;
   for (int64_t i = 0; i < n; ++i) {
     if (numel[i] > 0) {
-      t.in[t.n] = in[i];
-      t.out[t.n] = out ? out[i] : nullptr;
+      set(t, t.n, i);
       t.numel[t.n] = numel[i];
-      t.in_type[t.n] = (uint8_t)ty[i];
-      t.out_type[t.n] = out ? (uint8_t)oty[i] : 0;
       t.first[t.n + 1] = t.first[t.n] + (int32_t)clip_blocks(numel[i]);
       ++t.n;
     }
-    if (t.n > 0 && (t.n == kd::kClipTensors || i + 1 == n)) {
+    if (t.n > 0 && (t.n == Table::kTensors || i + 1 == n)) {
       KD_TRY(f(t, base));
       base += t.first[t.n];
       t.n = 0;
@@ -659,10 +656,16 @@ kd_status kd_grad_sumsq(const void* const* grads, const int64_t* numel, const in
   KD_TRY(check_workspace(workspace, workspace_bytes, up((size_t)blocks * 8, kAlign)));
   double* part = at<double>(workspace, 0);
   hipStream_t st = static_cast<hipStream_t>(stream);
-  KD_TRY(over_tables(grads, numel, dtypes, n, nullptr, nullptr, [&](const kd::ClipTable& t, int64_t base) {
-    KD_LAUNCH("grad_sumsq", st, kd::launch_sumsq(t, part + base, st));
-    return KD_OK;
-  }));
+  KD_TRY(over_tables<kd::SumsqTable>(
+      numel, n,
+      [&](kd::SumsqTable& t, int k, int64_t i) {
+        t.in[k] = grads[i];
+        t.type[k] = (uint8_t)dtypes[i];
+      },
+      [&](const kd::SumsqTable& t, int64_t base) {
+        KD_LAUNCH("grad_sumsq", st, kd::launch_sumsq(t, part + base, st));
+        return KD_OK;
+      }));
   KD_LAUNCH("grad_sumsq_total", st, kd::launch_sumsq_total(part, blocks, sumsq, st));
   return KD_OK;
 }
@@ -682,12 +685,19 @@ kd_status kd_grad_clip(const void* const* grads, const int64_t* numel, const int
   KD_TRY(need_align(sumsq, 8, "sumsq"));
   KD_TRY(need_align(norm, 4, "norm"));
   hipStream_t st = static_cast<hipStream_t>(stream);
-  KD_LAUNCH("grad_norm", st, kd::launch_norm(sumsq, norm, st));
-  KD_TRY(over_tables(grads, numel, dtypes, n, outs, out_dtypes, [&](const kd::ClipTable& t, int64_t) {
-    KD_LAUNCH("grad_clip", st, kd::launch_clip(t, sumsq, max_norm, st));
-    return KD_OK;
-  }));
-  return KD_OK;
+  if (blocks == 0) KD_LAUNCH("grad_norm", st, kd::launch_norm(sumsq, norm, st));
+  return over_tables<kd::ClipTable>(
+      numel, n,
+      [&](kd::ClipTable& t, int k, int64_t i) {
+        t.in[k] = grads[i];
+        t.out[k] = outs[i];
+        t.in_type[k] = (uint8_t)dtypes[i];
+        t.out_type[k] = (uint8_t)out_dtypes[i];
+      },
+      [&](const kd::ClipTable& t, int64_t base) {  // the first launch writes the norm
+        KD_LAUNCH("grad_clip", st, kd::launch_clip(t, sumsq, max_norm, base == 0 ? norm : nullptr, st));
+        return KD_OK;
+      });
 }
 
 }  // extern "C"

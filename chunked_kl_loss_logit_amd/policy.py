@@ -272,23 +272,18 @@ def grad_sumsq(tensors):
 
 
 def clip_grad_norm(tensors, max_norm, out=None, sumsq=None):
-    """Writes tensors[i] * min(1, max_norm / (norm + 1e-6)) to out[i] (same shapes and strides, float32, bfloat16 or
-    float16) and returns the global L2 norm, [1] float32 on the device.  out = None: in place.  None entries among
+    """Writes tensors[i] * min(1, max_norm / (norm + 1e-6)) to out[i] (the same number of elements in the same order
+    in memory; float32, bfloat16 or float16) and returns the global L2 norm, one float32 on the device.  out = None: in place.  None entries among
     the tensors are left out (not with out).  sumsq: the squared norm if it is not that of these tensors alone."""
     kept = _tensors(tensors)
     table = outs = B.TensorTable("tensors", kept)
     if out is not None:
-        out = [out] if isinstance(out, torch.Tensor) else list(out)
-        outs = B.TensorTable("out", out)
-        if len(out) != (1 if isinstance(tensors, torch.Tensor) else len(tensors)) or len(kept) != len(out):
-            raise ValueError(f"out must hold one tensor for each of {len(kept)}, got {len(out)}")
-        for t, o in zip(kept, out):
-            if t.shape != o.shape or (t.stride() != o.stride() and not (t.is_contiguous() and o.is_contiguous())):
-                raise ValueError(f"out must match the tensors' shapes and strides, got {tuple(o.shape)} {o.stride()} "
-                                 f"for {tuple(t.shape)} {t.stride()}")
+        outs = B.TensorTable("out", [out] if isinstance(out, torch.Tensor) else list(out))
+        if len(kept) != (1 if isinstance(tensors, torch.Tensor) else len(tensors)):
+            raise ValueError("with out, no tensor may be None")
     if sumsq is None:
         sumsq = _sumsq(table, kept[0].device)
-    norm = torch.empty(1, dtype=torch.float32, device=kept[0].device)
+    norm = torch.empty((), dtype=torch.float32, device=kept[0].device)
     B.kd_grad_clip(table, outs, sumsq, max_norm, norm)
     return norm
 

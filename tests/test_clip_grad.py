@@ -22,7 +22,7 @@ def check(tensors, max_norm, out=None):
     want = norm64(tensors)
     before = [t.clone() for t in tensors]
     norm = kd.clip_grad_norm(tensors, max_norm, out)
-    assert norm.shape == (1,) and abs(float(norm) - want) <= 2 * U32 * want
+    assert norm.shape == () and abs(float(norm) - want) <= 2 * U32 * want
     c = min(1.0, max_norm / (want + 1e-6))
     for b, o in zip(before, tensors if out is None else out):
         w = b.double() * c
