@@ -127,7 +127,7 @@ __device__ inline void zout_nb(const f32x16_t (&acc)[4], float* zr, int base, in
 }  // namespace
 
 // ------------------------------------------------------------------ forward tiles
-template <class Main, class E, bool kEnt, bool kOut>
+template <bool kEnt, bool kOut>
 __global__ __launch_bounds__(kThreads, 1) void logp_fwd_kernel(LogpFwdArgs a) {
   __shared__ __attribute__((aligned(16))) char sl_0[kSlotBytes];
   __shared__ __attribute__((aligned(16))) char sl_1[kSlotBytes];
@@ -148,10 +148,10 @@ __global__ __launch_bounds__(kThreads, 1) void logp_fwd_kernel(LogpFwdArgs a) {
   const int te = (int)((long)a.ntiles * (sp + 1) / a.S);
   const int V = (int)a.V;
 
-  Main mainloop;
+  DmaNN<kBN> mainloop;
   mainloop.init(
       a.Hp, [&](int r) -> const char* { return row0 + r < M ? a.Hp + (row0 + r) * kRowB : nullptr; }, a.W,
-      a.V * E::kElem, a.V, a.d, a.C * kRowB);
+      a.V * 2, a.V, a.d, a.C * kRowB);
 
   const int w = wave_id(), wm = w >> 1, wn = w & 1;
   const int lane = (int)threadIdx.x & 63;
@@ -271,29 +271,55 @@ __device__ inline void zero_row(long t, const LogpOut& o) {
 
 }  // namespace
 
-__global__ __launch_bounds__(256) void logp_combine_kernel(const float4* part, int S, Compact c, const uint8_t* mask,
-                                                           const int32_t* tokens, long T, int V, long c0, long C,
-                                                           float c2, LogpOut o, int zero_masked) {
-  const long j = (long)blockIdx.x * blockDim.x + threadIdx.x;
-  if (zero_masked && j < T && mask != nullptr && mask[j] == 0) zero_row(j, o);
-  if (j >= min(C, (long)*c.count - c0)) return;
-  float4 r = merge_records(part + j, S, C);
-  const long t = c.rows[c0 + j];
+// One wave per row of the chunk: lanes merge every 64th record, then each
+// other (a row has up to a thousand records; one thread walking them took as
+// long as the tiles did for a few rows).  With zero_masked, threads also zero
+// the outputs of masked rows.
+template <bool kEnt>
+__global__ __launch_bounds__(256) void logp_combine_kernel(const float4* part, int S, RowSet rs, const uint8_t* mask,
+                                                           const int32_t* tokens, int V, float c2, LogpOut o,
+                                                           int zero_masked) {
+  const int lane = threadIdx.x & 63;
+  const long j = (long)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (zero_masked && mask != nullptr)
+    for (long t = (long)blockIdx.x * 256 + threadIdx.x; t < rs.T; t += (long)gridDim.x * 256)
+      if (mask[t] == 0) zero_row(t, o);
+  const long M = rs.rows ? min((long)rs.C, (long)*rs.count - (long)rs.c0) : min((long)rs.C, (long)(rs.T - rs.c0));
+  if (j >= M) return;
+  float m = -INFINITY, l = 0.f, e = 0.f, x = 0.f;
+  for (int s = lane; s < S; s += 64) {
+    const float4 q = part[(long)s * rs.C + j];
+    merge<kEnt>(m, l, e, q.x, q.y, q.z);
+    x += q.w;
+  }
+#pragma unroll
+  for (int k = 1; k < 64; k <<= 1) {
+    const float om = __shfl_xor(m, k), ol = __shfl_xor(l, k), oe = __shfl_xor(e, k);
+    merge<kEnt>(m, l, e, om, ol, oe);
+    x += __shfl_xor(x, k);
+  }
+  if (lane != 0) return;
+  const long t = rs.rows ? rs.rows[rs.c0 + j] : rs.c0 + j;
   if (o.rec) {
-    o.rec[t] = r;
+    o.rec[t] = make_float4(m, l, e, x);
     return;
   }
-  if ((uint32_t)tokens[t] >= (uint32_t)V) r.w = NAN;  // no such token: loud, not a plausible number
-  finish_row(t, r, c2, o);
+  if ((uint32_t)tokens[t] >= (uint32_t)V) x = NAN;  // no such token: loud, not a plausible number
+  finish_row(t, make_float4(m, l, e, x), c2, o);
 }
 
-hipError_t launch_logp_combine(const float* part, int S, Compact c, const uint8_t* mask, const int32_t* tokens,
-                               int64_t T, int64_t V, int64_t c0, int64_t C, float c2, const LogpOut& o,
-                               bool zero_masked, hipStream_t st) {
-  const int64_t n = zero_masked ? T : (T < C ? T : C);
-  hipLaunchKernelGGL(logp_combine_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st,
-                     reinterpret_cast<const float4*>(part), S, c, mask, tokens, (long)T, (int)V, (long)c0, (long)C, c2,
-                     o, zero_masked ? 1 : 0);
+hipError_t launch_logp_combine(const float* part, int S, const RowSet& rs, const uint8_t* mask,
+                               const int32_t* tokens, int64_t V, float c2, const LogpOut& o, bool zero_masked,
+                               hipStream_t st) {
+  const int64_t n = rs.C < rs.T - rs.c0 ? rs.C : rs.T - rs.c0;
+  const dim3 grid((unsigned)((n + 3) / 4));
+  const float4* p = reinterpret_cast<const float4*>(part);
+  if (o.rec || o.entropy)
+    hipLaunchKernelGGL(logp_combine_kernel<true>, grid, dim3(256), 0, st, p, S, rs, mask, tokens, (int)V, c2, o,
+                       zero_masked ? 1 : 0);
+  else
+    hipLaunchKernelGGL(logp_combine_kernel<false>, grid, dim3(256), 0, st, p, S, rs, mask, tokens, (int)V, c2, o,
+                       zero_masked ? 1 : 0);
   return hipGetLastError();
 }
 
@@ -347,11 +373,10 @@ __device__ inline float dz_value(float z, const float4 k, float c2) {
 
 // One 32 x 32 block: dZ of the lane's row at its 16 columns, to the chunk's
 // panels.  Columns from hi on are zero, columns below lo belong to the
-// previous tile and are not stored.  bf16 goes through a wave-private 2 KB
-// LDS region (LDS accesses of one wave complete in order: no barrier), so
-// that a store instruction writes 16 consecutive rows of one 64-byte piece;
-// fp32 is stored as it lies, 32 bytes of a piece per row.
-template <class E, bool kEnt, bool kFull>
+// previous tile and are not stored.  The block goes through a wave-private
+// 2 KB LDS region (LDS accesses of one wave complete in order: no barrier),
+// so that a store instruction writes 16 consecutive rows of one 64-byte piece.
+template <bool kEnt, bool kFull>
 __device__ inline void dz_block(const f32x16_t& v, const float4 k, float c2, int label, int cb, int lo, int hi,
                                 char* stg, char* dz, long C, long brow0) {
   const int lane = opaque((int)threadIdx.x) & 63, h = lane >> 5, cl = lane & 31;
@@ -367,33 +392,23 @@ __device__ inline void dz_block(const f32x16_t& v, const float4 k, float c2, int
 #pragma unroll
     for (int i = 0; i < 16; ++i) o[i] = i == at ? o[i] + k.w : o[i];
   }
-  if constexpr (E::kElem == 2) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      *reinterpret_cast<uint2*>(stg + stg8(cl, j, h)) =
-          make_uint2(pk_bf16(o[4 * j], o[4 * j + 1]), pk_bf16(o[4 * j + 2], o[4 * j + 3]));
+  for (int j = 0; j < 4; ++j)
+    *reinterpret_cast<uint2*>(stg + stg8(cl, j, h)) =
+        make_uint2(pk_bf16(o[4 * j], o[4 * j + 1]), pk_bf16(o[4 * j + 2], o[4 * j + 3]));
 #pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-      const int r = kk * 16 + (lane >> 2), j = lane & 3;
-      const uint4 q = *reinterpret_cast<const uint4*>(stg + r * 64 + ((j ^ ((r >> 2) & 3)) << 4));
-      const uint4 x = ((r >> 4) & 1) ? make_uint4(q.z, q.w, q.x, q.y) : q;  // halves stored exchanged
-      const int col = cb + 8 * j;
-      if (kFull || col >= lo) *reinterpret_cast<uint4*>(dz + panel_off(C, brow0 + r, (long)col * 2)) = x;
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int col = cb + 8 * j + 4 * h;
-      if (kFull || col >= lo)
-        *reinterpret_cast<float4*>(dz + panel_off(C, brow0 + cl, (long)col * 4)) =
-            make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
-    }
+  for (int kk = 0; kk < 2; ++kk) {
+    const int r = kk * 16 + (lane >> 2), j = lane & 3;
+    const uint4 q = *reinterpret_cast<const uint4*>(stg + r * 64 + ((j ^ ((r >> 2) & 3)) << 4));
+    const uint4 x = ((r >> 4) & 1) ? make_uint4(q.z, q.w, q.x, q.y) : q;  // halves stored exchanged
+    const int col = cb + 8 * j;
+    if (kFull || col >= lo) *reinterpret_cast<uint4*>(dz + panel_off(C, brow0 + r, (long)col * 2)) = x;
   }
 }
 
 }  // namespace
 
-template <class Main, class E, bool kEnt>
+template <bool kEnt>
 __global__ __launch_bounds__(kThreads, 1) void logp_dz_kernel(LogpDzArgs a) {
   __shared__ __attribute__((aligned(16))) char sl_0[kSlotBytes];
   __shared__ __attribute__((aligned(16))) char sl_1[kSlotBytes];
@@ -415,10 +430,10 @@ __global__ __launch_bounds__(kThreads, 1) void logp_dz_kernel(LogpDzArgs a) {
   const int te = (int)((long)a.ntiles * (sp + 1) / a.S);
   const int V = (int)a.V;
 
-  Main mainloop;
+  DmaNN<kBN> mainloop;
   mainloop.init(
       a.Hp, [&](int r) -> const char* { return row0 + r < M ? a.Hp + (row0 + r) * kRowB : nullptr; }, a.W,
-      a.V * E::kElem, a.V, a.d, a.C * kRowB);
+      a.V * 2, a.V, a.d, a.C * kRowB);
 
   {
     const int i = (int)threadIdx.x;
@@ -447,10 +462,10 @@ __global__ __launch_bounds__(kThreads, 1) void logp_dz_kernel(LogpDzArgs a) {
 #pragma unroll
           for (int nb = 0; nb < 4; ++nb) {
             if (full)
-              dz_block<E, kEnt, true>(acc[mb][nb], k, cc.x, label, base + 32 * nb, lo, hi, stg, a.dz, a.C,
+              dz_block<kEnt, true>(acc[mb][nb], k, cc.x, label, base + 32 * nb, lo, hi, stg, a.dz, a.C,
                                       row0 + trow0 + mb * 32);
             else
-              dz_block<E, kEnt, false>(acc[mb][nb], k, cc.x, label, base + 32 * nb, lo, hi, stg, a.dz, a.C,
+              dz_block<kEnt, false>(acc[mb][nb], k, cc.x, label, base + 32 * nb, lo, hi, stg, a.dz, a.C,
                                        row0 + trow0 + mb * 32);
           }
         }
@@ -464,13 +479,13 @@ __global__ __launch_bounds__(kThreads, 1) void logp_dz_kernel(LogpDzArgs a) {
 // to the end of the chunk, get zeros.
 constexpr int kFzRows = 64, kFzRanges = 64;
 
-template <class E, bool kEnt>
+template <bool kEnt>
 __global__ __launch_bounds__(256) void logp_dz_from_z_kernel(LogpDzArgs a) {
-  constexpr int EPT = E::kEpc;
-  constexpr int PC = kRowB / E::kElem;  // columns per piece
+  constexpr int EPT = Bf16::kEpc;
+  constexpr int PC = kRowB / 2;  // columns per piece
   const long i = (long)blockIdx.y * kFzRows + (threadIdx.x >> 2);
   const int sub = threadIdx.x & 3;
-  const long np = (a.V * E::kElem + kRowB - 1) / kRowB;
+  const long np = (a.V * 2 + kRowB - 1) / kRowB;
   const long pb = np * blockIdx.x / gridDim.x, pe = np * (blockIdx.x + 1) / gridDim.x;
   const long M = min(a.C, (long)*a.c.count - a.c0);
   const bool rv = i < M;
@@ -494,7 +509,7 @@ __global__ __launch_bounds__(256) void logp_dz_from_z_kernel(LogpDzArgs a) {
 #pragma unroll
       for (int q = 0; q < EPT; ++q) o[q] = (long)r.label == v0 + q ? o[q] + r.k.w : o[q];
     }
-    *reinterpret_cast<u32x4_t*>(a.dz + panel_off(a.C, i, v0 * E::kElem)) = pack16<E>(o);
+    *reinterpret_cast<u32x4_t*>(a.dz + panel_off(a.C, i, v0 * 2)) = pack16<Bf16>(o);
   }
 }
 
@@ -516,69 +531,39 @@ hipError_t launch_to_bf16(const float* in, void* out, int64_t n, hipStream_t st)
 }
 
 // ------------------------------------------------------------------ launches
-namespace {
-
-// The direct-load ring needs bf16, a hidden width of whole ring turns, a
-// whole 256-column tile of vocabulary and operands within its 32-bit offsets.
-bool ring_fits(int elem, int64_t C, int64_t d, int64_t V) {
+bool logp_ring_fits(int elem, int64_t C, int64_t d, int64_t V) {
   return elem == 2 && d % kDmaKMult == 0 && V >= kBN && fits32(C * d * 2) && fits32(d * V * 2);
 }
 
-template <class Main, class E>
-void fwd(const LogpFwdArgs& a, bool entropy, hipStream_t st) {
+hipError_t launch_logp_fwd(const LogpFwdArgs& a, bool entropy, hipStream_t st) {
   const dim3 grid(a.nrb * a.S), block(kThreads);
   if (entropy && a.zout)
-    hipLaunchKernelGGL((logp_fwd_kernel<Main, E, true, true>), grid, block, 0, st, a);
+    hipLaunchKernelGGL((logp_fwd_kernel<true, true>), grid, block, 0, st, a);
   else if (entropy)
-    hipLaunchKernelGGL((logp_fwd_kernel<Main, E, true, false>), grid, block, 0, st, a);
+    hipLaunchKernelGGL((logp_fwd_kernel<true, false>), grid, block, 0, st, a);
   else if (a.zout)
-    hipLaunchKernelGGL((logp_fwd_kernel<Main, E, false, true>), grid, block, 0, st, a);
+    hipLaunchKernelGGL((logp_fwd_kernel<false, true>), grid, block, 0, st, a);
   else
-    hipLaunchKernelGGL((logp_fwd_kernel<Main, E, false, false>), grid, block, 0, st, a);
+    hipLaunchKernelGGL((logp_fwd_kernel<false, false>), grid, block, 0, st, a);
+  return hipGetLastError();
 }
 
-template <class Main, class E>
-void dz(const LogpDzArgs& a, hipStream_t st) {
+hipError_t launch_logp_dz(const LogpDzArgs& a, hipStream_t st) {
   const dim3 grid(a.nrb * a.S), block(kThreads);
   if (a.ge)
-    hipLaunchKernelGGL((logp_dz_kernel<Main, E, true>), grid, block, 0, st, a);
+    hipLaunchKernelGGL(logp_dz_kernel<true>, grid, block, 0, st, a);
   else
-    hipLaunchKernelGGL((logp_dz_kernel<Main, E, false>), grid, block, 0, st, a);
-}
-
-}  // namespace
-
-hipError_t launch_logp_fwd(int elem, const LogpFwdArgs& a, bool entropy, hipStream_t st) {
-  if (ring_fits(elem, a.C, a.d, a.V))
-    fwd<DmaNN<kBN>, Bf16>(a, entropy, st);
-  else if (elem == 2)
-    fwd<GenNN<Bf16, kBN>, Bf16>(a, entropy, st);
-  else
-    fwd<GenNN<F32, kBN>, F32>(a, entropy, st);
+    hipLaunchKernelGGL(logp_dz_kernel<false>, grid, block, 0, st, a);
   return hipGetLastError();
 }
 
-hipError_t launch_logp_dz(int elem, const LogpDzArgs& a, hipStream_t st) {
-  if (ring_fits(elem, a.C, a.d, a.V))
-    dz<DmaNN<kBN>, Bf16>(a, st);
-  else if (elem == 2)
-    dz<GenNN<Bf16, kBN>, Bf16>(a, st);
-  else
-    dz<GenNN<F32, kBN>, F32>(a, st);
-  return hipGetLastError();
-}
-
-hipError_t launch_logp_dz_from_z(int elem, const LogpDzArgs& a, hipStream_t st) {
-  const int64_t pieces = (a.V * elem + kRowB - 1) / kRowB;
+hipError_t launch_logp_dz_from_z(const LogpDzArgs& a, hipStream_t st) {
+  const int64_t pieces = (a.V * 2 + kRowB - 1) / kRowB;
   const dim3 grid((unsigned)(pieces < kFzRanges ? pieces : kFzRanges), (unsigned)(a.C / kFzRows)), block(256);
-  if (elem == 2 && a.ge)
-    hipLaunchKernelGGL((logp_dz_from_z_kernel<Bf16, true>), grid, block, 0, st, a);
-  else if (elem == 2)
-    hipLaunchKernelGGL((logp_dz_from_z_kernel<Bf16, false>), grid, block, 0, st, a);
-  else if (a.ge)
-    hipLaunchKernelGGL((logp_dz_from_z_kernel<F32, true>), grid, block, 0, st, a);
+  if (a.ge)
+    hipLaunchKernelGGL(logp_dz_from_z_kernel<true>, grid, block, 0, st, a);
   else
-    hipLaunchKernelGGL((logp_dz_from_z_kernel<F32, false>), grid, block, 0, st, a);
+    hipLaunchKernelGGL(logp_dz_from_z_kernel<false>, grid, block, 0, st, a);
   return hipGetLastError();
 }
 

@@ -1,0 +1,495 @@
+// Token log-probabilities, dZ, dH and dW on the register-fed tiles of
+// kd_direct.h: float32 of any size, and bf16 where the 256 x 256 ring tiles of
+// kd_logp.hip would leave most of the chip idle or do not apply.
+//
+//   forward  a = W (128 columns), b = H rows      z = W^T H^T, then each row's (m, l, e, x) record per tile
+//   dZ       the same product; each row becomes its dZ (row-major)
+//   dH       a = W rows (128 of d), b = dZ rows   contraction over the vocabulary
+//   dW       a = dZ (128 columns), b = H columns  contraction over the rows
+//
+// The mathematics is that of kd_logp.hip.  Bounds: a few rows, the read of W
+// (each workgroup streams its columns once, 16 KB a wave in flight); many
+// rows, float32, the matrix cores (64 instructions of 64 cycles per 64 KB of
+// operands).
+#include <type_traits>
+
+#include "kd_direct.h"
+#include "kd_policy.h"
+
+namespace kd {
+
+namespace {
+
+constexpr int kDirThreads = 256;
+
+__device__ inline long chunk_rows_of(const RowSet& rs) {
+  return rs.rows ? min((long)rs.C, (long)*rs.count - (long)rs.c0) : min((long)rs.C, (long)(rs.T - rs.c0));
+}
+__device__ inline long row_at(const RowSet& rs, long i) { return rs.rows ? rs.rows[rs.c0 + i] : rs.c0 + i; }
+
+// over the eight lanes of a row
+__device__ inline float row_max(float v) {
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) v = fmaxf(v, __shfl_xor(v, o));
+  return v;
+}
+__device__ inline float row_sum(float v) {
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) v += __shfl_xor(v, o);
+  return v;
+}
+__device__ inline float at4(const float4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+
+template <int R>
+__device__ inline void zero(f32x16_t (&acc)[4][R]) {
+#pragma unroll
+  for (int a = 0; a < 4; ++a)
+#pragma unroll
+    for (int b = 0; b < R; ++b)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[a][b][i] = 0.f;
+}
+
+// The product of W's columns [n0, n0 + 128) and the chunk's rows [r0, r0 + 32 R),
+// the contraction split over the four waves.
+template <class E, int R>
+__device__ inline void logits_tile(const LogpDirectArgs& a, long M, long r0, int n0, f32x16_t (&acc)[4][R]) {
+  constexpr int U = 2;
+  const int lane = threadIdx.x & 63, m = lane & 31;
+  ColsN<E, U> wl;
+  // a lane past the last column reads the last four: its results are left out
+  wl.init(a.W, a.V * E::kElem, (int)a.d, min(n0 + 4 * m, (int)a.V - 4));
+  RowsK<E, R, U> hl;
+  hl.K = (int)a.d;
+#pragma unroll
+  for (int b = 0; b < R; ++b) hl.row(b, a.H + row_at(a.rs, min(r0 + 32 * b + m, M - 1)) * a.d * E::kElem);
+  int kb, ke;
+  k_range((int)a.d, kDirStep<E, U>, wave_id(), 4, kb, ke);
+  zero(acc);
+  direct_contract<E, U>(wl, hl, kb, ke, acc);
+}
+
+}  // namespace
+
+// ------------------------------------------------------------------ forward
+template <class E, int R, bool kEnt>
+__global__ __launch_bounds__(kDirThreads, R == 4 ? 1 : 2) void logp_direct_fwd_kernel(LogpDirectArgs a, int nrb) {
+  __shared__ __attribute__((aligned(16))) float reg[4 * kDirRegion];
+  const long M = chunk_rows_of(a.rs);
+  const int id = xcd_remap(blockIdx.x, gridDim.x);  // row blocks of one W panel run together on one XCD
+  const long r0 = (long)(id % nrb) * 32 * R;
+  const int tile = id / nrb, n0 = tile * kDirA;
+  if (r0 >= M) return;
+  const int V = (int)a.V, lane = threadIdx.x & 63;
+  const int mine = 8 * wave_id() + (lane >> 3);  // the row of each block this lane will get
+  int label[R];  // relative to the tile
+#pragma unroll
+  for (int b = 0; b < R; ++b) {
+    const long i = r0 + 32 * b + mine;
+    label[b] = i < M ? (int)((long)a.tokens[row_at(a.rs, i)] - a.v0 - n0) : -1;
+  }
+  f32x16_t acc[4][R];
+  logits_tile<E, R>(a, M, r0, n0, acc);
+  float4* part = reinterpret_cast<float4*>(a.part) + (long)tile * a.rs.C + r0;
+  const int cols = min(kDirA, V - n0);  // a multiple of 4
+  direct_rows<ColsN<E, 2>, R, 4>(acc, reg, [&](int b, int m, int q, const float4 (&z)[4]) {
+    const int i = 32 * b + m;
+    if (a.z && r0 + i < M) {
+      float* zr = a.z + (r0 + i) * a.ldz + n0 + 4 * q;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (4 * q + 32 * j < cols) *reinterpret_cast<float4*>(zr + 32 * j) = z[j];
+    }
+    float mx = -INFINITY, x = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (4 * q + 32 * j >= cols) continue;
+      mx = fmaxf(mx, fmaxf(fmaxf(z[j].x, z[j].y), fmaxf(z[j].z, z[j].w)));
+      if ((label[b] >> 2) == q + 8 * j) x = at4(z[j], label[b] & 3);
+    }
+    mx = row_max(mx) * a.c2;
+    float l = 0.f, e = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (4 * q + 32 * j >= cols) continue;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float w = fmaf(at4(z[j], k), a.c2, -mx), p = fast_exp2(w);
+        l += p;
+        if constexpr (kEnt) e = fmaf(p, w, e);
+      }
+    }
+    l = row_sum(l);
+    if constexpr (kEnt) e = row_sum(e);
+    x = row_sum(x);
+    if (q == 0 && r0 + i < M) part[i] = make_float4(mx, l, e, x);
+  });
+}
+
+// ------------------------------------------------------------------ dZ
+namespace {
+
+// -q (A + B log2 q), and ga more at the token
+template <bool kEnt>
+__device__ inline float dz_of(float z, float c2, float L2, float A, float B) {
+  const float lq = fmaf(z, c2, -L2), q = fast_exp2(lq);
+  if constexpr (kEnt) return -q * fmaf(B, lq, A);
+  return -q * A;
+}
+
+struct DzConst {
+  float L2, A, B, ga;
+  int label;
+};
+__device__ inline DzConst dz_const(const LogpDirectArgs& a, bool rv, long t) {
+  DzConst k{0.f, 0.f, 0.f, 0.f, -1};
+  if (!rv) return k;
+  k.ga = a.g ? a.g[t] * a.inv_tau : 0.f;
+  const float gb = a.ge ? a.ge[t] * a.inv_tau : 0.f;
+  k.L2 = a.lse[t] * kLog2e;
+  k.A = a.ge ? fmaf(gb, a.ent[t], k.ga) : k.ga;
+  k.B = gb * kLn2;
+  k.label = (int)((long)a.tokens[t] - a.v0);
+  return k;
+}
+
+// the four columns from c
+template <bool kEnt>
+__device__ inline float4 dz_four(float4 z, const DzConst& k, float c2, long c) {
+  return make_float4(dz_of<kEnt>(z.x, c2, k.L2, k.A, k.B) + (k.label == c ? k.ga : 0.f),
+                     dz_of<kEnt>(z.y, c2, k.L2, k.A, k.B) + (k.label == c + 1 ? k.ga : 0.f),
+                     dz_of<kEnt>(z.z, c2, k.L2, k.A, k.B) + (k.label == c + 2 ? k.ga : 0.f),
+                     dz_of<kEnt>(z.w, c2, k.L2, k.A, k.B) + (k.label == c + 3 ? k.ga : 0.f));
+}
+
+template <class E>
+__device__ inline void store4(char* p, float4 x) {
+  if constexpr (E::kElem == 2)
+    *reinterpret_cast<uint2*>(p) = make_uint2(Bf16::pack2(x.x, x.y), Bf16::pack2(x.z, x.w));
+  else
+    *reinterpret_cast<float4*>(p) = x;
+}
+
+}  // namespace
+
+template <class E, int R, bool kEnt>
+__global__ __launch_bounds__(kDirThreads, R == 1 ? 2 : 1) void logp_direct_dz_kernel(LogpDirectArgs a, int nrb) {
+  __shared__ __attribute__((aligned(16))) float reg[4 * kDirRegion];
+  const long M = chunk_rows_of(a.rs);
+  const int id = xcd_remap(blockIdx.x, gridDim.x);
+  const long r0 = (long)(id % nrb) * 32 * R;
+  const int n0 = id / nrb * kDirA;
+  if (r0 >= (M + 127) / 128 * 128) return;
+  const int V = (int)a.V, lane = threadIdx.x & 63, mine = 8 * wave_id() + (lane >> 3);
+  DzConst k[R];
+#pragma unroll
+  for (int b = 0; b < R; ++b) {
+    const long i = r0 + 32 * b + mine;
+    k[b] = dz_const(a, i < M, i < M ? row_at(a.rs, i) : 0);
+  }
+  f32x16_t acc[4][R];
+  logits_tile<E, R>(a, M, min(r0, M - 1), n0, acc);
+  direct_rows<ColsN<E, 2>, R, 4>(acc, reg, [&](int b, int m, int q, const float4 (&z)[4]) {
+    const long i = r0 + 32 * b + m;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int c = n0 + 4 * q + 32 * j;
+      if (c >= V) break;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i < M) o = dz_four<kEnt>(z[j], k[b], a.c2, c);
+      store4<E>(a.dz + (i * a.ldz + c) * E::kElem, o);
+    }
+  });
+}
+
+// From stored logits: a block takes one row and up to kFzCols columns, eight per thread.
+constexpr int kFzCols = 2048;
+template <class E, bool kEnt>
+__global__ __launch_bounds__(256) void logp_direct_dz_from_z_kernel(LogpDirectArgs a) {
+  const long M = chunk_rows_of(a.rs);
+  const long i = blockIdx.y;
+  if (i >= (M + 127) / 128 * 128) return;
+  const DzConst k = dz_const(a, i < M, i < M ? row_at(a.rs, i) : 0);
+  const long c0 = (long)blockIdx.x * kFzCols + threadIdx.x * 4;
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const long c = c0 + q * (kFzCols / 2);
+    if (c >= a.V) break;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (i < M) o = dz_four<kEnt>(*reinterpret_cast<const float4*>(a.z + i * a.ldz + c), k, a.c2, c);
+    store4<E>(a.dz + (i * a.ldz + c) * E::kElem, o);
+  }
+}
+
+// ------------------------------------------------------------------ dH
+// Tile: 128 of d x 32 R rows, vocabulary range s of S over the four waves.
+// S = 1: dH itself; else the range's float32 part [S][C][d].
+template <class E, int R, class O>
+__global__ __launch_bounds__(kDirThreads, 1) void logp_direct_dh_kernel(LogpDirectArgs a, int nrb, int nda, int S,
+                                                                        float* part, char* dH) {
+  constexpr int U = 4;
+  __shared__ __attribute__((aligned(16))) float reg[4 * kDirRegion];
+  const long M = chunk_rows_of(a.rs);
+  int id = xcd_remap(blockIdx.x, gridDim.x);
+  const long r0 = (long)(id % nrb) * 32 * R;
+  id /= nrb;
+  const int d0 = (id % nda) * kDirA, s = id / nda;
+  if (r0 >= M) return;
+  const int lane = threadIdx.x & 63, m = lane & 31, d = (int)a.d;
+  RowsK<E, 4, U> wl;
+  RowsK<E, R, U> zl;
+  wl.K = zl.K = (int)a.V;
+#pragma unroll
+  for (int f = 0; f < 4; ++f) wl.row(f, a.W + (long)min(d0 + 32 * f + m, d - 1) * a.V * E::kElem);
+#pragma unroll
+  for (int b = 0; b < R; ++b) zl.row(b, a.dz + min(r0 + 32 * b + m, M - 1) * a.ldz * E::kElem);
+  int kb, ke;
+  k_range((int)a.V, kDirStep<E, U>, 4 * s + wave_id(), 4 * S, kb, ke);
+  f32x16_t acc[4][R];
+  zero(acc);
+  direct_contract<E, U>(wl, zl, kb, ke, acc);
+  direct_rows<RowsK<E, 4, U>, R, 4>(acc, reg, [&](int b, int mm, int q, const float4 (&x)[4]) {
+    const long i = r0 + 32 * b + mm;
+    if (i >= M) return;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int c = d0 + 4 * q + 32 * j;
+      if (c >= d) break;
+      if (S > 1)
+        *reinterpret_cast<float4*>(part + ((long)s * a.rs.C + i) * d + c) = x[j];
+      else
+        store4<O>(dH + (row_at(a.rs, i) * d + c) * O::kElem, x[j]);
+    }
+  });
+}
+
+// dH of a row = its S parts in order, four elements per thread
+template <class O>
+__global__ __launch_bounds__(256) void logp_direct_reduce_kernel(RowSet rs, const float* part, int S, long d,
+                                                                 char* dH) {
+  const long q = (long)blockIdx.x * 256 + threadIdx.x, d4 = d / 4;
+  const long i = q / d4, j = (q - i * d4) * 4;
+  if (i >= chunk_rows_of(rs)) return;
+  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s = 0; s < S; ++s) {
+    const float4 y = *reinterpret_cast<const float4*>(part + ((long)s * rs.C + i) * d + j);
+    x.x += y.x;
+    x.y += y.y;
+    x.z += y.z;
+    x.w += y.w;
+  }
+  store4<O>(dH + (row_at(rs, i) * d + j) * O::kElem, x);
+}
+
+// ------------------------------------------------------------------ dW
+// KS = 4: one 128 x 128 tile of [V] x [d], the rows split over the four
+// waves; KS = 1: four tiles side by side in d, all rows each.
+template <class E, int KS, class O>
+__global__ __launch_bounds__(kDirThreads, 1) void logp_direct_dw_kernel(LogpDirectArgs a, const char* Hc, int nda,
+                                                                        const float* add, char* out) {
+  constexpr int U = E::kElem == 4 ? 1 : 2;  // two chunks of float32 would not leave room for the accumulators
+  __shared__ __attribute__((aligned(16))) float reg[4 * kDirRegion];
+  const long M = max(0L, chunk_rows_of(a.rs));
+  const int id = xcd_remap(blockIdx.x, gridDim.x);
+  const int w = wave_id(), lane = threadIdx.x & 63, m = lane & 31;
+  const int d0 = ((id % nda) * (KS == 1 ? 4 : 1) + (KS == 1 ? w : 0)) * kDirA, n0 = id / nda * kDirA;
+  const int d = (int)a.d, V = (int)a.V;
+  ColsN<E, U> zl, hl;
+  zl.init(a.dz, a.ldz * E::kElem, (int)((M + 127) / 128 * 128), min(n0 + 4 * m, V - 4));  // zero rows behind the last
+  hl.init(Hc, (long)d * E::kElem, (int)M, min(d0 + 4 * m, d - 4));
+  int kb, ke;
+  k_range((int)M, kDirStep<E, U>, KS == 1 ? 0 : w, KS, kb, ke);
+  f32x16_t acc[4][4];
+  zero(acc);
+  direct_contract<E, U>(zl, hl, kb, ke, acc);
+  direct_rows<ColsN<E, U>, 4, KS>(acc, reg, [&](int b, int mm, int q, const float4 (&x)[4]) {
+    const int i = d0 + ColsN<E, U>::index(b, mm);
+    if (i >= d) return;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int c = n0 + 4 * q + 32 * j;
+      if (c >= V) break;
+      const long at = (long)i * V + c;
+      float4 v = x[j];
+      if (add) {
+        const float4 y = *reinterpret_cast<const float4*>(add + at);
+        v = make_float4(v.x + y.x, v.y + y.y, v.z + y.z, v.w + y.w);
+      }
+      store4<O>(out + at * O::kElem, v);
+    }
+  });
+}
+
+// ------------------------------------------------------------------ rows of the mask
+// A block of 256 threads takes 64 rows of the mask: how many valid ones come
+// before them (counted anew by every block: at most T bytes), where each of
+// its own goes, and the copying.
+__global__ __launch_bounds__(256) void logp_prep_kernel(const uint8_t* mask, long T, int32_t* rows, int32_t* count,
+                                                        const char* H, long rowb, long c0, long C, char* Hc, char* dH,
+                                                        long dhb) {
+  __shared__ int red[4];
+  __shared__ int pos[64];  // compacted position, or -1
+  const long t0 = (long)blockIdx.x * 64;
+  int n = 0;
+  for (long t = (long)threadIdx.x * 8; t < t0; t += 2048) {  // t0 is a multiple of 64: whole eights
+    uint2 v;
+    __builtin_memcpy(&v, mask + t, 8);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) n += ((v.x >> (8 * i) & 255u) != 0) + ((v.y >> (8 * i) & 255u) != 0);
+  }
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) n += __shfl_xor(n, o);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = n;
+  __syncthreads();
+  const int before = red[0] + red[1] + red[2] + red[3];
+  if (threadIdx.x < 64) {
+    const long t = t0 + threadIdx.x;
+    const bool on = t < T && mask[t] != 0;
+    const unsigned long long b = __ballot(on);
+    const int at = before + __popcll(b & ((1ull << threadIdx.x) - 1));
+    pos[threadIdx.x] = on ? at : -1;
+    if (on) rows[at] = (int32_t)t;
+    if (t0 + 64 >= T && threadIdx.x == 0) *count = before + __popcll(b);
+  }
+  __syncthreads();
+  for (int r = 0; r < 64; ++r) {
+    const long t = t0 + r;
+    if (t >= T) break;
+    const int at = pos[r];
+    if (at < 0) {
+      if (dH)
+        for (long q = (long)threadIdx.x * 16; q < dhb; q += 4096) *reinterpret_cast<u32x4_t*>(dH + t * dhb + q) = zero4();
+    } else if (Hc && at >= c0 && at < c0 + C) {
+      for (long q = (long)threadIdx.x * 16; q < rowb; q += 4096)
+        *reinterpret_cast<u32x4_t*>(Hc + (at - c0) * rowb + q) = ld16(H + t * rowb + q);
+    }
+  }
+}
+
+hipError_t launch_logp_prep(const uint8_t* mask, int64_t T, int32_t* rows, int32_t* count, const void* H,
+                            int64_t row_bytes, int64_t c0, int64_t C, void* Hc, void* dH, int64_t dh_row_bytes,
+                            hipStream_t st) {
+  hipLaunchKernelGGL(logp_prep_kernel, dim3((unsigned)((T + 63) / 64)), dim3(256), 0, st, mask, (long)T, rows, count,
+                     static_cast<const char*>(H), (long)row_bytes, (long)c0, (long)C, static_cast<char*>(Hc),
+                     static_cast<char*>(dH), (long)dh_row_bytes);
+  return hipGetLastError();
+}
+
+// ------------------------------------------------------------------ launches
+namespace {
+
+int64_t rows_upto(const RowSet& rs) { return rs.C < rs.T - rs.c0 ? rs.C : rs.T - rs.c0; }
+int cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
+
+template <class E, int R>
+void fwd(const LogpDirectArgs& a, bool entropy, hipStream_t st) {
+  const int nrb = cdiv(rows_upto(a.rs), 32 * R);
+  const dim3 grid((unsigned)(nrb * cdiv(a.V, kDirA)));
+  if (entropy)
+    hipLaunchKernelGGL((logp_direct_fwd_kernel<E, R, true>), grid, dim3(kDirThreads), 0, st, a, nrb);
+  else
+    hipLaunchKernelGGL((logp_direct_fwd_kernel<E, R, false>), grid, dim3(kDirThreads), 0, st, a, nrb);
+}
+template <class E, int R>
+void dz(const LogpDirectArgs& a, hipStream_t st) {
+  const int nrb = cdiv(cdiv(rows_upto(a.rs), 128) * 128, 32 * R);  // to the zero rows' end
+  const dim3 grid((unsigned)(nrb * cdiv(a.V, kDirA)));
+  if (a.ge)
+    hipLaunchKernelGGL((logp_direct_dz_kernel<E, R, true>), grid, dim3(kDirThreads), 0, st, a, nrb);
+  else
+    hipLaunchKernelGGL((logp_direct_dz_kernel<E, R, false>), grid, dim3(kDirThreads), 0, st, a, nrb);
+}
+// Block columns of rows per tile: 1, 2 or 4, no more than hold the rows, and
+// fewer where the tiles would not go round the CUs (at 4 a tile's operands are
+// used best; at 128 rows of a 4096 x 4096 float32 head 1 takes 99 us, 4 takes 261).
+template <class F>
+void by_rows(int64_t n, int64_t V, F&& f) {
+  const int64_t cols = cdiv(V, kDirA);
+  if (n > 64 && cdiv(n, 128) * cols >= 200) f(std::integral_constant<int, 4>());
+  else if (n > 32 && cdiv(n, 64) * cols >= 200) f(std::integral_constant<int, 2>());
+  else f(std::integral_constant<int, 1>());
+}
+
+}  // namespace
+
+hipError_t launch_logp_direct_fwd(int elem, const LogpDirectArgs& a, bool entropy, hipStream_t st) {
+  by_rows(rows_upto(a.rs), a.V, [&](auto r) {
+    if (elem == 2) fwd<Bf16, decltype(r)::value>(a, entropy, st);
+    else fwd<F32, decltype(r)::value>(a, entropy, st);
+  });
+  return hipGetLastError();
+}
+
+hipError_t launch_logp_direct_dz(int elem, const LogpDirectArgs& a, hipStream_t st) {
+  by_rows(rows_upto(a.rs), a.V, [&](auto r) {
+    if (elem == 2) dz<Bf16, decltype(r)::value>(a, st);
+    else dz<F32, decltype(r)::value>(a, st);
+  });
+  return hipGetLastError();
+}
+
+hipError_t launch_logp_direct_dz_from_z(int elem, const LogpDirectArgs& a, hipStream_t st) {
+  const dim3 grid((unsigned)cdiv(a.V, kFzCols), (unsigned)(cdiv(rows_upto(a.rs), 128) * 128));
+  if (elem == 2 && a.ge)
+    hipLaunchKernelGGL((logp_direct_dz_from_z_kernel<Bf16, true>), grid, dim3(256), 0, st, a);
+  else if (elem == 2)
+    hipLaunchKernelGGL((logp_direct_dz_from_z_kernel<Bf16, false>), grid, dim3(256), 0, st, a);
+  else if (a.ge)
+    hipLaunchKernelGGL((logp_direct_dz_from_z_kernel<F32, true>), grid, dim3(256), 0, st, a);
+  else
+    hipLaunchKernelGGL((logp_direct_dz_from_z_kernel<F32, false>), grid, dim3(256), 0, st, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_logp_direct_dh(int elem, const LogpDirectArgs& a, int S, float* part, void* dH, int dh_elem,
+                                 hipStream_t st) {
+  const int64_t n = rows_upto(a.rs);
+  const int nda = cdiv(a.d, kDirA);
+  char* out = static_cast<char*>(dH);
+  auto go = [&](auto r) {
+    constexpr int R = decltype(r)::value;
+    const int nrb = cdiv(n, 32 * R);
+    const dim3 grid((unsigned)(nrb * nda * S)), block(kDirThreads);
+    if (elem == 4)
+      hipLaunchKernelGGL((logp_direct_dh_kernel<F32, R, F32>), grid, block, 0, st, a, nrb, nda, S, part, out);
+    else if (dh_elem == 4)
+      hipLaunchKernelGGL((logp_direct_dh_kernel<Bf16, R, F32>), grid, block, 0, st, a, nrb, nda, S, part, out);
+    else
+      hipLaunchKernelGGL((logp_direct_dh_kernel<Bf16, R, Bf16>), grid, block, 0, st, a, nrb, nda, S, part, out);
+  };
+  if (n <= 32) go(std::integral_constant<int, 1>());
+  else go(std::integral_constant<int, 2>());
+  if (S > 1) {
+    const dim3 grid((unsigned)cdiv(n * (a.d / 4), 256));
+    if (dh_elem == 2)
+      hipLaunchKernelGGL(logp_direct_reduce_kernel<Bf16>, grid, dim3(256), 0, st, a.rs, part, S, (long)a.d, out);
+    else
+      hipLaunchKernelGGL(logp_direct_reduce_kernel<F32>, grid, dim3(256), 0, st, a.rs, part, S, (long)a.d, out);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_logp_direct_dw(int elem, const LogpDirectArgs& a, const void* Hc, const float* add32, void* out,
+                                 int out_elem, hipStream_t st) {
+  const int nda = cdiv(a.d, kDirA), nv = cdiv(a.V, kDirA);
+  // four waves on a tile where there are too few tiles for every wave to have its own
+  const bool split = (int64_t)nda * nv < 1024 && rows_upto(a.rs) > 64;
+  const int n4 = split ? nda : cdiv(nda, 4);
+  const dim3 grid((unsigned)(n4 * nv)), block(kDirThreads);
+  const char* h = static_cast<const char*>(Hc);
+  char* o = static_cast<char*>(out);
+  auto go = [&](auto ks) {
+    constexpr int KS = decltype(ks)::value;
+    if (elem == 4)
+      hipLaunchKernelGGL((logp_direct_dw_kernel<F32, KS, F32>), grid, block, 0, st, a, h, n4, add32, o);
+    else if (out_elem == 4)
+      hipLaunchKernelGGL((logp_direct_dw_kernel<Bf16, KS, F32>), grid, block, 0, st, a, h, n4, add32, o);
+    else
+      hipLaunchKernelGGL((logp_direct_dw_kernel<Bf16, KS, Bf16>), grid, block, 0, st, a, h, n4, add32, o);
+  };
+  if (split) go(std::integral_constant<int, 4>());
+  else go(std::integral_constant<int, 1>());
+  return hipGetLastError();
+}
+
+}  // namespace kd

@@ -35,8 +35,8 @@ struct TileAt {
 };
 
 // ------------------------------------------------------------------ shared stage product
-// Both operands k-contiguous rows; kT: into transposed accumulators (mma_frags_t).
-template <class E, int BN, bool kT = false>
+// Both operands k-contiguous rows.
+template <class E, int BN>
 __device__ inline void mma_stage_rows(const char* As, const char* Bs, f32x16_t (&acc)[4][BN / 64]) {
   constexpr int NB = BN / 64;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
@@ -52,12 +52,7 @@ __device__ inline void mma_stage_rows(const char* As, const char* Bs, f32x16_t (
 #pragma unroll
     for (int mb = 0; mb < 4; ++mb)
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
-        if constexpr (kT)
-          E::mma(acc[mb][nb], b[nb], a[mb]);
-        else
-          E::mma(acc[mb][nb], a[mb], b[nb]);
-      }
+      for (int nb = 0; nb < NB; ++nb) E::mma(acc[mb][nb], a[mb], b[nb]);
   }
 }
 
@@ -193,19 +188,17 @@ struct GenNN {
     nst = (kbytes + kRowB - 1) / kRowB;
   }
 
-  // tiles t = 0 .. ntiles-1 described by at(t); done(t, acc) after each.
-  // kT: the accumulators hold the transposed tile (mma_frags_t).
-  template <bool kT = false, class At, class Done>
+  // tiles t = 0 .. ntiles-1 described by at(t); done(t, acc) after each
+  template <class At, class Done>
   __device__ inline void run(const Slots& sl, int ntiles, At&& at, Done&& done) {
     f32x16_t acc[4][BN / 64];
     for (int t = 0; t < ntiles; ++t) {
       const TileAt ta = at(t);
-      tile<kT>(sl, ta.n0, acc, ta.a_off);
+      tile(sl, ta.n0, acc, ta.a_off);
       done(t, acc);
     }
   }
 
-  template <bool kT = false>
   __device__ inline void tile(const Slots& sl, long n0, f32x16_t (&acc)[4][BN / 64], long a_off = 0) {
     constexpr int KS = kRowB / E::kElem;
     bl.base = B + n0 * E::kElem;
@@ -221,7 +214,7 @@ struct GenNN {
           al.store(da);
           bl.store(db);
         },
-        [&](const char* as, const char* bs) { mma_stage_rows<E, BN, kT>(as, bs, acc); });
+        [&](const char* as, const char* bs) { mma_stage_rows<E, BN>(as, bs, acc); });
   }
 };
 

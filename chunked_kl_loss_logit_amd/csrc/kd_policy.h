@@ -12,6 +12,13 @@
 namespace kd {
 
 // ---------------------------------------------------------------- token log-probabilities
+// The rows of one chunk: valid rows [c0, c0 + C) of T, listed in rows and
+// counted in *count, or without a mask (rows null) simply rows c0 + i.
+struct RowSet {
+  const int32_t* rows;
+  const int32_t* count;
+  int64_t c0, C, T;
+};
 // One record per (vocabulary split, row): with y = z log2(e) / tau over the
 // split's columns, (m, l, e, x) = (max y, sum 2^(y - m), sum 2^(y - m) (y - m),
 // z at the row's token or 0).
@@ -29,7 +36,9 @@ struct LogpFwdArgs {
   int group;
   float c2;               // log2(e) / tau
 };
-hipError_t launch_logp_fwd(int elem, const LogpFwdArgs& a, bool entropy, hipStream_t st);
+// whether the ring tiles take a head with chunks of C rows
+bool logp_ring_fits(int elem, int64_t C, int64_t d, int64_t V);
+hipError_t launch_logp_fwd(const LogpFwdArgs& a, bool entropy, hipStream_t st);
 
 // Per-row outputs of compacted rows [c0, c0 + C) from the records; with
 // zero_masked, also zeroes the outputs of every masked row.  rec != nullptr:
@@ -40,9 +49,9 @@ struct LogpOut {
   float* entropy;  // nullable
   float4* rec;     // nullable
 };
-hipError_t launch_logp_combine(const float* part, int S, Compact c, const uint8_t* mask, const int32_t* tokens,
-                               int64_t T, int64_t V, int64_t c0, int64_t C, float c2, const LogpOut& o,
-                               bool zero_masked, hipStream_t st);
+hipError_t launch_logp_combine(const float* part, int S, const RowSet& rs, const uint8_t* mask,
+                               const int32_t* tokens, int64_t V, float c2, const LogpOut& o, bool zero_masked,
+                               hipStream_t st);
 // The same outputs from R shards' records rec [R][T].
 hipError_t launch_logp_shard_combine(const float4* rec, int R, int64_t T, const uint8_t* mask, float c2,
                                      const LogpOut& o, hipStream_t st);
@@ -65,8 +74,38 @@ struct LogpDzArgs {
   int group;
   float c2, inv_tau;
 };
-hipError_t launch_logp_dz(int elem, const LogpDzArgs& a, hipStream_t st);
-hipError_t launch_logp_dz_from_z(int elem, const LogpDzArgs& a, hipStream_t st);
+hipError_t launch_logp_dz(const LogpDzArgs& a, hipStream_t st);
+hipError_t launch_logp_dz_from_z(const LogpDzArgs& a, hipStream_t st);
+
+// ---------------------------------------------------------------- the same without LDS-staged tiles
+// rows and *count from the mask (not null); the chunk's rows of H packed into
+// Hc [C][row_bytes] (nullable); masked rows of dH (nullable) zeroed.
+hipError_t launch_logp_prep(const uint8_t* mask, int64_t T, int32_t* rows, int32_t* count, const void* H,
+                            int64_t row_bytes, int64_t c0, int64_t C, void* Hc, void* dH, int64_t dh_row_bytes,
+                            hipStream_t st);
+constexpr int kDirectCols = 128;  // vocabulary columns per tile
+struct LogpDirectArgs {
+  RowSet rs;
+  const char* H;          // [T][d]
+  const char* W;          // [d][V]
+  const int32_t* tokens;
+  int64_t d, V, ldz;
+  int32_t v0;
+  float c2, inv_tau;
+  float* part;            // forward: records [tiles][C][4] as LogpFwdArgs::part
+  float* z;               // forward: nullable, logits out [C][ldz]; dz from z: the logits
+  const float *lse, *ent, *g, *ge;
+  char* dz;               // backward: [roundup(C, 128)][ldz], row-major; zero rows up to a multiple of 128
+};
+hipError_t launch_logp_direct_fwd(int elem, const LogpDirectArgs& a, bool entropy, hipStream_t st);
+hipError_t launch_logp_direct_dz(int elem, const LogpDirectArgs& a, hipStream_t st);
+hipError_t launch_logp_direct_dz_from_z(int elem, const LogpDirectArgs& a, hipStream_t st);
+// dH of the chunk: dz . W^T, the vocabulary split S ways (part [S][C][d], summed in order; S = 1: not used)
+hipError_t launch_logp_direct_dh(int elem, const LogpDirectArgs& a, int S, float* part, void* dH, int dh_elem,
+                                 hipStream_t st);
+// dW of the chunk: sum over its rows of Hc^T dz, plus add32 (nullable), to out (float32 or bf16)
+hipError_t launch_logp_direct_dw(int elem, const LogpDirectArgs& a, const void* Hc, const float* add32, void* out,
+                                 int out_elem, hipStream_t st);
 
 // out[i] = bf16(in[i]) for i < n, n a multiple of 8, both 16-byte aligned
 hipError_t launch_to_bf16(const float* in, void* out, int64_t n, hipStream_t st);

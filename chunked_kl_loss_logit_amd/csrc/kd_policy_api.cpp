@@ -9,27 +9,60 @@ using namespace kdh;
 namespace {
 
 // ---------------------------------------------------------------- token log-probabilities
+// Whether a head runs on the register-fed tiles (kd_direct.h) rather than the
+// 256 x 256 ring tiles: float32, shapes the ring does not take, and bf16
+// products too small to fill the ring's rounds of 256 workgroups.  A round
+// costs the ring the same however few of its rows and tiles are real; the
+// register-fed tiles run at 0.4 of a full round's rate.  Forward, us, ring /
+// register-fed: 32 x 4096 x 8192 84 / 31, 64 x 2048 x 128256 152 / 125, 128 x
+// 4096 x 32000 87 / 67, 512 x 4096 x 8192 88 / 63; on the other side 128 x 2048
+// x 128256 153 / 185, 256 x 4096 x 32000 95 / 124, 1024 x 4096 x 8192 94 / 119.
+bool use_direct(int64_t T, int64_t d, int64_t V, int elem) {
+  const int64_t C = chunk_of(T, V, elem, 0);
+  if (!kd::logp_ring_fits(elem, C, d, V)) return true;
+  const int64_t rounds = cdiv(cdiv(std::min(T, C), kd::kTileM) * cdiv(V, kd::kTileN), 256);
+  return std::min(T, C) * V < rounds * 7000000;
+}
+
 struct LogpPlan {
-  int ntiles;
-  int64_t Cf;  // rows per forward chunk
+  bool direct;
+  int ntiles;    // column tiles of the forward
+  int64_t Cf;    // rows per forward chunk
+  int64_t C, ldz;  // rows per backward chunk, columns of its dZ
+  int S_dh;      // direct: vocabulary ranges of dH
   size_t o_rows, o_count, o_part, o_hp_f, fwd_total;
-  ChunkPlan ch;
+  ChunkPlan ch;  // ring
+  size_t o_dz, o_hc, o_dhp;  // direct
   size_t o_dw32, total;  // float32 dW where a bf16 one adds up over chunks
 };
 
 LogpPlan plan_logp(int64_t T, int64_t d, int64_t V, int elem, int dw_elem, int64_t chunk_rows) {
   LogpPlan p{};
-  p.ntiles = (int)cdiv(V, kd::kTileN);
+  p.direct = use_direct(T, d, V, elem);
+  p.ntiles = (int)cdiv(V, p.direct ? kd::kDirectCols : kd::kTileN);
   p.Cf = chunk_of(T, V, elem, 0);
+  p.ldz = cdiv(V, kd::kTileN) * kd::kTileN;
   Carver cv;
   p.o_rows = cv.take((size_t)T * 4);
   p.o_count = cv.take(16);
   Carver fw = cv, bw = cv;  // the two calls' buffers overlap
-  p.o_part = fw.take((size_t)max_splits(p.ntiles) * p.Cf * 16);
-  p.o_hp_f = fw.take(panel_bytes(p.Cf, d * elem));
+  if (p.direct) {
+    p.o_part = fw.take((size_t)p.ntiles * p.Cf * 16);
+    p.C = chunk_of(T, V, elem, chunk_rows);
+    const int64_t n = std::min(p.C, T), units = cdiv(n, n <= 32 ? 32 : 64) * cdiv(d, 128);
+    // dH's vocabulary ranges: workgroups for every CU, at least 1 KB of W's rows each
+    p.S_dh = balanced_splits(units, cdiv(V * elem, 1024), std::max<int64_t>(1, cdiv(1024, units)));
+    p.o_dz = bw.take((size_t)up(p.C, 128) * p.ldz * elem);
+    p.o_hc = bw.take((size_t)p.C * d * elem);
+    p.o_dhp = bw.take(p.S_dh > 1 ? (size_t)p.S_dh * p.C * d * 4 : 0);
+  } else {
+    p.o_part = fw.take((size_t)max_splits(p.ntiles) * p.Cf * 16);
+    p.o_hp_f = fw.take(panel_bytes(p.Cf, d * elem));
+    p.ch = plan_chunk(T, d, V, elem, chunk_rows, bw);
+    p.C = p.ch.C;
+  }
   p.fwd_total = fw.off;
-  p.ch = plan_chunk(T, d, V, elem, chunk_rows, bw);
-  p.o_dw32 = bw.take(dw_elem == 2 ? (size_t)d * V * 4 : 0);
+  p.o_dw32 = bw.take(dw_elem == 2 && (!p.direct || p.C < T) ? (size_t)d * V * 4 : 0);
   p.total = std::max(fw.off, bw.off);
   return p;
 }
@@ -65,6 +98,34 @@ kd_status logp_fwd(const void* H, const void* W, const int32_t* tokens, const ui
   hipStream_t st = static_cast<hipStream_t>(stream);
   const kd::Compact c{at<int32_t>(workspace, p.o_rows), at<int32_t>(workspace, p.o_count)};
   float* part = at<float>(workspace, p.o_part);
+  const float c2 = (float)(1.4426950408889634 / (double)tau);
+  kd::RowSet rs{c.rows, c.count, 0, p.Cf, T};
+  if (p.direct) {
+    if (mask)
+      KD_LAUNCH("logp_prep", st,
+                kd::launch_logp_prep(mask, T, c.rows, c.count, H, d * elem, 0, T, nullptr, nullptr, 0, st));
+    else
+      rs.rows = rs.count = nullptr;
+    kd::LogpDirectArgs a{};
+    a.H = static_cast<const char*>(H);
+    a.W = static_cast<const char*>(W);
+    a.tokens = tokens;
+    a.d = d;
+    a.V = V;
+    a.ldz = p.ldz;
+    a.v0 = (int32_t)v0;
+    a.c2 = c2;
+    a.part = part;
+    for (int64_t c0 = 0; c0 < T; c0 += p.Cf) {
+      rs.c0 = c0;
+      a.rs = rs;
+      a.z = logits ? logits + c0 * p.ldz : nullptr;
+      KD_LAUNCH("logp_direct_fwd", st, kd::launch_logp_direct_fwd(elem, a, entropy, st));
+      KD_LAUNCH("logp_combine", st,
+                kd::launch_logp_combine(part, p.ntiles, rs, mask, tokens, V, c2, out, c0 == 0, st));
+    }
+    return KD_OK;
+  }
   char* hp = at<char>(workspace, p.o_hp_f);
   KD_LAUNCH("compact", st, kd::launch_compact(mask, T, c, st));
   kd::LogpFwdArgs a{};
@@ -73,24 +134,24 @@ kd_status logp_fwd(const void* H, const void* W, const int32_t* tokens, const ui
   a.c = c;
   a.tokens = tokens;
   a.part = part;
-  a.ldz = p.ch.ldz;
+  a.ldz = p.ldz;
   a.C = p.Cf;
   a.d = d;
   a.V = V;
   a.v0 = (int32_t)v0;
   a.ntiles = p.ntiles;
   a.group = kRasterGroup;
-  a.c2 = (float)(1.4426950408889634 / (double)tau);
+  a.c2 = c2;
   for (int64_t c0 = 0; c0 < T; c0 += p.Cf) {
     const ChunkShape sh = chunk_shape(T, c0, p.Cf, p.ntiles);
     KD_LAUNCH("gather_panels", st, kd::launch_gather_panels(H, d * elem, c, c0, p.Cf, hp, st));
-    a.c0 = c0;
-    a.zout = logits ? logits + c0 * p.ch.ldz : nullptr;
+    a.c0 = rs.c0 = c0;
+    a.zout = logits ? logits + c0 * p.ldz : nullptr;
     a.nrb = sh.nrb;
     a.S = sh.S;
-    KD_LAUNCH("logp_fwd_tile", st, kd::launch_logp_fwd(elem, a, entropy, st));
+    KD_LAUNCH("logp_fwd_tile", st, kd::launch_logp_fwd(a, entropy, st));
     KD_LAUNCH("logp_combine", st,
-              kd::launch_logp_combine(part, sh.S, c, mask, tokens, T, V, c0, p.Cf, a.c2, out, c0 == 0, st));
+              kd::launch_logp_combine(part, sh.S, rs, mask, tokens, V, c2, out, c0 == 0, st));
   }
   return KD_OK;
 }
@@ -127,6 +188,51 @@ kd_status logp_bwd(const void* H, const void* W, const int32_t* tokens, const ui
   KD_TRY(check_workspace(workspace, workspace_bytes, p.total));
 
   const kd::Compact c{at<int32_t>(workspace, p.o_rows), at<int32_t>(workspace, p.o_count)};
+  const float c2 = (float)(1.4426950408889634 / (double)tau), inv_tau = (float)(1.0 / (double)tau);
+  if (p.direct) {
+    kd::LogpDirectArgs a{};
+    a.H = static_cast<const char*>(H);
+    a.W = static_cast<const char*>(W);
+    a.tokens = tokens;
+    a.d = d;
+    a.V = V;
+    a.ldz = p.ldz;
+    a.v0 = (int32_t)v0;
+    a.c2 = c2;
+    a.inv_tau = inv_tau;
+    a.lse = lse;
+    a.ent = entropy;
+    a.g = g;
+    a.ge = ge;
+    a.dz = at<char>(workspace, p.o_dz);
+    float* dw32 = p.C < T ? at<float>(workspace, p.o_dw32) : nullptr;
+    for (int64_t c0 = 0; c0 < T; c0 += p.C) {
+      a.rs = kd::RowSet{mask ? c.rows : nullptr, c.count, c0, p.C, T};
+      const char* hc = a.H + c0 * d * elem;
+      if (mask) {
+        char* packed = at<char>(workspace, p.o_hc);
+        KD_LAUNCH("logp_prep", st,
+                  kd::launch_logp_prep(mask, T, c.rows, c.count, H, d * elem, c0, p.C, packed, c0 == 0 ? dH : nullptr,
+                                       d * dh_elem, st));
+        hc = packed;
+      }
+      if (logits) {
+        a.z = const_cast<float*>(logits) + c0 * p.ldz;
+        KD_LAUNCH("logp_direct_dz_from_z", st, kd::launch_logp_direct_dz_from_z(elem, a, st));
+      } else {
+        KD_LAUNCH("logp_direct_dz", st, kd::launch_logp_direct_dz(elem, a, st));
+      }
+      KD_LAUNCH("logp_direct_dh", st,
+                kd::launch_logp_direct_dh(elem, a, p.S_dh, at<float>(workspace, p.o_dhp), dH, dh_elem, st));
+      // a float32 dW adds up in place; a bf16 one in the workspace, rounded with the last chunk
+      const bool f32 = dw_dtype == KD_F32, last = c0 + p.C >= T;
+      float* acc = f32 ? static_cast<float*>(dW) : dw32;
+      KD_LAUNCH("logp_direct_dw", st,
+                kd::launch_logp_direct_dw(elem, a, hc, c0 > 0 ? acc : nullptr, f32 || !last ? acc : dW,
+                                          f32 || !last ? 4 : 2, st));
+    }
+    return KD_OK;
+  }
   const ChunkPlan& ch = p.ch;
   char* dz = at<char>(workspace, ch.o_dz);
   char* hT = at<char>(workspace, ch.o_hT);
@@ -152,19 +258,19 @@ kd_status logp_bwd(const void* H, const void* W, const int32_t* tokens, const ui
   a.v0 = (int32_t)v0;
   a.ntiles = p.ntiles;
   a.group = kRasterGroup;
-  a.c2 = (float)(1.4426950408889634 / (double)tau);
-  a.inv_tau = (float)(1.0 / (double)tau);
+  a.c2 = c2;
+  a.inv_tau = inv_tau;
   for (int64_t c0 = 0; c0 < T; c0 += ch.C) {
     a.c0 = c0;
     if (logits) {
       a.z = logits + c0 * ch.ldz;
-      KD_LAUNCH("logp_dz_from_z", st, kd::launch_logp_dz_from_z(elem, a, st));
+      KD_LAUNCH("logp_dz_from_z", st, kd::launch_logp_dz_from_z(a, st));
     } else {
       const ChunkShape sh = chunk_shape(T, c0, ch.C, p.ntiles);
       a.nrb = sh.nrb;
       a.S = sh.S;
       KD_LAUNCH("gather_panels", st, kd::launch_gather_panels(H, d * elem, c, c0, ch.C, hp, st));
-      KD_LAUNCH("logp_dz_tile", st, kd::launch_logp_dz(elem, a, st));
+      KD_LAUNCH("logp_dz_tile", st, kd::launch_logp_dz(a, st));
     }
     KD_TRY(grad_chunk(H, W, dH, dw32, elem, d, V, c, ch, dz, hT, dhp, c0, c0 > 0, st, dh_elem));
   }
