@@ -17,6 +17,8 @@
 //   backward: each register becomes its dZ.
 // The tile contraction (2 T d V flops) bounds both; without the entropy the
 // extra terms are compiled out.
+#include <type_traits>
+
 #include "kd_gemm.h"
 #include "kd_main.h"
 #include "kd_policy.h"
@@ -29,7 +31,37 @@ constexpr int kBN = kTileN;
 constexpr int kStgBytes = 2048;       // per wave: 32 rows x 64 bytes of bf16 dZ
 constexpr int kFstWords = 4 * 4 * 64;  // per wave: (m, l, e, x) of 4 rows x 64 lanes
 
-__device__ inline int tile_n0(int vt, int V) { return V >= kBN ? min(vt * kBN, V - kBN) : 0; }
+// The ring takes whole tiles only (V >= 256): a last partial tile is shifted
+// left to end at V, and its first columns, up to the tile's own lo, were the
+// previous tile's.
+__device__ inline int tile_n0(int vt, int V) { return min(vt * kBN, V - kBN); }
+
+// The forward product's operands.  The contraction runs over d rounded up to
+// whole ring turns (128): the panels of H hold zeros there, and W's stages
+// past d (a multiple of 32) read its last one again.
+struct LogpMain : DmaNN<kBN> {
+  int b_last;
+  template <class RowPtr>
+  __device__ inline void open(const char* hp, RowPtr&& row, const char* W, long V, long d, long C) {
+    init(hp, row, W, V * 2, V, (d + kDmaKMult - 1) / kDmaKMult * kDmaKMult, (uint32_t)(C * kRowB));
+    b_last = (int)(d / kDmaKs) - 1;
+    b.init(W, LONG_MAX);
+  }
+  // transposed accumulators of tiles n0(0) .. n0(ntiles - 1)
+  template <class N0, class Done>
+  __device__ inline void tiles(const Slots& sl, int ntiles, N0&& n0, Done&& done) {
+    f32x16_t acc[4][kBN / 64];
+    ring_run<kLpw, FragsNN<kBN>>(
+        sl, ntiles, nst,
+        [&](long t, int s, char* da, char* db) {
+          a.issue(s, da);
+          b.issue(min(s, b_last), (long)n0((int)t), db);
+        },
+        [&](const char* slot, FragsNN<kBN>& f) { rd.read_nn(slot, f); },
+        [&](const FragsNN<kBN>& f) { mma_frags_t(f, acc); },
+        [&](const FragsNN<kBN>& f) { mma_frags_first<true>(f, acc); }, [&](int t) { done(t, acc); });
+  }
+};
 
 // Byte position of 8 bytes (half hh of 16-byte chunk j) of row r in a wave's
 // [32][64 B] staging region: chunk and half XOR-swizzled, so the 32 rows that
@@ -59,15 +91,15 @@ __device__ inline void merge(float& m, float& l, float& e, float om, float ol, f
 }
 
 // One row's update from the lane's 64 values of the tile (register i of
-// block nb: column base + 32 nb + 8 (i / 4) + 4 h + i % 4).  Columns outside
-// [lo, hi) (multiples of 4) are left out unless kFull.
+// block nb: column base + 32 nb + 8 (i / 4) + 4 h + i % 4).  Columns below lo
+// (a multiple of 8) are left out unless kFull.
 template <bool kEnt, bool kFull>
-__device__ inline void fwd_row(const f32x16_t (&v)[4], float c2, float* st, int label, int base, int lo, int hi) {
+__device__ inline void fwd_row(const f32x16_t (&v)[4], float c2, float* st, int label, int base, int lo) {
   const int h = (opaque((int)threadIdx.x) >> 5) & 1;
   float m = st[0], l = st[64];
   auto in = [&](int nb, int i) {
     const int col = base + 32 * nb + 8 * (i >> 2) + 4 * h;
-    return kFull || (col >= lo && col < hi);
+    return kFull || col >= lo;
   };
   float cm = -INFINITY;
 #pragma unroll
@@ -97,7 +129,7 @@ __device__ inline void fwd_row(const f32x16_t (&v)[4], float c2, float* st, int 
   st[64] = l + sum;
   if constexpr (kEnt) st[128] = e + es;
   const int dc = label - base;
-  if ((unsigned)dc < 128u && label >= lo && label < hi && ((dc >> 2) & 1) == h) {
+  if ((unsigned)dc < 128u && label >= lo && ((dc >> 2) & 1) == h) {
     const int nbl = dc >> 5, at = ((dc >> 3 & 3) << 2) | (dc & 3);
     float z = 0.f;
 #pragma unroll
@@ -108,20 +140,28 @@ __device__ inline void fwd_row(const f32x16_t (&v)[4], float c2, float* st, int 
   }
 }
 
-// The tile's raw logits of one row (the columns of [lo, hi)), fp32, 16 bytes per store.
+// The tile's raw logits of one row (the columns from lo on), fp32, 16 bytes
+// per store, taken from the accumulator registers as they lie.
 template <int NB, int J>
-__device__ inline void zout4(const f32x16_t (&acc)[4], float* zr, int base, int lo, int hi, int h) {
-  const int col = base + 32 * NB + 8 * J + 4 * h;
-  if (col >= lo && col < hi)
-    *reinterpret_cast<f32x4_t*>(zr + col) =
+__device__ inline void zout4(const f32x16_t (&acc)[4], float* zr, int base, int lo, int h) {
+  if (base + 32 * NB + 8 * J + 4 * h >= lo)
+    *reinterpret_cast<f32x4_t*>(zr + 32 * NB + 8 * J) =
         __builtin_shufflevector(acc[NB], acc[NB], 4 * J, 4 * J + 1, 4 * J + 2, 4 * J + 3);
 }
 template <int NB>
-__device__ inline void zout_nb(const f32x16_t (&acc)[4], float* zr, int base, int lo, int hi, int h) {
-  zout4<NB, 0>(acc, zr, base, lo, hi, h);
-  zout4<NB, 1>(acc, zr, base, lo, hi, h);
-  zout4<NB, 2>(acc, zr, base, lo, hi, h);
-  zout4<NB, 3>(acc, zr, base, lo, hi, h);
+__device__ inline void zout_nb(const f32x16_t (&acc)[4], float* zr, int base, int lo, int h) {
+  zout4<NB, 0>(acc, zr, base, lo, h);
+  zout4<NB, 1>(acc, zr, base, lo, h);
+  zout4<NB, 2>(acc, zr, base, lo, h);
+  zout4<NB, 3>(acc, zr, base, lo, h);
+}
+// zr: the row at the lane's first column, base + 4 h
+__device__ inline void zout_row(const f32x16_t (&acc)[4], float* zr, int base, int lo) {
+  const int h = (opaque((int)threadIdx.x) >> 5) & 1;
+  zout_nb<0>(acc, zr, base, lo, h);
+  zout_nb<1>(acc, zr, base, lo, h);
+  zout_nb<2>(acc, zr, base, lo, h);
+  zout_nb<3>(acc, zr, base, lo, h);
 }
 
 }  // namespace
@@ -148,10 +188,10 @@ __global__ __launch_bounds__(kThreads, 1) void logp_fwd_kernel(LogpFwdArgs a) {
   const int te = (int)((long)a.ntiles * (sp + 1) / a.S);
   const int V = (int)a.V;
 
-  DmaNN<kBN> mainloop;
-  mainloop.init(
-      a.Hp, [&](int r) -> const char* { return row0 + r < M ? a.Hp + (row0 + r) * kRowB : nullptr; }, a.W,
-      a.V * 2, a.V, a.d, a.C * kRowB);
+  LogpMain mainloop;
+  mainloop.open(
+      a.Hp, [&](int r) -> const char* { return row0 + r < M ? a.Hp + (row0 + r) * kRowB : nullptr; }, a.W, a.V, a.d,
+      a.C);
 
   const int w = wave_id(), wm = w >> 1, wn = w & 1;
   const int lane = (int)threadIdx.x & 63;
@@ -168,25 +208,19 @@ __global__ __launch_bounds__(kThreads, 1) void logp_fwd_kernel(LogpFwdArgs a) {
     fst[mb * 256 + 192 + lane] = 0.f;
   }
 
-  mainloop.template run<true>(
-      sl, te - tb, [&](int i) { return TileAt{0, tile_n0(tb + i, V)}; },
+  mainloop.tiles(
+      sl, te - tb, [&](int i) { return tile_n0(tb + i, V); },
       [&](int i, const f32x16_t (&acc)[4][4]) {
-        const int vt = tb + i, n0 = tile_n0(vt, V), lo = vt * kBN, hi = min(lo + kBN, V);
+        const int vt = tb + i, n0 = tile_n0(vt, V), lo = vt * kBN;
         const int base = n0 + wn * 128;
-        const bool full = n0 == lo && lo + kBN <= hi;
         const int ln = opaque((int)threadIdx.x) & 63;
-        if constexpr (kOut) {
-          const int zr0 = opaque(row0 + trow0 + (ln & 31)), h = ln >> 5;
-          float* zp = a.zout + (long)zr0 * a.ldz;
+        const bool full = n0 == lo;
+        if constexpr (kOut) {  // the logits first, straight from the accumulators
+          const int r = opaque(row0 + trow0 + (ln & 31));  // the lane's row of block row 0
+          float* zr = a.zout + (long)r * a.ldz + base + 4 * (ln >> 5);
 #pragma unroll
           for (int mb = 0; mb < 4; ++mb)
-            if (zr0 + mb * 32 < M) {
-              float* zr = zp + (long)mb * 32 * a.ldz;
-              zout_nb<0>(acc[mb], zr, base, lo, hi, h);
-              zout_nb<1>(acc[mb], zr, base, lo, hi, h);
-              zout_nb<2>(acc[mb], zr, base, lo, hi, h);
-              zout_nb<3>(acc[mb], zr, base, lo, hi, h);
-            }
+            if (r + mb * 32 < M) zout_row(acc[mb], zr + (long)mb * 32 * a.ldz, base, lo);
           __builtin_amdgcn_sched_barrier(0);
         }
 #pragma unroll
@@ -194,9 +228,9 @@ __global__ __launch_bounds__(kThreads, 1) void logp_fwd_kernel(LogpFwdArgs a) {
           float* st = fst + mb * 256 + ln;
           const int label = labk[trow0 + mb * 32 + (ln & 31)];
           if (full)
-            fwd_row<kEnt, true>(acc[mb], a.c2, st, label, base, lo, hi);
+            fwd_row<kEnt, true>(acc[mb], a.c2, st, label, base, lo);
           else
-            fwd_row<kEnt, false>(acc[mb], a.c2, st, label, base, lo, hi);
+            fwd_row<kEnt, false>(acc[mb], a.c2, st, label, base, lo);
         }
       });
 
@@ -372,20 +406,19 @@ __device__ inline float dz_value(float z, const float4 k, float c2) {
 }
 
 // One 32 x 32 block: dZ of the lane's row at its 16 columns, to the chunk's
-// panels.  Columns from hi on are zero, columns below lo belong to the
-// previous tile and are not stored.  The block goes through a wave-private
-// 2 KB LDS region (LDS accesses of one wave complete in order: no barrier),
-// so that a store instruction writes 16 consecutive rows of one 64-byte piece.
+// panels.  Columns below lo belong to the previous tile and are not stored.
+// The block goes through a wave-private 2 KB LDS region (LDS accesses of one
+// wave complete in order: no barrier), so that a store instruction writes 16
+// consecutive rows of one 64-byte piece.  tail (nullable): the block ends at
+// V inside a piece; the columns from V rounded down to 32 on go out again in
+// the tail piece (logp_dh_kernel), the others there as zeros.
 template <bool kEnt, bool kFull>
-__device__ inline void dz_block(const f32x16_t& v, const float4 k, float c2, int label, int cb, int lo, int hi,
-                                char* stg, char* dz, long C, long brow0) {
+__device__ inline void dz_block(const f32x16_t& v, const float4 k, float c2, int label, int cb, int lo, char* stg,
+                                char* dz, long C, long brow0, char* tail, int tail0) {
   const int lane = opaque((int)threadIdx.x) & 63, h = lane >> 5, cl = lane & 31;
   float o[16];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const float e = dz_value<kEnt>(v[i], k, c2);
-    o[i] = kFull || cb + 8 * (i >> 2) + 4 * h < hi ? e : 0.f;
-  }
+  for (int i = 0; i < 16; ++i) o[i] = dz_value<kEnt>(v[i], k, c2);
   const int dc = label - cb;
   if ((unsigned)dc < 32u && ((dc >> 2) & 1) == h) {
     const int at = ((dc >> 3) << 2) | (dc & 3);
@@ -403,6 +436,8 @@ __device__ inline void dz_block(const f32x16_t& v, const float4 k, float c2, int
     const uint4 x = ((r >> 4) & 1) ? make_uint4(q.z, q.w, q.x, q.y) : q;  // halves stored exchanged
     const int col = cb + 8 * j;
     if (kFull || col >= lo) *reinterpret_cast<uint4*>(dz + panel_off(C, brow0 + r, (long)col * 2)) = x;
+    if (!kFull && tail)
+      *reinterpret_cast<uint4*>(tail + (brow0 + r) * kRowB + 16 * j) = col >= tail0 ? x : make_uint4(0, 0, 0, 0);
   }
 }
 
@@ -430,10 +465,10 @@ __global__ __launch_bounds__(kThreads, 1) void logp_dz_kernel(LogpDzArgs a) {
   const int te = (int)((long)a.ntiles * (sp + 1) / a.S);
   const int V = (int)a.V;
 
-  DmaNN<kBN> mainloop;
-  mainloop.init(
-      a.Hp, [&](int r) -> const char* { return row0 + r < M ? a.Hp + (row0 + r) * kRowB : nullptr; }, a.W,
-      a.V * 2, a.V, a.d, a.C * kRowB);
+  LogpMain mainloop;
+  mainloop.open(
+      a.Hp, [&](int r) -> const char* { return row0 + r < M ? a.Hp + (row0 + r) * kRowB : nullptr; }, a.W, a.V, a.d,
+      a.C);
 
   {
     const int i = (int)threadIdx.x;
@@ -447,12 +482,12 @@ __global__ __launch_bounds__(kThreads, 1) void logp_dz_kernel(LogpDzArgs a) {
   const int trow0 = wm * 128;
   char* stg = stg_all + w * kStgBytes;
 
-  mainloop.template run<true>(
-      sl, te - tb, [&](int i) { return TileAt{0, tile_n0(tb + i, V)}; },
+  mainloop.tiles(
+      sl, te - tb, [&](int i) { return tile_n0(tb + i, V); },
       [&](int i, const f32x16_t (&acc)[4][4]) {
-        const int vt = tb + i, n0 = tile_n0(vt, V), lo = vt * kBN, hi = min(lo + kBN, V);
+        const int vt = tb + i, n0 = tile_n0(vt, V), lo = vt * kBN;
         const int base = n0 + wn * 128;
-        const bool full = n0 == lo && lo + kBN <= hi;
+        const bool full = n0 == lo;
         const int ln = opaque((int)threadIdx.x) & 31;
 #pragma unroll
         for (int mb = 0; mb < 4; ++mb) {
@@ -461,12 +496,13 @@ __global__ __launch_bounds__(kThreads, 1) void logp_dz_kernel(LogpDzArgs a) {
           const int label = __float_as_int(cc.y);
 #pragma unroll
           for (int nb = 0; nb < 4; ++nb) {
+            const int cb = base + 32 * nb;
             if (full)
-              dz_block<kEnt, true>(acc[mb][nb], k, cc.x, label, base + 32 * nb, lo, hi, stg, a.dz, a.C,
-                                      row0 + trow0 + mb * 32);
+              dz_block<kEnt, true>(acc[mb][nb], k, cc.x, label, cb, lo, stg, a.dz, a.C, row0 + trow0 + mb * 32, nullptr,
+                                   0);
             else
-              dz_block<kEnt, false>(acc[mb][nb], k, cc.x, label, base + 32 * nb, lo, hi, stg, a.dz, a.C,
-                                       row0 + trow0 + mb * 32);
+              dz_block<kEnt, false>(acc[mb][nb], k, cc.x, label, cb, lo, stg, a.dz, a.C, row0 + trow0 + mb * 32,
+                                    V % 32 && cb + 32 == V ? a.dz + a.ldz / 32 * a.C * kRowB : nullptr, V / 32 * 32);
           }
         }
       });
@@ -509,7 +545,126 @@ __global__ __launch_bounds__(256) void logp_dz_from_z_kernel(LogpDzArgs a) {
 #pragma unroll
       for (int q = 0; q < EPT; ++q) o[q] = (long)r.label == v0 + q ? o[q] + r.k.w : o[q];
     }
-    *reinterpret_cast<u32x4_t*>(a.dz + panel_off(a.C, i, v0 * 2)) = pack16<Bf16>(o);
+    const u32x4_t x = pack16<Bf16>(o);
+    *reinterpret_cast<u32x4_t*>(a.dz + panel_off(a.C, i, v0 * 2)) = x;
+    if (a.V % 32 && v0 >= a.V - 32) {  // the tail piece: columns V - 32 .. V - 1 (logp_dh_kernel)
+      char* tail = a.dz + (a.ldz / 32 * a.C + i) * kRowB;
+      *reinterpret_cast<u32x4_t*>(tail + (v0 - (a.V - 32)) * 2) = v0 >= a.V / 32 * 32 ? x : zero4();
+    }
+  }
+}
+
+// ------------------------------------------------------------------ dH
+// dz . W^T over the vocabulary: 256 rows x 256 of d, S ranges of whole ring
+// turns, each into its own float32 part (summed in order afterwards).  Both
+// operands are contiguous along the vocabulary and come 32 columns a stage:
+//   stages 0 .. V/32 - 1          dz piece s,          W columns 32 s ..
+//   one more where V % 32 != 0    dz's tail piece,     W columns V - 32 .. V - 1
+//   to the end of the last turn   zero pieces of dz,   W's first columns
+// so W is never read past a row's end; the pieces after dz's own ldz / 32
+// hold the tail and the zeros (kDzTailPieces).
+namespace {
+
+struct DhMain : DmaNT<256> {
+  int full, tail, tail_piece;
+  long tail_at;  // bytes to W's last 32 columns
+  __device__ inline void tile(const Slots& sl, long s0, long s1, f32x16_t (&acc)[4][4]) {
+    zero_acc<4>(acc);
+    ring_contract<kLpw, FragsRows<256>>(
+        sl, (int)(s1 - s0),
+        [&](long s, char* da, char* db) {
+          const int t = (int)(s0 + s);
+          a.issue((long)(t < full ? t : t - full + tail_piece), da);
+          b.issue(0L, t < full ? (long)t * kRowB : t < full + tail ? tail_at : 0L, db);
+        },
+        [&](const char* slot, FragsRows<256>& f) { rd.read_rows(slot, f); },
+        [&](const FragsRows<256>& f) { mma_frags(f, acc); });
+  }
+};
+
+}  // namespace
+
+__global__ __launch_bounds__(kThreads, 1) void logp_dh_kernel(DhArgs a) {
+  KD_DECLARE_SLOTS(sl);
+  const long M = min(a.C, (long)*a.count - a.c0);
+  if (M <= 0) return;
+  const int logical = xcd_remap(blockIdx.x, gridDim.x);
+  const int per_split = a.nrb * a.ncb;
+  const int sp = logical / per_split;
+  int rb, cb;
+  grouped_coords(logical - sp * per_split, a.nrb, a.ncb, a.group, rb, cb);
+  const long row0 = (long)rb * kBM, n0 = (long)cb * 256;
+  if (row0 >= M) return;
+  DhMain mainloop;
+  mainloop.init(a.dz, [&](int r) -> const char* { return row0 + r < M ? a.dz + (row0 + r) * kRowB : nullptr; },
+                a.W, [&](int r) -> const char* { return n0 + r < a.d ? a.W + (n0 + r) * a.V * 2 : nullptr; }, a.V,
+                a.C * kRowB);
+  mainloop.full = (int)(a.V / 32);
+  mainloop.tail = a.V % 32 ? 1 : 0;
+  mainloop.tail_piece = (int)(a.ldz / 32);
+  mainloop.tail_at = (a.V - 32) * 2;
+  const long ng = (mainloop.full + mainloop.tail + kRing - 1) / kRing;
+  f32x16_t acc[4][4];
+  mainloop.tile(sl, ng * sp / a.S * kRing, ng * (sp + 1) / a.S * kRing, acc);
+  float* dst = a.part + (long)sp * a.C * a.d;
+  const StPair s0 = st_pair<0>(sl), s1 = st_pair<1>(sl);
+  auto round = [&](auto nb) {
+    constexpr int NBI = decltype(nb)::value;
+    stage_block<NBI, 4>(s0, s1, acc);
+    __syncthreads();
+    rmw_pair_f32(s0, s1, dst, a.d, row0, n0 + NBI * 32, n0 + 128 + NBI * 32, M, a.d, false);
+    __syncthreads();
+  };
+  round(std::integral_constant<int, 0>());
+  round(std::integral_constant<int, 1>());
+  round(std::integral_constant<int, 2>());
+  round(std::integral_constant<int, 3>());
+}
+
+// ------------------------------------------------------------------ dW in bf16
+// H^T . dz over the chunk's rows, one 256 x 256 tile per workgroup, rounded
+// once: the transposed accumulators give four consecutive columns per
+// register group, the whole tile goes through LDS as bf16 (128 KB, the ring's
+// four slots, 64 rows each) and leaves in rows of 512 contiguous bytes.
+// 16-byte chunk c of row r sits at c ^ (r % 32), so neither the writes of 32
+// rows at once nor the reads of whole rows collide.
+__global__ __launch_bounds__(kThreads, 1) void logp_dw_bf16_kernel(DwArgs a, char* out) {
+  KD_DECLARE_SLOTS(sl);
+  const long M = max(0L, min(a.C, (long)*a.count - a.c0));
+  int rb, cb;
+  grouped_coords(xcd_remap(blockIdx.x, gridDim.x), a.nrb, a.ncb, a.group, rb, cb);
+  const long row0 = (long)rb * kBM, n0 = (long)cb * 256;
+  // both buffers hold zeros between M and the end of their last 256-row tile
+  const long K = (M + kDmaKMult - 1) / kDmaKMult * kDmaKMult;
+  DmaNN<256> mainloop;
+  mainloop.init(a.hT, [&](int r) -> const char* { return row0 + r < a.d ? a.hT + (row0 + r) * kRowB : nullptr; },
+                a.dz, 0, a.V, K, a.d * kRowB, a.C);
+  f32x16_t acc[4][4];
+  mainloop.tile<true>(sl, n0, acc);
+
+  const int w = wave_id(), wm = w >> 1, wn = w & 1, lane = threadIdx.x & 63, h = lane >> 5, r32 = lane & 31;
+#pragma unroll
+  for (int mb = 0; mb < 4; ++mb) {
+    char* slot = (wm ? (mb < 2 ? sl.s2 : sl.s3) : (mb < 2 ? sl.s0 : sl.s1)) + ((mb & 1) * 32 + r32) * 512;
+#pragma unroll
+    for (int nb = 0; nb < 4; ++nb)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int chunk = wn * 16 + nb * 4 + j;  // columns 8 chunk + 4 h ..
+        *reinterpret_cast<uint2*>(slot + 16 * (chunk ^ r32) + 8 * h) =
+            make_uint2(pk_bf16(acc[mb][nb][4 * j], acc[mb][nb][4 * j + 1]),
+                       pk_bf16(acc[mb][nb][4 * j + 2], acc[mb][nb][4 * j + 3]));
+      }
+  }
+  __syncthreads();
+  const char* mine = w == 0 ? sl.s0 : w == 1 ? sl.s1 : w == 2 ? sl.s2 : sl.s3;  // rows 64 w ..
+  const long col = n0 + 8 * r32;
+#pragma unroll 8
+  for (int i = 0; i < 32; ++i) {
+    const int r = 2 * i + h;
+    const long row = row0 + 64 * w + r;
+    const u32x4_t x = *reinterpret_cast<const u32x4_t*>(mine + r * 512 + 16 * (r32 ^ (r & 31)));
+    if (row < a.d && col < a.V) *reinterpret_cast<u32x4_t*>(out + (row * a.V + col) * 2) = x;
   }
 }
 
@@ -532,7 +687,18 @@ hipError_t launch_to_bf16(const float* in, void* out, int64_t n, hipStream_t st)
 
 // ------------------------------------------------------------------ launches
 bool logp_ring_fits(int elem, int64_t C, int64_t d, int64_t V) {
-  return elem == 2 && d % kDmaKMult == 0 && V >= kBN && fits32(C * d * 2) && fits32(d * V * 2);
+  const int64_t dp = (d + kDmaKMult - 1) / kDmaKMult * kDmaKMult;
+  return elem == 2 && d % kDmaKs == 0 && V >= kBN && fits32(C * dp * 2) && fits32(d * V * 2);
+}
+
+hipError_t launch_logp_dh(const DhArgs& a, hipStream_t st) {
+  hipLaunchKernelGGL(logp_dh_kernel, dim3(a.nrb * a.ncb * a.S), dim3(kThreads), 0, st, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_logp_dw_bf16(const DwArgs& a, void* out, hipStream_t st) {
+  hipLaunchKernelGGL(logp_dw_bf16_kernel, dim3(a.nrb * a.ncb), dim3(kThreads), 0, st, a, static_cast<char*>(out));
+  return hipGetLastError();
 }
 
 hipError_t launch_logp_fwd(const LogpFwdArgs& a, bool entropy, hipStream_t st) {

@@ -36,9 +36,17 @@ struct LogpFwdArgs {
   int group;
   float c2;               // log2(e) / tau
 };
-// whether the ring tiles take a head with chunks of C rows
+// Whether the ring tiles take a head with chunks of C rows.  Where d is not a
+// multiple of 128, Hp's panels hold zeros from d to the next one.
 bool logp_ring_fits(int elem, int64_t C, int64_t d, int64_t V);
 hipError_t launch_logp_fwd(const LogpFwdArgs& a, bool entropy, hipStream_t st);
+
+// dZ panels of the ring hold kDzTailPieces pieces after their ldz / 32: the
+// last 32 columns once more where V is not a multiple of 32 (written with
+// dZ), and zeros up to a whole ring turn of dH's contraction.
+constexpr int kDzTailPieces = 4;
+hipError_t launch_logp_dh(const DhArgs& a, hipStream_t st);                  // as launch_dh, any V
+hipError_t launch_logp_dw_bf16(const DwArgs& a, void* out, hipStream_t st);  // one chunk: out = bf16(H^T dZ)
 
 // Per-row outputs of compacted rows [c0, c0 + C) from the records; with
 // zero_masked, also zeroes the outputs of every masked row.  rec != nullptr:

@@ -29,10 +29,11 @@ struct LogpPlan {
   int ntiles;    // column tiles of the forward
   int64_t Cf;    // rows per forward chunk
   int64_t C, ldz;  // rows per backward chunk, columns of its dZ
-  int S_dh;      // direct: vocabulary ranges of dH
+  int S_dh;      // vocabulary ranges of dH
   size_t o_rows, o_count, o_part, o_hp_f, fwd_total;
-  ChunkPlan ch;  // ring
-  size_t o_dz, o_hc, o_dhp;  // direct
+  size_t o_dz, o_dhp;
+  size_t o_hc;        // direct: the chunk's rows of H
+  size_t o_hT, o_hp;  // ring: the same transposed and as they are, in panels
   size_t o_dw32, total;  // float32 dW where a bf16 one adds up over chunks
 };
 
@@ -56,13 +57,21 @@ LogpPlan plan_logp(int64_t T, int64_t d, int64_t V, int elem, int dw_elem, int64
     p.o_hc = bw.take((size_t)p.C * d * elem);
     p.o_dhp = bw.take(p.S_dh > 1 ? (size_t)p.S_dh * p.C * d * 4 : 0);
   } else {
+    // H's panels run to whole ring turns of d; dZ's hold the tail pieces too,
+    // within the same 32-bit reach
+    const int64_t dp = cdiv(d, 128) * 128;
     p.o_part = fw.take((size_t)max_splits(p.ntiles) * p.Cf * 16);
-    p.o_hp_f = fw.take(panel_bytes(p.Cf, d * elem));
-    p.ch = plan_chunk(T, d, V, elem, chunk_rows, bw);
-    p.C = p.ch.C;
+    p.o_hp_f = fw.take(panel_bytes(p.Cf, dp * elem));
+    p.C = chunk_of(T, V + 32 * kd::kDzTailPieces, elem, chunk_rows);
+    const int64_t units = cdiv(p.C, kd::kTileM) * cdiv(d, 256);
+    p.S_dh = balanced_splits(units, cdiv(V, 128), std::max<int64_t>(1, cdiv(1024, units)));
+    p.o_dz = bw.take((size_t)p.C * (p.ldz + 32 * kd::kDzTailPieces) * elem);
+    p.o_hT = bw.take((size_t)d * p.C * elem);
+    p.o_dhp = bw.take((size_t)p.S_dh * p.C * d * 4);
+    p.o_hp = bw.take(panel_bytes(p.C, dp * elem));
   }
   p.fwd_total = fw.off;
-  p.o_dw32 = bw.take(dw_elem == 2 && (!p.direct || p.C < T) ? (size_t)d * V * 4 : 0);
+  p.o_dw32 = bw.take(dw_elem == 2 && p.C < T ? (size_t)d * V * 4 : 0);
   p.total = std::max(fw.off, bw.off);
   return p;
 }
@@ -86,6 +95,16 @@ kd_status check_head(const void* H, const void* W, const int32_t* tokens) {
   KD_TRY(need_align(H, 16, "H"));
   KD_TRY(need_align(W, 16, "W"));
   KD_TRY(need_align(tokens, 4, "tokens"));
+  return KD_OK;
+}
+
+// The chunk's rows of H in panels, with zeros from d to the next multiple of 128.
+kd_status head_panels(const void* H, int64_t d, const kd::Compact& c, int64_t c0, int64_t C, char* hp,
+                      hipStream_t st) {
+  KD_LAUNCH("gather_panels", st, kd::launch_gather_panels(H, d * 2, c, c0, C, hp, st));
+  const int64_t dp = cdiv(d, 128) * 128;
+  if (dp > d && c0 == 0)  // later chunks find them there
+    KD_LAUNCH("fill_zero", st, kd::launch_fill_zero(hp + d / 32 * C * 64, (dp - d) / 32 * C * 64, st));
   return KD_OK;
 }
 
@@ -144,7 +163,7 @@ kd_status logp_fwd(const void* H, const void* W, const int32_t* tokens, const ui
   a.c2 = c2;
   for (int64_t c0 = 0; c0 < T; c0 += p.Cf) {
     const ChunkShape sh = chunk_shape(T, c0, p.Cf, p.ntiles);
-    KD_LAUNCH("gather_panels", st, kd::launch_gather_panels(H, d * elem, c, c0, p.Cf, hp, st));
+    KD_TRY(head_panels(H, d, c, c0, p.Cf, hp, st));
     a.c0 = rs.c0 = c0;
     a.zout = logits ? logits + c0 * p.ldz : nullptr;
     a.nrb = sh.nrb;
@@ -233,14 +252,18 @@ kd_status logp_bwd(const void* H, const void* W, const int32_t* tokens, const ui
     }
     return KD_OK;
   }
-  const ChunkPlan& ch = p.ch;
-  char* dz = at<char>(workspace, ch.o_dz);
-  char* hT = at<char>(workspace, ch.o_hT);
-  char* hp = at<char>(workspace, ch.o_hp);
-  float* dhp = at<float>(workspace, ch.o_dhp);
+  char* dz = at<char>(workspace, p.o_dz);
+  char* hT = at<char>(workspace, p.o_hT);
+  char* hp = at<char>(workspace, p.o_hp);
+  float* dhp = at<float>(workspace, p.o_dhp);
+  const bool dw_direct = dw_dtype == KD_BF16 && p.C >= T;  // one chunk: rounded where it is made
   float* dw32 = dw_dtype == KD_F32 ? static_cast<float*>(dW) : at<float>(workspace, p.o_dw32);
   KD_LAUNCH("compact", st, kd::launch_compact(mask, T, c, st));
   KD_LAUNCH("zero_masked_rows", st, kd::launch_zero_masked_rows(mask, T, d * dh_elem, dH, st));
+  // dH's last ring turn: zero pieces after dZ's tail piece
+  const int64_t stages = cdiv(V, 32), pads = cdiv(stages, 4) * 4 - stages, tail = V % 32 ? 1 : 0;
+  if (pads > 0)
+    KD_LAUNCH("fill_zero", st, kd::launch_fill_zero(dz + (p.ldz / 32 + tail) * p.C * 64, pads * p.C * 64, st));
   kd::LogpDzArgs a{};
   a.Hp = hp;
   a.W = static_cast<const char*>(W);
@@ -251,8 +274,8 @@ kd_status logp_bwd(const void* H, const void* W, const int32_t* tokens, const ui
   a.g = g;
   a.ge = ge;
   a.dz = dz;
-  a.ldz = ch.ldz;
-  a.C = ch.C;
+  a.ldz = p.ldz;
+  a.C = p.C;
   a.d = d;
   a.V = V;
   a.v0 = (int32_t)v0;
@@ -260,21 +283,56 @@ kd_status logp_bwd(const void* H, const void* W, const int32_t* tokens, const ui
   a.group = kRasterGroup;
   a.c2 = c2;
   a.inv_tau = inv_tau;
-  for (int64_t c0 = 0; c0 < T; c0 += ch.C) {
+  for (int64_t c0 = 0; c0 < T; c0 += p.C) {
     a.c0 = c0;
     if (logits) {
-      a.z = logits + c0 * ch.ldz;
+      a.z = logits + c0 * p.ldz;
       KD_LAUNCH("logp_dz_from_z", st, kd::launch_logp_dz_from_z(a, st));
     } else {
-      const ChunkShape sh = chunk_shape(T, c0, ch.C, p.ntiles);
+      const ChunkShape sh = chunk_shape(T, c0, p.C, p.ntiles);
       a.nrb = sh.nrb;
       a.S = sh.S;
-      KD_LAUNCH("gather_panels", st, kd::launch_gather_panels(H, d * elem, c, c0, ch.C, hp, st));
+      KD_TRY(head_panels(H, d, c, c0, p.C, hp, st));
       KD_LAUNCH("logp_dz_tile", st, kd::launch_logp_dz(a, st));
     }
-    KD_TRY(grad_chunk(H, W, dH, dw32, elem, d, V, c, ch, dz, hT, dhp, c0, c0 > 0, st, dh_elem));
+    KD_LAUNCH("gather_transpose", st, kd::launch_gather_transpose(H, elem, d, c, c0, p.C, hT, st));
+    kd::DhArgs ha{};
+    ha.dz = dz;
+    ha.W = a.W;
+    ha.part = dhp;
+    ha.count = c.count;
+    ha.c0 = c0;
+    ha.C = p.C;
+    ha.ldz = p.ldz;
+    ha.d = d;
+    ha.V = V;
+    ha.nrb = (int)(p.C / kd::kTileM);
+    ha.ncb = (int)cdiv(d, 256);
+    ha.S = p.S_dh;
+    ha.group = kRasterGroup;
+    // whole turns of the vocabulary need none of the tail's stage arithmetic (4% of the kernel)
+    KD_LAUNCH("logp_dh_tile", st, V % 128 == 0 ? kd::launch_dh(elem, ha, st) : kd::launch_logp_dh(ha, st));
+    KD_LAUNCH("reduce_dh", st, kd::launch_reduce_dh(dhp, p.S_dh, p.C, d, c, c0, dH, dh_elem, st));
+    kd::DwArgs wa{};
+    wa.hT = hT;
+    wa.dz = dz;
+    wa.dW = dw32;
+    wa.count = c.count;
+    wa.c0 = c0;
+    wa.C = p.C;
+    wa.ldz = p.ldz;
+    wa.d = d;
+    wa.V = V;
+    wa.nrb = (int)cdiv(d, 256);
+    wa.ncb = (int)cdiv(V, 256);
+    wa.group = kRasterGroup;
+    wa.accumulate = c0 > 0;
+    if (dw_direct)
+      KD_LAUNCH("logp_dw_tile", st, kd::launch_logp_dw_bf16(wa, dW, st));
+    else
+      KD_LAUNCH("dw_tile", st, kd::launch_dw(elem, wa, st));
   }
-  if (dw_dtype == KD_BF16) KD_LAUNCH("to_bf16", st, kd::launch_to_bf16(dw32, dW, d * V, st));
+  if (dw_dtype == KD_BF16 && !dw_direct) KD_LAUNCH("to_bf16", st, kd::launch_to_bf16(dw32, dW, d * V, st));
   return KD_OK;
 }
 

@@ -34,6 +34,11 @@ SHAPES = [
     (9, 72, 328, bf, 0.0, 1.0, 0),
     (300, 200, 8, bf, 0.1, 1.0, 0),     # less than a tile of vocabulary
     (5, 8, 16, bf, 0.0, 1.0, 0),
+    # products of at least 7 million logits a round run on the 256 x 256 ring tiles
+    (600, 256, 12032, bf, 0.0, 1.0, 0),     # whole ring turns everywhere
+    (601, 160, 12008, bf, 0.2, 0.8, 0),     # d, V inside a turn, V inside a 32-column stage
+    (1100, 96, 6624, bf, 0.3, 1.0, 512),    # several chunks of a bf16 dW, V inside a turn
+    (1300, 384, 5592, bf, 0.0, 1.0, 0),
     (1, 4, 4, f32, 0.0, 1.0, 0),
     (33, 12, 20, f32, 0.3, 1.0, 0),
     (65, 100, 260, f32, 0.0, 0.5, 0),
@@ -105,10 +110,11 @@ def test_gradient_against_differences():
     assert abs(diff - along) <= 3e-3 * (1 + abs(along)), (diff, along)
 
 
-def test_tokens_at_every_tile_edge():
+@pytest.mark.parametrize("V,rows", [(1000, 0), (7016, 1024)])
+def test_tokens_at_every_tile_edge(V, rows):
     """One row per column where a tile, a wave's half or a lane's group begins or ends."""
-    V = 1000
     edges = sorted({max(0, min(V - 1, b + o)) for b in range(0, V + 32, 32) for o in (-1, 0, 3, 4)} | {744, 743, 767, 768})
+    edges = (edges + list(range(rows)))[:max(rows, len(edges))]
     T = len(edges)
     H, W, _, _ = make_head(T, 128, V, bf, 11)
     tokens = torch.tensor(edges, dtype=torch.int32)
@@ -123,11 +129,11 @@ def test_tokens_at_every_tile_edge():
         within(dW, want["dW"], bound["dW"], "dW")
 
 
-@pytest.mark.parametrize("T", [20, 300])
-def test_large_logits(T):
+@pytest.mark.parametrize("T,V", [(20, 776), (300, 776), (1000, 7016)])
+def test_large_logits(T, V):
     """Logits of hundreds: every 2^x must be taken relative to the row's maximum, and rows past the last valid one
     (whose accumulators hold a copy of a real row) must not reach dW."""
-    H, W, tokens, mask = make_head(T, 128, 776, bf, 13, scale=30.0, masked=0.1)
+    H, W, tokens, mask = make_head(T, 128, V, bf, 13, scale=30.0, masked=0.1)
     g, ge = upstream(T, 13)
     want, bound = logp_reference(H, W, tokens, mask, 1.0, g, ge)
     a = [dev(x) for x in (H, W, tokens, mask)]
@@ -140,9 +146,9 @@ def test_large_logits(T):
         within(dW, want["dW"], bound["dW"], "dW")
 
 
-@pytest.mark.parametrize("T,dtype", [(12, bf), (300, bf), (12, f32)])
-def test_masked_rows_are_not_read(T, dtype):
-    H, W, tokens, _ = make_head(T, 128, 520, dtype, 17)
+@pytest.mark.parametrize("T,V,dtype", [(12, 520, bf), (300, 520, bf), (1000, 7016, bf), (12, 520, f32)])
+def test_masked_rows_are_not_read(T, V, dtype):
+    H, W, tokens, _ = make_head(T, 128, V, dtype, 17)
     mask = torch.ones(T, dtype=torch.uint8)
     mask[::3] = 0
     g, ge = upstream(T, 17)
@@ -162,11 +168,12 @@ def test_masked_rows_are_not_read(T, dtype):
     assert torch.equal(some[0], logp)
 
 
-def test_every_row_masked_and_no_rows():
-    H, W, tokens, _ = make_head(5, 128, 264, bf, 19)
-    a = [dev(x) for x in (H, W, tokens, torch.zeros(5, dtype=torch.uint8))]
+@pytest.mark.parametrize("T,V", [(5, 264), (1000, 7016)])
+def test_every_row_masked_and_no_rows(T, V):
+    H, W, tokens, _ = make_head(T, 128, V, bf, 19)
+    a = [dev(x) for x in (H, W, tokens, torch.zeros(T, dtype=torch.uint8))]
     logp, lse, ent, z = kd.token_logp_forward(*a, 1.0, want_entropy=True, keep_logits=True)
-    g = torch.ones(5, device="cuda")
+    g = torch.ones(T, device="cuda")
     for zz in (None, z):
         for dt in (f32, bf):
             dH, dW = kd.token_logp_backward(*a, 1.0, lse, g, ent, g, zz, dw_dtype=dt)
@@ -178,11 +185,11 @@ def test_every_row_masked_and_no_rows():
     assert logp.numel() == 0 and dH.shape == (0, 128) and (dW == 0).all()
 
 
-@pytest.mark.parametrize("T", [6, 300])
-def test_a_token_outside_the_vocabulary_is_nan(T):
-    H, W, tokens, _ = make_head(T, 128, 264, bf, 23)
+@pytest.mark.parametrize("T,V", [(6, 264), (300, 264), (1000, 7016)])
+def test_a_token_outside_the_vocabulary_is_nan(T, V):
+    H, W, tokens, _ = make_head(T, 128, V, bf, 23)
     want, bound = logp_reference(H, W, tokens, None, 1.0)
-    tokens[1], tokens[4] = -100, 264
+    tokens[1], tokens[4] = -100, V
     logp, lse, _, _ = kd.token_logp_forward(dev(H), dev(W), dev(tokens), None, 1.0)
     got = logp.cpu()
     assert torch.isnan(got[[1, 4]]).all()
@@ -191,9 +198,10 @@ def test_a_token_outside_the_vocabulary_is_nan(T):
     within(lse, want["lse"], bound["lse"], "lse")
 
 
-@pytest.mark.parametrize("cuts,dtype", [((0, 264, 600, 1288), bf), ((0, 8, 1288), bf), ((0, 500, 1004), f32)])
-def test_vocabulary_shards(cuts, dtype):
-    T, d, V = 90, 128, cuts[-1]
+@pytest.mark.parametrize("T,cuts,dtype", [(90, (0, 264, 600, 1288), bf), (90, (0, 8, 1288), bf),
+                                          (90, (0, 500, 1004), f32), (1000, (0, 7016, 14048), bf)])
+def test_vocabulary_shards(T, cuts, dtype):
+    d, V = 128, cuts[-1]
     H, W, tokens, mask = make_head(T, d, V, dtype, 29, masked=0.2)
     g, ge = upstream(T, 29)
     want, bound = logp_reference(H, W, tokens, mask, 1.3, g, ge)
@@ -226,9 +234,10 @@ def test_autograd(keep):
     within(dH, only["dH"], bo["dH"], "dH alone")
 
 
-def test_float_rows_of_a_larger_buffer_stay_as_they_were():
-    """Outputs and workspace of exactly the asked size inside larger buffers: nothing around them changes."""
-    T, d, V = 70, 128, 520
+@pytest.mark.parametrize("T,d,V", [(70, 128, 520), (1000, 160, 7016)])
+def test_nothing_around_the_buffers_changes(T, d, V):
+    """Outputs and workspace of exactly the asked size inside larger buffers."""
+    Vp = -(-V // 256) * 256
     H, W, tokens, mask = make_head(T, d, V, bf, 37, masked=0.3)
     B = kd._policy_binding
     say("guards around every output and the workspace")
@@ -241,10 +250,10 @@ def test_float_rows_of_a_larger_buffer_stay_as_they_were():
     nb = B.kd_token_logp_workspace_size(T, d, V, bf, bf)
     raws = {}
     out = {}
-    for k, (n, dt) in dict(ws=(nb, torch.uint8), logp=(T, f32), lse=(T, f32), ent=(T, f32), z=(T * 768, f32),
+    for k, (n, dt) in dict(ws=(nb, torch.uint8), logp=(T, f32), lse=(T, f32), ent=(T, f32), z=(T * Vp, f32),
                            dH=(T * d, bf), dW=(d * V, bf)).items():
         raws[k], out[k] = guarded(n, dt)
-    z = out["z"].view(T, 768)
+    z = out["z"].view(T, Vp)
     a = [dev(x) for x in (H, W, tokens, mask)]
     B.kd_token_logp_fwd(*a, 1.0, out["logp"], out["lse"], out["ent"], z, out["ws"])
     g = torch.randn(T, device="cuda")
@@ -256,10 +265,11 @@ def test_float_rows_of_a_larger_buffer_stay_as_they_were():
         assert (raw[:256] == 0x5A).all() and (raw[-256:] == 0x5A).all(), k
 
 
-def test_another_stream_and_the_same_bits():
-    H, W, tokens, mask = make_head(300, 256, 1288, bf, 41, masked=0.2)
+@pytest.mark.parametrize("T,V", [(300, 1288), (1000, 7016)])
+def test_another_stream_and_the_same_bits(T, V):
+    H, W, tokens, mask = make_head(T, 256, V, bf, 41, masked=0.2)
     a = [dev(x) for x in (H, W, tokens, mask)]
-    g = torch.randn(300, device="cuda")
+    g = torch.randn(T, device="cuda")
 
     def calls():
         logp, lse, ent, z = kd.token_logp_forward(*a, 1.0, want_entropy=True, keep_logits=True)
@@ -277,9 +287,9 @@ def test_another_stream_and_the_same_bits():
         assert torch.equal(x, y)
 
 
-@pytest.mark.parametrize("T", [9, 300])
-def test_captured_and_replayed(T):
-    H, W, tokens, mask = make_head(T, 256, 776, bf, 43, masked=0.2)
+@pytest.mark.parametrize("T,V", [(9, 776), (300, 776), (1000, 7016)])
+def test_captured_and_replayed(T, V):
+    H, W, tokens, mask = make_head(T, 256, V, bf, 43, masked=0.2)
     a = [dev(x) for x in (H, W, tokens, mask)]
     g = torch.randn(T, device="cuda")
 
@@ -293,7 +303,7 @@ def test_captured_and_replayed(T):
     with torch.cuda.graph(graph):
         out = calls()
     for k in range(4):
-        h2, _, t2, m2 = make_head(T, 256, 776, bf, 50 + k, masked=0.1 * k)
+        h2, _, t2, m2 = make_head(T, 256, V, bf, 50 + k, masked=0.1 * k)
         a[0].copy_(h2)
         a[2].copy_(t2)
         a[3].copy_(torch.ones(T, dtype=torch.uint8) if m2 is None else m2)
