@@ -8,8 +8,8 @@ one is given.
 from __future__ import annotations
 
 import array
-import contextlib
 import ctypes
+import functools
 
 import torch
 
@@ -84,34 +84,25 @@ def plib() -> ctypes.CDLL:
     return L
 
 
+@functools.lru_cache(maxsize=1024)  # a plain function of its arguments
 def _size(fn, *args) -> int:
     out = ctypes.c_size_t(0)
     _check(getattr(plib(), fn)(*args, ctypes.byref(out)), fn)
     return out.value
 
 
-@contextlib.contextmanager
-def _device_guard(device):
-    with torch.cuda.device(device):
-        yield
-
-
-def _on(t):
-    """The context in which the library's launches reach t's device."""
-    if t.device.type != "cuda" or t.device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return _device_guard(t.device)
-
-
-def _stream_of(t, stream):
-    if stream is None:
-        stream = torch.cuda.current_stream(t.device)
-    return ctypes.c_void_p(stream.cuda_stream)
-
-
 def _run(name, t, stream, *args):
-    with _on(t):
-        _check(getattr(plib(), name)(*args, _stream_of(t, stream)), name)
+    """Calls a library function on t's device, on its current stream unless one is given."""
+    fn = getattr(plib(), name)
+    index = t.device.index
+    handle = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    if index == torch.cuda.current_device():
+        status = fn(*args, handle)
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, handle)
+    if status != 0:
+        _check(status, name)
 
 
 # ---------------------------------------------------------------- token log-probabilities
@@ -405,7 +396,9 @@ class TensorTable:
 
 
 def kd_grad_norm_workspace_size(table) -> int:
-    return _size("kd_grad_norm_workspace_size", table.numel, table.n)
+    out = ctypes.c_size_t(0)
+    _check(plib().kd_grad_norm_workspace_size(table.numel, table.n, ctypes.byref(out)), "kd_grad_norm_workspace_size")
+    return out.value
 
 
 def kd_grad_sumsq(table, sumsq, workspace, stream=None):

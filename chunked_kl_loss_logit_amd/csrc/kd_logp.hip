@@ -180,12 +180,13 @@ __global__ __launch_bounds__(kThreads, 1) void logp_fwd_kernel(LogpFwdArgs a) {
   const long count = *a.c.count;
   const long M = min(a.C, count - a.c0);  // valid rows of the chunk
   if (M <= 0) return;
+  const int nrb = (int)((M + kBM - 1) / kBM), S = ring_splits(M, a.ntiles, a.grid);
+  if ((int)blockIdx.x >= nrb * S) return;
   int rb, sp;
-  grouped_coords(xcd_remap(blockIdx.x, gridDim.x), a.nrb, a.S, a.group, rb, sp);
+  grouped_coords(xcd_remap(blockIdx.x, nrb * S), nrb, S, a.group, rb, sp);
   const int row0 = rb * kBM;
-  if (row0 >= M) return;
-  const int tb = (int)((long)a.ntiles * sp / a.S);
-  const int te = (int)((long)a.ntiles * (sp + 1) / a.S);
+  const int tb = (int)((long)a.ntiles * sp / S);
+  const int te = (int)((long)a.ntiles * (sp + 1) / S);
   const int V = (int)a.V;
 
   LogpMain mainloop;
@@ -310,7 +311,7 @@ __device__ inline void zero_row(long t, const LogpOut& o) {
 // long as the tiles did for a few rows).  With zero_masked, threads also zero
 // the outputs of masked rows.
 template <bool kEnt>
-__global__ __launch_bounds__(256) void logp_combine_kernel(const float4* part, int S, RowSet rs, const uint8_t* mask,
+__global__ __launch_bounds__(256) void logp_combine_kernel(const float4* part, int S, int grid, RowSet rs, const uint8_t* mask,
                                                            const int32_t* tokens, int V, float c2, LogpOut o,
                                                            int zero_masked) {
   const int lane = threadIdx.x & 63;
@@ -320,6 +321,7 @@ __global__ __launch_bounds__(256) void logp_combine_kernel(const float4* part, i
       if (mask[t] == 0) zero_row(t, o);
   const long M = rs.rows ? min((long)rs.C, (long)*rs.count - (long)rs.c0) : min((long)rs.C, (long)(rs.T - rs.c0));
   if (j >= M) return;
+  if (grid > 0) S = ring_splits(M, S, grid);
   float m = -INFINITY, l = 0.f, e = 0.f, x = 0.f;
   for (int s = lane; s < S; s += 64) {
     const float4 q = part[(long)s * rs.C + j];
@@ -342,17 +344,17 @@ __global__ __launch_bounds__(256) void logp_combine_kernel(const float4* part, i
   finish_row(t, make_float4(m, l, e, x), c2, o);
 }
 
-hipError_t launch_logp_combine(const float* part, int S, const RowSet& rs, const uint8_t* mask,
+hipError_t launch_logp_combine(const float* part, int S, int grid, const RowSet& rs, const uint8_t* mask,
                                const int32_t* tokens, int64_t V, float c2, const LogpOut& o, bool zero_masked,
                                hipStream_t st) {
   const int64_t n = rs.C < rs.T - rs.c0 ? rs.C : rs.T - rs.c0;
-  const dim3 grid((unsigned)((n + 3) / 4));
+  const dim3 blocks((unsigned)((n + 3) / 4));
   const float4* p = reinterpret_cast<const float4*>(part);
   if (o.rec || o.entropy)
-    hipLaunchKernelGGL(logp_combine_kernel<true>, grid, dim3(256), 0, st, p, S, rs, mask, tokens, (int)V, c2, o,
+    hipLaunchKernelGGL(logp_combine_kernel<true>, blocks, dim3(256), 0, st, p, S, grid, rs, mask, tokens, (int)V, c2, o,
                        zero_masked ? 1 : 0);
   else
-    hipLaunchKernelGGL(logp_combine_kernel<false>, grid, dim3(256), 0, st, p, S, rs, mask, tokens, (int)V, c2, o,
+    hipLaunchKernelGGL(logp_combine_kernel<false>, blocks, dim3(256), 0, st, p, S, grid, rs, mask, tokens, (int)V, c2, o,
                        zero_masked ? 1 : 0);
   return hipGetLastError();
 }
@@ -457,12 +459,13 @@ __global__ __launch_bounds__(kThreads, 1) void logp_dz_kernel(LogpDzArgs a) {
   const long count = *a.c.count;
   const long M = min(a.C, count - a.c0);
   if (M <= 0) return;
+  const int nrb = (int)((M + kBM - 1) / kBM), S = ring_splits(M, a.ntiles, a.grid);
+  if ((int)blockIdx.x >= nrb * S) return;
   int rb, sp;
-  grouped_coords(xcd_remap(blockIdx.x, gridDim.x), a.nrb, a.S, a.group, rb, sp);
+  grouped_coords(xcd_remap(blockIdx.x, nrb * S), nrb, S, a.group, rb, sp);
   const int row0 = rb * kBM;
-  if (row0 >= M) return;
-  const int tb = (int)((long)a.ntiles * sp / a.S);
-  const int te = (int)((long)a.ntiles * (sp + 1) / a.S);
+  const int tb = (int)((long)a.ntiles * sp / S);
+  const int te = (int)((long)a.ntiles * (sp + 1) / S);
   const int V = (int)a.V;
 
   LogpMain mainloop;
@@ -702,7 +705,7 @@ hipError_t launch_logp_dw_bf16(const DwArgs& a, void* out, hipStream_t st) {
 }
 
 hipError_t launch_logp_fwd(const LogpFwdArgs& a, bool entropy, hipStream_t st) {
-  const dim3 grid(a.nrb * a.S), block(kThreads);
+  const dim3 grid(a.grid), block(kThreads);
   if (entropy && a.zout)
     hipLaunchKernelGGL((logp_fwd_kernel<true, true>), grid, block, 0, st, a);
   else if (entropy)
@@ -715,7 +718,7 @@ hipError_t launch_logp_fwd(const LogpFwdArgs& a, bool entropy, hipStream_t st) {
 }
 
 hipError_t launch_logp_dz(const LogpDzArgs& a, hipStream_t st) {
-  const dim3 grid(a.nrb * a.S), block(kThreads);
+  const dim3 grid(a.grid), block(kThreads);
   if (a.ge)
     hipLaunchKernelGGL(logp_dz_kernel<true>, grid, block, 0, st, a);
   else

@@ -19,6 +19,19 @@ struct RowSet {
   const int32_t* count;
   int64_t c0, C, T;
 };
+// How many vocabulary splits `grid` workgroups give M rows in blocks of 256.
+// The valid rows are only counted on the device: a split count chosen for
+// all T rows would leave a sixth of the CUs without work where a mask takes
+// one of six row blocks, so the kernels divide the grid among the rows there are.
+constexpr int kRingMaxSplits = 512;
+__host__ __device__ inline int ring_splits(int64_t M, int ntiles, int grid) {
+  const int64_t nrb = (M + kTileM - 1) / kTileM;
+  int64_t s = nrb > 0 ? grid / nrb : 1;
+  s = s < ntiles ? s : ntiles;
+  s = s < kRingMaxSplits ? s : kRingMaxSplits;
+  return s > 1 ? (int)s : 1;
+}
+
 // One record per (vocabulary split, row): with y = z log2(e) / tau over the
 // split's columns, (m, l, e, x) = (max y, sum 2^(y - m), sum 2^(y - m) (y - m),
 // z at the row's token or 0).
@@ -32,7 +45,7 @@ struct LogpFwdArgs {
   int64_t ldz;
   int64_t c0, C, d, V;
   int32_t v0;             // first column of W in the whole head (tokens are whole-head indices)
-  int nrb, S, ntiles;
+  int grid, ntiles;       // workgroups, whole rounds of them (ring_splits)
   int group;
   float c2;               // log2(e) / tau
 };
@@ -57,7 +70,8 @@ struct LogpOut {
   float* entropy;  // nullable
   float4* rec;     // nullable
 };
-hipError_t launch_logp_combine(const float* part, int S, const RowSet& rs, const uint8_t* mask,
+// (S records a row, or with grid > 0 ring_splits of S tiles)
+hipError_t launch_logp_combine(const float* part, int S, int grid, const RowSet& rs, const uint8_t* mask,
                                const int32_t* tokens, int64_t V, float c2, const LogpOut& o, bool zero_masked,
                                hipStream_t st);
 // The same outputs from R shards' records rec [R][T].
@@ -78,7 +92,7 @@ struct LogpDzArgs {
   char* dz;               // [C][ldz] in panels of C rows
   int64_t ldz, c0, C, d, V;
   int32_t v0;
-  int nrb, S, ntiles;
+  int grid, ntiles;
   int group;
   float c2, inv_tau;
 };
@@ -161,8 +175,8 @@ struct PrefArgs {
   double* part;           // workspace: [pref_chunks(T)][4]
 };
 int64_t pref_chunks(int64_t T);
-hipError_t launch_pref_fwd(const PrefArgs& a, hipStream_t st);  // sums, loss, rewards
-hipError_t launch_pref_bwd(const PrefArgs& a, hipStream_t st);  // grad_logp from sums
+hipError_t launch_pref(const PrefArgs& a, hipStream_t st);       // sums, loss, rewards, and grad_logp if set
+hipError_t launch_pref_grad(const PrefArgs& a, hipStream_t st);  // grad_logp from sums
 
 // ---------------------------------------------------------------- gradient norm and clipping
 // One launch's tensors, by value (a table stays within a kernel argument

@@ -60,7 +60,7 @@ LogpPlan plan_logp(int64_t T, int64_t d, int64_t V, int elem, int dw_elem, int64
     // H's panels run to whole ring turns of d; dZ's hold the tail pieces too,
     // within the same 32-bit reach
     const int64_t dp = cdiv(d, 128) * 128;
-    p.o_part = fw.take((size_t)max_splits(p.ntiles) * p.Cf * 16);
+    p.o_part = fw.take((size_t)std::min(p.ntiles, kd::kRingMaxSplits) * p.Cf * 16);
     p.o_hp_f = fw.take(panel_bytes(p.Cf, dp * elem));
     p.C = chunk_of(T, V + 32 * kd::kDzTailPieces, elem, chunk_rows);
     const int64_t units = cdiv(p.C, kd::kTileM) * cdiv(d, 256);
@@ -96,6 +96,13 @@ kd_status check_head(const void* H, const void* W, const int32_t* tokens) {
   KD_TRY(need_align(W, 16, "W"));
   KD_TRY(need_align(tokens, 4, "tokens"));
   return KD_OK;
+}
+
+// Workgroups of the forward and dZ tiles for the chunk at c0: as many rounds
+// of 256 as suit all its rows; the kernels divide them among the valid ones.
+int ring_grid(int64_t T, int64_t c0, int64_t C, int64_t ntiles) {
+  const ChunkShape sh = chunk_shape(T, c0, C, ntiles);
+  return (int)(cdiv((int64_t)sh.nrb * sh.S, 256) * 256);
 }
 
 // The chunk's rows of H in panels, with zeros from d to the next multiple of 128.
@@ -141,7 +148,7 @@ kd_status logp_fwd(const void* H, const void* W, const int32_t* tokens, const ui
       a.z = logits ? logits + c0 * p.ldz : nullptr;
       KD_LAUNCH("logp_direct_fwd", st, kd::launch_logp_direct_fwd(elem, a, entropy, st));
       KD_LAUNCH("logp_combine", st,
-                kd::launch_logp_combine(part, p.ntiles, rs, mask, tokens, V, c2, out, c0 == 0, st));
+                kd::launch_logp_combine(part, p.ntiles, 0, rs, mask, tokens, V, c2, out, c0 == 0, st));
     }
     return KD_OK;
   }
@@ -162,15 +169,14 @@ kd_status logp_fwd(const void* H, const void* W, const int32_t* tokens, const ui
   a.group = kRasterGroup;
   a.c2 = c2;
   for (int64_t c0 = 0; c0 < T; c0 += p.Cf) {
-    const ChunkShape sh = chunk_shape(T, c0, p.Cf, p.ntiles);
+    const int grid = ring_grid(T, c0, p.Cf, p.ntiles);
     KD_TRY(head_panels(H, d, c, c0, p.Cf, hp, st));
     a.c0 = rs.c0 = c0;
     a.zout = logits ? logits + c0 * p.ldz : nullptr;
-    a.nrb = sh.nrb;
-    a.S = sh.S;
+    a.grid = grid;
     KD_LAUNCH("logp_fwd_tile", st, kd::launch_logp_fwd(a, entropy, st));
     KD_LAUNCH("logp_combine", st,
-              kd::launch_logp_combine(part, sh.S, rs, mask, tokens, V, c2, out, c0 == 0, st));
+              kd::launch_logp_combine(part, p.ntiles, grid, rs, mask, tokens, V, c2, out, c0 == 0, st));
   }
   return KD_OK;
 }
@@ -289,9 +295,7 @@ kd_status logp_bwd(const void* H, const void* W, const int32_t* tokens, const ui
       a.z = logits + c0 * p.ldz;
       KD_LAUNCH("logp_dz_from_z", st, kd::launch_logp_dz_from_z(a, st));
     } else {
-      const ChunkShape sh = chunk_shape(T, c0, p.C, p.ntiles);
-      a.nrb = sh.nrb;
-      a.S = sh.S;
+      a.grid = ring_grid(T, c0, p.C, p.ntiles);
       KD_TRY(head_panels(H, d, c, c0, p.C, hp, st));
       KD_LAUNCH("logp_dz_tile", st, kd::launch_logp_dz(a, st));
     }
@@ -677,7 +681,7 @@ kd_status kd_preference_loss_fwd(const float* logp, const int32_t* cu_seqlens, c
   KD_TRY(pref_args(cu_seqlens, mask, opts, T, P, a));
   KD_TRY(pref_fwd_args(logp, loss, rewards, sums, workspace, workspace_bytes, a));
   hipStream_t st = static_cast<hipStream_t>(stream);
-  KD_LAUNCH("preference_loss", st, kd::launch_pref_fwd(a, st));
+  KD_LAUNCH("preference_loss", st, kd::launch_pref(a, st));
   return KD_OK;
 }
 
@@ -688,7 +692,7 @@ kd_status kd_preference_loss_bwd(const int32_t* cu_seqlens, const uint8_t* mask,
   KD_TRY(pref_args(cu_seqlens, mask, opts, T, P, a));
   KD_TRY(pref_bwd_args(sums, grad_loss, grad_logp, a));
   hipStream_t st = static_cast<hipStream_t>(stream);
-  KD_LAUNCH("preference_grad", st, kd::launch_pref_bwd(a, st));
+  KD_LAUNCH("preference_grad", st, kd::launch_pref_grad(a, st));
   return KD_OK;
 }
 
@@ -701,8 +705,7 @@ kd_status kd_preference_loss_fwd_bwd(const float* logp, const int32_t* cu_seqlen
   KD_TRY(pref_fwd_args(logp, loss, rewards, sums, workspace, workspace_bytes, a));
   KD_TRY(pref_bwd_args(sums, grad_loss, grad_logp, a));
   hipStream_t st = static_cast<hipStream_t>(stream);
-  KD_LAUNCH("preference_loss", st, kd::launch_pref_fwd(a, st));
-  KD_LAUNCH("preference_grad", st, kd::launch_pref_bwd(a, st));
+  KD_LAUNCH("preference_loss", st, kd::launch_pref(a, st));
   return KD_OK;
 }
 

@@ -145,13 +145,16 @@ def policy_loss_forward(logp, old_logp, advantages, mask=None, workspace=None, *
     return stats, weights
 
 
-def policy_loss_backward(logp, old_logp, advantages, mask, weights, grad_total, **options):
-    """grad_logp [T] and, with an entropy, grad_entropy [T] (else None) for the total's upstream gradient."""
-    o = B.PolicyOptions(logp, old_logp, advantages, mask, **options)
-    g = _f32(logp, o.T)
-    ge = _f32(logp, o.T) if o.tensors[5] is not None else None
+def _policy_backward(o, weights, grad_total):
+    g = _f32(weights, o.T)
+    ge = _f32(weights, o.T) if o.tensors[5] is not None else None
     B.kd_policy_loss_bwd(o, weights, _grad(grad_total), g, ge)
     return g, ge
+
+
+def policy_loss_backward(logp, old_logp, advantages, mask, weights, grad_total, **options):
+    """grad_logp [T] and, with an entropy, grad_entropy [T] (else None) for the total's upstream gradient."""
+    return _policy_backward(B.PolicyOptions(logp, old_logp, advantages, mask, **options), weights, grad_total)
 
 
 def policy_loss_forward_backward(logp, old_logp, advantages, mask=None, workspace=None, **options):
@@ -169,15 +172,17 @@ class _PolicyLoss(torch.autograd.Function):
         total = _f32(logp, ())  # a tensor of its own: a view of stats could not be changed in place by its user
         stats, weights, _, _ = _policy_forward(o, False, None, total)
         ctx.save_for_backward(logp, entropy, old_logp, advantages, mask, ref_logp, cu_seqlens, weights)
-        ctx.options = options
+        ctx.o = o
         ctx.mark_non_differentiable(stats)
+        ctx.set_materialize_grads(False)
         return total, stats
 
     @staticmethod
     def backward(ctx, g, _):
-        logp, entropy, old_logp, advantages, mask, ref_logp, cu_seqlens, weights = ctx.saved_tensors
-        options = dict(ctx.options, entropy=entropy, ref_logp=ref_logp, cu_seqlens=cu_seqlens)
-        gl, ge = policy_loss_backward(logp, old_logp, advantages, mask, weights, g, **options)
+        if g is None:
+            return (None,) * 8
+        weights = ctx.saved_tensors[-1]  # refuses tensors changed in place since
+        gl, ge = _policy_backward(ctx.o, weights, g)
         return gl, ge, None, None, None, None, None, None
 
 
@@ -203,20 +208,26 @@ def _pref_out(logp, o, workspace):
             workspace)
 
 
-def preference_loss_forward(logp, cu_seqlens, mask=None, workspace=None, **options):
-    """loss [P], rewards [2P] and the sums the backward takes."""
-    o = _pref_in(logp, cu_seqlens, mask, options)
+def _pref_forward(o, logp, workspace):
     loss, rewards, sums, workspace = _pref_out(logp, o, workspace)
     B.kd_preference_loss_fwd(o, logp, loss, rewards, sums, workspace)
     return loss, rewards, sums
 
 
-def preference_loss_backward(T, cu_seqlens, mask, sums, grad_loss, **options):
-    """grad_logp [T] for the upstream gradient of the pair losses."""
-    o = B.PreferenceOptions(int(T), sums, cu_seqlens, mask, **options)
+def _pref_backward(o, sums, grad_loss):
     g = _f32(sums, o.T)
     B.kd_preference_loss_bwd(o, sums, _grad(grad_loss), g)
     return g
+
+
+def preference_loss_forward(logp, cu_seqlens, mask=None, workspace=None, **options):
+    """loss [P], rewards [2P] and the sums the backward takes."""
+    return _pref_forward(_pref_in(logp, cu_seqlens, mask, options), logp, workspace)
+
+
+def preference_loss_backward(T, cu_seqlens, mask, sums, grad_loss, **options):
+    """grad_logp [T] for the upstream gradient of the pair losses."""
+    return _pref_backward(B.PreferenceOptions(int(T), sums, cu_seqlens, mask, **options), sums, grad_loss)
 
 
 def preference_loss_forward_backward(logp, cu_seqlens, mask, grad_loss, workspace=None, **options):
@@ -231,16 +242,20 @@ def preference_loss_forward_backward(logp, cu_seqlens, mask, grad_loss, workspac
 class _PreferenceLoss(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logp, cu_seqlens, mask, ref_logp, options):
-        loss, rewards, sums = preference_loss_forward(logp, cu_seqlens, mask, ref_logp=ref_logp, **options)
+        o = _pref_in(logp, cu_seqlens, mask, dict(options, ref_logp=ref_logp))
+        loss, rewards, sums = _pref_forward(o, logp, None)
         ctx.save_for_backward(cu_seqlens, mask, ref_logp, sums)
-        ctx.T, ctx.options = logp.shape[0], options
+        ctx.o = o
         ctx.mark_non_differentiable(rewards)
+        ctx.set_materialize_grads(False)
         return loss, rewards
 
     @staticmethod
     def backward(ctx, g, _):
-        cu_seqlens, mask, ref_logp, sums = ctx.saved_tensors
-        return preference_loss_backward(ctx.T, cu_seqlens, mask, sums, g, ref_logp=ref_logp, **ctx.options), None, None, None, None
+        if g is None:
+            return (None,) * 5
+        sums = ctx.saved_tensors[-1]  # refuses tensors changed in place since
+        return _pref_backward(ctx.o, sums, g), None, None, None, None
 
 
 def preference_loss(logp, cu_seqlens, mask=None, ref_logp=None, **options):
