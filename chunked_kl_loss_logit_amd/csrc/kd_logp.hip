@@ -28,7 +28,7 @@ namespace kd {
 namespace {
 
 constexpr int kBN = kTileN;
-constexpr int kStgBytes = 2048;       // per wave: 32 rows x 64 bytes of bf16 dZ
+constexpr int kStgBytes = 2048;        // per wave: 32 rows x 64 bytes of dZ, or 16 x 128 of logits
 constexpr int kFstWords = 4 * 4 * 64;  // per wave: (m, l, e, x) of 4 rows x 64 lanes
 
 // The ring takes whole tiles only (V >= 256): a last partial tile is shifted
@@ -140,28 +140,30 @@ __device__ inline void fwd_row(const f32x16_t (&v)[4], float c2, float* st, int 
   }
 }
 
-// The tile's raw logits of one row (the columns from lo on), fp32, 16 bytes
-// per store, taken from the accumulator registers as they lie.
-template <int NB, int J>
-__device__ inline void zout4(const f32x16_t (&acc)[4], float* zr, int base, int lo, int h) {
-  if (base + 32 * NB + 8 * J + 4 * h >= lo)
-    *reinterpret_cast<f32x4_t*>(zr + 32 * NB + 8 * J) =
-        __builtin_shufflevector(acc[NB], acc[NB], 4 * J, 4 * J + 1, 4 * J + 2, 4 * J + 3);
-}
-template <int NB>
-__device__ inline void zout_nb(const f32x16_t (&acc)[4], float* zr, int base, int lo, int h) {
-  zout4<NB, 0>(acc, zr, base, lo, h);
-  zout4<NB, 1>(acc, zr, base, lo, h);
-  zout4<NB, 2>(acc, zr, base, lo, h);
-  zout4<NB, 3>(acc, zr, base, lo, h);
-}
-// zr: the row at the lane's first column, base + 4 h
-__device__ inline void zout_row(const f32x16_t (&acc)[4], float* zr, int base, int lo) {
-  const int h = (opaque((int)threadIdx.x) >> 5) & 1;
-  zout_nb<0>(acc, zr, base, lo, h);
-  zout_nb<1>(acc, zr, base, lo, h);
-  zout_nb<2>(acc, zr, base, lo, h);
-  zout_nb<3>(acc, zr, base, lo, h);
+// The raw logits of one 32 x 32 block (the columns from lo on, rows below M),
+// fp32, through a wave-private 2 KB LDS region, 16 rows at a time: a store
+// instruction then writes 8 rows of 128 contiguous bytes.  Straight from the
+// registers it would touch 32 rows of 32 bytes, and the next tile's operand
+// loads, which complete in order behind it, wait for four times the requests.
+__device__ inline void zout_block(const f32x16_t& v, char* stg, float* zout, long ldz, int brow0, long M, int cb,
+                                  int lo) {
+  const int lane = opaque((int)threadIdx.x) & 63, h = lane >> 5, r16 = lane & 15;
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    if (((lane >> 4) & 1) == p) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)  // 16-byte chunk 2 j + h of the row, swizzled against bank conflicts
+        *reinterpret_cast<float4*>(stg + r16 * 128 + 16 * ((2 * j + h) ^ (r16 & 7))) =
+            make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int r = 8 * k + (lane >> 3), c = lane & 7;
+      const float4 x = *reinterpret_cast<const float4*>(stg + r * 128 + 16 * (c ^ (r & 7)));
+      const int row = brow0 + 16 * p + r, col = cb + 4 * c;
+      if (row < M && col >= lo) *reinterpret_cast<float4*>(zout + (long)row * ldz + col) = x;
+    }
+  }
 }
 
 }  // namespace
@@ -175,6 +177,7 @@ __global__ __launch_bounds__(kThreads, 1) void logp_fwd_kernel(LogpFwdArgs a) {
   __shared__ __attribute__((aligned(16))) char sl_3[kSlotBytes];
   __shared__ float fst_all[4 * kFstWords];
   __shared__ int labk[kBM];
+  __shared__ __attribute__((aligned(16))) char stg_all[kOut ? 4 * kStgBytes : 16];
   const Slots sl{sl_0, sl_1, sl_2, sl_3, nullptr};
 
   const long count = *a.c.count;
@@ -216,14 +219,6 @@ __global__ __launch_bounds__(kThreads, 1) void logp_fwd_kernel(LogpFwdArgs a) {
         const int base = n0 + wn * 128;
         const int ln = opaque((int)threadIdx.x) & 63;
         const bool full = n0 == lo;
-        if constexpr (kOut) {  // the logits first, straight from the accumulators
-          const int r = opaque(row0 + trow0 + (ln & 31));  // the lane's row of block row 0
-          float* zr = a.zout + (long)r * a.ldz + base + 4 * (ln >> 5);
-#pragma unroll
-          for (int mb = 0; mb < 4; ++mb)
-            if (r + mb * 32 < M) zout_row(acc[mb], zr + (long)mb * 32 * a.ldz, base, lo);
-          __builtin_amdgcn_sched_barrier(0);
-        }
 #pragma unroll
         for (int mb = 0; mb < 4; ++mb) {
           float* st = fst + mb * 256 + ln;
@@ -232,6 +227,17 @@ __global__ __launch_bounds__(kThreads, 1) void logp_fwd_kernel(LogpFwdArgs a) {
             fwd_row<kEnt, true>(acc[mb], a.c2, st, label, base, lo);
           else
             fwd_row<kEnt, false>(acc[mb], a.c2, st, label, base, lo);
+        }
+        if constexpr (kOut) {  // the logits last: a register spilled before them would wait for their stores
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int mb = 0; mb < 4; ++mb)
+#pragma unroll
+            for (int nb = 0; nb < 4; ++nb) {
+              zout_block(acc[mb][nb], stg_all + w * kStgBytes, a.zout, a.ldz, row0 + trow0 + mb * 32, M, base + 32 * nb,
+                         lo);
+              __builtin_amdgcn_sched_barrier(0);
+            }
         }
       });
 
