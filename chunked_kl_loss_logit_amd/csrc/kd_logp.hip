@@ -593,29 +593,48 @@ struct DhMain : DmaNT<256> {
 
 }  // namespace
 
-__global__ __launch_bounds__(kThreads, 1) void logp_dh_kernel(DhArgs a) {
+// How the grid is divided: whole 256-row blocks of valid rows, 256-wide
+// blocks of d, and as many vocabulary ranges as workgroups are left for (the
+// mask's rows are only counted here, as for ring_splits).  A range's part
+// holds the valid row blocks' rows.
+struct DhShape {
+  int nrb, S;
+  long rows;  // of a part
+};
+__device__ inline DhShape dh_shape(const LogpDhArgs& a, long M) {
+  const int nrb = (int)((M + kBM - 1) / kBM);
+  const int ng = (int)((a.V + 32 * kRing - 1) / (32 * kRing));
+  const int s = nrb > 0 ? a.grid / (nrb * a.ncb) : 1;
+  return {nrb, max(1, min(s, ng)), (long)nrb * kBM};
+}
+
+template <bool kTail>
+__global__ __launch_bounds__(kThreads, 1) void logp_dh_kernel(LogpDhArgs a) {
   KD_DECLARE_SLOTS(sl);
-  const long M = min(a.C, (long)*a.count - a.c0);
+  const long M = min((long)a.C, (long)*a.count - (long)a.c0);
   if (M <= 0) return;
-  const int logical = xcd_remap(blockIdx.x, gridDim.x);
-  const int per_split = a.nrb * a.ncb;
+  const DhShape sh = dh_shape(a, M);
+  const int per_split = sh.nrb * a.ncb;
+  if ((int)blockIdx.x >= per_split * sh.S) return;
+  const int logical = xcd_remap(blockIdx.x, per_split * sh.S);
   const int sp = logical / per_split;
   int rb, cb;
-  grouped_coords(logical - sp * per_split, a.nrb, a.ncb, a.group, rb, cb);
+  grouped_coords(logical - sp * per_split, sh.nrb, a.ncb, a.group, rb, cb);
   const long row0 = (long)rb * kBM, n0 = (long)cb * 256;
-  if (row0 >= M) return;
-  DhMain mainloop;
+  std::conditional_t<kTail, DhMain, DmaNT<256>> mainloop;
   mainloop.init(a.dz, [&](int r) -> const char* { return row0 + r < M ? a.dz + (row0 + r) * kRowB : nullptr; },
                 a.W, [&](int r) -> const char* { return n0 + r < a.d ? a.W + (n0 + r) * a.V * 2 : nullptr; }, a.V,
                 a.C * kRowB);
-  mainloop.full = (int)(a.V / 32);
-  mainloop.tail = a.V % 32 ? 1 : 0;
-  mainloop.tail_piece = (int)(a.ldz / 32);
-  mainloop.tail_at = (a.V - 32) * 2;
-  const long ng = (mainloop.full + mainloop.tail + kRing - 1) / kRing;
+  if constexpr (kTail) {
+    mainloop.full = (int)(a.V / 32);
+    mainloop.tail = a.V % 32 ? 1 : 0;
+    mainloop.tail_piece = (int)(a.ldz / 32);
+    mainloop.tail_at = (a.V - 32) * 2;
+  }
+  const long ng = (a.V + 32 * kRing - 1) / (32 * kRing);
   f32x16_t acc[4][4];
-  mainloop.tile(sl, ng * sp / a.S * kRing, ng * (sp + 1) / a.S * kRing, acc);
-  float* dst = a.part + (long)sp * a.C * a.d;
+  mainloop.tile(sl, ng * sp / sh.S * kRing, ng * (sp + 1) / sh.S * kRing, acc);
+  float* dst = a.part + (long)sp * sh.rows * a.d;
   const StPair s0 = st_pair<0>(sl), s1 = st_pair<1>(sl);
   auto round = [&](auto nb) {
     constexpr int NBI = decltype(nb)::value;
@@ -628,6 +647,29 @@ __global__ __launch_bounds__(kThreads, 1) void logp_dh_kernel(DhArgs a) {
   round(std::integral_constant<int, 1>());
   round(std::integral_constant<int, 2>());
   round(std::integral_constant<int, 3>());
+}
+
+// dH of the valid rows = their parts added in order; four elements per thread.
+template <int ELEM>
+__global__ __launch_bounds__(256) void logp_dh_reduce_kernel(LogpDhArgs a, const int32_t* rows, char* dH) {
+  const long M = min((long)a.C, (long)*a.count - (long)a.c0);
+  const long q = (long)blockIdx.x * 256 + threadIdx.x, d4 = a.d / 4;
+  const long i = q / d4, j = (q - i * d4) * 4;
+  if (i >= M) return;
+  const DhShape sh = dh_shape(a, M);
+  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s = 0; s < sh.S; ++s) {
+    const float4 y = *reinterpret_cast<const float4*>(a.part + ((long)s * sh.rows + i) * a.d + j);
+    x.x += y.x;
+    x.y += y.y;
+    x.z += y.z;
+    x.w += y.w;
+  }
+  char* p = dH + ((long)rows[a.c0 + i] * a.d + j) * ELEM;
+  if constexpr (ELEM == 2)
+    *reinterpret_cast<uint2*>(p) = make_uint2(pk_bf16(x.x, x.y), pk_bf16(x.z, x.w));
+  else
+    *reinterpret_cast<float4*>(p) = x;
 }
 
 // ------------------------------------------------------------------ dW in bf16
@@ -700,8 +742,18 @@ bool logp_ring_fits(int elem, int64_t C, int64_t d, int64_t V) {
   return elem == 2 && d % kDmaKs == 0 && V >= kBN && fits32(C * dp * 2) && fits32(d * V * 2);
 }
 
-hipError_t launch_logp_dh(const DhArgs& a, hipStream_t st) {
-  hipLaunchKernelGGL(logp_dh_kernel, dim3(a.nrb * a.ncb * a.S), dim3(kThreads), 0, st, a);
+hipError_t launch_logp_dh(const LogpDhArgs& a, const int32_t* rows, void* dH, int dh_elem, hipStream_t st) {
+  // whole turns of the vocabulary need none of the tail's stage arithmetic (4% of the kernel)
+  if (a.V % (32 * kRing))
+    hipLaunchKernelGGL(logp_dh_kernel<true>, dim3(a.grid), dim3(kThreads), 0, st, a);
+  else
+    hipLaunchKernelGGL(logp_dh_kernel<false>, dim3(a.grid), dim3(kThreads), 0, st, a);
+  const int64_t n = (a.C < a.T - a.c0 ? a.C : a.T - a.c0) * (a.d / 4);
+  const dim3 blocks((unsigned)((n + 255) / 256));
+  if (dh_elem == 2)
+    hipLaunchKernelGGL(logp_dh_reduce_kernel<2>, blocks, dim3(256), 0, st, a, rows, static_cast<char*>(dH));
+  else
+    hipLaunchKernelGGL(logp_dh_reduce_kernel<4>, blocks, dim3(256), 0, st, a, rows, static_cast<char*>(dH));
   return hipGetLastError();
 }
 

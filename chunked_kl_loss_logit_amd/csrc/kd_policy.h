@@ -58,7 +58,16 @@ hipError_t launch_logp_fwd(const LogpFwdArgs& a, bool entropy, hipStream_t st);
 // last 32 columns once more where V is not a multiple of 32 (written with
 // dZ), and zeros up to a whole ring turn of dH's contraction.
 constexpr int kDzTailPieces = 4;
-hipError_t launch_logp_dh(const DhArgs& a, hipStream_t st);                  // as launch_dh, any V
+struct LogpDhArgs {
+  const char* dz;  // panels of C rows, the tail pieces included
+  const char* W;
+  float* part;     // [grid / ncb][256][d] floats
+  const int32_t* count;
+  int64_t T, c0, C, ldz, d, V;
+  int grid, ncb, group;  // workgroups, 256-wide blocks of d
+};
+// dH of the chunk's valid rows (rows: Compact's list), in elements of dh_elem bytes
+hipError_t launch_logp_dh(const LogpDhArgs& a, const int32_t* rows, void* dH, int dh_elem, hipStream_t st);
 hipError_t launch_logp_dw_bf16(const DwArgs& a, void* out, hipStream_t st);  // one chunk: out = bf16(H^T dZ)
 
 // Per-row outputs of compacted rows [c0, c0 + C) from the records; with

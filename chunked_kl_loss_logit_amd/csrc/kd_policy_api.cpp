@@ -29,7 +29,8 @@ struct LogpPlan {
   int ntiles;    // column tiles of the forward
   int64_t Cf;    // rows per forward chunk
   int64_t C, ldz;  // rows per backward chunk, columns of its dZ
-  int S_dh;      // vocabulary ranges of dH
+  int S_dh;      // direct: vocabulary ranges of dH
+  int grid_dh;   // ring: workgroups of dH
   size_t o_rows, o_count, o_part, o_hp_f, fwd_total;
   size_t o_dz, o_dhp;
   size_t o_hc;        // direct: the chunk's rows of H
@@ -63,11 +64,11 @@ LogpPlan plan_logp(int64_t T, int64_t d, int64_t V, int elem, int dw_elem, int64
     p.o_part = fw.take((size_t)std::min(p.ntiles, kd::kRingMaxSplits) * p.Cf * 16);
     p.o_hp_f = fw.take(panel_bytes(p.Cf, dp * elem));
     p.C = chunk_of(T, V + 32 * kd::kDzTailPieces, elem, chunk_rows);
-    const int64_t units = cdiv(p.C, kd::kTileM) * cdiv(d, 256);
-    p.S_dh = balanced_splits(units, cdiv(V, 128), std::max<int64_t>(1, cdiv(1024, units)));
+    const int64_t ncb = cdiv(d, 256), units = cdiv(std::min(p.C, T), kd::kTileM) * ncb;
+    p.grid_dh = (int)up(units * balanced_splits(units, cdiv(V, 128), std::max<int64_t>(1, cdiv(1024, units))), 256);
     p.o_dz = bw.take((size_t)p.C * (p.ldz + 32 * kd::kDzTailPieces) * elem);
     p.o_hT = bw.take((size_t)d * p.C * elem);
-    p.o_dhp = bw.take((size_t)p.S_dh * p.C * d * 4);
+    p.o_dhp = bw.take((size_t)cdiv(p.grid_dh, ncb) * 256 * d * 4);
     p.o_hp = bw.take(panel_bytes(p.C, dp * elem));
   }
   p.fwd_total = fw.off;
@@ -300,23 +301,21 @@ kd_status logp_bwd(const void* H, const void* W, const int32_t* tokens, const ui
       KD_LAUNCH("logp_dz_tile", st, kd::launch_logp_dz(a, st));
     }
     KD_LAUNCH("gather_transpose", st, kd::launch_gather_transpose(H, elem, d, c, c0, p.C, hT, st));
-    kd::DhArgs ha{};
+    kd::LogpDhArgs ha{};
     ha.dz = dz;
     ha.W = a.W;
     ha.part = dhp;
     ha.count = c.count;
+    ha.T = T;
     ha.c0 = c0;
     ha.C = p.C;
     ha.ldz = p.ldz;
     ha.d = d;
     ha.V = V;
-    ha.nrb = (int)(p.C / kd::kTileM);
+    ha.grid = p.grid_dh;
     ha.ncb = (int)cdiv(d, 256);
-    ha.S = p.S_dh;
     ha.group = kRasterGroup;
-    // whole turns of the vocabulary need none of the tail's stage arithmetic (4% of the kernel)
-    KD_LAUNCH("logp_dh_tile", st, V % 128 == 0 ? kd::launch_dh(elem, ha, st) : kd::launch_logp_dh(ha, st));
-    KD_LAUNCH("reduce_dh", st, kd::launch_reduce_dh(dhp, p.S_dh, p.C, d, c, c0, dH, dh_elem, st));
+    KD_LAUNCH("logp_dh_tile", st, kd::launch_logp_dh(ha, c.rows, dH, dh_elem, st));
     kd::DwArgs wa{};
     wa.hT = hT;
     wa.dz = dz;
