@@ -29,7 +29,7 @@ POLICY_EXPORTS = (
     "kd_policy_loss_workspace_size", "kd_policy_loss_fwd", "kd_policy_loss_bwd", "kd_policy_loss_fwd_bwd",
     "kd_preference_loss_workspace_size", "kd_preference_loss_fwd", "kd_preference_loss_bwd",
     "kd_preference_loss_fwd_bwd",
-    "kd_grad_norm_workspace_size", "kd_grad_sumsq", "kd_grad_clip",
+    "kd_grad_norm_workspace_size", "kd_grad_sumsq", "kd_grad_clip", "kd_grad_clip_norm",
 )
 
 
@@ -78,6 +78,7 @@ def plib() -> ctypes.CDLL:
     L.kd_grad_norm_workspace_size.argtypes = [vp, i64, psz]
     L.kd_grad_sumsq.argtypes = [vp, vp, vp, i64, vp, vp, sz, vp]
     L.kd_grad_clip.argtypes = [vp, vp, vp, i64, vp, vp, vp, f64, vp, vp]
+    L.kd_grad_clip_norm.argtypes = [vp, vp, vp, i64, vp, vp, f64, vp, vp, vp, sz, vp]
     for f in POLICY_EXPORTS:
         getattr(L, f).restype = st
     _plib = L
@@ -141,20 +142,22 @@ def _logp_bwd_in(H, W, tokens, mask, lse, entropy, logits, grad_logp, grad_entro
     _need("lse", lse, (T,), _F32)
     for n, t in (("entropy", entropy), ("grad_logp", grad_logp), ("grad_entropy", grad_entropy)):
         _need(n, t, (T,), _F32, optional=True)
-    _need("dH", dH, (T, d), (dh_dtype,))
-    _need("dW", dW, (d, V), _HEAD)
+    _need("dH", dH, (T, d), (dh_dtype,), optional=True)
+    _need("dW", dW, (d, V), _HEAD, optional=True)
+    if dH is None and dW is None:
+        raise ValueError("dH and dW are both None")
     return T, d, V
 
 
 def kd_token_logp_bwd(H, W, tokens, mask, tau, lse, entropy, logits, grad_logp, grad_entropy, dH, dW, chunk_rows,
                       workspace, stream=None):
-    """Enqueue the backward; dH and dW (float32 or bfloat16) in place."""
+    """Enqueue the backward; dH and dW (float32 or bfloat16; None: not wanted) in place."""
     T, d, V = _logp_bwd_in(H, W, tokens, mask, lse, entropy, logits, grad_logp, grad_entropy, dH, dW, H.dtype)
     nb = _ws_bytes(workspace)
     _one_device(H, W, tokens, mask, lse, entropy, logits, grad_logp, grad_entropy, dH, dW, workspace)
     _run("kd_token_logp_bwd", H, stream, _ptr(H), _ptr(W), _ptr(tokens), _ptr(mask), float(tau), T, d, V,
          _dtype_code(H.dtype), _ptr(lse), _ptr(entropy), _ptr(logits), _ptr(grad_logp), _ptr(grad_entropy), _ptr(dH),
-         _ptr(dW), _dtype_code(dW.dtype), int(chunk_rows), _ptr(workspace), nb)
+         _ptr(dW), KD_F32 if dW is None else _dtype_code(dW.dtype), int(chunk_rows), _ptr(workspace), nb)
 
 
 def kd_token_logp_fwd_shard(H, W, v0, tokens, mask, tau, rec, logits, workspace, stream=None):
@@ -189,7 +192,7 @@ def kd_token_logp_bwd_shard(H, W, v0, tokens, mask, tau, lse, entropy, logits, g
     _one_device(H, W, tokens, mask, lse, entropy, logits, grad_logp, grad_entropy, dH, dW, workspace)
     _run("kd_token_logp_bwd_shard", H, stream, _ptr(H), _ptr(W), _ptr(tokens), _ptr(mask), float(tau), T, d, V, int(v0),
          _dtype_code(H.dtype), _ptr(lse), _ptr(entropy), _ptr(logits), _ptr(grad_logp), _ptr(grad_entropy), _ptr(dH),
-         _ptr(dW), _dtype_code(dW.dtype), int(chunk_rows), _ptr(workspace), nb)
+         _ptr(dW), KD_F32 if dW is None else _dtype_code(dW.dtype), int(chunk_rows), _ptr(workspace), nb)
 
 
 # ---------------------------------------------------------------- clipped policy loss
@@ -409,12 +412,31 @@ def kd_grad_sumsq(table, sumsq, workspace, stream=None):
          _ws_bytes(workspace))
 
 
-def kd_grad_clip(table, outs, sumsq, max_norm, norm, stream=None):
-    """Enqueue the scaling of a TensorTable into another (or itself); norm (one float32) in place."""
+def _clip_in(table, outs, sumsq, norm):
     _need("sumsq", sumsq, (1,), _F64)
     _need("norm", norm, (), _F32)
     if outs is not table and not table.same_layout(outs):
         raise ValueError("out must match the tensors' number, sizes and strides")
     _one_device(sumsq, norm, *table.tensors[:1], *outs.tensors[:1])
+
+
+def _written(outs):
+    """Tells autograd that the tensors changed: tensors saved for a backward pass are refused there, not used."""
+    torch.autograd.graph.increment_version(outs.tensors)
+
+
+def kd_grad_clip(table, outs, sumsq, max_norm, norm, stream=None):
+    """Enqueue the scaling of a TensorTable into another (or itself); norm (one float32) in place."""
+    _clip_in(table, outs, sumsq, norm)
     _run("kd_grad_clip", sumsq, stream, table.ptrs, table.numel, table.types, table.n, outs.ptrs, outs.types, _ptr(sumsq),
          float(max_norm), _ptr(norm))
+    _written(outs)
+
+
+def kd_grad_clip_norm(table, outs, max_norm, sumsq, norm, workspace, stream=None):
+    """Enqueue the sum of squares and the scaling; sumsq and norm in place."""
+    _clip_in(table, outs, sumsq, norm)
+    _one_device(sumsq, workspace)
+    _run("kd_grad_clip_norm", sumsq, stream, table.ptrs, table.numel, table.types, table.n, outs.ptrs, outs.types,
+         float(max_norm), _ptr(sumsq), _ptr(norm), _ptr(workspace), _ws_bytes(workspace))
+    _written(outs)

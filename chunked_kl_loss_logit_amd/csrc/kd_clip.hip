@@ -87,12 +87,11 @@ struct Elem<kTypeF16> {
   }
 };
 
-// Elements [b, e) (at most kClipBlock, from a multiple of it) of a tensor:
-// 16-byte pieces, kDeep of a thread's loads in flight at once, then the
+// Elements [b, e) of a tensor (fewer than 2^31) by NT threads: 16-byte pieces, kDeep of a thread's loads in flight at once, then the
 // last few elements one by one.
 constexpr int kDeep = 4;
 
-template <int TY>
+template <int TY, int NT>
 __device__ inline double sumsq_range(const void* base, long b, long e) {
   using E = Elem<TY>;
   constexpr int N = 16 / E::kBytes;
@@ -107,14 +106,14 @@ __device__ inline double sumsq_range(const void* base, long b, long e) {
     }
   };
   int q = threadIdx.x;
-  for (; q + (kDeep - 1) * kClipThreads < pieces; q += kDeep * kClipThreads) {
+  for (; q + (kDeep - 1) * NT < pieces; q += kDeep * NT) {
     u32x4_t v[kDeep];
 #pragma unroll
-    for (int k = 0; k < kDeep; ++k) v[k] = load16(p + 16 * (q + k * kClipThreads));
+    for (int k = 0; k < kDeep; ++k) v[k] = load16(p + 16 * (q + k * NT));
 #pragma unroll
     for (int k = 0; k < kDeep; ++k) add(v[k]);
   }
-  for (; q < pieces; q += kClipThreads) add(load16(p + 16 * q));
+  for (; q < pieces; q += NT) add(load16(p + 16 * q));
   const int last = pieces * N + threadIdx.x;
   if (last < n) {
     const double x = E::get1(p + last * E::kBytes);
@@ -145,7 +144,7 @@ __device__ inline void scale_piece(u32x4_t v, char* o, float c) {
   }
 }
 
-template <int TI, int TO>
+template <int TI, int TO, int NT>
 __device__ inline void scale_range(const void* base, void* out, long b, long e, float c) {
   using I = Elem<TI>;
   using O = Elem<TO>;
@@ -154,23 +153,43 @@ __device__ inline void scale_range(const void* base, void* out, long b, long e, 
   char* o = static_cast<char*>(out) + b * O::kBytes;
   const int n = (int)(e - b), pieces = n / N;
   int q = threadIdx.x;
-  for (; q + (kDeep - 1) * kClipThreads < pieces; q += kDeep * kClipThreads) {
+  for (; q + (kDeep - 1) * NT < pieces; q += kDeep * NT) {
     u32x4_t v[kDeep];
 #pragma unroll
-    for (int k = 0; k < kDeep; ++k) v[k] = load16(p + 16 * (q + k * kClipThreads));
+    for (int k = 0; k < kDeep; ++k) v[k] = load16(p + 16 * (q + k * NT));
 #pragma unroll
-    for (int k = 0; k < kDeep; ++k) scale_piece<TI, TO>(v[k], o + N * O::kBytes * (q + k * kClipThreads), c);
+    for (int k = 0; k < kDeep; ++k) scale_piece<TI, TO>(v[k], o + N * O::kBytes * (q + k * NT), c);
   }
-  for (; q < pieces; q += kClipThreads) scale_piece<TI, TO>(load16(p + 16 * q), o + N * O::kBytes * q, c);
+  for (; q < pieces; q += NT) scale_piece<TI, TO>(load16(p + 16 * q), o + N * O::kBytes * q, c);
   const int last = pieces * N + threadIdx.x;
   if (last < n) O::put1(o + last * O::kBytes, I::get1(p + last * I::kBytes) * c);
 }
 
-template <int TI>
+template <int TI, int NT>
 __device__ inline void scale_to(int to, const void* p, void* o, long b, long e, float c) {
-  if (to == kTypeF32) scale_range<TI, kTypeF32>(p, o, b, e, c);
-  else if (to == kTypeBf16) scale_range<TI, kTypeBf16>(p, o, b, e, c);
-  else scale_range<TI, kTypeF16>(p, o, b, e, c);
+  if (to == kTypeF32) scale_range<TI, kTypeF32, NT>(p, o, b, e, c);
+  else if (to == kTypeBf16) scale_range<TI, kTypeBf16, NT>(p, o, b, e, c);
+  else scale_range<TI, kTypeF16, NT>(p, o, b, e, c);
+}
+
+template <int NT>
+__device__ inline double sumsq_of(int ty, const void* p, long b, long e) {
+  if (ty == kTypeF32) return sumsq_range<kTypeF32, NT>(p, b, e);
+  if (ty == kTypeBf16) return sumsq_range<kTypeBf16, NT>(p, b, e);
+  return sumsq_range<kTypeF16, NT>(p, b, e);
+}
+
+template <int NT>
+__device__ inline void scale_of(int ty, int to, const void* p, void* o, long b, long e, float c) {
+  if (ty == kTypeF32) scale_to<kTypeF32, NT>(to, p, o, b, e, c);
+  else if (ty == kTypeBf16) scale_to<kTypeBf16, NT>(to, p, o, b, e, c);
+  else scale_to<kTypeF16, NT>(to, p, o, b, e, c);
+}
+
+// min(1, max_norm / (n + 1e-6)); a NaN norm stays NaN, no limit is no limit
+__device__ inline float clip_factor(double n, double max_norm) {
+  const double r = max_norm / (n + 1e-6);
+  return r >= 1.0 || max_norm == INFINITY ? 1.f : (float)r;
 }
 
 }  // namespace
@@ -178,12 +197,7 @@ __device__ inline void scale_to(int to, const void* p, void* o, long b, long e, 
 __global__ __launch_bounds__(kClipThreads) void sumsq_kernel(SumsqTable t, double* part) {
   const int i = tensor_of(t.first, t.n, blockIdx.x);
   const long b = (long)(blockIdx.x - t.first[i]) * kClipBlock, e = min(b + kClipBlock, (long)t.numel[i]);
-  const int ty = t.type[i];
-  double s;
-  if (ty == kTypeF32) s = sumsq_range<kTypeF32>(t.in[i], b, e);
-  else if (ty == kTypeBf16) s = sumsq_range<kTypeBf16>(t.in[i], b, e);
-  else s = sumsq_range<kTypeF16>(t.in[i], b, e);
-  s = block_sum<kClipThreads>(s);
+  const double s = block_sum<kClipThreads>(sumsq_of<kClipThreads>(t.type[i], t.in[i], b, e));
   if (threadIdx.x == 0) part[blockIdx.x] = s;
 }
 
@@ -204,13 +218,26 @@ __global__ __launch_bounds__(kClipThreads) void clip_kernel(ClipTable t, const d
   const long b = (long)(blockIdx.x - t.first[i]) * kClipBlock, e = min(b + kClipBlock, (long)t.numel[i]);
   const double n = sqrt(*sumsq);
   if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)n;
-  const double r = max_norm / (n + 1e-6);
-  const float c = r >= 1.0 || max_norm == INFINITY ? 1.f : (float)r;  // a NaN norm stays NaN
+  const float c = clip_factor(n, max_norm);
   if (c == 1.f && t.in[i] == t.out[i]) return;
-  const int ty = t.in_type[i], to = t.out_type[i];
-  if (ty == kTypeF32) scale_to<kTypeF32>(to, t.in[i], t.out[i], b, e, c);
-  else if (ty == kTypeBf16) scale_to<kTypeBf16>(to, t.in[i], t.out[i], b, e, c);
-  else scale_to<kTypeF16>(to, t.in[i], t.out[i], b, e, c);
+  scale_of<kClipThreads>(t.in_type[i], t.out_type[i], t.in[i], t.out[i], b, e, c);
+}
+
+// Few elements: norm and clip by one workgroup (three launches would take
+// three times as long as the work).
+__global__ __launch_bounds__(1024) void clip_small_kernel(ClipTable t, double* sumsq, double max_norm, float* norm) {
+  double s = 0;
+  for (int i = 0; i < t.n; ++i) s += sumsq_of<1024>(t.in_type[i], t.in[i], 0, t.numel[i]);
+  s = block_sum<1024>(s);
+  const double n = sqrt(s);
+  const float c = clip_factor(n, max_norm);
+  if (threadIdx.x == 0) {
+    *sumsq = s;
+    *norm = (float)n;
+  }
+  for (int i = 0; i < t.n; ++i)
+    if (c != 1.f || t.in[i] != t.out[i])
+      scale_of<1024>(t.in_type[i], t.out_type[i], t.in[i], t.out[i], 0, t.numel[i], c);
 }
 
 __global__ void norm_kernel(const double* sumsq, float* norm) { *norm = (float)sqrt(*sumsq); }
@@ -225,6 +252,10 @@ hipError_t launch_sumsq_total(const double* part, int64_t n, double* sumsq, hipS
 }
 hipError_t launch_clip(const ClipTable& t, const double* sumsq, double max_norm, float* norm, hipStream_t st) {
   hipLaunchKernelGGL(clip_kernel, dim3(t.first[t.n]), dim3(kClipThreads), 0, st, t, sumsq, max_norm, norm);
+  return hipGetLastError();
+}
+hipError_t launch_clip_small(const ClipTable& t, double* sumsq, double max_norm, float* norm, hipStream_t st) {
+  hipLaunchKernelGGL(clip_small_kernel, dim3(1), dim3(1024), 0, st, t, sumsq, max_norm, norm);
   return hipGetLastError();
 }
 hipError_t launch_norm(const double* sumsq, float* norm, hipStream_t st) {

@@ -207,10 +207,10 @@ constexpr int kFzCols = 2048;
 template <class E, bool kEnt>
 __global__ __launch_bounds__(256) void logp_direct_dz_from_z_kernel(LogpDirectArgs a) {
   const long M = chunk_rows_of(a.rs);
-  const long i = blockIdx.y;
+  const long per = (a.V + kFzCols - 1) / kFzCols, i = blockIdx.x / per;
   if (i >= (M + 127) / 128 * 128) return;
   const DzConst k = dz_const(a, i < M, i < M ? row_at(a.rs, i) : 0);
-  const long c0 = (long)blockIdx.x * kFzCols + threadIdx.x * 4;
+  const long c0 = (long)(blockIdx.x - i * per) * kFzCols + threadIdx.x * 4;
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
     const long c = c0 + q * (kFzCols / 2);
@@ -429,7 +429,7 @@ hipError_t launch_logp_direct_dz(int elem, const LogpDirectArgs& a, hipStream_t 
 }
 
 hipError_t launch_logp_direct_dz_from_z(int elem, const LogpDirectArgs& a, hipStream_t st) {
-  const dim3 grid((unsigned)cdiv(a.V, kFzCols), (unsigned)(cdiv(rows_upto(a.rs), 128) * 128));
+  const dim3 grid((unsigned)((int64_t)cdiv(a.V, kFzCols) * cdiv(rows_upto(a.rs), 128) * 128));
   if (elem == 2 && a.ge)
     hipLaunchKernelGGL((logp_direct_dz_from_z_kernel<Bf16, true>), grid, dim3(256), 0, st, a);
   else if (elem == 2)

@@ -216,5 +216,8 @@ hipError_t launch_sumsq_total(const double* part, int64_t n, double* sumsq, hipS
 // norm (nullable) is written too
 hipError_t launch_clip(const ClipTable& t, const double* sumsq, double max_norm, float* norm, hipStream_t st);
 hipError_t launch_norm(const double* sumsq, float* norm, hipStream_t st);
+// everything in one workgroup, for at most kClipSmall elements in all
+constexpr int64_t kClipSmall = 65536;
+hipError_t launch_clip_small(const ClipTable& t, double* sumsq, double max_norm, float* norm, hipStream_t st);
 
 }  // namespace kd

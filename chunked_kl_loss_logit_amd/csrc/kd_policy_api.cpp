@@ -1,5 +1,7 @@
 // C-ABI entry points of kdpolicy.h: argument checks, workspace planning and
 // the launch sequence of each call.
+#include <exception>
+
 #include "kd_host.h"
 #include "kd_policy.h"
 #include "kdpolicy.h"
@@ -80,6 +82,13 @@ LogpPlan plan_logp(int64_t T, int64_t d, int64_t V, int elem, int dw_elem, int64
 kd_status check_dw_type(kd_dtype dt, kd_dtype dw) {
   if (dw != KD_F32 && dw != KD_BF16) return fail(KD_ERR_INVALID_ARG, "dw_dtype must be KD_F32 or KD_BF16");
   if (dw == KD_BF16 && dt != KD_BF16) return fail(KD_ERR_UNSUPPORTED, "a bf16 dW needs bf16 inputs");
+  return KD_OK;
+}
+
+kd_status check_widths(int64_t T, int64_t d, int64_t V, kd_dtype dt, float tau) {
+  KD_TRY(check_common(T, d, V, dt, tau));
+  // the register-fed tiles address up to 16 rows of an operand with 32 bits
+  if (d >= (1 << 25) || V >= (1 << 25)) return fail(KD_ERR_UNSUPPORTED, "d and V must be below 2^25");
   return KD_OK;
 }
 
@@ -187,20 +196,19 @@ kd_status logp_bwd(const void* H, const void* W, const int32_t* tokens, const ui
                    const float* logits, const float* g, const float* ge, void* dH, int dh_elem, void* dW,
                    kd_dtype dw_dtype, int64_t chunk_rows, void* workspace, size_t workspace_bytes, void* stream) {
   g_err.clear();
-  KD_TRY(check_common(T, d, V, dt, tau));
+  KD_TRY(check_widths(T, d, V, dt, tau));
   KD_TRY(check_v0(V, v0));
   KD_TRY(check_dw_type(dt, dw_dtype));
   if (chunk_rows < 0) return fail(KD_ERR_INVALID_ARG, "chunk_rows must be >= 0");
-  KD_TRY(need(dW, "dW"));
+  if (!dH && !dW && T > 0) return fail(KD_ERR_INVALID_ARG, "dH and dW are both NULL");
   KD_TRY(need_align(dW, 16, "dW"));
   hipStream_t st = static_cast<hipStream_t>(stream);
   if (T == 0) {
-    KD_LAUNCH("fill_zero", st, kd::launch_fill_zero(dW, d * V * elem_of(dw_dtype), st));
+    if (dW) KD_LAUNCH("fill_zero", st, kd::launch_fill_zero(dW, d * V * elem_of(dw_dtype), st));
     return KD_OK;
   }
   KD_TRY(check_head(H, W, tokens));
   KD_TRY(need(lse, "lse"));
-  KD_TRY(need(dH, "dH"));
   KD_TRY(need_align(dH, 16, "dH"));
   KD_TRY(need_align(lse, 4, "lse"));
   KD_TRY(need_align(g, 4, "grad_logp"));
@@ -238,8 +246,8 @@ kd_status logp_bwd(const void* H, const void* W, const int32_t* tokens, const ui
       if (mask) {
         char* packed = at<char>(workspace, p.o_hc);
         KD_LAUNCH("logp_prep", st,
-                  kd::launch_logp_prep(mask, T, c.rows, c.count, H, d * elem, c0, p.C, packed, c0 == 0 ? dH : nullptr,
-                                       d * dh_elem, st));
+                  kd::launch_logp_prep(mask, T, c.rows, c.count, H, d * elem, c0, p.C, dW ? packed : nullptr,
+                                       c0 == 0 ? dH : nullptr, d * dh_elem, st));
         hc = packed;
       }
       if (logits) {
@@ -248,8 +256,10 @@ kd_status logp_bwd(const void* H, const void* W, const int32_t* tokens, const ui
       } else {
         KD_LAUNCH("logp_direct_dz", st, kd::launch_logp_direct_dz(elem, a, st));
       }
-      KD_LAUNCH("logp_direct_dh", st,
-                kd::launch_logp_direct_dh(elem, a, p.S_dh, at<float>(workspace, p.o_dhp), dH, dh_elem, st));
+      if (dH)
+        KD_LAUNCH("logp_direct_dh", st,
+                  kd::launch_logp_direct_dh(elem, a, p.S_dh, at<float>(workspace, p.o_dhp), dH, dh_elem, st));
+      if (!dW) continue;
       // a float32 dW adds up in place; a bf16 one in the workspace, rounded with the last chunk
       const bool f32 = dw_dtype == KD_F32, last = c0 + p.C >= T;
       float* acc = f32 ? static_cast<float*>(dW) : dw32;
@@ -266,10 +276,10 @@ kd_status logp_bwd(const void* H, const void* W, const int32_t* tokens, const ui
   const bool dw_direct = dw_dtype == KD_BF16 && p.C >= T;  // one chunk: rounded where it is made
   float* dw32 = dw_dtype == KD_F32 ? static_cast<float*>(dW) : at<float>(workspace, p.o_dw32);
   KD_LAUNCH("compact", st, kd::launch_compact(mask, T, c, st));
-  KD_LAUNCH("zero_masked_rows", st, kd::launch_zero_masked_rows(mask, T, d * dh_elem, dH, st));
+  if (dH) KD_LAUNCH("zero_masked_rows", st, kd::launch_zero_masked_rows(mask, T, d * dh_elem, dH, st));
   // dH's last ring turn: zero pieces after dZ's tail piece
   const int64_t stages = cdiv(V, 32), pads = cdiv(stages, 4) * 4 - stages, tail = V % 32 ? 1 : 0;
-  if (pads > 0)
+  if (dH && pads > 0)
     KD_LAUNCH("fill_zero", st, kd::launch_fill_zero(dz + (p.ldz / 32 + tail) * p.C * 64, pads * p.C * 64, st));
   kd::LogpDzArgs a{};
   a.Hp = hp;
@@ -300,7 +310,6 @@ kd_status logp_bwd(const void* H, const void* W, const int32_t* tokens, const ui
       KD_TRY(head_panels(H, d, c, c0, p.C, hp, st));
       KD_LAUNCH("logp_dz_tile", st, kd::launch_logp_dz(a, st));
     }
-    KD_LAUNCH("gather_transpose", st, kd::launch_gather_transpose(H, elem, d, c, c0, p.C, hT, st));
     kd::LogpDhArgs ha{};
     ha.dz = dz;
     ha.W = a.W;
@@ -315,7 +324,9 @@ kd_status logp_bwd(const void* H, const void* W, const int32_t* tokens, const ui
     ha.grid = p.grid_dh;
     ha.ncb = (int)cdiv(d, 256);
     ha.group = kRasterGroup;
-    KD_LAUNCH("logp_dh_tile", st, kd::launch_logp_dh(ha, c.rows, dH, dh_elem, st));
+    if (dH) KD_LAUNCH("logp_dh_tile", st, kd::launch_logp_dh(ha, c.rows, dH, dh_elem, st));
+    if (!dW) continue;
+    KD_LAUNCH("gather_transpose", st, kd::launch_gather_transpose(H, elem, d, c, c0, p.C, hT, st));
     kd::DwArgs wa{};
     wa.hT = hT;
     wa.dz = dz;
@@ -335,7 +346,7 @@ kd_status logp_bwd(const void* H, const void* W, const int32_t* tokens, const ui
     else
       KD_LAUNCH("dw_tile", st, kd::launch_dw(elem, wa, st));
   }
-  if (dw_dtype == KD_BF16 && !dw_direct) KD_LAUNCH("to_bf16", st, kd::launch_to_bf16(dw32, dW, d * V, st));
+  if (dW && dw_dtype == KD_BF16 && !dw_direct) KD_LAUNCH("to_bf16", st, kd::launch_to_bf16(dw32, dW, d * V, st));
   return KD_OK;
 }
 
@@ -346,7 +357,7 @@ extern "C" {
 kd_status kd_token_logp_logits_size(int64_t T, int64_t V, size_t* bytes) {
   g_err.clear();
   KD_TRY(need(bytes, "bytes"));
-  KD_TRY(check_common(T, 8, V, KD_F32, 1.0f));
+  KD_TRY(check_widths(T, 8, V, KD_F32, 1.0f));
   *bytes = (size_t)T * (size_t)(cdiv(V, kd::kTileN) * kd::kTileN) * 4;
   return KD_OK;
 }
@@ -355,7 +366,7 @@ kd_status kd_token_logp_workspace_size(int64_t T, int64_t d, int64_t V, kd_dtype
                                        int64_t chunk_rows, size_t* bytes) {
   g_err.clear();
   KD_TRY(need(bytes, "bytes"));
-  KD_TRY(check_common(T, d, V, dt, 1.0f));
+  KD_TRY(check_widths(T, d, V, dt, 1.0f));
   KD_TRY(check_dw_type(dt, dw_dtype));
   if (chunk_rows < 0) return fail(KD_ERR_INVALID_ARG, "chunk_rows must be >= 0");
   *bytes = T == 0 ? 0 : plan_logp(T, d, V, elem_of(dt), elem_of(dw_dtype), chunk_rows).total;
@@ -366,7 +377,7 @@ kd_status kd_token_logp_fwd(const void* H, const void* W, const int32_t* tokens,
                             int64_t T, int64_t d, int64_t V, kd_dtype dt, float* logp, float* lse, float* entropy,
                             float* logits, void* workspace, size_t workspace_bytes, void* stream) {
   g_err.clear();
-  KD_TRY(check_common(T, d, V, dt, tau));
+  KD_TRY(check_widths(T, d, V, dt, tau));
   if (T == 0) return KD_OK;
   KD_TRY(check_head(H, W, tokens));
   KD_TRY(need(logp, "logp"));
@@ -392,7 +403,7 @@ kd_status kd_token_logp_fwd_shard(const void* H, const void* W, const int32_t* t
                                   int64_t T, int64_t d, int64_t V, int64_t v0, kd_dtype dt, float* rec, float* logits,
                                   void* workspace, size_t workspace_bytes, void* stream) {
   g_err.clear();
-  KD_TRY(check_common(T, d, V, dt, tau));
+  KD_TRY(check_widths(T, d, V, dt, tau));
   KD_TRY(check_v0(V, v0));
   if (T == 0) return KD_OK;
   KD_TRY(check_head(H, W, tokens));
@@ -755,7 +766,11 @@ kd_status check_overlap(const void* const* in, const int32_t* ty, void* const* o
     bool out;
   };
   std::vector<Range> r;
-  r.reserve(2 * n);
+  try {
+    r.reserve(2 * n);
+  } catch (const std::exception&) {  // no exception leaves a C entry
+    return fail(KD_ERR_UNSUPPORTED, "too many tensors");
+  }
   for (int64_t i = 0; i < n; ++i) {
     if (numel[i] == 0) continue;
     const uintptr_t x = reinterpret_cast<uintptr_t>(in[i]), y = reinterpret_cast<uintptr_t>(out[i]);
@@ -798,6 +813,57 @@ kd_status over_tables(const int64_t* numel, int64_t n, Set&& set, F&& f) {
   return KD_OK;
 }
 
+kd_status sumsq_launches(const void* const* grads, const int64_t* numel, const int32_t* dtypes, int64_t n,
+                         int64_t blocks, double* sumsq, double* part, hipStream_t st) {
+  KD_TRY(over_tables<kd::SumsqTable>(
+      numel, n,
+      [&](kd::SumsqTable& t, int k, int64_t i) {
+        t.in[k] = grads[i];
+        t.type[k] = (uint8_t)dtypes[i];
+      },
+      [&](const kd::SumsqTable& t, int64_t base) {
+        KD_LAUNCH("grad_sumsq", st, kd::launch_sumsq(t, part + base, st));
+        return KD_OK;
+      }));
+  KD_LAUNCH("grad_sumsq_total", st, kd::launch_sumsq_total(part, blocks, sumsq, st));
+  return KD_OK;
+}
+
+kd_status check_clip(const void* const* grads, const int64_t* numel, const int32_t* dtypes, int64_t n,
+                     void* const* outs, const int32_t* out_dtypes, const double* sumsq, double max_norm,
+                     const float* norm, int64_t* blocks) {
+  KD_TRY(check_counts(numel, n, blocks));
+  KD_TRY(check_tensors(grads, numel, dtypes, n, "grads"));
+  KD_TRY(check_tensors(outs, numel, out_dtypes, n, "outs"));
+  if (n > 0) KD_TRY(check_overlap(grads, dtypes, outs, out_dtypes, numel, n));
+  if (!(max_norm >= 0)) return fail(KD_ERR_INVALID_ARG, "max_norm must be >= 0");
+  KD_TRY(need(sumsq, "sumsq"));
+  KD_TRY(need(norm, "norm"));
+  KD_TRY(need_align(sumsq, 8, "sumsq"));
+  KD_TRY(need_align(norm, 4, "norm"));
+  return KD_OK;
+}
+
+void set_clip(kd::ClipTable& t, int k, const void* const* grads, const int32_t* dtypes, void* const* outs,
+              const int32_t* out_dtypes, int64_t i) {
+  t.in[k] = grads[i];
+  t.out[k] = outs[i];
+  t.in_type[k] = (uint8_t)dtypes[i];
+  t.out_type[k] = (uint8_t)out_dtypes[i];
+}
+
+kd_status clip_launches(const void* const* grads, const int64_t* numel, const int32_t* dtypes, int64_t n,
+                        int64_t blocks, void* const* outs, const int32_t* out_dtypes, const double* sumsq,
+                        double max_norm, float* norm, hipStream_t st) {
+  if (blocks == 0) KD_LAUNCH("grad_norm", st, kd::launch_norm(sumsq, norm, st));
+  return over_tables<kd::ClipTable>(
+      numel, n, [&](kd::ClipTable& t, int k, int64_t i) { set_clip(t, k, grads, dtypes, outs, out_dtypes, i); },
+      [&](const kd::ClipTable& t, int64_t base) {  // the first launch writes the norm
+        KD_LAUNCH("grad_clip", st, kd::launch_clip(t, sumsq, max_norm, base == 0 ? norm : nullptr, st));
+        return KD_OK;
+      });
+}
+
 }  // namespace
 
 extern "C" {
@@ -820,20 +886,8 @@ kd_status kd_grad_sumsq(const void* const* grads, const int64_t* numel, const in
   KD_TRY(need(sumsq, "sumsq"));
   KD_TRY(need_align(sumsq, 8, "sumsq"));
   KD_TRY(check_workspace(workspace, workspace_bytes, up((size_t)blocks * 8, kAlign)));
-  double* part = at<double>(workspace, 0);
-  hipStream_t st = static_cast<hipStream_t>(stream);
-  KD_TRY(over_tables<kd::SumsqTable>(
-      numel, n,
-      [&](kd::SumsqTable& t, int k, int64_t i) {
-        t.in[k] = grads[i];
-        t.type[k] = (uint8_t)dtypes[i];
-      },
-      [&](const kd::SumsqTable& t, int64_t base) {
-        KD_LAUNCH("grad_sumsq", st, kd::launch_sumsq(t, part + base, st));
-        return KD_OK;
-      }));
-  KD_LAUNCH("grad_sumsq_total", st, kd::launch_sumsq_total(part, blocks, sumsq, st));
-  return KD_OK;
+  return sumsq_launches(grads, numel, dtypes, n, blocks, sumsq, at<double>(workspace, 0),
+                        static_cast<hipStream_t>(stream));
 }
 
 kd_status kd_grad_clip(const void* const* grads, const int64_t* numel, const int32_t* dtypes, int64_t n,
@@ -841,29 +895,30 @@ kd_status kd_grad_clip(const void* const* grads, const int64_t* numel, const int
                        float* norm, void* stream) {
   g_err.clear();
   int64_t blocks = 0;
-  KD_TRY(check_counts(numel, n, &blocks));
-  KD_TRY(check_tensors(grads, numel, dtypes, n, "grads"));
-  KD_TRY(check_tensors(outs, numel, out_dtypes, n, "outs"));
-  if (n > 0) KD_TRY(check_overlap(grads, dtypes, outs, out_dtypes, numel, n));
-  if (!(max_norm >= 0)) return fail(KD_ERR_INVALID_ARG, "max_norm must be >= 0");
-  KD_TRY(need(sumsq, "sumsq"));
-  KD_TRY(need(norm, "norm"));
-  KD_TRY(need_align(sumsq, 8, "sumsq"));
-  KD_TRY(need_align(norm, 4, "norm"));
+  KD_TRY(check_clip(grads, numel, dtypes, n, outs, out_dtypes, sumsq, max_norm, norm, &blocks));
+  return clip_launches(grads, numel, dtypes, n, blocks, outs, out_dtypes, sumsq, max_norm, norm,
+                       static_cast<hipStream_t>(stream));
+}
+
+kd_status kd_grad_clip_norm(const void* const* grads, const int64_t* numel, const int32_t* dtypes, int64_t n,
+                            void* const* outs, const int32_t* out_dtypes, double max_norm, double* sumsq,
+                            float* norm, void* workspace, size_t workspace_bytes, void* stream) {
+  g_err.clear();
+  int64_t blocks = 0;
+  KD_TRY(check_clip(grads, numel, dtypes, n, outs, out_dtypes, sumsq, max_norm, norm, &blocks));
+  KD_TRY(check_workspace(workspace, workspace_bytes, up((size_t)blocks * 8, kAlign)));
   hipStream_t st = static_cast<hipStream_t>(stream);
-  if (blocks == 0) KD_LAUNCH("grad_norm", st, kd::launch_norm(sumsq, norm, st));
-  return over_tables<kd::ClipTable>(
-      numel, n,
-      [&](kd::ClipTable& t, int k, int64_t i) {
-        t.in[k] = grads[i];
-        t.out[k] = outs[i];
-        t.in_type[k] = (uint8_t)dtypes[i];
-        t.out_type[k] = (uint8_t)out_dtypes[i];
-      },
-      [&](const kd::ClipTable& t, int64_t base) {  // the first launch writes the norm
-        KD_LAUNCH("grad_clip", st, kd::launch_clip(t, sumsq, max_norm, base == 0 ? norm : nullptr, st));
-        return KD_OK;
-      });
+  int64_t total = 0;
+  for (int64_t i = 0; i < n; ++i) total += numel[i];  // below 2^46: check_counts bounds the blocks
+  if (blocks > 0 && n <= kd::ClipTable::kTensors && total <= kd::kClipSmall)
+    return over_tables<kd::ClipTable>(
+        numel, n, [&](kd::ClipTable& t, int k, int64_t i) { set_clip(t, k, grads, dtypes, outs, out_dtypes, i); },
+        [&](const kd::ClipTable& t, int64_t) {
+          KD_LAUNCH("grad_clip_small", st, kd::launch_clip_small(t, sumsq, max_norm, norm, st));
+          return KD_OK;
+        });
+  KD_TRY(sumsq_launches(grads, numel, dtypes, n, blocks, sumsq, at<double>(workspace, 0), st));
+  return clip_launches(grads, numel, dtypes, n, blocks, outs, out_dtypes, sumsq, max_norm, norm, st);
 }
 
 }  // extern "C"

@@ -13,6 +13,7 @@ libkdloss.so; this module allocates outputs and workspaces with torch.
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _policy_binding as B
 
@@ -45,11 +46,12 @@ def token_logp_forward(H, W, tokens, mask=None, tau=1.0, want_entropy=False, kee
 
 
 def token_logp_backward(H, W, tokens, mask, tau, lse, grad_logp, entropy=None, grad_entropy=None, logits=None,
-                        chunk_rows=0, dw_dtype=torch.float32, workspace=None):
-    """dH (dtype of H) and dW (dw_dtype) for the upstream gradients of logp and of the entropy (either may be None)."""
+                        chunk_rows=0, dw_dtype=torch.float32, workspace=None, want=(True, True)):
+    """dH (dtype of H) and dW (dw_dtype) for the upstream gradients of logp and of the entropy (either may be None).
+    want: whether dH and dW are wanted; the other is None and costs nothing."""
     T, d, V = B._logp_in(H, W, tokens, mask)
-    dH = torch.empty_like(H)
-    dW = torch.empty(d, V, dtype=dw_dtype, device=H.device)
+    dH = torch.empty_like(H) if want[0] else None
+    dW = torch.empty(d, V, dtype=dw_dtype, device=H.device) if want[1] else None
     if workspace is None:
         workspace = _workspace(B.kd_token_logp_workspace_size(T, d, V, H.dtype, dw_dtype, chunk_rows), H.device)
     B.kd_token_logp_bwd(H, W, tokens, mask, tau, lse, entropy, logits, _grad(grad_logp), _grad(grad_entropy), dH, dW,
@@ -103,11 +105,13 @@ class _TokenLogp(torch.autograd.Function):
         return (logp, entropy) if want_entropy else logp
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, g, ge=None):
         H, W, tokens, mask, lse, entropy, logits = ctx.saved_tensors
         if g is None and ge is None:
             return (None,) * 8
-        dH, dW = token_logp_backward(H, W, tokens, mask, ctx.tau, lse, g, entropy, ge, logits, ctx.chunk_rows, W.dtype)
+        dH, dW = token_logp_backward(H, W, tokens, mask, ctx.tau, lse, g, entropy, ge, logits, ctx.chunk_rows, W.dtype,
+                                     want=ctx.needs_input_grad[:2])
         return dH, dW, None, None, None, None, None, None
 
 
@@ -178,6 +182,7 @@ class _PolicyLoss(torch.autograd.Function):
         return total, stats
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, g, _):
         if g is None:
             return (None,) * 8
@@ -251,6 +256,7 @@ class _PreferenceLoss(torch.autograd.Function):
         return loss, rewards
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, g, _):
         if g is None:
             return (None,) * 5
@@ -264,14 +270,6 @@ def preference_loss(logp, cu_seqlens, mask=None, ref_logp=None, **options):
 
 
 # ---------------------------------------------------------------- gradient norm and clipping
-def _sumsq(table, device, workspace=None):
-    sumsq = torch.empty(1, dtype=torch.float64, device=device)
-    if workspace is None:
-        workspace = _workspace(B.kd_grad_norm_workspace_size(table), device)
-    B.kd_grad_sumsq(table, sumsq, workspace)
-    return sumsq
-
-
 def _tensors(tensors):
     tensors = [tensors] if isinstance(tensors, torch.Tensor) else [t for t in tensors if t is not None]
     if not tensors:
@@ -282,24 +280,33 @@ def _tensors(tensors):
 def grad_sumsq(tensors):
     """The sum of all elements' squares, [1] float64 on the device: what ranks that hold parts of the gradients add up
     before clip_grad_norm(..., sumsq=...)."""
-    tensors = _tensors(tensors)
-    return _sumsq(B.TensorTable("tensors", tensors), tensors[0].device)
+    table = B.TensorTable("tensors", _tensors(tensors))
+    device = table.tensors[0].device
+    sumsq = torch.empty(1, dtype=torch.float64, device=device)
+    B.kd_grad_sumsq(table, sumsq, _workspace(B.kd_grad_norm_workspace_size(table), device))
+    return sumsq
 
 
 def clip_grad_norm(tensors, max_norm, out=None, sumsq=None):
     """Writes tensors[i] * min(1, max_norm / (norm + 1e-6)) to out[i] (the same number of elements in the same order
-    in memory; float32, bfloat16 or float16) and returns the global L2 norm, one float32 on the device.  out = None: in place.  None entries among
-    the tensors are left out (not with out).  sumsq: the squared norm if it is not that of these tensors alone."""
+    in memory; float32, bfloat16 or float16) and returns the global L2 norm, one float32 on the device.  out = None: in
+    place, and None entries among the tensors are left out.  sumsq: the squared norm, if it is not that of these
+    tensors alone."""
+    if not isinstance(tensors, torch.Tensor):
+        tensors = list(tensors)
     kept = _tensors(tensors)
     table = outs = B.TensorTable("tensors", kept)
     if out is not None:
         outs = B.TensorTable("out", [out] if isinstance(out, torch.Tensor) else list(out))
-        if len(kept) != (1 if isinstance(tensors, torch.Tensor) else len(tensors)):
+        if not isinstance(tensors, torch.Tensor) and len(kept) != len(tensors):
             raise ValueError("with out, no tensor may be None")
-    if sumsq is None:
-        sumsq = _sumsq(table, kept[0].device)
-    norm = torch.empty((), dtype=torch.float32, device=kept[0].device)
-    B.kd_grad_clip(table, outs, sumsq, max_norm, norm)
+    device = kept[0].device
+    norm = torch.empty((), dtype=torch.float32, device=device)
+    if sumsq is not None:
+        B.kd_grad_clip(table, outs, sumsq, max_norm, norm)
+    else:
+        B.kd_grad_clip_norm(table, outs, max_norm, torch.empty(1, dtype=torch.float64, device=device), norm,
+                            _workspace(B.kd_grad_norm_workspace_size(table), device))
     return norm
 
 

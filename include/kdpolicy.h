@@ -36,7 +36,8 @@ extern "C" {
  *   dZ_t       = (1/tau) ( g_t [v = tokens[t]] - q_v (g_t + e_t (entropy[t] + log q_v)) )
  * for the upstream gradients g = grad_logp and e = grad_entropy; dH = dZ . W^T, dW = H^T . dZ.
  * tokens [T] int32; logp, lse, entropy, grad_logp, grad_entropy [T] float32.
- * The rules for H, W, d, V, mask and tau are those of kd_topk_kl_fwd.
+ * The rules for H, W, d, V, mask and tau are those of kd_topk_kl_fwd; d and V
+ * must be below 2^25 (KD_ERR_UNSUPPORTED).
  * Masked rows get logp = lse = entropy = 0 and dH = 0, add nothing to dW and
  * are never read beyond mask[t].  A token of a valid row outside [0, V) gives
  * logp = NaN; its dZ has no token term.
@@ -58,7 +59,9 @@ kd_status kd_token_logp_fwd(const void* H, const void* W, const int32_t* tokens,
                             int64_t T, int64_t d, int64_t V, kd_dtype dt, float* logp, float* lse, float* entropy,
                             float* logits, void* workspace, size_t workspace_bytes, void* stream);
 /* dH [T,d] (dtype dt) and dW [d,V] (dw_dtype: KD_F32, or KD_BF16 for bf16
- * inputs), both overwritten.  grad_logp or grad_entropy may be NULL (zero),
+ * inputs), both overwritten; either may be NULL where it is not needed (a
+ * frozen head), not both.  dZ is rounded to the inputs' type before its two
+ * products, as for the other losses.  grad_logp or grad_entropy may be NULL (zero),
  * not both.  grad_entropy needs entropy, the forward's output.  logits: the
  * forward's, or NULL.  A bf16 dW is the rounded float32 sum over all rows
  * (several chunks add up in a float32 buffer of the workspace).
@@ -202,6 +205,12 @@ kd_status kd_grad_sumsq(const void* const* grads, const int64_t* numel, const in
 kd_status kd_grad_clip(const void* const* grads, const int64_t* numel, const int32_t* dtypes, int64_t n,
                        void* const* outs, const int32_t* out_dtypes, const double* sumsq, double max_norm,
                        float* norm, void* stream);
+
+/* Both at once, over the same tensors: sumsq and norm as above.  Up to 2^16
+ * elements in at most 128 tensors are one launch. */
+kd_status kd_grad_clip_norm(const void* const* grads, const int64_t* numel, const int32_t* dtypes, int64_t n,
+                            void* const* outs, const int32_t* out_dtypes, double max_norm, double* sumsq,
+                            float* norm, void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

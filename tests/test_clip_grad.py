@@ -59,7 +59,7 @@ def test_unaligned_views(offset, dtype):
         assert torch.equal(flat[lo:hi], keep[lo:hi])
 
 
-@pytest.mark.parametrize("count", [2, 95, 96, 97, 300])
+@pytest.mark.parametrize("count", [2, 20, 95, 96, 97, 131, 132, 133, 188, 189, 300, 400])
 def test_many_tensors_of_all_types(count):
     """More tensors than one launch takes, empty ones among them."""
     types = [f32, bf, f16]
@@ -149,3 +149,39 @@ def test_repeatable_and_graph():
         got = kd.clip_grad_norm(ts, 0.5, outs)
     s.synchronize()
     assert torch.equal(got, want)
+
+
+def test_refusals():
+    x, y = torch.ones(100, device="cuda"), torch.ones(100, device="cuda")
+    for bad, err in (([x, x], kd.KDError), ([x, x[50:]], kd.KDError), ([x[::2]], ValueError), ([x, y.cpu()], ValueError),
+                     ([x, torch.ones(3, dtype=torch.int32, device="cuda")], TypeError)):
+        with pytest.raises(err):
+            kd.clip_grad_norm_(bad, 1.0)
+    for out in ([y[:50]], [y, y], [x[1:]], [torch.ones(100, 2, device="cuda")]):
+        with pytest.raises((ValueError, kd.KDError)):
+            kd.clip_grad_norm([x], 1.0, out)
+    with pytest.raises(ValueError):
+        kd.clip_grad_norm([x, None], 1.0, [y, y])
+    a = torch.ones(4, 5, device="cuda")
+    with pytest.raises(ValueError, match="strides"):
+        kd.clip_grad_norm([a], 1.0, [torch.ones(5, 4, device="cuda").t()])
+    with pytest.raises(kd.KDError):
+        kd.clip_grad_norm([x], -1.0)
+    assert (x == 1).all() and (y == 1).all()
+
+
+def test_no_gradients_and_generators():
+    x = torch.full((9,), 2.0, device="cuda")
+    assert float(kd.clip_grad_norm_((t for t in (None, x)), 1.0)) == 6.0
+    assert abs(float(x.norm()) - 1.0) < 1e-5
+    assert float(kd.clip_grad_norm_([torch.empty(0, device="cuda")], 1.0)) == 0.0
+
+
+def test_autograd_sees_the_change():
+    """A tensor clipped in place between a forward and its backward is refused there."""
+    w = torch.ones(50, device="cuda", requires_grad=True)
+    x = torch.full((50,), 3.0, device="cuda")
+    y = (w * x).sum()
+    kd.clip_grad_norm_([x], 1.0)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward()

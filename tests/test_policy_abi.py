@@ -76,7 +76,7 @@ def logp_bwd(L, H=F, W=F, tok=F, tau=1.0, T=8, d=64, V=256, dt=1, lse=F, ent=F, 
 @pytest.mark.parametrize("kw,code", [
     (dict(), 4), (dict(H=0), 1), (dict(W=0), 1), (dict(tok=0), 1), (dict(logp=0), 1), (dict(lse=0), 1),
     (dict(ent=0), 4), (dict(z=0), 4), (dict(tau=0.0), 1), (dict(tau=math.nan), 1), (dict(T=-1), 1), (dict(d=60), 2),
-    (dict(V=260), 2), (dict(dt=2), 1), (dict(T=1 << 31), 2), (dict(H=F + 8), 3), (dict(W=F + 2), 3), (dict(tok=F + 1), 3),
+    (dict(V=260), 2), (dict(V=1 << 25), 2), (dict(d=1 << 25), 2), (dict(dt=2), 1), (dict(T=1 << 31), 2), (dict(H=F + 8), 3), (dict(W=F + 2), 3), (dict(tok=F + 1), 3),
     (dict(z=F + 4), 3), (dict(ent=F + 1), 3), (dict(ws=0), 1), (dict(ws=F + 16, wsb=1 << 40), 3), (dict(T=0, H=0), 0),
 ])
 def test_token_logp_fwd_refuses(L, kw, code):
@@ -86,7 +86,7 @@ def test_token_logp_fwd_refuses(L, kw, code):
 
 @pytest.mark.parametrize("kw,code", [
     (dict(), 4), (dict(lse=0), 1), (dict(g=0, ge=0), 1), (dict(g=0), 4), (dict(ge=0, ent=0), 4), (dict(ent=0), 1),
-    (dict(dH=0), 1), (dict(dW=0), 1), (dict(dW=F + 8), 3), (dict(dH=F + 8), 3), (dict(dw=1), 4), (dict(dw=2), 1),
+    (dict(dH=0, dW=0), 1), (dict(dH=0), 4), (dict(dW=0), 4), (dict(dW=F + 8), 3), (dict(dH=F + 8), 3), (dict(dw=1), 4), (dict(dw=2), 1),
     (dict(dt=0, dw=1), 2), (dict(chunk=-1), 1), (dict(z=F + 8), 3), (dict(g=F + 2), 3), (dict(V=0), 1),
 ])
 def test_token_logp_bwd_refuses(L, kw, code):
@@ -198,3 +198,15 @@ def test_grad_calls_refuse(L):
     assert L.kd_grad_sumsq((vp * 1)(A), n, t, 1, vp(F + 4), vp(F), 1 << 20, None) == 3
     assert L.kd_grad_sumsq((vp * 1)(A), n, t, 1, vp(F), vp(F), 8, None) == 4
     assert L.kd_grad_sumsq((vp * 1)(A), n, t, -1, vp(F), vp(F), 8, None) == 1
+
+
+def test_grad_clip_norm_refuses(L):
+    n, t = (ctypes.c_int64 * 2)(8, 100000), (ctypes.c_int32 * 2)(0, 1)
+    p, q = (vp * 2)(F, F + (1 << 20)), (vp * 2)(F, F + (1 << 21))
+
+    def call(outs=p, max_norm=1.0, sumsq=F, norm=F, ws=F, wsb=0):
+        return L.kd_grad_clip_norm(p, n, t, 2, outs, t, max_norm, vp(sumsq), vp(norm), vp(ws), wsb, None)
+
+    assert [call(), call(outs=q), call(max_norm=-1.0), call(sumsq=0), call(norm=0), call(norm=F + 2), call(sumsq=F + 4),
+            call(ws=0), call(ws=F + 8, wsb=1 << 20)] == [4, 4, 1, 1, 1, 3, 3, 1, 3]
+    assert call(outs=(vp * 2)(F, F + 16)) == 1 and "overlaps" in err()

@@ -313,3 +313,21 @@ def test_captured_and_replayed(T, V):
         torch.cuda.synchronize()
         for x, y in zip(out, want):
             assert torch.equal(x, y), f"replay {k}"
+
+
+@pytest.mark.parametrize("T,V,dtype", [(40, 520, bf), (1000, 7016, bf), (40, 520, f32)])
+def test_one_gradient_alone(T, V, dtype):
+    """A frozen head wants dH only, a probe on frozen states dW only; each is the same bits as together."""
+    H, W, tokens, mask = make_head(T, 128, V, dtype, 61, masked=0.2)
+    a = [dev(x) for x in (H, W, tokens, mask)]
+    g = torch.randn(T, device="cuda")
+    _, lse, _, z = kd.token_logp_forward(*a, 1.0, keep_logits=True)
+    for zz in (None, z):
+        dH, dW = kd.token_logp_backward(*a, 1.0, lse, g, logits=zz, dw_dtype=dtype)
+        x, none = kd.token_logp_backward(*a, 1.0, lse, g, logits=zz, dw_dtype=dtype, want=(True, False))
+        assert none is None and torch.equal(x, dH)
+        none, y = kd.token_logp_backward(*a, 1.0, lse, g, logits=zz, dw_dtype=dtype, want=(False, True))
+        assert none is None and torch.equal(y, dW)
+    h = a[0].clone().requires_grad_(True)
+    kd.token_logp(h, a[1], a[2], a[3]).backward(g)
+    assert a[1].grad is None and torch.equal(h.grad, kd.token_logp_backward(*a, 1.0, lse, g, dw_dtype=dtype)[0])
