@@ -238,12 +238,13 @@ __device__ inline Grads policy_token(const PolicyArgs& a, const Token& k, double
   double kl = 0.0;
   if (a.ref) {
     const double d = (double)k.ref - lp;
+    double dkl;
     if (a.kl_kind == 1) {
       kl = -d;
-      g += a.klw;
+      dkl = 1.0;
     } else if (a.kl_kind == 2) {
       kl = 0.5 * d * d;
-      g -= a.klw * d;
+      dkl = -d;
     } else {  // e = exp(d) - 1, exp(d) - 1 - d: by the series where the subtraction would cost digits
       double e, f;
       if (fabs(d) < 0x1p-6) {  // the first term left out, d^7 / 5040, is below 2^-48 of d
@@ -254,8 +255,9 @@ __device__ inline Grads policy_token(const PolicyArgs& a, const Token& k, double
         f = e - d;
       }
       kl = f;
-      g -= a.klw * e;
+      dkl = -e;
     }
+    if (a.klw != 0) g += a.klw * dkl;  // without weight it is only counted, infinite or not
   }
   const double h = a.ent ? (double)k.ent : 0.0;
   double loss = pg;
@@ -487,7 +489,8 @@ __device__ inline Pair pair_loss(const PrefArgs& a, double D) {
     const double soft = log1p(exp(-fabs(h)));
     const double q = exp(-fabs(h)) / (1.0 + exp(-fabs(h)));  // s(-|h|)
     const double up = h >= 0 ? q : 1.0 - q;                  // s(-h)
-    return {soft + (h >= 0 ? a.eps * h : -(1.0 - a.eps) * h), a.beta * (a.eps - up)};
+    const double wrong = a.eps == 0 ? 0.0 : a.eps * h;  // no part of an infinite h
+    return {soft + (h < 0 ? wrong - h : wrong), a.beta * (a.eps - up)};
   }
   if (a.kind == 1) return {h < 1 ? 1 - h : (h >= 1 ? 0.0 : h), h < 1 ? -a.beta : 0.0};
   const double u = D - 0.5 / a.beta;

@@ -40,6 +40,10 @@ struct LogpPlan {
   size_t o_dw32, total;  // float32 dW where a bf16 one adds up over chunks
 };
 
+// The most rows of a ring chunk, however many are asked for: H's panels keep
+// to the ring's 32-bit reach.  (At least the default chunk's rows: logp_ring_fits.)
+int64_t ring_rows(int64_t row_bytes) { return ((int64_t(1) << 32) - 65537) / row_bytes / 256 * 256; }
+
 LogpPlan plan_logp(int64_t T, int64_t d, int64_t V, int elem, int dw_elem, int64_t chunk_rows) {
   LogpPlan p{};
   p.direct = use_direct(T, d, V, elem);
@@ -65,7 +69,7 @@ LogpPlan plan_logp(int64_t T, int64_t d, int64_t V, int elem, int dw_elem, int64
     const int64_t dp = cdiv(d, 128) * 128;
     p.o_part = fw.take((size_t)std::min(p.ntiles, kd::kRingMaxSplits) * p.Cf * 16);
     p.o_hp_f = fw.take(panel_bytes(p.Cf, dp * elem));
-    p.C = chunk_of(T, V + 32 * kd::kDzTailPieces, elem, chunk_rows);
+    p.C = std::min(chunk_of(T, V + 32 * kd::kDzTailPieces, elem, chunk_rows), ring_rows(dp * elem));
     const int64_t ncb = cdiv(d, 256), units = cdiv(std::min(p.C, T), kd::kTileM) * ncb;
     p.grid_dh = (int)up(units * balanced_splits(units, cdiv(V, 128), std::max<int64_t>(1, cdiv(1024, units))), 256);
     p.o_dz = bw.take((size_t)p.C * (p.ldz + 32 * kd::kDzTailPieces) * elem);

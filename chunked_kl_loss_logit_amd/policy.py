@@ -7,6 +7,10 @@
 
     loss, rewards = preference_loss(logp, cu_seqlens, mask, ref_logp=ref)   # P pairs, autograd
 
+In a captured graph the _forward and _backward functions are the safe form:
+torch ends the process where a backward of its autograd is captured while an
+uncaptured graph of the same leaves is alive, whatever functions are in it.
+
 As for the distillation losses, all arithmetic runs in the HIP kernels of
 libkdloss.so; this module allocates outputs and workspaces with torch.
 """
@@ -82,11 +86,12 @@ def token_logp_shard_combine(recs, mask=None, tau=1.0, want_entropy=False):
 
 
 def token_logp_shard_backward(H, W_shard, v0, tokens, mask, tau, lse, grad_logp, entropy=None, grad_entropy=None,
-                              logits=None, chunk_rows=0, dw_dtype=torch.float32, workspace=None):
-    """This shard's dH partial [T,d] float32 (the caller sums them over the ranks) and its columns of dW."""
+                              logits=None, chunk_rows=0, dw_dtype=torch.float32, workspace=None, want=(True, True)):
+    """This shard's dH partial [T,d] float32 (the caller sums them over the ranks) and its columns of dW; want as for
+    token_logp_backward."""
     T, d, V = B._logp_in(H, W_shard, tokens, mask)
-    dH = _f32(H, T, d)
-    dW = torch.empty(d, V, dtype=dw_dtype, device=H.device)
+    dH = _f32(H, T, d) if want[0] else None
+    dW = torch.empty(d, V, dtype=dw_dtype, device=H.device) if want[1] else None
     if workspace is None:
         workspace = _workspace(B.kd_token_logp_workspace_size(T, d, V, H.dtype, dw_dtype, chunk_rows), H.device)
     B.kd_token_logp_bwd_shard(H, W_shard, v0, tokens, mask, tau, lse, entropy, logits, _grad(grad_logp),

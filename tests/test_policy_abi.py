@@ -200,6 +200,14 @@ def test_grad_calls_refuse(L):
     assert L.kd_grad_sumsq((vp * 1)(A), n, t, -1, vp(F), vp(F), 8, None) == 1
 
 
+@pytest.mark.parametrize("V", [2048, 2056])
+def test_huge_chunks_are_cut(L, V):
+    """A chunk's rows, in panels, keep within 32-bit offsets whatever chunk_rows asks for: 131072 rows of 16384 bf16
+    are 4 GB."""
+    s = [size(L, "kd_token_logp_workspace_size", 1 << 22, 16384, V, 1, 0, c) for c in (130560, 130816, 131072, 1 << 22)]
+    assert s[0][0] == 0 and s[0][1] < s[1][1] and s[1] == s[2] == s[3]
+
+
 def test_grad_clip_norm_refuses(L):
     n, t = (ctypes.c_int64 * 2)(8, 100000), (ctypes.c_int32 * 2)(0, 1)
     p, q = (vp * 2)(F, F + (1 << 20)), (vp * 2)(F, F + (1 << 21))

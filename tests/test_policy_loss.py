@@ -136,6 +136,17 @@ def test_extremes():
     near(stats[:1], torch.tensor([-1.2 + 3.0 - math.exp(-300.0)]), "total")
 
 
+@pytest.mark.parametrize("kl_kind", ["k1", "k2", "k3"])
+def test_unweighted_kl_leaves_the_gradient_alone(kl_kind):
+    """A reference that is only counted may be infinitely far off."""
+    logp, old, adv = torch.tensor([-1.0, -2.0]), torch.tensor([-1.25, -2.0]), torch.tensor([1.0, -1.0])
+    ref = torch.tensor([-math.inf, math.inf])
+    plain = kd.policy_loss_forward_backward(*[dev(x) for x in (logp, old, adv)])
+    stats, g, _ = kd.policy_loss_forward_backward(*[dev(x) for x in (logp, old, adv)], ref_logp=dev(ref), kl_kind=kl_kind)
+    assert torch.equal(g, plain[1]) and torch.equal(stats[:2], plain[0][:2])
+    assert not torch.isfinite(stats[2])
+
+
 def test_autograd_and_in_place_use():
     logp, old, ref, ent, adv, mask, cu = make(800, 6, 17)
     kw = dict(ref_logp=ref, cu_seqlens=cu, kl_weight=0.2, entropy_weight=0.05, reduction="sequence")

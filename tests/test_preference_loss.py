@@ -98,6 +98,15 @@ def test_far_margins():
     check(logp, cu, None, torch.ones(2), "far", beta=1.0)
 
 
+def test_infinite_margins():
+    """A rejected sequence of no probability costs nothing, a chosen one everything; the gradients are the limits."""
+    logp = torch.tensor([0.0, -math.inf, -math.inf, 0.0], device="cuda")
+    cu = torch.tensor([0, 1, 2, 3, 4], dtype=torch.int32, device="cuda")
+    loss, rewards, g = kd.preference_loss_forward_backward(logp, cu, None, torch.ones(2, device="cuda"), beta=0.5)
+    assert loss.tolist() == [0.0, math.inf] and rewards.tolist() == [0.0, -math.inf, -math.inf, 0.0]
+    assert g.tolist() == [0.0, -0.5, 0.0, 0.5]
+
+
 def test_autograd():
     logp, ref, mask, cu, grad = make(700, 5, 11)
     _, _, g = preference_reference(logp, cu, mask, ref_logp=ref, grad=grad, average=True)
