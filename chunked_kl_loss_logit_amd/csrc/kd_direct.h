@@ -130,7 +130,7 @@ struct ColsN {
 // acc += A . B over k in [kb, ke): ke is kb plus whole steps, or the operands'
 // end, behind which one of them is zero up to a whole step.
 template <class E, int U, class A, class B>
-__device__ inline void direct_contract(A& a, B& b, int kb, int ke, f32x16_t (&acc)[4][B::kFrags]) {
+__device__ __forceinline__ void direct_contract(A& a, B& b, int kb, int ke, f32x16_t (&acc)[4][B::kFrags]) {
   constexpr int KS = kDirStep<E, U>;
   auto mma = [&](int buf) {
 #pragma unroll
@@ -190,7 +190,7 @@ __device__ inline void k_range(int K, int unit, int i, int parts, int& kb, int& 
 // KS = 1: every wave hands out its own tile.  A: the a-side operand's type.
 // reg: LDS, 4 regions.
 template <class A, int R, int KS, class Row>
-__device__ inline void direct_rows(const f32x16_t (&acc)[4][R], float* reg, Row&& row) {
+__device__ __forceinline__ void direct_rows(const f32x16_t (&acc)[4][R], float* reg, Row&& row) {
   const int w = wave_id(), lane = threadIdx.x & 63, h = lane >> 5;
   float* mine = reg + w * kDirRegion + (lane & 31) * kDirLd;
 #pragma unroll

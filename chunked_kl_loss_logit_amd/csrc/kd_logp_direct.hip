@@ -25,6 +25,16 @@ constexpr int kDirThreads = 256;
 __device__ inline long chunk_rows_of(const RowSet& rs) {
   return rs.rows ? min((long)rs.C, (long)*rs.count - (long)rs.c0) : min((long)rs.C, (long)(rs.T - rs.c0));
 }
+// The valid rows' blocks of `rows` rows: how many, and this workgroup's place
+// among those blocks times `per`, or -1.  Workgroups without work are the last
+// of the grid (rows may be masked), so that those with work go round the chip
+// evenly: with one row block of four in use by its place in the grid, 33 rows
+// of 2048 x 32000 float32 took 250 us, and 75 when it was one of one.
+__device__ inline int row_blocks(long M, int rows, int per, int& nrb) {
+  nrb = M > 0 ? (int)((M + rows - 1) / rows) : 0;
+  const int total = nrb * per;
+  return (int)blockIdx.x < total ? xcd_remap(blockIdx.x, total) : -1;
+}
 __device__ inline long row_at(const RowSet& rs, long i) { return rs.rows ? rs.rows[rs.c0 + i] : rs.c0 + i; }
 
 // over the eight lanes of a row
@@ -53,7 +63,7 @@ __device__ inline void zero(f32x16_t (&acc)[4][R]) {
 // The product of W's columns [n0, n0 + 128) and the chunk's rows [r0, r0 + 32 R),
 // the contraction split over the four waves.
 template <class E, int R>
-__device__ inline void logits_tile(const LogpDirectArgs& a, long M, long r0, int n0, f32x16_t (&acc)[4][R]) {
+__device__ __forceinline__ void logits_tile(const LogpDirectArgs& a, long M, long r0, int n0, f32x16_t (&acc)[4][R]) {
   constexpr int U = 2;
   const int lane = threadIdx.x & 63, m = lane & 31;
   ColsN<E, U> wl;
@@ -71,15 +81,24 @@ __device__ inline void logits_tile(const LogpDirectArgs& a, long M, long r0, int
 
 }  // namespace
 
+// A row block of up to 32 R rows: f with as many block columns (1, 2 or 4) as
+// its rows fill, so that a short last block costs what its rows do (700 rows
+// of a 1024 x 32000 float32 head: fp32 forward 525 -> 468 us).
+template <int R, class F>
+__device__ __forceinline__ void by_left(long left, F&& f) {
+  if constexpr (R > 1) {
+    if (left <= 16 * R) {
+      by_left<R / 2>(left, f);
+      return;
+    }
+  }
+  f(std::integral_constant<int, R>());
+}
+
 // ------------------------------------------------------------------ forward
 template <class E, int R, bool kEnt>
-__global__ __launch_bounds__(kDirThreads, R == 4 ? 1 : 2) void logp_direct_fwd_kernel(LogpDirectArgs a, int nrb) {
-  __shared__ __attribute__((aligned(16))) float reg[4 * kDirRegion];
-  const long M = chunk_rows_of(a.rs);
-  const int id = xcd_remap(blockIdx.x, gridDim.x);  // row blocks of one W panel run together on one XCD
-  const long r0 = (long)(id % nrb) * 32 * R;
-  const int tile = id / nrb, n0 = tile * kDirA;
-  if (r0 >= M) return;
+__device__ __forceinline__ void fwd_tile(const LogpDirectArgs& a, long M, long r0, int tile, float* reg) {
+  const int n0 = tile * kDirA;
   const int V = (int)a.V, lane = threadIdx.x & 63;
   const int mine = 8 * wave_id() + (lane >> 3);  // the row of each block this lane will get
   int label[R];  // relative to the tile
@@ -124,6 +143,17 @@ __global__ __launch_bounds__(kDirThreads, R == 4 ? 1 : 2) void logp_direct_fwd_k
     x = row_sum(x);
     if (q == 0 && r0 + i < M) part[i] = make_float4(mx, l, e, x);
   });
+}
+
+template <class E, int R, bool kEnt>
+__global__ __launch_bounds__(kDirThreads, R == 4 ? 1 : 2) void logp_direct_fwd_kernel(LogpDirectArgs a) {
+  __shared__ __attribute__((aligned(16))) float reg[4 * kDirRegion];
+  const long M = chunk_rows_of(a.rs);
+  int nrb;
+  const int id = row_blocks(M, 32 * R, (int)((a.V + kDirA - 1) / kDirA), nrb);
+  if (id < 0) return;
+  const long r0 = (long)(id % nrb) * 32 * R;  // row blocks of one W panel run together on one XCD
+  by_left<R>(M - r0, [&](auto r) { fwd_tile<E, decltype(r)::value, kEnt>(a, M, r0, id / nrb, reg); });
 }
 
 // ------------------------------------------------------------------ dZ
@@ -173,13 +203,7 @@ __device__ inline void store4(char* p, float4 x) {
 }  // namespace
 
 template <class E, int R, bool kEnt>
-__global__ __launch_bounds__(kDirThreads, R == 1 ? 2 : 1) void logp_direct_dz_kernel(LogpDirectArgs a, int nrb) {
-  __shared__ __attribute__((aligned(16))) float reg[4 * kDirRegion];
-  const long M = chunk_rows_of(a.rs);
-  const int id = xcd_remap(blockIdx.x, gridDim.x);
-  const long r0 = (long)(id % nrb) * 32 * R;
-  const int n0 = id / nrb * kDirA;
-  if (r0 >= (M + 127) / 128 * 128) return;
+__device__ __forceinline__ void dz_tile(const LogpDirectArgs& a, long M, long r0, int n0, float* reg) {
   const int V = (int)a.V, lane = threadIdx.x & 63, mine = 8 * wave_id() + (lane >> 3);
   DzConst k[R];
 #pragma unroll
@@ -188,7 +212,7 @@ __global__ __launch_bounds__(kDirThreads, R == 1 ? 2 : 1) void logp_direct_dz_ke
     k[b] = dz_const(a, i < M, i < M ? row_at(a.rs, i) : 0);
   }
   f32x16_t acc[4][R];
-  logits_tile<E, R>(a, M, min(r0, M - 1), n0, acc);
+  logits_tile<E, R>(a, M, r0, n0, acc);
   direct_rows<ColsN<E, 2>, R, 4>(acc, reg, [&](int b, int m, int q, const float4 (&z)[4]) {
     const long i = r0 + 32 * b + m;
 #pragma unroll
@@ -200,6 +224,30 @@ __global__ __launch_bounds__(kDirThreads, R == 1 ? 2 : 1) void logp_direct_dz_ke
       store4<E>(a.dz + (i * a.ldz + c) * E::kElem, o);
     }
   });
+}
+
+template <class E, int R, bool kEnt>
+__global__ __launch_bounds__(kDirThreads, R == 1 ? 2 : 1) void logp_direct_dz_kernel(LogpDirectArgs a) {
+  __shared__ __attribute__((aligned(16))) float reg[4 * kDirRegion];
+  const long M = chunk_rows_of(a.rs);
+  int nrb;
+  const int id = row_blocks(M, 32 * R, (int)((a.V + kDirA - 1) / kDirA), nrb);
+  if (id < 0) return;
+  const int rb = id % nrb, n0 = id / nrb * kDirA;
+  const long r0 = (long)rb * 32 * R;
+  long done = r0;
+  by_left<R>(M - r0, [&](auto r) {
+    dz_tile<E, decltype(r)::value, kEnt>(a, M, r0, n0, reg);
+    done += 32 * decltype(r)::value;
+  });
+  if (rb < nrb - 1) return;
+  // zeros to the next multiple of 128 rows
+  constexpr int kChunks = kDirA / E::kEpc;
+  const int n = (int)((M + 127) / 128 * 128 - done) * kChunks;
+  for (int q = threadIdx.x; q < n; q += kDirThreads) {
+    const long i = done + q / kChunks, c = n0 + q % kChunks * E::kEpc;
+    if (c < a.V) *reinterpret_cast<u32x4_t*>(a.dz + (i * a.ldz + c) * E::kElem) = zero4();
+  }
 }
 
 // From stored logits: a block takes one row and up to kFzCols columns, eight per thread.
@@ -225,16 +273,17 @@ __global__ __launch_bounds__(256) void logp_direct_dz_from_z_kernel(LogpDirectAr
 // Tile: 128 of d x 32 R rows, vocabulary range s of S over the four waves.
 // S = 1: dH itself; else the range's float32 part [S][C][d].
 template <class E, int R, class O>
-__global__ __launch_bounds__(kDirThreads, 1) void logp_direct_dh_kernel(LogpDirectArgs a, int nrb, int nda, int S,
+__global__ __launch_bounds__(kDirThreads, 1) void logp_direct_dh_kernel(LogpDirectArgs a, int nda, int S,
                                                                         float* part, char* dH) {
   constexpr int U = 4;
   __shared__ __attribute__((aligned(16))) float reg[4 * kDirRegion];
   const long M = chunk_rows_of(a.rs);
-  int id = xcd_remap(blockIdx.x, gridDim.x);
+  int nrb;
+  int id = row_blocks(M, 32 * R, nda * S, nrb);
+  if (id < 0) return;
   const long r0 = (long)(id % nrb) * 32 * R;
   id /= nrb;
   const int d0 = (id % nda) * kDirA, s = id / nda;
-  if (r0 >= M) return;
   const int lane = threadIdx.x & 63, m = lane & 31, d = (int)a.d;
   RowsK<E, 4, U> wl;
   RowsK<E, R, U> zl;
@@ -383,21 +432,19 @@ int cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
 template <class E, int R>
 void fwd(const LogpDirectArgs& a, bool entropy, hipStream_t st) {
-  const int nrb = cdiv(rows_upto(a.rs), 32 * R);
-  const dim3 grid((unsigned)(nrb * cdiv(a.V, kDirA)));
+  const dim3 grid((unsigned)(cdiv(rows_upto(a.rs), 32 * R) * cdiv(a.V, kDirA)));
   if (entropy)
-    hipLaunchKernelGGL((logp_direct_fwd_kernel<E, R, true>), grid, dim3(kDirThreads), 0, st, a, nrb);
+    hipLaunchKernelGGL((logp_direct_fwd_kernel<E, R, true>), grid, dim3(kDirThreads), 0, st, a);
   else
-    hipLaunchKernelGGL((logp_direct_fwd_kernel<E, R, false>), grid, dim3(kDirThreads), 0, st, a, nrb);
+    hipLaunchKernelGGL((logp_direct_fwd_kernel<E, R, false>), grid, dim3(kDirThreads), 0, st, a);
 }
 template <class E, int R>
 void dz(const LogpDirectArgs& a, hipStream_t st) {
-  const int nrb = cdiv(cdiv(rows_upto(a.rs), 128) * 128, 32 * R);  // to the zero rows' end
-  const dim3 grid((unsigned)(nrb * cdiv(a.V, kDirA)));
+  const dim3 grid((unsigned)(cdiv(rows_upto(a.rs), 32 * R) * cdiv(a.V, kDirA)));
   if (a.ge)
-    hipLaunchKernelGGL((logp_direct_dz_kernel<E, R, true>), grid, dim3(kDirThreads), 0, st, a, nrb);
+    hipLaunchKernelGGL((logp_direct_dz_kernel<E, R, true>), grid, dim3(kDirThreads), 0, st, a);
   else
-    hipLaunchKernelGGL((logp_direct_dz_kernel<E, R, false>), grid, dim3(kDirThreads), 0, st, a, nrb);
+    hipLaunchKernelGGL((logp_direct_dz_kernel<E, R, false>), grid, dim3(kDirThreads), 0, st, a);
 }
 // Block columns of rows per tile: 1, 2 or 4, no more than hold the rows, and
 // fewer where the tiles would not go round the CUs (at 4 a tile's operands are
@@ -448,14 +495,13 @@ hipError_t launch_logp_direct_dh(int elem, const LogpDirectArgs& a, int S, float
   char* out = static_cast<char*>(dH);
   auto go = [&](auto r) {
     constexpr int R = decltype(r)::value;
-    const int nrb = cdiv(n, 32 * R);
-    const dim3 grid((unsigned)(nrb * nda * S)), block(kDirThreads);
+    const dim3 grid((unsigned)(cdiv(n, 32 * R) * nda * S)), block(kDirThreads);
     if (elem == 4)
-      hipLaunchKernelGGL((logp_direct_dh_kernel<F32, R, F32>), grid, block, 0, st, a, nrb, nda, S, part, out);
+      hipLaunchKernelGGL((logp_direct_dh_kernel<F32, R, F32>), grid, block, 0, st, a, nda, S, part, out);
     else if (dh_elem == 4)
-      hipLaunchKernelGGL((logp_direct_dh_kernel<Bf16, R, F32>), grid, block, 0, st, a, nrb, nda, S, part, out);
+      hipLaunchKernelGGL((logp_direct_dh_kernel<Bf16, R, F32>), grid, block, 0, st, a, nda, S, part, out);
     else
-      hipLaunchKernelGGL((logp_direct_dh_kernel<Bf16, R, Bf16>), grid, block, 0, st, a, nrb, nda, S, part, out);
+      hipLaunchKernelGGL((logp_direct_dh_kernel<Bf16, R, Bf16>), grid, block, 0, st, a, nda, S, part, out);
   };
   if (n <= 32) go(std::integral_constant<int, 1>());
   else go(std::integral_constant<int, 2>());
