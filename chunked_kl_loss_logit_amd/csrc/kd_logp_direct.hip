@@ -370,17 +370,25 @@ __global__ __launch_bounds__(kDirThreads, 1) void logp_direct_dw_kernel(LogpDire
 }
 
 // ------------------------------------------------------------------ rows of the mask
-// A block of 256 threads takes 64 rows of the mask: how many valid ones come
-// before them (counted anew by every block: at most T bytes), where each of
-// its own goes, and the copying.
+// A block of 256 threads takes kPrepRows rows of the mask: how many valid ones
+// come before them (counted anew by every block: at most T bytes), where each
+// of its own goes, and the copying, a wave to a row: one launch where counting,
+// packing and zeroing apart are three.
+constexpr int kPrepRows = 16;
+
+__device__ inline void copy_row(char* to, const char* from, long bytes) {
+  for (long q = (threadIdx.x & 63) * 16; q < bytes; q += 1024)
+    *reinterpret_cast<u32x4_t*>(to + q) = from ? ld16(from + q) : zero4();
+}
+
 __global__ __launch_bounds__(256) void logp_prep_kernel(const uint8_t* mask, long T, int32_t* rows, int32_t* count,
-                                                        const char* H, long rowb, long c0, long C, char* Hc, char* dH,
+                                                        const char* H, long rowb, long C, char* Hc, char* dH,
                                                         long dhb) {
   __shared__ int red[4];
-  __shared__ int pos[64];  // compacted position, or -1
-  const long t0 = (long)blockIdx.x * 64;
+  __shared__ int pos[kPrepRows];  // compacted position, or -1
+  const long t0 = (long)blockIdx.x * kPrepRows;
   int n = 0;
-  for (long t = (long)threadIdx.x * 8; t < t0; t += 2048) {  // t0 is a multiple of 64: whole eights
+  for (long t = (long)threadIdx.x * 8; t < t0; t += 2048) {  // t0 is a multiple of 16: whole eights
     uint2 v;
     __builtin_memcpy(&v, mask + t, 8);
 #pragma unroll
@@ -393,34 +401,44 @@ __global__ __launch_bounds__(256) void logp_prep_kernel(const uint8_t* mask, lon
   const int before = red[0] + red[1] + red[2] + red[3];
   if (threadIdx.x < 64) {
     const long t = t0 + threadIdx.x;
-    const bool on = t < T && mask[t] != 0;
+    const bool on = threadIdx.x < kPrepRows && t < T && mask[t] != 0;
     const unsigned long long b = __ballot(on);
     const int at = before + __popcll(b & ((1ull << threadIdx.x) - 1));
-    pos[threadIdx.x] = on ? at : -1;
+    if (threadIdx.x < kPrepRows) pos[threadIdx.x] = on ? at : -1;
     if (on) rows[at] = (int32_t)t;
-    if (t0 + 64 >= T && threadIdx.x == 0) *count = before + __popcll(b);
+    if (t0 + kPrepRows >= T && threadIdx.x == 0) *count = before + __popcll(b);
   }
   __syncthreads();
-  for (int r = 0; r < 64; ++r) {
+  for (int r = threadIdx.x >> 6; r < kPrepRows; r += 4) {
     const long t = t0 + r;
     if (t >= T) break;
     const int at = pos[r];
     if (at < 0) {
-      if (dH)
-        for (long q = (long)threadIdx.x * 16; q < dhb; q += 4096) *reinterpret_cast<u32x4_t*>(dH + t * dhb + q) = zero4();
-    } else if (Hc && at >= c0 && at < c0 + C) {
-      for (long q = (long)threadIdx.x * 16; q < rowb; q += 4096)
-        *reinterpret_cast<u32x4_t*>(Hc + (at - c0) * rowb + q) = ld16(H + t * rowb + q);
+      if (dH) copy_row(dH + t * dhb, nullptr, dhb);
+    } else if (Hc && at < C) {
+      copy_row(Hc + at * rowb, H + t * rowb, rowb);
     }
   }
 }
 
+// The chunk's rows of H one after the other, a wave to a row
+__global__ __launch_bounds__(256) void logp_pack_kernel(RowSet rs, const char* H, long rowb, char* Hc) {
+  const long i = (long)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (i < chunk_rows_of(rs)) copy_row(Hc + i * rowb, H + row_at(rs, i) * rowb, rowb);
+}
+
 hipError_t launch_logp_prep(const uint8_t* mask, int64_t T, int32_t* rows, int32_t* count, const void* H,
-                            int64_t row_bytes, int64_t c0, int64_t C, void* Hc, void* dH, int64_t dh_row_bytes,
-                            hipStream_t st) {
-  hipLaunchKernelGGL(logp_prep_kernel, dim3((unsigned)((T + 63) / 64)), dim3(256), 0, st, mask, (long)T, rows, count,
-                     static_cast<const char*>(H), (long)row_bytes, (long)c0, (long)C, static_cast<char*>(Hc),
-                     static_cast<char*>(dH), (long)dh_row_bytes);
+                            int64_t row_bytes, int64_t C, void* Hc, void* dH, int64_t dh_row_bytes, hipStream_t st) {
+  hipLaunchKernelGGL(logp_prep_kernel, dim3((unsigned)((T + kPrepRows - 1) / kPrepRows)), dim3(256), 0, st, mask,
+                     (long)T, rows, count, static_cast<const char*>(H), (long)row_bytes, (long)C,
+                     static_cast<char*>(Hc), static_cast<char*>(dH), (long)dh_row_bytes);
+  return hipGetLastError();
+}
+
+hipError_t launch_logp_pack(const RowSet& rs, const void* H, int64_t row_bytes, void* Hc, hipStream_t st) {
+  const int64_t n = rs.C < rs.T - rs.c0 ? rs.C : rs.T - rs.c0;
+  hipLaunchKernelGGL(logp_pack_kernel, dim3((unsigned)((n + 3) / 4)), dim3(256), 0, st, rs,
+                     static_cast<const char*>(H), (long)row_bytes, static_cast<char*>(Hc));
   return hipGetLastError();
 }
 

@@ -109,11 +109,12 @@ hipError_t launch_logp_dz(const LogpDzArgs& a, hipStream_t st);
 hipError_t launch_logp_dz_from_z(const LogpDzArgs& a, hipStream_t st);
 
 // ---------------------------------------------------------------- the same without LDS-staged tiles
-// rows and *count from the mask (not null); the chunk's rows of H packed into
-// Hc [C][row_bytes] (nullable); masked rows of dH (nullable) zeroed.
+// rows and *count from the mask (not null); the first C valid rows of H packed
+// into Hc [C][row_bytes] (nullable); masked rows of dH (nullable) zeroed.
 hipError_t launch_logp_prep(const uint8_t* mask, int64_t T, int32_t* rows, int32_t* count, const void* H,
-                            int64_t row_bytes, int64_t c0, int64_t C, void* Hc, void* dH, int64_t dh_row_bytes,
-                            hipStream_t st);
+                            int64_t row_bytes, int64_t C, void* Hc, void* dH, int64_t dh_row_bytes, hipStream_t st);
+// The chunk's rows of H packed into Hc.
+hipError_t launch_logp_pack(const RowSet& rs, const void* H, int64_t row_bytes, void* Hc, hipStream_t st);
 constexpr int kDirectCols = 128;  // vocabulary columns per tile
 struct LogpDirectArgs {
   RowSet rs;

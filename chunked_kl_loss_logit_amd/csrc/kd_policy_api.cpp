@@ -129,6 +129,25 @@ kd_status head_panels(const void* H, int64_t d, const kd::Compact& c, int64_t c0
   return KD_OK;
 }
 
+// The valid rows, the masked rows of dH (nullable) zeroed, and up to kPrepMax
+// rows the first C of H's packed (Hc nullable): one launch, whose blocks each
+// count the mask before them (T^2 / 16 bytes in all); beyond, one block counts
+// (forward and backward of 1024 x 256 float32, us, one launch / apart: 777 rows
+// 27 + 92 / 28 + 95, 16384 rows 107 + 1026 / 117 + 1049, 65536 rows 347 + 4050 /
+// 415 + 4130).
+constexpr int64_t kPrepMax = 65536;
+kd_status direct_rows(const uint8_t* mask, int64_t T, const kd::Compact& c, const void* H, int64_t row_bytes,
+                      int64_t C, char* Hc, void* dH, int64_t dh_row_bytes, hipStream_t st) {
+  if (T <= kPrepMax) {
+    KD_LAUNCH("logp_prep", st,
+              kd::launch_logp_prep(mask, T, c.rows, c.count, H, row_bytes, C, Hc, dH, dh_row_bytes, st));
+    return KD_OK;
+  }
+  KD_LAUNCH("compact", st, kd::launch_compact(mask, T, c, st));
+  if (dH) KD_LAUNCH("zero_masked_rows", st, kd::launch_zero_masked_rows(mask, T, dh_row_bytes, dH, st));
+  return KD_OK;
+}
+
 kd_status logp_fwd(const void* H, const void* W, const int32_t* tokens, const uint8_t* mask, float tau, int64_t T,
                    int64_t d, int64_t V, int64_t v0, kd_dtype dt, const kd::LogpOut& out, bool entropy, float* logits,
                    void* workspace, size_t workspace_bytes, void* stream) {
@@ -142,8 +161,7 @@ kd_status logp_fwd(const void* H, const void* W, const int32_t* tokens, const ui
   kd::RowSet rs{c.rows, c.count, 0, p.Cf, T};
   if (p.direct) {
     if (mask)
-      KD_LAUNCH("logp_prep", st,
-                kd::launch_logp_prep(mask, T, c.rows, c.count, H, d * elem, 0, T, nullptr, nullptr, 0, st));
+      KD_TRY(direct_rows(mask, T, c, H, d * elem, 0, nullptr, nullptr, 0, st));
     else
       rs.rows = rs.count = nullptr;
     kd::LogpDirectArgs a{};
@@ -248,10 +266,11 @@ kd_status logp_bwd(const void* H, const void* W, const int32_t* tokens, const ui
       a.rs = kd::RowSet{mask ? c.rows : nullptr, c.count, c0, p.C, T};
       const char* hc = a.H + c0 * d * elem;
       if (mask) {
-        char* packed = at<char>(workspace, p.o_hc);
-        KD_LAUNCH("logp_prep", st,
-                  kd::launch_logp_prep(mask, T, c.rows, c.count, H, d * elem, c0, p.C, dW ? packed : nullptr,
-                                       c0 == 0 ? dH : nullptr, d * dh_elem, st));
+        char* packed = dW ? at<char>(workspace, p.o_hc) : nullptr;
+        if (c0 == 0)
+          KD_TRY(direct_rows(mask, T, c, H, d * elem, p.C, packed, dH, d * dh_elem, st));
+        if (packed && (c0 > 0 || T > kPrepMax))
+          KD_LAUNCH("logp_pack", st, kd::launch_logp_pack(a.rs, H, d * elem, packed, st));
         hc = packed;
       }
       if (logits) {

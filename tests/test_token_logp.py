@@ -331,3 +331,18 @@ def test_one_gradient_alone(T, V, dtype):
     h = a[0].clone().requires_grad_(True)
     kd.token_logp(h, a[1], a[2], a[3]).backward(g)
     assert a[1].grad is None and torch.equal(h.grad, kd.token_logp_backward(*a, 1.0, lse, g, dw_dtype=dtype)[0])
+
+
+@pytest.mark.parametrize("T", [65536, 65537, 70001])
+def test_many_short_rows(T):
+    """Many chunks of rows, where the mask is counted in another way than for few."""
+    H, W, tokens, mask = make_head(T, 16, 64, f32, 67, masked=0.3)
+    mask[:5000] = 0
+    g = torch.randn(T, generator=torch.Generator().manual_seed(68))
+    want, bound = logp_reference(H, W, tokens, mask, 1.0, g)
+    a = [dev(x) for x in (H, W, tokens, mask)]
+    logp, lse, _, _ = kd.token_logp_forward(*a)
+    dH, dW = kd.token_logp_backward(*a, 1.0, lse, dev(g))
+    for name, got in (("logp", logp), ("lse", lse), ("dH", dH), ("dW", dW)):
+        within(got, want[name], bound[name], name)
+    assert (dH[a[3] == 0] == 0).all() and (logp[a[3] == 0] == 0).all()
