@@ -192,12 +192,27 @@ __device__ inline float4 dz_four(float4 z, const DzConst& k, float c2, long c) {
                      dz_of<kEnt>(z.w, c2, k.L2, k.A, k.B) + (k.label == c + 3 ? k.ga : 0.f));
 }
 
+// What rounding to bf16 leaves of x (0 of what is not finite).
+__device__ inline float rest(float x) {
+  const float r = x - __uint_as_float(Bf16::pack2(x, 0.f) << 16);
+  return fabsf(r) < INFINITY ? r : 0.f;
+}
+
 template <class E>
 __device__ inline void store4(char* p, float4 x) {
   if constexpr (E::kElem == 2)
     *reinterpret_cast<uint2*>(p) = make_uint2(Bf16::pack2(x.x, x.y), Bf16::pack2(x.z, x.w));
   else
     *reinterpret_cast<float4*>(p) = x;
+}
+
+// dZ, and where the chunk has them (LogpDirectArgs::lo) the rests of its rounding
+template <class E>
+__device__ inline void put_dz(const LogpDirectArgs& a, long i, long c, float4 x) {
+  char* p = a.dz + (i * a.ldz + c) * E::kElem;
+  store4<E>(p, x);
+  if constexpr (E::kElem == 2)
+    if (a.lo) store4<E>(p + a.lo, make_float4(rest(x.x), rest(x.y), rest(x.z), rest(x.w)));
 }
 
 }  // namespace
@@ -221,7 +236,7 @@ __device__ __forceinline__ void dz_tile(const LogpDirectArgs& a, long M, long r0
       if (c >= V) break;
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
       if (i < M) o = dz_four<kEnt>(z[j], k[b], a.c2, c);
-      store4<E>(a.dz + (i * a.ldz + c) * E::kElem, o);
+      put_dz<E>(a, i, c, o);
     }
   });
 }
@@ -233,21 +248,8 @@ __global__ __launch_bounds__(kDirThreads, R == 1 ? 2 : 1) void logp_direct_dz_ke
   int nrb;
   const int id = row_blocks(M, 32 * R, (int)((a.V + kDirA - 1) / kDirA), nrb);
   if (id < 0) return;
-  const int rb = id % nrb, n0 = id / nrb * kDirA;
-  const long r0 = (long)rb * 32 * R;
-  long done = r0;
-  by_left<R>(M - r0, [&](auto r) {
-    dz_tile<E, decltype(r)::value, kEnt>(a, M, r0, n0, reg);
-    done += 32 * decltype(r)::value;
-  });
-  if (rb < nrb - 1) return;
-  // zeros to the next multiple of 128 rows
-  constexpr int kChunks = kDirA / E::kEpc;
-  const int n = (int)((M + 127) / 128 * 128 - done) * kChunks;
-  for (int q = threadIdx.x; q < n; q += kDirThreads) {
-    const long i = done + q / kChunks, c = n0 + q % kChunks * E::kEpc;
-    if (c < a.V) *reinterpret_cast<u32x4_t*>(a.dz + (i * a.ldz + c) * E::kElem) = zero4();
-  }
+  const long r0 = (long)(id % nrb) * 32 * R;
+  by_left<R>(M - r0, [&](auto r) { dz_tile<E, decltype(r)::value, kEnt>(a, M, r0, id / nrb * kDirA, reg); });
 }
 
 // From stored logits: a block takes one row and up to kFzCols columns, eight per thread.
@@ -256,7 +258,7 @@ template <class E, bool kEnt>
 __global__ __launch_bounds__(256) void logp_direct_dz_from_z_kernel(LogpDirectArgs a) {
   const long M = chunk_rows_of(a.rs);
   const long per = (a.V + kFzCols - 1) / kFzCols, i = blockIdx.x / per;
-  if (i >= (M + 127) / 128 * 128) return;
+  if (i >= (M + 31) / 32 * 32) return;
   const DzConst k = dz_const(a, i < M, i < M ? row_at(a.rs, i) : 0);
   const long c0 = (long)(blockIdx.x - i * per) * kFzCols + threadIdx.x * 4;
 #pragma unroll
@@ -265,23 +267,25 @@ __global__ __launch_bounds__(256) void logp_direct_dz_from_z_kernel(LogpDirectAr
     if (c >= a.V) break;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     if (i < M) o = dz_four<kEnt>(*reinterpret_cast<const float4*>(a.z + i * a.ldz + c), k, a.c2, c);
-    store4<E>(a.dz + (i * a.ldz + c) * E::kElem, o);
+    put_dz<E>(a, i, c, o);
   }
 }
 
 // ------------------------------------------------------------------ dH
 // Tile: 128 of d x 32 R rows, vocabulary range s of S over the four waves.
-// S = 1: dH itself; else the range's float32 part [S][C][d].
-template <class E, int R, class O>
+// S = 1: dH itself; else the range's float32 part [S][C][d].  kTwo: 32 rows,
+// the second block column their rests, added at the end.
+template <class E, int R, class O, bool kTwo = false>
 __global__ __launch_bounds__(kDirThreads, 1) void logp_direct_dh_kernel(LogpDirectArgs a, int nda, int S,
                                                                         float* part, char* dH) {
   constexpr int U = 4;
   __shared__ __attribute__((aligned(16))) float reg[4 * kDirRegion];
   const long M = chunk_rows_of(a.rs);
   int nrb;
-  int id = row_blocks(M, 32 * R, nda * S, nrb);
+  constexpr int kRows = kTwo ? 32 : 32 * R;
+  int id = row_blocks(M, kRows, nda * S, nrb);
   if (id < 0) return;
-  const long r0 = (long)(id % nrb) * 32 * R;
+  const long r0 = (long)(id % nrb) * kRows;
   id /= nrb;
   const int d0 = (id % nda) * kDirA, s = id / nda;
   const int lane = threadIdx.x & 63, m = lane & 31, d = (int)a.d;
@@ -291,14 +295,26 @@ __global__ __launch_bounds__(kDirThreads, 1) void logp_direct_dh_kernel(LogpDire
 #pragma unroll
   for (int f = 0; f < 4; ++f) wl.row(f, a.W + (long)min(d0 + 32 * f + m, d - 1) * a.V * E::kElem);
 #pragma unroll
-  for (int b = 0; b < R; ++b) zl.row(b, a.dz + min(r0 + 32 * b + m, M - 1) * a.ldz * E::kElem);
+  for (int b = 0; b < R; ++b)
+    zl.row(b, a.dz + min(r0 + (kTwo ? m : 32 * b + m), M - 1) * a.ldz * E::kElem + (kTwo && b ? a.lo : 0));
   int kb, ke;
   k_range((int)a.V, kDirStep<E, U>, 4 * s + wave_id(), 4 * S, kb, ke);
   f32x16_t acc[4][R];
   zero(acc);
   direct_contract<E, U>(wl, zl, kb, ke, acc);
-  direct_rows<RowsK<E, 4, U>, R, 4>(acc, reg, [&](int b, int mm, int q, const float4 (&x)[4]) {
-    const long i = r0 + 32 * b + mm;
+  float4 first[4];
+  direct_rows<RowsK<E, 4, U>, R, 4>(acc, reg, [&](int b, int mm, int q, float4 (&x)[4]) {
+    const long i = r0 + (kTwo ? mm : 32 * b + mm);
+    if constexpr (kTwo) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (b == 0)
+          first[j] = x[j];
+        else
+          x[j] = make_float4(first[j].x + x[j].x, first[j].y + x[j].y, first[j].z + x[j].z, first[j].w + x[j].w);
+      }
+      if (b == 0) return;
+    }
     if (i >= M) return;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -344,13 +360,17 @@ __global__ __launch_bounds__(kDirThreads, 1) void logp_direct_dw_kernel(LogpDire
   const int d0 = ((id % nda) * (KS == 1 ? 4 : 1) + (KS == 1 ? w : 0)) * kDirA, n0 = id / nda * kDirA;
   const int d = (int)a.d, V = (int)a.V;
   ColsN<E, U> zl, hl;
-  zl.init(a.dz, a.ldz * E::kElem, (int)((M + 127) / 128 * 128), min(n0 + 4 * m, V - 4));  // zero rows behind the last
+  zl.init(a.dz, a.ldz * E::kElem, (int)((M + 31) / 32 * 32), min(n0 + 4 * m, V - 4));  // zero rows behind the last
   hl.init(Hc, (long)d * E::kElem, (int)M, min(d0 + 4 * m, d - 4));
   int kb, ke;
   k_range((int)M, kDirStep<E, U>, KS == 1 ? 0 : w, KS, kb, ke);
   f32x16_t acc[4][4];
   zero(acc);
-  direct_contract<E, U>(zl, hl, kb, ke, acc);
+  for (int plane = a.lo ? 2 : 1;;) {
+    direct_contract<E, U>(zl, hl, kb, ke, acc);
+    if (--plane == 0) break;
+    zl.base += a.lo;
+  }
   direct_rows<ColsN<E, U>, 4, KS>(acc, reg, [&](int b, int mm, int q, const float4 (&x)[4]) {
     const int i = d0 + ColsN<E, U>::index(b, mm);
     if (i >= d) return;
@@ -494,7 +514,7 @@ hipError_t launch_logp_direct_dz(int elem, const LogpDirectArgs& a, hipStream_t 
 }
 
 hipError_t launch_logp_direct_dz_from_z(int elem, const LogpDirectArgs& a, hipStream_t st) {
-  const dim3 grid((unsigned)((int64_t)cdiv(a.V, kFzCols) * cdiv(rows_upto(a.rs), 128) * 128));
+  const dim3 grid((unsigned)((int64_t)cdiv(a.V, kFzCols) * cdiv(rows_upto(a.rs), 32) * 32));
   if (elem == 2 && a.ge)
     hipLaunchKernelGGL((logp_direct_dz_from_z_kernel<Bf16, true>), grid, dim3(256), 0, st, a);
   else if (elem == 2)
@@ -521,8 +541,17 @@ hipError_t launch_logp_direct_dh(int elem, const LogpDirectArgs& a, int S, float
     else
       hipLaunchKernelGGL((logp_direct_dh_kernel<Bf16, R, Bf16>), grid, block, 0, st, a, nda, S, part, out);
   };
-  if (n <= 32) go(std::integral_constant<int, 1>());
-  else go(std::integral_constant<int, 2>());
+  if (a.lo) {
+    const dim3 grid((unsigned)(cdiv(n, 32) * nda * S)), block(kDirThreads);
+    if (dh_elem == 4)
+      hipLaunchKernelGGL((logp_direct_dh_kernel<Bf16, 2, F32, true>), grid, block, 0, st, a, nda, S, part, out);
+    else
+      hipLaunchKernelGGL((logp_direct_dh_kernel<Bf16, 2, Bf16, true>), grid, block, 0, st, a, nda, S, part, out);
+  } else if (n <= 32) {
+    go(std::integral_constant<int, 1>());
+  } else {
+    go(std::integral_constant<int, 2>());
+  }
   if (S > 1) {
     const dim3 grid((unsigned)cdiv(n * (a.d / 4), 256));
     if (dh_elem == 2)

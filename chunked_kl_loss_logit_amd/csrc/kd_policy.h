@@ -127,7 +127,8 @@ struct LogpDirectArgs {
   float* part;            // forward: records [tiles][C][4] as LogpFwdArgs::part
   float* z;               // forward: nullable, logits out [C][ldz]; dz from z: the logits
   const float *lse, *ent, *g, *ge;
-  char* dz;               // backward: [roundup(C, 128)][ldz], row-major; zero rows up to a multiple of 128
+  char* dz;               // backward: [C][ldz], row-major; zero rows up to a multiple of 32
+  int64_t lo;             // nonzero (chunks of up to 32 rows, bf16): dz's bytes to a second plane, what rounding left
 };
 hipError_t launch_logp_direct_fwd(int elem, const LogpDirectArgs& a, bool entropy, hipStream_t st);
 hipError_t launch_logp_direct_dz(int elem, const LogpDirectArgs& a, hipStream_t st);

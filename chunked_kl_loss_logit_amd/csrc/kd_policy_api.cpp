@@ -60,7 +60,7 @@ LogpPlan plan_logp(int64_t T, int64_t d, int64_t V, int elem, int dw_elem, int64
     const int64_t n = std::min(p.C, T), units = cdiv(n, n <= 32 ? 32 : 64) * cdiv(d, 128);
     // dH's vocabulary ranges: workgroups for every CU, at least 1 KB of W's rows each
     p.S_dh = balanced_splits(units, cdiv(V * elem, 1024), std::max<int64_t>(1, cdiv(1024, units)));
-    p.o_dz = bw.take((size_t)up(p.C, 128) * p.ldz * elem);
+    p.o_dz = bw.take((size_t)p.C * p.ldz * elem);
     p.o_hc = bw.take((size_t)p.C * d * elem);
     p.o_dhp = bw.take(p.S_dh > 1 ? (size_t)p.S_dh * p.C * d * 4 : 0);
   } else {
@@ -128,6 +128,14 @@ kd_status head_panels(const void* H, int64_t d, const kd::Compact& c, int64_t c0
     KD_LAUNCH("fill_zero", st, kd::launch_fill_zero(hp + d / 32 * C * 64, (dp - d) / 32 * C * 64, st));
   return KD_OK;
 }
+
+// Whether a bf16 dZ keeps what its rounding leaves in a second plane: up to 32
+// rows, where the products read and write W's size whatever dZ holds (MEASURE).  With so few rows one
+// entry of dZ, the token's, is most of a row of dH and of a column of dW, and
+// its rounding, up to 2^-9 and more of it, is that of the whole; over many
+// rows the roundings differ, and dH and dW are off by 0.0023 on average where
+// their own rounding to bf16 makes 0.0017.
+bool logp_planes(int64_t T, int elem) { return elem == 2 && T <= 32; }
 
 // The valid rows, the masked rows of dH (nullable) zeroed, and up to kPrepMax
 // rows the first C of H's packed (Hc nullable): one launch, whose blocks each
@@ -261,6 +269,7 @@ kd_status logp_bwd(const void* H, const void* W, const int32_t* tokens, const ui
     a.g = g;
     a.ge = ge;
     a.dz = at<char>(workspace, p.o_dz);
+    a.lo = logp_planes(T, elem) ? 128 * p.ldz * elem : 0;  // a chunk has at least 256 rows of room
     float* dw32 = p.C < T ? at<float>(workspace, p.o_dw32) : nullptr;
     for (int64_t c0 = 0; c0 < T; c0 += p.C) {
       a.rs = kd::RowSet{mask ? c.rows : nullptr, c.count, c0, p.C, T};

@@ -26,7 +26,8 @@ def logp_reference(H, W, tokens, mask, tau, g=None, ge=None):
 
     z is a sum of d products in 32 bits: off by at most d u |h|.|w| (a(t) below, the row's largest, over tau).  logp and
     lse move by at most twice that, 2^x and log2 by a few u of the result.  d ent / d s = -q (log q + ent) sums to at
-    most 2 ent + 2 <= 2 log V + 2 in absolute value.  dZ is rounded to the inputs' type; its own 32-bit error is q's
+    most 2 ent + 2 <= 2 log V + 2 in absolute value.  dZ is rounded to the inputs' type (twice its bits up to 32 rows);
+    its own 32-bit error is q's
     relative one, 2 a plus a few u.  dH and dW then sum V or T products in 32 bits and are rounded once."""
     T, d = H.shape
     V = W.shape[1]
@@ -57,7 +58,8 @@ def logp_reference(H, W, tokens, mask, tau, g=None, ge=None):
     dz, size = dz / tau, size / tau
     r["dH"], r["dW"] = dz @ Wd.t(), Hd.t() @ dz
     uz = half_step(H.dtype)
-    rel = (uz + 4 * base[:, None] + 2.0 ** -18)
+    udz = min(uz, 2.0 ** -16) if T <= 32 else uz  # up to 32 rows keep what the rounding leaves, rounded again
+    rel = (udz + 4 * base[:, None] + 2.0 ** -18)
     szW, Hsz = (rel * size) @ Wd.abs().t(), Hd.abs().t() @ (rel * size)
     bound["dH"] = szW + V * U32 * (size @ Wd.abs().t()) + uz * (r["dH"].abs() + szW) + 1e-30
     bound["dW"] = Hsz + T * U32 * (Hd.abs().t() @ size) + uz * (r["dW"].abs() + Hsz) + 1e-30
