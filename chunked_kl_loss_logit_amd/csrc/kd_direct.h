@@ -38,8 +38,6 @@ constexpr int kDirA = 128;             // a-side indices of a tile
 constexpr int kDirLd = 132;            // LDS row stride, floats
 constexpr int kDirRegion = 32 * kDirLd;  // floats of one wave's region
 
-typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
-
 template <class E, int U>
 constexpr int kDirStep = 2 * U * E::kEpc;  // k per step
 
@@ -79,20 +77,24 @@ struct RowsK {
   __device__ inline u32x4_t frag(int buf, int f, int u) const { return r[buf][f][u]; }
 };
 
-template <class E, int U>
+// F consecutive indices to a lane: 4, or 2 where the tile is narrower
+template <class E, int U, int F = 4>
 struct ColsN {
   static constexpr bool kColumns = true;
-  static constexpr int kFrags = 4;
+  static constexpr int kFrags = F;
   static constexpr int kRows = U * E::kEpc;  // k per half and step
-  using V = std::conditional_t<E::kElem == 2, u32x2_t, u32x4_t>;
+  static constexpr int kWords = F * E::kElem / 4;
+  struct __attribute__((aligned(4 * kWords))) Vec {
+    uint32_t w[kWords];
+  };
   const char* base;  // row 0, uniform
-  uint32_t off;      // the lane's four indices, in its half's first row
-  uint32_t col;      // the lane's four indices
+  uint32_t off;      // the lane's indices, in its half's first row
+  uint32_t col;      // the lane's indices
   long ld;           // bytes, uniform; 16 rows of it below 4 GB
   int K;
-  V r[2][kRows];
-  __device__ inline static int index(int f, int m) { return 4 * m + f; }
-  // n: the lane's first index (of four that exist)
+  Vec r[2][kRows];
+  __device__ inline static int index(int f, int m) { return F * m + f; }
+  // n: the lane's first index (of F that exist)
   __device__ inline void init(const char* b, long ld_, int K_, int n) {
     base = b;
     ld = ld_;
@@ -103,13 +105,13 @@ struct ColsN {
   __device__ inline void load(int buf, int k) {
     const char* q = base + (long)k * ld;
 #pragma unroll
-    for (int s = 0; s < kRows; ++s) r[buf][s] = *reinterpret_cast<const V*>(q + s * ld + off);
+    for (int s = 0; s < kRows; ++s) r[buf][s] = *reinterpret_cast<const Vec*>(q + s * ld + off);
   }
   __device__ inline void load_end(int buf, int k) {
     const int h = (threadIdx.x >> 5) & 1;
 #pragma unroll
     for (int s = 0; s < kRows; ++s)
-      r[buf][s] = *reinterpret_cast<const V*>(base + (long)max(0, min(k + kRows * h + s, K - 1)) * ld + col);
+      r[buf][s] = *reinterpret_cast<const Vec*>(base + (long)max(0, min(k + kRows * h + s, K - 1)) * ld + col);
   }
   // chunk u of index f: 8 bf16 or 4 float32 along k
   __device__ inline u32x4_t frag(int buf, int f, int u) const {
@@ -118,10 +120,10 @@ struct ColsN {
       const uint32_t sel = f & 1 ? 0x07060302u : 0x05040100u;
 #pragma unroll
       for (int w = 0; w < 4; ++w)
-        o[w] = __builtin_amdgcn_perm(r[buf][8 * u + 2 * w + 1][f >> 1], r[buf][8 * u + 2 * w][f >> 1], sel);
+        o[w] = __builtin_amdgcn_perm(r[buf][8 * u + 2 * w + 1].w[f >> 1], r[buf][8 * u + 2 * w].w[f >> 1], sel);
     } else {
 #pragma unroll
-      for (int w = 0; w < 4; ++w) o[w] = r[buf][4 * u + w][f];
+      for (int w = 0; w < 4; ++w) o[w] = r[buf][4 * u + w].w[f];
     }
     return o;
   }
@@ -184,12 +186,17 @@ __device__ inline void k_range(int K, int unit, int i, int parts, int& kb, int& 
 }
 
 // Sums the KS waves' accumulators and hands the tile out: row(b, m, q, x) has
-// the sums of b-index B::index(b, m) at the four a-indices from 4 q, with
-// eight lanes (q % 8) side by side on a row and m differing by lane.  Each
-// lane gets its row's q, q + 8, q + 16 and q + 24 in one call, x[0 .. 3].
+// the sums of b-index B::index(b, m) in x[0 .. 3], four a-indices each, from
+// quad_at<kPairs>(q, 0 .. 3) on, with eight lanes (q = 0 .. 7) side by side on
+// a row and m differing by lane.  kPairs: x[0], x[1] and x[2], x[3] are eight
+// consecutive a-indices, 16 bytes of bf16 (put_row).
 // KS = 1: every wave hands out its own tile.  A: the a-side operand's type.
 // reg: LDS, 4 regions.
-template <class A, int R, int KS, class Row>
+template <bool kPairs>
+__device__ inline int quad_at(int q, int j) {
+  return 4 * (kPairs ? 2 * q + (j & 1) + 16 * (j >> 1) : q + 8 * j);
+}
+template <class A, int R, int KS, bool kPairs, class Row>
 __device__ __forceinline__ void direct_rows(const f32x16_t (&acc)[4][R], float* reg, Row&& row) {
   const int w = wave_id(), lane = threadIdx.x & 63, h = lane >> 5;
   float* mine = reg + w * kDirRegion + (lane & 31) * kDirLd;
@@ -223,7 +230,7 @@ __device__ __forceinline__ void direct_rows(const f32x16_t (&acc)[4][R], float* 
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const float4 y = *reinterpret_cast<const float4*>(reg + (KS == 1 ? w : s) * kDirRegion + m * kDirLd +
-                                                            4 * (q + 8 * j));
+                                                            quad_at<kPairs>(q, j));
           x[j].x += y.x;
           x[j].y += y.y;
           x[j].z += y.z;

@@ -111,7 +111,7 @@ __device__ __forceinline__ void fwd_tile(const LogpDirectArgs& a, long M, long r
   logits_tile<E, R>(a, M, r0, n0, acc);
   float4* part = reinterpret_cast<float4*>(a.part) + (long)tile * a.rs.C + r0;
   const int cols = min(kDirA, V - n0);  // a multiple of 4
-  direct_rows<ColsN<E, 2>, R, 4>(acc, reg, [&](int b, int m, int q, const float4 (&z)[4]) {
+  direct_rows<ColsN<E, 2>, R, 4, false>(acc, reg, [&](int b, int m, int q, const float4 (&z)[4]) {
     const int i = 32 * b + m;
     if (a.z && r0 + i < M) {
       float* zr = a.z + (r0 + i) * a.ldz + n0 + 4 * q;
@@ -206,14 +206,27 @@ __device__ inline void store4(char* p, float4 x) {
     *reinterpret_cast<float4*>(p) = x;
 }
 
-// dZ, and where the chunk has them (LogpDirectArgs::lo) the rests of its rounding
+// A row's x of direct_rows<.., E::kElem == 2, ..>, to the columns from p on, `cols` of them there
 template <class E>
-__device__ inline void put_dz(const LogpDirectArgs& a, long i, long c, float4 x) {
-  char* p = a.dz + (i * a.ldz + c) * E::kElem;
-  store4<E>(p, x);
-  if constexpr (E::kElem == 2)
-    if (a.lo) store4<E>(p + a.lo, make_float4(rest(x.x), rest(x.y), rest(x.z), rest(x.w)));
+__device__ inline void put_row(char* p, int q, int cols, const float4 (&x)[4]) {
+  if constexpr (E::kElem == 2) {
+#pragma unroll
+    for (int j = 0; j < 4; j += 2) {
+      const int c = quad_at<true>(q, j);
+      if (c < cols)
+        *reinterpret_cast<uint4*>(p + 2 * c) =
+            make_uint4(Bf16::pack2(x[j].x, x[j].y), Bf16::pack2(x[j].z, x[j].w), Bf16::pack2(x[j + 1].x, x[j + 1].y),
+                       Bf16::pack2(x[j + 1].z, x[j + 1].w));
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int c = quad_at<false>(q, j);
+      if (c < cols) *reinterpret_cast<float4*>(p + 4 * c) = x[j];
+    }
+  }
 }
+__device__ inline float4 rest4(float4 x) { return make_float4(rest(x.x), rest(x.y), rest(x.z), rest(x.w)); }
 
 }  // namespace
 
@@ -228,15 +241,19 @@ __device__ __forceinline__ void dz_tile(const LogpDirectArgs& a, long M, long r0
   }
   f32x16_t acc[4][R];
   logits_tile<E, R>(a, M, r0, n0, acc);
-  direct_rows<ColsN<E, 2>, R, 4>(acc, reg, [&](int b, int m, int q, const float4 (&z)[4]) {
+  constexpr bool kPairs = E::kElem == 2;
+  direct_rows<ColsN<E, 2>, R, 4, kPairs>(acc, reg, [&](int b, int m, int q, const float4 (&z)[4]) {
     const long i = r0 + 32 * b + m;
+    float4 o[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int c = n0 + 4 * q + 32 * j;
-      if (c >= V) break;
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (i < M) o = dz_four<kEnt>(z[j], k[b], a.c2, c);
-      put_dz<E>(a, i, c, o);
+    for (int j = 0; j < 4; ++j)
+      o[j] = i < M ? dz_four<kEnt>(z[j], k[b], a.c2, n0 + quad_at<kPairs>(q, j)) : make_float4(0.f, 0.f, 0.f, 0.f);
+    char* p = a.dz + (i * a.ldz + n0) * E::kElem;
+    put_row<E>(p, q, V - n0, o);
+    if (kPairs && a.lo) {  // what the rounding left
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[j] = rest4(o[j]);
+      put_row<E>(p + a.lo, q, V - n0, o);
     }
   });
 }
@@ -267,7 +284,9 @@ __global__ __launch_bounds__(256) void logp_direct_dz_from_z_kernel(LogpDirectAr
     if (c >= a.V) break;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     if (i < M) o = dz_four<kEnt>(*reinterpret_cast<const float4*>(a.z + i * a.ldz + c), k, a.c2, c);
-    put_dz<E>(a, i, c, o);
+    char* p = a.dz + (i * a.ldz + c) * E::kElem;
+    store4<E>(p, o);
+    if (E::kElem == 2 && a.lo) store4<E>(p + a.lo, rest4(o));
   }
 }
 
@@ -303,7 +322,7 @@ __global__ __launch_bounds__(kDirThreads, 1) void logp_direct_dh_kernel(LogpDire
   zero(acc);
   direct_contract<E, U>(wl, zl, kb, ke, acc);
   float4 first[4];
-  direct_rows<RowsK<E, 4, U>, R, 4>(acc, reg, [&](int b, int mm, int q, float4 (&x)[4]) {
+  direct_rows<RowsK<E, 4, U>, R, 4, false>(acc, reg, [&](int b, int mm, int q, float4 (&x)[4]) {
     const long i = r0 + (kTwo ? mm : 32 * b + mm);
     if constexpr (kTwo) {
 #pragma unroll
@@ -347,45 +366,50 @@ __global__ __launch_bounds__(256) void logp_direct_reduce_kernel(RowSet rs, cons
 }
 
 // ------------------------------------------------------------------ dW
-// KS = 4: one 128 x 128 tile of [V] x [d], the rows split over the four
-// waves; KS = 1: four tiles side by side in d, all rows each.
-template <class E, int KS, class O>
-__global__ __launch_bounds__(kDirThreads, 1) void logp_direct_dw_kernel(LogpDirectArgs a, const char* Hc, int nda,
-                                                                        const float* add, char* out) {
-  constexpr int U = E::kElem == 4 ? 1 : 2;  // two chunks of float32 would not leave room for the accumulators
+// Tiles of 128 columns of V x 32 F of d.  KS = 4: the rows split over the four
+// waves; KS = 1: four tiles side by side in d, all rows each.  F = 2 leaves
+// room for a second workgroup on the CU, for few rows, where a tile is little
+// more than its stores.
+template <class E, int KS, class O, int F>
+__global__ __launch_bounds__(kDirThreads, F == 2 ? 2 : 1) void logp_direct_dw_kernel(LogpDirectArgs a, const char* Hc,
+                                                                                     int nda, const float* add,
+                                                                                     char* out) {
+  constexpr int U = E::kElem == 4 || F == 2 ? 1 : 2;  // two chunks would not leave room for the accumulators
+  constexpr int kD = 32 * F;
   __shared__ __attribute__((aligned(16))) float reg[4 * kDirRegion];
   const long M = max(0L, chunk_rows_of(a.rs));
   const int id = xcd_remap(blockIdx.x, gridDim.x);
   const int w = wave_id(), lane = threadIdx.x & 63, m = lane & 31;
-  const int d0 = ((id % nda) * (KS == 1 ? 4 : 1) + (KS == 1 ? w : 0)) * kDirA, n0 = id / nda * kDirA;
+  const int d0 = ((id % nda) * (KS == 1 ? 4 : 1) + (KS == 1 ? w : 0)) * kD, n0 = id / nda * kDirA;
   const int d = (int)a.d, V = (int)a.V;
-  ColsN<E, U> zl, hl;
+  ColsN<E, U> zl;
+  ColsN<E, U, F> hl;
   zl.init(a.dz, a.ldz * E::kElem, (int)((M + 31) / 32 * 32), min(n0 + 4 * m, V - 4));  // zero rows behind the last
-  hl.init(Hc, (long)d * E::kElem, (int)M, min(d0 + 4 * m, d - 4));
+  hl.init(Hc, (long)d * E::kElem, (int)M, min(d0 + F * m, d - F));
   int kb, ke;
   k_range((int)M, kDirStep<E, U>, KS == 1 ? 0 : w, KS, kb, ke);
-  f32x16_t acc[4][4];
+  f32x16_t acc[4][F];
   zero(acc);
   for (int plane = a.lo ? 2 : 1;;) {
     direct_contract<E, U>(zl, hl, kb, ke, acc);
     if (--plane == 0) break;
     zl.base += a.lo;
   }
-  direct_rows<ColsN<E, U>, 4, KS>(acc, reg, [&](int b, int mm, int q, const float4 (&x)[4]) {
-    const int i = d0 + ColsN<E, U>::index(b, mm);
+  constexpr bool kPairs = O::kElem == 2;
+  direct_rows<ColsN<E, U>, F, KS, kPairs>(acc, reg, [&](int b, int mm, int q, float4 (&x)[4]) {
+    const int i = d0 + ColsN<E, U, F>::index(b, mm);
     if (i >= d) return;
+    const long at = (long)i * V + n0;
+    if (add) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int c = n0 + 4 * q + 32 * j;
-      if (c >= V) break;
-      const long at = (long)i * V + c;
-      float4 v = x[j];
-      if (add) {
-        const float4 y = *reinterpret_cast<const float4*>(add + at);
-        v = make_float4(v.x + y.x, v.y + y.y, v.z + y.z, v.w + y.w);
+      for (int j = 0; j < 4; ++j) {
+        const int c = quad_at<kPairs>(q, j);
+        if (n0 + c >= V) break;
+        const float4 y = *reinterpret_cast<const float4*>(add + at + c);
+        x[j] = make_float4(x[j].x + y.x, x[j].y + y.y, x[j].z + y.z, x[j].w + y.w);
       }
-      store4<O>(out + at * O::kElem, v);
     }
+    put_row<O>(out + at * O::kElem, q, V - n0, x);
   });
 }
 
@@ -564,24 +588,28 @@ hipError_t launch_logp_direct_dh(int elem, const LogpDirectArgs& a, int S, float
 
 hipError_t launch_logp_direct_dw(int elem, const LogpDirectArgs& a, const void* Hc, const float* add32, void* out,
                                  int out_elem, hipStream_t st) {
-  const int nda = cdiv(a.d, kDirA), nv = cdiv(a.V, kDirA);
-  // four waves on a tile where there are too few tiles for every wave to have its own
-  const bool split = (int64_t)nda * nv < 1024 && rows_upto(a.rs) > 64;
-  const int n4 = split ? nda : cdiv(nda, 4);
+  // Tiles 64 of d wide up to 64 rows (7 rows of 2048 x 32000 bf16, from logits,
+  // 41 us, with tiles of 128 68; 64 rows 44 and 68); else four waves on a tile where there are
+  // too few tiles for every wave to have its own.
+  const int nv = cdiv(a.V, kDirA), nda = cdiv(a.d, kDirA);
+  const bool few = rows_upto(a.rs) <= 64, split = !few && (int64_t)nda * nv < 1024;
+  const int n4 = few ? cdiv(a.d, 256) : split ? nda : cdiv(nda, 4);
   const dim3 grid((unsigned)(n4 * nv)), block(kDirThreads);
   const char* h = static_cast<const char*>(Hc);
   char* o = static_cast<char*>(out);
-  auto go = [&](auto ks) {
-    constexpr int KS = decltype(ks)::value;
+  auto go = [&](auto ks, auto f) {
+    constexpr int KS = decltype(ks)::value, F = decltype(f)::value;
     if (elem == 4)
-      hipLaunchKernelGGL((logp_direct_dw_kernel<F32, KS, F32>), grid, block, 0, st, a, h, n4, add32, o);
+      hipLaunchKernelGGL((logp_direct_dw_kernel<F32, KS, F32, F>), grid, block, 0, st, a, h, n4, add32, o);
     else if (out_elem == 4)
-      hipLaunchKernelGGL((logp_direct_dw_kernel<Bf16, KS, F32>), grid, block, 0, st, a, h, n4, add32, o);
+      hipLaunchKernelGGL((logp_direct_dw_kernel<Bf16, KS, F32, F>), grid, block, 0, st, a, h, n4, add32, o);
     else
-      hipLaunchKernelGGL((logp_direct_dw_kernel<Bf16, KS, Bf16>), grid, block, 0, st, a, h, n4, add32, o);
+      hipLaunchKernelGGL((logp_direct_dw_kernel<Bf16, KS, Bf16, F>), grid, block, 0, st, a, h, n4, add32, o);
   };
-  if (split) go(std::integral_constant<int, 4>());
-  else go(std::integral_constant<int, 1>());
+  using std::integral_constant;
+  if (few) go(integral_constant<int, 1>(), integral_constant<int, 2>());
+  else if (split) go(integral_constant<int, 4>(), integral_constant<int, 4>());
+  else go(integral_constant<int, 1>(), integral_constant<int, 4>());
   return hipGetLastError();
 }
 

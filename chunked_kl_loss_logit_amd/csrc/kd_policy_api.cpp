@@ -129,12 +129,14 @@ kd_status head_panels(const void* H, int64_t d, const kd::Compact& c, int64_t c0
   return KD_OK;
 }
 
-// Whether a bf16 dZ keeps what its rounding leaves in a second plane: up to 32
-// rows, where the products read and write W's size whatever dZ holds (MEASURE).  With so few rows one
-// entry of dZ, the token's, is most of a row of dH and of a column of dW, and
-// its rounding, up to 2^-9 and more of it, is that of the whole; over many
-// rows the roundings differ, and dH and dW are off by 0.0023 on average where
-// their own rounding to bf16 makes 0.0017.
+// Whether a bf16 dZ keeps what its rounding leaves in a second plane.  dZ is
+// rounded to the type of the products it feeds, as for the other losses; over
+// many rows the roundings differ, and dH and dW are off by 0.0023 on average
+// where their own rounding to bf16 makes 0.0017.  With few rows one entry of
+// dZ, the token's, is most of a row of dH and of a column of dW, and its
+// rounding, up to 2^-8, is that of the whole.  Up to 32 rows the products read
+// and write W's size whatever dZ holds: a backward of 7 rows of 2048 x 32000
+// took 110 us without the second plane and 119 with it.
 bool logp_planes(int64_t T, int elem) { return elem == 2 && T <= 32; }
 
 // The valid rows, the masked rows of dH (nullable) zeroed, and up to kPrepMax

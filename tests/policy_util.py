@@ -27,8 +27,8 @@ def logp_reference(H, W, tokens, mask, tau, g=None, ge=None):
     z is a sum of d products in 32 bits: off by at most d u |h|.|w| (a(t) below, the row's largest, over tau).  logp and
     lse move by at most twice that, 2^x and log2 by a few u of the result.  d ent / d s = -q (log q + ent) sums to at
     most 2 ent + 2 <= 2 log V + 2 in absolute value.  dZ is rounded to the inputs' type (twice its bits up to 32 rows);
-    its own 32-bit error is q's
-    relative one, 2 a plus a few u.  dH and dW then sum V or T products in 32 bits and are rounded once."""
+    its own 32-bit error is q's relative one, 2 a plus a few u.  dH and dW then sum V or T products in 32 bits and are
+    rounded once."""
     T, d = H.shape
     V = W.shape[1]
     Hd, Wd = H.double(), W.double()
