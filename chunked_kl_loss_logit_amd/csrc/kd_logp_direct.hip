@@ -10,7 +10,11 @@
 // The mathematics is that of kd_logp.hip.  Bounds: a few rows, the read of W
 // (each workgroup streams its columns once, 16 KB a wave in flight); many
 // rows, float32, the matrix cores (64 instructions of 64 cycles per 64 KB of
-// operands).
+// operands).  Measured: forward of 7 rows of 2048 x 32000 bf16 22 us (6.0 TB/s
+// of W, half of it from the last-level cache), its dW 34 us (3.9 TB/s written);
+// 700 rows of 1024 x 32000 float32, of the 152 TFLOP/s that a large product
+// reaches: forward with kept logits 459 us (100 TFLOP/s), dH 470 (98), dW 373
+// (123); dZ from the logits 34 us (5.3 TB/s).
 #include <type_traits>
 
 #include "kd_direct.h"
@@ -83,7 +87,7 @@ __device__ __forceinline__ void logits_tile(const LogpDirectArgs& a, long M, lon
 
 // A row block of up to 32 R rows: f with as many block columns (1, 2 or 4) as
 // its rows fill, so that a short last block costs what its rows do (700 rows
-// of a 1024 x 32000 float32 head: fp32 forward 525 -> 468 us).
+// of a 1024 x 32000 float32 head: forward 525 us without, 468 with).
 template <int R, class F>
 __device__ __forceinline__ void by_left(long left, F&& f) {
   if constexpr (R > 1) {
@@ -510,7 +514,8 @@ void dz(const LogpDirectArgs& a, hipStream_t st) {
 }
 // Block columns of rows per tile: 1, 2 or 4, no more than hold the rows, and
 // fewer where the tiles would not go round the CUs (at 4 a tile's operands are
-// used best; at 128 rows of a 4096 x 4096 float32 head 1 takes 99 us, 4 takes 261).
+// used best; forward of float32, us, 1 / 4: 128 rows of 4096 x 4096 73 / 246, of
+// 1024 x 32000 123 / 78).
 template <class F>
 void by_rows(int64_t n, int64_t V, F&& f) {
   const int64_t cols = cdiv(V, kDirA);

@@ -11,7 +11,7 @@ using namespace kdh;
 namespace {
 
 // ---------------------------------------------------------------- token log-probabilities
-// Whether a head runs on the register-fed tiles (kd_direct.h) rather than the
+// Whether the forward runs on the register-fed tiles (kd_direct.h) rather than the
 // 256 x 256 ring tiles: float32, shapes the ring does not take, and bf16
 // products too small to fill the ring's rounds of 256 workgroups.  A round
 // costs the ring the same however few of its rows and tiles are real; the
@@ -19,16 +19,30 @@ namespace {
 // register-fed: 32 x 4096 x 8192 84 / 31, 64 x 2048 x 128256 152 / 125, 128 x
 // 4096 x 32000 87 / 67, 512 x 4096 x 8192 88 / 63; on the other side 128 x 2048
 // x 128256 153 / 185, 256 x 4096 x 32000 95 / 124, 1024 x 4096 x 8192 94 / 119.
-bool use_direct(int64_t T, int64_t d, int64_t V, int elem) {
+bool direct_fwd(int64_t T, int64_t d, int64_t V, int elem) {
   const int64_t C = chunk_of(T, V, elem, 0);
   if (!kd::logp_ring_fits(elem, C, d, V)) return true;
   const int64_t rounds = cdiv(cdiv(std::min(T, C), kd::kTileM) * cdiv(V, kd::kTileN), 256);
   return std::min(T, C) * V < rounds * 7000000;
 }
 
+// The same for the backward, whose products the ring splits better (dH over
+// the vocabulary) but pays more launches for: up to 64 rows, and products of
+// fewer than 7e9 terms.  Backward, us, recomputing / from kept logits, ring
+// against register-fed: 64 x 2048 x 128256 501 / 438, 477 / 368; 1024 x 1024 x
+// 4096 102 / 75, 78 / 61; 4096 x 512 x 2048 145 / 126, 113 / 85; on the other
+// side 65 x 2048 x 128256 498 / 438, 646 / 476; 700 x 4096 x 4096 165 / 91, 200
+// / 137; 512 x 4096 x 8192 187 / 114, 213 / 163.
+bool direct_bwd(int64_t T, int64_t d, int64_t V, int elem) {
+  const int64_t C = chunk_of(T, V, elem, 0);
+  if (!kd::logp_ring_fits(elem, C, d, V)) return true;
+  const int64_t n = std::min(T, C);
+  return n <= 64 || (double)n * d * V < 7e9;
+}
+
 struct LogpPlan {
-  bool direct;
-  int ntiles;    // column tiles of the forward
+  bool fwd_direct, bwd_direct;
+  int ntiles_f, ntiles;  // column tiles of the forward and of the backward's dZ
   int64_t Cf;    // rows per forward chunk
   int64_t C, ldz;  // rows per backward chunk, columns of its dZ
   int S_dh;      // direct: vocabulary ranges of dH
@@ -46,16 +60,26 @@ int64_t ring_rows(int64_t row_bytes) { return ((int64_t(1) << 32) - 65537) / row
 
 LogpPlan plan_logp(int64_t T, int64_t d, int64_t V, int elem, int dw_elem, int64_t chunk_rows) {
   LogpPlan p{};
-  p.direct = use_direct(T, d, V, elem);
-  p.ntiles = (int)cdiv(V, p.direct ? kd::kDirectCols : kd::kTileN);
+  p.fwd_direct = direct_fwd(T, d, V, elem);
+  p.bwd_direct = direct_bwd(T, d, V, elem);
+  p.ntiles_f = (int)cdiv(V, p.fwd_direct ? kd::kDirectCols : kd::kTileN);
+  p.ntiles = (int)cdiv(V, kd::kTileN);
   p.Cf = chunk_of(T, V, elem, 0);
   p.ldz = cdiv(V, kd::kTileN) * kd::kTileN;
   Carver cv;
   p.o_rows = cv.take((size_t)T * 4);
   p.o_count = cv.take(16);
   Carver fw = cv, bw = cv;  // the two calls' buffers overlap
-  if (p.direct) {
-    p.o_part = fw.take((size_t)p.ntiles * p.Cf * 16);
+  // the ring's H panels run to whole ring turns of d; dZ's hold the tail pieces
+  // too, within the same 32-bit reach
+  const int64_t dp = cdiv(d, 128) * 128;
+  if (p.fwd_direct) {
+    p.o_part = fw.take((size_t)p.ntiles_f * p.Cf * 16);
+  } else {
+    p.o_part = fw.take((size_t)std::min(p.ntiles_f, kd::kRingMaxSplits) * p.Cf * 16);
+    p.o_hp_f = fw.take(panel_bytes(p.Cf, dp * elem));
+  }
+  if (p.bwd_direct) {
     p.C = chunk_of(T, V, elem, chunk_rows);
     const int64_t n = std::min(p.C, T), units = cdiv(n, n <= 32 ? 32 : 64) * cdiv(d, 128);
     // dH's vocabulary ranges: workgroups for every CU, at least 1 KB of W's rows each
@@ -64,11 +88,6 @@ LogpPlan plan_logp(int64_t T, int64_t d, int64_t V, int elem, int dw_elem, int64
     p.o_hc = bw.take((size_t)p.C * d * elem);
     p.o_dhp = bw.take(p.S_dh > 1 ? (size_t)p.S_dh * p.C * d * 4 : 0);
   } else {
-    // H's panels run to whole ring turns of d; dZ's hold the tail pieces too,
-    // within the same 32-bit reach
-    const int64_t dp = cdiv(d, 128) * 128;
-    p.o_part = fw.take((size_t)std::min(p.ntiles, kd::kRingMaxSplits) * p.Cf * 16);
-    p.o_hp_f = fw.take(panel_bytes(p.Cf, dp * elem));
     p.C = std::min(chunk_of(T, V + 32 * kd::kDzTailPieces, elem, chunk_rows), ring_rows(dp * elem));
     const int64_t ncb = cdiv(d, 256), units = cdiv(std::min(p.C, T), kd::kTileM) * ncb;
     p.grid_dh = (int)up(units * balanced_splits(units, cdiv(V, 128), std::max<int64_t>(1, cdiv(1024, units))), 256);
@@ -169,7 +188,7 @@ kd_status logp_fwd(const void* H, const void* W, const int32_t* tokens, const ui
   float* part = at<float>(workspace, p.o_part);
   const float c2 = (float)(1.4426950408889634 / (double)tau);
   kd::RowSet rs{c.rows, c.count, 0, p.Cf, T};
-  if (p.direct) {
+  if (p.fwd_direct) {
     if (mask)
       KD_TRY(direct_rows(mask, T, c, H, d * elem, 0, nullptr, nullptr, 0, st));
     else
@@ -190,7 +209,7 @@ kd_status logp_fwd(const void* H, const void* W, const int32_t* tokens, const ui
       a.z = logits ? logits + c0 * p.ldz : nullptr;
       KD_LAUNCH("logp_direct_fwd", st, kd::launch_logp_direct_fwd(elem, a, entropy, st));
       KD_LAUNCH("logp_combine", st,
-                kd::launch_logp_combine(part, p.ntiles, 0, rs, mask, tokens, V, c2, out, c0 == 0, st));
+                kd::launch_logp_combine(part, p.ntiles_f, 0, rs, mask, tokens, V, c2, out, c0 == 0, st));
     }
     return KD_OK;
   }
@@ -207,18 +226,18 @@ kd_status logp_fwd(const void* H, const void* W, const int32_t* tokens, const ui
   a.d = d;
   a.V = V;
   a.v0 = (int32_t)v0;
-  a.ntiles = p.ntiles;
+  a.ntiles = p.ntiles_f;
   a.group = kRasterGroup;
   a.c2 = c2;
   for (int64_t c0 = 0; c0 < T; c0 += p.Cf) {
-    const int grid = ring_grid(T, c0, p.Cf, p.ntiles);
+    const int grid = ring_grid(T, c0, p.Cf, p.ntiles_f);
     KD_TRY(head_panels(H, d, c, c0, p.Cf, hp, st));
     a.c0 = rs.c0 = c0;
     a.zout = logits ? logits + c0 * p.ldz : nullptr;
     a.grid = grid;
     KD_LAUNCH("logp_fwd_tile", st, kd::launch_logp_fwd(a, entropy, st));
     KD_LAUNCH("logp_combine", st,
-              kd::launch_logp_combine(part, p.ntiles, grid, rs, mask, tokens, V, c2, out, c0 == 0, st));
+              kd::launch_logp_combine(part, p.ntiles_f, grid, rs, mask, tokens, V, c2, out, c0 == 0, st));
   }
   return KD_OK;
 }
@@ -255,7 +274,7 @@ kd_status logp_bwd(const void* H, const void* W, const int32_t* tokens, const ui
 
   const kd::Compact c{at<int32_t>(workspace, p.o_rows), at<int32_t>(workspace, p.o_count)};
   const float c2 = (float)(1.4426950408889634 / (double)tau), inv_tau = (float)(1.0 / (double)tau);
-  if (p.direct) {
+  if (p.bwd_direct) {
     kd::LogpDirectArgs a{};
     a.H = static_cast<const char*>(H);
     a.W = static_cast<const char*>(W);

@@ -34,11 +34,16 @@ SHAPES = [
     (9, 72, 328, bf, 0.0, 1.0, 0),
     (300, 200, 8, bf, 0.1, 1.0, 0),     # less than a tile of vocabulary
     (5, 8, 16, bf, 0.0, 1.0, 0),
-    # products of at least 7 million logits a round run on the 256 x 256 ring tiles
+    # from 7 million logits a round on, the forward runs on the 256 x 256 ring tiles
     (600, 256, 12032, bf, 0.0, 1.0, 0),     # whole ring turns everywhere
     (601, 160, 12008, bf, 0.2, 0.8, 0),     # d, V inside a turn, V inside a 32-column stage
     (1100, 96, 6624, bf, 0.3, 1.0, 512),    # several chunks of a bf16 dW, V inside a turn
     (1300, 384, 5592, bf, 0.0, 1.0, 0),
+    # and the backward from 7e9 terms of a product on
+    (400, 2080, 8456, bf, 0.3, 0.9, 0),     # d inside a turn, V inside a 32-column stage
+    (1500, 1056, 4456, bf, 0.2, 1.0, 512),  # several chunks of a bf16 dW
+    (90, 8192, 9504, bf, 0.0, 1.0, 0),      # a row block mostly empty, V inside a turn
+    (330, 4096, 5248, bf, 0.1, 1.0, 0),     # whole turns
     (1, 4, 4, f32, 0.0, 1.0, 0),
     (33, 12, 20, f32, 0.3, 1.0, 0),
     (65, 100, 260, f32, 0.0, 0.5, 0),
@@ -110,13 +115,13 @@ def test_gradient_against_differences():
     assert abs(diff - along) <= 3e-3 * (1 + abs(along)), (diff, along)
 
 
-@pytest.mark.parametrize("V,rows", [(1000, 0), (7016, 1024)])
-def test_tokens_at_every_tile_edge(V, rows):
+@pytest.mark.parametrize("V,rows,d", [(1000, 0, 128), (7016, 1024, 128), (7016, 1024, 1024)])
+def test_tokens_at_every_tile_edge(V, rows, d):
     """One row per column where a tile, a wave's half or a lane's group begins or ends."""
     edges = sorted({max(0, min(V - 1, b + o)) for b in range(0, V + 32, 32) for o in (-1, 0, 3, 4)} | {744, 743, 767, 768})
     edges = (edges + list(range(rows)))[:max(rows, len(edges))]
     T = len(edges)
-    H, W, _, _ = make_head(T, 128, V, bf, 11)
+    H, W, _, _ = make_head(T, d, V, bf, 11)
     tokens = torch.tensor(edges, dtype=torch.int32)
     g, _ = upstream(T, 11)
     want, bound = logp_reference(H, W, tokens, None, 1.0, g)
@@ -129,11 +134,11 @@ def test_tokens_at_every_tile_edge(V, rows):
         within(dW, want["dW"], bound["dW"], "dW")
 
 
-@pytest.mark.parametrize("T,V", [(20, 776), (300, 776), (1000, 7016)])
-def test_large_logits(T, V):
+@pytest.mark.parametrize("T,V,d", [(20, 776, 128), (300, 776, 128), (1000, 7016, 128), (1000, 7016, 1024)])
+def test_large_logits(T, V, d):
     """Logits of hundreds: every 2^x must be taken relative to the row's maximum, and rows past the last valid one
     (whose accumulators hold a copy of a real row) must not reach dW."""
-    H, W, tokens, mask = make_head(T, 128, V, bf, 13, scale=30.0, masked=0.1)
+    H, W, tokens, mask = make_head(T, d, V, bf, 13, scale=30.0, masked=0.1)
     g, ge = upstream(T, 13)
     want, bound = logp_reference(H, W, tokens, mask, 1.0, g, ge)
     a = [dev(x) for x in (H, W, tokens, mask)]
@@ -146,9 +151,10 @@ def test_large_logits(T, V):
         within(dW, want["dW"], bound["dW"], "dW")
 
 
-@pytest.mark.parametrize("T,V,dtype", [(12, 520, bf), (300, 520, bf), (1000, 7016, bf), (12, 520, f32)])
-def test_masked_rows_are_not_read(T, V, dtype):
-    H, W, tokens, _ = make_head(T, 128, V, dtype, 17)
+@pytest.mark.parametrize("T,V,d,dtype", [(12, 520, 128, bf), (300, 520, 128, bf), (1000, 7016, 128, bf),
+                                         (1000, 7016, 1024, bf), (12, 520, 128, f32)])
+def test_masked_rows_are_not_read(T, V, d, dtype):
+    H, W, tokens, _ = make_head(T, d, V, dtype, 17)
     mask = torch.ones(T, dtype=torch.uint8)
     mask[::3] = 0
     g, ge = upstream(T, 17)
@@ -168,9 +174,9 @@ def test_masked_rows_are_not_read(T, V, dtype):
     assert torch.equal(some[0], logp)
 
 
-@pytest.mark.parametrize("T,V", [(5, 264), (1000, 7016)])
-def test_every_row_masked_and_no_rows(T, V):
-    H, W, tokens, _ = make_head(T, 128, V, bf, 19)
+@pytest.mark.parametrize("T,V,d", [(5, 264, 128), (1000, 7016, 128), (1000, 7016, 1024)])
+def test_every_row_masked_and_no_rows(T, V, d):
+    H, W, tokens, _ = make_head(T, d, V, bf, 19)
     a = [dev(x) for x in (H, W, tokens, torch.zeros(T, dtype=torch.uint8))]
     logp, lse, ent, z = kd.token_logp_forward(*a, 1.0, want_entropy=True, keep_logits=True)
     g = torch.ones(T, device="cuda")
@@ -182,7 +188,7 @@ def test_every_row_masked_and_no_rows(T, V):
     e = [a[0][:0], a[1], a[2][:0], None]
     logp, lse, ent, z = kd.token_logp_forward(*e, 1.0, want_entropy=True, keep_logits=True)
     dH, dW = kd.token_logp_backward(*e, 1.0, lse, g[:0], dw_dtype=bf)
-    assert logp.numel() == 0 and dH.shape == (0, 128) and (dW == 0).all()
+    assert logp.numel() == 0 and dH.shape == (0, d) and (dW == 0).all()
 
 
 @pytest.mark.parametrize("T,V", [(6, 264), (300, 264), (1000, 7016)])
@@ -198,10 +204,11 @@ def test_a_token_outside_the_vocabulary_is_nan(T, V):
     within(lse, want["lse"], bound["lse"], "lse")
 
 
-@pytest.mark.parametrize("T,cuts,dtype", [(90, (0, 264, 600, 1288), bf), (90, (0, 8, 1288), bf),
-                                          (90, (0, 500, 1004), f32), (1000, (0, 7016, 14048), bf)])
-def test_vocabulary_shards(T, cuts, dtype):
-    d, V = 128, cuts[-1]
+@pytest.mark.parametrize("T,cuts,dtype,d", [(90, (0, 264, 600, 1288), bf, 128), (90, (0, 8, 1288), bf, 128),
+                                            (90, (0, 500, 1004), f32, 128), (1000, (0, 7016, 14048), bf, 128),
+                                            (1000, (0, 7016, 14048), bf, 1024)])
+def test_vocabulary_shards(T, cuts, dtype, d):
+    V = cuts[-1]
     H, W, tokens, mask = make_head(T, d, V, dtype, 29, masked=0.2)
     g, ge = upstream(T, 29)
     want, bound = logp_reference(H, W, tokens, mask, 1.3, g, ge)
@@ -234,7 +241,7 @@ def test_autograd(keep):
     within(dH, only["dH"], bo["dH"], "dH alone")
 
 
-@pytest.mark.parametrize("T,d,V", [(70, 128, 520), (1000, 160, 7016)])
+@pytest.mark.parametrize("T,d,V", [(70, 128, 520), (1000, 160, 7016), (1000, 1056, 7016)])
 def test_nothing_around_the_buffers_changes(T, d, V):
     """Outputs and workspace of exactly the asked size inside larger buffers."""
     Vp = -(-V // 256) * 256
@@ -265,9 +272,9 @@ def test_nothing_around_the_buffers_changes(T, d, V):
         assert (raw[:256] == 0x5A).all() and (raw[-256:] == 0x5A).all(), k
 
 
-@pytest.mark.parametrize("T,V", [(300, 1288), (1000, 7016)])
-def test_another_stream_and_the_same_bits(T, V):
-    H, W, tokens, mask = make_head(T, 256, V, bf, 41, masked=0.2)
+@pytest.mark.parametrize("T,V,d", [(300, 1288, 256), (1000, 7016, 256), (1000, 7016, 1024)])
+def test_another_stream_and_the_same_bits(T, V, d):
+    H, W, tokens, mask = make_head(T, d, V, bf, 41, masked=0.2)
     a = [dev(x) for x in (H, W, tokens, mask)]
     g = torch.randn(T, device="cuda")
 
@@ -287,9 +294,9 @@ def test_another_stream_and_the_same_bits(T, V):
         assert torch.equal(x, y)
 
 
-@pytest.mark.parametrize("T,V", [(9, 776), (300, 776), (1000, 7016)])
-def test_captured_and_replayed(T, V):
-    H, W, tokens, mask = make_head(T, 256, V, bf, 43, masked=0.2)
+@pytest.mark.parametrize("T,V,d", [(9, 776, 256), (300, 776, 256), (1000, 7016, 256), (1000, 7016, 1024)])
+def test_captured_and_replayed(T, V, d):
+    H, W, tokens, mask = make_head(T, d, V, bf, 43, masked=0.2)
     a = [dev(x) for x in (H, W, tokens, mask)]
     g = torch.randn(T, device="cuda")
 
@@ -303,7 +310,7 @@ def test_captured_and_replayed(T, V):
     with torch.cuda.graph(graph):
         out = calls()
     for k in range(4):
-        h2, _, t2, m2 = make_head(T, 256, V, bf, 50 + k, masked=0.1 * k)
+        h2, _, t2, m2 = make_head(T, d, V, bf, 50 + k, masked=0.1 * k)
         a[0].copy_(h2)
         a[2].copy_(t2)
         a[3].copy_(torch.ones(T, dtype=torch.uint8) if m2 is None else m2)
@@ -315,10 +322,11 @@ def test_captured_and_replayed(T, V):
             assert torch.equal(x, y), f"replay {k}"
 
 
-@pytest.mark.parametrize("T,V,dtype", [(40, 520, bf), (1000, 7016, bf), (40, 520, f32)])
-def test_one_gradient_alone(T, V, dtype):
+@pytest.mark.parametrize("T,V,d,dtype", [(40, 520, 128, bf), (1000, 7016, 128, bf), (1000, 7016, 1024, bf),
+                                         (40, 520, 128, f32)])
+def test_one_gradient_alone(T, V, d, dtype):
     """A frozen head wants dH only, a probe on frozen states dW only; each is the same bits as together."""
-    H, W, tokens, mask = make_head(T, 128, V, dtype, 61, masked=0.2)
+    H, W, tokens, mask = make_head(T, d, V, dtype, 61, masked=0.2)
     a = [dev(x) for x in (H, W, tokens, mask)]
     g = torch.randn(T, device="cuda")
     _, lse, _, z = kd.token_logp_forward(*a, 1.0, keep_logits=True)
