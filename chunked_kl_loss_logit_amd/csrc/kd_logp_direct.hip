@@ -295,18 +295,33 @@ __global__ __launch_bounds__(256) void logp_direct_dz_from_z_kernel(LogpDirectAr
 }
 
 // ------------------------------------------------------------------ dH
+// How the grid is divided among the row blocks there are: as many vocabulary
+// ranges as it has room for, at least 1 KB of W's rows each.  A range's part
+// holds the row blocks' rows.  (700 valid rows of 777, 1024 x 32000 float32:
+// dH from logits 495 us with as many ranges as suit 777 rows, 464 so; 1024 rows,
+// half of them masked, of 2048 x 8192 259 and 151.)
+struct DirectDh {
+  int nrb, S;
+  long rows;  // of a part
+};
+__device__ inline DirectDh direct_dh(long M, int rows, int nda, int grid, int smax) {
+  const int nrb = M > 0 ? (int)((M + rows - 1) / rows) : 0;
+  return {nrb, max(1, min(nrb > 0 ? grid / (nrb * nda) : 1, smax)), (long)nrb * rows};
+}
+
 // Tile: 128 of d x 32 R rows, vocabulary range s of S over the four waves.
-// S = 1: dH itself; else the range's float32 part [S][C][d].  kTwo: 32 rows,
+// S = 1: dH itself; else the range's float32 part [S][rows][d].  kTwo: 32 rows,
 // the second block column their rests, added at the end.
 template <class E, int R, class O, bool kTwo = false>
-__global__ __launch_bounds__(kDirThreads, 1) void logp_direct_dh_kernel(LogpDirectArgs a, int nda, int S,
+__global__ __launch_bounds__(kDirThreads, 1) void logp_direct_dh_kernel(LogpDirectArgs a, int nda, int smax,
                                                                         float* part, char* dH) {
   constexpr int U = 4;
   __shared__ __attribute__((aligned(16))) float reg[4 * kDirRegion];
   const long M = chunk_rows_of(a.rs);
-  int nrb;
   constexpr int kRows = kTwo ? 32 : 32 * R;
-  int id = row_blocks(M, kRows, nda * S, nrb);
+  const DirectDh sh = direct_dh(M, kRows, nda, gridDim.x, smax);
+  int nrb;
+  int id = row_blocks(M, kRows, nda * sh.S, nrb);
   if (id < 0) return;
   const long r0 = (long)(id % nrb) * kRows;
   id /= nrb;
@@ -321,7 +336,7 @@ __global__ __launch_bounds__(kDirThreads, 1) void logp_direct_dh_kernel(LogpDire
   for (int b = 0; b < R; ++b)
     zl.row(b, a.dz + min(r0 + (kTwo ? m : 32 * b + m), M - 1) * a.ldz * E::kElem + (kTwo && b ? a.lo : 0));
   int kb, ke;
-  k_range((int)a.V, kDirStep<E, U>, 4 * s + wave_id(), 4 * S, kb, ke);
+  k_range((int)a.V, kDirStep<E, U>, 4 * s + wave_id(), 4 * sh.S, kb, ke);
   f32x16_t acc[4][R];
   zero(acc);
   direct_contract<E, U>(wl, zl, kb, ke, acc);
@@ -343,24 +358,26 @@ __global__ __launch_bounds__(kDirThreads, 1) void logp_direct_dh_kernel(LogpDire
     for (int j = 0; j < 4; ++j) {
       const int c = d0 + 4 * q + 32 * j;
       if (c >= d) break;
-      if (S > 1)
-        *reinterpret_cast<float4*>(part + ((long)s * a.rs.C + i) * d + c) = x[j];
+      if (sh.S > 1)
+        *reinterpret_cast<float4*>(part + ((long)s * sh.rows + i) * d + c) = x[j];
       else
         store4<O>(dH + (row_at(a.rs, i) * d + c) * O::kElem, x[j]);
     }
   });
 }
 
-// dH of a row = its S parts in order, four elements per thread
+// dH of a row = its parts in order, four elements per thread
 template <class O>
-__global__ __launch_bounds__(256) void logp_direct_reduce_kernel(RowSet rs, const float* part, int S, long d,
-                                                                 char* dH) {
+__global__ __launch_bounds__(256) void logp_direct_reduce_kernel(RowSet rs, const float* part, int rows, int nda,
+                                                                 int grid, int smax, long d, char* dH) {
   const long q = (long)blockIdx.x * 256 + threadIdx.x, d4 = d / 4;
-  const long i = q / d4, j = (q - i * d4) * 4;
-  if (i >= chunk_rows_of(rs)) return;
+  const long i = q / d4, j = (q - i * d4) * 4, M = chunk_rows_of(rs);
+  if (i >= M) return;
+  const DirectDh sh = direct_dh(M, rows, nda, grid, smax);
+  if (sh.S == 1) return;  // there already
   float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s = 0; s < S; ++s) {
-    const float4 y = *reinterpret_cast<const float4*>(part + ((long)s * rs.C + i) * d + j);
+  for (int s = 0; s < sh.S; ++s) {
+    const float4 y = *reinterpret_cast<const float4*>(part + ((long)s * sh.rows + i) * d + j);
     x.x += y.x;
     x.y += y.y;
     x.z += y.z;
@@ -555,39 +572,36 @@ hipError_t launch_logp_direct_dz_from_z(int elem, const LogpDirectArgs& a, hipSt
   return hipGetLastError();
 }
 
-hipError_t launch_logp_direct_dh(int elem, const LogpDirectArgs& a, int S, float* part, void* dH, int dh_elem,
+hipError_t launch_logp_direct_dh(int elem, const LogpDirectArgs& a, int g, float* part, void* dH, int dh_elem,
                                  hipStream_t st) {
   const int64_t n = rows_upto(a.rs);
-  const int nda = cdiv(a.d, kDirA);
+  const int nda = cdiv(a.d, kDirA), smax = cdiv(a.V * elem, 1024), rows = direct_dh_rows(n);
+  const dim3 grid((unsigned)g), block(kDirThreads);
   char* out = static_cast<char*>(dH);
   auto go = [&](auto r) {
     constexpr int R = decltype(r)::value;
-    const dim3 grid((unsigned)(cdiv(n, 32 * R) * nda * S)), block(kDirThreads);
     if (elem == 4)
-      hipLaunchKernelGGL((logp_direct_dh_kernel<F32, R, F32>), grid, block, 0, st, a, nda, S, part, out);
+      hipLaunchKernelGGL((logp_direct_dh_kernel<F32, R, F32>), grid, block, 0, st, a, nda, smax, part, out);
     else if (dh_elem == 4)
-      hipLaunchKernelGGL((logp_direct_dh_kernel<Bf16, R, F32>), grid, block, 0, st, a, nda, S, part, out);
+      hipLaunchKernelGGL((logp_direct_dh_kernel<Bf16, R, F32>), grid, block, 0, st, a, nda, smax, part, out);
     else
-      hipLaunchKernelGGL((logp_direct_dh_kernel<Bf16, R, Bf16>), grid, block, 0, st, a, nda, S, part, out);
+      hipLaunchKernelGGL((logp_direct_dh_kernel<Bf16, R, Bf16>), grid, block, 0, st, a, nda, smax, part, out);
   };
-  if (a.lo) {
-    const dim3 grid((unsigned)(cdiv(n, 32) * nda * S)), block(kDirThreads);
-    if (dh_elem == 4)
-      hipLaunchKernelGGL((logp_direct_dh_kernel<Bf16, 2, F32, true>), grid, block, 0, st, a, nda, S, part, out);
-    else
-      hipLaunchKernelGGL((logp_direct_dh_kernel<Bf16, 2, Bf16, true>), grid, block, 0, st, a, nda, S, part, out);
-  } else if (n <= 32) {
+  if (a.lo && dh_elem == 4)
+    hipLaunchKernelGGL((logp_direct_dh_kernel<Bf16, 2, F32, true>), grid, block, 0, st, a, nda, smax, part, out);
+  else if (a.lo)
+    hipLaunchKernelGGL((logp_direct_dh_kernel<Bf16, 2, Bf16, true>), grid, block, 0, st, a, nda, smax, part, out);
+  else if (rows == 32)
     go(std::integral_constant<int, 1>());
-  } else {
+  else
     go(std::integral_constant<int, 2>());
-  }
-  if (S > 1) {
-    const dim3 grid((unsigned)cdiv(n * (a.d / 4), 256));
-    if (dh_elem == 2)
-      hipLaunchKernelGGL(logp_direct_reduce_kernel<Bf16>, grid, dim3(256), 0, st, a.rs, part, S, (long)a.d, out);
-    else
-      hipLaunchKernelGGL(logp_direct_reduce_kernel<F32>, grid, dim3(256), 0, st, a.rs, part, S, (long)a.d, out);
-  }
+  const dim3 rgrid((unsigned)cdiv(n * (a.d / 4), 256));
+  if (dh_elem == 2)
+    hipLaunchKernelGGL(logp_direct_reduce_kernel<Bf16>, rgrid, dim3(256), 0, st, a.rs, part, rows, nda, g, smax,
+                       (long)a.d, out);
+  else
+    hipLaunchKernelGGL(logp_direct_reduce_kernel<F32>, rgrid, dim3(256), 0, st, a.rs, part, rows, nda, g, smax,
+                       (long)a.d, out);
   return hipGetLastError();
 }
 

@@ -133,8 +133,10 @@ struct LogpDirectArgs {
 hipError_t launch_logp_direct_fwd(int elem, const LogpDirectArgs& a, bool entropy, hipStream_t st);
 hipError_t launch_logp_direct_dz(int elem, const LogpDirectArgs& a, hipStream_t st);
 hipError_t launch_logp_direct_dz_from_z(int elem, const LogpDirectArgs& a, hipStream_t st);
-// dH of the chunk: dz . W^T, the vocabulary split S ways (part [S][C][d], summed in order; S = 1: not used)
-hipError_t launch_logp_direct_dh(int elem, const LogpDirectArgs& a, int S, float* part, void* dH, int dh_elem,
+// dH of the chunk: dz . W^T by `grid` workgroups, the vocabulary in as many ranges as they leave room for, each into
+// its part (float32, grid / cdiv(d, 128) blocks of direct_dh_rows rows of d), summed in order
+inline int direct_dh_rows(int64_t n) { return n <= 32 ? 32 : 64; }  // rows of a block, of n in the chunk
+hipError_t launch_logp_direct_dh(int elem, const LogpDirectArgs& a, int grid, float* part, void* dH, int dh_elem,
                                  hipStream_t st);
 // dW of the chunk: sum over its rows of Hc^T dz, plus add32 (nullable), to out (float32 or bf16)
 hipError_t launch_logp_direct_dw(int elem, const LogpDirectArgs& a, const void* Hc, const float* add32, void* out,

@@ -45,8 +45,7 @@ struct LogpPlan {
   int ntiles_f, ntiles;  // column tiles of the forward and of the backward's dZ
   int64_t Cf;    // rows per forward chunk
   int64_t C, ldz;  // rows per backward chunk, columns of its dZ
-  int S_dh;      // direct: vocabulary ranges of dH
-  int grid_dh;   // ring: workgroups of dH
+  int grid_dh;  // workgroups of dH
   size_t o_rows, o_count, o_part, o_hp_f, fwd_total;
   size_t o_dz, o_dhp;
   size_t o_hc;        // direct: the chunk's rows of H
@@ -81,12 +80,14 @@ LogpPlan plan_logp(int64_t T, int64_t d, int64_t V, int elem, int dw_elem, int64
   }
   if (p.bwd_direct) {
     p.C = chunk_of(T, V, elem, chunk_rows);
-    const int64_t n = std::min(p.C, T), units = cdiv(n, n <= 32 ? 32 : 64) * cdiv(d, 128);
-    // dH's vocabulary ranges: workgroups for every CU, at least 1 KB of W's rows each
-    p.S_dh = balanced_splits(units, cdiv(V * elem, 1024), std::max<int64_t>(1, cdiv(1024, units)));
+    // dH's workgroups: for every CU, of vocabulary ranges of at least 1 KB of W's rows
+    const int64_t nda = cdiv(d, 128), rows = kd::direct_dh_rows(std::min(p.C, T));
+    const int64_t units = cdiv(std::min(p.C, T), rows) * nda;
+    const int64_t S = balanced_splits(units, cdiv(V * elem, 1024), std::max<int64_t>(1, cdiv(1024, units)));
+    p.grid_dh = (int)up(units * S, 256);
     p.o_dz = bw.take((size_t)p.C * p.ldz * elem);
     p.o_hc = bw.take((size_t)p.C * d * elem);
-    p.o_dhp = bw.take(p.S_dh > 1 ? (size_t)p.S_dh * p.C * d * 4 : 0);
+    p.o_dhp = bw.take((size_t)cdiv(p.grid_dh, nda) * kd::direct_dh_rows(T) * d * 4);
   } else {
     p.C = std::min(chunk_of(T, V + 32 * kd::kDzTailPieces, elem, chunk_rows), ring_rows(dp * elem));
     const int64_t ncb = cdiv(d, 256), units = cdiv(std::min(p.C, T), kd::kTileM) * ncb;
@@ -311,7 +312,7 @@ kd_status logp_bwd(const void* H, const void* W, const int32_t* tokens, const ui
       }
       if (dH)
         KD_LAUNCH("logp_direct_dh", st,
-                  kd::launch_logp_direct_dh(elem, a, p.S_dh, at<float>(workspace, p.o_dhp), dH, dh_elem, st));
+                  kd::launch_logp_direct_dh(elem, a, p.grid_dh, at<float>(workspace, p.o_dhp), dH, dh_elem, st));
       if (!dW) continue;
       // a float32 dW adds up in place; a bf16 one in the workspace, rounded with the last chunk
       const bool f32 = dw_dtype == KD_F32, last = c0 + p.C >= T;
