@@ -13,7 +13,7 @@
 // operands).  Measured: forward of 7 rows of 2048 x 32000 bf16 22 us (6.0 TB/s
 // of W, half of it from the last-level cache), its dW 34 us (3.9 TB/s written);
 // 700 rows of 1024 x 32000 float32, of the 152 TFLOP/s that a large product
-// reaches: forward with kept logits 459 us (100 TFLOP/s), dH 470 (98), dW 373
+// reaches: forward with kept logits 458 us (100 TFLOP/s), dH 427 (107), dW 373
 // (123); dZ from the logits 34 us (5.3 TB/s).
 #include <type_traits>
 
