@@ -26,6 +26,14 @@ bool direct_fwd(int64_t T, int64_t d, int64_t V, int elem) {
   return std::min(T, C) * V < rounds * 7000000;
 }
 
+// The most rows of row_bytes each, in whole 256-row tiles, that the ring's
+// 32-bit offsets reach; 0 where not even one tile's.
+int64_t ring_rows(int64_t row_bytes) { return ((int64_t(1) << 32) - 65537) / row_bytes / 256 * 256; }
+
+// Columns of dZ, and what a row of the ring's dZ panels takes with the tail pieces.
+int64_t ldz_of(int64_t V) { return cdiv(V, kd::kTileN) * kd::kTileN; }
+int64_t ring_dz_bytes(int64_t V) { return (ldz_of(V) + 32 * kd::kDzTailPieces) * 2; }
+
 // The same for the backward, whose products the ring splits better (dH over
 // the vocabulary) but pays more launches for: up to 64 rows, and products of
 // fewer than 7e9 terms.  Backward, us, recomputing / from kept logits, ring
@@ -35,7 +43,7 @@ bool direct_fwd(int64_t T, int64_t d, int64_t V, int elem) {
 // / 137; 512 x 4096 x 8192 187 / 114, 213 / 163.
 bool direct_bwd(int64_t T, int64_t d, int64_t V, int elem) {
   const int64_t C = chunk_of(T, V, elem, 0);
-  if (!kd::logp_ring_fits(elem, C, d, V)) return true;
+  if (!kd::logp_ring_fits(elem, C, d, V) || ring_rows(ring_dz_bytes(V)) == 0) return true;
   const int64_t n = std::min(T, C);
   return n <= 64 || (double)n * d * V < 7e9;
 }
@@ -53,9 +61,14 @@ struct LogpPlan {
   size_t o_dw32, total;  // float32 dW where a bf16 one adds up over chunks
 };
 
-// The most rows of a ring chunk, however many are asked for: H's panels keep
-// to the ring's 32-bit reach.  (At least the default chunk's rows: logp_ring_fits.)
-int64_t ring_rows(int64_t row_bytes) { return ((int64_t(1) << 32) - 65537) / row_bytes / 256 * 256; }
+// Rows of a ring chunk, however many are asked for: H's panels (dp columns; at
+// least the default chunk's rows, logp_ring_fits) and dZ's with the tail pieces
+// keep to the ring's reach, dZ's cap in whole default chunks as chunk_of's is.
+int64_t ring_chunk(int64_t T, int64_t V, int64_t dp, int64_t chunk_rows) {
+  int64_t most = ring_rows(ring_dz_bytes(V));
+  if (most >= KD_DEFAULT_CHUNK_ROWS) most = most / KD_DEFAULT_CHUNK_ROWS * KD_DEFAULT_CHUNK_ROWS;
+  return std::min({chunk_of(T, V + 32 * kd::kDzTailPieces, 2, chunk_rows), ring_rows(dp * 2), most});
+}
 
 LogpPlan plan_logp(int64_t T, int64_t d, int64_t V, int elem, int dw_elem, int64_t chunk_rows) {
   LogpPlan p{};
@@ -64,14 +77,12 @@ LogpPlan plan_logp(int64_t T, int64_t d, int64_t V, int elem, int dw_elem, int64
   p.ntiles_f = (int)cdiv(V, p.fwd_direct ? kd::kDirectCols : kd::kTileN);
   p.ntiles = (int)cdiv(V, kd::kTileN);
   p.Cf = chunk_of(T, V, elem, 0);
-  p.ldz = cdiv(V, kd::kTileN) * kd::kTileN;
+  p.ldz = ldz_of(V);
   Carver cv;
   p.o_rows = cv.take((size_t)T * 4);
   p.o_count = cv.take(16);
   Carver fw = cv, bw = cv;  // the two calls' buffers overlap
-  // the ring's H panels run to whole ring turns of d; dZ's hold the tail pieces
-  // too, within the same 32-bit reach
-  const int64_t dp = cdiv(d, 128) * 128;
+  const int64_t dp = cdiv(d, 128) * 128;  // the ring's H panels run to whole ring turns of d
   if (p.fwd_direct) {
     p.o_part = fw.take((size_t)p.ntiles_f * p.Cf * 16);
   } else {
@@ -89,10 +100,10 @@ LogpPlan plan_logp(int64_t T, int64_t d, int64_t V, int elem, int dw_elem, int64
     p.o_hc = bw.take((size_t)p.C * d * elem);
     p.o_dhp = bw.take((size_t)cdiv(p.grid_dh, nda) * kd::direct_dh_rows(T) * d * 4);
   } else {
-    p.C = std::min(chunk_of(T, V + 32 * kd::kDzTailPieces, elem, chunk_rows), ring_rows(dp * elem));
+    p.C = ring_chunk(T, V, dp, chunk_rows);
     const int64_t ncb = cdiv(d, 256), units = cdiv(std::min(p.C, T), kd::kTileM) * ncb;
     p.grid_dh = (int)up(units * balanced_splits(units, cdiv(V, 128), std::max<int64_t>(1, cdiv(1024, units))), 256);
-    p.o_dz = bw.take((size_t)p.C * (p.ldz + 32 * kd::kDzTailPieces) * elem);
+    p.o_dz = bw.take((size_t)p.C * ring_dz_bytes(V));
     p.o_hT = bw.take((size_t)d * p.C * elem);
     p.o_dhp = bw.take((size_t)cdiv(p.grid_dh, ncb) * 256 * d * 4);
     p.o_hp = bw.take(panel_bytes(p.C, dp * elem));
@@ -412,7 +423,7 @@ kd_status kd_token_logp_logits_size(int64_t T, int64_t V, size_t* bytes) {
   g_err.clear();
   KD_TRY(need(bytes, "bytes"));
   KD_TRY(check_widths(T, 8, V, KD_F32, 1.0f));
-  *bytes = (size_t)T * (size_t)(cdiv(V, kd::kTileN) * kd::kTileN) * 4;
+  *bytes = (size_t)T * (size_t)ldz_of(V) * 4;
   return KD_OK;
 }
 

@@ -1,0 +1,68 @@
+"""Sizes next to the limits of the policy operators' plans, on the CPU: what the library reports for a shape tells how
+many rows a chunk has."""
+import ctypes
+import os
+import sys
+
+import pytest
+
+kd = pytest.importorskip("chunked_kl_loss_logit_amd")
+B = kd._policy_binding
+BF16, F32 = 1, 0
+REACH = (1 << 32) - 65537  # bytes that 32-bit offsets span, less what one load may reach beyond
+
+
+@pytest.fixture(scope="module")
+def L():
+    if not os.path.exists(kd.LIB_PATH):
+        pytest.fail("libkdloss.so is not built (run __graft_entry__.build())")
+    return B.plib()
+
+
+def size(L, T, d, V, chunk, dt=BF16, dw=F32):
+    out = ctypes.c_size_t()
+    assert L.kd_token_logp_workspace_size(T, d, V, dt, dw, chunk, ctypes.byref(out)) == 0
+    return out.value
+
+
+def most_rows(L, T, d, V):
+    """The rows of the largest chunk: the smallest chunk_rows that is given what any larger one is."""
+    top = size(L, T, d, V, T)
+    lo, hi = 1, T // 256  # in 256 rows
+    while lo < hi:
+        mid = (lo + hi) // 2
+        if size(L, T, d, V, 256 * mid) == top:
+            hi = mid
+        else:
+            lo = mid + 1
+    return 256 * lo
+
+
+def in_reach(rows, V):
+    """dZ's columns in whole tiles, then four pieces of 32 for its tail and the zeros behind it, 2 bytes each."""
+    return rows * (-(-V // 256) * 256 + 128) * 2 <= REACH
+
+
+@pytest.mark.parametrize("d,V", [(64, 47368), (1024, 87048), (2048, 87048), (64, 37128), (256, 23560), (256, 22536),
+                                 (1024, 1198088), (1024, 1397768), (64, 47360), (64, 47104), (2048, 2056)])
+def test_dz_panels_keep_to_32_bits(L, d, V):
+    rows = most_rows(L, 1 << 20, d, V)
+    assert in_reach(rows, V), f"{rows} rows of {V}"
+
+
+def test_dz_panels_keep_to_32_bits_everywhere(L):
+    """Vocabularies whose last tile leaves the tail pieces no room of its own, and others beside them."""
+    for V in list(range(8 * 1024, 300000, 1016)) + [256 * k + r for k in range(40, 1200, 7) for r in (8, 32, 128, 136, 248)]:
+        rows = most_rows(L, 1 << 18, 512, V)
+        assert in_reach(rows, V), f"{rows} rows of {V}"
+
+
+def test_a_row_tile_too_large_for_the_ring(L):
+    """256 rows of 16 M columns are 8 GB of dZ, beyond 32-bit offsets whatever the chunk: the register-fed tiles take
+    them, with little beside dZ (the ring would keep 8 MB of dH parts)."""
+    V = 1 << 24
+    a, b = size(L, 128, 32, V, 256), size(L, 128, 32, V, 256, dw=BF16)
+    assert a == b  # one chunk: a bf16 dW needs no float32 buffer
+    dz = 256 * V * 2
+    assert dz <= a < dz + (4 << 20)
+    assert size(L, 300, 32, V, 0) < dz + (4 << 20)
