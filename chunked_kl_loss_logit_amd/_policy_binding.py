@@ -359,11 +359,20 @@ def _dense(t):
     return True
 
 
+def _writable(name, tensors):
+    """Refuses what a write past autograd would falsify: parameters (it is their gradients that are clipped), and in
+    grad mode every tensor that autograd follows."""
+    for t in tensors:
+        if t.requires_grad and (t.is_leaf or torch.is_grad_enabled()):
+            raise ValueError(f"{name} must not require a gradient where they are written to: pass the parameters' .grad "
+                             "(a tensor whose own values are meant: its .detach())")
+
+
 class TensorTable:
     """Host arrays of pointers, element counts and types of a list of tensors on one device.  One pass per attribute:
-    a few hundred tensors are checked in less time than their kernels take."""
+    a few hundred tensors are checked in less time than their kernels take.  written: they are to be written to."""
 
-    def __init__(self, name, tensors):
+    def __init__(self, name, tensors, written=False):
         try:
             types = [GRAD_TYPES[t.dtype] for t in tensors]
         except (KeyError, AttributeError):
@@ -373,6 +382,8 @@ class TensorTable:
                 if t.dtype not in GRAD_TYPES:
                     raise TypeError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}") from None
             raise
+        if written and any([t.requires_grad for t in tensors]):
+            _writable(name, tensors)
         devices = {t.get_device() for t in tensors}
         if -1 in devices:
             raise ValueError("libkdloss tensors must be on the GPU")

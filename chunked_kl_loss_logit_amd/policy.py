@@ -296,13 +296,14 @@ def clip_grad_norm(tensors, max_norm, out=None, sumsq=None):
     """Writes tensors[i] * min(1, max_norm / (norm + 1e-6)) to out[i] (the same number of elements in the same order
     in memory; float32, bfloat16 or float16) and returns the global L2 norm, one float32 on the device.  out = None: in
     place, and None entries among the tensors are left out.  sumsq: the squared norm, if it is not that of these
-    tensors alone."""
+    tensors alone.  The tensors are the gradients themselves: what is written to may not be a parameter (a leaf that
+    requires a gradient), nor in grad mode any tensor that requires one."""
     if not isinstance(tensors, torch.Tensor):
         tensors = list(tensors)
     kept = _tensors(tensors)
-    table = outs = B.TensorTable("tensors", kept)
+    table = outs = B.TensorTable("tensors", kept, written=out is None)
     if out is not None:
-        outs = B.TensorTable("out", [out] if isinstance(out, torch.Tensor) else list(out))
+        outs = B.TensorTable("out", [out] if isinstance(out, torch.Tensor) else list(out), written=True)
         if not isinstance(tensors, torch.Tensor) and len(kept) != len(tensors):
             raise ValueError("with out, no tensor may be None")
     device = kept[0].device
@@ -316,5 +317,5 @@ def clip_grad_norm(tensors, max_norm, out=None, sumsq=None):
 
 
 def clip_grad_norm_(tensors, max_norm, sumsq=None):
-    """clip_grad_norm in place."""
+    """clip_grad_norm in place, on the gradients (p.grad), not on the parameters that have them."""
     return clip_grad_norm(tensors, max_norm, None, sumsq)

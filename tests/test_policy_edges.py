@@ -34,3 +34,17 @@ def test_the_largest_chunk_of_an_odd_vocabulary():
     moved = (u + 4 * (2 * off + 2.0 ** -20 * (1 + l64.abs())) + 2.0 ** -18) * sized
     bound = moved + V * U32 * sized + u * (want.abs() + moved)
     assert ((dH[at].double() - want).abs() <= bound).all()
+
+
+def test_parameters_are_not_clipped():
+    """Their gradients are what is clipped; the weights stay as they were."""
+    p = torch.nn.Parameter(torch.full((1000,), 3.0, device="cuda"))
+    for call in (lambda: kd.clip_grad_norm_([p], 1.0), lambda: kd.clip_grad_norm([torch.ones_like(p)], 1.0, out=[p])):
+        with pytest.raises(ValueError, match=r"\.grad"):
+            call()
+    p.grad = torch.full((1000,), 2.0, device="cuda")
+    norm = kd.clip_grad_norm_([p.grad], 1.0)
+    assert (p == 3.0).all() and abs(float(norm) - 2 * 1000 ** 0.5) < 1e-3 and abs(float(p.grad.norm()) - 1) < 1e-5
+    kd.clip_grad_norm_([p.detach()], 1.0)
+    assert abs(float(p.detach().norm()) - 1) < 1e-5
+    assert abs(float(kd.clip_grad_norm([p], 0.5, out=[torch.empty(1000, device="cuda")])) - 1) < 1e-5

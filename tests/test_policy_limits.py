@@ -5,6 +5,7 @@ import os
 import sys
 
 import pytest
+import torch
 
 kd = pytest.importorskip("chunked_kl_loss_logit_amd")
 B = kd._policy_binding
@@ -66,3 +67,26 @@ def test_a_row_tile_too_large_for_the_ring(L):
     dz = 256 * V * 2
     assert dz <= a < dz + (4 << 20)
     assert size(L, 300, 32, V, 0) < dz + (4 << 20)
+
+
+@pytest.mark.parametrize("call", [lambda p: kd.clip_grad_norm_([p], 1.0), lambda p: kd.clip_grad_norm_(iter([p]), 1.0),
+                                  lambda p: kd.clip_grad_norm_(p, 1.0),
+                                  lambda p: kd.clip_grad_norm_([torch.ones(3), p], 1.0)])
+def test_parameters_are_not_clipped(call):
+    """Refused before anything is looked up on a device, in and out of grad mode."""
+    p = torch.nn.Parameter(torch.full((3,), 5.0))
+    with pytest.raises(ValueError, match=r"\.grad"):
+        call(p)
+    with torch.no_grad(), pytest.raises(ValueError, match=r"\.grad"):
+        call(p)
+    assert (p == 5.0).all()
+
+
+def test_what_autograd_follows_is_not_clipped_in_grad_mode():
+    x = torch.ones(3, requires_grad=True) * 2
+    with pytest.raises(ValueError, match="must not require a gradient"):
+        kd.clip_grad_norm_([x], 1.0)
+    with torch.no_grad(), pytest.raises(ValueError, match="on the GPU"):  # accepted so far
+        kd.clip_grad_norm_([x], 1.0)
+    with pytest.raises(ValueError, match="on the GPU"):  # only read
+        kd.clip_grad_norm([x], 1.0, out=[torch.ones(3)])
