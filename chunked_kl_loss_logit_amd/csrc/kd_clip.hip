@@ -227,8 +227,8 @@ __global__ __launch_bounds__(kClipThreads) void clip_kernel(ClipTable t, const d
   scale_of<kClipThreads>(t.in_type[i], t.out_type[i], t.in[i], t.out[i], b, e, c);
 }
 
-// Few elements: norm and clip by one workgroup (three launches would take
-// three times as long as the work).
+// Few elements in few tensors: norm and clip by one workgroup, the tensors one
+// after the other (both sides of the rule at kClipSmallTensors).
 __global__ __launch_bounds__(1024) void clip_small_kernel(ClipTable t, double* sumsq, double max_norm, float* norm) {
   double s = 0;
   for (int i = 0; i < t.n; ++i) s += sumsq_of<1024>(t.in_type[i], t.in[i], 0, t.numel[i]);

@@ -973,9 +973,12 @@ kd_status kd_grad_clip_norm(const void* const* grads, const int64_t* numel, cons
   KD_TRY(check_clip(grads, numel, dtypes, n, outs, out_dtypes, sumsq, max_norm, norm, &blocks));
   KD_TRY(check_workspace(workspace, workspace_bytes, up((size_t)blocks * 8, kAlign)));
   hipStream_t st = static_cast<hipStream_t>(stream);
-  int64_t total = 0;
-  for (int64_t i = 0; i < n; ++i) total += numel[i];  // below 2^46: check_counts bounds the blocks
-  if (blocks > 0 && n <= kd::ClipTable::kTensors && total <= kd::kClipSmall)
+  int64_t total = 0, some = 0;
+  for (int64_t i = 0; i < n; ++i) {
+    total += numel[i];  // below 2^46: check_counts bounds the blocks
+    some += numel[i] > 0;
+  }
+  if (blocks > 0 && some <= kd::kClipSmallTensors && total <= kd::kClipSmall)
     return over_tables<kd::ClipTable>(
         numel, n, [&](kd::ClipTable& t, int k, int64_t i) { set_clip(t, k, grads, dtypes, outs, out_dtypes, i); },
         [&](const kd::ClipTable& t, int64_t) {

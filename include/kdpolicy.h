@@ -207,7 +207,7 @@ kd_status kd_grad_clip(const void* const* grads, const int64_t* numel, const int
                        float* norm, void* stream);
 
 /* Both at once, over the same tensors: sumsq and norm as above.  Up to 2^16
- * elements in at most 132 tensors are one launch. */
+ * elements in at most 8 tensors that have any are one launch. */
 kd_status kd_grad_clip_norm(const void* const* grads, const int64_t* numel, const int32_t* dtypes, int64_t n,
                             void* const* outs, const int32_t* out_dtypes, double max_norm, double* sumsq,
                             float* norm, void* workspace, size_t workspace_bytes, void* stream);
