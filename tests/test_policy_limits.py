@@ -90,3 +90,20 @@ def test_what_autograd_follows_is_not_clipped_in_grad_mode():
         kd.clip_grad_norm_([x], 1.0)
     with pytest.raises(ValueError, match="on the GPU"):  # only read
         kd.clip_grad_norm([x], 1.0, out=[torch.ones(3)])
+
+
+@pytest.mark.parametrize("chunk", [2 ** 63 - 1, 2 ** 63 - 254, 2 ** 63 - 255, 2 ** 63 - 256, 2 ** 62, 1000])
+@pytest.mark.parametrize("dt", [BF16, F32])
+def test_any_number_of_chunk_rows_is_cut_to_the_rows_present(L, chunk, dt):
+    """The largest numbers round up to beyond 63 bits."""
+    for T, d, V in ((1000, 1024, 7016), (1000, 256, 1032), (1, 64, 64)):
+        assert size(L, T, d, V, chunk, dt) == size(L, T, d, V, 1024, dt)
+    sizes = [("kd_topk_kl_workspace_size", (1000, 1024, 7016, 16, dt)), ("kd_topk_kl_fwd_bwd_workspace_size", (1000, 1024, 7016, 16, dt)),
+             ("kd_full_kl_workspace_size", (1000, 1024, 256, 7016, dt)), ("kd_full_kl_fwd_bwd_workspace_size", (1000, 1024, 256, 7016, dt))]
+    for fn, args in sizes:
+        got = []
+        for c in (chunk, 1024):
+            out = ctypes.c_size_t()
+            assert getattr(L, fn)(*args, c, ctypes.byref(out)) == 0
+            got.append(out.value)
+        assert got[0] == got[1], fn
