@@ -89,7 +89,7 @@ __device__ inline void merge(float& m, float& l, float& e, float om, float ol, f
   const float d = m - M, od = om - M;
   const float f = m == -INFINITY ? 0.f : fast_exp2(d), of = om == -INFINITY ? 0.f : fast_exp2(od);
   if constexpr (kEnt)
-    e = (m == -INFINITY ? 0.f : f * fmaf(d, l, e)) + (om == -INFINITY ? 0.f : of * fmaf(od, ol, oe));
+    e = (m == -INFINITY ? 0.f : f * fmaf(at_least(d), l, e)) + (om == -INFINITY ? 0.f : of * fmaf(at_least(od), ol, oe));
   l = l * f + ol * of;
   m = M;
 }
@@ -110,24 +110,25 @@ __device__ inline void fwd_row(const f32x16_t (&v)[4], float c2, float* st, int 
   for (int nb = 0; nb < 4; ++nb)
 #pragma unroll
     for (int i = 0; i < 16; ++i) cm = in(nb, i) ? fmaxf(cm, v[nb][i]) : cm;
-  const float cmy = cm * c2;
+  const float cmy = top_of(cm, c2);
   float e = 0.f;
   if constexpr (kEnt) e = st[128];
   if (cmy > m) {
     const float f = fast_exp2(m - cmy);  // 2^(-inf) = 0 while nothing is summed yet
-    if constexpr (kEnt) e = l == 0.f ? 0.f : f * fmaf(m - cmy, l, e);
+    if constexpr (kEnt) e = l == 0.f ? 0.f : f * fmaf(at_least(m - cmy), l, e);
     l *= f;
     m = cmy;
   }
   float sum = 0.f, es = 0.f;
+  const float from = subtrahend(m);
 #pragma unroll
   for (int nb = 0; nb < 4; ++nb)
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      const float w = in(nb, i) ? fmaf(v[nb][i], c2, -m) : -1e30f;
+      const float w = in(nb, i) ? fmaf(v[nb][i], c2, -from) : -256.f;
       const float p = fast_exp2(w);
       sum += p;
-      if constexpr (kEnt) es = fmaf(p, w, es);
+      if constexpr (kEnt) es = fmaf(p, at_least(w), es);
     }
   st[0] = m;
   st[64] = l + sum;
@@ -289,7 +290,7 @@ __device__ inline float4 merge_records(const float4* pp, int S, long stride) {
     const float4 q = pp[s * stride];
     const float dm = q.x - M, f = exp2f(dm);
     l = fmaf(q.y, f, l);
-    if (q.x != -INFINITY) e = fmaf(f, fmaf(dm, q.y, q.z), e);
+    if (q.x != -INFINITY) e = fmaf(f, fmaf(at_least(dm), q.y, q.z), e);
     x += q.w;
   }
   return make_float4(M, l, e, x);
@@ -297,9 +298,12 @@ __device__ inline float4 merge_records(const float4* pp, int S, long stride) {
 
 // logp = ln2 ((y at the token - m) - log2 l): the maximum goes out first, so
 // only the small log2 l is subtracted from the row's distance to its maximum.
+// (In halves: in base 2 the log-probability of a column masked by the type's
+// lowest value passes the 32-bit range, in base e it does not.)  A row of
+// nothing but columns below the 32-bit range (l = 0) is NaN.
 __device__ inline void finish_row(long t, const float4 r, float c2, const LogpOut& o) {
-  const float ll = log2f(r.y);
-  o.logp[t] = kLn2 * (fmaf(r.w, c2, -r.x) - ll);
+  const float ll = r.y > 0.f ? log2f(r.y) : NAN;
+  o.logp[t] = 2.f * kLn2 * (fmaf(0.5f * r.w, c2, -0.5f * r.x) - 0.5f * ll);
   o.lse[t] = kLn2 * (r.x + ll);
   if (o.entropy) o.entropy[t] = kLn2 * (ll - r.z / r.y);
 }
@@ -413,7 +417,7 @@ template <bool kEnt>
 __device__ inline float dz_value(float z, const float4 k, float c2) {
   const float lq = fmaf(z, c2, -k.x);
   const float q = fast_exp2(lq);
-  if constexpr (kEnt) return -q * fmaf(k.z, lq, k.y);
+  if constexpr (kEnt) return -q * fmaf(k.z, at_least(lq), k.y);
   return -q * k.y;
 }
 

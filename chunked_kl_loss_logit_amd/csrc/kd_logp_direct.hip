@@ -130,16 +130,17 @@ __device__ __forceinline__ void fwd_tile(const LogpDirectArgs& a, long M, long r
       mx = fmaxf(mx, fmaxf(fmaxf(z[j].x, z[j].y), fmaxf(z[j].z, z[j].w)));
       if ((label[b] >> 2) == q + 8 * j) x = at4(z[j], label[b] & 3);
     }
-    mx = row_max(mx) * a.c2;
+    mx = top_of(row_max(mx), a.c2);
+    const float from = subtrahend(mx);
     float l = 0.f, e = 0.f;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       if (4 * q + 32 * j >= cols) continue;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const float w = fmaf(at4(z[j], k), a.c2, -mx), p = fast_exp2(w);
+        const float w = fmaf(at4(z[j], k), a.c2, -from), p = fast_exp2(w);
         l += p;
-        if constexpr (kEnt) e = fmaf(p, w, e);
+        if constexpr (kEnt) e = fmaf(p, at_least(w), e);
       }
     }
     l = row_sum(l);
@@ -167,7 +168,7 @@ namespace {
 template <bool kEnt>
 __device__ inline float dz_of(float z, float c2, float L2, float A, float B) {
   const float lq = fmaf(z, c2, -L2), q = fast_exp2(lq);
-  if constexpr (kEnt) return -q * fmaf(B, lq, A);
+  if constexpr (kEnt) return -q * fmaf(B, at_least(lq), A);
   return -q * A;
 }
 

@@ -32,9 +32,28 @@ __host__ __device__ inline int ring_splits(int64_t M, int ntiles, int grid) {
   return s > 1 ? (int)s : 1;
 }
 
+// What a base-2 logit relative to another (an exponent, or the factor of a term
+// whose 2^x is 0 there) counts as at least: 2^-256 is 0 in 32 bits, and the
+// product of such a 2^x with a column masked by the type's lowest value, whose
+// difference passes the 32-bit range, would be 0 times infinity.  (A NaN difference
+// stays visible: its 2^x is taken from the value itself.)
+__device__ inline float at_least(float x) { return fmaxf(x, -256.f); }
+// z c2 of a tile's largest z, which differences are taken from.  Where rounding
+// it down leaves more than 1 (beyond 2^24), a step up, so that no difference
+// passes 1: a tile of masked columns alone, at -1e30 say, would have sums of
+// infinity, which no later maximum scales away.
+__device__ inline float top_of(float z, float c2) {
+  const float m = z * c2, rest = fmaf(z, c2, -m);  // infinite where m is
+  return rest > 1.f && rest < INFINITY ? fmaf(fabsf(m), 0x1p-23f, m) : m;
+}
+// What is subtracted for a maximum m: below the 32-bit range it is -infinity,
+// and there every 2^y is 0.
+__device__ inline float subtrahend(float m) { return m == -INFINITY ? 0.f : m; }
+
 // One record per (vocabulary split, row): with y = z log2(e) / tau over the
 // split's columns, (m, l, e, x) = (max y, sum 2^(y - m), sum 2^(y - m) (y - m),
-// z at the row's token or 0).
+// z at the row's token or 0); (-infinity, 0, 0, x) where every y is below the
+// 32-bit range.
 struct LogpFwdArgs {
   const char* Hp;         // rows [c0, c0 + C) of H in panels of C rows
   const char* W;          // [d][V]

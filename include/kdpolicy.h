@@ -40,7 +40,11 @@ extern "C" {
  * must be below 2^25 (KD_ERR_UNSUPPORTED).
  * Masked rows get logp = lse = entropy = 0 and dH = 0, add nothing to dW and
  * are never read beyond mask[t].  A token of a valid row outside [0, V) gives
- * logp = NaN; its dZ has no token term.
+ * logp = NaN; its dZ has no token term.  Columns masked by large negative
+ * logits, down to the type's lowest value (in a row of W that every hidden
+ * state meets with 1, say), have probability 0 and add nothing; a row with
+ * nothing but such columns may be NaN.  A NaN or infinite logit makes its
+ * row's results NaN.
  */
 
 /* Bytes of the optional buffer `logits` in which the forward call leaves the
@@ -77,8 +81,10 @@ kd_status kd_token_logp_bwd(const void* H, const void* W, const int32_t* tokens,
  * (optional) entropy on every rank; each rank's backward, with those, gives
  * its columns of dW and a float32 partial of dH [T,d] to be summed over the
  * ranks.  rec = (m, l, e, x): with y = s log2(e) over the shard's columns
- * m = max y, l = sum 2^(y - m), e = sum 2^(y - m) (y - m), and x the raw logit
- * at the token, or 0 in the shards that do not hold it.  A token that no
+ * m = max y (-infinity, with l = e = 0, where all are below the 32-bit range;
+ * beyond 2^24 in size at most two steps above), l = sum 2^(y - m), e = sum
+ * 2^(y - m) (y - m), and x the raw logit at the token, or 0 in the shards that
+ * do not hold it.  A token that no
  * shard holds is not told from one whose logit is 0. */
 kd_status kd_token_logp_fwd_shard(const void* H, const void* W, const int32_t* tokens, const uint8_t* mask, float tau,
                                   int64_t T, int64_t d, int64_t V, int64_t v0, kd_dtype dt, float* rec, float* logits,

@@ -6,7 +6,7 @@ import torch
 
 import chunked_kl_loss_logit_amd as kd
 from tests.gpu_util import dev, say
-from tests.policy_util import U32, half_step, make_head
+from tests.policy_util import U32, half_step, logp_reference, make_head, within
 
 pytestmark = pytest.mark.gpu
 bf, f32 = torch.bfloat16, torch.float32
@@ -93,3 +93,103 @@ def test_one_launch_and_three_agree(count, empty):
     for t, o in zip(ts, outs):
         w = t.double() * (0.5 * want / (want + 1e-6))
         assert ((o.double() - w).abs() <= 5 * U32 * w.abs()).all()
+
+
+def masked_head(T, d, V, dtype, blocked, value, seed, masked=0.0):
+    """A head with columns masked through its last row, which every hidden state meets with 1: logits of `value` there,
+    and the same head without those columns."""
+    H, W, tokens, mask = make_head(T, d, V, dtype, seed, masked=masked)
+    keep = torch.ones(V, dtype=torch.bool)
+    for a, b in blocked:
+        keep[a:b] = False
+    H[:, -1] = 1
+    W[-1] = 0
+    W[:, ~keep] = 0
+    W[-1, ~keep] = value
+    to = torch.cumsum(keep, 0) - 1  # place among the columns that stay
+    allowed = torch.nonzero(keep)[:, 0]
+    tokens = allowed[tokens.long() % allowed.numel()].to(torch.int32)
+    return H, W, tokens, mask, keep, W[:, keep].contiguous(), to[tokens.long()].to(torch.int32)
+
+
+# the register-fed tiles, then the forward and everything on the ring tiles
+MASKED_HEADS = [(5, 128, 1024, bf), (90, 128, 1032, bf), (40, 72, 520, f32), (1000, 160, 7016, bf), (1000, 1056, 7016, bf)]
+
+
+@pytest.mark.parametrize("T,d,V,dtype", MASKED_HEADS)
+@pytest.mark.parametrize("value", [-1e4, -3.7e9, -1e38, None])
+@pytest.mark.parametrize("blocks", ["one", "tiles", "first", "last"])
+def test_masked_columns(T, d, V, dtype, value, blocks):
+    """A vocabulary partly masked by large negative logits, down to the type's lowest value: such columns have
+    probability 0 and add nothing, also where a whole tile of them comes first."""
+    value = torch.finfo(dtype).min if value is None else value
+    blocked = dict(one=[(7, 8)], tiles=[(128, 512)], first=[(0, 264)], last=[(V - 200, V)])[blocks]
+    say(f"masked columns T={T} d={d} V={V} {dtype} {value} {blocked}")
+    H, W, tokens, mask, keep, Wk, tk = masked_head(T, d, V, dtype, blocked, value, 53, masked=0.2 if T > 5 else 0.0)
+    gen = torch.Generator().manual_seed(54)
+    g, ge = torch.randn(T, generator=gen), torch.randn(T, generator=gen)
+    want, bound = logp_reference(H, Wk, tk, mask, 1.0, g, ge)
+    a = [dev(x) for x in (H, W, tokens, mask)]
+    logp, lse, ent, z = kd.token_logp_forward(*a, 1.0, want_entropy=True, keep_logits=True)
+    for name, got in (("logp", logp), ("lse", lse), ("entropy", ent)):
+        within(got, want[name], bound[name], name)
+    for zz in (None, z):
+        dH, dW = kd.token_logp_backward(*a, 1.0, lse, dev(g), ent, dev(ge), zz)
+        within(dH, want["dH"], bound["dH"], "dH")
+        within(dW.cpu()[:, keep], want["dW"], bound["dW"], "dW")
+        assert (dW.cpu()[:, ~keep] == 0).all()
+
+
+@pytest.mark.parametrize("T,d,V,dtype", MASKED_HEADS[1:4])
+def test_masked_columns_of_any_size(T, d, V, dtype):
+    """Whichever way the largest logit of a masked tile rounds in base 2."""
+    H, W, tokens, _, keep, Wk, tk = masked_head(T, d, V, dtype, [(0, 264)], 0.0, 59)
+    want, bound = logp_reference(H, Wk, tk, None, 1.0)
+    h, w, t = dev(H), dev(W), dev(tokens)
+    gen = torch.Generator().manual_seed(60)
+    for value in (-10 ** (3 + 35.5 * torch.rand(24, generator=gen))).tolist():
+        w[-1, :264] = value * (1 + 0.1 * torch.rand(264, generator=gen)).cuda()
+        for tau in (1.0, 0.4):
+            logp, lse, ent, _ = kd.token_logp_forward(h, w, t, None, tau, want_entropy=True)
+            if tau == 1.0:
+                for name, got in (("logp", logp), ("lse", lse), ("entropy", ent)):
+                    within(got, want[name], bound[name], f"{name} at {value}")
+            assert torch.isfinite(logp).all() and torch.isfinite(ent).all(), value
+
+
+def test_a_masked_shard_and_a_masked_token():
+    T, d, V = 30, 128, 1024
+    H, W, tokens, _, keep, Wk, tk = masked_head(T, d, V, bf, [(0, 512)], torch.finfo(bf).min, 55)
+    want, bound = logp_reference(H, Wk, tk, None, 1.0)
+    h, t = dev(H), dev(tokens)
+    recs = [kd.token_logp_shard_forward(h, dev(W[:, a:a + 512].contiguous()), a, t)[0] for a in (0, 512)]
+    logp, lse, ent = kd.token_logp_shard_combine(recs, want_entropy=True)
+    for name, got in (("logp", logp), ("lse", lse), ("entropy", ent)):
+        within(got, want[name], bound[name], name)
+    tokens[3] = 9  # masked: log-probability -3.39e38, which 32 bits hold
+    logp = kd.token_logp_forward(h, dev(W), dev(tokens))[0].cpu()
+    assert abs(float(logp[3]) / float(torch.finfo(bf).min) - 1) < 1e-6
+    W[-1] = torch.finfo(bf).min  # every column: below what 32 bits hold in base 2, NaN rather than a wrong number
+    H[:, :-1] = 0
+    logp, lse, ent, _ = kd.token_logp_forward(dev(H), dev(W), t, want_entropy=True)
+    assert torch.isnan(logp).all() and torch.isnan(lse).all() and torch.isnan(ent).all()
+
+
+@pytest.mark.parametrize("T,d,V,dtype", MASKED_HEADS)
+def test_nan_and_infinite_logits_stay_visible(T, d, V, dtype):
+    """A row whose hidden state is NaN, or overflows, is NaN in all it gives; the others are as they were."""
+    H, W, tokens, _ = make_head(T, d, V, dtype, 57)
+    a = (dev(W), dev(tokens), None)
+    clean = kd.token_logp_forward(dev(H), *a, 1.0, want_entropy=True)[:3]
+    H[1, 0], H[3, :] = float("nan"), 3e38
+    h = dev(H)
+    got = kd.token_logp_forward(h, *a, 1.0, want_entropy=True, keep_logits=True)
+    z = got[3]
+    bad = torch.zeros(T, dtype=torch.bool, device="cuda")
+    bad[1] = bad[3] = True
+    for x, y in zip(got, clean):
+        assert torch.isnan(x[bad]).all() and torch.equal(x[~bad], y[~bad])
+    g = torch.ones(T, device="cuda")
+    for zz in (None, z):
+        dH, _ = kd.token_logp_backward(h, *a, 1.0, got[1], g, got[2], g, zz)
+        assert torch.isnan(dH[bad]).all() and torch.isfinite(dH[~bad]).all()
