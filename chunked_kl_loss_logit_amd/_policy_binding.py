@@ -210,7 +210,23 @@ def _cu(cu_seqlens, name="cu_seqlens"):
     return int(cu_seqlens.shape[0]) - 1
 
 
-class PolicyOptions:
+class _Options:
+    """What a loss's backward needs of its forward's options, without their tensors: autograd saves those, and gives
+    them back where they were, unless hooks moved them in between."""
+
+    def keep(self):
+        self.places, self.tensors = _places(self.tensors), (None,) * len(self.tensors)
+
+    def hold(self, tensors):
+        """Whether the saved tensors lie where these options point to."""
+        return _places(tensors) == self.places
+
+
+def _places(tensors):
+    return [t if t is None else (t.data_ptr(), t.numel()) for t in tensors]
+
+
+class PolicyOptions(_Options):
     """The loss's parameters and optional tensors, checked once against T tokens."""
 
     def __init__(self, logp, old_logp, advantages, mask, ref_logp=None, entropy=None, cu_seqlens=None, clip_low=0.2,
@@ -288,7 +304,7 @@ def kd_policy_loss_fwd_bwd(o, stats, weights, grad_logp, grad_entropy, workspace
 
 
 # ---------------------------------------------------------------- preference loss
-class PreferenceOptions:
+class PreferenceOptions(_Options):
     """The loss's parameters and optional tensors, checked once."""
 
     def __init__(self, T, device_of, cu_seqlens, mask, ref_logp=None, beta=0.1, kind="sigmoid", label_smoothing=0.0,

@@ -156,7 +156,7 @@ def policy_loss_forward(logp, old_logp, advantages, mask=None, workspace=None, *
 
 def _policy_backward(o, weights, grad_total):
     g = _f32(weights, o.T)
-    ge = _f32(weights, o.T) if o.tensors[5] is not None else None
+    ge = _f32(weights, o.T) if o.c.entropy is not None else None
     B.kd_policy_loss_bwd(o, weights, _grad(grad_total), g, ge)
     return g, ge
 
@@ -180,8 +180,9 @@ class _PolicyLoss(torch.autograd.Function):
                             cu_seqlens=cu_seqlens, **options)
         total = _f32(logp, ())  # a tensor of its own: a view of stats could not be changed in place by its user
         stats, weights, _, _ = _policy_forward(o, False, None, total)
-        ctx.save_for_backward(logp, entropy, old_logp, advantages, mask, ref_logp, cu_seqlens, weights)
-        ctx.o = o
+        ctx.save_for_backward(*o.tensors, weights)
+        o.keep()
+        ctx.o, ctx.options = o, options
         ctx.mark_non_differentiable(stats)
         ctx.set_materialize_grads(False)
         return total, stats
@@ -191,8 +192,12 @@ class _PolicyLoss(torch.autograd.Function):
     def backward(ctx, g, _):
         if g is None:
             return (None,) * 8
-        weights = ctx.saved_tensors[-1]  # refuses tensors changed in place since
-        gl, ge = _policy_backward(ctx.o, weights, g)
+        *tensors, weights = ctx.saved_tensors  # refuses tensors changed in place since
+        o = ctx.o
+        if not o.hold(tensors):
+            logp, old_logp, advantages, mask, ref_logp, entropy, cu_seqlens = tensors
+            o = B.PolicyOptions(logp, old_logp, advantages, mask, ref_logp, entropy, cu_seqlens, **ctx.options)
+        gl, ge = _policy_backward(o, weights, g)
         return gl, ge, None, None, None, None, None, None
 
 
@@ -254,8 +259,9 @@ class _PreferenceLoss(torch.autograd.Function):
     def forward(ctx, logp, cu_seqlens, mask, ref_logp, options):
         o = _pref_in(logp, cu_seqlens, mask, dict(options, ref_logp=ref_logp))
         loss, rewards, sums = _pref_forward(o, logp, None)
-        ctx.save_for_backward(cu_seqlens, mask, ref_logp, sums)
-        ctx.o = o
+        ctx.save_for_backward(*o.tensors, sums)
+        o.keep()
+        ctx.o, ctx.options = o, options
         ctx.mark_non_differentiable(rewards)
         ctx.set_materialize_grads(False)
         return loss, rewards
@@ -265,8 +271,12 @@ class _PreferenceLoss(torch.autograd.Function):
     def backward(ctx, g, _):
         if g is None:
             return (None,) * 5
-        sums = ctx.saved_tensors[-1]  # refuses tensors changed in place since
-        return _pref_backward(ctx.o, sums, g), None, None, None, None
+        *tensors, sums = ctx.saved_tensors  # refuses tensors changed in place since
+        o = ctx.o
+        if not o.hold(tensors):
+            cu_seqlens, mask, ref_logp = tensors
+            o = B.PreferenceOptions(o.T, sums, cu_seqlens, mask, ref_logp, **ctx.options)
+        return _pref_backward(o, sums, g), None, None, None, None
 
 
 def preference_loss(logp, cu_seqlens, mask=None, ref_logp=None, **options):

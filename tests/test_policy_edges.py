@@ -193,3 +193,60 @@ def test_nan_and_infinite_logits_stay_visible(T, d, V, dtype):
     for zz in (None, z):
         dH, _ = kd.token_logp_backward(h, *a, 1.0, got[1], g, got[2], g, zz)
         assert torch.isnan(dH[bad]).all() and torch.isfinite(dH[~bad]).all()
+
+
+def big_inputs(which, T):
+    gen = torch.Generator(device="cuda").manual_seed(61)
+    r = lambda: torch.randn(T, generator=gen, device="cuda")  # noqa: E731
+    cu = torch.tensor([0, 5, T // 2, T // 2, T], dtype=torch.int32, device="cuda")
+    mask = (r() > -1).to(torch.uint8)
+    if which == "policy":
+        return r().requires_grad_(True), (r(), r(), mask), dict(ref_logp=r(), entropy=r(), cu_seqlens=cu, kl_weight=0.1,
+                                                                entropy_weight=0.1, reduction="sequence", per_sequence=False)
+    return r().requires_grad_(True), (cu, mask), dict(ref_logp=r(), average=True)
+
+
+def loss_of(which, x, args, kw):
+    return kd.policy_loss(x, *args, **kw)[0] if which == "policy" else kd.preference_loss(x, *args, **kw)[0].sum()
+
+
+@pytest.mark.parametrize("which", ["policy", "preference"])
+def test_inputs_go_where_saved_tensors_go(which):
+    """Offloaded while the loss waits for its backward, and let go after it; the gradients are the same bits."""
+    T = 1 << 20
+    x, args, kw = big_inputs(which, T)
+    loss = loss_of(which, x, args, kw)
+    want, = torch.autograd.grad(loss, x, retain_graph=True)
+    again, = torch.autograd.grad(loss, x)
+    assert torch.equal(again, want)
+    ref = kw["ref_logp"]
+    size = ref.numel() * 4
+    del loss
+    with torch.autograd.graph.save_on_cpu():
+        loss = loss_of(which, x, args, kw)
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    del ref, args, kw
+    assert before - torch.cuda.memory_allocated() >= size
+    got, = torch.autograd.grad(loss, x)
+    assert torch.equal(got, want)
+    x, args, kw = big_inputs(which, T)
+    loss = loss_of(which, x, args, kw)
+    loss.backward()
+    before = torch.cuda.memory_allocated()
+    del args, kw
+    assert before - torch.cuda.memory_allocated() >= size and float(loss.detach()) == float(loss.detach())
+
+
+@pytest.mark.parametrize("which", ["policy", "preference"])
+def test_saved_tensors_that_come_back_changed_are_refused(which):
+    x, args, kw = big_inputs(which, 1000)
+    for unpack in (lambda t: t[:-1], lambda t: t.double(), lambda t: t.cpu(), lambda t: t.repeat_interleave(2, 0)[::2]):
+        with torch.autograd.graph.saved_tensors_hooks(lambda t: t, unpack):
+            loss = loss_of(which, x, args, kw)
+        with pytest.raises((ValueError, TypeError, RuntimeError)):
+            loss.backward()
+    loss = loss_of(which, x, args, kw)
+    kw["ref_logp"].add_(1)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
