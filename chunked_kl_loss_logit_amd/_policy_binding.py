@@ -24,7 +24,8 @@ GRAD_TYPES = {torch.float32: KD_F32, torch.bfloat16: KD_BF16, torch.float16: KD_
 _F64 = (torch.float64,)
 
 POLICY_EXPORTS = (
-    "kd_token_logp_logits_size", "kd_token_logp_workspace_size", "kd_token_logp_fwd", "kd_token_logp_bwd",
+    "kd_token_logp_logits_size", "kd_token_logp_fwd_workspace_size", "kd_token_logp_workspace_size", "kd_token_logp_fwd",
+    "kd_token_logp_bwd",
     "kd_token_logp_fwd_shard", "kd_token_logp_shard_combine", "kd_token_logp_bwd_shard",
     "kd_policy_loss_workspace_size", "kd_policy_loss_fwd", "kd_policy_loss_bwd", "kd_policy_loss_fwd_bwd",
     "kd_preference_loss_workspace_size", "kd_preference_loss_fwd", "kd_preference_loss_bwd",
@@ -59,6 +60,7 @@ def plib() -> ctypes.CDLL:
                                  ctypes.c_int)
     psz, po, fo = ctypes.POINTER(sz), ctypes.POINTER(KdPolicyOpts), ctypes.POINTER(KdPrefOpts)
     L.kd_token_logp_logits_size.argtypes = [i64, i64, psz]
+    L.kd_token_logp_fwd_workspace_size.argtypes = [i64, i64, i64, st, psz]
     L.kd_token_logp_workspace_size.argtypes = [i64, i64, i64, st, st, i64, psz]
     L.kd_token_logp_fwd.argtypes = [vp, vp, vp, vp, f32, i64, i64, i64, st, vp, vp, vp, vp, vp, sz, vp]
     L.kd_token_logp_bwd.argtypes = [vp, vp, vp, vp, f32, i64, i64, i64, st, vp, vp, vp, vp, vp, vp, vp, st, i64, vp, sz,
@@ -109,6 +111,10 @@ def _run(name, t, stream, *args):
 # ---------------------------------------------------------------- token log-probabilities
 def kd_token_logp_logits_size(T, V) -> int:
     return _size("kd_token_logp_logits_size", T, V)
+
+
+def kd_token_logp_fwd_workspace_size(T, d, V, dtype) -> int:
+    return _size("kd_token_logp_fwd_workspace_size", T, d, V, _dtype_code(dtype))
 
 
 def kd_token_logp_workspace_size(T, d, V, dtype, dw_dtype=torch.float32, chunk_rows=0) -> int:

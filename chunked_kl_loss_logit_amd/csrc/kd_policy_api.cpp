@@ -427,6 +427,14 @@ kd_status kd_token_logp_logits_size(int64_t T, int64_t V, size_t* bytes) {
   return KD_OK;
 }
 
+kd_status kd_token_logp_fwd_workspace_size(int64_t T, int64_t d, int64_t V, kd_dtype dt, size_t* bytes) {
+  g_err.clear();
+  KD_TRY(need(bytes, "bytes"));
+  KD_TRY(check_widths(T, d, V, dt, 1.0f));
+  *bytes = T == 0 ? 0 : plan_logp(T, d, V, elem_of(dt), 4, 0).fwd_total;
+  return KD_OK;
+}
+
 kd_status kd_token_logp_workspace_size(int64_t T, int64_t d, int64_t V, kd_dtype dt, kd_dtype dw_dtype,
                                        int64_t chunk_rows, size_t* bytes) {
   g_err.clear();

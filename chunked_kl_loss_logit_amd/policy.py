@@ -44,7 +44,7 @@ def token_logp_forward(H, W, tokens, mask=None, tau=1.0, want_entropy=False, kee
     entropy = _f32(H, T) if want_entropy else None
     logits = _f32(H, T, -(-V // 256) * 256) if keep_logits else None
     if workspace is None:
-        workspace = _workspace(B.kd_token_logp_workspace_size(T, d, V, H.dtype), H.device)
+        workspace = _workspace(B.kd_token_logp_fwd_workspace_size(T, d, V, H.dtype), H.device)
     B.kd_token_logp_fwd(H, W, tokens, mask, tau, logp, lse, entropy, logits, workspace)
     return logp, lse, entropy, logits
 
@@ -70,7 +70,7 @@ def token_logp_shard_forward(H, W_shard, v0, tokens, mask=None, tau=1.0, keep_lo
     rec = _f32(H, T, 4)
     logits = _f32(H, T, -(-V // 256) * 256) if keep_logits else None
     if workspace is None:
-        workspace = _workspace(B.kd_token_logp_workspace_size(T, d, V, H.dtype), H.device)
+        workspace = _workspace(B.kd_token_logp_fwd_workspace_size(T, d, V, H.dtype), H.device)
     B.kd_token_logp_fwd_shard(H, W_shard, v0, tokens, mask, tau, rec, logits, workspace)
     return rec, logits
 

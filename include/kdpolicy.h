@@ -52,8 +52,12 @@ extern "C" {
  * with it the backward call reads them instead of computing the projection
  * again. */
 kd_status kd_token_logp_logits_size(int64_t T, int64_t V, size_t* bytes);
+/* Workspace bytes for a forward call alone (kd_token_logp_fwd, its shard
+ * form): the tiles' records and up to a default chunk's rows of H. */
+kd_status kd_token_logp_fwd_workspace_size(int64_t T, int64_t d, int64_t V, kd_dtype dt, size_t* bytes);
 /* Workspace bytes for kd_token_logp_fwd and kd_token_logp_bwd (one size
- * serves both, and the shard calls).  dw_dtype: the type of dW below.
+ * serves both, and the shard calls; it holds a chunk's dZ).  dw_dtype: the
+ * type of dW below.
  * chunk_rows as in kd_topk_kl_workspace_size. */
 kd_status kd_token_logp_workspace_size(int64_t T, int64_t d, int64_t V, kd_dtype dt, kd_dtype dw_dtype,
                                        int64_t chunk_rows, size_t* bytes);

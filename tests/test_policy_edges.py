@@ -250,3 +250,26 @@ def test_saved_tensors_that_come_back_changed_are_refused(which):
     kw["ref_logp"].add_(1)
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         loss.backward()
+
+
+@pytest.mark.parametrize("T,d,V,dtype", [(70, 128, 520, bf), (70, 128, 520, f32), (1000, 160, 7016, bf), (5000, 160, 2056, bf)])
+def test_a_forward_in_its_own_workspace(T, d, V, dtype):
+    """In exactly the bytes asked for, between guards, with the results of any other workspace; a scoring call takes no
+    more than that and its outputs."""
+    H, W, tokens, mask = make_head(T, d, V, dtype, 63, masked=0.3)
+    a = [dev(x) for x in (H, W, tokens, mask)]
+    B = kd._policy_binding
+    nb = B.kd_token_logp_fwd_workspace_size(T, d, V, dtype)
+    raw = torch.full((nb + 8192,), 0xA5, dtype=torch.uint8, device="cuda")
+    ws = raw[4096:4096 + nb]
+    big = torch.empty(B.kd_token_logp_workspace_size(T, d, V, dtype), dtype=torch.uint8, device="cuda")
+    want = kd.token_logp_forward(*a, 1.0, want_entropy=True, keep_logits=True, workspace=big)
+    got = kd.token_logp_forward(*a, 1.0, want_entropy=True, keep_logits=True, workspace=ws)
+    rec = kd.token_logp_shard_forward(a[0], a[1], 0, a[2], a[3], workspace=ws)[0]
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(got[:3], want[:3])) and torch.isfinite(rec).all()
+    assert (raw[:4096] == 0xA5).all() and (raw[-4096:] == 0xA5).all()
+    torch.cuda.reset_peak_memory_stats()
+    before = torch.cuda.memory_allocated()
+    kd.token_logp_forward(*a, 1.0)
+    assert torch.cuda.max_memory_allocated() - before <= nb + 2 * 4 * T + 4 * 512

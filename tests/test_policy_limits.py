@@ -107,3 +107,25 @@ def test_any_number_of_chunk_rows_is_cut_to_the_rows_present(L, chunk, dt):
             assert getattr(L, fn)(*args, c, ctypes.byref(out)) == 0
             got.append(out.value)
         assert got[0] == got[1], fn
+
+
+@pytest.mark.parametrize("T,d,V,dt", [(1500, 4096, 128256, BF16), (4096, 2048, 128256, BF16), (1, 4096, 128256, BF16),
+                                      (100000, 2048, 32000, BF16), (777, 1024, 32000, F32), (20000, 64, 264, F32)])
+def test_a_forward_alone_needs_no_dz(L, T, d, V, dt):
+    """Its workspace is records (16 bytes a row and tile of at least 128 columns, of a chunk of up to 4096 rows), the
+    chunk's rows of H and the list of valid rows."""
+    out = ctypes.c_size_t()
+    assert L.kd_token_logp_fwd_workspace_size(T, d, V, dt, ctypes.byref(out)) == 0
+    rows, elem = min(4096, -(-T // 256) * 256), 2 if dt == BF16 else 4
+    assert out.value <= -(-V // 128) * rows * 16 + rows * -(-d // 128) * 128 * elem + 4 * T + 2048
+    assert out.value <= size(L, T, d, V, 0, dt)
+    assert out.value < rows * V * elem / 3
+
+
+def test_forward_size_refuses(L):
+    out = ctypes.c_size_t()
+    assert L.kd_token_logp_fwd_workspace_size(0, 64, 264, BF16, ctypes.byref(out)) == 0 and out.value == 0
+    assert L.kd_token_logp_fwd_workspace_size(8, 60, 264, BF16, ctypes.byref(out)) == 2
+    assert L.kd_token_logp_fwd_workspace_size(-1, 64, 264, BF16, ctypes.byref(out)) == 1
+    assert L.kd_token_logp_fwd_workspace_size(8, 64, 264, 2, ctypes.byref(out)) == 1
+    assert L.kd_token_logp_fwd_workspace_size(8, 64, 264, BF16, None) == 1
