@@ -273,3 +273,34 @@ def test_a_forward_in_its_own_workspace(T, d, V, dtype):
     before = torch.cuda.memory_allocated()
     kd.token_logp_forward(*a, 1.0)
     assert torch.cuda.max_memory_allocated() - before <= nb + 2 * 4 * T + 4 * 512
+
+
+@pytest.mark.parametrize("T", [1, 7, 32])
+@pytest.mark.parametrize("cuts", [(0, 256, 768), (0, 512, 520), (0, 1288, 4096)])
+@pytest.mark.parametrize("masked", [0.0, 0.4])
+def test_vocabulary_shards_of_few_rows(T, cuts, masked):
+    """A float32 part of dH from the two planes of dZ: shards of one vocabulary range (512 columns and fewer) and of
+    several."""
+    d, V = 160, cuts[-1]
+    H, W, tokens, mask = make_head(T, d, V, bf, 65, masked=masked if T > 1 else 0.0)
+    gen = torch.Generator().manual_seed(66)
+    g, ge = torch.randn(T, generator=gen), torch.randn(T, generator=gen)
+    want, bound = logp_reference(H, W, tokens, mask, 0.8, g, ge)
+    h, t, m = dev(H), dev(tokens), dev(mask)
+    parts = [dev(W[:, a:b].contiguous()) for a, b in zip(cuts, cuts[1:])]
+    fw = [kd.token_logp_shard_forward(h, w, a, t, m, 0.8, keep_logits=True) for w, a in zip(parts, cuts)]
+    logp, lse, ent = kd.token_logp_shard_combine([r for r, _ in fw], m, 0.8, want_entropy=True)
+    for name, got in (("logp", logp), ("lse", lse), ("entropy", ent)):
+        within(got, want[name], bound[name], name)
+    for keep in (False, True):
+        for dw in (f32, bf):
+            bw = [kd.token_logp_shard_backward(h, w, a, t, m, 0.8, lse, dev(g), ent, dev(ge), z if keep else None, dw_dtype=dw)
+                  for w, a, (_, z) in zip(parts, cuts, fw)]
+            assert all(x.dtype == f32 and y.dtype == dw for x, y in bw)
+            dH = sum(x for x, _ in bw)
+            within(dH, want["dH"], bound["dH"], "dH")
+            within(torch.cat([y for _, y in bw], 1), want["dW"], bound["dW"], "dW")
+            # float32 parts are off by dZ's 2^-16 and the logits' own error alone
+            assert (dH.double().cpu() - want["dH"]).norm() <= 2.0 ** -12 * want["dH"].norm() + 1e-30
+            if mask is not None:
+                assert (dH[m == 0] == 0).all()
