@@ -17,9 +17,9 @@
 //   backward: each register becomes its dZ.
 // The tile contraction (2 T d V flops) bounds both; without the entropy its
 // terms are compiled out.  Measured, T 4096, d 2048, V 128256 (2.15 TFLOP a
-// product): forward with the entropy 1.63 ms (1.32 PFLOP/s), with kept logits
-// (2.1 GB written) 1.93 ms, dZ 1.71 ms (1.26 PFLOP/s), dZ from kept logits 0.62
-// ms (5.1 TB/s), dH 1.56 ms (1.38 PFLOP/s), dW in bf16 1.61 ms (1.34 PFLOP/s);
+// product): forward with the entropy 1.69 ms (1.28 PFLOP/s), with kept logits
+// (2.1 GB written) 1.99 ms, dZ 1.79 ms (1.20 PFLOP/s), dZ from kept logits 0.66
+// ms (4.8 TB/s), dH 1.60 ms (1.34 PFLOP/s), dW in bf16 1.65 ms (1.30 PFLOP/s);
 // a torch product of 8192^3 reaches 1.15 PFLOP/s.
 #include <type_traits>
 

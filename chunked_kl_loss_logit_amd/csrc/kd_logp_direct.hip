@@ -1,6 +1,7 @@
 // Token log-probabilities, dZ, dH and dW on the register-fed tiles of
-// kd_direct.h: float32 of any size, and bf16 where the 256 x 256 ring tiles of
-// kd_logp.hip would leave most of the chip idle or do not apply.
+// kd_direct.h: float32 (d and V multiples of 4), and bf16 (of 8) where the 256 x
+// 256 ring tiles of kd_logp.hip would leave most of the chip idle or do not
+// apply: d not a multiple of 32, V < 256, a head of 4 GiB or more.
 //
 //   forward  a = W (128 columns), b = H rows      z = W^T H^T, then each row's (m, l, e, x) record per tile
 //   dZ       the same product; each row becomes its dZ (row-major)

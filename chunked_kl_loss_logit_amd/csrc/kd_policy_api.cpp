@@ -167,7 +167,9 @@ kd_status head_panels(const void* H, int64_t d, const kd::Compact& c, int64_t c0
 // dZ, the token's, is most of a row of dH and of a column of dW, and its
 // rounding, up to 2^-8, is that of the whole.  Up to 32 rows the products read
 // and write W's size whatever dZ holds: a backward of 7 rows of 2048 x 32000
-// took 110 us without the second plane and 119 with it.
+// took 110 us without the second plane and 119 with it.  T counts the masked
+// rows too, since the launches are chosen where the mask is not known: 40 rows
+// of which 5 are valid do without the plane, at the error of one rounding more.
 bool logp_planes(int64_t T, int elem) { return elem == 2 && T <= 32; }
 
 // The valid rows, the masked rows of dH (nullable) zeroed, and up to kPrepMax

@@ -43,8 +43,11 @@ extern "C" {
  * logp = NaN; its dZ has no token term.  Columns masked by large negative
  * logits, down to the type's lowest value (in a row of W that every hidden
  * state meets with 1, say), have probability 0 and add nothing; a row with
- * nothing but such columns may be NaN.  A NaN or infinite logit makes its
- * row's results NaN.
+ * nothing but such columns may be NaN.  Infinite and NaN entries of H and W are
+ * no such mask: the results that they enter may be NaN.
+ * Speed: bf16 heads below 4 GiB with d a multiple of 32 and V >= 256 run at the
+ * matrix cores' rate from a few hundred rows on, other bf16 heads at about 0.4
+ * of it.
  */
 
 /* Bytes of the optional buffer `logits` in which the forward call leaves the
@@ -88,8 +91,8 @@ kd_status kd_token_logp_bwd(const void* H, const void* W, const int32_t* tokens,
  * m = max y (-infinity, with l = e = 0, where all are below the 32-bit range;
  * beyond 2^24 in size at most two steps above), l = sum 2^(y - m), e = sum
  * 2^(y - m) (y - m), and x the raw logit at the token, or 0 in the shards that
- * do not hold it.  A token that no
- * shard holds is not told from one whose logit is 0. */
+ * do not hold it.  A token that no shard holds is not told from one whose logit
+ * is 0. */
 kd_status kd_token_logp_fwd_shard(const void* H, const void* W, const int32_t* tokens, const uint8_t* mask, float tau,
                                   int64_t T, int64_t d, int64_t V, int64_t v0, kd_dtype dt, float* rec, float* logits,
                                   void* workspace, size_t workspace_bytes, void* stream);
