@@ -26,7 +26,16 @@ from ._binding import (  # noqa: F401
     kd_topk_kl_shard_workspace_size, kd_topk_kl_fwd_shard, kd_topk_kl_shard_combine, kd_topk_kl_bwd_shard,
     kd_full_kl_fwd_shard, kd_full_kl_shard_combine, kd_full_kl_bwd_shard,
 )
+from ._layers_binding import (  # noqa: F401
+    LAYERS_EXPORTS, kd_embedding_bwd, kd_embedding_fwd, kd_embedding_workspace_size, kd_int8_matmul,
+    kd_int8_matmul_workspace_size, kd_layer_norm_bwd, kd_layer_norm_fwd, kd_layer_norm_workspace_size,
+    kd_rows_dequantize, kd_rows_quantize,
+)
 from ._policy_binding import POLICY_EXPORTS  # noqa: F401
+from .layers import (  # noqa: F401
+    checkpoint_8bit, dequantize_rows, embedding, embedding_backward, embedding_forward, int8_matmul, layer_norm,
+    layer_norm_backward, layer_norm_forward, quantize_rows,
+)
 from .policy import (  # noqa: F401
     clip_grad_norm, clip_grad_norm_, grad_sumsq, policy_loss, policy_loss_backward, policy_loss_forward,
     policy_loss_forward_backward, preference_loss, preference_loss_backward, preference_loss_forward,
@@ -50,6 +59,8 @@ __all__ = [
     "token_logp_shard_backward", "policy_loss", "policy_loss_forward", "policy_loss_backward",
     "policy_loss_forward_backward", "preference_loss", "preference_loss_forward", "preference_loss_backward",
     "preference_loss_forward_backward", "grad_sumsq", "clip_grad_norm", "clip_grad_norm_",
+    "embedding", "embedding_forward", "embedding_backward", "layer_norm", "layer_norm_forward", "layer_norm_backward",
+    "quantize_rows", "dequantize_rows", "checkpoint_8bit", "int8_matmul",
 ]
 
 

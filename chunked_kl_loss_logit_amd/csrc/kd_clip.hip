@@ -13,9 +13,7 @@
 // Measured: 400 M float32 elements, the sum 290 us (5.5 TB/s), the scaling 565
 // us (5.7 TB/s; a large copy reaches 5.0); 290 bf16 tensors, 30 M elements,
 // into others 57 us in five launches; 6 tensors, 40000 elements, 12 us in one.
-#include <hip/hip_fp16.h>
-
-#include "kd_gemm.h"
+#include "kd_elem.h"
 #include "kd_policy.h"
 
 namespace kd {
@@ -23,7 +21,6 @@ namespace kd {
 namespace {
 
 constexpr int kClipThreads = 512;
-enum { kTypeF32 = 0, kTypeBf16 = 1, kTypeF16 = 2 };
 
 template <int NT>
 __device__ inline double block_sum(double v) {
@@ -47,49 +44,6 @@ __device__ inline int tensor_of(const int32_t* first, int n, int b) {
   }
   return lo - 1;
 }
-
-// 16 bytes at any element-aligned address (the hardware takes unaligned
-// vector accesses; only those that cross a cache line cost more).
-__device__ inline u32x4_t load16(const char* p) {
-  u32x4_t v;
-  __builtin_memcpy(&v, p, 16);
-  return v;
-}
-__device__ inline void store16(char* p, u32x4_t v) { __builtin_memcpy(p, &v, 16); }
-
-template <int TY>
-struct Elem;
-template <>
-struct Elem<kTypeF32> {
-  static constexpr int kBytes = 4;
-  __device__ static inline float get(u32x4_t v, int i) { return __uint_as_float(v[i]); }
-  __device__ static inline float get1(const char* p) { return *reinterpret_cast<const float*>(p); }
-  __device__ static inline void put1(char* p, float x) { *reinterpret_cast<float*>(p) = x; }
-};
-template <>
-struct Elem<kTypeBf16> {
-  static constexpr int kBytes = 2;
-  __device__ static inline float get(u32x4_t v, int i) {
-    return __uint_as_float(i & 1 ? v[i >> 1] & 0xffff0000u : v[i >> 1] << 16);
-  }
-  __device__ static inline float get1(const char* p) {
-    return __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t*>(p) << 16);
-  }
-  __device__ static inline void put1(char* p, float x) { *reinterpret_cast<uint16_t*>(p) = (uint16_t)Bf16::cvt(x); }
-  __device__ static inline uint32_t pack(float a, float b) { return Bf16::pack2(a, b); }
-};
-template <>
-struct Elem<kTypeF16> {
-  static constexpr int kBytes = 2;
-  __device__ static inline float get(u32x4_t v, int i) {
-    return __half2float(__ushort_as_half((unsigned short)(v[i >> 1] >> (16 * (i & 1)))));
-  }
-  __device__ static inline float get1(const char* p) { return __half2float(*reinterpret_cast<const __half*>(p)); }
-  __device__ static inline void put1(char* p, float x) { *reinterpret_cast<__half*>(p) = __float2half_rn(x); }
-  __device__ static inline uint32_t pack(float a, float b) {
-    return (uint32_t)__half_as_ushort(__float2half_rn(a)) | ((uint32_t)__half_as_ushort(__float2half_rn(b)) << 16);
-  }
-};
 
 // Elements [b, e) of a tensor (fewer than 2^31) by NT threads: 16-byte pieces, kDeep of a thread's loads in flight at once, then the
 // last few elements one by one.

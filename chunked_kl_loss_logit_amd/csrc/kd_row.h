@@ -1,0 +1,103 @@
+// One row in the registers of R threads: thread i holds the pieces of 8
+// elements i, i + R, .., i + (K - 1) R.  R = 64 is a wave of its own, so that
+// a workgroup of 256 holds four rows; otherwise the workgroup is the row's.
+#pragma once
+
+#include "kd_elem.h"
+#include "kd_rows8.h"
+
+namespace kd {
+
+// Rows of up to kRowMost elements are held in registers, longer ones are read
+// again for every pass over them.
+constexpr int64_t kRowMost = 16384;
+
+template <int R>
+struct RowTeam {
+  static constexpr int kThreads = R < 256 ? 256 : R;
+  static constexpr int kRows = kThreads / R;  // rows of a workgroup
+  static constexpr int kWaves = R / 64;
+  __device__ static inline int lane() { return threadIdx.x % R; }
+  __device__ static inline int slot() { return threadIdx.x / R; }
+
+  // Sums over the row's threads, each of N values, in the same order every
+  // time.  lds: N kWaves floats, free again after the next barrier.
+  template <int N>
+  __device__ static inline void sum(float (&v)[N], float* lds) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
+    if constexpr (R > 64) {
+      const int w = threadIdx.x >> 6;
+      __syncthreads();
+      if ((threadIdx.x & 63) == 0)
+#pragma unroll
+        for (int i = 0; i < N; ++i) lds[i * kWaves + w] = v[i];
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        v[i] = 0;
+#pragma unroll
+        for (int k = 0; k < kWaves; ++k) v[i] += lds[i * kWaves + k];
+      }
+    }
+  }
+  __device__ static inline uint32_t most(uint32_t v, uint32_t* lds) {
+    v = wave_max(v);
+    if constexpr (R > 64) {
+      __syncthreads();
+      if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < kWaves; ++k) v = max(v, lds[k]);
+    }
+    return v;
+  }
+};
+
+template <int TY>
+__device__ inline void load_row(const char* row, int64_t d, int p, float (&x)[8]) {
+  unpack8<TY>(load8<TY>(row + (int64_t)p * 8 * Elem<TY>::kBytes, (int)(d - 8 * (int64_t)p)), x);
+}
+
+// 8 values of a vector whose type is known at run time
+__device__ inline void load_any(const char* base, int type, int64_t d, int p, float (&x)[8]) {
+  if (type == kTypeF32) load_row<kTypeF32>(base, d, p, x);
+  else if (type == kTypeBf16) load_row<kTypeBf16>(base, d, p, x);
+  else load_row<kTypeF16>(base, d, p, x);
+}
+__device__ inline void store_any1(char* base, int type, int64_t i, float v) {
+  if (type == kTypeF32) Elem<kTypeF32>::put1(base + 4 * i, v);
+  else if (type == kTypeBf16) Elem<kTypeBf16>::put1(base + 2 * i, v);
+  else Elem<kTypeF16>::put1(base + 2 * i, v);
+}
+
+// launch(R, K) with the fewest threads whose registers hold a row of d
+// elements; false if none does.
+template <class F>
+inline bool pick_row(int64_t d, F&& launch) {
+  const int64_t pieces = (d + 7) / 8;
+  auto with = [&](auto r, auto k) {
+    launch(r, k);
+    return true;
+  };
+  using std::integral_constant;
+  if (pieces <= 64) return with(integral_constant<int, 64>(), integral_constant<int, 1>());
+  if (pieces <= 128) return with(integral_constant<int, 64>(), integral_constant<int, 2>());
+  if (pieces <= 256) return with(integral_constant<int, 64>(), integral_constant<int, 4>());
+  if (pieces <= 512) return with(integral_constant<int, 256>(), integral_constant<int, 2>());
+  if (pieces <= 1024) return with(integral_constant<int, 256>(), integral_constant<int, 4>());
+  if (pieces <= 2048) return with(integral_constant<int, 1024>(), integral_constant<int, 2>());
+  static_assert(kRowMost == 2048 * 8, "the longest row that registers hold");
+  return false;
+}
+
+// launch with the element type as a constant
+template <class F>
+inline void pick_type(int type, F&& launch) {
+  using std::integral_constant;
+  if (type == kTypeF32) launch(integral_constant<int, kTypeF32>());
+  else if (type == kTypeBf16) launch(integral_constant<int, kTypeBf16>());
+  else launch(integral_constant<int, kTypeF16>());
+}
+
+}  // namespace kd

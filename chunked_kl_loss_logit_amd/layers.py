@@ -1,0 +1,212 @@
+"""The layers on the model's side of the output head (include/kdlayers.h).
+
+    X = embedding(tokens, E, mask, scale)                  # or embedding(tokens, W, ..., tied=True): W [d,V], the head
+    H = layer_norm(X, weight, bias, mask)                  # autograd; checkpoint="int8" keeps X in 8 bits
+    logp = token_logp(H, W, tokens, mask)                  # any loss over the head
+
+    y = checkpoint_8bit(block, x)                          # keeps x in 8 bits, runs block again in the backward pass
+
+    q, scale = quantize_rows(H, "int8", 0)                 # one scale a row
+    Z = int8_matmul(q, scale, wq, w_scale)                 # logits through a frozen 8-bit head
+
+In a captured graph the _forward and _backward functions are the safe form:
+torch ends the process where a backward of its autograd is captured while an
+uncaptured graph of the same leaves is alive, whatever functions are in it.
+
+All arithmetic runs in the HIP kernels of libkdloss.so; this module allocates
+outputs and workspaces with torch.
+"""
+from __future__ import annotations
+
+import torch
+from torch.autograd.function import once_differentiable
+
+from . import _layers_binding as B
+from .policy import _f32, _workspace
+
+
+# ---------------------------------------------------------------- token embeddings
+def embedding_forward(tokens, table, mask=None, scale=1.0, tied=False):
+    """scale * table[tokens] [T,d] in the table's type: rows of table [V,d], or with tied the columns of the head
+    W [d,V].  Masked rows are 0; a valid token outside the vocabulary gives a row of NaN."""
+    n, m = B._matrix("table", table, None, B.TYPES)
+    out = torch.empty(B._tokens(tokens, mask), n if tied else m, dtype=table.dtype, device=table.device)
+    B.kd_embedding_fwd(tokens, table, mask, scale, tied, out)
+    return out
+
+
+def embedding_backward(grad, tokens, V, mask=None, scale=1.0, tied=False, grad_dtype=None, out=None, workspace=None):
+    """The table's gradient [V,d] (or [d,V] if tied) of grad_dtype (None: grad's).  out: a tensor that takes it on
+    top of what it holds and is returned, such as the gradient of the head that the embedding shares."""
+    T, d = B._matrix("grad", grad, None, B.TYPES)
+    if out is None:
+        shape = (d, V) if tied else (V, d)
+        table = torch.empty(shape, dtype=grad_dtype or grad.dtype, device=grad.device)
+    else:
+        if grad_dtype is not None and out.dtype != grad_dtype:
+            raise TypeError(f"out must be {grad_dtype}, got {out.dtype}")
+        B.P._writable("out", [out])
+        table = out
+    if workspace is None:
+        workspace = _workspace(B.kd_embedding_workspace_size(T, V, d), grad.device)
+    B.kd_embedding_bwd(grad, tokens, mask, scale, V, tied, out is not None, table, workspace)
+    if out is not None:
+        torch.autograd.graph.increment_version([out])
+    return table
+
+
+class _Embedding(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, table, tokens, mask, scale, tied):
+        out = embedding_forward(tokens, table, mask, scale, tied)
+        ctx.save_for_backward(tokens, mask)
+        ctx.V, ctx.scale, ctx.tied = table.shape[1 if tied else 0], scale, tied
+        return out
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, g):
+        tokens, mask = ctx.saved_tensors
+        return (embedding_backward(g.contiguous(), tokens, ctx.V, mask, ctx.scale, ctx.tied), None, None, None, None)
+
+
+def embedding(tokens, table, mask=None, scale=1.0, tied=False):
+    """embedding_forward, differentiable in the table; its gradient has its type and layout."""
+    return _Embedding.apply(table, tokens, mask, float(scale), bool(tied))
+
+
+# ---------------------------------------------------------------- rows in 8 bits
+def quantize_rows(x, kind="int8", group=0):
+    """x [T,d] in 8 bits: q [T,d] (int8, or float8_e4m3fn for kind "e4m3") and scale [T, groups] float32, for groups
+    of 32, 64, 128, 256 or 512 values of a row, or of whole rows (0)."""
+    T, d = B._matrix("x", x, None, B.TYPES)
+    B._kind(kind, group)
+    q = torch.empty(T, d, dtype=B.ROWS_TYPES[kind], device=x.device)
+    scale = _f32(x, T, B._groups(d, group))
+    B.kd_rows_quantize(x, kind, group, q, scale)
+    return q, scale
+
+
+def dequantize_rows(q, scale, group=0, dtype=torch.bfloat16):
+    """What rows in 8 bits stand for, rounded to dtype."""
+    out = torch.empty(q.shape, dtype=dtype, device=q.device)
+    B.kd_rows_dequantize(q, scale, group, out)
+    return out
+
+
+def _rows(x):
+    return x.detach().contiguous().reshape(-1, x.shape[-1])
+
+
+class _Checkpoint(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, fn, kind, group, x, *others):
+        out = fn(x, *others)
+        q, scale = quantize_rows(_rows(x), kind, group)
+        tensors = [t if isinstance(t, torch.Tensor) else None for t in others]
+        ctx.save_for_backward(q, scale, *tensors)
+        ctx.fn, ctx.group, ctx.shape, ctx.dtype = fn, group, x.shape, x.dtype
+        ctx.plain = [None if isinstance(t, torch.Tensor) else t for t in others]
+        ctx.set_materialize_grads(False)
+        return out
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, *grads):
+        q, scale, *others = ctx.saved_tensors
+        x = dequantize_rows(q, scale, ctx.group, ctx.dtype).reshape(ctx.shape)
+        need = ctx.needs_input_grad[3:]
+        args = [t.detach().requires_grad_(n) if isinstance(t, torch.Tensor) else p
+                for t, p, n in zip([x, *others], [None, *ctx.plain], need)]
+        with torch.enable_grad():
+            out = ctx.fn(*args)
+        out = [out] if isinstance(out, torch.Tensor) else list(out)
+        pairs = [(o, g) for o, g in zip(out, grads) if g is not None and isinstance(o, torch.Tensor) and o.requires_grad]
+        if pairs:
+            torch.autograd.backward([o for o, _ in pairs], [g for _, g in pairs])
+        return (None, None, None, *(a.grad if isinstance(a, torch.Tensor) and n else None for a, n in zip(args, need)))
+
+
+def checkpoint_8bit(fn, x, *others, kind="int8", group=128):
+    """fn(x, *others), keeping x in 8 bits for the backward pass (any shape, groups along the last axis) and nothing
+    of what fn computes: the backward pass runs fn again on what those 8 bits stand for, and its gradients are exactly
+    the gradients there.  others (tensors or not) are kept as they are.  Tensors that fn takes from elsewhere get their
+    .grad from backward(), as parameters do; torch.autograd.grad with respect to them needs them among the others.  fn
+    has to compute the same both times: random numbers and autocast belong inside it or not in it."""
+    if not isinstance(x, torch.Tensor) or x.dim() == 0:
+        raise TypeError("x must be a tensor of at least one axis")
+    if x.dtype not in B.TYPES:
+        raise TypeError(f"x must be one of {', '.join(map(str, B.TYPES))}, got {x.dtype}")
+    B._kind(kind, group)
+    if not torch.is_grad_enabled() or not any(isinstance(t, torch.Tensor) and t.requires_grad for t in (x, *others)):
+        return fn(x, *others)  # nothing of it is kept, or only what fn takes from elsewhere needs it
+    return _Checkpoint.apply(fn, kind, int(group), x, *others)
+
+
+# ---------------------------------------------------------------- layer norm
+def layer_norm_forward(x, weight=None, bias=None, mask=None, eps=1e-5, checkpoint=None, group=128):
+    """y [T,d], mean [T], rstd [T] and, with checkpoint "int8" or "e4m3", x in 8 bits (q, scale) for the backward
+    (else None)."""
+    T, d = B._norm_in(x, weight, bias, mask)
+    y, mean, rstd = torch.empty_like(x), _f32(x, T), _f32(x, T)
+    if checkpoint is None:
+        B.kd_layer_norm_fwd(x, weight, bias, mask, eps, y, mean, rstd)
+        return y, mean, rstd, None
+    B._kind(checkpoint, group)
+    q = torch.empty(T, d, dtype=B.ROWS_TYPES[checkpoint], device=x.device)
+    scale = _f32(x, T, B._groups(d, group))
+    B.kd_layer_norm_fwd(x, weight, bias, mask, eps, y, mean, rstd, checkpoint, group, q, scale)
+    return y, mean, rstd, (q, scale)
+
+
+def layer_norm_backward(grad, x, weight, mask, mean, rstd, kept=None, group=128, grad_dtype=None,
+                        want=(True, True, True), workspace=None):
+    """dx (grad's type), dweight and dbias (weight's type; without a weight grad_dtype, None: grad's), each None where
+    `want` is false.  kept: the forward's (q, scale) in place of x, which is None then."""
+    T, d = B._norm_in(grad, weight, None, mask, "grad")
+    wt = weight.dtype if weight is not None else grad_dtype or grad.dtype
+    dx = torch.empty_like(grad) if want[0] else None
+    dw, db = (torch.empty(d, dtype=wt, device=grad.device) if w else None for w in want[1:])
+    if workspace is None:
+        workspace = _workspace(B.kd_layer_norm_workspace_size(T, d), grad.device)
+    q, scale = (None, None) if kept is None else kept
+    B.kd_layer_norm_bwd(grad, x, weight, mask, mean, rstd, dx, dw, db, workspace, group, q, scale)
+    return dx, dw, db
+
+
+class _LayerNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, mask, eps, checkpoint, group):
+        need = any(ctx.needs_input_grad[:3])
+        y, mean, rstd, kept = layer_norm_forward(x, weight, bias, mask, eps, checkpoint if need else None, group)
+        ctx.save_for_backward(x if kept is None else None, weight, mask, mean, rstd, *(kept or (None, None)))
+        ctx.group, ctx.wtype = group, None if bias is None else bias.dtype
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, g):
+        x, weight, mask, mean, rstd, q, scale = ctx.saved_tensors
+        grads = layer_norm_backward(g.contiguous(), x, weight, mask, mean, rstd, None if q is None else (q, scale),
+                                    ctx.group, ctx.wtype, ctx.needs_input_grad[:3])
+        return (*grads, None, None, None, None)
+
+
+def layer_norm(x, weight=None, bias=None, mask=None, eps=1e-5, checkpoint=None, group=128):
+    """Layer norm of the rows of x [T,d], 0 on masked rows; differentiable in x, weight and bias, whose gradients have
+    their types.  weight and bias are of x's type or float32.  checkpoint "int8" or "e4m3": the backward pass takes x
+    from 8 bits, in groups of `group` values with a scale each, and x itself is not kept."""
+    return _LayerNorm.apply(x, weight, bias, mask, float(eps), checkpoint, int(group))
+
+
+# ---------------------------------------------------------------- product of 8-bit integers
+def int8_matmul(x, x_scale, w, w_scale, out_dtype=torch.bfloat16, workspace=None):
+    """out [T,V] = x w^T with x_scale [T] and w_scale [V] (or [T,1], [V,1]): x [T,d] int8, w [V,d] int8 with a row for
+    each channel, d a multiple of 16.  quantize_rows(H, "int8", 0) gives x, quantize_rows of a head's transpose w."""
+    T, d = B._matrix("x", x, None, B._I8)
+    V, _ = B._matrix("w", w, None, B._I8)
+    out = torch.empty(T, V, dtype=out_dtype, device=x.device)
+    if workspace is None:
+        workspace = _workspace(B.kd_int8_matmul_workspace_size(T, d, V), x.device)
+    B.kd_int8_matmul(x, x_scale, w, w_scale, out, workspace)
+    return out

@@ -1,0 +1,151 @@
+"""Rows in 8 bits against their exact definition, bit for bit."""
+import pytest
+import torch
+
+import chunked_kl_loss_logit_amd as kd
+from tests import layers_util as R
+from tests.gpu_util import say
+
+pytestmark = pytest.mark.gpu
+
+SHAPES = [(1, 1), (3, 31), (2, 32), (70, 33), (5, 129), (33, 1000), (64, 1337), (9, 4096), (4, 8200), (3, 16384),
+          (2, 16385), (2, 40007)]
+KINDS = ["int8", "e4m3"]
+
+
+def compare(x, kind, group):
+    q, scale = kd.quantize_rows(x.cuda(), kind, group)
+    wq, ws = R.rows_reference(x, kind, group)
+    assert torch.equal(scale.cpu().nan_to_num(-1.0), ws.nan_to_num(-1.0)), "scale"
+    assert torch.equal(scale.cpu().isnan(), ws.isnan())
+    got = q.cpu().double()
+    wrong = (got != wq).nonzero()
+    assert len(wrong) == 0, f"{len(wrong)} values, first {wrong[0].tolist()}: {got[tuple(wrong[0])]} for {wq[tuple(wrong[0])]}"
+    for dtype in R.TYPES:
+        back = kd.dequantize_rows(q, scale, group, dtype).cpu()
+        want = R.rows_values(wq, ws, group).float().to(dtype)  # one product in 32 bits, then the type's rounding
+        assert torch.equal(back.isnan(), want.isnan()) and torch.equal(back.nan_to_num(), want.nan_to_num()), dtype
+
+
+@pytest.mark.parametrize("group", [0, 32, 64, 128, 256, 512])
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("dtype", R.TYPES)
+def test_shapes(dtype, kind, group):
+    for T, d in SHAPES:
+        say(f"rows {dtype} {kind} group={group} T={T} d={d}")
+        x = (torch.randn(T, d, generator=R.gen(T * d + group)) * torch.rand(T, 1, generator=R.gen(7)) * 3).to(dtype)
+        compare(x, kind, group)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_next_to_the_middle_of_two_steps(kind):
+    """Values whose quotient is a tie, and their neighbours on both sides: rounding must see the exact quotient."""
+    top = 127.0 if kind == "int8" else 448.0
+    if kind == "int8":
+        mids = torch.arange(-126.5, 127, 1.0, dtype=torch.float64)
+    else:
+        grid = R.e4m3_grid()
+        mids = (grid[1:] + grid[:-1]) / 2
+        mids = torch.cat([-mids, mids])
+    rows = []
+    for k in range(200):
+        s = torch.rand((), generator=R.gen(k), dtype=torch.float64) * 2.0 ** ((k % 40) - 20)
+        scale = ((s * top).float().double() / top).float().double()
+        at = (mids * scale).float()
+        near = torch.stack([at, torch.nextafter(at, at * 2), torch.nextafter(at, at * 0)]).flatten()
+        rows.append(torch.cat([(s * top).float()[None], near.clamp(-float((s * top).float()), float((s * top).float()))]))
+    x = torch.stack(rows)
+    say(f"rows {kind}: {x.numel()} values at ties")
+    compare(x, kind, 0)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_ties_go_to_even(kind):
+    top = 127.0 if kind == "int8" else 448.0
+    for e in (-20, 0, 9):
+        v = torch.arange(-126.5, 127, 1.0) if kind == "int8" else ((R.e4m3_grid()[1:] + R.e4m3_grid()[:-1]) / 2).float()
+        x = torch.cat([torch.tensor([top]), v])[None] * 2.0 ** e
+        compare(x, kind, 0)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("group", [0, 32])
+def test_small_large_and_not_finite(kind, group):
+    g = R.gen(3)
+    base = torch.randn(12, 96, generator=g)
+    x = base.clone()
+    x[0] = 0
+    x[1] = -0.0
+    x[2] *= 1e-38
+    x[3] *= 1e-40  # subnormal
+    x[4] = 0
+    x[4, 5] = 2.0 ** -149  # a scale that rounds to 0
+    x[5] *= 1e38 / 5
+    x[6, 40] = float("inf")
+    x[7, 3] = float("-inf")
+    x[8, 95] = float("nan")
+    x[9] = 0
+    x[9, 70] = torch.finfo(torch.float32).max
+    x[10] = torch.linspace(-1e-30, 1e-30, 96)
+    x[11, :64] *= 2.0 ** -95
+    compare(x, kind, group)
+    compare(x.to(torch.float16), kind, group)
+    compare(x.to(torch.bfloat16), kind, group)
+
+
+def test_every_value_of_a_16_bit_type():
+    """All finite bfloat16 and float16 values with a scale each."""
+    for dtype in (torch.bfloat16, torch.float16):
+        v = torch.arange(-32768, 32768, dtype=torch.int32).to(torch.int16).view(dtype)
+        v = v[torch.isfinite(v)]
+        x = v[: v.numel() // 64 * 64].reshape(-1, 64)
+        for kind in KINDS:
+            compare(x, kind, 32)
+
+
+def test_nothing_and_offsets_beyond_32_bits():
+    q, s = kd.quantize_rows(torch.empty(0, 64, device="cuda"), "int8", 32)
+    assert q.shape == (0, 64) and s.shape == (0, 2) and kd.dequantize_rows(q, s, 32).shape == (0, 64)
+    T, d = 1100000, 4096
+    say(f"rows T={T} d={d}")
+    x = torch.empty(T, d, dtype=torch.bfloat16, device="cuda").normal_(generator=torch.Generator("cuda").manual_seed(1))
+    q, s = kd.quantize_rows(x, "int8", 128)
+    back = kd.dequantize_rows(q, s, 128)
+    for a in (0, T // 2, T - 64):
+        part = kd.quantize_rows(x[a:a + 64].contiguous(), "int8", 128)
+        assert torch.equal(q[a:a + 64], part[0]) and torch.equal(s[a:a + 64], part[1])
+        assert torch.equal(back[a:a + 64], kd.dequantize_rows(*part, 128))
+
+
+# ------------------------------------------------------------------ checkpoints
+@pytest.mark.parametrize("kind", KINDS)
+def test_checkpoint_gives_the_gradients_at_what_8_bits_hold(kind):
+    g = R.gen(1)
+    x = torch.randn(2, 33, 70, generator=g).cuda().requires_grad_(True)
+    w = torch.randn(70, 20, generator=g).cuda().requires_grad_(True)
+    b = torch.randn(20, generator=g).cuda().requires_grad_(True)  # from elsewhere
+
+    def block(x, w, k):
+        return torch.tanh(x @ w) * k + b
+
+    up = torch.randn(2, 33, 20, generator=g).cuda()
+    y = kd.checkpoint_8bit(block, x, w, 0.5, kind=kind, group=32)
+    assert torch.equal(y, block(x, w, 0.5))  # the forward pass sees x itself
+    y.backward(up)
+    q, s = kd.quantize_rows(x.detach().reshape(-1, 70), kind, 32)
+    xd = kd.dequantize_rows(q, s, 32, torch.float32).reshape(x.shape).requires_grad_(True)
+    wd = w.detach().clone().requires_grad_(True)
+    dx, dw, db = torch.autograd.grad(block(xd, wd, 0.5), (xd, wd, b), up)
+    assert torch.equal(x.grad, dx) and torch.equal(w.grad, dw) and torch.equal(b.grad, db)
+
+
+def test_checkpoint_of_several_outputs_and_of_nothing_to_keep():
+    x = torch.randn(8, 64, device="cuda", requires_grad=True)
+    w = torch.randn(64, 64, device="cuda", requires_grad=True)
+    a, b = kd.checkpoint_8bit(lambda x: (x * 2, x @ w), x)
+    (dx,) = torch.autograd.grad(b.sum(), x)
+    torch.testing.assert_close(dx, torch.ones(8, 64, device="cuda") @ w.t(), rtol=1e-5, atol=1e-5)
+    y = kd.checkpoint_8bit(lambda x: x @ w, x.detach())  # only w, from elsewhere, needs a gradient
+    assert torch.autograd.grad(y.sum(), w)[0].shape == w.shape
+    with torch.no_grad():
+        assert not kd.checkpoint_8bit(lambda x: x @ w, x).requires_grad
