@@ -12,7 +12,7 @@ import ctypes
 import torch
 
 from . import _policy_binding as P
-from ._binding import _F32, _I32, _MASK, _matrix, _need, _one_device, _ptr, _ws_bytes, lib
+from ._binding import _F32, _I32, _MASK, _check, _matrix, _need, _one_device, _ptr, _ws_bytes, lib
 from ._policy_binding import GRAD_TYPES, _choice
 
 TYPES = tuple(GRAD_TYPES)
@@ -39,7 +39,7 @@ def llib() -> ctypes.CDLL:
                                       ctypes.c_size_t, ctypes.c_int)
     psz = ctypes.POINTER(sz)
     L.kd_embedding_fwd.argtypes = [vp, vp, vp, f32, i64, i64, i64, st, i32, vp, vp]
-    L.kd_embedding_workspace_size.argtypes = [i64, i64, i64, psz]
+    L.kd_embedding_workspace_size.argtypes = [i64, i64, i64, i32, psz]
     L.kd_embedding_bwd.argtypes = [vp, vp, vp, f32, i64, i64, i64, st, st, i32, i32, vp, vp, sz, vp]
     L.kd_rows_quantize.argtypes = [vp, i64, i64, st, st, i64, vp, vp, vp]
     L.kd_rows_dequantize.argtypes = [vp, vp, i64, i64, st, i64, st, vp, vp]
@@ -59,9 +59,42 @@ def _size(fn, *args) -> int:
     return P._size(fn, *args)
 
 
-def _run(name, t, stream, *args):
-    llib()
-    P._run(name, t, stream, *args)
+def _place(*tensors):
+    """The tensors' device index and their pointers (None stays None): all on one GPU, all contiguous.  One pass, as
+    small calls take no longer on the GPU than on the host."""
+    index, ptrs = None, []
+    for t in tensors:
+        if t is None:
+            ptrs.append(None)
+            continue
+        i = t.get_device()
+        if i != index:
+            if index is not None or i < 0:
+                _one_device(*tensors)
+                _ptr(t)  # not on a GPU
+            index = i
+        if not t.is_contiguous():
+            _ptr(t)
+        ptrs.append(t.data_ptr())
+    return index, ptrs
+
+
+_entries = {}
+
+
+def _run(name, index, stream, *args):
+    """Calls a library function on a device, on its current stream unless one is given."""
+    fn = _entries.get(name)
+    if fn is None:
+        fn = _entries[name] = getattr(llib(), name)
+    handle = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    if index == torch.cuda.current_device():
+        status = fn(*args, handle)
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, handle)
+    if status != 0:
+        _check(status, name)
 
 
 def _kind(kind, group):
@@ -77,8 +110,8 @@ def _groups(d, group):
 
 
 # ---------------------------------------------------------------- token embeddings
-def kd_embedding_workspace_size(T, V, d) -> int:
-    return _size("kd_embedding_workspace_size", T, V, d)
+def kd_embedding_workspace_size(T, V, d, tied=False) -> int:
+    return _size("kd_embedding_workspace_size", T, V, d, int(bool(tied)))
 
 
 def _tokens(tokens, mask):
@@ -90,15 +123,24 @@ def _tokens(tokens, mask):
     return T
 
 
-def kd_embedding_fwd(tokens, table, mask, scale, tied, out, stream=None):
-    """Enqueue the lookup; out [T,d] in place."""
+def _embedding_in(tokens, table, mask, tied):
+    """T, V and d."""
     T = _tokens(tokens, mask)
     n, m = _matrix("table", table, None, TYPES)
-    V, d = (m, n) if tied else (n, m)
+    return (T, m, n) if tied else (T, n, m)
+
+
+def _embedding_fwd(T, V, d, tokens, table, mask, scale, tied, out, stream=None):
+    index, (tokens, src, mask, out) = _place(tokens, table, mask, out)
+    _run("kd_embedding_fwd", index, stream, tokens, src, mask, float(scale), T, V, d, GRAD_TYPES[table.dtype],
+         bool(tied), out)
+
+
+def kd_embedding_fwd(tokens, table, mask, scale, tied, out, stream=None):
+    """Enqueue the lookup; out [T,d] in place."""
+    T, V, d = _embedding_in(tokens, table, mask, tied)
     _need("out", out, (T, d), (table.dtype,))
-    _one_device(tokens, table, mask, out)
-    _run("kd_embedding_fwd", table, stream, _ptr(tokens), _ptr(table), _ptr(mask), float(scale), T, V, d,
-         GRAD_TYPES[table.dtype], int(bool(tied)), _ptr(out))
+    _embedding_fwd(T, V, d, tokens, table, mask, scale, tied, out, stream)
 
 
 def kd_embedding_bwd(grad, tokens, mask, scale, V, tied, accumulate, grad_table, workspace, stream=None):
@@ -107,10 +149,9 @@ def kd_embedding_bwd(grad, tokens, mask, scale, V, tied, accumulate, grad_table,
     _, d = _matrix("grad", grad, T, TYPES)
     _need("grad_table", grad_table, (d, V) if tied else (V, d), TYPES)
     nb = _ws_bytes(workspace)
-    _one_device(grad, tokens, mask, grad_table, workspace)
-    _run("kd_embedding_bwd", grad_table, stream, _ptr(grad), _ptr(tokens), _ptr(mask), float(scale), T, int(V), d,
-         GRAD_TYPES[grad.dtype], GRAD_TYPES[grad_table.dtype], int(bool(tied)), int(bool(accumulate)),
-         _ptr(grad_table), _ptr(workspace), nb)
+    index, (g, tokens, mask, out, ws) = _place(grad, tokens, mask, grad_table, workspace)
+    _run("kd_embedding_bwd", index, stream, g, tokens, mask, float(scale), T, int(V), d, GRAD_TYPES[grad.dtype],
+         GRAD_TYPES[grad_table.dtype], bool(tied), bool(accumulate), out, ws, nb)
 
 
 # ---------------------------------------------------------------- rows in 8 bits
@@ -125,21 +166,24 @@ def _quantized(q, scale, group, T=None, d=None, kind=None):
     return kind, n, m
 
 
+def _rows_quantize(T, d, x, code, group, q, scale, stream=None):
+    index, (src, q, scale) = _place(x, q, scale)
+    _run("kd_rows_quantize", index, stream, src, T, d, GRAD_TYPES[x.dtype], code, group, q, scale)
+
+
 def kd_rows_quantize(x, kind, group, q, scale, stream=None):
     """Enqueue the rounding to 8 bits; q [T,d] and scale [T, groups] in place."""
     T, d = _matrix("x", x, None, TYPES)
     code = _kind(kind, group)
     _quantized(q, scale, group, T, d, kind)
-    _one_device(x, q, scale)
-    _run("kd_rows_quantize", x, stream, _ptr(x), T, d, GRAD_TYPES[x.dtype], code, int(group), _ptr(q), _ptr(scale))
+    _rows_quantize(T, d, x, code, group, q, scale, stream)
 
 
 def kd_rows_dequantize(q, scale, group, out, stream=None):
     kind, T, d = _quantized(q, scale, group)
     _need("out", out, (T, d), TYPES)
-    _one_device(q, scale, out)
-    _run("kd_rows_dequantize", out, stream, _ptr(q), _ptr(scale), T, d, ROWS_KINDS[kind], int(group),
-         GRAD_TYPES[out.dtype], _ptr(out))
+    index, (q, scale, to) = _place(q, scale, out)
+    _run("kd_rows_dequantize", index, stream, q, scale, T, d, ROWS_KINDS[kind], group, GRAD_TYPES[out.dtype], to)
 
 
 # ---------------------------------------------------------------- layer norm
@@ -162,6 +206,12 @@ def _norm_type(x, weight, bias):
     return GRAD_TYPES[x.dtype if given is None else given.dtype]
 
 
+def _layer_norm_fwd(T, d, x, weight, bias, mask, eps, y, mean, rstd, code=0, group=0, q=None, scale=None, stream=None):
+    index, (src, w, b, mask, y, mean, rstd, q, scale) = _place(x, weight, bias, mask, y, mean, rstd, q, scale)
+    _run("kd_layer_norm_fwd", index, stream, src, w, b, mask, float(eps), T, d, GRAD_TYPES[x.dtype],
+         _norm_type(x, weight, bias), y, mean, rstd, code, group, q, scale)
+
+
 def kd_layer_norm_fwd(x, weight, bias, mask, eps, y, mean, rstd, kind=None, group=0, q=None, scale=None, stream=None):
     """Enqueue the forward; y, mean, rstd (None: not kept) and, of a kind, q and scale in place."""
     T, d = _norm_in(x, weight, bias, mask)
@@ -174,15 +224,11 @@ def kd_layer_norm_fwd(x, weight, bias, mask, eps, y, mean, rstd, kind=None, grou
         _quantized(q, scale, group, T, d, kind)
     elif q is not None or scale is not None:
         raise ValueError("q and scale need a kind")
-    _one_device(x, weight, bias, mask, y, mean, rstd, q, scale)
-    _run("kd_layer_norm_fwd", x, stream, _ptr(x), _ptr(weight), _ptr(bias), _ptr(mask), float(eps), T, d,
-         GRAD_TYPES[x.dtype], _norm_type(x, weight, bias), _ptr(y), _ptr(mean), _ptr(rstd), code, int(group), _ptr(q),
-         _ptr(scale))
+    _layer_norm_fwd(T, d, x, weight, bias, mask, eps, y, mean, rstd, code, group, q, scale, stream)
 
 
-def kd_layer_norm_bwd(grad, x, weight, mask, mean, rstd, dx, dweight, dbias, workspace, group=0, q=None, scale=None,
-                      stream=None):
-    """Enqueue the backward; dx, dweight and dbias (None: not wanted) in place.  x, or q and scale in its place."""
+def _norm_bwd_in(grad, x, weight, mask, mean, rstd, group, q, scale):
+    """T, d and the code of the kind of 8-bit rows that stand for x."""
     T, d = _norm_in(grad, weight, None, mask, "grad")
     code = 0
     if q is None:
@@ -193,8 +239,24 @@ def kd_layer_norm_bwd(grad, x, weight, mask, mean, rstd, dx, dweight, dbias, wor
         if x is not None:
             raise ValueError("x must be None where q and scale stand for it")
         code = ROWS_KINDS[_quantized(q, scale, group, T, d)[0]]
-    for n, t in (("mean", mean), ("rstd", rstd)):
-        _need(n, t, (T,), _F32)
+    _need("mean", mean, (T,), _F32)
+    _need("rstd", rstd, (T,), _F32)
+    return T, d, code
+
+
+def _layer_norm_bwd(T, d, code, wtype, grad, x, weight, mask, mean, rstd, dx, dweight, dbias, workspace, group, q, scale,
+                    stream=None):
+    nb = _ws_bytes(workspace)
+    index, (g, x, w, mask, mean, rstd, q, scale, dx, dw, db, ws) = _place(
+        grad, x, weight, mask, mean, rstd, q, scale, dx, dweight, dbias, workspace)
+    _run("kd_layer_norm_bwd", index, stream, g, x, w, mask, mean, rstd, T, d, GRAD_TYPES[grad.dtype], GRAD_TYPES[wtype],
+         code, group, q, scale, dx, dw, db, ws, nb)
+
+
+def kd_layer_norm_bwd(grad, x, weight, mask, mean, rstd, dx, dweight, dbias, workspace, group=0, q=None, scale=None,
+                      stream=None):
+    """Enqueue the backward; dx, dweight and dbias (None: not wanted) in place.  x, or q and scale in its place."""
+    T, d, code = _norm_bwd_in(grad, x, weight, mask, mean, rstd, group, q, scale)
     _need("dx", dx, (T, d), (grad.dtype,), optional=True)
     wtypes = (grad.dtype, torch.float32) if weight is None else (weight.dtype,)
     for n, t in (("dweight", dweight), ("dbias", dbias)):
@@ -203,12 +265,9 @@ def kd_layer_norm_bwd(grad, x, weight, mask, mean, rstd, dx, dweight, dbias, wor
         raise TypeError(f"dweight and dbias must have one type, got {dweight.dtype} and {dbias.dtype}")
     if dx is None and dweight is None and dbias is None:
         raise ValueError("dx, dweight and dbias are all None")
-    wt = next((t.dtype for t in (weight, dweight, dbias) if t is not None), grad.dtype)
-    nb = _ws_bytes(workspace)
-    _one_device(grad, x, weight, mask, mean, rstd, q, scale, dx, dweight, dbias, workspace)
-    _run("kd_layer_norm_bwd", grad, stream, _ptr(grad), _ptr(x), _ptr(weight), _ptr(mask), _ptr(mean), _ptr(rstd), T, d,
-         GRAD_TYPES[grad.dtype], GRAD_TYPES[wt], code, int(group), _ptr(q), _ptr(scale), _ptr(dx), _ptr(dweight),
-         _ptr(dbias), _ptr(workspace), nb)
+    wtype = next((t.dtype for t in (weight, dweight, dbias) if t is not None), grad.dtype)
+    _layer_norm_bwd(T, d, code, wtype, grad, x, weight, mask, mean, rstd, dx, dweight, dbias, workspace, group, q, scale,
+                    stream)
 
 
 # ---------------------------------------------------------------- product of 8-bit integers
@@ -223,16 +282,25 @@ def _scales(name, t, n):
         raise ValueError(f"{name} must have shape {(n,)} or {(n, 1)}, got {tuple(t.shape)}")
 
 
-def kd_int8_matmul(x, x_scale, w, w_scale, out, workspace, stream=None):
-    """Enqueue the product; out [T,V] in place."""
+def _int8_in(x, x_scale, w, w_scale):
+    """T, d and V."""
     T, d = _matrix("x", x, None, _I8)
     V, dw = _matrix("w", w, None, _I8)
     if dw != d:
         raise ValueError(f"w must have {d} columns, got shape {tuple(w.shape)}")
     _scales("x_scale", x_scale, T)
     _scales("w_scale", w_scale, V)
-    _need("out", out, (T, V), TYPES)
+    return T, d, V
+
+
+def _int8_matmul(T, d, V, x, x_scale, w, w_scale, out, workspace, stream=None):
     nb = _ws_bytes(workspace)
-    _one_device(x, x_scale, w, w_scale, out, workspace)
-    _run("kd_int8_matmul", x, stream, _ptr(x), _ptr(x_scale), _ptr(w), _ptr(w_scale), T, d, V, GRAD_TYPES[out.dtype],
-         _ptr(out), _ptr(workspace), nb)
+    index, (x, sx, w, sw, to, ws) = _place(x, x_scale, w, w_scale, out, workspace)
+    _run("kd_int8_matmul", index, stream, x, sx, w, sw, T, d, V, GRAD_TYPES[out.dtype], to, ws, nb)
+
+
+def kd_int8_matmul(x, x_scale, w, w_scale, out, workspace, stream=None):
+    """Enqueue the product; out [T,V] in place."""
+    T, d, V = _int8_in(x, x_scale, w, w_scale)
+    _need("out", out, (T, V), TYPES)
+    _int8_matmul(T, d, V, x, x_scale, w, w_scale, out, workspace, stream)

@@ -13,6 +13,8 @@
 // every sum is that of the positions, cut at multiples of the piece: the same
 // bits each time.  A frequent token (the first few take a tenth of a text)
 // then costs as many partial rows as it has pieces, spread over the chip.
+// For tied weights the runs' sums go to rows of their own first, and a third
+// kernel turns them into columns of the head's gradient.
 #include <type_traits>
 
 #include "kd_launch.h"
@@ -30,61 +32,76 @@ constexpr int kSlab = 512;  // columns of a wave
 }  // namespace
 
 // ------------------------------------------------------------------ forward
-template <int TY>
-__global__ __launch_bounds__(256) void embed_kernel(EmbedArgs a, int slabs) {
-  const int64_t waves = (int64_t)gridDim.x * 4;
-  const int lane = threadIdx.x & 63;
-  for (int64_t u = wave_in_grid(); u < a.T * slabs; u += waves) {
-    const int64_t t = u / slabs;
-    const int p = (int)(u - t * slabs) * 64 + lane;
-    const int n = (int)(a.d - 8 * (int64_t)p);
-    if (n <= 0) continue;
-    float x[8];
-    if (a.mask && !a.mask[t]) {
+// A wave takes kSlabs slabs of a row, all their loads in flight at once.
+template <int TY, int SLABS>
+__global__ __launch_bounds__(256) void embed_kernel(EmbedArgs a, int units) {
+  const int wave = wave_in_grid();
+  const int64_t t = wave / units;
+  if (t >= a.T) return;
+  const int p0 = (wave - (int)t * units) * SLABS * 64 + (threadIdx.x & 63);
+  const bool valid = !a.mask || a.mask[t];
+  const int64_t v = valid ? a.tokens[t] : -1;
+  const bool in = v >= 0 && v < a.V;
+  Raw8<TY> r[SLABS];
+  if (in) {
+    const char* row = a.table + v * a.d * Elem<TY>::kBytes;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = 0.f;
-    } else {
-      const int64_t v = a.tokens[t];
-      if (v < 0 || v >= a.V) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(0x7fc00000u);
-      } else {
-        load_row<TY>(a.table + v * a.d * Elem<TY>::kBytes, a.d, p, x);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] *= a.scale;
-      }
+    for (int i = 0; i < SLABS; ++i) {
+      const int64_t at = 8 * (int64_t)(p0 + 64 * i);
+      r[i] = load8<TY>(row + at * Elem<TY>::kBytes, (int)(a.d - at));
     }
-    store8<TY>(a.out + (t * a.d + 8 * (int64_t)p) * Elem<TY>::kBytes, x, n);
+  }
+#pragma unroll
+  for (int i = 0; i < SLABS; ++i) {
+    const int64_t at = 8 * (int64_t)(p0 + 64 * i);
+    if (at >= a.d) continue;
+    float x[8];
+    if (in) {
+      unpack8<TY>(r[i], x);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] *= a.scale;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = valid ? __uint_as_float(0x7fc00000u) : 0.f;
+    }
+    store8<TY>(a.out + (t * a.d + at) * Elem<TY>::kBytes, x, (int)(a.d - at));
   }
 }
 
-// Tied: 64 tokens x 64 rows of W a workgroup.  A lane keeps its token and goes
-// down the rows; the tile is turned in LDS, so that the output is written in
-// runs of 64 elements.
+// Tied: kTiedT tokens x kTiedK rows of W a workgroup.  A lane keeps its token
+// and goes down the rows; the tile is turned in LDS, so that the output is
+// written in runs of kTiedK elements.  Every load takes a cache line for two
+// bytes, and what limits the kernel is how often a line is fetched: workgroups
+// of the same rows of W run on one XCD, next to each other, and share its L2.
+constexpr int kTiedT = 64, kTiedK = 32;
+
 template <int TY>
 __global__ __launch_bounds__(256) void embed_tied_kernel(EmbedArgs a, int blocks_t) {
   using E = Elem<TY>;
-  __shared__ float tile[64][65];
+  constexpr int kPer = kTiedK / 4;  // rows of a wave
+  __shared__ float tile[kTiedT][kTiedK + 1];
   const int lane = threadIdx.x & 63, w = wave_id();
-  const int64_t t0 = (int64_t)(blockIdx.x % blocks_t) * 64, k0 = (int64_t)(blockIdx.x / blocks_t) * 64;
+  const int logical = xcd_remap(blockIdx.x, gridDim.x);
+  const int64_t t0 = (int64_t)(logical % blocks_t) * kTiedT, k0 = (int64_t)(logical / blocks_t) * kTiedK;
   const int64_t t = t0 + lane;
   const bool valid = t < a.T && (!a.mask || a.mask[t]);
   const int64_t v = valid ? a.tokens[t] : 0;
   const bool in = valid && v >= 0 && v < a.V;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int64_t k = k0 + w * 16 + i;
+  for (int i = 0; i < kPer; ++i) {
+    const int64_t k = k0 + w * kPer + i;
     float x = valid ? __uint_as_float(0x7fc00000u) : 0.f;
     if (in && k < a.d) x = E::get1(a.table + (k * a.V + v) * E::kBytes) * a.scale;
-    tile[lane][w * 16 + i] = x;
+    tile[lane][w * kPer + i] = x;
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < 64 * 8; i += 256) {
-    const int64_t to = t0 + (i >> 3), k = k0 + 8 * (i & 7);
+  for (int i = threadIdx.x; i < kTiedT * kTiedK / 8; i += 256) {
+    const int row = i / (kTiedK / 8), c = 8 * (i % (kTiedK / 8));
+    const int64_t to = t0 + row, k = k0 + c;
     if (to >= a.T || k >= a.d) continue;
     float x[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = tile[i >> 3][8 * (i & 7) + j];
+    for (int j = 0; j < 8; ++j) x[j] = tile[row][c + j];
     store8<TY>(a.out + (to * a.d + k) * E::kBytes, x, (int)(a.d - k));
   }
 }
@@ -93,14 +110,17 @@ hipError_t launch_embed(const EmbedArgs& a, hipStream_t st) {
   pick_type(a.type, [&](auto ty) {
     constexpr int TY = decltype(ty)::value;
     if (a.tied) {
-      const int64_t bt = (a.T + 63) / 64, bk = (a.d + 63) / 64;
+      const int64_t bt = (a.T + kTiedT - 1) / kTiedT, bk = (a.d + kTiedK - 1) / kTiedK;
       hipLaunchKernelGGL((embed_tied_kernel<TY>), dim3((unsigned)(bt * bk)), dim3(256), 0, st, a, (int)bt);
-    } else {
-      const int slabs = (int)((a.d + kSlab - 1) / kSlab);
-      const int64_t blocks = (a.T * slabs + 3) / 4;
-      hipLaunchKernelGGL((embed_kernel<TY>), dim3((unsigned)std::min<int64_t>(blocks, 1 << 20)), dim3(256), 0, st, a,
-                         slabs);
+      return;
     }
+    auto with = [&](auto n) {
+      constexpr int N = decltype(n)::value;
+      const int units = (int)((a.d + kSlab * N - 1) / (kSlab * N));
+      hipLaunchKernelGGL((embed_kernel<TY, N>), dim3((unsigned)((a.T * units + 3) / 4)), dim3(256), 0, st, a, units);
+    };
+    if (a.T * a.d <= (1 << 20)) with(std::integral_constant<int, 1>());  // waves for the whole chip first
+    else with(std::integral_constant<int, 4>());
   });
   return hipGetLastError();
 }
@@ -173,57 +193,70 @@ int bits_of(int64_t V) {  // of the keys 0 .. V
 
 }  // namespace
 
-// Up to kSortSmall tokens in one workgroup: digits of 6 bits, keys and
-// positions in LDS between the passes and in registers within one.
-template <int ROUNDS>
-__global__ __launch_bounds__(1024) void sort_small_kernel(SortArgs a, int bits) {
-  __shared__ uint32_t keys[1024 * ROUNDS], poss[1024 * ROUNDS];
-  __shared__ uint32_t seen[64 * 16], lds[16];
+// Up to kSortSmall tokens: chunks of 1024, each sorted by one workgroup in LDS
+// with digits of 6 bits, and then every entry's place among all chunks by
+// binary search in each of them.  (One workgroup for all of 16384 tokens took
+// 44 us, the instructions of 16 waves on one CU.)
+__global__ __launch_bounds__(1024) void sort_chunk_kernel(SortArgs a, int bits, int to_result) {
+  __shared__ uint32_t keys[kSortChunk], poss[kSortChunk];
+  __shared__ uint32_t seen[16 * 65], lds[16];  // [wave][digit]
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  uint32_t k[ROUNDS], p[ROUNDS];
-#pragma unroll
-  for (int r = 0; r < ROUNDS; ++r) {
-    const int64_t i = (int64_t)w * 64 * ROUNDS + r * 64 + lane;
-    k[r] = i < a.T ? key_of(a, i) : 0xffffffffu;  // behind the last one, and stays there
-    p[r] = (uint32_t)i;
-  }
+  const int64_t i = (int64_t)blockIdx.x * kSortChunk + threadIdx.x;
+  uint32_t k = i < a.T ? key_of(a, i) : 0xffffffffu;  // behind the last one, and stays there
+  uint32_t p = (uint32_t)i;
   for (int shift = 0; shift < bits; shift += 6) {
-    seen[threadIdx.x] = 0;
+    seen[w * 65 + lane] = 0;
     __syncthreads();
-    uint32_t at[ROUNDS];
-#pragma unroll
-    for (int r = 0; r < ROUNDS; ++r) {
-      const uint32_t digit = (k[r] >> shift) & 63u;
-      at[r] = place_in_wave(same_digit<6>(digit), &seen[digit * 16 + w]);
-    }
+    const uint32_t digit = (k >> shift) & 63u;
+    const uint32_t at = place_in_wave(same_digit<6>(digit), &seen[w * 65 + digit]);
     __syncthreads();
-    const uint32_t base = block_exclusive(seen[threadIdx.x], lds);
+    uint32_t* const mine = &seen[(threadIdx.x & 15) * 65 + (threadIdx.x >> 4)];  // in the order digit, wave
+    const uint32_t base = block_exclusive(*mine, lds);
+    *mine = base;
     __syncthreads();
-    seen[threadIdx.x] = base;
+    const uint32_t to = seen[w * 65 + digit] + at;
+    keys[to] = k;
+    poss[to] = p;
     __syncthreads();
-#pragma unroll
-    for (int r = 0; r < ROUNDS; ++r) {
-      const uint32_t to = seen[((k[r] >> shift) & 63u) * 16 + w] + at[r];
-      keys[to] = k[r];
-      poss[to] = p[r];
-    }
-    __syncthreads();
-#pragma unroll
-    for (int r = 0; r < ROUNDS; ++r) {
-      const int i = w * 64 * ROUNDS + r * 64 + lane;
-      k[r] = keys[i];
-      p[r] = poss[i];
-    }
-    __syncthreads();
+    k = keys[threadIdx.x];
+    p = poss[threadIdx.x];
   }
-#pragma unroll
-  for (int r = 0; r < ROUNDS; ++r) {
-    const int64_t i = (int64_t)w * 64 * ROUNDS + r * 64 + lane;
-    if (i < a.T) {
-      a.key[0][i] = k[r];
-      a.pos[0][i] = p[r];
-    }
+  if (i < a.T) {
+    a.key[to_result ? 0 : 1][i] = k;
+    a.pos[to_result ? 0 : 1][i] = p;
   }
+}
+
+// 256 entries of one chunk a workgroup; every chunk's keys in LDS.
+__global__ __launch_bounds__(256) void sort_rank_kernel(SortArgs a) {
+  extern __shared__ uint32_t keys[];
+  const int T = (int)a.T, chunks = (T + kSortChunk - 1) / kSortChunk;
+  for (int i = 4 * threadIdx.x; i < T; i += 1024) {
+    if (i + 4 <= T)
+      *reinterpret_cast<u32x4_t*>(keys + i) = ld16(reinterpret_cast<const char*>(a.key[1] + i));
+    else
+      for (int j = i; j < T; ++j) keys[j] = a.key[1][j];
+  }
+  __syncthreads();
+  const int i = blockIdx.x * 256 + threadIdx.x;
+  if (i >= T) return;
+  const int own = i / kSortChunk;
+  const uint32_t k = keys[i];
+  uint32_t place = (uint32_t)(i - own * kSortChunk);
+#pragma unroll 4
+  for (int c = 0; c < chunks; ++c) {
+    if (c == own) continue;
+    const uint32_t* in = keys + c * kSortChunk;
+    const int n = min(kSortChunk, T - c * kSortChunk);
+    const uint32_t v = c < own ? k + 1 : k;  // earlier chunks' equal keys come first
+    int lo = 0;                              // entries below v
+#pragma unroll
+    for (int step = kSortChunk; step > 0; step >>= 1)
+      if (lo + step <= n && in[lo + step - 1] < v) lo += step;
+    place += (uint32_t)lo;
+  }
+  a.key[0][place] = k;
+  a.pos[0][place] = a.pos[1][i];
 }
 
 // More tokens: per pass of 9 bits the workgroups' counts of every digit, their
@@ -321,10 +354,10 @@ int sort_passes(int64_t V) { return (bits_of(V) + kDigitBits - 1) / kDigitBits; 
 int sort_result(int64_t T, int64_t V) { return T <= kSortSmall ? 0 : (sort_passes(V) - 1) & 1; }
 
 hipError_t launch_sort_small(const SortArgs& a, hipStream_t st) {
-  const int bits = bits_of(a.V);
-  if (a.T <= 1024) hipLaunchKernelGGL((sort_small_kernel<1>), dim3(1), dim3(1024), 0, st, a, bits);
-  else if (a.T <= 4096) hipLaunchKernelGGL((sort_small_kernel<4>), dim3(1), dim3(1024), 0, st, a, bits);
-  else hipLaunchKernelGGL((sort_small_kernel<16>), dim3(1), dim3(1024), 0, st, a, bits);
+  const unsigned chunks = (unsigned)((a.T + kSortChunk - 1) / kSortChunk);
+  hipLaunchKernelGGL(sort_chunk_kernel, dim3(chunks), dim3(kSortChunk), 0, st, a, bits_of(a.V), chunks == 1 ? 1 : 0);
+  if (chunks > 1)
+    hipLaunchKernelGGL(sort_rank_kernel, dim3((unsigned)((a.T + 255) / 256)), dim3(256), (unsigned)a.T * 4, st, a);
   return hipGetLastError();
 }
 hipError_t launch_sort_count(const SortArgs& a, int pass, hipStream_t st) {
@@ -350,24 +383,28 @@ __device__ inline float get_any1(const char* base, int type, int64_t i) {
   return Elem<kTypeF16>::get1(base + 2 * i);
 }
 
-// dE_v's piece p from the sum x
-__device__ inline void put_sum(const EmbedGradArgs& a, int64_t v, int p, const float (&x)[8]) {
-  const int64_t n = a.d - 8 * (int64_t)p;
+// f with the gradient's type as a constant
+template <class F>
+__device__ inline void with_type(int type, F&& f) {
+  if (type == kTypeF32) f(std::integral_constant<int, kTypeF32>());
+  else if (type == kTypeBf16) f(std::integral_constant<int, kTypeBf16>());
+  else f(std::integral_constant<int, kTypeF16>());
+}
+
+// Piece p of the slab of columns from the sum x of the run of token v that
+// begins at entry `first`: to the table, or for tied weights to the run's row
+// of sums.
+__device__ inline void put_sum(const EmbedGradArgs& a, int64_t v, int64_t first, int p, const float (&x)[8]) {
+  const int64_t n = a.cols - 8 * (int64_t)p;
   if (n <= 0) return;
   float y[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) y[i] = x[i] * a.scale;
   if (a.tied) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (i >= n) continue;
-      const int64_t at = (8 * (int64_t)p + i) * a.V + v;
-      if (a.accumulate) y[i] += get_any1(a.out, a.grad_type, at);
-      store_any1(a.out, a.grad_type, at, y[i]);
-    }
+    store8<kTypeF32>(reinterpret_cast<char*>(a.sums + first * a.cols + 8 * (int64_t)p), y, (int)n);
     return;
   }
-  auto put = [&](auto ty) {
+  with_type(a.grad_type, [&](auto ty) {
     constexpr int G = decltype(ty)::value;
     char* row = a.out + v * a.d * Elem<G>::kBytes;
     if (a.accumulate) {
@@ -377,16 +414,15 @@ __device__ inline void put_sum(const EmbedGradArgs& a, int64_t v, int p, const f
       for (int i = 0; i < 8; ++i) y[i] += was[i];
     }
     store8<G>(row + 8 * (int64_t)p * Elem<G>::kBytes, y, (int)n);
-  };
-  if (a.grad_type == kTypeF32) put(std::integral_constant<int, kTypeF32>());
-  else if (a.grad_type == kTypeBf16) put(std::integral_constant<int, kTypeBf16>());
-  else put(std::integral_constant<int, kTypeF16>());
+  });
 }
 
+__device__ inline float* part_row(const EmbedGradArgs& a, int64_t piece, int which) {
+  return a.part + (piece * 2 + which) * a.cols;
+}
 __device__ inline void put_part(const EmbedGradArgs& a, int64_t piece, int which, int p, const float (&x)[8]) {
-  const int64_t n = a.d - 8 * (int64_t)p;
-  if (n <= 0) return;
-  store8<kTypeF32>(reinterpret_cast<char*>(a.part + (piece * 2 + which) * a.d + 8 * (int64_t)p), x, (int)n);
+  const int64_t n = a.cols - 8 * (int64_t)p;
+  if (n > 0) store8<kTypeF32>(reinterpret_cast<char*>(part_row(a, piece, which) + 8 * (int64_t)p), x, (int)n);
 }
 
 // the first entry whose key is at least v
@@ -443,6 +479,7 @@ __global__ __launch_bounds__(256) void embed_grad_kernel(EmbedGradArgs a, int64_
   float x[8] = {};
   uint32_t v = lane_of(keys, 0);
   bool first = before == v;  // the run began in the piece before
+  int from = 0;              // where it begins in this one
   constexpr int U = 4;
   for (int e = 0; e < ne; e += U) {
     Raw8<TY> r[U];
@@ -450,8 +487,8 @@ __global__ __launch_bounds__(256) void embed_grad_kernel(EmbedGradArgs a, int64_
     for (int u = 0; u < U; ++u) {
       const int i = min(e + u, ne - 1);
       const int64_t t = lane_of(poss, i);
-      r[u] = load8<TY>(a.grad + (t * a.d + 8 * (int64_t)p) * Elem<TY>::kBytes,
-                       lane_of(keys, i) < (uint32_t)a.V ? (int)(a.d - 8 * (int64_t)p) : 0);
+      r[u] = load8<TY>(a.grad + (t * a.d + a.col0 + 8 * (int64_t)p) * Elem<TY>::kBytes,
+                       lane_of(keys, i) < (uint32_t)a.V ? (int)(a.cols - 8 * (int64_t)p) : 0);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -459,9 +496,10 @@ __global__ __launch_bounds__(256) void embed_grad_kernel(EmbedGradArgs a, int64_
       const uint32_t k = lane_of(keys, e + u);
       if (k != v) {
         if (first) put_part(a, piece, 0, p, x);
-        else put_sum(a, v, p, x);
+        else put_sum(a, v, e0 + from, p, x);
         first = false;
         v = k;
+        from = e + u;
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] = 0.f;
       }
@@ -474,28 +512,125 @@ __global__ __launch_bounds__(256) void embed_grad_kernel(EmbedGradArgs a, int64_
   }
   if (first) put_part(a, piece, 0, p, x);
   else if (after == v) put_part(a, piece, 1, p, x);
-  else put_sum(a, v, p, x);
+  else put_sum(a, v, e0 + from, p, x);
 }
 
-// A wave for each piece in which a run begins that goes on: its partial rows in order.
-__global__ __launch_bounds__(256) void embed_join_kernel(EmbedGradArgs a, int64_t pieces, int slabs) {
-  const int64_t wave = wave_in_grid();
-  const int64_t piece = wave / slabs;
-  if (piece + 1 >= pieces) return;
-  const int p = (int)(wave - piece * slabs) * 64 + (threadIdx.x & 63);
-  const int64_t e0 = piece * a.piece, e1 = e0 + a.piece;
-  const uint32_t v = a.key[e1 - 1];
-  if (v >= (uint32_t)a.V || a.key[e1] != v) return;              // nothing goes on
-  if (e0 > 0 && a.key[e0 - 1] == v) return;                      // it began before
-  float x[8], y[8];
-  load_row<kTypeF32>(reinterpret_cast<const char*>(a.part + (piece * 2 + 1) * a.d), a.d, p, x);
-  const int64_t last = (lower_bound(a.key, a.T, v + 1) - 1) / a.piece;
-  for (int64_t j = piece + 1; j <= last; ++j) {
-    load_row<kTypeF32>(reinterpret_cast<const char*>(a.part + j * 2 * a.d), a.d, p, y);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] += y[i];
+// A workgroup for each piece in which a run begins that goes on, and each
+// slab: its partial rows in order, a quarter of them to each wave.  Behind
+// those, workgroups that note for tied weights where each tile's entries begin.
+__global__ __launch_bounds__(256) void embed_join_kernel(EmbedGradArgs a, int64_t pieces, int slabs, int64_t joins) {
+  __shared__ float sums[3][64 * 8 + 8];
+  if (blockIdx.x >= joins) {
+    const int64_t i = ((int64_t)blockIdx.x - joins) * 256 + threadIdx.x;
+    if (i > a.T) return;
+    const int64_t tiles = (a.V + kEmbedTileV - 1) / kEmbedTileV;
+    const int64_t from = i == 0 ? 0 : min((int64_t)a.key[i - 1] / kEmbedTileV + 1, tiles + 1);
+    const int64_t to = i == a.T ? tiles : min((int64_t)a.key[i] / kEmbedTileV, tiles);
+    for (int64_t k = from; k <= to; ++k) a.tile_first[k] = (uint32_t)i;
+    return;
   }
-  put_sum(a, v, p, x);
+  const int64_t piece = blockIdx.x / slabs;
+  const int64_t e0 = piece * a.piece, e1 = e0 + a.piece;
+  if (e1 >= a.T) return;
+  const uint32_t v = a.key[e1 - 1];
+  if (v >= (uint32_t)a.V || a.key[e1] != v) return;  // nothing goes on
+  if (e0 > 0 && a.key[e0 - 1] == v) return;          // it began before
+  const int lane = threadIdx.x & 63, w = wave_id();
+  const int p = (int)(blockIdx.x - piece * slabs) * 64 + lane;
+  // rows: this piece's last run, then the first runs of the pieces up to the one where the token's entries end
+  int64_t lo = piece + 1, hi = pieces;  // first piece behind the run
+  while (lo < hi) {
+    const int64_t mid = (lo + hi) >> 1;
+    if (a.key[mid * a.piece] == v) lo = mid + 1; else hi = mid;
+  }
+  const int64_t n = lo - piece;
+  float x[8] = {};
+  constexpr int U = 4;
+  for (int64_t j = n * w / 4, end = n * (w + 1) / 4; j < end; j += U) {
+    Raw8<kTypeF32> r[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t q = piece + j + u;
+      const float* row = part_row(a, min(q, lo - 1), q == piece ? 1 : 0);
+      r[u] = load8<kTypeF32>(reinterpret_cast<const char*>(row + 8 * (int64_t)p),
+                             j + u < end ? (int)(a.cols - 8 * (int64_t)p) : 0);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float y[8];
+      unpack8<kTypeF32>(r[u], y);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] += y[i];
+    }
+  }
+  if (n > 1) {
+    if (w > 0)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sums[w - 1][i * 64 + lane] = x[i];
+    __syncthreads();
+    if (w == 0)
+#pragma unroll
+      for (int k = 0; k < 3; ++k)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] += sums[k][i * 64 + lane];
+  }
+  if (w != 0) return;
+  put_sum(a, v, a.tied ? e0 + lower_bound(a.key + e0, a.piece, v) : 0, p, x);
+}
+
+// Tied weights: kEmbedTileV columns x kTurnK rows of the head's gradient a
+// workgroup, from the runs' rows of sums, turned in LDS.  Without accumulate
+// the whole tile is written, zeros and sums alike, in whole rows; with it only
+// the columns whose tokens occur are read and written.
+constexpr int kTurnK = 32, kTurnLd = kEmbedTileV + 4;
+
+__global__ __launch_bounds__(256) void embed_turn_kernel(EmbedGradArgs a, int tiles) {
+  __shared__ __attribute__((aligned(16))) float tile[kTurnK * kTurnLd];
+  __shared__ int first[kEmbedTileV], runs[kEmbedTileV], count;
+  const int64_t v0 = (int64_t)(blockIdx.x % tiles) * kEmbedTileV, k0 = (int64_t)(blockIdx.x / tiles) * kTurnK;
+  const int64_t i0 = a.tile_first[v0 / kEmbedTileV], i1 = a.tile_first[v0 / kEmbedTileV + 1];
+  if (a.accumulate && i0 == i1) return;
+  first[threadIdx.x] = -1;
+  if (threadIdx.x == 0) count = 0;
+  if (!a.accumulate)
+    for (int i = threadIdx.x; i < kTurnK * kTurnLd / 4; i += 256)
+      reinterpret_cast<float4*>(tile)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  __syncthreads();
+  for (int64_t i = i0 + threadIdx.x; i < i1; i += 256) {
+    const uint32_t v = a.key[i];
+    if (v < (uint32_t)a.V && (i == 0 || a.key[i - 1] != v)) {
+      first[v - v0] = (int)i;
+      runs[atomicAdd(&count, 1)] = (int)(v - v0);  // in any order: each is a column of its own
+    }
+  }
+  __syncthreads();
+  const int n = count;
+  for (int j = threadIdx.x; j < n * kTurnK; j += 256) {
+    const int c = runs[j / kTurnK], k = j % kTurnK;
+    if (k0 + k < a.cols) tile[k * kTurnLd + c] = a.sums[(int64_t)first[c] * a.cols + k0 + k];
+  }
+  __syncthreads();
+  const int64_t rows = min((int64_t)kTurnK, a.cols - k0);
+  if (a.accumulate) {
+    const int c = threadIdx.x;
+    if (first[c] < 0) return;
+    for (int k = 0; k < rows; ++k) {
+      const int64_t at = (a.col0 + k0 + k) * a.V + v0 + c;
+      store_any1(a.out, a.grad_type, at, get_any1(a.out, a.grad_type, at) + tile[k * kTurnLd + c]);
+    }
+    return;
+  }
+  const int c = 8 * (threadIdx.x & 31), left = (int)min((int64_t)8, a.V - v0 - c);
+  if (left <= 0) return;
+  with_type(a.grad_type, [&](auto ty) {
+    constexpr int G = decltype(ty)::value;
+    for (int k = threadIdx.x >> 5; k < rows; k += 8) {
+      const float4 u = *reinterpret_cast<const float4*>(tile + k * kTurnLd + c);
+      const float4 w = *reinterpret_cast<const float4*>(tile + k * kTurnLd + c + 4);
+      const float y[8] = {u.x, u.y, u.z, u.w, w.x, w.y, w.z, w.w};
+      store8<G>(a.out + ((a.col0 + k0 + k) * a.V + v0 + c) * Elem<G>::kBytes, y, left);
+    }
+  });
 }
 
 __global__ __launch_bounds__(256) void fill_table_kernel(char* p, int64_t bytes) {
@@ -506,7 +641,7 @@ __global__ __launch_bounds__(256) void fill_table_kernel(char* p, int64_t bytes)
   if (tail < bytes) *reinterpret_cast<uint16_t*>(p + tail) = 0;
 }
 
-int embed_piece(int64_t T) { return T <= kSortSmall ? 16 : 64; }
+int embed_piece(int64_t T) { return T <= 16384 ? 16 : 64; }
 
 namespace {
 struct GradShape {
@@ -514,7 +649,7 @@ struct GradShape {
   int slabs;
 };
 GradShape grad_shape(const EmbedGradArgs& a) {
-  return {(a.T + a.piece - 1) / a.piece, (int)((a.d + kSlab - 1) / kSlab)};
+  return {(a.T + a.piece - 1) / a.piece, (int)((a.cols + kSlab - 1) / kSlab)};
 }
 }  // namespace
 
@@ -527,15 +662,21 @@ hipError_t launch_embed_grad(const EmbedGradArgs& a, hipStream_t st) {
   });
   return hipGetLastError();
 }
+hipError_t launch_embed_join(const EmbedGradArgs& a, hipStream_t st) {
+  const GradShape s = grad_shape(a);
+  const int64_t joins = s.pieces > 1 ? (s.pieces - 1) * s.slabs : 0, notes = a.tied ? a.T / 256 + 1 : 0;
+  if (joins + notes == 0) return hipSuccess;
+  hipLaunchKernelGGL(embed_join_kernel, dim3((unsigned)(joins + notes)), dim3(256), 0, st, a, s.pieces, s.slabs, joins);
+  return hipGetLastError();
+}
+hipError_t launch_embed_turn(const EmbedGradArgs& a, hipStream_t st) {
+  const int64_t tiles = (a.V + kEmbedTileV - 1) / kEmbedTileV, blocks = tiles * ((a.cols + kTurnK - 1) / kTurnK);
+  hipLaunchKernelGGL(embed_turn_kernel, dim3((unsigned)blocks), dim3(256), 0, st, a, (int)tiles);
+  return hipGetLastError();
+}
 hipError_t launch_fill_table(char* p, int64_t bytes, hipStream_t st) {
   const int64_t blocks = std::min<int64_t>(std::max<int64_t>((bytes / 16 + 255) / 256, 1), 8192);
   hipLaunchKernelGGL(fill_table_kernel, dim3((unsigned)blocks), dim3(256), 0, st, p, bytes);
-  return hipGetLastError();
-}
-hipError_t launch_embed_join(const EmbedGradArgs& a, hipStream_t st) {
-  const GradShape s = grad_shape(a);
-  hipLaunchKernelGGL(embed_join_kernel, dim3((unsigned)((s.pieces * s.slabs + 3) / 4)), dim3(256), 0, st, a, s.pieces,
-                     s.slabs);
   return hipGetLastError();
 }
 

@@ -20,40 +20,47 @@ struct EmbedArgs {
 hipError_t launch_embed(const EmbedArgs& a, hipStream_t st);
 
 // Sorted entries (key, position) of the tokens; entries that count for nothing have key V and come last.
-constexpr int64_t kSortSmall = 16384;  // tokens that one workgroup sorts
+constexpr int64_t kSortSmall = 32768;  // tokens sorted in chunks of one workgroup each (every chunk's keys in LDS at once)
+constexpr int kSortChunk = 1024;
 constexpr int kSortItems = 8192;       // tokens of a workgroup otherwise
 struct SortArgs {
   const int32_t* tokens;
   const uint8_t* mask;
   int64_t T, V;
-  uint32_t* key[2];  // [T] each; the second pair for T > kSortSmall only
+  uint32_t* key[2];  // [T] each
   uint32_t* pos[2];
-  uint32_t* count;   // [kSortDigits x blocks], T > kSortSmall only
+  uint32_t* count;   // [kSortDigits x workgroups], T > kSortSmall only
 };
 constexpr int kSortDigits = 512;
 // where the result lies: key[i], pos[i] of the returned index
 int sort_result(int64_t T, int64_t V);
+int sort_passes(int64_t V);
 hipError_t launch_sort_count(const SortArgs& a, int pass, hipStream_t st);
 hipError_t launch_sort_scan(const SortArgs& a, int pass, hipStream_t st);
 hipError_t launch_sort_scatter(const SortArgs& a, int pass, hipStream_t st);
 hipError_t launch_sort_small(const SortArgs& a, hipStream_t st);
-int sort_passes(int64_t V);
 
+constexpr int kEmbedTileV = 256;  // columns of a tied head's tile
 struct EmbedGradArgs {
   const char* grad;  // [T,d]
   const uint32_t* key;
   const uint32_t* pos;
   float scale;
   int64_t T, V, d;
+  int64_t col0, cols;  // the slab of grad's columns that the call takes (all of them unless tied)
   int type, grad_type;
   bool tied, accumulate;
   char* out;    // the table's gradient
-  float* part;  // [pieces][2][d]: what a piece holds of a token that it shares with the piece before, or after
+  float* part;  // [pieces][2][cols]: what a piece holds of a token that it shares with the piece before, or after
   int piece;    // entries of a piece
+  // tied only
+  float* sums;           // [T][cols]: the sum of the run that begins at an entry
+  uint32_t* tile_first;  // [tiles + 1]: the first entry of each tile's columns
 };
 int embed_piece(int64_t T);
 hipError_t launch_embed_grad(const EmbedGradArgs& a, hipStream_t st);
 hipError_t launch_embed_join(const EmbedGradArgs& a, hipStream_t st);
+hipError_t launch_embed_turn(const EmbedGradArgs& a, hipStream_t st);
 hipError_t launch_fill_table(char* p, int64_t bytes, hipStream_t st);  // zeros, any alignment of 2 bytes
 
 // ---------------------------------------------------------------- rows in 8 bits

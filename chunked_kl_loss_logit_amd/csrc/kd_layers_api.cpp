@@ -78,23 +78,26 @@ kd::RowsArgs rows_args(const void* x, const void* q, const float* scale, int64_t
 
 // ------------------------------------------------------------------ embeddings
 struct EmbedPlan {
-  size_t key[2], pos[2], count, part, total;
+  size_t key[2], pos[2], count, part, sums, tile_first, total;
+  int64_t cols;  // columns of a slab
 };
-EmbedPlan plan_embed(int64_t T, int64_t d) {
+// A tied head's sums take a row a token: slabs of columns keep them to 1 GiB.
+constexpr int64_t kSumsMost = int64_t(1) << 30;
+EmbedPlan plan_embed(int64_t T, int64_t V, int64_t d, bool tied) {
   EmbedPlan p{};
   Carver cv;
-  const bool small = T <= kd::kSortSmall;
-  for (int i = 0; i < (small ? 1 : 2); ++i) {
+  p.cols = tied && T > 0 ? std::min<int64_t>(d, std::max<int64_t>(kSumsMost / (4 * T) / 64 * 64, 64)) : d;
+  if (T == 0) return p;
+  for (int i = 0; i < 2; ++i) {
     p.key[i] = cv.take((size_t)T * 4);
     p.pos[i] = cv.take((size_t)T * 4);
   }
-  if (small) {
-    p.key[1] = p.key[0];
-    p.pos[1] = p.pos[0];
-  } else {
-    p.count = cv.take((size_t)cdiv(T, kd::kSortItems) * kd::kSortDigits * 4);
+  if (T > kd::kSortSmall) p.count = cv.take((size_t)cdiv(T, kd::kSortItems) * kd::kSortDigits * 4);
+  p.part = cv.take((size_t)cdiv(T, kd::embed_piece(T)) * 2 * p.cols * 4);
+  if (tied) {
+    p.sums = cv.take((size_t)T * p.cols * 4);
+    p.tile_first = cv.take((size_t)(cdiv(V, kd::kEmbedTileV) + 1) * 4);
   }
-  p.part = cv.take((size_t)cdiv(T, kd::embed_piece(T)) * 2 * d * 4);
   p.total = cv.off;
   return p;
 }
@@ -158,12 +161,12 @@ kd_status kd_embedding_fwd(const int32_t* tokens, const void* table, const uint8
   return KD_OK;
 }
 
-kd_status kd_embedding_workspace_size(int64_t T, int64_t V, int64_t d, size_t* bytes) {
+kd_status kd_embedding_workspace_size(int64_t T, int64_t V, int64_t d, int32_t tied, size_t* bytes) {
   g_err.clear();
   KD_TRY(need(bytes, "bytes"));
   KD_TRY(check_rows(T, d));
   KD_TRY(check_vocab(V));
-  *bytes = plan_embed(T, d).total;
+  *bytes = plan_embed(T, V, d, tied != 0).total;
   return KD_OK;
 }
 
@@ -181,13 +184,14 @@ kd_status kd_embedding_bwd(const void* grad, const int32_t* tokens, const uint8_
     KD_TRY(need_array(grad, type_bytes(dt), "grad"));
     KD_TRY(need_array(tokens, 4, "tokens"));
   }
-  const EmbedPlan p = plan_embed(T, d);
+  const EmbedPlan p = plan_embed(T, V, d, tied != 0);
   KD_TRY(check_workspace(workspace, workspace_bytes, p.total));
   hipStream_t st = static_cast<hipStream_t>(stream);
   char* out = static_cast<char*>(grad_table);
-  if (!accumulate && (tied || T == 0))
-    KD_LAUNCH("embedding_fill", st, kd::launch_fill_table(out, V * d * type_bytes(grad_dt), st));
-  if (T == 0) return KD_OK;
+  if (T == 0) {
+    if (!accumulate) KD_LAUNCH("embedding_fill", st, kd::launch_fill_table(out, V * d * type_bytes(grad_dt), st));
+    return KD_OK;
+  }
 
   kd::SortArgs s{};
   s.tokens = tokens;
@@ -224,8 +228,14 @@ kd_status kd_embedding_bwd(const void* grad, const int32_t* tokens, const uint8_
   a.out = out;
   a.part = at<float>(workspace, p.part);
   a.piece = kd::embed_piece(T);
-  KD_LAUNCH("embedding_grad", st, kd::launch_embed_grad(a, st));
-  if (T > a.piece) KD_LAUNCH("embedding_join", st, kd::launch_embed_join(a, st));
+  a.sums = at<float>(workspace, p.sums);
+  a.tile_first = at<uint32_t>(workspace, p.tile_first);
+  for (a.col0 = 0; a.col0 < d; a.col0 += p.cols) {
+    a.cols = std::min(p.cols, d - a.col0);
+    KD_LAUNCH("embedding_grad", st, kd::launch_embed_grad(a, st));
+    KD_LAUNCH("embedding_join", st, kd::launch_embed_join(a, st));
+    if (tied) KD_LAUNCH("embedding_turn", st, kd::launch_embed_turn(a, st));
+  }
   return KD_OK;
 }
 

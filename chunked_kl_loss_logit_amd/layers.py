@@ -29,9 +29,9 @@ from .policy import _f32, _workspace
 def embedding_forward(tokens, table, mask=None, scale=1.0, tied=False):
     """scale * table[tokens] [T,d] in the table's type: rows of table [V,d], or with tied the columns of the head
     W [d,V].  Masked rows are 0; a valid token outside the vocabulary gives a row of NaN."""
-    n, m = B._matrix("table", table, None, B.TYPES)
-    out = torch.empty(B._tokens(tokens, mask), n if tied else m, dtype=table.dtype, device=table.device)
-    B.kd_embedding_fwd(tokens, table, mask, scale, tied, out)
+    T, V, d = B._embedding_in(tokens, table, mask, tied)
+    out = torch.empty(T, d, dtype=table.dtype, device=table.device)
+    B._embedding_fwd(T, V, d, tokens, table, mask, scale, tied, out)
     return out
 
 
@@ -48,7 +48,7 @@ def embedding_backward(grad, tokens, V, mask=None, scale=1.0, tied=False, grad_d
         B.P._writable("out", [out])
         table = out
     if workspace is None:
-        workspace = _workspace(B.kd_embedding_workspace_size(T, V, d), grad.device)
+        workspace = _workspace(B.kd_embedding_workspace_size(T, V, d, tied), grad.device)
     B.kd_embedding_bwd(grad, tokens, mask, scale, V, tied, out is not None, table, workspace)
     if out is not None:
         torch.autograd.graph.increment_version([out])
@@ -80,10 +80,10 @@ def quantize_rows(x, kind="int8", group=0):
     """x [T,d] in 8 bits: q [T,d] (int8, or float8_e4m3fn for kind "e4m3") and scale [T, groups] float32, for groups
     of 32, 64, 128, 256 or 512 values of a row, or of whole rows (0)."""
     T, d = B._matrix("x", x, None, B.TYPES)
-    B._kind(kind, group)
+    code = B._kind(kind, group)
     q = torch.empty(T, d, dtype=B.ROWS_TYPES[kind], device=x.device)
     scale = _f32(x, T, B._groups(d, group))
-    B.kd_rows_quantize(x, kind, group, q, scale)
+    B._rows_quantize(T, d, x, code, group, q, scale)
     return q, scale
 
 
@@ -150,12 +150,12 @@ def layer_norm_forward(x, weight=None, bias=None, mask=None, eps=1e-5, checkpoin
     T, d = B._norm_in(x, weight, bias, mask)
     y, mean, rstd = torch.empty_like(x), _f32(x, T), _f32(x, T)
     if checkpoint is None:
-        B.kd_layer_norm_fwd(x, weight, bias, mask, eps, y, mean, rstd)
+        B._layer_norm_fwd(T, d, x, weight, bias, mask, eps, y, mean, rstd)
         return y, mean, rstd, None
-    B._kind(checkpoint, group)
+    code = B._kind(checkpoint, group)
     q = torch.empty(T, d, dtype=B.ROWS_TYPES[checkpoint], device=x.device)
     scale = _f32(x, T, B._groups(d, group))
-    B.kd_layer_norm_fwd(x, weight, bias, mask, eps, y, mean, rstd, checkpoint, group, q, scale)
+    B._layer_norm_fwd(T, d, x, weight, bias, mask, eps, y, mean, rstd, code, group, q, scale)
     return y, mean, rstd, (q, scale)
 
 
@@ -163,14 +163,18 @@ def layer_norm_backward(grad, x, weight, mask, mean, rstd, kept=None, group=128,
                         want=(True, True, True), workspace=None):
     """dx (grad's type), dweight and dbias (weight's type; without a weight grad_dtype, None: grad's), each None where
     `want` is false.  kept: the forward's (q, scale) in place of x, which is None then."""
-    T, d = B._norm_in(grad, weight, None, mask, "grad")
+    q, scale = (None, None) if kept is None else kept
+    T, d, code = B._norm_bwd_in(grad, x, weight, mask, mean, rstd, group, q, scale)
+    if not any(want):
+        raise ValueError("dx, dweight and dbias are all not wanted")
     wt = weight.dtype if weight is not None else grad_dtype or grad.dtype
+    if wt != grad.dtype and wt != torch.float32:
+        raise TypeError(f"grad_dtype must be {grad.dtype} or torch.float32, got {wt}")
     dx = torch.empty_like(grad) if want[0] else None
     dw, db = (torch.empty(d, dtype=wt, device=grad.device) if w else None for w in want[1:])
     if workspace is None:
         workspace = _workspace(B.kd_layer_norm_workspace_size(T, d), grad.device)
-    q, scale = (None, None) if kept is None else kept
-    B.kd_layer_norm_bwd(grad, x, weight, mask, mean, rstd, dx, dw, db, workspace, group, q, scale)
+    B._layer_norm_bwd(T, d, code, wt, grad, x, weight, mask, mean, rstd, dx, dw, db, workspace, group, q, scale)
     return dx, dw, db
 
 
@@ -203,10 +207,12 @@ def layer_norm(x, weight=None, bias=None, mask=None, eps=1e-5, checkpoint=None, 
 def int8_matmul(x, x_scale, w, w_scale, out_dtype=torch.bfloat16, workspace=None):
     """out [T,V] = x w^T with x_scale [T] and w_scale [V] (or [T,1], [V,1]): x [T,d] int8, w [V,d] int8 with a row for
     each channel, d a multiple of 16.  quantize_rows(H, "int8", 0) gives x, quantize_rows of a head's transpose w."""
-    T, d = B._matrix("x", x, None, B._I8)
-    V, _ = B._matrix("w", w, None, B._I8)
+    T, d, V = B._int8_in(x, x_scale, w, w_scale)
+    if out_dtype not in B.TYPES:
+        raise TypeError(f"out_dtype must be one of {', '.join(map(str, B.TYPES))}, got {out_dtype}")
     out = torch.empty(T, V, dtype=out_dtype, device=x.device)
     if workspace is None:
-        workspace = _workspace(B.kd_int8_matmul_workspace_size(T, d, V), x.device)
-    B.kd_int8_matmul(x, x_scale, w, w_scale, out, workspace)
+        n = B.kd_int8_matmul_workspace_size(T, d, V)
+        workspace = _workspace(n, x.device) if n else None
+    B._int8_matmul(T, d, V, x, x_scale, w, w_scale, out, workspace)
     return out

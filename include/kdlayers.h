@@ -43,9 +43,11 @@ extern "C" {
  * tokens [T] int32; out [T,d] of type dt. */
 kd_status kd_embedding_fwd(const int32_t* tokens, const void* table, const uint8_t* mask, float scale, int64_t T,
                            int64_t V, int64_t d, kd_dtype dt, int32_t tied, void* out, void* stream);
-/* Workspace bytes for kd_embedding_bwd: the sorted tokens (16 bytes a token)
- * and float32 partial sums (up to d / 2 bytes a token). */
-kd_status kd_embedding_workspace_size(int64_t T, int64_t V, int64_t d, size_t* bytes);
+/* Workspace bytes for kd_embedding_bwd: the sorted tokens (16 bytes a token),
+ * float32 partial sums (up to d / 2 bytes a token) and, if tied, a float32 row
+ * of sums for each token (in slabs of columns of 1 GiB at most, or of 64
+ * columns). */
+kd_status kd_embedding_workspace_size(int64_t T, int64_t V, int64_t d, int32_t tied, size_t* bytes);
 /* dE_v = scale sum of grad[t] over the valid t with tokens[t] = v, added up in
  * float32 in an order that T and the tokens decide (no atomics), rounded once
  * to grad_dt.

@@ -30,15 +30,15 @@ int main() {
   for (int64_t T : {int64_t(0), int64_t(1), int64_t(255), int64_t(16384), int64_t(16385), top})
     for (int64_t d : {int64_t(1), int64_t(16), int64_t(4096), int64_t(131056), (int64_t(1) << 24) - 1}) {
       for (int64_t V : {int64_t(1), int64_t(300), int64_t(128256), top})
-        EXPECT(kd_embedding_workspace_size(T, V, d, &b) == KD_OK);
+        for (int tied : {0, 1}) EXPECT(kd_embedding_workspace_size(T, V, d, tied, &b) == KD_OK);
       EXPECT(kd_layer_norm_workspace_size(T, d, &b) == KD_OK);
       const kd_status want = d % 16 || d >= (1 << 17) ? KD_ERR_UNSUPPORTED : KD_OK;
       EXPECT(kd_int8_matmul_workspace_size(T, d, 128256, &b) == want);
     }
   for (int64_t bad : {far, std::numeric_limits<int64_t>::min(), int64_t(-1)}) {
-    EXPECT(kd_embedding_workspace_size(bad, 10, 8, &b) != KD_OK);
-    EXPECT(kd_embedding_workspace_size(10, bad, 8, &b) != KD_OK);
-    EXPECT(kd_embedding_workspace_size(10, 10, bad, &b) != KD_OK);
+    EXPECT(kd_embedding_workspace_size(bad, 10, 8, 1, &b) != KD_OK);
+    EXPECT(kd_embedding_workspace_size(10, bad, 8, 0, &b) != KD_OK);
+    EXPECT(kd_embedding_workspace_size(10, 10, bad, 1, &b) != KD_OK);
     EXPECT(kd_layer_norm_workspace_size(bad, 8, &b) != KD_OK);
     EXPECT(kd_int8_matmul_workspace_size(bad, 16, 8, &b) != KD_OK);
     EXPECT(kd_int8_matmul_workspace_size(8, 16, bad, &b) != KD_OK);

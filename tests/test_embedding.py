@@ -67,17 +67,18 @@ def test_backward(T, V, d, tied, dtype, grad_dtype):
         assert torch.equal(left, was[~seen]), "rows of tokens that do not occur"
 
 
-@pytest.mark.parametrize("T", [16383, 16384, 16385, 24576, 50001])
+@pytest.mark.parametrize("tied", [False, True])
+@pytest.mark.parametrize("T", [1023, 1024, 2049, 16384, 16385, 32767, 32768, 32769, 50001])
 @pytest.mark.parametrize("V", [3, 300, 5000, 300001])
-def test_backward_of_many_tokens(T, V):
-    """One workgroup's sort and the passes over several, keys of one to three digits, runs over many pieces."""
-    say(f"embedding backward T={T} V={V}")
+def test_backward_of_many_tokens(T, V, tied):
+    """Chunks of a workgroup's sort, the passes over many, keys of one to three digits, runs over many pieces."""
+    say(f"embedding backward T={T} V={V} tied={tied}")
     d = 8
     grad = torch.randn(T, d, generator=R.gen(T))
     tokens, mask = R.make_tokens(T, V, T + V, 0.1)
-    got = kd.embedding_backward(grad.cuda(), tokens.cuda(), V, mask.cuda())
+    got = kd.embedding_backward(grad.cuda(), tokens.cuda(), V, mask.cuda(), tied=tied)
     want, bound = R.embedding_grad_reference(grad, tokens, mask, 1.0, V, torch.float32)
-    R.check(got, want, bound, "dE")
+    R.check(got.t() if tied else got, want, bound, "dE")
 
 
 @pytest.mark.parametrize("tied", [False, True])
@@ -133,6 +134,19 @@ def test_autograd(tied):
     diff = ((ys[1] - ys[0]).cpu().double() * up.double()).sum() / 2
     assert abs(diff - (want * step.double()).sum()) <= 16 * R.U32 * (y.detach().cpu().double().abs() * up.double().abs()).sum() \
         + 16 * R.U32 * (want.abs() * step.double().abs()).sum() + 64 * R.U32 * up.double().abs().sum()
+
+
+def test_slabs_of_a_tied_heads_columns():
+    """A row of sums for each token, which pass 1 GiB: the columns are taken in slabs."""
+    T, V, d = 300000, 600, 1100
+    say(f"embedding backward tied T={T} V={V} d={d}")
+    assert kd.kd_embedding_workspace_size(T, V, d, True) < 4 * T * d
+    grad = torch.randn(T, d, device="cuda", generator=torch.Generator("cuda").manual_seed(1))
+    tokens = torch.randint(0, V, (T,), dtype=torch.int32, generator=R.gen(4)).cuda()
+    rows = kd.embedding_backward(grad, tokens, V)  # the same sums, tested above
+    assert torch.equal(kd.embedding_backward(grad, tokens, V, tied=True), rows.t())
+    out = torch.zeros(d, V, device="cuda")
+    assert torch.equal(kd.embedding_backward(grad, tokens, V, tied=True, out=out), rows.t())
 
 
 def test_offsets_beyond_32_bits():

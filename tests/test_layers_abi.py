@@ -41,14 +41,16 @@ def size(L, fn, *args):
 
 
 def test_sizes(L):
-    assert size(L, "kd_embedding_workspace_size", 0, 10, 8) == (0, 0)
+    assert size(L, "kd_embedding_workspace_size", 0, 10, 8, 0) == (0, 0)
     for T, d in ((1, 8), (16384, 2048), (16385, 2048), (1 << 20, 512)):
-        st, n = size(L, "kd_embedding_workspace_size", T, 32000, d)
+        st, n = size(L, "kd_embedding_workspace_size", T, 32000, d, 0)
         assert st == 0 and 8 * T <= n <= T * (17 + d // 2) + 2 * 4 * d + 1024 * 1024
-    assert size(L, "kd_embedding_workspace_size", -1, 10, 8)[0] == 1
-    assert size(L, "kd_embedding_workspace_size", 1 << 30, 10, 8)[0] == 2
-    assert size(L, "kd_embedding_workspace_size", 10, 0, 8)[0] == 1
-    assert size(L, "kd_embedding_workspace_size", 10, 10, 1 << 24)[0] == 2
+        st, m = size(L, "kd_embedding_workspace_size", T, 32000, d, 1)
+        assert st == 0 and min(4 * T * d, 1 << 29) <= m <= n + (1 << 30) + 1024
+    assert size(L, "kd_embedding_workspace_size", -1, 10, 8, 1)[0] == 1
+    assert size(L, "kd_embedding_workspace_size", 1 << 30, 10, 8, 1)[0] == 2
+    assert size(L, "kd_embedding_workspace_size", 10, 0, 8, 1)[0] == 1
+    assert size(L, "kd_embedding_workspace_size", 10, 10, 1 << 24, 1)[0] == 2
     assert size(L, "kd_layer_norm_workspace_size", 0, 100)[0] == 0
     assert size(L, "kd_layer_norm_workspace_size", 100, 0)[0] == 1
     a, b = (size(L, "kd_layer_norm_workspace_size", T, 4096)[1] for T in (1 << 16, 1 << 20))
@@ -59,7 +61,7 @@ def test_sizes(L):
     assert size(L, "kd_int8_matmul_workspace_size", 1 << 24, 4096, 32000)[1] <= 1 << 30
     assert size(L, "kd_int8_matmul_workspace_size", 4, 4100, 32000)[0] == 2
     assert size(L, "kd_int8_matmul_workspace_size", 4, 1 << 17, 32000)[0] == 2
-    assert L.kd_embedding_workspace_size(1, 1, 1, None) == 1
+    assert L.kd_embedding_workspace_size(1, 1, 1, 0, None) == 1
 
 
 def embed(L, tokens=F, table=F, scale=1.0, T=8, V=100, d=64, dt=1, tied=0, out=F):

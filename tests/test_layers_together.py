@@ -148,10 +148,11 @@ def test_workspaces_are_kept_to(T):
     V, d = 900, 72
     s = model(V, d, T)
     grad = torch.randn(T, d, device="cuda").to(bf)
-    w = Guarded(kd.kd_embedding_workspace_size(T, V, d))
-    out = torch.empty(V, d, device="cuda")
-    kd.kd_embedding_bwd(grad, s["tokens"], s["mask"], 1.0, V, False, False, out, w.ws)
-    assert w.intact()
+    for tied in (False, True):
+        w = Guarded(kd.kd_embedding_workspace_size(T, V, d, tied))
+        out = torch.empty((d, V) if tied else (V, d), device="cuda")
+        kd.kd_embedding_bwd(grad, s["tokens"], s["mask"], 1.0, V, tied, False, out, w.ws)
+        assert w.intact()
     y, mean, rstd, _ = kd.layer_norm_forward(grad, s["w"], s["b"], s["mask"])
     w = Guarded(kd.kd_layer_norm_workspace_size(T, d))
     dx, dw, db = torch.empty_like(grad), torch.empty_like(s["w"]), torch.empty_like(s["w"])
