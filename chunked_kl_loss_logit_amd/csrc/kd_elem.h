@@ -118,15 +118,33 @@ __device__ inline void store8(char* p, const float (&x)[8], int n) {
 }
 
 // ------------------------------------------------------------------ reductions
-__device__ inline float wave_sum(float v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
-  return v;
+// The value of another lane: of the other one of two, the other pair of four,
+// the mirrored one of 8 and of 16 (which holds what the other half holds once
+// the halves agree), without going through LDS; 16 and 32 lanes further.
+template <int D>
+__device__ inline uint32_t other_lane(uint32_t v) {
+  if constexpr (D == 1) return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xb1, 0xf, 0xf, true);
+  else if constexpr (D == 2) return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4e, 0xf, 0xf, true);
+  else if constexpr (D == 4) return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xf, 0xf, true);
+  else if constexpr (D == 8) return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xf, 0xf, true);
+  else if constexpr (D == 16) return (uint32_t)__builtin_amdgcn_ds_swizzle((int)v, 0x401f);
+  else return (uint32_t)__shfl_xor((int)v, D);
 }
-__device__ inline uint32_t wave_max(uint32_t v, int lanes = 64) {  // over aligned runs of `lanes` lanes
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1)
-    if (o < lanes) v = max(v, (uint32_t)__shfl_xor((int)v, o));
+template <int D>
+__device__ inline float add_lane(float v) {
+  return v + __uint_as_float(other_lane<D>(__float_as_uint(v)));
+}
+__device__ inline float wave_sum(float v) {
+  return add_lane<32>(add_lane<16>(add_lane<8>(add_lane<4>(add_lane<2>(add_lane<1>(v))))));
+}
+// the largest of each aligned run of `lanes` lanes (4 to 64)
+__device__ inline uint32_t wave_max(uint32_t v, int lanes = 64) {
+  v = max(v, other_lane<1>(v));
+  v = max(v, other_lane<2>(v));
+  if (lanes > 4) v = max(v, other_lane<4>(v));
+  if (lanes > 8) v = max(v, other_lane<8>(v));
+  if (lanes > 16) v = max(v, other_lane<16>(v));
+  if (lanes > 32) v = max(v, other_lane<32>(v));
   return v;
 }
 

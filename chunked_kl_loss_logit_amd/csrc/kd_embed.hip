@@ -14,7 +14,7 @@
 // bits each time.  A frequent token (the first few take a tenth of a text)
 // then costs as many partial rows as it has pieces, spread over the chip.
 // For tied weights the runs' sums go to rows of their own first, and a third
-// kernel turns them into columns of the head's gradient.
+// kernel makes them columns of the head's gradient.
 #include <type_traits>
 
 #include "kd_launch.h"
@@ -68,64 +68,7 @@ __global__ __launch_bounds__(256) void embed_kernel(EmbedArgs a, int units) {
   }
 }
 
-// Tied: kTiedT tokens x kTiedK rows of W a workgroup.  A lane keeps its token
-// and goes down the rows; the tile is turned in LDS, so that the output is
-// written in runs of kTiedK elements.  Every load takes a cache line for two
-// bytes, and what limits the kernel is how often a line is fetched: workgroups
-// of the same rows of W run on one XCD, next to each other, and share its L2.
-constexpr int kTiedT = 64, kTiedK = 32;
-
-template <int TY>
-__global__ __launch_bounds__(256) void embed_tied_kernel(EmbedArgs a, int blocks_t) {
-  using E = Elem<TY>;
-  constexpr int kPer = kTiedK / 4;  // rows of a wave
-  __shared__ float tile[kTiedT][kTiedK + 1];
-  const int lane = threadIdx.x & 63, w = wave_id();
-  const int logical = xcd_remap(blockIdx.x, gridDim.x);
-  const int64_t t0 = (int64_t)(logical % blocks_t) * kTiedT, k0 = (int64_t)(logical / blocks_t) * kTiedK;
-  const int64_t t = t0 + lane;
-  const bool valid = t < a.T && (!a.mask || a.mask[t]);
-  const int64_t v = valid ? a.tokens[t] : 0;
-  const bool in = valid && v >= 0 && v < a.V;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int64_t k = k0 + w * kPer + i;
-    float x = valid ? __uint_as_float(0x7fc00000u) : 0.f;
-    if (in && k < a.d) x = E::get1(a.table + (k * a.V + v) * E::kBytes) * a.scale;
-    tile[lane][w * kPer + i] = x;
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < kTiedT * kTiedK / 8; i += 256) {
-    const int row = i / (kTiedK / 8), c = 8 * (i % (kTiedK / 8));
-    const int64_t to = t0 + row, k = k0 + c;
-    if (to >= a.T || k >= a.d) continue;
-    float x[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = tile[row][c + j];
-    store8<TY>(a.out + (to * a.d + k) * E::kBytes, x, (int)(a.d - k));
-  }
-}
-
-hipError_t launch_embed(const EmbedArgs& a, hipStream_t st) {
-  pick_type(a.type, [&](auto ty) {
-    constexpr int TY = decltype(ty)::value;
-    if (a.tied) {
-      const int64_t bt = (a.T + kTiedT - 1) / kTiedT, bk = (a.d + kTiedK - 1) / kTiedK;
-      hipLaunchKernelGGL((embed_tied_kernel<TY>), dim3((unsigned)(bt * bk)), dim3(256), 0, st, a, (int)bt);
-      return;
-    }
-    auto with = [&](auto n) {
-      constexpr int N = decltype(n)::value;
-      const int units = (int)((a.d + kSlab * N - 1) / (kSlab * N));
-      hipLaunchKernelGGL((embed_kernel<TY, N>), dim3((unsigned)((a.T * units + 3) / 4)), dim3(256), 0, st, a, units);
-    };
-    if (a.T * a.d <= (1 << 20)) with(std::integral_constant<int, 1>());  // waves for the whole chip first
-    else with(std::integral_constant<int, 4>());
-  });
-  return hipGetLastError();
-}
-
-// ------------------------------------------------------------------ sorting the positions by token
+// ------------------------------------------------------------------ sorting
 // Least significant digit first, every pass stable.  Within a workgroup wave w
 // holds consecutive items, 64 a round; an item's place among the items of its
 // digit is the number of such items in earlier waves, earlier rounds and
@@ -193,28 +136,153 @@ int bits_of(int64_t V) {  // of the keys 0 .. V
 
 }  // namespace
 
+namespace {
+// Where an item of a workgroup of 1024 goes when they are ordered by a digit of 6 bits, stable.  seen: 16 x 65.
+__device__ inline uint32_t place_in_block(uint32_t digit, uint32_t* seen, uint32_t* lds16) {
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  seen[w * 65 + lane] = 0;
+  __syncthreads();
+  const uint32_t at = place_in_wave(same_digit<6>(digit), &seen[w * 65 + digit]);
+  __syncthreads();
+  uint32_t* const mine = &seen[(threadIdx.x & 15) * 65 + (threadIdx.x >> 4)];  // in the order digit, wave
+  const uint32_t base = block_exclusive(*mine, lds16);
+  *mine = base;
+  __syncthreads();
+  return seen[w * 65 + digit] + at;
+}
+}  // namespace
+
+// ------------------------------------------------------------------ forward, tied weights
+// Tied weights: every load takes a cache line for one element, and what limits
+// the kernel is how many lines are asked for.  A workgroup takes kTiedT tokens,
+// sorts them by the cache line of W's rows that they lie in, and goes down
+// kTiedK rows: the lanes of a wave then share lines, and neighbouring waves do.
+// The elements are turned in LDS and written in runs of kTiedK, each to its
+// token's row.  Workgroups of the same rows of W run on one XCD.  Up to
+// kTiedFew tokens, 64 to a workgroup and unsorted, sorting costs more than it
+// saves.
+constexpr int kTiedT = 1024, kTiedK = 16;
+constexpr int64_t kTiedFew = 512;
+
+template <int TY>
+__global__ __launch_bounds__(kTiedT) void embed_tied_kernel(EmbedArgs a, int blocks_t, int bits) {
+  using E = Elem<TY>;
+  using Bits = typename std::conditional<E::kBytes == 4, uint32_t, uint16_t>::type;
+  constexpr int kLd = kTiedK + 4 / E::kBytes;  // rows of words an odd number apart
+  __shared__ uint32_t seen[16 * 65], sums[16];
+  __shared__ uint32_t order[kTiedT];
+  __shared__ __attribute__((aligned(16))) Bits tile[kTiedT * kLd];
+  const int lane = threadIdx.x & 63, w = wave_id();
+  const int logical = xcd_remap(blockIdx.x, gridDim.x);
+  const int64_t t0 = (int64_t)(logical % blocks_t) * kTiedT, k0 = (int64_t)(logical / blocks_t) * kTiedK;
+  constexpr uint32_t kNone = 0xfffffffeu, kOutside = 0xffffffffu;  // masked or behind the last one; no such token
+  auto token = [&](int i) -> uint32_t {
+    const int64_t t = t0 + i;
+    if (t >= a.T || (a.mask && !a.mask[t])) return kNone;
+    const int64_t v = a.tokens[t];
+    return v < 0 || v >= a.V ? kOutside : (uint32_t)v;
+  };
+  uint32_t p = threadIdx.x;
+  uint32_t line = min(token(p), (uint32_t)a.V) / (128 / E::kBytes);
+  for (int shift = 0; shift < bits; shift += 6) {
+    const uint32_t digit = (line >> shift) & 63u;
+    const uint32_t to = place_in_block(digit, seen, sums);
+    order[to] = p | line << 10;
+    __syncthreads();
+    p = order[threadIdx.x] & 1023u;
+    line = order[threadIdx.x] >> 10;
+  }
+  const uint32_t v = token(p);
+  const char* from = a.table + (k0 * a.V + (v < kNone ? v : 0)) * E::kBytes;
+  const int rows = (int)min((int64_t)kTiedK, a.d - k0);
+#pragma unroll
+  for (int i = 0; i < kTiedK; ++i) {
+    float x = v == kNone ? 0.f : __uint_as_float(0x7fc00000u);
+    if (v < kNone && i < rows) x = E::get1(from + i * a.V * E::kBytes) * a.scale;
+    E::put1(reinterpret_cast<char*>(&tile[p * kLd + i]), x);
+  }
+  __syncthreads();
+  constexpr int kPer = kTiedK / 8;  // pieces of a token's run
+  for (int i = threadIdx.x; i < kTiedT * kPer; i += kTiedT) {
+    const int row = i / kPer, c = 8 * (i % kPer);
+    if (t0 + row >= a.T || c >= rows) continue;
+    float x[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = E::get1(reinterpret_cast<const char*>(&tile[row * kLd + c + j]));
+    store8<TY>(a.out + ((t0 + row) * a.d + k0 + c) * E::kBytes, x, rows - c);
+  }
+}
+
+constexpr int kFewT = 64, kFewK = 32;
+
+template <int TY>
+__global__ __launch_bounds__(256) void embed_tied_few_kernel(EmbedArgs a, int blocks_t) {
+  using E = Elem<TY>;
+  constexpr int kPer = kFewK / 4;  // rows of a wave
+  __shared__ float tile[kFewT][kFewK + 1];
+  const int lane = threadIdx.x & 63, w = wave_id();
+  const int64_t t0 = (int64_t)(blockIdx.x % blocks_t) * kFewT, k0 = (int64_t)(blockIdx.x / blocks_t) * kFewK;
+  const int64_t t = t0 + lane;
+  const bool valid = t < a.T && (!a.mask || a.mask[t]);
+  const int64_t v = valid ? a.tokens[t] : 0;
+  const bool in = valid && v >= 0 && v < a.V;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int64_t k = k0 + w * kPer + i;
+    float x = valid ? __uint_as_float(0x7fc00000u) : 0.f;
+    if (in && k < a.d) x = E::get1(a.table + (k * a.V + v) * E::kBytes) * a.scale;
+    tile[lane][w * kPer + i] = x;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < kFewT * kFewK / 8; i += 256) {
+    const int row = i / (kFewK / 8), c = 8 * (i % (kFewK / 8));
+    const int64_t to = t0 + row, k = k0 + c;
+    if (to >= a.T || k >= a.d) continue;
+    float x[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = tile[row][c + j];
+    store8<TY>(a.out + (to * a.d + k) * E::kBytes, x, (int)(a.d - k));
+  }
+}
+
+hipError_t launch_embed(const EmbedArgs& a, hipStream_t st) {
+  pick_type(a.type, [&](auto ty) {
+    constexpr int TY = decltype(ty)::value;
+    if (a.tied && a.T > kTiedFew) {
+      const int64_t bt = (a.T + kTiedT - 1) / kTiedT, bk = (a.d + kTiedK - 1) / kTiedK;
+      const int bits = bits_of(a.V / (128 / Elem<TY>::kBytes));
+      hipLaunchKernelGGL((embed_tied_kernel<TY>), dim3((unsigned)(bt * bk)), dim3(kTiedT), 0, st, a, (int)bt, bits);
+      return;
+    }
+    if (a.tied) {
+      const int64_t bt = (a.T + kFewT - 1) / kFewT, bk = (a.d + kFewK - 1) / kFewK;
+      hipLaunchKernelGGL((embed_tied_few_kernel<TY>), dim3((unsigned)(bt * bk)), dim3(256), 0, st, a, (int)bt);
+      return;
+    }
+    auto with = [&](auto n) {
+      constexpr int N = decltype(n)::value;
+      const int units = (int)((a.d + kSlab * N - 1) / (kSlab * N));
+      hipLaunchKernelGGL((embed_kernel<TY, N>), dim3((unsigned)((a.T * units + 3) / 4)), dim3(256), 0, st, a, units);
+    };
+    if (a.T * a.d <= (1 << 20)) with(std::integral_constant<int, 1>());  // waves for the whole chip first
+    else with(std::integral_constant<int, 4>());
+  });
+  return hipGetLastError();
+}
+
+// ------------------------------------------------------------------ all tokens by token
 // Up to kSortSmall tokens: chunks of 1024, each sorted by one workgroup in LDS
 // with digits of 6 bits, and then every entry's place among all chunks by
 // binary search in each of them.  (One workgroup for all of 16384 tokens took
 // 44 us, the instructions of 16 waves on one CU.)
 __global__ __launch_bounds__(1024) void sort_chunk_kernel(SortArgs a, int bits, int to_result) {
   __shared__ uint32_t keys[kSortChunk], poss[kSortChunk];
-  __shared__ uint32_t seen[16 * 65], lds[16];  // [wave][digit]
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  __shared__ uint32_t seen[16 * 65], lds[16];
   const int64_t i = (int64_t)blockIdx.x * kSortChunk + threadIdx.x;
   uint32_t k = i < a.T ? key_of(a, i) : 0xffffffffu;  // behind the last one, and stays there
   uint32_t p = (uint32_t)i;
   for (int shift = 0; shift < bits; shift += 6) {
-    seen[w * 65 + lane] = 0;
-    __syncthreads();
-    const uint32_t digit = (k >> shift) & 63u;
-    const uint32_t at = place_in_wave(same_digit<6>(digit), &seen[w * 65 + digit]);
-    __syncthreads();
-    uint32_t* const mine = &seen[(threadIdx.x & 15) * 65 + (threadIdx.x >> 4)];  // in the order digit, wave
-    const uint32_t base = block_exclusive(*mine, lds);
-    *mine = base;
-    __syncthreads();
-    const uint32_t to = seen[w * 65 + digit] + at;
+    const uint32_t to = place_in_block((k >> shift) & 63u, seen, lds);
     keys[to] = k;
     poss[to] = p;
     __syncthreads();
@@ -227,9 +295,11 @@ __global__ __launch_bounds__(1024) void sort_chunk_kernel(SortArgs a, int bits, 
   }
 }
 
-// 256 entries of one chunk a workgroup; every chunk's keys in LDS.
+// 64 entries of one chunk a workgroup, every chunk's keys in LDS; each of the
+// four waves searches a quarter of the chunks for all 64.
 __global__ __launch_bounds__(256) void sort_rank_kernel(SortArgs a) {
   extern __shared__ uint32_t keys[];
+  __shared__ uint32_t places[4][64];
   const int T = (int)a.T, chunks = (T + kSortChunk - 1) / kSortChunk;
   for (int i = 4 * threadIdx.x; i < T; i += 1024) {
     if (i + 4 <= T)
@@ -238,23 +308,38 @@ __global__ __launch_bounds__(256) void sort_rank_kernel(SortArgs a) {
       for (int j = i; j < T; ++j) keys[j] = a.key[1][j];
   }
   __syncthreads();
-  const int i = blockIdx.x * 256 + threadIdx.x;
-  if (i >= T) return;
-  const int own = i / kSortChunk;
+  const int lane = threadIdx.x & 63, w = wave_id();
+  const int i = min((int)blockIdx.x * 64 + lane, T - 1);
+  const int own = (int)blockIdx.x * 64 / kSortChunk;
   const uint32_t k = keys[i];
-  uint32_t place = (uint32_t)(i - own * kSortChunk);
-#pragma unroll 4
-  for (int c = 0; c < chunks; ++c) {
-    if (c == own) continue;
-    const uint32_t* in = keys + c * kSortChunk;
-    const int n = min(kSortChunk, T - c * kSortChunk);
-    const uint32_t v = c < own ? k + 1 : k;  // earlier chunks' equal keys come first
-    int lo = 0;                              // entries below v
+  uint32_t place = 0;
+  constexpr int U = 4;  // chunks searched at once: a step waits for the LDS, not for the others
+  for (int c0 = w * U; c0 < chunks; c0 += 4 * U) {
+    int lo[U], n[U];  // entries below the bound, of n
+    uint32_t v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int c = c0 + u;
+      lo[u] = 0;
+      n[u] = c < chunks && c != own ? min(kSortChunk, T - c * kSortChunk) : 0;
+      v[u] = c < own ? k + 1 : k;  // earlier chunks' equal keys come first
+    }
 #pragma unroll
     for (int step = kSortChunk; step > 0; step >>= 1)
-      if (lo + step <= n && in[lo + step - 1] < v) lo += step;
-    place += (uint32_t)lo;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int at = min((c0 + u) * kSortChunk + lo[u] + step - 1, T - 1);
+        if (keys[at] < v[u] && lo[u] + step <= n[u]) lo[u] += step;
+      }
+#pragma unroll
+    for (int u = 0; u < U; ++u) place += (uint32_t)lo[u];
   }
+  places[w][lane] = place;
+  __syncthreads();
+  if (w != 0 || (int)blockIdx.x * 64 + lane >= T) return;
+  place = (uint32_t)(i - own * kSortChunk);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) place += places[j][lane];
   a.key[0][place] = k;
   a.pos[0][place] = a.pos[1][i];
 }
@@ -357,7 +442,7 @@ hipError_t launch_sort_small(const SortArgs& a, hipStream_t st) {
   const unsigned chunks = (unsigned)((a.T + kSortChunk - 1) / kSortChunk);
   hipLaunchKernelGGL(sort_chunk_kernel, dim3(chunks), dim3(kSortChunk), 0, st, a, bits_of(a.V), chunks == 1 ? 1 : 0);
   if (chunks > 1)
-    hipLaunchKernelGGL(sort_rank_kernel, dim3((unsigned)((a.T + 255) / 256)), dim3(256), (unsigned)a.T * 4, st, a);
+    hipLaunchKernelGGL(sort_rank_kernel, dim3((unsigned)((a.T + 63) / 64)), dim3(256), (unsigned)a.T * 4, st, a);
   return hipGetLastError();
 }
 hipError_t launch_sort_count(const SortArgs& a, int pass, hipStream_t st) {
@@ -376,12 +461,6 @@ hipError_t launch_sort_scatter(const SortArgs& a, int pass, hipStream_t st) {
 
 // ------------------------------------------------------------------ gradient
 namespace {
-
-__device__ inline float get_any1(const char* base, int type, int64_t i) {
-  if (type == kTypeF32) return Elem<kTypeF32>::get1(base + 4 * i);
-  if (type == kTypeBf16) return Elem<kTypeBf16>::get1(base + 2 * i);
-  return Elem<kTypeF16>::get1(base + 2 * i);
-}
 
 // f with the gradient's type as a constant
 template <class F>
@@ -444,13 +523,20 @@ __device__ inline uint32_t lane_of(uint32_t v, int lane) {
 }  // namespace
 
 // Waves [0, pieces * slabs) add up, the waves behind them write zeros to the
-// table's rows whose tokens do not occur.
+// table's rows whose tokens do not occur (tied: clear the places of the runs).
 template <int TY>
 __global__ __launch_bounds__(256) void embed_grad_kernel(EmbedGradArgs a, int64_t pieces, int slabs) {
   const int lane = threadIdx.x & 63;
   const int64_t wave = wave_in_grid();
   if (wave >= pieces * slabs) {
-    if (a.tied || a.accumulate) return;
+    if (a.tied) {
+      const int64_t v = (wave - pieces * slabs) * 256 + 4 * lane;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (v + i < a.V) a.run_of[v + i] = -1;
+      return;
+    }
+    if (a.accumulate) return;
     const int64_t v0 = (wave - pieces * slabs) * kFillRows, v = v0 + lane;
     bool empty = false;
     if (lane < kFillRows && v < a.V) {
@@ -517,42 +603,39 @@ __global__ __launch_bounds__(256) void embed_grad_kernel(EmbedGradArgs a, int64_
 
 // A workgroup for each piece in which a run begins that goes on, and each
 // slab: its partial rows in order, a quarter of them to each wave.  Behind
-// those, workgroups that note for tied weights where each tile's entries begin.
+// those, workgroups that note for tied weights where each token's run begins.
 __global__ __launch_bounds__(256) void embed_join_kernel(EmbedGradArgs a, int64_t pieces, int slabs, int64_t joins) {
-  __shared__ float sums[3][64 * 8 + 8];
+  __shared__ float sums[3][64 * 8];
   if (blockIdx.x >= joins) {
     const int64_t i = ((int64_t)blockIdx.x - joins) * 256 + threadIdx.x;
-    if (i > a.T) return;
-    const int64_t tiles = (a.V + kEmbedTileV - 1) / kEmbedTileV;
-    const int64_t from = i == 0 ? 0 : min((int64_t)a.key[i - 1] / kEmbedTileV + 1, tiles + 1);
-    const int64_t to = i == a.T ? tiles : min((int64_t)a.key[i] / kEmbedTileV, tiles);
-    for (int64_t k = from; k <= to; ++k) a.tile_first[k] = (uint32_t)i;
+    if (i >= a.T) return;
+    const uint32_t v = a.key[i];
+    if (v < (uint32_t)a.V && (i == 0 || a.key[i - 1] != v)) a.run_of[v] = (int32_t)i;
     return;
   }
   const int64_t piece = blockIdx.x / slabs;
   const int64_t e0 = piece * a.piece, e1 = e0 + a.piece;
-  if (e1 >= a.T) return;
-  const uint32_t v = a.key[e1 - 1];
-  if (v >= (uint32_t)a.V || a.key[e1] != v) return;  // nothing goes on
-  if (e0 > 0 && a.key[e0 - 1] == v) return;          // it began before
   const int lane = threadIdx.x & 63, w = wave_id();
-  const int p = (int)(blockIdx.x - piece * slabs) * 64 + lane;
-  // rows: this piece's last run, then the first runs of the pieces up to the one where the token's entries end
-  int64_t lo = piece + 1, hi = pieces;  // first piece behind the run
-  while (lo < hi) {
-    const int64_t mid = (lo + hi) >> 1;
-    if (a.key[mid * a.piece] == v) lo = mid + 1; else hi = mid;
+  const uint32_t v = a.key[e1 - 1], begin = e0 > 0 ? a.key[e0 - 1] : 0xffffffffu;
+  if (v >= (uint32_t)a.V || begin == v) return;  // nothing, or it began before
+  // the partial rows: this piece's last run, then the first runs of the pieces that begin with the token
+  int64_t n = 1;
+  for (;;) {
+    const int64_t q = piece + n + lane;
+    const uint64_t goes_on = __ballot(q < pieces && a.key[min(q * a.piece, a.T - 1)] == v);
+    n += goes_on == ~uint64_t(0) ? 64 : __builtin_ctzll(~goes_on);
+    if (goes_on != ~uint64_t(0)) break;
   }
-  const int64_t n = lo - piece;
+  if (n == 1) return;
+  const int p = (int)(blockIdx.x - piece * slabs) * 64 + lane;
   float x[8] = {};
   constexpr int U = 4;
   for (int64_t j = n * w / 4, end = n * (w + 1) / 4; j < end; j += U) {
     Raw8<kTypeF32> r[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int64_t q = piece + j + u;
-      const float* row = part_row(a, min(q, lo - 1), q == piece ? 1 : 0);
-      r[u] = load8<kTypeF32>(reinterpret_cast<const char*>(row + 8 * (int64_t)p),
+      const int64_t q = piece + min(j + u, n - 1);
+      r[u] = load8<kTypeF32>(reinterpret_cast<const char*>(part_row(a, q, q == piece ? 1 : 0) + 8 * (int64_t)p),
                              j + u < end ? (int)(a.cols - 8 * (int64_t)p) : 0);
     }
 #pragma unroll
@@ -563,74 +646,91 @@ __global__ __launch_bounds__(256) void embed_join_kernel(EmbedGradArgs a, int64_
       for (int i = 0; i < 8; ++i) x[i] += y[i];
     }
   }
-  if (n > 1) {
-    if (w > 0)
+  if (w > 0)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sums[w - 1][i * 64 + lane] = x[i];
-    __syncthreads();
-    if (w == 0)
+    for (int i = 0; i < 8; ++i) sums[w - 1][i * 64 + lane] = x[i];
+  __syncthreads();
+  if (w > 0) return;
 #pragma unroll
-      for (int k = 0; k < 3; ++k)
+  for (int k = 0; k < 3; ++k)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] += sums[k][i * 64 + lane];
-  }
-  if (w != 0) return;
+    for (int i = 0; i < 8; ++i) x[i] += sums[k][i * 64 + lane];
   put_sum(a, v, a.tied ? e0 + lower_bound(a.key + e0, a.piece, v) : 0, p, x);
 }
 
-// Tied weights: kEmbedTileV columns x kTurnK rows of the head's gradient a
-// workgroup, from the runs' rows of sums, turned in LDS.  Without accumulate
-// the whole tile is written, zeros and sums alike, in whole rows; with it only
-// the columns whose tokens occur are read and written.
-constexpr int kTurnK = 32, kTurnLd = kEmbedTileV + 4;
+// Tied weights: 256 columns x kTurnK rows of the head's gradient a workgroup,
+// from the runs' rows of sums, turned in LDS.  The columns whose tokens do not
+// occur (most of them) are zeros there from the start.  Without accumulate
+// whole rows are written, a kilobyte by each wave at once; with it only the
+// columns whose tokens occur are read and written.  A tile of frequent tokens
+// has up to 256 runs and is what the call waits for in the end: few rows a
+// workgroup, and 16 loads of a thread in flight.
+constexpr int kTurnV = 256, kTurnK = 16, kTurnLd = kTurnV + 4;
 
+template <int G>
 __global__ __launch_bounds__(256) void embed_turn_kernel(EmbedGradArgs a, int tiles) {
   __shared__ __attribute__((aligned(16))) float tile[kTurnK * kTurnLd];
-  __shared__ int first[kEmbedTileV], runs[kEmbedTileV], count;
-  const int64_t v0 = (int64_t)(blockIdx.x % tiles) * kEmbedTileV, k0 = (int64_t)(blockIdx.x / tiles) * kTurnK;
-  const int64_t i0 = a.tile_first[v0 / kEmbedTileV], i1 = a.tile_first[v0 / kEmbedTileV + 1];
-  if (a.accumulate && i0 == i1) return;
-  first[threadIdx.x] = -1;
-  if (threadIdx.x == 0) count = 0;
-  if (!a.accumulate)
-    for (int i = threadIdx.x; i < kTurnK * kTurnLd / 4; i += 256)
-      reinterpret_cast<float4*>(tile)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  __shared__ int first[kTurnV], column[kTurnV], counts[4];
+  const int tid = threadIdx.x, lane = tid & 63, w = wave_id();
+  const int64_t v0 = (int64_t)(blockIdx.x % tiles) * kTurnV, k0 = (int64_t)(blockIdx.x / tiles) * kTurnK;
+  const int rows = (int)min((int64_t)kTurnK, a.cols - k0);
+  const int run = v0 + tid < a.V ? a.run_of[v0 + tid] : -1;  // the entry at which the column's run begins
+  for (int i = tid; i < kTurnK * kTurnLd / 4; i += 256)
+    reinterpret_cast<float4*>(tile)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  const uint64_t here = __ballot(run >= 0);
+  if (lane == 0) counts[w] = __popcll(here);
   __syncthreads();
-  for (int64_t i = i0 + threadIdx.x; i < i1; i += 256) {
-    const uint32_t v = a.key[i];
-    if (v < (uint32_t)a.V && (i == 0 || a.key[i - 1] != v)) {
-      first[v - v0] = (int)i;
-      runs[atomicAdd(&count, 1)] = (int)(v - v0);  // in any order: each is a column of its own
-    }
+  int n = 0, before = __popcll(here & ((uint64_t(1) << lane) - 1));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (i < w) before += counts[i];
+    n += counts[i];
+  }
+  if (a.accumulate && n == 0) return;
+  if (run >= 0) {
+    first[before] = run;
+    column[before] = tid;
   }
   __syncthreads();
-  const int n = count;
-  for (int j = threadIdx.x; j < n * kTurnK; j += 256) {
-    const int c = runs[j / kTurnK], k = j % kTurnK;
-    if (k0 + k < a.cols) tile[k * kTurnLd + c] = a.sums[(int64_t)first[c] * a.cols + k0 + k];
+  const int k = tid % kTurnK;
+  const float* const from = a.sums + k0 + min(k, rows - 1);
+  constexpr int kStep = 256 / kTurnK;
+  for (int j0 = tid / kTurnK; j0 < n; j0 += 16 * kStep) {
+    float held[16];
+#pragma unroll
+    for (int u = 0; u < 16; ++u) held[u] = from[(int64_t)first[min(j0 + u * kStep, n - 1)] * a.cols];
+#pragma unroll
+    for (int u = 0; u < 16; ++u)
+      if (j0 + u * kStep < n) tile[k * kTurnLd + column[j0 + u * kStep]] = held[u];
   }
   __syncthreads();
-  const int64_t rows = min((int64_t)kTurnK, a.cols - k0);
+  char* const out = a.out + ((a.col0 + k0) * a.V + v0) * Elem<G>::kBytes;
+  const int64_t ld = a.V * Elem<G>::kBytes;
   if (a.accumulate) {
-    const int c = threadIdx.x;
-    if (first[c] < 0) return;
-    for (int k = 0; k < rows; ++k) {
-      const int64_t at = (a.col0 + k0 + k) * a.V + v0 + c;
-      store_any1(a.out, a.grad_type, at, get_any1(a.out, a.grad_type, at) + tile[k * kTurnLd + c]);
-    }
+    if (run >= 0)
+#pragma unroll 4
+      for (int q = 0; q < rows; ++q) {
+        char* to = out + q * ld + tid * Elem<G>::kBytes;
+        Elem<G>::put1(to, Elem<G>::get1(to) + tile[q * kTurnLd + tid]);
+      }
     return;
   }
-  const int c = 8 * (threadIdx.x & 31), left = (int)min((int64_t)8, a.V - v0 - c);
-  if (left <= 0) return;
-  with_type(a.grad_type, [&](auto ty) {
-    constexpr int G = decltype(ty)::value;
-    for (int k = threadIdx.x >> 5; k < rows; k += 8) {
-      const float4 u = *reinterpret_cast<const float4*>(tile + k * kTurnLd + c);
-      const float4 w = *reinterpret_cast<const float4*>(tile + k * kTurnLd + c + 4);
-      const float y[8] = {u.x, u.y, u.z, u.w, w.x, w.y, w.z, w.w};
-      store8<G>(a.out + ((a.col0 + k0 + k) * a.V + v0 + c) * Elem<G>::kBytes, y, left);
+  constexpr int kCols = 16 / Elem<G>::kBytes, kLanes = kTurnV / kCols;  // 64 lanes a row, or 32
+  const int c = kCols * (tid % kLanes), left = (int)min((int64_t)kCols, a.V - v0 - c);
+#pragma unroll
+  for (int q = tid / kLanes; q < kTurnK; q += 256 / kLanes) {
+    if (q >= rows || left <= 0) continue;
+    const float* y = tile + q * kTurnLd + c;
+    char* to = out + q * ld + c * Elem<G>::kBytes;
+    if (left < kCols) {
+      for (int i = 0; i < left; ++i) Elem<G>::put1(to + i * Elem<G>::kBytes, y[i]);
+    } else if constexpr (G == kTypeF32) {
+      store16(to, *reinterpret_cast<const u32x4_t*>(y));
+    } else {
+      const float4 p = *reinterpret_cast<const float4*>(y), r = *reinterpret_cast<const float4*>(y + 4);
+      store16(to, u32x4_t{pack2x16<G>(p.x, p.y), pack2x16<G>(p.z, p.w), pack2x16<G>(r.x, r.y), pack2x16<G>(r.z, r.w)});
     }
-  });
+  }
 }
 
 __global__ __launch_bounds__(256) void fill_table_kernel(char* p, int64_t bytes) {
@@ -655,7 +755,7 @@ GradShape grad_shape(const EmbedGradArgs& a) {
 
 hipError_t launch_embed_grad(const EmbedGradArgs& a, hipStream_t st) {
   const GradShape s = grad_shape(a);
-  const int64_t fill = a.tied || a.accumulate ? 0 : (a.V + kFillRows - 1) / kFillRows;
+  const int64_t fill = a.tied ? (a.V + 255) / 256 : a.accumulate ? 0 : (a.V + kFillRows - 1) / kFillRows;
   const dim3 grid((unsigned)((s.pieces * s.slabs + fill + 3) / 4));
   pick_type(a.type, [&](auto ty) {
     hipLaunchKernelGGL((embed_grad_kernel<decltype(ty)::value>), grid, dim3(256), 0, st, a, s.pieces, s.slabs);
@@ -664,14 +764,17 @@ hipError_t launch_embed_grad(const EmbedGradArgs& a, hipStream_t st) {
 }
 hipError_t launch_embed_join(const EmbedGradArgs& a, hipStream_t st) {
   const GradShape s = grad_shape(a);
-  const int64_t joins = s.pieces > 1 ? (s.pieces - 1) * s.slabs : 0, notes = a.tied ? a.T / 256 + 1 : 0;
+  const int64_t joins = (s.pieces - 1) * s.slabs, notes = a.tied ? (a.T + 255) / 256 : 0;
   if (joins + notes == 0) return hipSuccess;
   hipLaunchKernelGGL(embed_join_kernel, dim3((unsigned)(joins + notes)), dim3(256), 0, st, a, s.pieces, s.slabs, joins);
   return hipGetLastError();
 }
 hipError_t launch_embed_turn(const EmbedGradArgs& a, hipStream_t st) {
-  const int64_t tiles = (a.V + kEmbedTileV - 1) / kEmbedTileV, blocks = tiles * ((a.cols + kTurnK - 1) / kTurnK);
-  hipLaunchKernelGGL(embed_turn_kernel, dim3((unsigned)blocks), dim3(256), 0, st, a, (int)tiles);
+  pick_type(a.grad_type, [&](auto ty) {
+    constexpr int G = decltype(ty)::value;
+    const int64_t tiles = (a.V + kTurnV - 1) / kTurnV, blocks = tiles * ((a.cols + kTurnK - 1) / kTurnK);
+    hipLaunchKernelGGL((embed_turn_kernel<G>), dim3((unsigned)blocks), dim3(256), 0, st, a, (int)tiles);
+  });
   return hipGetLastError();
 }
 hipError_t launch_fill_table(char* p, int64_t bytes, hipStream_t st) {

@@ -40,7 +40,6 @@ hipError_t launch_sort_scan(const SortArgs& a, int pass, hipStream_t st);
 hipError_t launch_sort_scatter(const SortArgs& a, int pass, hipStream_t st);
 hipError_t launch_sort_small(const SortArgs& a, hipStream_t st);
 
-constexpr int kEmbedTileV = 256;  // columns of a tied head's tile
 struct EmbedGradArgs {
   const char* grad;  // [T,d]
   const uint32_t* key;
@@ -54,8 +53,8 @@ struct EmbedGradArgs {
   float* part;  // [pieces][2][cols]: what a piece holds of a token that it shares with the piece before, or after
   int piece;    // entries of a piece
   // tied only
-  float* sums;           // [T][cols]: the sum of the run that begins at an entry
-  uint32_t* tile_first;  // [tiles + 1]: the first entry of each tile's columns
+  float* sums;      // [T][cols]: the sum of the run that begins at an entry
+  int32_t* run_of;  // [V]: the entry at which the token's run begins, or -1
 };
 int embed_piece(int64_t T);
 hipError_t launch_embed_grad(const EmbedGradArgs& a, hipStream_t st);

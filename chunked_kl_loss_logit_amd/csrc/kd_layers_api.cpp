@@ -78,7 +78,7 @@ kd::RowsArgs rows_args(const void* x, const void* q, const float* scale, int64_t
 
 // ------------------------------------------------------------------ embeddings
 struct EmbedPlan {
-  size_t key[2], pos[2], count, part, sums, tile_first, total;
+  size_t key[2], pos[2], count, part, sums, run_of, total;
   int64_t cols;  // columns of a slab
 };
 // A tied head's sums take a row a token: slabs of columns keep them to 1 GiB.
@@ -96,7 +96,7 @@ EmbedPlan plan_embed(int64_t T, int64_t V, int64_t d, bool tied) {
   p.part = cv.take((size_t)cdiv(T, kd::embed_piece(T)) * 2 * p.cols * 4);
   if (tied) {
     p.sums = cv.take((size_t)T * p.cols * 4);
-    p.tile_first = cv.take((size_t)(cdiv(V, kd::kEmbedTileV) + 1) * 4);
+    p.run_of = cv.take((size_t)V * 4);
   }
   p.total = cv.off;
   return p;
@@ -229,7 +229,7 @@ kd_status kd_embedding_bwd(const void* grad, const int32_t* tokens, const uint8_
   a.part = at<float>(workspace, p.part);
   a.piece = kd::embed_piece(T);
   a.sums = at<float>(workspace, p.sums);
-  a.tile_first = at<uint32_t>(workspace, p.tile_first);
+  a.run_of = at<int32_t>(workspace, p.run_of);
   for (a.col0 = 0; a.col0 < d; a.col0 += p.cols) {
     a.cols = std::min(p.cols, d - a.col0);
     KD_LAUNCH("embedding_grad", st, kd::launch_embed_grad(a, st));

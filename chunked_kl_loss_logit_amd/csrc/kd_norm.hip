@@ -18,9 +18,15 @@
 #include "kd_layers.h"
 #include "kd_row.h"
 
+// Products and sums are fused where fmaf says so and nowhere else: what a call
+// computes does not hang on what else its kernel has to do.
+#pragma clang fp contract(off)
+
 namespace kd {
 
 namespace {
+
+constexpr int64_t kNormBlocks = 2048;  // workgroups of the forward pass at most
 
 __device__ inline bool row_valid(const uint8_t* mask, int64_t t) { return !mask || mask[t]; }
 
@@ -40,73 +46,139 @@ __device__ inline void keep_piece(const NormArgs& a, int64_t t, int p, const flo
 }  // namespace
 
 // ------------------------------------------------------------------ forward
-template <int TY, int R, int K>
-__global__ __launch_bounds__(RowTeam<R>::kThreads) void norm_fwd_kernel(NormArgs a) {
+// The thread's weights and biases: in registers, or in LDS where the 8-bit copy
+// takes the registers (two workgroups of a wide row's 1024 threads then fit a
+// CU: 8192 x 8192 with its copy 123 us -> 95; without a copy LDS costs 46 -> 56).
+template <bool LDS, int N>
+struct Affine {
+  float w[N][8], b[N][8];
+};
+template <int N>
+struct Affine<true, N> {};
+
+// The row's pieces stay in registers as they were loaded, and the next row's
+// are loaded while one is worked on.
+template <int TY, int KIND, int R, int K>
+__global__ __launch_bounds__(RowTeam<R>::kThreads, K == 1 ? 8 : 4) void norm_fwd_kernel(NormArgs a) {
   using Team = RowTeam<R>;
+  constexpr bool kLds = KIND != kRowsNone;
   __shared__ float lds[16];
+  __shared__ __attribute__((aligned(16))) float affine[2][kLds ? R * K * 8 : 4];
   const int lane = Team::lane();
-  float w[K][8], b[K][8];
-#pragma unroll
-  for (int k = 0; k < K; ++k) {
-    const int p = lane + k * R;
-    if (a.w) load_any(a.w, a.wtype, a.d, p, w[k]);
-    if (a.b) load_any(a.b, a.wtype, a.d, p, b[k]);
+  Affine<kLds, K> own;
+  auto piece = [&](int p, float (&w)[8], float (&b)[8]) {
+    if (a.w) load_any(a.w, a.wtype, a.d, p, w);
+    if (a.b) load_any(a.b, a.wtype, a.d, p, b);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      if (!a.w) w[k][i] = 1.f;
-      if (!a.b) b[k][i] = 0.f;
+      if (!a.w) w[i] = 1.f;
+      if (!a.b) b[i] = 0.f;
     }
+  };
+  if constexpr (kLds) {
+    for (int p = threadIdx.x; p < R * K; p += Team::kThreads) {
+      float w[8], b[8];
+      piece(p, w, b);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        affine[0][8 * p + i] = w[i];
+        affine[1][8 * p + i] = b[i];
+      }
+    }
+    __syncthreads();
+  } else {
+#pragma unroll
+    for (int k = 0; k < K; ++k) piece(lane + k * R, own.w[k], own.b[k]);
   }
   const float inv_d = 1.f / (float)a.d;
-  for (int64_t t = (int64_t)blockIdx.x * Team::kRows + Team::slot(); t < a.T; t += (int64_t)gridDim.x * Team::kRows) {
-    const bool valid = row_valid(a.mask, t);
-    float x[K][8];
-    const char* row = a.x + t * a.d * Elem<TY>::kBytes;
+  const int64_t step = (int64_t)gridDim.x * Team::kRows;
+  int64_t t = (int64_t)blockIdx.x * Team::kRows + Team::slot();
+  Raw8<TY> r[K], next[K];
+  auto load = [&](Raw8<TY> (&to)[K], int64_t row) {  // masked rows and those behind the last one as zeros
+    const bool there = row < a.T && row_valid(a.mask, row);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      if (valid) load_row<TY>(row, a.d, lane + k * R, x[k]);
-      else
+      const int64_t at = 8 * (int64_t)(lane + k * R);
+      to[k] = load8<TY>(a.x + (row * a.d + at) * Elem<TY>::kBytes, there ? (int)(a.d - at) : 0);
+    }
+  };
+  load(next, t);
+  for (; t < a.T; t += step) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[k][i] = 0.f;
+    for (int k = 0; k < K; ++k) r[k] = next[k];
+    load(next, t + step);
+    if (!row_valid(a.mask, t)) {
+      if (lane == 0) {
+        if (a.mean) a.mean[t] = 0.f;
+        if (a.rstd) a.rstd[t] = 0.f;
+      }
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const int p = lane + k * R;
+        const float zero[8] = {};
+        if constexpr (KIND != kRowsNone) keep_piece<KIND>(a, t, p, zero, 0u);
+        store8<TY>(a.y + (t * a.d + 8 * (int64_t)p) * Elem<TY>::kBytes, zero, (int)(a.d - 8 * (int64_t)p));
+      }
+      continue;
     }
     float s[1] = {0.f};
+    float x[8];
 #pragma unroll
-    for (int k = 0; k < K; ++k)
+    for (int k = 0; k < K; ++k) {
+      unpack8<TY>(r[k], x);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s[0] += x[k][i];
+      for (int i = 0; i < 8; ++i) s[0] += x[i];
+    }
     Team::sum(s, lds);
     const float mean = s[0] * inv_d;
     s[0] = 0.f;
+    uint32_t top = 0;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const int64_t n = a.d - 8 * (int64_t)(lane + k * R);
+      const int n = (int)(a.d - 8 * (int64_t)(lane + k * R));
+      unpack8<TY>(r[k], x);
+      if (n >= 8) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float c = i < n ? x[k][i] - mean : 0.f;
-        s[0] = fmaf(c, c, s[0]);
+        for (int i = 0; i < 8; ++i) {
+          const float c = x[i] - mean;
+          s[0] = fmaf(c, c, s[0]);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float c = i < n ? x[i] - mean : 0.f;
+          s[0] = fmaf(c, c, s[0]);
+        }
       }
+      if (KIND != kRowsNone && a.groups == 1) top = max(top, top8(x));
     }
     Team::sum(s, lds);
     const float rstd = 1.f / sqrtf(s[0] * inv_d + a.eps);
     if (lane == 0) {
-      if (a.mean) a.mean[t] = valid ? mean : 0.f;
-      if (a.rstd) a.rstd[t] = valid ? rstd : 0.f;
+      if (a.mean) a.mean[t] = mean;
+      if (a.rstd) a.rstd[t] = rstd;
     }
-    uint32_t top = 0;
-    if (a.kind && a.groups == 1) {
-#pragma unroll
-      for (int k = 0; k < K; ++k) top = max(top, top8(x[k]));
-      top = Team::most(top, reinterpret_cast<uint32_t*>(lds));
-    }
+    if (KIND != kRowsNone && a.groups == 1) top = Team::most(top, reinterpret_cast<uint32_t*>(lds));
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int p = lane + k * R;
-      if (a.kind == kRowsInt8) keep_piece<kRowsInt8>(a, t, p, x[k], top);
-      if (a.kind == kRowsE4m3) keep_piece<kRowsE4m3>(a, t, p, x[k], top);
-      float y[8];
+      unpack8<TY>(r[k], x);
+      if constexpr (KIND != kRowsNone) keep_piece<KIND>(a, t, p, x, top);
+      if constexpr (kLds) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = valid ? fmaf((x[k][i] - mean) * rstd, w[k][i], b[k][i]) : 0.f;
-      store8<TY>(a.y + (t * a.d + 8 * (int64_t)p) * Elem<TY>::kBytes, y, (int)(a.d - 8 * (int64_t)p));
+        for (int h = 0; h < 8; h += 4) {
+          const float4 w = *reinterpret_cast<const float4*>(&affine[0][8 * p + h]);
+          const float4 b = *reinterpret_cast<const float4*>(&affine[1][8 * p + h]);
+          x[h] = fmaf((x[h] - mean) * rstd, w.x, b.x);
+          x[h + 1] = fmaf((x[h + 1] - mean) * rstd, w.y, b.y);
+          x[h + 2] = fmaf((x[h + 2] - mean) * rstd, w.z, b.z);
+          x[h + 3] = fmaf((x[h + 3] - mean) * rstd, w.w, b.w);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = fmaf((x[i] - mean) * rstd, own.w[k][i], own.b[k][i]);
+      }
+      store8<TY>(a.y + (t * a.d + 8 * (int64_t)p) * Elem<TY>::kBytes, x, (int)(a.d - 8 * (int64_t)p));
     }
   }
 }
@@ -171,29 +243,49 @@ __global__ __launch_bounds__(1024) void norm_fwd_long_kernel(NormArgs a) {
 
 // ------------------------------------------------------------------ backward
 namespace {
-// piece p of the input of row t: as it is, or from 8 bits
+// A piece of the input as it lies in memory: as it is, or 8 bits and a scale.
 template <int TY, int KIND>
-__device__ inline void input_piece(const NormGradArgs& a, int64_t t, int p, float (&x)[8]) {
+struct Input {
+  Raw8<TY> x;
+};
+template <int TY>
+struct Input<TY, kRowsInt8> {
+  uint2 q;
+  float scale;
+};
+template <int TY>
+struct Input<TY, kRowsE4m3> {
+  uint2 q;
+  float scale;
+};
+
+// n values of piece p of row t
+template <int TY, int KIND>
+__device__ inline Input<TY, KIND> load_input(const NormGradArgs& a, int64_t t, int p, int n) {
+  Input<TY, KIND> r;
+  const int64_t at = t * a.d + 8 * (int64_t)p;
   if constexpr (KIND == kRowsNone) {
-    load_row<TY>(a.x + t * a.d * Elem<TY>::kBytes, a.d, p, x);
+    r.x = load8<TY>(a.x + at * Elem<TY>::kBytes, n);
   } else {
-    const int n = (int)(a.d - 8 * (int64_t)p);
-    if (n <= 0) {
+    r.q = load_q8(a.q + at, n);
+    r.scale = n > 0 ? a.scale[t * a.groups + (a.groups == 1 ? 0 : 8 * p / a.group)] : 0.f;
+  }
+  return r;
+}
+template <int TY, int KIND>
+__device__ inline void input_values(const Input<TY, KIND>& r, float (&x)[8]) {
+  if constexpr (KIND == kRowsNone) {
+    unpack8<TY>(r.x, x);
+  } else {
+    values8<KIND>(r.q, x);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = 0.f;
-      return;
-    }
-    const uint2 q = load_q8(a.q + t * a.d + 8 * (int64_t)p, n);
-    const float s = a.scale[t * a.groups + (a.groups == 1 ? 0 : 8 * p / a.group)];
-    values8<KIND>(q, x);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] *= s;
+    for (int i = 0; i < 8; ++i) x[i] *= r.scale;
   }
 }
 }  // namespace
 
 template <int TY, int KIND, int R, int K>
-__global__ __launch_bounds__(RowTeam<R>::kThreads) void norm_grad_kernel(NormGradArgs a) {
+__global__ __launch_bounds__(RowTeam<R>::kThreads, 4) void norm_grad_kernel(NormGradArgs a) {
   using Team = RowTeam<R>;
   __shared__ float lds[2 * 16];
   const int lane = Team::lane();
@@ -208,36 +300,53 @@ __global__ __launch_bounds__(RowTeam<R>::kThreads) void norm_grad_kernel(NormGra
     }
   }
   const float inv_d = 1.f / (float)a.d;
-  for (int64_t t = (int64_t)blockIdx.x * Team::kRows + Team::slot(); t < a.T; t += (int64_t)gridDim.x * Team::kRows) {
-    char* out = a.dx ? a.dx + t * a.d * Elem<TY>::kBytes : nullptr;
-    if (!row_valid(a.mask, t)) {
-      if (out) {
-        const float zero[8] = {};
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-          const int64_t at = 8 * (int64_t)(lane + k * R);
-          store8<TY>(out + at * Elem<TY>::kBytes, zero, (int)(a.d - at));
-        }
-      }
-      continue;
-    }
-    const float mean = a.mean[t], rstd = a.rstd[t];
-    float h[K][8], g[K][8];
-    float s[2] = {0.f, 0.f};
+  const int64_t step = (int64_t)gridDim.x * Team::kRows;
+  int64_t t = (int64_t)blockIdx.x * Team::kRows + Team::slot();
+  Input<TY, KIND> xr[K], xn[K];
+  Raw8<TY> gr[K], gn[K];
+  float mean = 0.f, rstd = 0.f;
+  auto load = [&](int64_t row) {  // masked rows and those behind the last one as zeros
+    const bool there = row < a.T && row_valid(a.mask, row);
+    mean = there ? a.mean[row] : 0.f;
+    rstd = there ? a.rstd[row] : 0.f;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int p = lane + k * R;
-      const int64_t n = a.d - 8 * (int64_t)p;
-      input_piece<TY, KIND>(a, t, p, h[k]);
-      load_row<TY>(a.grad + t * a.d * Elem<TY>::kBytes, a.d, p, g[k]);
+      const int n = there ? (int)(a.d - 8 * (int64_t)p) : 0;
+      xn[k] = load_input<TY, KIND>(a, row, p, n);
+      gn[k] = load8<TY>(a.grad + (row * a.d + 8 * (int64_t)p) * Elem<TY>::kBytes, n);
+    }
+  };
+  load(t);
+  for (; t < a.T; t += step) {
+    char* out = a.dx ? a.dx + t * a.d * Elem<TY>::kBytes : nullptr;
+    const float m = mean, r = rstd;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      xr[k] = xn[k];
+      gr[k] = gn[k];
+    }
+    load(t + step);  // the next row, while this one is worked on
+    // a piece's h and g from what lies in registers as it was loaded
+    auto values = [&](int k, float (&h)[8], float (&g)[8]) {
+      const int64_t n = a.d - 8 * (int64_t)(lane + k * R);
+      input_values<TY, KIND>(xr[k], h);
+      unpack8<TY>(gr[k], g);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) h[i] = i < n ? (h[i] - m) * r : 0.f;
+    };
+    float s[2] = {0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      float h[8], g[8];
+      values(k, h, g);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        h[k][i] = i < n ? (h[k][i] - mean) * rstd : 0.f;
-        dw[k][i] = fmaf(g[k][i], h[k][i], dw[k][i]);
-        db[k][i] += g[k][i];
-        g[k][i] *= w[k][i];
-        s[0] += g[k][i];
-        s[1] = fmaf(g[k][i], h[k][i], s[1]);
+        dw[k][i] = fmaf(g[i], h[i], dw[k][i]);
+        db[k][i] += g[i];
+        const float v = g[i] * w[k][i];
+        s[0] += v;
+        s[1] = fmaf(v, h[i], s[1]);
       }
     }
     if (!out) continue;
@@ -246,10 +355,11 @@ __global__ __launch_bounds__(RowTeam<R>::kThreads) void norm_grad_kernel(NormGra
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int64_t at = 8 * (int64_t)(lane + k * R);
-      float o[8];
+      float h[8], g[8];
+      values(k, h, g);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] = rstd * (g[k][i] - c0 - h[k][i] * c1);
-      store8<TY>(out + at * Elem<TY>::kBytes, o, (int)(a.d - at));
+      for (int i = 0; i < 8; ++i) g[i] = r * fmaf(-h[i], c1, g[i] * w[k][i] - c0);
+      store8<TY>(out + at * Elem<TY>::kBytes, g, (int)(a.d - at));
     }
   }
   if (!a.dw && !a.db) return;
@@ -309,7 +419,7 @@ __global__ __launch_bounds__(1024) void norm_grad_long_kernel(NormGradArgs a) {
     const float mean = a.mean[t], rstd = a.rstd[t];
     auto piece = [&](int p, float (&h)[8], float (&g)[8], float (&w)[8]) {
       const int64_t n = a.d - 8 * (int64_t)p;
-      input_piece<TY, KIND>(a, t, p, h);
+      input_values<TY, KIND>(load_input<TY, KIND>(a, t, p, (int)n), h);
       load_row<TY>(a.grad + t * a.d * Elem<TY>::kBytes, a.d, p, g);
       if (a.w) load_any(a.w, a.wtype, a.d, p, w);
 #pragma unroll
@@ -342,22 +452,31 @@ __global__ __launch_bounds__(1024) void norm_grad_long_kernel(NormGradArgs a) {
       float h[8], g[8], w[8], o[8];
       piece(p, h, g, w);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] = rstd * (g[i] * w[i] - c0 - h[i] * c1);
+      for (int i = 0; i < 8; ++i) o[i] = rstd * fmaf(-h[i], c1, g[i] * w[i] - c0);
       store8<TY>(out + 8 * (int64_t)p * Elem<TY>::kBytes, o, (int)(a.d - 8 * (int64_t)p));
     }
   }
 }
 
 // dw and db from the workgroups' partial rows: 64 columns a workgroup, the
-// partial rows dealt to 16 waves and added up through LDS.
+// partial rows dealt to 16 waves, eight loads of a wave in flight, and the
+// waves' sums added up through LDS.
 __global__ __launch_bounds__(1024) void norm_sum_kernel(NormGradArgs a) {
   __shared__ float col[16][64];
   const int which = blockIdx.y;
   const int64_t c = (int64_t)blockIdx.x * 64 + (threadIdx.x & 63);
   const int w = threadIdx.x >> 6;
   float v = 0.f;
-  if (c < a.d)
-    for (int b = w; b < a.blocks; b += 16) v += a.part[((int64_t)b * 2 + which) * a.d + c];
+  if (c < a.d) {
+    const float* p = a.part + (int64_t)which * a.d + c;
+    for (int b = w; b < a.blocks; b += 128) {
+      float q[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) q[j] = b + 16 * j < a.blocks ? p[(int64_t)(b + 16 * j) * 2 * a.d] : 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v += q[j];
+    }
+  }
   col[w][threadIdx.x & 63] = v;
   __syncthreads();
   if (w != 0 || c >= a.d) return;
@@ -369,28 +488,34 @@ __global__ __launch_bounds__(1024) void norm_sum_kernel(NormGradArgs a) {
 }
 
 // ------------------------------------------------------------------ launches
-namespace {
-// rows that a workgroup holds at once
-int64_t team_rows(int64_t d) { return d <= 2048 ? 4 : 1; }
-}  // namespace
-
 hipError_t launch_norm_fwd(const NormArgs& a, hipStream_t st) {
-  const int64_t rows = (a.T + team_rows(a.d) - 1) / team_rows(a.d);
   pick_type(a.type, [&](auto ty) {
     constexpr int TY = decltype(ty)::value;
-    const bool held = pick_row(a.d, [&](auto r, auto k) {
-      constexpr int R = decltype(r)::value, K = decltype(k)::value;
-      const dim3 grid((unsigned)std::min<int64_t>(rows, 2048));
-      hipLaunchKernelGGL((norm_fwd_kernel<TY, R, K>), grid, dim3(RowTeam<R>::kThreads), 0, st, a);
-    });
-    if (!held)
-      hipLaunchKernelGGL((norm_fwd_long_kernel<TY>), dim3((unsigned)std::min<int64_t>(a.T, 512)), dim3(1024), 0, st, a);
+    auto with = [&](auto kind) {
+      constexpr int KIND = decltype(kind)::value;
+      auto launch = [&](auto r, auto k) {
+        constexpr int R = decltype(r)::value, K = decltype(k)::value;
+        const int64_t rows = (a.T + RowTeam<R>::kRows - 1) / RowTeam<R>::kRows;
+        hipLaunchKernelGGL((norm_fwd_kernel<TY, KIND, R, K>), dim3((unsigned)std::min<int64_t>(rows, kNormBlocks)),
+                           dim3(RowTeam<R>::kThreads), 0, st, a);
+      };
+      // by the width alone, so that a row's bits do not hang on how many rows there are
+      const bool held = pick_shape<Shape<64, 1>, Shape<256, 1>, Shape<512, 1>, Shape<1024, 1>, Shape<1024, 2>>(
+          a.d, launch);
+      if (!held)
+        hipLaunchKernelGGL((norm_fwd_long_kernel<TY>), dim3((unsigned)std::min<int64_t>(a.T, 512)), dim3(1024), 0, st, a);
+    };
+    using std::integral_constant;
+    if (a.kind == kRowsInt8) with(integral_constant<int, kRowsInt8>());
+    else if (a.kind == kRowsE4m3) with(integral_constant<int, kRowsE4m3>());
+    else with(integral_constant<int, kRowsNone>());
   });
   return hipGetLastError();
 }
 
 int norm_grad_blocks(int64_t T, int64_t d) {
-  return (int)std::min<int64_t>(std::max<int64_t>((T + team_rows(d) - 1) / team_rows(d), 1), d <= kRowMost ? 512 : 256);
+  const int64_t rows = d <= 512 ? 4 : 1;  // of a workgroup
+  return (int)std::min<int64_t>(std::max<int64_t>((T + rows - 1) / rows, 1), d <= kRowMost ? 512 : 256);
 }
 
 hipError_t launch_norm_grad(const NormGradArgs& a, hipStream_t st) {
@@ -399,7 +524,8 @@ hipError_t launch_norm_grad(const NormGradArgs& a, hipStream_t st) {
     constexpr int TY = decltype(ty)::value;
     auto with = [&](auto kind) {
       constexpr int KIND = decltype(kind)::value;
-      const bool held = pick_row(a.d, [&](auto r, auto k) {
+      const bool held = pick_shape<Shape<64, 1>, Shape<256, 1>, Shape<512, 1>, Shape<1024, 1>, Shape<1024, 2>>(
+          a.d, [&](auto r, auto k) {
         constexpr int R = decltype(r)::value, K = decltype(k)::value;
         hipLaunchKernelGGL((norm_grad_kernel<TY, KIND, R, K>), grid, dim3(RowTeam<R>::kThreads), 0, st, a);
       });

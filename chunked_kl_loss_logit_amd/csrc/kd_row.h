@@ -3,6 +3,8 @@
 // a workgroup of 256 holds four rows; otherwise the workgroup is the row's.
 #pragma once
 
+#include <type_traits>
+
 #include "kd_elem.h"
 #include "kd_rows8.h"
 
@@ -12,9 +14,25 @@ namespace kd {
 // again for every pass over them.
 constexpr int64_t kRowMost = 16384;
 
+// launch(R, K) of the first of the shapes R x K whose registers hold d
+// elements (R K pieces of 8); false if none does.
+template <int R, int K>
+struct Shape {
+  static constexpr int kR = R, kK = K;
+};
+template <class S, class... More, class F>
+inline bool pick_shape(int64_t d, F&& launch) {
+  if (d <= (int64_t)8 * S::kR * S::kK) {
+    launch(std::integral_constant<int, S::kR>(), std::integral_constant<int, S::kK>());
+    return true;
+  }
+  if constexpr (sizeof...(More) > 0) return pick_shape<More...>(d, launch);
+  return false;
+}
+
 template <int R>
 struct RowTeam {
-  static constexpr int kThreads = R < 256 ? 256 : R;
+  static constexpr int kThreads = R < 256 ? 256 : R;  // a wave that has a row of its own, or the row's workgroup
   static constexpr int kRows = kThreads / R;  // rows of a workgroup
   static constexpr int kWaves = R / 64;
   __device__ static inline int lane() { return threadIdx.x % R; }
@@ -69,26 +87,6 @@ __device__ inline void store_any1(char* base, int type, int64_t i, float v) {
   if (type == kTypeF32) Elem<kTypeF32>::put1(base + 4 * i, v);
   else if (type == kTypeBf16) Elem<kTypeBf16>::put1(base + 2 * i, v);
   else Elem<kTypeF16>::put1(base + 2 * i, v);
-}
-
-// launch(R, K) with the fewest threads whose registers hold a row of d
-// elements; false if none does.
-template <class F>
-inline bool pick_row(int64_t d, F&& launch) {
-  const int64_t pieces = (d + 7) / 8;
-  auto with = [&](auto r, auto k) {
-    launch(r, k);
-    return true;
-  };
-  using std::integral_constant;
-  if (pieces <= 64) return with(integral_constant<int, 64>(), integral_constant<int, 1>());
-  if (pieces <= 128) return with(integral_constant<int, 64>(), integral_constant<int, 2>());
-  if (pieces <= 256) return with(integral_constant<int, 64>(), integral_constant<int, 4>());
-  if (pieces <= 512) return with(integral_constant<int, 256>(), integral_constant<int, 2>());
-  if (pieces <= 1024) return with(integral_constant<int, 256>(), integral_constant<int, 4>());
-  if (pieces <= 2048) return with(integral_constant<int, 1024>(), integral_constant<int, 2>());
-  static_assert(kRowMost == 2048 * 8, "the longest row that registers hold");
-  return false;
 }
 
 // launch with the element type as a constant

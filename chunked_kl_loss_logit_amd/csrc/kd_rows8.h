@@ -1,10 +1,15 @@
 // Groups of a row's values in 8 bits (the definition is kdlayers.h's).
 //
-// The quotient x / scale is rounded to few bits exactly, ties to even, without
-// 64-bit arithmetic: it is computed to within an ulp, the residual's sign
-// says on which side the exact quotient lies, and the 24-bit value next to it
-// towards zero gets its last bit set if the quotient was not exact ("round to
-// odd").  Rounding such a value to any format at least two bits shorter gives
+// The exact quotient x / scale is rounded, ties to even, without 64-bit
+// arithmetic.  x times the scale's reciprocal is off by less than 4 ulps; as
+// long as that leaves no doubt on which side of the middle of two steps the
+// quotient lies, rounding it is all there is to do.  Where a lane of the wave
+// holds a value in doubt (16-bit values hit ties often: half of a group's
+// largest is one for int8), all its values go the exact way.  Integers: the
+// residual of the nearest one says whether it is.  e4m3: the quotient to
+// within an ulp, the residual's sign, and the 24-bit value next to the exact
+// quotient towards zero with its last bit set if that is not exact ("round to
+// odd"); rounding such a value to any format at least two bits shorter gives
 // what rounding the exact quotient gives.
 #pragma once
 
@@ -21,20 +26,30 @@ struct Scale8 {
   float s, inv;   // scale lift, and its reciprocal; inv = 0: every q is 0
 };
 
-// top: |x|'s largest, as bits (NaN above infinity above every number)
+// top: |x|'s largest, as bits (NaN above infinity above every number).
+// The quotient by 127 or 448 is rounded correctly: the residual of the first
+// product is exact, the correction's own error is 2^-24 of an ulp, and a
+// 24-bit number over 127 or 7 is never nearer than 1/254 ulp to the middle of
+// two numbers.
 template <int KIND>
 __device__ inline Scale8 scale8(uint32_t top) {
+  constexpr float most = KIND == kRowsInt8 ? 127.f : 448.f, part = 1.f / most;
+  const float x = __uint_as_float(top);
   Scale8 r;
-  if (top >= 0x7f800000u) return Scale8{__uint_as_float(0x7fc00000u), 0.f, 1.f, 0.f};
-  r.scale = __fdiv_rn(__uint_as_float(top), KIND == kRowsInt8 ? 127.f : 448.f);
+  const float q = x * part;
+  r.scale = fmaf(fmaf(-q, most, x), part, q);
   r.lift = r.scale < 0x1p-90f ? 0x1p60f : 1.f;
   r.s = r.scale * r.lift;
-  r.inv = r.scale > 0.f ? __fdiv_rn(1.f, r.s) : 0.f;
+  r.inv = r.scale > 0.f ? __builtin_amdgcn_rcpf(r.s) : 0.f;  // off by an ulp at most
+  if (top >= 0x7f800000u) {
+    r.scale = __uint_as_float(0x7fc00000u);
+    r.s = 1.f;
+    r.inv = 0.f;
+  }
   return r;
 }
 
-// x / scale rounded to odd, at most the format's largest in size
-template <int KIND>
+// x / scale rounded to odd
 __device__ inline float odd_quotient(float x, const Scale8& g) {
   x *= g.lift;
   float q = x * g.inv;
@@ -43,30 +58,83 @@ __device__ inline float odd_quotient(float x, const Scale8& g) {
   uint32_t u = __float_as_uint(q);
   u -= (__float_as_uint(r) ^ u) >> 31;  // |quotient| below |q|: one step down
   u |= 1u;
-  q = r == 0.f ? q : __uint_as_float(u);
-  const float most = KIND == kRowsInt8 ? 127.f : 448.f;
-  return __builtin_amdgcn_fmed3f(q, -most, most);
+  return r == 0.f ? q : __uint_as_float(u);
 }
 
-// 8 values of one group
+// The integer nearest to x / scale, ties to even: the nearest to a quotient
+// that is a few ulps off, moved by one where the residual (exact: x and n s
+// agree in all but the last 24 bits) is above half the scale, or half of it
+// and n odd.
+__device__ inline int nearest_int(float x, const Scale8& g) {
+  x *= g.lift;
+  const float n = rintf(x * g.inv), r = fmaf(-n, g.s, x), a = fabsf(r), half = 0.5f * g.s;
+  int i = (int)n;
+  const bool move = a > half || (a == half && (i & 1));
+  if (move) i += r > 0.f ? 1 : -1;
+  return min(max(i, -127), 127);
+}
+
+__device__ inline uint32_t pack_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {  // their lowest
+  return __builtin_amdgcn_perm(__builtin_amdgcn_perm(d, c, 0x0c0c0400u), __builtin_amdgcn_perm(b, a, 0x0c0c0400u),
+                               0x05040100u);
+}
+__device__ inline uint32_t pack_e4m3(float a, float b, float c, float d) {
+  const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, lo, true);
+}
+
+// 8 values of one group, exactly, whatever its scale
 template <int KIND>
-__device__ inline uint2 quantize8(const float (&x)[8], const Scale8& g) {
-  if (g.inv == 0.f) return uint2{0u, 0u};
-  float q[8];
+__device__ inline uint2 quantize8_exact(const float (&x)[8], const Scale8& g) {
+  uint32_t w[2];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) q[i] = odd_quotient<KIND>(x[i], g);
-  uint32_t w[2] = {0u, 0u};
-  if constexpr (KIND == kRowsInt8) {
+  for (int h = 0; h < 2; ++h) {
+    if constexpr (KIND == kRowsInt8) {
+      w[h] = pack_bytes(nearest_int(x[4 * h], g), nearest_int(x[4 * h + 1], g), nearest_int(x[4 * h + 2], g),
+                        nearest_int(x[4 * h + 3], g));
+    } else {
+      float q[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w[i >> 2] |= ((uint32_t)(int)rintf(q[i]) & 0xffu) << (8 * (i & 3));
-  } else {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      int v = __builtin_amdgcn_cvt_pk_fp8_f32(q[4 * i], q[4 * i + 1], 0, false);
-      w[i] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q[4 * i + 2], q[4 * i + 3], v, true);
+      for (int i = 0; i < 4; ++i) q[i] = __builtin_amdgcn_fmed3f(odd_quotient(x[4 * h + i], g), -448.f, 448.f);
+      w[h] = pack_e4m3(q[0], q[1], q[2], q[3]);
     }
   }
-  return uint2{w[0], w[1]};
+  return g.inv == 0.f ? uint2{0u, 0u} : uint2{w[0], w[1]};
+}
+
+template <int KIND>
+__device__ inline uint2 quantize8(const float (&x)[8], const Scale8& g) {
+  uint2 w;
+  bool doubt = g.lift != 1.f || g.inv == 0.f;
+  if constexpr (KIND == kRowsInt8) {
+    // adding 1.5 2^23 rounds to the integer, which then is what the sum's last bits say
+    constexpr float magic = 12582912.f;
+    float m[8], far = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      m[i] = fmaf(x[i], g.inv, magic);
+      far = fmaxf(far, fabsf(fmaf(x[i], g.inv, magic - m[i])));
+    }
+    doubt |= far > 0.5f - 0x1p-15f;  // 4 ulps of 127 are 2^-15
+    w.x = pack_bytes(__float_as_uint(m[0]), __float_as_uint(m[1]), __float_as_uint(m[2]), __float_as_uint(m[3]));
+    w.y = pack_bytes(__float_as_uint(m[4]), __float_as_uint(m[5]), __float_as_uint(m[6]), __float_as_uint(m[7]));
+  } else {
+    float q[8];
+    uint32_t near = ~0u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      q[i] = x[i] * g.inv;
+      // the 20 bits behind the significand that is kept; below 2^-6 the steps are as wide as above it
+      const float a = fabsf(q[i]);
+      const uint32_t u = __float_as_uint(a < 0x1p-6f ? a + 0x1p-6f : a);
+      near = min(near, (u - 0x80000u + 8u) & 0xfffffu);
+    }
+    doubt |= near <= 16u;  // within 8 ulps of the middle of two steps
+    w.x = pack_e4m3(q[0], q[1], q[2], q[3]);
+    w.y = pack_e4m3(q[4], q[5], q[6], q[7]);
+  }
+  if (__any(doubt)) w = quantize8_exact<KIND>(x, g);
+  return w;
 }
 
 // the values in units of their scale
