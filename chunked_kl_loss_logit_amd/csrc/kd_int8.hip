@@ -31,6 +31,11 @@ __device__ inline void mma_i8(i32x16_t& acc, u32x4_t a, u32x4_t b) {
                                               0);
 }
 
+__device__ inline void mma0_i8(i32x16_t& acc, u32x4_t a, u32x4_t b) {  // into a fresh accumulator
+  acc = __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(i32x4_t, a), __builtin_bit_cast(i32x4_t, b), i32x16_t{},
+                                              0, 0, 0);
+}
+
 constexpr int kKTurn = kRing * kRowB;  // k of a ring turn
 
 }  // namespace
@@ -49,86 +54,156 @@ __global__ __launch_bounds__(256) void int8_panels_kernel(const char* x, long T,
 // ------------------------------------------------------------------ tiles
 namespace {
 
-template <int NBI>
-__device__ inline void stage_i32(const Slots& sl, const i32x16_t (&acc)[4][4]) {
-  const int w = wave_id();
-  const int lane = opaque((int)threadIdx.x) & 63;
-  const StageOff so = stage_offsets(w >> 1, lane);
-  float* st = (w & 1) ? st_pair<1>(sl) : st_pair<0>(sl);
-#pragma unroll
-  for (int mb = 0; mb < 4; ++mb) {
-    i32x16_t v = acc[mb][NBI];
-    asm volatile("" : "+a"(v));
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      st[so.o[((i & 3) >> 1) + 2 * ((i >> 2) & 1)] + mb * 1024 + (i >> 2) * 256 + (i & 3) * 32] = (float)v[i];
-  }
+// Two tiles' scales: sx of 256 rows, sw of 256 columns.
+struct ScaleSlots {
+  float* f;  // [2][512]
+  __device__ inline float* sx(int t) const { return f + (t & 1) * 512; }
+  __device__ inline float* sw(int t) const { return f + (t & 1) * 512 + 256; }
+};
+
+__device__ inline void dma4(__amdgpu_buffer_rsrc_t rs, uint32_t voff, uint32_t soff, float* lds_wave_base) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (KD_LDS void*)lds_wave_base, 4, (int)voff, (int)soff, 0, 0);
 }
 
-template <int TO, int NBI>
-__device__ inline void store_round(const Slots& sl, const Int8Args& a, const i32x16_t (&acc)[4][4], long row0, long n0) {
-  stage_i32<NBI>(sl, acc);
-  __syncthreads();
-  const int tid = opaque((int)threadIdx.x);
-  const int q = tid & 3;
+// The lane's half of 16 packed columns: lane l holds columns 4 (l / 32) .. + 3
+// of both groups of 8, and gets all of group l / 32.
+__device__ inline u32x4_t join_halves(uint32_t a0, uint32_t a1, uint32_t b0, uint32_t b1) {
+  const auto p = __builtin_amdgcn_permlane32_swap((int)a0, (int)b0, false, false);
+  const auto q = __builtin_amdgcn_permlane32_swap((int)a1, (int)b1, false, false);
+  return u32x4_t{(uint32_t)p[0], (uint32_t)q[0], (uint32_t)p[1], (uint32_t)q[1]};
+}
+
+// Stores n (at most 16 bytes' worth of) values that lie in v.
+template <int TO>
+__device__ inline void store_some(char* to, u32x4_t v, long n) {
+  constexpr int N = 16 / Elem<TO>::kBytes;
+  if (n >= N) {
+    store16(to, v);
+    return;
+  }
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const StPair st = h ? st_pair<1>(sl) : st_pair<0>(sl);
-    const long col = n0 + 128 * h + 32 * NBI + 8 * q;
-    const int n = (int)min(8L, a.V - col);
-    if (n <= 0) continue;
-    float sw[8];
+  for (int i = 0; i < N; ++i)
+    if (i < n) {
+      if constexpr (TO == kTypeF32) reinterpret_cast<uint32_t*>(to)[i] = v[i];
+      else reinterpret_cast<uint16_t*>(to)[i] = (uint16_t)(v[i >> 1] >> (16 * (i & 1)));
+    }
+}
+
+// A wave's quarter of a tile from its accumulators, which hold it transposed
+// (mma_frags_t): lane l has row 32 mb + l % 32 and in register i column 32 nb +
+// 8 (i / 4) + 4 (l / 32) + i % 4.  No staging in LDS and no barriers: the waves
+// go on to the next tile by themselves, whose operands keep landing.
+template <int TO>
+__device__ inline void store_quarter(const Int8Args& a, const i32x16_t (&acc)[4][4], const float* sx, const float* sw,
+                                     long row0, long n0) {
+  const int w = wave_id();
+  const int lane = opaque((int)threadIdx.x) & 63;
+  const int m = lane & 31, h = lane >> 5;
+  const int r0 = (w >> 1) * 128, c0 = (w & 1) * 128;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sw[i] = i < n ? a.sw[col + i] : 0.f;
+  for (int nb = 0; nb < 4; ++nb) {
+    float4 s[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int r = (tid >> 2) + 64 * k;
-      if (row0 + r >= a.T) break;
-      const float sx = a.sx[row0 + r];
-      const float4 u = st_read4(st, r, 2 * q), v = st_read4(st, r, 2 * q + 1);
-      const float y[8] = {u.x * sx * sw[0], u.y * sx * sw[1], u.z * sx * sw[2], u.w * sx * sw[3],
-                          v.x * sx * sw[4], v.y * sx * sw[5], v.z * sx * sw[6], v.w * sx * sw[7]};
-      store8<TO>(a.out + ((row0 + r) * a.V + col) * Elem<TO>::kBytes, y, n);
+    for (int q = 0; q < 4; ++q) s[q] = *reinterpret_cast<const float4*>(sw + c0 + 32 * nb + 8 * q + 4 * h);
+#pragma unroll
+    for (int mb = 0; mb < 4; ++mb) {
+      const long row = row0 + r0 + 32 * mb + m;
+      const float x = sx[r0 + 32 * mb + m];
+      i32x16_t v = acc[mb][nb];
+      asm volatile("" : "+a"(v));
+      float y[16];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        y[4 * q] = (float)v[4 * q] * x * s[q].x;
+        y[4 * q + 1] = (float)v[4 * q + 1] * x * s[q].y;
+        y[4 * q + 2] = (float)v[4 * q + 2] * x * s[q].z;
+        y[4 * q + 3] = (float)v[4 * q + 3] * x * s[q].w;
+      }
+      const long col = n0 + c0 + 32 * nb;
+      char* const to = a.out + (row * a.V + col) * Elem<TO>::kBytes;
+      u32x4_t o[4];
+      if constexpr (TO == kTypeF32) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          o[q] = u32x4_t{__float_as_uint(y[4 * q]), __float_as_uint(y[4 * q + 1]), __float_as_uint(y[4 * q + 2]),
+                         __float_as_uint(y[4 * q + 3])};
+      } else {
+#pragma unroll
+        for (int g = 0; g < 2; ++g)
+          o[g] = join_halves(pack2x16<TO>(y[8 * g], y[8 * g + 1]), pack2x16<TO>(y[8 * g + 2], y[8 * g + 3]),
+                             pack2x16<TO>(y[8 * g + 4], y[8 * g + 5]), pack2x16<TO>(y[8 * g + 6], y[8 * g + 7]));
+      }
+      if (row < a.T) {
+        if constexpr (TO == kTypeF32) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) store_some<TO>(to + 4 * (8 * q + 4 * h), o[q], a.V - col - 8 * q - 4 * h);
+        } else {
+#pragma unroll
+          for (int g = 0; g < 2; ++g) store_some<TO>(to + 2 * (16 * g + 8 * h), o[g], a.V - col - 16 * g - 8 * h);
+        }
+      }
     }
   }
-  __syncthreads();
 }
 
 }  // namespace
 
+// Persistent: one workgroup a CU, and one ring that never drains.  XCD x has
+// one contiguous range of the tiles (rows grouped, see grouped_coords), its
+// workgroups take turns in it, so that what they read at one time shares
+// panels of both operands in the XCD's cache.
 template <int TO>
 __global__ __launch_bounds__(kThreads, 1) void int8_tile_kernel(Int8Args a, int nrb, int ncb, int group) {
   KD_DECLARE_SLOTS(sl);
-  int rb, cb;
-  grouped_coords(xcd_remap(blockIdx.x, gridDim.x), nrb, ncb, group, rb, cb);
-  const long row0 = (long)rb * kBM, n0 = (long)cb * 256;
-  const long stages = (a.d + kRowB - 1) / kRowB, nst = (stages + kRing - 1) / kRing * kRing;
+  const int tiles = nrb * ncb, xcd = blockIdx.x & 7, turn = gridDim.x >> 3;  // the grid is a multiple of 8
+  const int begin = (int)((long)tiles * xcd / 8) + (int)(blockIdx.x >> 3), end = (int)((long)tiles * (xcd + 1) / 8);
+  const int mine = begin < end ? (end - begin + turn - 1) / turn : 0;
+  const long stages = (a.d + kRowB - 1) / kRowB, nst = (stages + kRing - 1) / kRing * kRing, w_last = stages - 1;
+  const long panel_bytes = a.T * nst * kRowB;
+
+  // what a tile's loads start from; rows behind the last one of either operand
+  // and w's bytes behind its end are past the descriptors' ranges
+  struct Place {
+    long row0, n0;
+    __amdgpu_buffer_rsrc_t x, w;
+  };
+  auto place = [&](int t) {
+    int rb, cb;
+    grouped_coords(min(begin + t * turn, tiles - 1), nrb, ncb, group, rb, cb);
+    Place p;
+    p.row0 = (long)rb * kBM;
+    p.n0 = (long)cb * 256;
+    p.x = make_rsrc(a.panels + p.row0 * kRowB, min(panel_bytes - p.row0 * kRowB, 0xffffffffL));
+    p.w = make_rsrc(a.w + p.n0 * a.d, min((a.V - p.n0) * a.d, 0xffffffffL));
+    return p;
+  };
+  const __amdgpu_buffer_rsrc_t rsx = make_rsrc(reinterpret_cast<const char*>(a.sx), a.T * 4);
+  const __amdgpu_buffer_rsrc_t rsw = make_rsrc(reinterpret_cast<const char*>(a.sw), min((long)a.V * 4, 0xffffffffL));
+  const ScaleSlots scales{sl.ep};
+  const uint32_t own = 4 * (threadIdx.x & 63);
+  auto load_scales = [&](int t, const Place& p) {
+    const uint32_t at = 256u * (uint32_t)wave_id();
+    dma4(rsx, own, (uint32_t)(p.row0 * 4) + at, scales.sx(t) + 64 * wave_id());
+    dma4(rsw, own, (uint32_t)(p.n0 * 4) + at, scales.sw(t) + 64 * wave_id());
+  };
 
   DmaRows<256> ra, rw;
-  const char* xbase = a.panels + row0 * kRowB;
-  ra.init(
-      xbase, [&](int i) { return xbase + (row0 + DmaRows<256>::row_of(i) < a.T ? DmaRows<256>::row_of(i) : 0) * (long)kRowB; },
-      (uint32_t)(a.T * kRowB));
-  const char* wbase = a.w + n0 * a.d;
-  rw.init(wbase, [&](int i) { return wbase + (n0 + DmaRows<256>::row_of(i) < a.V ? DmaRows<256>::row_of(i) : 0) * a.d; });
-  // the last rows' stages end behind w where d is no multiple of 64: past the range, loads give nothing
-  rw.rs = make_rsrc(wbase, min((a.V - n0) * a.d, 0xffffffffL));
-
+  ra.init(a.panels, [&](int i) { return a.panels + DmaRows<256>::row_of(i) * (long)kRowB; }, (uint32_t)(a.T * kRowB));
+  rw.init(a.w, [&](int i) { return a.w + DmaRows<256>::row_of(i) * a.d; });
   FragReader<256> rd;
   rd.init_rows();
   i32x16_t acc[4][4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0;
-  const long w_last = stages - 1;
-  ring_contract<DmaRows<256>::kPer * 2, FragsRows<256>>(
-      sl, (int)nst,
-      [&](long s, char* da, char* db) {
+  Place now = place(0), next = place(1);
+  load_scales(0, now);
+  int at = 0;  // the tile of `now`
+  ring_run<DmaRows<256>::kPer * 2, FragsRows<256>>(
+      sl, mine, (int)nst,
+      [&](long t, int s, char* da, char* db) {
+        const bool cur = t == at;
+        ra.rs = cur ? now.x : next.x;
+        rw.rs = cur ? now.w : next.w;
         ra.issue(s, da);
-        rw.issue(min(s, w_last), db);
+        rw.issue(min((long)s, w_last), db);
       },
       [&](const char* slot, FragsRows<256>& f) { rd.read_rows(slot, f); },
       [&](const FragsRows<256>& f) {
@@ -137,12 +212,25 @@ __global__ __launch_bounds__(kThreads, 1) void int8_tile_kernel(Int8Args a, int 
 #pragma unroll
           for (int mb = 0; mb < 4; ++mb)
 #pragma unroll
-            for (int nb = 0; nb < 4; ++nb) mma_i8(acc[mb][nb], f.a[kg][mb], f.b[kg][nb]);
+            for (int nb = 0; nb < 4; ++nb) mma_i8(acc[mb][nb], f.b[kg][nb], f.a[kg][mb]);
+      },
+      [&](const FragsRows<256>& f) {
+#pragma unroll
+        for (int mb = 0; mb < 4; ++mb)
+#pragma unroll
+          for (int nb = 0; nb < 4; ++nb) mma0_i8(acc[mb][nb], f.b[0][nb], f.a[0][mb]);
+#pragma unroll
+        for (int mb = 0; mb < 4; ++mb)
+#pragma unroll
+          for (int nb = 0; nb < 4; ++nb) mma_i8(acc[mb][nb], f.b[1][nb], f.a[1][mb]);
+      },
+      [&](int t) {
+        store_quarter<TO>(a, acc, scales.sx(t), scales.sw(t), now.row0, now.n0);
+        now = next;
+        at = t + 1;
+        next = place(t + 2);
+        load_scales(t + 1, now);  // those slots were read last after the tile before this one
       });
-  store_round<TO, 0>(sl, a, acc, row0, n0);
-  store_round<TO, 1>(sl, a, acc, row0, n0);
-  store_round<TO, 2>(sl, a, acc, row0, n0);
-  store_round<TO, 3>(sl, a, acc, row0, n0);
 }
 
 // ------------------------------------------------------------------ few rows
@@ -271,8 +359,7 @@ hipError_t launch_int8_panels(const Int8Args& a, hipStream_t st) {
 hipError_t launch_int8_tiles(const Int8Args& a, hipStream_t st) {
   const int nrb = (int)((a.T + 255) / 256), ncb = (int)((a.V + 255) / 256);
   pick_type(a.out_type, [&](auto ty) {
-    hipLaunchKernelGGL((int8_tile_kernel<decltype(ty)::value>), dim3((unsigned)(nrb * ncb)), dim3(kThreads), 0, st, a,
-                       nrb, ncb, 4);
+    hipLaunchKernelGGL((int8_tile_kernel<decltype(ty)::value>), dim3(256), dim3(kThreads), 0, st, a, nrb, ncb, 4);
   });
   return hipGetLastError();
 }
