@@ -11,7 +11,8 @@
 // (kd_dma.h) padded with zeros to whole ring turns, which cancel whatever w's
 // rows read past their end.  Few rows or few tiles: w is what has to be read;
 // a workgroup takes 64 channels and up to 128 rows, each of its four waves a
-// quarter of k, straight from global memory into registers.
+// quarter of k, straight from global memory into registers (few channels: 32
+// and eight waves).
 #include <type_traits>
 
 #include "kd_dma.h"
@@ -235,35 +236,35 @@ __global__ __launch_bounds__(kThreads, 1) void int8_tile_kernel(Int8Args a, int 
 
 // ------------------------------------------------------------------ few rows
 namespace {
-constexpr int kFewV = 64;     // channels of a workgroup
 constexpr int kFewU = 4;      // 16-byte chunks of a lane and step
 constexpr int kFewK = 2 * 16 * kFewU;  // k of a step
 }  // namespace
 
-// NB blocks of 32 rows of x
-template <int TO, int NB>
-__global__ __launch_bounds__(256) void int8_few_kernel(Int8Args a) {
-  __shared__ int part[4][32][36];
+// NB blocks of 32 rows of x and F of 32 channels a workgroup, W waves that
+// split k.
+template <int TO, int NB, int F, int W>
+__global__ __launch_bounds__(64 * W) void int8_few_kernel(Int8Args a) {
+  __shared__ __attribute__((aligned(16))) int part[W][32][36];
   const int lane = threadIdx.x & 63, w = wave_id();
   const int m = lane & 31, h = lane >> 5;
-  const long v0 = (long)blockIdx.x * kFewV, t0 = (long)blockIdx.y * 32 * NB;
-  const char* wp[2];
+  const long v0 = (long)blockIdx.x * 32 * F, t0 = (long)blockIdx.y * 32 * NB;
+  const char* wp[F];
   const char* xp[NB];
 #pragma unroll
-  for (int f = 0; f < 2; ++f) wp[f] = a.w + min(v0 + 32 * f + m, (long)a.V - 1) * a.d + h * 16 * kFewU;
+  for (int f = 0; f < F; ++f) wp[f] = a.w + min(v0 + 32 * f + m, (long)a.V - 1) * a.d + h * 16 * kFewU;
 #pragma unroll
   for (int f = 0; f < NB; ++f) xp[f] = a.x + min(t0 + 32 * f + m, (long)a.T - 1) * a.d + h * 16 * kFewU;
 
   const int steps = (int)((a.d + kFewK - 1) / kFewK), whole = (int)(a.d / kFewK);
-  const int s0 = steps * w / 4, s1 = steps * (w + 1) / 4;
-  u32x4_t rw[2][2][kFewU], rx[2][NB][kFewU];
+  const int s0 = steps * w / W, s1 = steps * (w + 1) / W;
+  u32x4_t rw[2][F][kFewU], rx[2][NB][kFewU];
   auto load = [&](int buf, int s) {
     const long at = (long)s * kFewK;
     if (s < whole) {
 #pragma unroll
       for (int u = 0; u < kFewU; ++u) {
 #pragma unroll
-        for (int f = 0; f < 2; ++f) rw[buf][f][u] = ld16(wp[f] + at + 16 * u);
+        for (int f = 0; f < F; ++f) rw[buf][f][u] = ld16(wp[f] + at + 16 * u);
 #pragma unroll
         for (int f = 0; f < NB; ++f) rx[buf][f][u] = ld16(xp[f] + at + 16 * u);
       }
@@ -272,15 +273,15 @@ __global__ __launch_bounds__(256) void int8_few_kernel(Int8Args a) {
       for (int u = 0; u < kFewU; ++u) {
         const bool in = at + h * 16 * kFewU + 16 * u < a.d;
 #pragma unroll
-        for (int f = 0; f < 2; ++f) rw[buf][f][u] = in ? ld16(wp[f] + at + 16 * u) : zero4();
+        for (int f = 0; f < F; ++f) rw[buf][f][u] = in ? ld16(wp[f] + at + 16 * u) : zero4();
 #pragma unroll
         for (int f = 0; f < NB; ++f) rx[buf][f][u] = in ? ld16(xp[f] + at + 16 * u) : zero4();
       }
     }
   };
-  i32x16_t acc[2][NB];
+  i32x16_t acc[F][NB];
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int i = 0; i < F; ++i)
 #pragma unroll
     for (int j = 0; j < NB; ++j)
 #pragma unroll
@@ -289,7 +290,7 @@ __global__ __launch_bounds__(256) void int8_few_kernel(Int8Args a) {
 #pragma unroll
     for (int u = 0; u < kFewU; ++u)
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < F; ++i)
 #pragma unroll
         for (int j = 0; j < NB; ++j) mma_i8(acc[i][j], rw[buf][i][u], rx[buf][j][u]);
   };
@@ -306,9 +307,9 @@ __global__ __launch_bounds__(256) void int8_few_kernel(Int8Args a) {
   }
 
   // the waves' sums, block by block: [row of x][channel]
-  const int r = threadIdx.x >> 3, c = 4 * (threadIdx.x & 7);
+  const int r = (threadIdx.x >> 3) & 31, c = 4 * (threadIdx.x & 7);
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int i = 0; i < F; ++i)
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
       __syncthreads();
@@ -317,9 +318,10 @@ __global__ __launch_bounds__(256) void int8_few_kernel(Int8Args a) {
         *reinterpret_cast<i32x4_t*>(&part[w][m][8 * q + 4 * h]) =
             i32x4_t{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
       __syncthreads();
+      if (threadIdx.x >= 256) continue;
       i32x4_t s = *reinterpret_cast<const i32x4_t*>(&part[0][r][c]);
 #pragma unroll
-      for (int k = 1; k < 4; ++k) s += *reinterpret_cast<const i32x4_t*>(&part[k][r][c]);
+      for (int k = 1; k < W; ++k) s += *reinterpret_cast<const i32x4_t*>(&part[k][r][c]);
       const long t = t0 + 32 * j + r, v = v0 + 32 * i + c;
       if (t >= a.T || v >= a.V) continue;
       const float sx = a.sx[t];
@@ -343,8 +345,16 @@ __global__ __launch_bounds__(256) void int8_few_kernel(Int8Args a) {
 }
 
 // ------------------------------------------------------------------ launches
+// Rounds of the chip's 256 CUs: a tile takes 48 us at d = 4096, a workgroup of
+// the other kernel with 128 rows 28 us, one of them a CU.  Either side, us at
+// d = 4096: V 32000, T 96 50 / 51, 128 50 / 59, 512 66 / 118; V 11008, T 128
+// 43 / 29, 192 43 / 50, 512 47 / 85; V 4096, T 512 45 / 28, 1024 48 / 55.  Up to
+// 64 rows the other kernel has two or three workgroups a CU and waits for w
+// only: V 128256, T 32 149 / 123, 64 153 / 160.
 bool int8_tiles(int64_t T, int64_t d, int64_t V) {
-  return T > 128 && ((T + 255) / 256) * ((V + 255) / 256) >= 128;
+  auto rounds = [](int64_t workgroups) { return (workgroups + 255) / 256; };
+  const int64_t tile = rounds(((T + 255) / 256) * ((V + 255) / 256)), few = rounds(((T + 127) / 128) * ((V + 63) / 64));
+  return T > 64 && 7 * few > 12 * tile;
 }
 int64_t int8_panel_bytes(int64_t T, int64_t d) { return T * ((d + kKTurn - 1) / kKTurn * kKTurn); }
 
@@ -367,14 +377,22 @@ hipError_t launch_int8_tiles(const Int8Args& a, hipStream_t st) {
 hipError_t launch_int8_few(const Int8Args& a, hipStream_t st) {
   pick_type(a.out_type, [&](auto ty) {
     constexpr int TO = decltype(ty)::value;
-    auto with = [&](auto nb) {
-      constexpr int NB = decltype(nb)::value;
-      const dim3 grid((unsigned)((a.V + kFewV - 1) / kFewV), (unsigned)((a.T + 32 * NB - 1) / (32 * NB)));
-      hipLaunchKernelGGL((int8_few_kernel<TO, NB>), grid, dim3(256), 0, st, a);
+    auto with = [&](auto nb, auto f, auto waves) {
+      constexpr int NB = decltype(nb)::value, F = decltype(f)::value, W = decltype(waves)::value;
+      const dim3 grid((unsigned)((a.V + 32 * F - 1) / (32 * F)), (unsigned)((a.T + 32 * NB - 1) / (32 * NB)));
+      hipLaunchKernelGGL((int8_few_kernel<TO, NB, F, W>), grid, dim3(64 * W), 0, st, a);
     };
-    if (a.T <= 32) with(std::integral_constant<int, 1>());
-    else if (a.T <= 64) with(std::integral_constant<int, 2>());
-    else with(std::integral_constant<int, 4>());
+    using std::integral_constant;
+    auto rows = [&](auto f, auto waves) {
+      if (a.T <= 32) with(integral_constant<int, 1>(), f, waves);
+      else if (a.T <= 64) with(integral_constant<int, 2>(), f, waves);
+      else with(integral_constant<int, 4>(), f, waves);
+    };
+    // Half the channels a workgroup and twice its waves, if one round takes
+    // them.  us, so / otherwise: V 4096, T 1 10 / 15, 64 14 / 18, 128 22 / 27; in
+    // two rounds V 4096, T 384 44 / 28, V 11008, T 128 44 / 29.
+    if ((a.V + 31) / 32 * ((a.T + 127) / 128) <= 256) rows(integral_constant<int, 1>(), integral_constant<int, 8>());
+    else rows(integral_constant<int, 2>(), integral_constant<int, 4>());
   });
   return hipGetLastError();
 }
