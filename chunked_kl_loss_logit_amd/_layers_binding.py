@@ -143,15 +143,19 @@ def kd_embedding_fwd(tokens, table, mask, scale, tied, out, stream=None):
     _embedding_fwd(T, V, d, tokens, table, mask, scale, tied, out, stream)
 
 
+def _embedding_bwd(T, V, d, grad, tokens, mask, scale, tied, accumulate, grad_table, workspace, stream=None):
+    nb = _ws_bytes(workspace)
+    index, (g, tokens, mask, out, ws) = _place(grad, tokens, mask, grad_table, workspace)
+    _run("kd_embedding_bwd", index, stream, g, tokens, mask, float(scale), T, int(V), d, GRAD_TYPES[grad.dtype],
+         GRAD_TYPES[grad_table.dtype], bool(tied), bool(accumulate), out, ws, nb)
+
+
 def kd_embedding_bwd(grad, tokens, mask, scale, V, tied, accumulate, grad_table, workspace, stream=None):
     """Enqueue the gradient; grad_table ([V,d], or [d,V] if tied) in place."""
     T = _tokens(tokens, mask)
     _, d = _matrix("grad", grad, T, TYPES)
     _need("grad_table", grad_table, (d, V) if tied else (V, d), TYPES)
-    nb = _ws_bytes(workspace)
-    index, (g, tokens, mask, out, ws) = _place(grad, tokens, mask, grad_table, workspace)
-    _run("kd_embedding_bwd", index, stream, g, tokens, mask, float(scale), T, int(V), d, GRAD_TYPES[grad.dtype],
-         GRAD_TYPES[grad_table.dtype], bool(tied), bool(accumulate), out, ws, nb)
+    _embedding_bwd(T, V, d, grad, tokens, mask, scale, tied, accumulate, grad_table, workspace, stream)
 
 
 # ---------------------------------------------------------------- rows in 8 bits
@@ -192,6 +196,21 @@ def kd_layer_norm_workspace_size(T, d) -> int:
 
 
 def _norm_in(x, weight, bias, mask, name="x"):
+    """T and d.  What a right call needs is looked at first, in one go; a wrong one is told what is wrong after that."""
+    try:
+        dtype, (T, d) = x.dtype, x.shape
+        if dtype in GRAD_TYPES:
+            row, wide = (d,), True
+            if weight is not None:
+                wide = weight.shape == row and weight.dtype in (dtype, torch.float32)
+                if bias is not None:
+                    wide = wide and bias.dtype == weight.dtype
+            if bias is not None:
+                wide = wide and bias.shape == row and bias.dtype in (dtype, torch.float32)
+            if wide and (mask is None or (mask.shape == (T,) and mask.dtype in _MASK)):
+                return T, d
+    except (AttributeError, TypeError, ValueError):
+        pass
     T, d = _matrix(name, x, None, TYPES)
     for n, t in (("weight", weight), ("bias", bias)):
         _need(n, t, (d,), (x.dtype, torch.float32), optional=True)
@@ -239,8 +258,8 @@ def _norm_bwd_in(grad, x, weight, mask, mean, rstd, group, q, scale):
         if x is not None:
             raise ValueError("x must be None where q and scale stand for it")
         code = ROWS_KINDS[_quantized(q, scale, group, T, d)[0]]
-    _need("mean", mean, (T,), _F32)
-    _need("rstd", rstd, (T,), _F32)
+    for n, t in (("mean", mean), ("rstd", rstd)):
+        _need(n, t, (T,), _F32)
     return T, d, code
 
 

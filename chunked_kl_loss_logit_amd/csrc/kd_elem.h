@@ -73,25 +73,53 @@ __device__ inline uint32_t pack2x16(float a, float b) {
 }
 
 // n of the piece's elements exist (8 or more: all); the others read as 0.
+// inner: 8 elements lie before the piece in its row.  A last piece of fewer is
+// then loaded as the row's last 8 elements, and settle8 moves its own to their
+// place once it is needed: until then nothing waits for the load.
 template <int TY>
-__device__ inline Raw8<TY> load8(const char* p, int n) {
-  Raw8<TY> r;
-  if (n >= 8) {
-    r.v[0] = load16(p);
-    if constexpr (TY == kTypeF32) r.v[1] = load16(p + 16);
-    return r;
-  }
-  uint32_t w[TY == kTypeF32 ? 8 : 4] = {};
+__device__ inline Raw8<TY> load8(const char* p, int n, bool inner) {
+  Raw8<TY> r = {};
+  if (n >= 8 || (n > 0 && inner)) {
+    const char* q = n >= 8 ? p : p - (8 - n) * Elem<TY>::kBytes;
+    r.v[0] = load16(q);
+    if constexpr (TY == kTypeF32) r.v[1] = load16(q + 16);
+  } else if (n > 0) {  // a row of fewer than 8
+    uint32_t w[TY == kTypeF32 ? 8 : 4] = {};
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    if (i >= n) continue;
-    if constexpr (TY == kTypeF32)
-      w[i] = *reinterpret_cast<const uint32_t*>(p + 4 * i);
-    else
-      w[i >> 1] |= (uint32_t)*reinterpret_cast<const uint16_t*>(p + 2 * i) << (16 * (i & 1));
+    for (int i = 0; i < 8; ++i) {
+      if (i >= n) continue;
+      if constexpr (TY == kTypeF32)
+        w[i] = *reinterpret_cast<const uint32_t*>(p + 4 * i);
+      else
+        w[i >> 1] |= (uint32_t)*reinterpret_cast<const uint16_t*>(p + 2 * i) << (16 * (i & 1));
+    }
+    __builtin_memcpy(&r, w, sizeof r);
+  }
+  return r;
+}
+template <int TY>
+__device__ inline void settle8(Raw8<TY>& r, int n, bool inner) {
+  if (n >= 8 || n <= 0 || !inner) return;
+  constexpr int W = TY == kTypeF32 ? 8 : 4;
+  uint32_t w[W];
+  __builtin_memcpy(w, &r, sizeof r);
+  const int bits = (8 - n) * Elem<TY>::kBytes * 8;  // down by so many
+#pragma unroll
+  for (int k = W / 2; k > 0; k >>= 1) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      const uint32_t from = i + k < W ? w[i + k] : 0u;
+      w[i] = (bits >> 5) & k ? from : w[i];
+    }
+  }
+  if constexpr (TY != kTypeF32) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      const uint32_t up = i + 1 < W ? w[i + 1] : 0u;
+      w[i] = bits & 16 ? (w[i] >> 16) | (up << 16) : w[i];
+    }
   }
   __builtin_memcpy(&r, w, sizeof r);
-  return r;
 }
 template <int TY>
 __device__ inline void unpack8(const Raw8<TY>& r, float (&x)[8]) {

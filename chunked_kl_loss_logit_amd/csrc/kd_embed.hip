@@ -48,7 +48,7 @@ __global__ __launch_bounds__(256) void embed_kernel(EmbedArgs a, int units) {
 #pragma unroll
     for (int i = 0; i < SLABS; ++i) {
       const int64_t at = 8 * (int64_t)(p0 + 64 * i);
-      r[i] = load8<TY>(row + at * Elem<TY>::kBytes, (int)(a.d - at));
+      r[i] = load8<TY>(row + at * Elem<TY>::kBytes, (int)(a.d - at), at > 0);
     }
   }
 #pragma unroll
@@ -57,6 +57,7 @@ __global__ __launch_bounds__(256) void embed_kernel(EmbedArgs a, int units) {
     if (at >= a.d) continue;
     float x[8];
     if (in) {
+      settle8<TY>(r[i], (int)(a.d - at), at > 0);
       unpack8<TY>(r[i], x);
 #pragma unroll
       for (int j = 0; j < 8; ++j) x[j] *= a.scale;
@@ -128,6 +129,19 @@ __device__ inline uint32_t key_of(const SortArgs& a, int64_t i) {
   return v < 0 || v >= a.V ? (uint32_t)a.V : (uint32_t)v;
 }
 
+// The first launch of a sort clears the tokens' marks, a workgroup of 1024 its
+// share of them; the last one sets those of the tokens that occur, to some
+// entry of theirs (the first one up to kSortChunk tokens).
+__device__ inline void clear_runs(const SortArgs& a) {
+  const int64_t step = (int64_t)gridDim.x * 4096;
+  for (int64_t v = (int64_t)blockIdx.x * 4096 + 4 * threadIdx.x; v < a.V; v += step) {
+    if (v + 4 <= a.V)
+      *reinterpret_cast<int4*>(a.run_of + v) = int4{-1, -1, -1, -1};
+    else
+      for (int64_t i = v; i < a.V; ++i) a.run_of[i] = -1;
+  }
+}
+
 int bits_of(int64_t V) {  // of the keys 0 .. V
   int b = 1;
   while ((V >> b) != 0) ++b;
@@ -156,25 +170,25 @@ __device__ inline uint32_t place_in_block(uint32_t digit, uint32_t* seen, uint32
 // Tied weights: every load takes a cache line for one element, and what limits
 // the kernel is how many lines are asked for.  A workgroup takes kTiedT tokens,
 // sorts them by the cache line of W's rows that they lie in, and goes down
-// kTiedK rows: the lanes of a wave then share lines, and neighbouring waves do.
-// The elements are turned in LDS and written in runs of kTiedK, each to its
+// ROWS rows: the lanes of a wave then share lines, and neighbouring waves do.
+// The elements are turned in LDS and written in runs of ROWS, each to its
 // token's row.  Workgroups of the same rows of W run on one XCD.  Up to
 // kTiedFew tokens, 64 to a workgroup and unsorted, sorting costs more than it
 // saves.
-constexpr int kTiedT = 1024, kTiedK = 16;
+constexpr int kTiedT = 1024;
 constexpr int64_t kTiedFew = 512;
 
-template <int TY>
+template <int TY, int ROWS>
 __global__ __launch_bounds__(kTiedT) void embed_tied_kernel(EmbedArgs a, int blocks_t, int bits) {
   using E = Elem<TY>;
   using Bits = typename std::conditional<E::kBytes == 4, uint32_t, uint16_t>::type;
-  constexpr int kLd = kTiedK + 4 / E::kBytes;  // rows of words an odd number apart
+  constexpr int kLd = ROWS + 4 / E::kBytes;  // rows of words an odd number apart
   __shared__ uint32_t seen[16 * 65], sums[16];
   __shared__ uint32_t order[kTiedT];
   __shared__ __attribute__((aligned(16))) Bits tile[kTiedT * kLd];
   const int lane = threadIdx.x & 63, w = wave_id();
   const int logical = xcd_remap(blockIdx.x, gridDim.x);
-  const int64_t t0 = (int64_t)(logical % blocks_t) * kTiedT, k0 = (int64_t)(logical / blocks_t) * kTiedK;
+  const int64_t t0 = (int64_t)(logical % blocks_t) * kTiedT, k0 = (int64_t)(logical / blocks_t) * ROWS;
   constexpr uint32_t kNone = 0xfffffffeu, kOutside = 0xffffffffu;  // masked or behind the last one; no such token
   auto token = [&](int i) -> uint32_t {
     const int64_t t = t0 + i;
@@ -194,15 +208,15 @@ __global__ __launch_bounds__(kTiedT) void embed_tied_kernel(EmbedArgs a, int blo
   }
   const uint32_t v = token(p);
   const char* from = a.table + (k0 * a.V + (v < kNone ? v : 0)) * E::kBytes;
-  const int rows = (int)min((int64_t)kTiedK, a.d - k0);
+  const int rows = (int)min((int64_t)ROWS, a.d - k0);
 #pragma unroll
-  for (int i = 0; i < kTiedK; ++i) {
+  for (int i = 0; i < ROWS; ++i) {
     float x = v == kNone ? 0.f : __uint_as_float(0x7fc00000u);
     if (v < kNone && i < rows) x = E::get1(from + i * a.V * E::kBytes) * a.scale;
     E::put1(reinterpret_cast<char*>(&tile[p * kLd + i]), x);
   }
   __syncthreads();
-  constexpr int kPer = kTiedK / 8;  // pieces of a token's run
+  constexpr int kPer = ROWS / 8;  // pieces of a token's run
   for (int i = threadIdx.x; i < kTiedT * kPer; i += kTiedT) {
     const int row = i / kPer, c = 8 * (i % kPer);
     if (t0 + row >= a.T || c >= rows) continue;
@@ -249,9 +263,17 @@ hipError_t launch_embed(const EmbedArgs& a, hipStream_t st) {
   pick_type(a.type, [&](auto ty) {
     constexpr int TY = decltype(ty)::value;
     if (a.tied && a.T > kTiedFew) {
-      const int64_t bt = (a.T + kTiedT - 1) / kTiedT, bk = (a.d + kTiedK - 1) / kTiedK;
+      const int64_t bt = (a.T + kTiedT - 1) / kTiedT;
       const int bits = bits_of(a.V / (128 / Elem<TY>::kBytes));
-      hipLaunchKernelGGL((embed_tied_kernel<TY>), dim3((unsigned)(bt * bk)), dim3(kTiedT), 0, st, a, (int)bt, bits);
+      auto with = [&](auto rows) {
+        constexpr int ROWS = decltype(rows)::value;
+        const dim3 grid((unsigned)(bt * ((a.d + ROWS - 1) / ROWS)));
+        hipLaunchKernelGGL((embed_tied_kernel<TY, ROWS>), grid, dim3(kTiedT), 0, st, a, (int)bt, bits);
+      };
+      // Longer runs where there are workgroups enough.  us, 32 / 16 rows, cold caches, d 2048: T 16384, V 32000 116 /
+      // 128, T 3001 46 / 48, T 700 (64 / 128 workgroups) 36 / 25.
+      if (bt * ((a.d + 31) / 32) >= 128) with(std::integral_constant<int, 32>());
+      else with(std::integral_constant<int, 16>());
       return;
     }
     if (a.tied) {
@@ -293,6 +315,10 @@ __global__ __launch_bounds__(1024) void sort_chunk_kernel(SortArgs a, int bits, 
     a.key[to_result ? 0 : 1][i] = k;
     a.pos[to_result ? 0 : 1][i] = p;
   }
+  clear_runs(a);
+  if (!to_result) return;
+  __syncthreads();  // the only workgroup
+  if (i < a.T && k < (uint32_t)a.V && (i == 0 || keys[i - 1] != k)) a.run_of[k] = (int32_t)i;
 }
 
 // 64 entries of one chunk a workgroup, every chunk's keys in LDS; each of the
@@ -342,6 +368,7 @@ __global__ __launch_bounds__(256) void sort_rank_kernel(SortArgs a) {
   for (int j = 0; j < 4; ++j) place += places[j][lane];
   a.key[0][place] = k;
   a.pos[0][place] = a.pos[1][i];
+  if (k < (uint32_t)a.V) a.run_of[k] = (int32_t)place;
 }
 
 // More tokens: per pass of 9 bits the workgroups' counts of every digit, their
@@ -365,6 +392,7 @@ __device__ inline void sort_item(const SortArgs& a, int pass, int64_t i, uint32_
 __global__ __launch_bounds__(1024) void sort_count_kernel(SortArgs a, int pass) {
   __shared__ uint32_t n[kSortDigits];
   for (int i = threadIdx.x; i < kSortDigits; i += 1024) n[i] = 0;
+  if (pass == 0) clear_runs(a);
   __syncthreads();
   for (int r = 0; r < kSortRounds; ++r) {
     const int64_t i = (int64_t)blockIdx.x * kSortItems + r * 1024 + threadIdx.x;
@@ -398,7 +426,7 @@ __global__ __launch_bounds__(1024) void sort_scan_kernel(uint32_t* count, int64_
   }
 }
 
-__global__ __launch_bounds__(1024) void sort_scatter_kernel(SortArgs a, int pass) {
+__global__ __launch_bounds__(1024) void sort_scatter_kernel(SortArgs a, int pass, int last) {
   __shared__ uint32_t seen[kSortDigits * 16];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, shift = pass * kDigitBits;
   for (int i = threadIdx.x; i < kSortDigits * 16; i += 1024) seen[i] = 0;
@@ -432,6 +460,7 @@ __global__ __launch_bounds__(1024) void sort_scatter_kernel(SortArgs a, int pass
     const uint32_t to = seen[((k[r] >> shift) & (kSortDigits - 1)) * 16 + w] + at[r];
     a.key[pass & 1][to] = k[r];
     a.pos[pass & 1][to] = p[r];
+    if (last && k[r] < (uint32_t)a.V) a.run_of[k[r]] = (int32_t)to;
   }
 }
 
@@ -455,44 +484,51 @@ hipError_t launch_sort_scan(const SortArgs& a, int, hipStream_t st) {
   return hipGetLastError();
 }
 hipError_t launch_sort_scatter(const SortArgs& a, int pass, hipStream_t st) {
-  hipLaunchKernelGGL(sort_scatter_kernel, dim3((unsigned)((a.T + kSortItems - 1) / kSortItems)), dim3(1024), 0, st, a, pass);
+  hipLaunchKernelGGL(sort_scatter_kernel, dim3((unsigned)((a.T + kSortItems - 1) / kSortItems)), dim3(1024), 0, st, a, pass,
+                     pass + 1 == sort_passes(a.V));
   return hipGetLastError();
 }
 
 // ------------------------------------------------------------------ gradient
 namespace {
 
-// f with the gradient's type as a constant
-template <class F>
-__device__ inline void with_type(int type, F&& f) {
-  if (type == kTypeF32) f(std::integral_constant<int, kTypeF32>());
-  else if (type == kTypeBf16) f(std::integral_constant<int, kTypeBf16>());
-  else f(std::integral_constant<int, kTypeF16>());
-}
+// Where a run's sum goes: to a row of sums (tied weights), to the table's
+// gradient, or on top of it.  (Constants of the kernels: with the choice made
+// where the sum is stored, the kernel's code was so long that fetching it took
+// a small call 10 us.)
+enum { kToSums, kToTable, kOnTable };
 
 // Piece p of the slab of columns from the sum x of the run of token v that
-// begins at entry `first`: to the table, or for tied weights to the run's row
-// of sums.
+// begins at entry `first`.
+template <int SINK, int G>
 __device__ inline void put_sum(const EmbedGradArgs& a, int64_t v, int64_t first, int p, const float (&x)[8]) {
   const int64_t n = a.cols - 8 * (int64_t)p;
   if (n <= 0) return;
   float y[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) y[i] = x[i] * a.scale;
-  if (a.tied) {
+  if constexpr (SINK == kToSums) {
     store8<kTypeF32>(reinterpret_cast<char*>(a.sums + first * a.cols + 8 * (int64_t)p), y, (int)n);
-    return;
-  }
-  with_type(a.grad_type, [&](auto ty) {
-    constexpr int G = decltype(ty)::value;
+  } else {
     char* row = a.out + v * a.d * Elem<G>::kBytes;
-    if (a.accumulate) {
+    if constexpr (SINK == kOnTable) {
       float was[8];
       load_row<G>(row, a.d, p, was);
 #pragma unroll
       for (int i = 0; i < 8; ++i) y[i] += was[i];
     }
     store8<G>(row + 8 * (int64_t)p * Elem<G>::kBytes, y, (int)n);
+  }
+}
+
+// launch(type, sink, gradient's type) as constants
+template <class F>
+void pick_sink(const EmbedGradArgs& a, F&& launch) {
+  using std::integral_constant;
+  if (a.tied) return launch(integral_constant<int, kToSums>(), integral_constant<int, kTypeF32>());
+  pick_type(a.grad_type, [&](auto g) {
+    if (a.accumulate) launch(integral_constant<int, kOnTable>(), g);
+    else launch(integral_constant<int, kToTable>(), g);
   });
 }
 
@@ -504,18 +540,6 @@ __device__ inline void put_part(const EmbedGradArgs& a, int64_t piece, int which
   if (n > 0) store8<kTypeF32>(reinterpret_cast<char*>(part_row(a, piece, which) + 8 * (int64_t)p), x, (int)n);
 }
 
-// the first entry whose key is at least v
-__device__ inline int64_t lower_bound(const uint32_t* key, int64_t n, uint32_t v) {
-  int64_t lo = 0, hi = n;
-  while (lo < hi) {
-    const int64_t mid = (lo + hi) >> 1;
-    if (key[mid] < v) lo = mid + 1; else hi = mid;
-  }
-  return lo;
-}
-
-constexpr int kFillRows = 16;  // table rows of a wave that writes zeros
-
 __device__ inline uint32_t lane_of(uint32_t v, int lane) {
   return (uint32_t)__builtin_amdgcn_readlane((int)v, lane);
 }
@@ -523,31 +547,23 @@ __device__ inline uint32_t lane_of(uint32_t v, int lane) {
 }  // namespace
 
 // Waves [0, pieces * slabs) add up, the waves behind them write zeros to the
-// table's rows whose tokens do not occur (tied: clear the places of the runs).
-template <int TY>
-__global__ __launch_bounds__(256) void embed_grad_kernel(EmbedGradArgs a, int64_t pieces, int slabs) {
+// table's rows whose tokens do not occur, `fill` rows each.
+template <int TY, int SINK, int G>
+__global__ __launch_bounds__(256) void embed_grad_kernel(EmbedGradArgs a, int64_t pieces, int slabs, int fill) {
   const int lane = threadIdx.x & 63;
   const int64_t wave = wave_in_grid();
   if (wave >= pieces * slabs) {
-    if (a.tied) {
-      const int64_t v = (wave - pieces * slabs) * 256 + 4 * lane;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (v + i < a.V) a.run_of[v + i] = -1;
-      return;
-    }
-    if (a.accumulate) return;
-    const int64_t v0 = (wave - pieces * slabs) * kFillRows, v = v0 + lane;
-    bool empty = false;
-    if (lane < kFillRows && v < a.V) {
-      const int64_t i = lower_bound(a.key, a.T, (uint32_t)v);
-      empty = i >= a.T || a.key[i] != (uint32_t)v;
-    }
-    const int64_t bytes = a.d * (a.grad_type == kTypeF32 ? 4 : 2);
-    for (uint64_t m = __ballot(empty); m; m &= m - 1) {
-      char* row = a.out + (v0 + __builtin_ctzll(m)) * bytes;
-      int64_t at = 16 * lane;
-      for (; at + 16 <= bytes; at += 1024) store16(row + at, zero4());
+    if constexpr (SINK != kToTable) return;
+    const int64_t v0 = (wave - pieces * slabs) * fill, v = v0 + lane;
+    const uint64_t rows = __ballot(lane < fill && v < a.V && a.run_of[min(v, a.V - 1)] < 0);
+    const int64_t bytes = a.d * Elem<G>::kBytes;
+    int per = 64;  // lanes of a row: as many as its 16-byte pieces, to a power of two
+    while (per > 1 && 8 * per >= bytes) per >>= 1;
+    for (int r = lane / per; r < fill; r += 64 / per) {
+      if (!(rows >> r & 1)) continue;
+      char* row = a.out + (v0 + r) * bytes;
+      int64_t at = 16 * (lane % per);
+      for (; at + 16 <= bytes; at += 16 * per) store16(row + at, zero4());
       if (at < bytes)
         for (; at < bytes; at += 2) *reinterpret_cast<uint16_t*>(row + at) = 0;
     }
@@ -566,7 +582,7 @@ __global__ __launch_bounds__(256) void embed_grad_kernel(EmbedGradArgs a, int64_
   uint32_t v = lane_of(keys, 0);
   bool first = before == v;  // the run began in the piece before
   int from = 0;              // where it begins in this one
-  constexpr int U = 4;
+  constexpr int U = 8;
   for (int e = 0; e < ne; e += U) {
     Raw8<TY> r[U];
 #pragma unroll
@@ -574,7 +590,7 @@ __global__ __launch_bounds__(256) void embed_grad_kernel(EmbedGradArgs a, int64_
       const int i = min(e + u, ne - 1);
       const int64_t t = lane_of(poss, i);
       r[u] = load8<TY>(a.grad + (t * a.d + a.col0 + 8 * (int64_t)p) * Elem<TY>::kBytes,
-                       lane_of(keys, i) < (uint32_t)a.V ? (int)(a.cols - 8 * (int64_t)p) : 0);
+                       lane_of(keys, i) < (uint32_t)a.V ? (int)(a.cols - 8 * (int64_t)p) : 0, p > 0);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -582,7 +598,7 @@ __global__ __launch_bounds__(256) void embed_grad_kernel(EmbedGradArgs a, int64_
       const uint32_t k = lane_of(keys, e + u);
       if (k != v) {
         if (first) put_part(a, piece, 0, p, x);
-        else put_sum(a, v, e0 + from, p, x);
+        else put_sum<SINK, G>(a, v, e0 + from, p, x);
         first = false;
         v = k;
         from = e + u;
@@ -591,6 +607,7 @@ __global__ __launch_bounds__(256) void embed_grad_kernel(EmbedGradArgs a, int64_
       }
       if (v >= (uint32_t)a.V) return;  // only entries that count for nothing from here on
       float y[8];
+      settle8<TY>(r[u], (int)(a.cols - 8 * (int64_t)p), p > 0);
       unpack8<TY>(r[u], y);
 #pragma unroll
       for (int i = 0; i < 8; ++i) x[i] += y[i];
@@ -598,12 +615,13 @@ __global__ __launch_bounds__(256) void embed_grad_kernel(EmbedGradArgs a, int64_
   }
   if (first) put_part(a, piece, 0, p, x);
   else if (after == v) put_part(a, piece, 1, p, x);
-  else put_sum(a, v, e0 + from, p, x);
+  else put_sum<SINK, G>(a, v, e0 + from, p, x);
 }
 
 // A workgroup for each piece in which a run begins that goes on, and each
 // slab: its partial rows in order, a quarter of them to each wave.  Behind
 // those, workgroups that note for tied weights where each token's run begins.
+template <int SINK, int G>
 __global__ __launch_bounds__(256) void embed_join_kernel(EmbedGradArgs a, int64_t pieces, int slabs, int64_t joins) {
   __shared__ float sums[3][64 * 8];
   if (blockIdx.x >= joins) {
@@ -636,11 +654,12 @@ __global__ __launch_bounds__(256) void embed_join_kernel(EmbedGradArgs a, int64_
     for (int u = 0; u < U; ++u) {
       const int64_t q = piece + min(j + u, n - 1);
       r[u] = load8<kTypeF32>(reinterpret_cast<const char*>(part_row(a, q, q == piece ? 1 : 0) + 8 * (int64_t)p),
-                             j + u < end ? (int)(a.cols - 8 * (int64_t)p) : 0);
+                             j + u < end ? (int)(a.cols - 8 * (int64_t)p) : 0, p > 0);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       float y[8];
+      settle8<kTypeF32>(r[u], (int)(a.cols - 8 * (int64_t)p), p > 0);
       unpack8<kTypeF32>(r[u], y);
 #pragma unroll
       for (int i = 0; i < 8; ++i) x[i] += y[i];
@@ -655,7 +674,17 @@ __global__ __launch_bounds__(256) void embed_join_kernel(EmbedGradArgs a, int64_
   for (int k = 0; k < 3; ++k)
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] += sums[k][i * 64 + lane];
-  put_sum(a, v, a.tied ? e0 + lower_bound(a.key + e0, a.piece, v) : 0, p, x);
+  int64_t first = e0;
+  if constexpr (SINK == kToSums)
+    if (begin != v) {  // the run's first entry in the piece
+      int lo = 0, hi = a.piece - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (a.key[e0 + mid] < v) lo = mid + 1; else hi = mid;
+      }
+      first += lo;
+    }
+  put_sum<SINK, G>(a, v, first, p, x);
 }
 
 // Tied weights: 256 columns x kTurnK rows of the head's gradient a workgroup,
@@ -741,6 +770,7 @@ __global__ __launch_bounds__(256) void fill_table_kernel(char* p, int64_t bytes)
   if (tail < bytes) *reinterpret_cast<uint16_t*>(p + tail) = 0;
 }
 
+// Entries of a piece (up to as many tokens need no joining).
 int embed_piece(int64_t T) { return T <= 16384 ? 16 : 64; }
 
 namespace {
@@ -755,18 +785,26 @@ GradShape grad_shape(const EmbedGradArgs& a) {
 
 hipError_t launch_embed_grad(const EmbedGradArgs& a, hipStream_t st) {
   const GradShape s = grad_shape(a);
-  const int64_t fill = a.tied ? (a.V + 255) / 256 : a.accumulate ? 0 : (a.V + kFillRows - 1) / kFillRows;
-  const dim3 grid((unsigned)((s.pieces * s.slabs + fill + 3) / 4));
+  // table rows of a wave that writes zeros: about one round of the chip's waves
+  const int fill = (int)std::min<int64_t>(std::max<int64_t>(a.V / 8192, 1), 16);
+  const int64_t more = a.tied || a.accumulate ? 0 : (a.V + fill - 1) / fill;
+  const dim3 grid((unsigned)((s.pieces * s.slabs + more + 3) / 4));
   pick_type(a.type, [&](auto ty) {
-    hipLaunchKernelGGL((embed_grad_kernel<decltype(ty)::value>), grid, dim3(256), 0, st, a, s.pieces, s.slabs);
+    pick_sink(a, [&](auto sink, auto g) {
+      hipLaunchKernelGGL((embed_grad_kernel<decltype(ty)::value, decltype(sink)::value, decltype(g)::value>), grid,
+                         dim3(256), 0, st, a, s.pieces, s.slabs, fill);
+    });
   });
   return hipGetLastError();
 }
 hipError_t launch_embed_join(const EmbedGradArgs& a, hipStream_t st) {
   const GradShape s = grad_shape(a);
-  const int64_t joins = (s.pieces - 1) * s.slabs, notes = a.tied ? (a.T + 255) / 256 : 0;
+  const int64_t joins = (s.pieces - 1) * s.slabs, notes = a.tied && a.T > kSortChunk ? (a.T + 255) / 256 : 0;
   if (joins + notes == 0) return hipSuccess;
-  hipLaunchKernelGGL(embed_join_kernel, dim3((unsigned)(joins + notes)), dim3(256), 0, st, a, s.pieces, s.slabs, joins);
+  pick_sink(a, [&](auto sink, auto g) {
+    hipLaunchKernelGGL((embed_join_kernel<decltype(sink)::value, decltype(g)::value>), dim3((unsigned)(joins + notes)),
+                       dim3(256), 0, st, a, s.pieces, s.slabs, joins);
+  });
   return hipGetLastError();
 }
 hipError_t launch_embed_turn(const EmbedGradArgs& a, hipStream_t st) {

@@ -30,6 +30,7 @@ struct SortArgs {
   uint32_t* key[2];  // [T] each
   uint32_t* pos[2];
   uint32_t* count;   // [kSortDigits x workgroups], T > kSortSmall only
+  int32_t* run_of;   // [V]: an entry of each token, or -1
 };
 constexpr int kSortDigits = 512;
 // where the result lies: key[i], pos[i] of the returned index
@@ -52,9 +53,8 @@ struct EmbedGradArgs {
   char* out;    // the table's gradient
   float* part;  // [pieces][2][cols]: what a piece holds of a token that it shares with the piece before, or after
   int piece;    // entries of a piece
-  // tied only
-  float* sums;      // [T][cols]: the sum of the run that begins at an entry
-  int32_t* run_of;  // [V]: the entry at which the token's run begins, or -1
+  int32_t* run_of;  // [V]: an entry of each token, or -1; for tied weights its first one, from launch_embed_join on
+  float* sums;      // tied only, [T][cols]: the sum of the run that begins at an entry
 };
 int embed_piece(int64_t T);
 hipError_t launch_embed_grad(const EmbedGradArgs& a, hipStream_t st);

@@ -94,10 +94,8 @@ EmbedPlan plan_embed(int64_t T, int64_t V, int64_t d, bool tied) {
   }
   if (T > kd::kSortSmall) p.count = cv.take((size_t)cdiv(T, kd::kSortItems) * kd::kSortDigits * 4);
   p.part = cv.take((size_t)cdiv(T, kd::embed_piece(T)) * 2 * p.cols * 4);
-  if (tied) {
-    p.sums = cv.take((size_t)T * p.cols * 4);
-    p.run_of = cv.take((size_t)V * 4);
-  }
+  p.run_of = cv.take((size_t)V * 4);
+  if (tied) p.sums = cv.take((size_t)T * p.cols * 4);
   p.total = cv.off;
   return p;
 }
@@ -203,6 +201,7 @@ kd_status kd_embedding_bwd(const void* grad, const int32_t* tokens, const uint8_
     s.pos[i] = at<uint32_t>(workspace, p.pos[i]);
   }
   s.count = at<uint32_t>(workspace, p.count);
+  s.run_of = at<int32_t>(workspace, p.run_of);
   if (T <= kd::kSortSmall) {
     KD_LAUNCH("embedding_sort", st, kd::launch_sort_small(s, st));
   } else {
@@ -229,7 +228,7 @@ kd_status kd_embedding_bwd(const void* grad, const int32_t* tokens, const uint8_
   a.part = at<float>(workspace, p.part);
   a.piece = kd::embed_piece(T);
   a.sums = at<float>(workspace, p.sums);
-  a.run_of = at<int32_t>(workspace, p.run_of);
+  a.run_of = s.run_of;
   for (a.col0 = 0; a.col0 < d; a.col0 += p.cols) {
     a.cols = std::min(p.cols, d - a.col0);
     KD_LAUNCH("embedding_grad", st, kd::launch_embed_grad(a, st));

@@ -99,13 +99,16 @@ __global__ __launch_bounds__(RowTeam<R>::kThreads, K == 1 ? 8 : 4) void norm_fwd
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int64_t at = 8 * (int64_t)(lane + k * R);
-      to[k] = load8<TY>(a.x + (row * a.d + at) * Elem<TY>::kBytes, there ? (int)(a.d - at) : 0);
+      to[k] = load8<TY>(a.x + (row * a.d + at) * Elem<TY>::kBytes, there ? (int)(a.d - at) : 0, at > 0);
     }
   };
   load(next, t);
   for (; t < a.T; t += step) {
 #pragma unroll
-    for (int k = 0; k < K; ++k) r[k] = next[k];
+    for (int k = 0; k < K; ++k) {
+      r[k] = next[k];
+      settle8<TY>(r[k], (int)(a.d - 8 * (int64_t)(lane + k * R)), lane + k * R > 0);
+    }
     load(next, t + step);
     if (!row_valid(a.mask, t)) {
       if (lane == 0) {
@@ -265,12 +268,17 @@ __device__ inline Input<TY, KIND> load_input(const NormGradArgs& a, int64_t t, i
   Input<TY, KIND> r;
   const int64_t at = t * a.d + 8 * (int64_t)p;
   if constexpr (KIND == kRowsNone) {
-    r.x = load8<TY>(a.x + at * Elem<TY>::kBytes, n);
+    r.x = load8<TY>(a.x + at * Elem<TY>::kBytes, n, p > 0);
   } else {
-    r.q = load_q8(a.q + at, n);
+    r.q = load_q8(a.q + at, n, p > 0);
     r.scale = n > 0 ? a.scale[t * a.groups + (a.groups == 1 ? 0 : 8 * p / a.group)] : 0.f;
   }
   return r;
+}
+template <int TY, int KIND>
+__device__ inline void settle_input(Input<TY, KIND>& r, int p, int n) {
+  if constexpr (KIND == kRowsNone) settle8<TY>(r.x, n, p > 0);
+  else settle_q8(r.q, n, p > 0);
 }
 template <int TY, int KIND>
 __device__ inline void input_values(const Input<TY, KIND>& r, float (&x)[8]) {
@@ -314,7 +322,7 @@ __global__ __launch_bounds__(RowTeam<R>::kThreads, 4) void norm_grad_kernel(Norm
       const int p = lane + k * R;
       const int n = there ? (int)(a.d - 8 * (int64_t)p) : 0;
       xn[k] = load_input<TY, KIND>(a, row, p, n);
-      gn[k] = load8<TY>(a.grad + (row * a.d + 8 * (int64_t)p) * Elem<TY>::kBytes, n);
+      gn[k] = load8<TY>(a.grad + (row * a.d + 8 * (int64_t)p) * Elem<TY>::kBytes, n, p > 0);
     }
   };
   load(t);
@@ -323,8 +331,11 @@ __global__ __launch_bounds__(RowTeam<R>::kThreads, 4) void norm_grad_kernel(Norm
     const float m = mean, r = rstd;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
+      const int p = lane + k * R, n = (int)(a.d - 8 * (int64_t)p);
       xr[k] = xn[k];
       gr[k] = gn[k];
+      settle_input<TY, KIND>(xr[k], p, n);
+      settle8<TY>(gr[k], n, p > 0);
     }
     load(t + step);  // the next row, while this one is worked on
     // a piece's h and g from what lies in registers as it was loaded
@@ -419,7 +430,9 @@ __global__ __launch_bounds__(1024) void norm_grad_long_kernel(NormGradArgs a) {
     const float mean = a.mean[t], rstd = a.rstd[t];
     auto piece = [&](int p, float (&h)[8], float (&g)[8], float (&w)[8]) {
       const int64_t n = a.d - 8 * (int64_t)p;
-      input_values<TY, KIND>(load_input<TY, KIND>(a, t, p, (int)n), h);
+      auto in = load_input<TY, KIND>(a, t, p, (int)n);
+      settle_input<TY, KIND>(in, p, (int)n);
+      input_values<TY, KIND>(in, h);
       load_row<TY>(a.grad + t * a.d * Elem<TY>::kBytes, a.d, p, g);
       if (a.w) load_any(a.w, a.wtype, a.d, p, w);
 #pragma unroll

@@ -74,7 +74,10 @@ struct RowTeam {
 
 template <int TY>
 __device__ inline void load_row(const char* row, int64_t d, int p, float (&x)[8]) {
-  unpack8<TY>(load8<TY>(row + (int64_t)p * 8 * Elem<TY>::kBytes, (int)(d - 8 * (int64_t)p)), x);
+  const int n = (int)(d - 8 * (int64_t)p);
+  Raw8<TY> r = load8<TY>(row + (int64_t)p * 8 * Elem<TY>::kBytes, n, p > 0);
+  settle8<TY>(r, n, p > 0);
+  unpack8<TY>(r, x);
 }
 
 // 8 values of a vector whose type is known at run time

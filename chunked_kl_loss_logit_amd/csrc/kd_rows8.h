@@ -164,17 +164,22 @@ __device__ inline uint32_t top8(const float (&x)[8]) {
   return t;
 }
 
-// 8 bytes at any address, n of them
-__device__ inline uint2 load_q8(const char* p, int n) {
+// 8 bytes at any address, n of them (as load8 and settle8)
+__device__ inline uint2 load_q8(const char* p, int n, bool inner) {
   uint2 w{0u, 0u};
-  if (n >= 8) {
-    __builtin_memcpy(&w, p, 8);
-    return w;
-  }
+  if (n >= 8 || (n > 0 && inner)) {
+    __builtin_memcpy(&w, n >= 8 ? p : p - (8 - n), 8);
+  } else {
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (i < n) (i < 4 ? w.x : w.y) |= (uint32_t)(uint8_t)p[i] << (8 * (i & 3));
+    for (int i = 0; i < 8; ++i)
+      if (i < n) (i < 4 ? w.x : w.y) |= (uint32_t)(uint8_t)p[i] << (8 * (i & 3));
+  }
   return w;
+}
+__device__ inline void settle_q8(uint2& w, int n, bool inner) {
+  if (n >= 8 || n <= 0 || !inner) return;
+  const uint64_t v = ((uint64_t)w.y << 32 | w.x) >> (8 * (8 - n));
+  w = uint2{(uint32_t)v, (uint32_t)(v >> 32)};
 }
 __device__ inline void store_q8(char* p, uint2 w, int n) {
   if (n >= 8) {

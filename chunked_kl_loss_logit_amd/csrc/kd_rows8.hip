@@ -102,7 +102,9 @@ __global__ __launch_bounds__(kRowsThreads) void dequantize_kernel(RowsArgs a, in
   char* const out = const_cast<char*>(a.x);
   for (int64_t t = (int64_t)(blockIdx.x / slabs) * rows + (threadIdx.x >> shift); t < a.T; t += step) {
     float x[8];
-    values8<KIND>(load_q8(a.q + t * a.d + 8 * (int64_t)p, n), x);
+    uint2 q = load_q8(a.q + t * a.d + 8 * (int64_t)p, n, p > 0);
+    settle_q8(q, n, p > 0);
+    values8<KIND>(q, x);
     const float s = a.scale[t * a.groups + (a.groups == 1 ? 0 : 8 * p / a.group)];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {

@@ -38,18 +38,21 @@ def embedding_forward(tokens, table, mask=None, scale=1.0, tied=False):
 def embedding_backward(grad, tokens, V, mask=None, scale=1.0, tied=False, grad_dtype=None, out=None, workspace=None):
     """The table's gradient [V,d] (or [d,V] if tied) of grad_dtype (None: grad's).  out: a tensor that takes it on
     top of what it holds and is returned, such as the gradient of the head that the embedding shares."""
-    T, d = B._matrix("grad", grad, None, B.TYPES)
+    T = B._tokens(tokens, mask)
+    _, d = B._matrix("grad", grad, T, B.TYPES)
+    shape = (d, V) if tied else (V, d)
     if out is None:
-        shape = (d, V) if tied else (V, d)
-        table = torch.empty(shape, dtype=grad_dtype or grad.dtype, device=grad.device)
+        dtype = grad_dtype or grad.dtype
+        if dtype not in B.TYPES:
+            raise TypeError(f"grad_dtype must be one of {', '.join(map(str, B.TYPES))}, got {dtype}")
+        table = torch.empty(shape, dtype=dtype, device=grad.device)
     else:
-        if grad_dtype is not None and out.dtype != grad_dtype:
-            raise TypeError(f"out must be {grad_dtype}, got {out.dtype}")
+        B._need("out", out, shape, B.TYPES if grad_dtype is None else (grad_dtype,))
         B.P._writable("out", [out])
         table = out
     if workspace is None:
         workspace = _workspace(B.kd_embedding_workspace_size(T, V, d, tied), grad.device)
-    B.kd_embedding_bwd(grad, tokens, mask, scale, V, tied, out is not None, table, workspace)
+    B._embedding_bwd(T, V, d, grad, tokens, mask, scale, tied, out is not None, table, workspace)
     if out is not None:
         torch.autograd.graph.increment_version([out])
     return table

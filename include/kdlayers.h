@@ -43,8 +43,8 @@ extern "C" {
  * tokens [T] int32; out [T,d] of type dt. */
 kd_status kd_embedding_fwd(const int32_t* tokens, const void* table, const uint8_t* mask, float scale, int64_t T,
                            int64_t V, int64_t d, kd_dtype dt, int32_t tied, void* out, void* stream);
-/* Workspace bytes for kd_embedding_bwd: the sorted tokens (16 bytes a token),
- * float32 partial sums (up to d / 2 bytes a token) and, if tied, a float32 row
+/* Workspace bytes for kd_embedding_bwd: the sorted tokens (16 bytes a token), 4
+ * bytes for each of the V tokens, float32 partial sums (up to d / 2 bytes a token) and, if tied, a float32 row
  * of sums for each token (in slabs of columns of 1 GiB at most, or of 64
  * columns). */
 kd_status kd_embedding_workspace_size(int64_t T, int64_t V, int64_t d, int32_t tied, size_t* bytes);

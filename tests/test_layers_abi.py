@@ -44,7 +44,7 @@ def test_sizes(L):
     assert size(L, "kd_embedding_workspace_size", 0, 10, 8, 0) == (0, 0)
     for T, d in ((1, 8), (16384, 2048), (16385, 2048), (1 << 20, 512)):
         st, n = size(L, "kd_embedding_workspace_size", T, 32000, d, 0)
-        assert st == 0 and 8 * T <= n <= T * (17 + d // 2) + 2 * 4 * d + 1024 * 1024
+        assert st == 0 and 8 * T <= n <= T * (17 + d // 2) + 4 * 32000 + 2 * 4 * d + 1024 * 1024
         st, m = size(L, "kd_embedding_workspace_size", T, 32000, d, 1)
         assert st == 0 and min(4 * T * d, 1 << 29) <= m <= n + (1 << 30) + 1024
     assert size(L, "kd_embedding_workspace_size", -1, 10, 8, 1)[0] == 1
