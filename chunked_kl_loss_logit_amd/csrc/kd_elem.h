@@ -76,9 +76,17 @@ __device__ inline uint32_t pack2x16(float a, float b) {
 // inner: 8 elements lie before the piece in its row.  A last piece of fewer is
 // then loaded as the row's last 8 elements, and settle8 moves its own to their
 // place once it is needed: until then nothing waits for the load.
-template <int TY>
+// WHOLE: pieces exist as a whole or not at all.
+template <int TY, bool WHOLE = false>
 __device__ inline Raw8<TY> load8(const char* p, int n, bool inner) {
   Raw8<TY> r = {};
+  if constexpr (WHOLE) {
+    if (n > 0) {
+      r.v[0] = load16(p);
+      if constexpr (TY == kTypeF32) r.v[1] = load16(p + 16);
+    }
+    return r;
+  }
   if (n >= 8 || (n > 0 && inner)) {
     const char* q = n >= 8 ? p : p - (8 - n) * Elem<TY>::kBytes;
     r.v[0] = load16(q);
@@ -97,8 +105,9 @@ __device__ inline Raw8<TY> load8(const char* p, int n, bool inner) {
   }
   return r;
 }
-template <int TY>
+template <int TY, bool WHOLE = false>
 __device__ inline void settle8(Raw8<TY>& r, int n, bool inner) {
+  if constexpr (WHOLE) return;
   if (n >= 8 || n <= 0 || !inner) return;
   constexpr int W = TY == kTypeF32 ? 8 : 4;
   uint32_t w[W];
@@ -127,9 +136,9 @@ __device__ inline void unpack8(const Raw8<TY>& r, float (&x)[8]) {
   for (int i = 0; i < 8; ++i) x[i] = Elem<TY>::get(r.v[TY == kTypeF32 ? i >> 2 : 0], TY == kTypeF32 ? i & 3 : i);
 }
 // The first n of 8 values, rounded to the type.
-template <int TY>
+template <int TY, bool WHOLE = false>
 __device__ inline void store8(char* p, const float (&x)[8], int n) {
-  if (n >= 8) {
+  if (WHOLE ? n > 0 : n >= 8) {
     if constexpr (TY == kTypeF32) {
 #pragma unroll
       for (int i = 0; i < 8; i += 4)
@@ -140,6 +149,7 @@ __device__ inline void store8(char* p, const float (&x)[8], int n) {
     }
     return;
   }
+  if constexpr (WHOLE) return;
 #pragma unroll
   for (int i = 0; i < 8; ++i)
     if (i < n) Elem<TY>::put1(p + i * Elem<TY>::kBytes, x[i]);

@@ -72,6 +72,8 @@ struct RowTeam {
   }
 };
 
+__device__ inline bool row_valid(const uint8_t* mask, int64_t t) { return !mask || mask[t]; }
+
 template <int TY>
 __device__ inline void load_row(const char* row, int64_t d, int p, float (&x)[8]) {
   const int n = (int)(d - 8 * (int64_t)p);

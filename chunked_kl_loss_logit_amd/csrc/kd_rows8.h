@@ -165,8 +165,13 @@ __device__ inline uint32_t top8(const float (&x)[8]) {
 }
 
 // 8 bytes at any address, n of them (as load8 and settle8)
+template <bool WHOLE = false>
 __device__ inline uint2 load_q8(const char* p, int n, bool inner) {
   uint2 w{0u, 0u};
+  if constexpr (WHOLE) {
+    if (n > 0) __builtin_memcpy(&w, p, 8);
+    return w;
+  }
   if (n >= 8 || (n > 0 && inner)) {
     __builtin_memcpy(&w, n >= 8 ? p : p - (8 - n), 8);
   } else {
@@ -176,16 +181,20 @@ __device__ inline uint2 load_q8(const char* p, int n, bool inner) {
   }
   return w;
 }
+template <bool WHOLE = false>
 __device__ inline void settle_q8(uint2& w, int n, bool inner) {
+  if constexpr (WHOLE) return;
   if (n >= 8 || n <= 0 || !inner) return;
   const uint64_t v = ((uint64_t)w.y << 32 | w.x) >> (8 * (8 - n));
   w = uint2{(uint32_t)v, (uint32_t)(v >> 32)};
 }
+template <bool WHOLE = false>
 __device__ inline void store_q8(char* p, uint2 w, int n) {
-  if (n >= 8) {
+  if (WHOLE ? n > 0 : n >= 8) {
     __builtin_memcpy(p, &w, 8);
     return;
   }
+  if constexpr (WHOLE) return;
 #pragma unroll
   for (int i = 0; i < 8; ++i)
     if (i < n) p[i] = (char)((i < 4 ? w.x : w.y) >> (8 * (i & 3)));
