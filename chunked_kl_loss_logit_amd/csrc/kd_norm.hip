@@ -254,7 +254,7 @@ hipError_t launch_norm_fwd(const NormArgs& a, hipStream_t st) {
         else hipLaunchKernelGGL((norm_fwd_kernel<TY, KIND, false, R, K>), grid, block, 0, st, a);
       };
       // by the width alone, so that a row's bits do not hang on how many rows there are
-      const bool held = pick_shape<Shape<64, 1>, Shape<256, 1>, Shape<512, 1>, Shape<1024, 1>, Shape<1024, 2>>(
+      const bool held = pick_shape<Shape<16, 1>, Shape<64, 1>, Shape<256, 1>, Shape<512, 1>, Shape<1024, 1>, Shape<1024, 2>>(
           a.d, launch);
       if (!held)
         hipLaunchKernelGGL((norm_fwd_long_kernel<TY>), dim3((unsigned)std::min<int64_t>(a.T, 512)), dim3(1024), 0, st, a);

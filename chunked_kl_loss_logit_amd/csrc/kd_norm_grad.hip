@@ -278,7 +278,7 @@ __global__ __launch_bounds__(1024) void norm_sum_kernel(NormGradArgs a) {
 
 // ------------------------------------------------------------------ launches
 int norm_grad_blocks(int64_t T, int64_t d) {
-  const int64_t rows = d <= 512 ? 4 : 1;  // of a workgroup
+  const int64_t rows = d <= 128 ? 16 : d <= 512 ? 4 : 1;  // of a workgroup
   return (int)std::min<int64_t>(std::max<int64_t>((T + rows - 1) / rows, 1), d <= kRowMost ? 512 : 256);
 }
 
@@ -288,7 +288,7 @@ hipError_t launch_norm_grad(const NormGradArgs& a, hipStream_t st) {
     constexpr int TY = decltype(ty)::value;
     auto with = [&](auto kind) {
       constexpr int KIND = decltype(kind)::value;
-      const bool held = pick_shape<Shape<64, 1>, Shape<256, 1>, Shape<512, 1>, Shape<1024, 1>, Shape<1024, 2>>(
+      const bool held = pick_shape<Shape<16, 1>, Shape<64, 1>, Shape<256, 1>, Shape<512, 1>, Shape<1024, 1>, Shape<1024, 2>>(
           a.d, [&](auto r, auto k) {
         constexpr int R = decltype(r)::value, K = decltype(k)::value;
         const dim3 block(RowTeam<R>::kThreads);

@@ -1,6 +1,7 @@
 // One row in the registers of R threads: thread i holds the pieces of 8
-// elements i, i + R, .., i + (K - 1) R.  R = 64 is a wave of its own, so that
-// a workgroup of 256 holds four rows; otherwise the workgroup is the row's.
+// elements i, i + R, .., i + (K - 1) R.  R = 16 is a quarter of a wave and R =
+// 64 a wave, so that a workgroup of 256 holds 16 rows or four; otherwise the
+// workgroup is the row's.
 #pragma once
 
 #include <type_traits>
@@ -32,7 +33,7 @@ inline bool pick_shape(int64_t d, F&& launch) {
 
 template <int R>
 struct RowTeam {
-  static constexpr int kThreads = R < 256 ? 256 : R;  // a wave that has a row of its own, or the row's workgroup
+  static constexpr int kThreads = R < 256 ? 256 : R;
   static constexpr int kRows = kThreads / R;  // rows of a workgroup
   static constexpr int kWaves = R / 64;
   __device__ static inline int lane() { return threadIdx.x % R; }
@@ -43,7 +44,10 @@ struct RowTeam {
   template <int N>
   __device__ static inline void sum(float (&v)[N], float* lds) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
+    for (int i = 0; i < N; ++i) {
+      if constexpr (R == 16) v[i] = add_lane<8>(add_lane<4>(add_lane<2>(add_lane<1>(v[i]))));
+      else v[i] = wave_sum(v[i]);
+    }
     if constexpr (R > 64) {
       const int w = threadIdx.x >> 6;
       __syncthreads();
@@ -60,7 +64,7 @@ struct RowTeam {
     }
   }
   __device__ static inline uint32_t most(uint32_t v, uint32_t* lds) {
-    v = wave_max(v);
+    v = wave_max(v, R);
     if constexpr (R > 64) {
       __syncthreads();
       if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;

@@ -136,7 +136,7 @@ hipError_t launch_rows_quantize(const RowsArgs& a, hipStream_t st) {
     constexpr int TY = decltype(ty)::value, KIND = decltype(kind)::value;
     // a group that is the row, unless a wave's lanes hold it
     if (a.groups == 1) {
-      const bool held = pick_shape<Shape<64, 1>, Shape<64, 2>, Shape<64, 4>, Shape<256, 2>, Shape<256, 4>, Shape<1024, 2>>(
+      const bool held = pick_shape<Shape<16, 1>, Shape<64, 1>, Shape<256, 1>, Shape<512, 1>, Shape<1024, 1>, Shape<1024, 2>>(
           a.d, [&](auto r, auto k) {
         constexpr int R = decltype(r)::value, K = decltype(k)::value;
         const int64_t rows = (a.T + RowTeam<R>::kRows - 1) / RowTeam<R>::kRows;
