@@ -129,12 +129,10 @@ __device__ inline uint32_t key_of(const SortArgs& a, int64_t i) {
   return v < 0 || v >= a.V ? (uint32_t)a.V : (uint32_t)v;
 }
 
-// The first launch of a sort clears the tokens' marks, a workgroup of 1024 its
-// share of them; the last one sets those of the tokens that occur, to some
-// entry of theirs (the first one up to kSortChunk tokens).
-__device__ inline void clear_runs(const SortArgs& a) {
-  const int64_t step = (int64_t)gridDim.x * 4096;
-  for (int64_t v = (int64_t)blockIdx.x * 4096 + 4 * threadIdx.x; v < a.V; v += step) {
+// The first launch of a sort clears the tokens' marks, workgroup b of n of 1024
+// threads its share of them.
+__device__ inline void clear_runs(const SortArgs& a, int64_t b, int64_t n) {
+  for (int64_t v = b * 4096 + 4 * threadIdx.x; v < a.V; v += n * 4096) {
     if (v + 4 <= a.V)
       *reinterpret_cast<int4*>(a.run_of + v) = int4{-1, -1, -1, -1};
     else
@@ -297,9 +295,11 @@ hipError_t launch_embed(const EmbedArgs& a, hipStream_t st) {
 // with digits of 6 bits, and then every entry's place among all chunks by
 // binary search in each of them.  (One workgroup for all of 16384 tokens took
 // 44 us, the instructions of 16 waves on one CU.)
-__global__ __launch_bounds__(1024) void sort_chunk_kernel(SortArgs a, int bits, int to_result) {
+// Workgroups behind the chunks' clear the marks.
+__global__ __launch_bounds__(1024) void sort_chunk_kernel(SortArgs a, int bits, int chunks) {
   __shared__ uint32_t keys[kSortChunk], poss[kSortChunk];
   __shared__ uint32_t seen[16 * 65], lds[16];
+  if ((int)blockIdx.x >= chunks) return clear_runs(a, blockIdx.x - chunks, gridDim.x - chunks);
   const int64_t i = (int64_t)blockIdx.x * kSortChunk + threadIdx.x;
   uint32_t k = i < a.T ? key_of(a, i) : 0xffffffffu;  // behind the last one, and stays there
   uint32_t p = (uint32_t)i;
@@ -311,14 +311,10 @@ __global__ __launch_bounds__(1024) void sort_chunk_kernel(SortArgs a, int bits, 
     k = keys[threadIdx.x];
     p = poss[threadIdx.x];
   }
-  if (i < a.T) {
-    a.key[to_result ? 0 : 1][i] = k;
-    a.pos[to_result ? 0 : 1][i] = p;
+  if (i < a.T) {  // one chunk: the result
+    a.key[chunks > 1][i] = k;
+    a.pos[chunks > 1][i] = p;
   }
-  clear_runs(a);
-  if (!to_result) return;
-  __syncthreads();  // the only workgroup
-  if (i < a.T && k < (uint32_t)a.V && (i == 0 || keys[i - 1] != k)) a.run_of[k] = (int32_t)i;
 }
 
 // 64 entries of one chunk a workgroup, every chunk's keys in LDS; each of the
@@ -368,7 +364,7 @@ __global__ __launch_bounds__(256) void sort_rank_kernel(SortArgs a) {
   for (int j = 0; j < 4; ++j) place += places[j][lane];
   a.key[0][place] = k;
   a.pos[0][place] = a.pos[1][i];
-  if (k < (uint32_t)a.V) a.run_of[k] = (int32_t)place;
+  if (a.run_of && k < (uint32_t)a.V) a.run_of[k] = (int32_t)place;
 }
 
 // More tokens: per pass of 9 bits the workgroups' counts of every digit, their
@@ -392,7 +388,7 @@ __device__ inline void sort_item(const SortArgs& a, int pass, int64_t i, uint32_
 __global__ __launch_bounds__(1024) void sort_count_kernel(SortArgs a, int pass) {
   __shared__ uint32_t n[kSortDigits];
   for (int i = threadIdx.x; i < kSortDigits; i += 1024) n[i] = 0;
-  if (pass == 0) clear_runs(a);
+  if (pass == 0 && a.run_of) clear_runs(a, blockIdx.x, gridDim.x);
   __syncthreads();
   for (int r = 0; r < kSortRounds; ++r) {
     const int64_t i = (int64_t)blockIdx.x * kSortItems + r * 1024 + threadIdx.x;
@@ -460,7 +456,7 @@ __global__ __launch_bounds__(1024) void sort_scatter_kernel(SortArgs a, int pass
     const uint32_t to = seen[((k[r] >> shift) & (kSortDigits - 1)) * 16 + w] + at[r];
     a.key[pass & 1][to] = k[r];
     a.pos[pass & 1][to] = p[r];
-    if (last && k[r] < (uint32_t)a.V) a.run_of[k[r]] = (int32_t)to;
+    if (last && a.run_of && k[r] < (uint32_t)a.V) a.run_of[k[r]] = (int32_t)to;
   }
 }
 
@@ -468,8 +464,9 @@ int sort_passes(int64_t V) { return (bits_of(V) + kDigitBits - 1) / kDigitBits; 
 int sort_result(int64_t T, int64_t V) { return T <= kSortSmall ? 0 : (sort_passes(V) - 1) & 1; }
 
 hipError_t launch_sort_small(const SortArgs& a, hipStream_t st) {
-  const unsigned chunks = (unsigned)((a.T + kSortChunk - 1) / kSortChunk);
-  hipLaunchKernelGGL(sort_chunk_kernel, dim3(chunks), dim3(kSortChunk), 0, st, a, bits_of(a.V), chunks == 1 ? 1 : 0);
+  const int chunks = (int)((a.T + kSortChunk - 1) / kSortChunk);
+  const int64_t clear = a.run_of ? std::min<int64_t>((a.V + 4095) / 4096, 64) : 0;
+  hipLaunchKernelGGL(sort_chunk_kernel, dim3((unsigned)(chunks + clear)), dim3(kSortChunk), 0, st, a, bits_of(a.V), chunks);
   if (chunks > 1)
     hipLaunchKernelGGL(sort_rank_kernel, dim3((unsigned)((a.T + 63) / 64)), dim3(256), (unsigned)a.T * 4, st, a);
   return hipGetLastError();
@@ -509,6 +506,7 @@ __device__ inline void put_sum(const EmbedGradArgs& a, int64_t v, int64_t first,
   for (int i = 0; i < 8; ++i) y[i] = x[i] * a.scale;
   if constexpr (SINK == kToSums) {
     store8<kTypeF32>(reinterpret_cast<char*>(a.sums + first * a.cols + 8 * (int64_t)p), y, (int)n);
+    if (p == 0) a.run_of[v] = (int32_t)first;
   } else {
     char* row = a.out + v * a.d * Elem<G>::kBytes;
     if constexpr (SINK == kOnTable) {
@@ -540,6 +538,16 @@ __device__ inline void put_part(const EmbedGradArgs& a, int64_t piece, int which
   if (n > 0) store8<kTypeF32>(reinterpret_cast<char*>(part_row(a, piece, which) + 8 * (int64_t)p), x, (int)n);
 }
 
+// whether a token is among up to kSortChunk sorted ones, which carry no marks
+__device__ inline bool occurs(const EmbedGradArgs& a, uint32_t v) {
+  int lo = 0, hi = (int)a.T;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (a.key[mid] < v) lo = mid + 1; else hi = mid;
+  }
+  return lo < a.T && a.key[lo] == v;
+}
+
 __device__ inline uint32_t lane_of(uint32_t v, int lane) {
   return (uint32_t)__builtin_amdgcn_readlane((int)v, lane);
 }
@@ -555,7 +563,9 @@ __global__ __launch_bounds__(256) void embed_grad_kernel(EmbedGradArgs a, int64_
   if (wave >= pieces * slabs) {
     if constexpr (SINK != kToTable) return;
     const int64_t v0 = (wave - pieces * slabs) * fill, v = v0 + lane;
-    const uint64_t rows = __ballot(lane < fill && v < a.V && a.run_of[min(v, a.V - 1)] < 0);
+    bool empty = lane < fill && v < a.V;
+    if (empty) empty = a.T <= kSortChunk ? !occurs(a, (uint32_t)v) : a.run_of[v] < 0;
+    const uint64_t rows = __ballot(empty);
     const int64_t bytes = a.d * Elem<G>::kBytes;
     int per = 64;  // lanes of a row: as many as its 16-byte pieces, to a power of two
     while (per > 1 && 8 * per >= bytes) per >>= 1;
@@ -619,18 +629,10 @@ __global__ __launch_bounds__(256) void embed_grad_kernel(EmbedGradArgs a, int64_
 }
 
 // A workgroup for each piece in which a run begins that goes on, and each
-// slab: its partial rows in order, a quarter of them to each wave.  Behind
-// those, workgroups that note for tied weights where each token's run begins.
+// slab: its partial rows in order, a quarter of them to each wave.
 template <int SINK, int G>
-__global__ __launch_bounds__(256) void embed_join_kernel(EmbedGradArgs a, int64_t pieces, int slabs, int64_t joins) {
+__global__ __launch_bounds__(256) void embed_join_kernel(EmbedGradArgs a, int64_t pieces, int slabs) {
   __shared__ float sums[3][64 * 8];
-  if (blockIdx.x >= joins) {
-    const int64_t i = ((int64_t)blockIdx.x - joins) * 256 + threadIdx.x;
-    if (i >= a.T) return;
-    const uint32_t v = a.key[i];
-    if (v < (uint32_t)a.V && (i == 0 || a.key[i - 1] != v)) a.run_of[v] = (int32_t)i;
-    return;
-  }
   const int64_t piece = blockIdx.x / slabs;
   const int64_t e0 = piece * a.piece, e1 = e0 + a.piece;
   const int lane = threadIdx.x & 63, w = wave_id();
@@ -799,11 +801,10 @@ hipError_t launch_embed_grad(const EmbedGradArgs& a, hipStream_t st) {
 }
 hipError_t launch_embed_join(const EmbedGradArgs& a, hipStream_t st) {
   const GradShape s = grad_shape(a);
-  const int64_t joins = (s.pieces - 1) * s.slabs, notes = a.tied && a.T > kSortChunk ? (a.T + 255) / 256 : 0;
-  if (joins + notes == 0) return hipSuccess;
+  if (s.pieces == 1) return hipSuccess;
   pick_sink(a, [&](auto sink, auto g) {
-    hipLaunchKernelGGL((embed_join_kernel<decltype(sink)::value, decltype(g)::value>), dim3((unsigned)(joins + notes)),
-                       dim3(256), 0, st, a, s.pieces, s.slabs, joins);
+    hipLaunchKernelGGL((embed_join_kernel<decltype(sink)::value, decltype(g)::value>),
+                       dim3((unsigned)((s.pieces - 1) * s.slabs)), dim3(256), 0, st, a, s.pieces, s.slabs);
   });
   return hipGetLastError();
 }

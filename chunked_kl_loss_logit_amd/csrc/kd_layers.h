@@ -30,7 +30,7 @@ struct SortArgs {
   uint32_t* key[2];  // [T] each
   uint32_t* pos[2];
   uint32_t* count;   // [kSortDigits x workgroups], T > kSortSmall only
-  int32_t* run_of;   // [V]: an entry of each token, or -1
+  int32_t* run_of;   // [V] or nullptr: cleared (-1); beyond kSortChunk tokens an entry of each token is noted
 };
 constexpr int kSortDigits = 512;
 // where the result lies: key[i], pos[i] of the returned index
@@ -53,7 +53,7 @@ struct EmbedGradArgs {
   char* out;    // the table's gradient
   float* part;  // [pieces][2][cols]: what a piece holds of a token that it shares with the piece before, or after
   int piece;    // entries of a piece
-  int32_t* run_of;  // [V]: an entry of each token, or -1; for tied weights its first one, from launch_embed_join on
+  int32_t* run_of;  // [V]: the sort's; with tied weights in the end each token's first entry, or -1
   float* sums;      // tied only, [T][cols]: the sum of the run that begins at an entry
 };
 int embed_piece(int64_t T);

@@ -201,7 +201,8 @@ kd_status kd_embedding_bwd(const void* grad, const int32_t* tokens, const uint8_
     s.pos[i] = at<uint32_t>(workspace, p.pos[i]);
   }
   s.count = at<uint32_t>(workspace, p.count);
-  s.run_of = at<int32_t>(workspace, p.run_of);
+  // a few tokens' gradient looks for the rows to clear among the tokens themselves
+  s.run_of = tied || (T > kd::kSortChunk && !accumulate) ? at<int32_t>(workspace, p.run_of) : nullptr;
   if (T <= kd::kSortSmall) {
     KD_LAUNCH("embedding_sort", st, kd::launch_sort_small(s, st));
   } else {

@@ -105,6 +105,7 @@ class _Checkpoint(torch.autograd.Function):
     @staticmethod
     def forward(ctx, fn, kind, group, x, *others):
         out = fn(x, *others)
+        out = tuple(out) if isinstance(out, list) else out
         q, scale = quantize_rows(_rows(x), kind, group)
         tensors = [t if isinstance(t, torch.Tensor) else None for t in others]
         ctx.save_for_backward(q, scale, *tensors)
@@ -136,8 +137,8 @@ def checkpoint_8bit(fn, x, *others, kind="int8", group=128):
     the gradients there.  others (tensors or not) are kept as they are.  Tensors that fn takes from elsewhere get their
     .grad from backward(), as parameters do; torch.autograd.grad with respect to them needs them among the others.  fn
     has to compute the same both times: random numbers and autocast belong inside it or not in it."""
-    if not isinstance(x, torch.Tensor) or x.dim() == 0:
-        raise TypeError("x must be a tensor of at least one axis")
+    if not isinstance(x, torch.Tensor) or x.dim() == 0 or x.shape[-1] == 0:
+        raise TypeError("x must be a tensor with a last axis of at least one element")
     if x.dtype not in B.TYPES:
         raise TypeError(f"x must be one of {', '.join(map(str, B.TYPES))}, got {x.dtype}")
     B._kind(kind, group)

@@ -12,6 +12,7 @@ SHAPES = [  # T, d, V: few rows, rows of one and several blocks, tiles; lengths 
     (1, 16, 1), (1, 4096, 300), (3, 144, 65), (31, 128, 64), (32, 1024, 127), (33, 1040, 129), (64, 48, 1000),
     (65, 272, 31), (128, 528, 333), (129, 256, 70), (300, 2064, 515), (1000, 16, 40), (129, 64, 33000),
     (257, 1040, 16500), (1030, 256, 8200), (2049, 304, 4100), (1500, 2000, 5537),
+    (2049, 48, 40000), (1030, 272, 20001),  # several tiles a workgroup, of one turn of the ring and of more
 ]
 
 

@@ -83,6 +83,42 @@ def test_checkpointed_step():
     assert all(torch.equal(p, q) for p, q in zip(got, want))
 
 
+def test_saved_tensors_moved_and_changed():
+    """What autograd saved may lie elsewhere by then (hooks that keep it on the host), and is refused if it changed."""
+    s = model(seed=4)
+    X = torch.randn(300, 128, device="cuda").to(bf)
+
+    def run(hooks, kept):
+        x, w, W = (t.clone().requires_grad_(True) for t in (X, s["w"], s["W"]))
+        with torch.autograd.graph.save_on_cpu() if hooks else torch.enable_grad():
+            y = kd.layer_norm(x, w, s["b"], s["mask"], checkpoint=kept) + kd.embedding(s["tokens"], W, s["mask"], tied=True)
+        return torch.autograd.grad(y, (x, w, W), X)
+
+    for kept in (None, "int8", "e4m3"):
+        assert all(torch.equal(a, b) for a, b in zip(run(False, kept), run(True, kept)))
+    x = X.clone().requires_grad_(True)
+    z = x * 1
+    y = kd.layer_norm(z, s["w"])
+    z.add_(1)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.sum().backward()
+
+
+def test_gradients_that_come_expanded_or_not_at_all():
+    s = model(seed=6)
+    x, w, b = (t.clone().requires_grad_(True) for t in (torch.randn(300, 128, device="cuda"), s["w"].float(), s["b"].float()))
+    y = kd.layer_norm(x, w, b, s["mask"])
+    got = torch.autograd.grad(y.sum(), (x, w, b), retain_graph=True)  # an expanded upstream gradient
+    want = torch.autograd.grad(y, (x, w, b), torch.ones_like(y))
+    assert all(torch.equal(p, q) for p, q in zip(got, want))
+    (only,) = torch.autograd.grad(kd.layer_norm(x.detach(), w, None, s["mask"]).sum(), w)  # a leaf alone
+    assert torch.equal(only, want[1])
+    W = s["W"].clone().requires_grad_(True)
+    (g,) = torch.autograd.grad(kd.embedding(s["tokens"], W, s["mask"], tied=True).sum(), W)
+    assert torch.equal(g, kd.embedding_backward(torch.ones(300, 128, device="cuda", dtype=bf), s["tokens"], 520, s["mask"],
+                                                tied=True))
+
+
 def test_teacher_through_8_bits_to_the_loss():
     s = model(T=64, seed=5, masked=0.0)
     s["wq"], s["ws"] = kd.quantize_rows(s["W"].t().contiguous(), "int8", 0)

@@ -149,3 +149,16 @@ def test_checkpoint_of_several_outputs_and_of_nothing_to_keep():
     assert torch.autograd.grad(y.sum(), w)[0].shape == w.shape
     with torch.no_grad():
         assert not kd.checkpoint_8bit(lambda x: x @ w, x).requires_grad
+    a, b = kd.checkpoint_8bit(lambda x: [x * 2, x * 3], x[:0])  # no rows, a list of outputs
+    assert torch.autograd.grad(a.sum() + b.sum(), x)[0].shape == x.shape
+
+
+def test_checkpoint_refuses_what_changed_since():
+    x = torch.randn(8, 64, device="cuda", requires_grad=True)
+    w = torch.randn(64, 64, device="cuda")
+    y = kd.checkpoint_8bit(lambda x, w: x @ w, x, w)
+    w.add_(1)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.sum().backward()
+    with pytest.raises(TypeError, match="last axis"):
+        kd.checkpoint_8bit(abs, torch.ones(3, 0))
