@@ -28,6 +28,7 @@ namespace {
 __device__ inline int wave_in_grid() { return blockIdx.x * (blockDim.x >> 6) + wave_id(); }
 
 constexpr int kSlab = 512;  // columns of a wave
+constexpr int64_t kMostWaves = int64_t(1) << 24;  // of a launch: its threads are counted in 32 bits
 
 }  // namespace
 
@@ -282,7 +283,14 @@ hipError_t launch_embed(const EmbedArgs& a, hipStream_t st) {
     auto with = [&](auto n) {
       constexpr int N = decltype(n)::value;
       const int units = (int)((a.d + kSlab * N - 1) / (kSlab * N));
-      hipLaunchKernelGGL((embed_kernel<TY, N>), dim3((unsigned)((a.T * units + 3) / 4)), dim3(256), 0, st, a, units);
+      EmbedArgs some = a;
+      for (int64_t t = 0; t < a.T; t += some.T) {
+        some.T = std::min(a.T - t, kMostWaves / units);
+        some.tokens = a.tokens + t;
+        some.mask = a.mask ? a.mask + t : nullptr;
+        some.out = a.out + t * a.d * Elem<TY>::kBytes;
+        hipLaunchKernelGGL((embed_kernel<TY, N>), dim3((unsigned)((some.T * units + 3) / 4)), dim3(256), 0, st, some, units);
+      }
     };
     if (a.T * a.d <= (1 << 20)) with(std::integral_constant<int, 1>());  // waves for the whole chip first
     else with(std::integral_constant<int, 4>());
@@ -787,8 +795,8 @@ GradShape grad_shape(const EmbedGradArgs& a) {
 
 hipError_t launch_embed_grad(const EmbedGradArgs& a, hipStream_t st) {
   const GradShape s = grad_shape(a);
-  // table rows of a wave that writes zeros: about one round of the chip's waves
-  const int fill = (int)std::min<int64_t>(std::max<int64_t>(a.V / 8192, 1), 16);
+  // table rows of a wave that writes zeros: about one round of the chip's waves (at most a lane each)
+  const int fill = a.V >= 16 * kMostWaves ? 64 : (int)std::min<int64_t>(std::max<int64_t>(a.V / 8192, 1), 16);
   const int64_t more = a.tied || a.accumulate ? 0 : (a.V + fill - 1) / fill;
   const dim3 grid((unsigned)((s.pieces * s.slabs + more + 3) / 4));
   pick_type(a.type, [&](auto ty) {
@@ -808,6 +816,7 @@ hipError_t launch_embed_join(const EmbedGradArgs& a, hipStream_t st) {
   });
   return hipGetLastError();
 }
+int64_t embed_turn_cols(int64_t V) { return std::max<int64_t>(kMostWaves / 2 / ((V + kTurnV - 1) / kTurnV), 1) * kTurnK; }
 hipError_t launch_embed_turn(const EmbedGradArgs& a, hipStream_t st) {
   pick_type(a.grad_type, [&](auto ty) {
     constexpr int G = decltype(ty)::value;

@@ -59,6 +59,7 @@ struct EmbedGradArgs {
 int embed_piece(int64_t T);
 hipError_t launch_embed_grad(const EmbedGradArgs& a, hipStream_t st);
 hipError_t launch_embed_join(const EmbedGradArgs& a, hipStream_t st);
+int64_t embed_turn_cols(int64_t V);  // columns that one launch of it takes
 hipError_t launch_embed_turn(const EmbedGradArgs& a, hipStream_t st);
 hipError_t launch_fill_table(char* p, int64_t bytes, hipStream_t st);  // zeros, any alignment of 2 bytes
 

@@ -81,12 +81,17 @@ struct EmbedPlan {
   size_t key[2], pos[2], count, part, sums, run_of, total;
   int64_t cols;  // columns of a slab
 };
-// A tied head's sums take a row a token: slabs of columns keep them to 1 GiB.
+// A tied head's sums take a row a token: slabs of columns keep them to 1 GiB,
+// and the launch that turns them below 2^32 threads.
 constexpr int64_t kSumsMost = int64_t(1) << 30;
 EmbedPlan plan_embed(int64_t T, int64_t V, int64_t d, bool tied) {
   EmbedPlan p{};
   Carver cv;
-  p.cols = tied && T > 0 ? std::min<int64_t>(d, std::max<int64_t>(kSumsMost / (4 * T) / 64 * 64, 64)) : d;
+  p.cols = d;
+  if (tied && T > 0) {
+    const int64_t wide = std::max<int64_t>(kSumsMost / (4 * T) / 64 * 64, 64);
+    p.cols = std::min({d, wide, kd::embed_turn_cols(V)});
+  }
   if (T == 0) return p;
   for (int i = 0; i < 2; ++i) {
     p.key[i] = cv.take((size_t)T * 4);

@@ -165,3 +165,24 @@ def test_offsets_beyond_32_bits():
         want = E[a:a + 1000].double() * n[a:a + 1000, None]
         off = (g[a:a + 1000].double() - want).abs()
         assert bool((off <= want.abs() * (2.0 ** -8 + 64 * R.U32)).all())
+
+
+def test_more_rows_than_a_launch_has_waves():
+    T, V = (1 << 26) + 77, 7
+    say(f"embedding T={T} V={V} d=1")
+    tokens = torch.randint(-1, V, (T,), dtype=torch.int32, device="cuda",
+                           generator=torch.Generator("cuda").manual_seed(1))
+    mask = torch.arange(T, device="cuda") % 5 != 0
+    E = torch.randn(V, 1, generator=R.gen(2)).to(torch.bfloat16).cuda()
+    y = kd.embedding_forward(tokens, E, mask)
+    want = torch.cat([E.new_full((1, 1), float("nan")), E])[tokens.long() + 1]
+    want[~mask] = 0
+    assert torch.equal(torch.isnan(y), torch.isnan(want)) and torch.equal(y.nan_to_num(), want.nan_to_num())
+
+
+def test_zeros_in_a_table_of_very_many_rows():
+    V = (1 << 28) + 77
+    say(f"embedding backward T=3 V={V} d=1")
+    out = kd.embedding_backward(torch.ones(3, 1, device="cuda", dtype=torch.bfloat16),
+                                torch.tensor([V - 1, 5, V - 1], dtype=torch.int32, device="cuda"), V)
+    assert out[V - 1] == 2 and out[5] == 1 and int(torch.count_nonzero(out)) == 2

@@ -47,6 +47,9 @@ def test_sizes(L):
         assert st == 0 and 8 * T <= n <= T * (17 + d // 2) + 4 * 32000 + 2 * 4 * d + 1024 * 1024
         st, m = size(L, "kd_embedding_workspace_size", T, 32000, d, 1)
         assert st == 0 and min(4 * T * d, 1 << 29) <= m <= n + (1 << 30) + 1024
+    a, b = (size(L, "kd_embedding_workspace_size", 10, 1 << 28, 1000, tied)[1] for tied in (0, 1))
+    # a large vocabulary: slabs of as many columns as a launch takes (of the partial rows too, 2 for 10 tokens)
+    assert b - a < 4 * 10 * 1000 - 2 * 4 * 1000
     assert size(L, "kd_embedding_workspace_size", -1, 10, 8, 1)[0] == 1
     assert size(L, "kd_embedding_workspace_size", 1 << 30, 10, 8, 1)[0] == 2
     assert size(L, "kd_embedding_workspace_size", 10, 0, 8, 1)[0] == 1
