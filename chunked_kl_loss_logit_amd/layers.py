@@ -104,8 +104,14 @@ def _rows(x):
 class _Checkpoint(torch.autograd.Function):
     @staticmethod
     def forward(ctx, fn, kind, group, x, *others):
+        before = [t._version for t in (x, *others) if isinstance(t, torch.Tensor)]
         out = fn(x, *others)
+        if before != [t._version for t in (x, *others) if isinstance(t, torch.Tensor)]:
+            raise RuntimeError("fn must not change its arguments in place: the backward pass runs it again on them")
         out = tuple(out) if isinstance(out, list) else out
+        for o in out if isinstance(out, tuple) else (out,):
+            if isinstance(o, (tuple, list, dict, set)):  # what they hold would have no gradient
+                raise TypeError(f"fn must return a tensor, or a tuple or list of them, got a {type(o).__name__} in its place")
         q, scale = quantize_rows(_rows(x), kind, group)
         tensors = [t if isinstance(t, torch.Tensor) else None for t in others]
         ctx.save_for_backward(q, scale, *tensors)
@@ -204,6 +210,8 @@ def layer_norm(x, weight=None, bias=None, mask=None, eps=1e-5, checkpoint=None, 
     """Layer norm of the rows of x [T,d], 0 on masked rows; differentiable in x, weight and bias, whose gradients have
     their types.  weight and bias are of x's type or float32.  checkpoint "int8" or "e4m3": the backward pass takes x
     from 8 bits, in groups of `group` values with a scale each, and x itself is not kept."""
+    if checkpoint is not None:
+        B._kind(checkpoint, group)
     return _LayerNorm.apply(x, weight, bias, mask, float(eps), checkpoint, int(group))
 
 

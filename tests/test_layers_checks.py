@@ -92,6 +92,14 @@ def test_rows():
     refused(lambda: kd.checkpoint_8bit(abs, z(3), group=31), ValueError, "group must be one of")
 
 
+def test_checkpointed_functions():
+    x, w = z(3, 8).requires_grad_(True), z(3, 8)
+    refused(lambda: kd.checkpoint_8bit(lambda x: x.add_(1), x * 2), RuntimeError, "in place")
+    refused(lambda: kd.checkpoint_8bit(lambda x, w: x * w.add_(1), x, w), RuntimeError, "in place")
+    refused(lambda: kd.checkpoint_8bit(lambda x: {"y": x * 2}, x), TypeError, "got a dict")
+    refused(lambda: kd.checkpoint_8bit(lambda x: (x * 2, [x * 3]), x), TypeError, "got a list")
+
+
 def test_layer_norm():
     a = dict(x=z(T, D, dtype=bf), weight=z(D), bias=z(D), mask=z(T, dtype=torch.bool), eps=1e-5, y=z(T, D, dtype=bf),
              mean=z(T), rstd=z(T))
@@ -111,6 +119,8 @@ def test_layer_norm():
         gpu_only(lambda: fn(z(T, D)))
         refused(lambda: fn(z(T, D), checkpoint="int4"), ValueError, "kind must be one of") if fn is not kd.layer_norm \
             else refused(lambda: fn(z(T, D).requires_grad_(True), checkpoint="int4"), ValueError, "kind must be one of")
+    refused(lambda: kd.layer_norm(z(T, D), checkpoint="int4"), ValueError, "kind must be one of")  # also without gradients
+    refused(lambda: kd.layer_norm(z(T, D), checkpoint="int8", group=31), ValueError, "group must be one of")
 
 
 def test_layer_norm_bwd():
