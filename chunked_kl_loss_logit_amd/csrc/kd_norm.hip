@@ -28,14 +28,14 @@ constexpr int64_t kNormBlocks = 2048;  // workgroups of the forward pass at most
 
 // ------------------------------------------------------------------ 8-bit copies of a row
 // One piece, whose group lies in this wave's neighbouring lanes.
-template <int KIND, bool WHOLE>
+template <int TY, int KIND, bool WHOLE>
 __device__ inline void keep_piece(const NormArgs& a, int64_t t, int p, const float (&x)[8], uint32_t row_top) {
   const int lanes = a.group >> 3;
   const bool whole = a.groups == 1;
-  const Scale8 g = scale8<KIND>(whole ? row_top : wave_max(top8(x), lanes));
+  const Scale8 g = scale8<KIND, TY != kTypeF32>(whole ? row_top : wave_max(top8(x), lanes));
   const int n = (int)(a.d - 8 * (int64_t)p);
   if (n <= 0) return;
-  store_q8<WHOLE>(a.q + t * a.d + 8 * (int64_t)p, quantize8<KIND>(x, g), n);
+  store_q8<WHOLE>(a.q + t * a.d + 8 * (int64_t)p, quantize8<KIND, TY != kTypeF32>(x, g), n);
   if (whole ? p == 0 : p % lanes == 0) a.scale[t * a.groups + (whole ? 0 : p / lanes)] = g.scale;
 }
 
@@ -115,7 +115,7 @@ __global__ __launch_bounds__(RowTeam<R>::kThreads, K == 1 ? 8 : 4) void norm_fwd
       for (int k = 0; k < K; ++k) {
         const int p = lane + k * R;
         const float zero[8] = {};
-        if constexpr (KIND != kRowsNone) keep_piece<KIND, WHOLE>(a, t, p, zero, 0u);
+        if constexpr (KIND != kRowsNone) keep_piece<TY, KIND, WHOLE>(a, t, p, zero, 0u);
         store8<TY, WHOLE>(a.y + (t * a.d + 8 * (int64_t)p) * Elem<TY>::kBytes, zero, (int)(a.d - 8 * (int64_t)p));
       }
       continue;
@@ -162,7 +162,7 @@ __global__ __launch_bounds__(RowTeam<R>::kThreads, K == 1 ? 8 : 4) void norm_fwd
     for (int k = 0; k < K; ++k) {
       const int p = lane + k * R;
       unpack8<TY>(r[k], x);
-      if constexpr (KIND != kRowsNone) keep_piece<KIND, WHOLE>(a, t, p, x, top);
+      if constexpr (KIND != kRowsNone) keep_piece<TY, KIND, WHOLE>(a, t, p, x, top);
       if constexpr (kLds) {
 #pragma unroll
         for (int h = 0; h < 8; h += 4) {
@@ -223,8 +223,8 @@ __global__ __launch_bounds__(1024) void norm_fwd_long_kernel(NormArgs a) {
     }
     if (a.kind && a.groups == 1) top = Team::most(top, reinterpret_cast<uint32_t*>(lds));
     over([&](int p, const float (&x)[8], int64_t n) {
-      if (a.kind == kRowsInt8) keep_piece<kRowsInt8, false>(a, t, p, x, top);
-      if (a.kind == kRowsE4m3) keep_piece<kRowsE4m3, false>(a, t, p, x, top);
+      if (a.kind == kRowsInt8) keep_piece<TY, kRowsInt8, false>(a, t, p, x, top);
+      if (a.kind == kRowsE4m3) keep_piece<TY, kRowsE4m3, false>(a, t, p, x, top);
       if (n <= 0) return;
       float w[8], b[8], y[8];
       if (a.w) load_any(a.w, a.wtype, a.d, p, w);

@@ -40,9 +40,9 @@ __global__ __launch_bounds__(kRowsThreads) void quantize_kernel(RowsArgs a, int 
     const int64_t t = t0 + (threadIdx.x >> shift);
     float x[8] = {};
     if (t < a.T) load_row<TY>(a.x + t * a.d * Elem<TY>::kBytes, a.d, p, x);
-    const Scale8 g = scale8<KIND>(wave_max(top8(x), lanes));
+    const Scale8 g = scale8<KIND, TY != kTypeF32>(wave_max(top8(x), lanes));
     if (t >= a.T || n <= 0) continue;
-    store_q8(a.q + t * a.d + 8 * (int64_t)p, quantize8<KIND>(x, g), n);
+    store_q8(a.q + t * a.d + 8 * (int64_t)p, quantize8<KIND, TY != kTypeF32>(x, g), n);
     if (p % lanes == 0) a.scale[t * a.groups + p / lanes] = g.scale;
   }
 }
@@ -60,12 +60,12 @@ __global__ __launch_bounds__(RowTeam<R>::kThreads) void quantize_row_kernel(Rows
       load_row<TY>(a.x + t * a.d * Elem<TY>::kBytes, a.d, lane + k * R, x[k]);
       top = max(top, top8(x[k]));
     }
-    const Scale8 g = scale8<KIND>(Team::most(top, lds));
+    const Scale8 g = scale8<KIND, TY != kTypeF32>(Team::most(top, lds));
     if (lane == 0) a.scale[t] = g.scale;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int64_t at = 8 * (int64_t)(lane + k * R);
-      if (at < a.d) store_q8(a.q + t * a.d + at, quantize8<KIND>(x[k], g), (int)(a.d - at));
+      if (at < a.d) store_q8(a.q + t * a.d + at, quantize8<KIND, TY != kTypeF32>(x[k], g), (int)(a.d - at));
     }
   }
 }
@@ -81,12 +81,12 @@ __global__ __launch_bounds__(1024) void quantize_long_kernel(RowsArgs a) {
       load_row<TY>(row, a.d, (int)(at / 8), x);
       top = max(top, top8(x));
     }
-    const Scale8 g = scale8<KIND>(RowTeam<1024>::most(top, lds));
+    const Scale8 g = scale8<KIND, TY != kTypeF32>(RowTeam<1024>::most(top, lds));
     if (threadIdx.x == 0) a.scale[t] = g.scale;
     for (int64_t at = 8 * (int64_t)threadIdx.x; at < a.d; at += 8192) {
       float x[8];
       load_row<TY>(row, a.d, (int)(at / 8), x);
-      store_q8(a.q + t * a.d + at, quantize8<KIND>(x, g), (int)(a.d - at));
+      store_q8(a.q + t * a.d + at, quantize8<KIND, TY != kTypeF32>(x, g), (int)(a.d - at));
     }
   }
 }

@@ -103,6 +103,23 @@ def test_every_value_of_a_16_bit_type():
             compare(x, kind, 32)
 
 
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_every_ratio_of_a_16_bit_types_values(dtype, kind):
+    """Every significand as the largest of its group and every one below it in 12 binades: all quotients that such
+    values can have, ties and the nearest to ties among them."""
+    n = 128 if dtype == torch.bfloat16 else 1024
+    sig = torch.arange(n, 2 * n, dtype=torch.float64)
+    below = torch.cat([sig / n * 2.0 ** -e for e in range(12)])
+    below[1::2] *= -1
+    for part in range(0, n, 256):
+        top = sig[part:part + 256, None] / n
+        x = torch.cat([top, torch.where(below.abs() < top, below, 0)], 1) * (1 if dtype == torch.float16 else 2.0 ** -40)
+        say(f"rows {dtype} {kind}: {x.numel()} values from significand {part}")
+        assert torch.equal(x, x.to(dtype).double())
+        compare(x.to(dtype), kind, 0)
+
+
 def test_nothing_and_offsets_beyond_32_bits():
     q, s = kd.quantize_rows(torch.empty(0, 64, device="cuda"), "int8", 32)
     assert q.shape == (0, 64) and s.shape == (0, 2) and kd.dequantize_rows(q, s, 32).shape == (0, 64)
