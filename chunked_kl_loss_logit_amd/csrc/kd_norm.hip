@@ -9,6 +9,11 @@
 // and a workgroup goes over many rows, so that weight and bias are read once
 // per workgroup.  One piece of 8 elements a thread, so that there are enough
 // waves: 16384 x 4096 bf16 with two pieces took 51 us, so 46 (268 MB, 5.8 TB/s).
+// Beyond 4096 elements three or two, as 16 waves at one barrier cost more: 8192 x
+// 8192 bf16 with one 50 us, so 46, and with its copy in 8 bits 82 and 77 (335 MB);
+// 14563 x 4608 58 and 47, 119 and 85.  Narrow rows share a workgroup, by the
+// smallest shape that holds them: 67 M values in rows of 136 116 us in whole
+// waves, 67 in halves; of 520 in four waves 110, in two 67.
 #include <type_traits>
 
 #include "kd_launch.h"
@@ -25,15 +30,15 @@ namespace {
 
 constexpr int64_t kNormBlocks = 2048;  // workgroups of the forward pass at most
 
-
 // ------------------------------------------------------------------ 8-bit copies of a row
-// One piece, whose group lies in this wave's neighbouring lanes.
+// One piece, whose group lies in this wave's neighbouring lanes; d: the row's
+// elements, or 0 for a row behind the last one.
 template <int TY, int KIND, bool WHOLE>
-__device__ inline void keep_piece(const NormArgs& a, int64_t t, int p, const float (&x)[8], uint32_t row_top) {
+__device__ inline void keep_piece(const NormArgs& a, int64_t t, int64_t d, int p, const float (&x)[8], uint32_t row_top) {
   const int lanes = a.group >> 3;
   const bool whole = a.groups == 1;
   const Scale8 g = scale8<KIND, TY != kTypeF32>(whole ? row_top : wave_max(top8(x), lanes));
-  const int n = (int)(a.d - 8 * (int64_t)p);
+  const int n = (int)(d - 8 * (int64_t)p);
   if (n <= 0) return;
   store_q8<WHOLE>(a.q + t * a.d + 8 * (int64_t)p, quantize8<KIND, TY != kTypeF32>(x, g), n);
   if (whole ? p == 0 : p % lanes == 0) a.scale[t * a.groups + (whole ? 0 : p / lanes)] = g.scale;
@@ -43,8 +48,8 @@ __device__ inline void keep_piece(const NormArgs& a, int64_t t, int p, const flo
 
 // ------------------------------------------------------------------ forward
 // The thread's weights and biases: in registers, or in LDS where the 8-bit copy
-// takes the registers (two workgroups of a wide row's 1024 threads then fit a
-// CU: 8192 x 8192 with its copy 123 us -> 95; without a copy LDS costs 46 -> 56).
+// takes the registers: 8192 x 8192 bf16 with its copy in registers 168 us, in LDS
+// 82; without a copy LDS costs 46 -> 56.
 template <bool LDS, int N>
 struct Affine {
   float w[N][8], b[N][8];
@@ -52,10 +57,17 @@ struct Affine {
 template <int N>
 struct Affine<true, N> {};
 
+// Waves a SIMD for which there have to be registers: as many as leave hardly any
+// of them in memory.
+constexpr int norm_waves(int type, int pieces) {
+  if (pieces == 1) return type != kTypeF32 ? 8 : 6;
+  return pieces > 2 && type == kTypeF32 ? 3 : 4;
+}
+
 // The row's pieces stay in registers as they were loaded, and the next row's
 // are loaded while one is worked on.
 template <int TY, int KIND, bool WHOLE, int R, int K>
-__global__ __launch_bounds__(RowTeam<R>::kThreads, K == 1 ? 8 : 4) void norm_fwd_kernel(NormArgs a) {
+__global__ __launch_bounds__(RowTeam<R>::kThreads, norm_waves(TY, K)) void norm_fwd_kernel(NormArgs a) {
   using Team = RowTeam<R>;
   constexpr bool kLds = KIND != kRowsNone;
   __shared__ float lds[16];
@@ -99,27 +111,15 @@ __global__ __launch_bounds__(RowTeam<R>::kThreads, K == 1 ? 8 : 4) void norm_fwd
     }
   };
   load(next, t);
-  for (; t < a.T; t += step) {
+  for (; Team::left(t, a.T); t += step) {
+    const int64_t d = Team::elements(t, a.T, a.d);
+    const bool valid = d > 0 && row_valid(a.mask, t);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       r[k] = next[k];
       settle8<TY, WHOLE>(r[k], (int)(a.d - 8 * (int64_t)(lane + k * R)), lane + k * R > 0);
     }
     load(next, t + step);
-    if (!row_valid(a.mask, t)) {
-      if (lane == 0) {
-        if (a.mean) a.mean[t] = 0.f;
-        if (a.rstd) a.rstd[t] = 0.f;
-      }
-#pragma unroll
-      for (int k = 0; k < K; ++k) {
-        const int p = lane + k * R;
-        const float zero[8] = {};
-        if constexpr (KIND != kRowsNone) keep_piece<TY, KIND, WHOLE>(a, t, p, zero, 0u);
-        store8<TY, WHOLE>(a.y + (t * a.d + 8 * (int64_t)p) * Elem<TY>::kBytes, zero, (int)(a.d - 8 * (int64_t)p));
-      }
-      continue;
-    }
     float s[1] = {0.f};
     float x[8];
 #pragma unroll
@@ -153,16 +153,16 @@ __global__ __launch_bounds__(RowTeam<R>::kThreads, K == 1 ? 8 : 4) void norm_fwd
     }
     Team::sum(s, lds);
     const float rstd = 1.f / sqrtf(s[0] * inv_d + a.eps);
-    if (lane == 0) {
-      if (a.mean) a.mean[t] = mean;
-      if (a.rstd) a.rstd[t] = rstd;
+    if (lane == 0 && d > 0) {
+      if (a.mean) a.mean[t] = valid ? mean : 0.f;
+      if (a.rstd) a.rstd[t] = valid ? rstd : 0.f;
     }
     if (KIND != kRowsNone && a.groups == 1) top = Team::most(top, reinterpret_cast<uint32_t*>(lds));
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int p = lane + k * R;
       unpack8<TY>(r[k], x);
-      if constexpr (KIND != kRowsNone) keep_piece<TY, KIND, WHOLE>(a, t, p, x, top);
+      if constexpr (KIND != kRowsNone) keep_piece<TY, KIND, WHOLE>(a, t, d, p, x, top);
       if constexpr (kLds) {
 #pragma unroll
         for (int h = 0; h < 8; h += 4) {
@@ -177,7 +177,11 @@ __global__ __launch_bounds__(RowTeam<R>::kThreads, K == 1 ? 8 : 4) void norm_fwd
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] = fmaf((x[i] - mean) * rstd, own.w[k][i], own.b[k][i]);
       }
-      store8<TY, WHOLE>(a.y + (t * a.d + 8 * (int64_t)p) * Elem<TY>::kBytes, x, (int)(a.d - 8 * (int64_t)p));
+      if (!valid) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = 0.f;
+      }
+      store8<TY, WHOLE>(a.y + (t * a.d + 8 * (int64_t)p) * Elem<TY>::kBytes, x, (int)(d - 8 * (int64_t)p));
     }
   }
 }
@@ -223,8 +227,8 @@ __global__ __launch_bounds__(1024) void norm_fwd_long_kernel(NormArgs a) {
     }
     if (a.kind && a.groups == 1) top = Team::most(top, reinterpret_cast<uint32_t*>(lds));
     over([&](int p, const float (&x)[8], int64_t n) {
-      if (a.kind == kRowsInt8) keep_piece<TY, kRowsInt8, false>(a, t, p, x, top);
-      if (a.kind == kRowsE4m3) keep_piece<TY, kRowsE4m3, false>(a, t, p, x, top);
+      if (a.kind == kRowsInt8) keep_piece<TY, kRowsInt8, false>(a, t, a.d, p, x, top);
+      if (a.kind == kRowsE4m3) keep_piece<TY, kRowsE4m3, false>(a, t, a.d, p, x, top);
       if (n <= 0) return;
       float w[8], b[8], y[8];
       if (a.w) load_any(a.w, a.wtype, a.d, p, w);
@@ -254,8 +258,8 @@ hipError_t launch_norm_fwd(const NormArgs& a, hipStream_t st) {
         else hipLaunchKernelGGL((norm_fwd_kernel<TY, KIND, false, R, K>), grid, block, 0, st, a);
       };
       // by the width alone, so that a row's bits do not hang on how many rows there are
-      const bool held = pick_shape<Shape<16, 1>, Shape<64, 1>, Shape<256, 1>, Shape<512, 1>, Shape<1024, 1>, Shape<1024, 2>>(
-          a.d, launch);
+      const bool held = pick_shape<Shape<16, 1>, Shape<32, 1>, Shape<64, 1>, Shape<128, 1>, Shape<256, 1>, Shape<512, 1>,
+                                   Shape<256, 3>, Shape<512, 2>, Shape<1024, 2>>(a.d, launch);
       if (!held)
         hipLaunchKernelGGL((norm_fwd_long_kernel<TY>), dim3((unsigned)std::min<int64_t>(a.T, 512)), dim3(1024), 0, st, a);
     };

@@ -69,8 +69,14 @@ __device__ inline void input_values(const Input<TY, KIND>& r, float (&x)[8]) {
 }  // namespace
 
 template <int TY, int KIND, bool WHOLE, int R, int K>
-__global__ __launch_bounds__(RowTeam<R>::kThreads, 4) void norm_grad_kernel(NormGradArgs a) {
+__global__ __launch_bounds__(RowTeam<R>::kThreads, K > 1 && R == 64 ? 3 : 4) void norm_grad_kernel(NormGradArgs a) {
   using Team = RowTeam<R>;
+  // Two pieces a thread: the weights are read again for each row, and with 16 waves to a row they come from LDS and
+  // there are no registers for the next row.  7282 x 9216 bf16 with all of it in (spilled) registers 267 us, with the
+  // weights from the cache 173, so 104.
+  constexpr bool kAhead = K == 1 || R == 64, kLds = K > 1 && R > 64;
+  __shared__ __attribute__((aligned(16))) float shared_w[kLds ? R * K * 8 : 4];
+  static_assert(!Team::kJoint, "the loop below ends for each row by itself");
   __shared__ float lds[2 * 16];
   const int lane = Team::lane();
   float w[K][8], dw[K][8], db[K][8];
@@ -81,6 +87,7 @@ __global__ __launch_bounds__(RowTeam<R>::kThreads, 4) void norm_grad_kernel(Norm
     for (int i = 0; i < 8; ++i) {
       if (!a.w) w[k][i] = 1.f;
       dw[k][i] = db[k][i] = 0.f;
+      if constexpr (kLds) shared_w[8 * (lane + k * R) + i] = w[k][i];
     }
   }
   const float inv_d = 1.f / (float)a.d;
@@ -101,8 +108,9 @@ __global__ __launch_bounds__(RowTeam<R>::kThreads, 4) void norm_grad_kernel(Norm
       gn[k] = load8<TY, WHOLE>(a.grad + (row * a.d + 8 * (int64_t)p) * Elem<TY>::kBytes, n, p > 0);
     }
   };
-  load(t);
+  if constexpr (kAhead) load(t);
   for (; t < a.T; t += step) {
+    if constexpr (!kAhead) load(t);
     char* out = a.dx ? a.dx + t * a.d * Elem<TY>::kBytes : nullptr;
     const float m = mean, r = rstd;
 #pragma unroll
@@ -113,7 +121,15 @@ __global__ __launch_bounds__(RowTeam<R>::kThreads, 4) void norm_grad_kernel(Norm
       settle_input<TY, KIND, WHOLE>(xr[k], p, n);
       settle8<TY, WHOLE>(gr[k], n, p > 0);
     }
-    load(t + step);  // the next row, while this one is worked on
+    if constexpr (kAhead) load(t + step);  // the next row, while this one is worked on
+    auto weights = [&](int k) {
+      if constexpr (kLds) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[k][i] = shared_w[8 * (lane + k * R) + i];  // this thread's own
+      } else if constexpr (K > 1) {
+        if (a.w) load_any(a.w, a.wtype, a.d, lane + k * R, w[k]);
+      }
+    };
     // a piece's h and g from what lies in registers as it was loaded
     auto values = [&](int k, float (&h)[8], float (&g)[8]) {
       const int64_t n = a.d - 8 * (int64_t)(lane + k * R);
@@ -127,6 +143,7 @@ __global__ __launch_bounds__(RowTeam<R>::kThreads, 4) void norm_grad_kernel(Norm
     for (int k = 0; k < K; ++k) {
       float h[8], g[8];
       values(k, h, g);
+      weights(k);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         dw[k][i] = fmaf(g[i], h[i], dw[k][i]);
@@ -144,6 +161,7 @@ __global__ __launch_bounds__(RowTeam<R>::kThreads, 4) void norm_grad_kernel(Norm
       const int64_t at = 8 * (int64_t)(lane + k * R);
       float h[8], g[8];
       values(k, h, g);
+      weights(k);
 #pragma unroll
       for (int i = 0; i < 8; ++i) g[i] = r * fmaf(-h[i], c1, g[i] * w[k][i] - c0);
       store8<TY, WHOLE>(out + at * Elem<TY>::kBytes, g, (int)(a.d - at));
@@ -278,7 +296,7 @@ __global__ __launch_bounds__(1024) void norm_sum_kernel(NormGradArgs a) {
 
 // ------------------------------------------------------------------ launches
 int norm_grad_blocks(int64_t T, int64_t d) {
-  const int64_t rows = d <= 128 ? 16 : d <= 512 ? 4 : 1;  // of a workgroup
+  const int64_t rows = d <= 128 ? 16 : d <= 256 ? 8 : d <= 1024 ? 4 : 1;  // of a workgroup
   return (int)std::min<int64_t>(std::max<int64_t>((T + rows - 1) / rows, 1), d <= kRowMost ? 512 : 256);
 }
 
@@ -288,8 +306,8 @@ hipError_t launch_norm_grad(const NormGradArgs& a, hipStream_t st) {
     constexpr int TY = decltype(ty)::value;
     auto with = [&](auto kind) {
       constexpr int KIND = decltype(kind)::value;
-      const bool held = pick_shape<Shape<16, 1>, Shape<64, 1>, Shape<256, 1>, Shape<512, 1>, Shape<1024, 1>, Shape<1024, 2>>(
-          a.d, [&](auto r, auto k) {
+      const bool held = pick_shape<Shape<16, 1>, Shape<32, 1>, Shape<64, 1>, Shape<64, 2>, Shape<256, 1>, Shape<512, 1>,
+                                   Shape<1024, 1>, Shape<1024, 2>>(a.d, [&](auto r, auto k) {
         constexpr int R = decltype(r)::value, K = decltype(k)::value;
         const dim3 block(RowTeam<R>::kThreads);
         if (a.d % 8 == 0) hipLaunchKernelGGL((norm_grad_kernel<TY, KIND, true, R, K>), grid, block, 0, st, a);

@@ -1,6 +1,6 @@
 // One row in the registers of R threads: thread i holds the pieces of 8
-// elements i, i + R, .., i + (K - 1) R.  R = 16 is a quarter of a wave and R =
-// 64 a wave, so that a workgroup of 256 holds 16 rows or four; otherwise the
+// elements i, i + R, .., i + (K - 1) R.  Below R = 256 a workgroup of 256 holds
+// several rows, each of a part of a wave, a wave, or two waves; otherwise the
 // workgroup is the row's.
 #pragma once
 
@@ -35,21 +35,30 @@ template <int R>
 struct RowTeam {
   static constexpr int kThreads = R < 256 ? 256 : R;
   static constexpr int kRows = kThreads / R;  // rows of a workgroup
-  static constexpr int kWaves = R / 64;
+  static constexpr int kWaves = R / 64;  // 0: less than one
+  // Rows of several waves each in one workgroup: gone through together, as their sums meet at its barriers.
+  static constexpr bool kJoint = R > 64 && kRows > 1;
   __device__ static inline int lane() { return threadIdx.x % R; }
   __device__ static inline int slot() { return threadIdx.x / R; }
+  __device__ static inline int wave() { return kJoint ? lane() >> 6 : (int)threadIdx.x >> 6; }  // of the row's
+  // whether row t, or one beside it that it waits for, is left; and its elements, none behind the last row
+  __device__ static inline bool left(int64_t t, int64_t T) { return (kJoint ? t - slot() : t) < T; }
+  __device__ static inline int64_t elements(int64_t t, int64_t T, int64_t d) { return !kJoint || t < T ? d : 0; }
 
   // Sums over the row's threads, each of N values, in the same order every
-  // time.  lds: N kWaves floats, free again after the next barrier.
+  // time.  lds: N floats for each wave of the workgroup, free again after the
+  // next barrier.
   template <int N>
   __device__ static inline void sum(float (&v)[N], float* lds) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      if constexpr (R == 16) v[i] = add_lane<8>(add_lane<4>(add_lane<2>(add_lane<1>(v[i]))));
-      else v[i] = wave_sum(v[i]);
+      v[i] = add_lane<8>(add_lane<4>(add_lane<2>(add_lane<1>(v[i]))));
+      if constexpr (R >= 32) v[i] = add_lane<16>(v[i]);
+      if constexpr (R >= 64) v[i] = add_lane<32>(v[i]);
     }
     if constexpr (R > 64) {
-      const int w = threadIdx.x >> 6;
+      const int w = wave();
+      if constexpr (kJoint) lds += slot() * N * kWaves;
       __syncthreads();
       if ((threadIdx.x & 63) == 0)
 #pragma unroll
@@ -66,8 +75,9 @@ struct RowTeam {
   __device__ static inline uint32_t most(uint32_t v, uint32_t* lds) {
     v = wave_max(v, R);
     if constexpr (R > 64) {
+      if constexpr (kJoint) lds += slot() * kWaves;
       __syncthreads();
-      if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
+      if ((threadIdx.x & 63) == 0) lds[wave()] = v;
       __syncthreads();
 #pragma unroll
       for (int k = 0; k < kWaves; ++k) v = max(v, lds[k]);

@@ -52,20 +52,21 @@ __global__ __launch_bounds__(RowTeam<R>::kThreads) void quantize_row_kernel(Rows
   using Team = RowTeam<R>;
   __shared__ uint32_t lds[16];
   const int lane = Team::lane();
-  for (int64_t t = (int64_t)blockIdx.x * Team::kRows + Team::slot(); t < a.T; t += (int64_t)gridDim.x * Team::kRows) {
+  for (int64_t t = (int64_t)blockIdx.x * Team::kRows + Team::slot(); Team::left(t, a.T); t += (int64_t)gridDim.x * Team::kRows) {
+    const int64_t d = Team::elements(t, a.T, a.d);
     float x[K][8];
     uint32_t top = 0;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      load_row<TY>(a.x + t * a.d * Elem<TY>::kBytes, a.d, lane + k * R, x[k]);
+      load_row<TY>(a.x + t * a.d * Elem<TY>::kBytes, d, lane + k * R, x[k]);
       top = max(top, top8(x[k]));
     }
     const Scale8 g = scale8<KIND, TY != kTypeF32>(Team::most(top, lds));
-    if (lane == 0) a.scale[t] = g.scale;
+    if (lane == 0 && d > 0) a.scale[t] = g.scale;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int64_t at = 8 * (int64_t)(lane + k * R);
-      if (at < a.d) store_q8(a.q + t * a.d + at, quantize8<KIND, TY != kTypeF32>(x[k], g), (int)(a.d - at));
+      if (at < d) store_q8(a.q + t * a.d + at, quantize8<KIND, TY != kTypeF32>(x[k], g), (int)(d - at));
     }
   }
 }
@@ -136,8 +137,8 @@ hipError_t launch_rows_quantize(const RowsArgs& a, hipStream_t st) {
     constexpr int TY = decltype(ty)::value, KIND = decltype(kind)::value;
     // a group that is the row, unless a wave's lanes hold it
     if (a.groups == 1) {
-      const bool held = pick_shape<Shape<16, 1>, Shape<64, 1>, Shape<256, 1>, Shape<512, 1>, Shape<1024, 1>, Shape<1024, 2>>(
-          a.d, [&](auto r, auto k) {
+      const bool held = pick_shape<Shape<16, 1>, Shape<32, 1>, Shape<64, 1>, Shape<128, 1>, Shape<256, 1>, Shape<512, 1>,
+                                   Shape<256, 3>, Shape<512, 2>, Shape<1024, 2>>(a.d, [&](auto r, auto k) {
         constexpr int R = decltype(r)::value, K = decltype(k)::value;
         const int64_t rows = (a.T + RowTeam<R>::kRows - 1) / RowTeam<R>::kRows;
         hipLaunchKernelGGL((quantize_row_kernel<TY, KIND, R, K>), dim3((unsigned)std::min<int64_t>(rows, 8192)),
