@@ -2,7 +2,10 @@
 //
 //   out[t] = scale E[tokens[t]],   dE_v = scale sum_{t: tokens[t] = v} grad[t]
 //
-// Forward: a copy of rows, or for tied weights a gather of columns.
+// Forward: a copy of rows, or for tied weights a gather of columns.  Bound by
+// memory: 16384 rows of 2048 bf16 from a table of 128256 17-28 us (134 MB); tied,
+// 4096 of 128256 columns of 2048 rows 35 us, cold 42 (some 236 MB of cache
+// lines for 17 MB of elements).
 //
 // Backward: rows that meet in one token are added up without atomics.  The
 // positions are sorted by token (stable, so in ascending order within one);
@@ -14,7 +17,10 @@
 // bits each time.  A frequent token (the first few take a tenth of a text)
 // then costs as many partial rows as it has pieces, spread over the chip.
 // For tied weights the runs' sums go to rows of their own first, and a third
-// kernel makes them columns of the head's gradient.
+// kernel makes them columns of the head's gradient.  Bound by the writes of the
+// table's gradient: 16384 x 2048 bf16 into 128256 rows 15 us to sort, 109 for the
+// sums and the zeros beside them (592 MB, 5.4 TB/s), 8 to join; tied, 3001 into
+// 2048 x 32000 float32 11, 12, 5 and 40 to turn (262 MB at a fill's 6.6 TB/s).
 #include <type_traits>
 
 #include "kd_launch.h"

@@ -9,10 +9,12 @@
 //
 // Many rows: 256 x 256 tiles on the direct-to-LDS ring.  x goes through panels
 // (kd_dma.h) padded with zeros to whole ring turns, which cancel whatever w's
-// rows read past their end.  Few rows or few tiles: w is what has to be read;
+// rows read past their end.  4001 x 4096 x 128256: 1.90 ms, 2.2 POP/s, the matrix
+// pipe busy 65% at the 1.6 GHz that the chip keeps under it, no LDS conflicts.
+// Few rows or few tiles: w is what has to be read;
 // a workgroup takes 64 channels and up to 128 rows, each of its four waves a
 // quarter of k, straight from global memory into registers (few channels: 32
-// and eight waves).
+// and eight waves).  4 x 4096 x 32000: 22 us, 131 MB of w at 6 TB/s.
 #include <type_traits>
 
 #include "kd_dma.h"

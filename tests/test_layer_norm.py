@@ -73,6 +73,17 @@ def test_backward_from_8_bits(T, d, group, kind):
                 R.check(t, want[name], bound[name], f"{dtype} masked={masked} {name}")
 
 
+@pytest.mark.parametrize("T,d", [(17, 130), (9, 200), (8, 256), (11, 257), (5, 520), (4099, 600), (7, 1024), (3, 4608),
+                                 (5, 6144), (3, 6145), (3, 9216)])
+def test_rows_that_share_a_workgroup_and_wide_ones(T, d):
+    """The last workgroup's rows end before the last of them, or its loop does; rows of three pieces a thread."""
+    for dtype, wtype in TYPES[:3]:
+        test_both_passes(T, d, dtype, wtype)
+    for group, kind in ((0, "int8"), (32, "e4m3"), (128, "int8")):
+        test_backward_from_8_bits(T, d, group, kind)
+
+
+
 def test_large_means_and_constant_rows():
     """The variance is taken around the mean: rows far from 0 keep their digits, constant rows give the bias."""
     for d in (100, 4096, 20000):

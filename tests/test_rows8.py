@@ -38,6 +38,14 @@ def test_shapes(dtype, kind, group):
 
 
 @pytest.mark.parametrize("kind", KINDS)
+def test_whole_rows_that_share_a_workgroup_and_wide_ones(kind):
+    for T, d in ((17, 130), (9, 256), (5, 520), (16387, 600), (7, 1024), (3, 4608), (3, 6145), (3, 9216)):
+        say(f"rows {kind} T={T} d={d}")
+        for dtype in R.TYPES:
+            compare(torch.randn(T, d, generator=R.gen(T)).to(dtype), kind, 0)
+
+
+@pytest.mark.parametrize("kind", KINDS)
 def test_next_to_the_middle_of_two_steps(kind):
     """Values whose quotient is a tie, and their neighbours on both sides: rounding must see the exact quotient."""
     top = 127.0 if kind == "int8" else 448.0
