@@ -58,7 +58,8 @@ constexpr int kDmaKMult = kRing * kDmaKs;  // the contraction length must be a m
 // lane, so the compiler keeps the descriptor in scalar registers even where
 // it cannot prove the pointer uniform; otherwise it wraps every load that
 // uses the descriptor in a loop over the distinct values.
-// `bytes`: the operand's size; a load past it touches no memory.
+// `bytes`: the operand's size; a lane whose vector offset lies past it touches
+// no memory.  (Whether the scalar offset counts there is not relied on.)
 __device__ inline __amdgpu_buffer_rsrc_t make_rsrc(const char* base, long bytes = 0xffffffffL) {
   // the builtin takes and returns int: widen through uint32_t, or a low
   // half with bit 31 set would be sign-extended over the high half
@@ -96,6 +97,8 @@ struct DmaRows {
     const int q = wave_id() * kPer + i;
     return 16 * q + ((threadIdx.x & 63) >> 2);
   }
+  // the 16-byte chunk of row m that this lane fetches
+  __device__ inline static int chunk_of(int m) { return (threadIdx.x & 3) ^ ((m >> 2) & 3); }
   // row_ptr(i) for i < kPer: address of row row_of(i) (clamped to a valid row)
   template <class RowAddr>
   __device__ inline void init(const char* b, RowAddr&& row_ptr, uint32_t stage_stride = kRowB) {
@@ -103,8 +106,7 @@ struct DmaRows {
     sst = stage_stride;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      const int m = row_of(i);
-      off[i] = (uint32_t)(row_ptr(i) - b) + 16u * ((threadIdx.x & 3) ^ ((m >> 2) & 3));
+      off[i] = (uint32_t)(row_ptr(i) - b) + 16u * (uint32_t)chunk_of(row_of(i));
     }
   }
   // stage s of the rows `extra` bytes further on (a uniform offset, such as

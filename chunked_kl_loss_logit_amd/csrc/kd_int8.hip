@@ -8,8 +8,8 @@
 // each, as the 16-bit one takes 8 elements.
 //
 // Many rows: 256 x 256 tiles on the direct-to-LDS ring.  x goes through panels
-// (kd_dma.h) padded with zeros to whole ring turns, which cancel whatever w's
-// rows read past their end.  4001 x 4096 x 128256: 1.90 ms, 2.2 POP/s, the matrix
+// (kd_dma.h) padded with zeros to whole ring turns, which cancel what w's
+// stages show twice (kd_int8_place.h).  4001 x 4096 x 128256: 1.90 ms, 2.2 POP/s, the matrix
 // pipe busy 65% at the 1.6 GHz that the chip keeps under it, no LDS conflicts.
 // Few rows or few tiles: w is what has to be read;
 // a workgroup takes 64 channels and up to 128 rows, each of its four waves a
@@ -18,6 +18,7 @@
 #include <type_traits>
 
 #include "kd_dma.h"
+#include "kd_int8_place.h"
 #include "kd_launch.h"
 #include "kd_layers.h"
 #include "kd_row.h"
@@ -39,18 +40,18 @@ __device__ inline void mma0_i8(i32x16_t& acc, u32x4_t a, u32x4_t b) {  // into a
                                               0, 0, 0);
 }
 
-constexpr int kKTurn = kRing * kRowB;  // k of a ring turn
+static_assert(kInt8Stage == kRowB && kInt8Turn == kRing * kRowB && kInt8Rows == kBM, "the ring's stages and blocks");
 
 }  // namespace
 
 // ------------------------------------------------------------------ x in panels
 __global__ __launch_bounds__(256) void int8_panels_kernel(const char* x, long T, long d, long chunks, char* panels) {
-  const long n = T * chunks;
+  const long n = T * chunks, rows = int8_panel_rows(T);
   for (long i = (long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long)gridDim.x * 256) {
     // four 16-byte chunks of a 64-byte piece are neighbours, then rows, then pieces
     const long c = (i / (4 * T)) * 4 + (i & 3), t = (i >> 2) % T;
-    const long byte = c * 16;
-    *reinterpret_cast<u32x4_t*>(panels + panel_off(T, t, byte)) = byte < d ? ld16(x + t * d + byte) : zero4();
+    const long at = int8_x_at(c >> 2, c & 3, d);
+    *reinterpret_cast<u32x4_t*>(panels + panel_off(rows, t, c * 16)) = at >= 0 ? ld16(x + t * d + at) : zero4();
   }
 }
 
@@ -161,11 +162,11 @@ __global__ __launch_bounds__(kThreads, 1) void int8_tile_kernel(Int8Args a, int 
   const int tiles = nrb * ncb, xcd = blockIdx.x & 7, turn = gridDim.x >> 3;  // the grid is a multiple of 8
   const int begin = (int)((long)tiles * xcd / 8) + (int)(blockIdx.x >> 3), end = (int)((long)tiles * (xcd + 1) / 8);
   const int mine = begin < end ? (end - begin + turn - 1) / turn : 0;
-  const long stages = (a.d + kRowB - 1) / kRowB, nst = (stages + kRing - 1) / kRing * kRing, w_last = stages - 1;
-  const long panel_bytes = a.T * nst * kRowB;
+  const long nst = int8_turns(a.d) * kRing, rows = int8_panel_rows(a.T);
+  const long panel_bytes = rows * nst * kRowB;
 
-  // what a tile's loads start from; rows behind the last one of either operand
-  // and w's bytes behind its end are past the descriptors' ranges
+  // what a tile's loads start from; w's rows behind the last one are past its
+  // descriptor's range by their vector offset alone
   struct Place {
     long row0, n0;
     __amdgpu_buffer_rsrc_t x, w;
@@ -183,16 +184,18 @@ __global__ __launch_bounds__(kThreads, 1) void int8_tile_kernel(Int8Args a, int 
   const __amdgpu_buffer_rsrc_t rsx = make_rsrc(reinterpret_cast<const char*>(a.sx), a.T * 4);
   const __amdgpu_buffer_rsrc_t rsw = make_rsrc(reinterpret_cast<const char*>(a.sw), min((long)a.V * 4, 0xffffffffL));
   const ScaleSlots scales{sl.ep};
-  const uint32_t own = 4 * (threadIdx.x & 63);
-  auto load_scales = [&](int t, const Place& p) {
-    const uint32_t at = 256u * (uint32_t)wave_id();
-    dma4(rsx, own, (uint32_t)(p.row0 * 4) + at, scales.sx(t) + 64 * wave_id());
-    dma4(rsw, own, (uint32_t)(p.n0 * 4) + at, scales.sw(t) + 64 * wave_id());
+  const uint32_t own = 4 * threadIdx.x;
+  auto load_scales = [&](int t, const Place& p) {  // all of the offset where the range is sure to be compared with it
+    dma4(rsx, (uint32_t)(p.row0 * 4) + own, 0, scales.sx(t) + 64 * wave_id());
+    dma4(rsw, (uint32_t)(p.n0 * 4) + own, 0, scales.sw(t) + 64 * wave_id());
   };
 
   DmaRows<256> ra, rw;
-  ra.init(a.panels, [&](int i) { return a.panels + DmaRows<256>::row_of(i) * (long)kRowB; }, (uint32_t)(a.T * kRowB));
-  rw.init(a.w, [&](int i) { return a.w + DmaRows<256>::row_of(i) * a.d; });
+  ra.init(a.panels, [&](int i) { return a.panels + DmaRows<256>::row_of(i) * (long)kRowB; }, (uint32_t)(rows * kRowB));
+  rw.init(a.w, [&](int i) {
+    const int m = DmaRows<256>::row_of(i), c = DmaRows<256>::chunk_of(m);
+    return a.w + m * a.d + int8_chunk_at(c, a.d) - 16 * c;  // (init adds 16 c)
+  });
   FragReader<256> rd;
   rd.init_rows();
   i32x16_t acc[4][4];
@@ -206,7 +209,7 @@ __global__ __launch_bounds__(kThreads, 1) void int8_tile_kernel(Int8Args a, int 
         ra.rs = cur ? now.x : next.x;
         rw.rs = cur ? now.w : next.w;
         ra.issue(s, da);
-        rw.issue(min((long)s, w_last), db);
+        rw.issue(0, int8_stage_at(s, a.d), db);
       },
       [&](const char* slot, FragsRows<256>& f) { rd.read_rows(slot, f); },
       [&](const FragsRows<256>& f) {
@@ -358,10 +361,10 @@ bool int8_tiles(int64_t T, int64_t d, int64_t V) {
   const int64_t tile = rounds(((T + 255) / 256) * ((V + 255) / 256)), few = rounds(((T + 127) / 128) * ((V + 63) / 64));
   return T > 64 && 7 * few > 12 * tile;
 }
-int64_t int8_panel_bytes(int64_t T, int64_t d) { return T * ((d + kKTurn - 1) / kKTurn * kKTurn); }
+int64_t int8_panel_bytes(int64_t T, int64_t d) { return int8_panel_rows(T) * int8_turns(d) * kInt8Turn; }
 
 hipError_t launch_int8_panels(const Int8Args& a, hipStream_t st) {
-  const long chunks = (a.d + kKTurn - 1) / kKTurn * kKTurn / 16;
+  const long chunks = int8_turns(a.d) * kInt8Turn / 16;
   const long blocks = std::min<long>((a.T * chunks + 255) / 256, 8192);
   hipLaunchKernelGGL(int8_panels_kernel, dim3((unsigned)blocks), dim3(256), 0, st, a.x, (long)a.T, (long)a.d, chunks,
                      a.panels);

@@ -127,7 +127,7 @@ struct Int8Args {
   int64_t T, d, V;
   int out_type;
   char* out;
-  char* panels;  // workspace: x in panels, whole ring turns
+  char* panels;  // workspace: x in panels of whole row blocks, whole ring turns
 };
 bool int8_tiles(int64_t T, int64_t d, int64_t V);  // whether the tile kernel takes the call
 int64_t int8_panel_bytes(int64_t T, int64_t d);

@@ -121,7 +121,7 @@ size_t norm_bytes(int64_t T, int64_t d) { return up((size_t)kd::norm_grad_blocks
 // ------------------------------------------------------------------ 8-bit integers
 // Rows of one launch of the tiles: their panels stay below 1 GiB.
 int64_t int8_rows(int64_t T, int64_t d) {
-  const int64_t most = std::max<int64_t>((int64_t(1) << 30) / kd::int8_panel_bytes(1, d) / 256 * 256, 256);
+  const int64_t most = std::max<int64_t>((int64_t(1) << 30) / kd::int8_panel_bytes(256, d) * 256, 256);
   return std::min(T, most);
 }
 
