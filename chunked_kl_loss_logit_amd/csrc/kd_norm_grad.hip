@@ -96,8 +96,9 @@ __global__ __launch_bounds__(RowTeam<R>::kThreads, K > 1 && R == 64 ? 3 : 4) voi
   Input<TY, KIND> xr[K], xn[K];
   Raw8<TY> gr[K], gn[K];
   float mean = 0.f, rstd = 0.f;
+  bool there = false;
   auto load = [&](int64_t row) {  // masked rows and those behind the last one as zeros
-    const bool there = row < a.T && row_valid(a.mask, row);
+    there = row < a.T && row_valid(a.mask, row);
     mean = there ? a.mean[row] : 0.f;
     rstd = there ? a.rstd[row] : 0.f;
 #pragma unroll
@@ -108,11 +109,25 @@ __global__ __launch_bounds__(RowTeam<R>::kThreads, K > 1 && R == 64 ? 3 : 4) voi
       gn[k] = load8<TY, WHOLE>(a.grad + (row * a.d + 8 * (int64_t)p) * Elem<TY>::kBytes, n, p > 0);
     }
   };
+  // A masked row's dx: as its grad counts as 0, it comes out 0 by itself unless a weight is not finite.  Rows of
+  // several waves are cleared instead of worked on; where a workgroup has several rows, a branch in the loop took 130 ->
+  // 148 us (400000 x 136 bf16, a tenth masked; 120000 x 520 197 -> 208), so that they are cleared after it, for such
+  // weights only.
+  auto clear = [&](int64_t row) {
+    const float zero[8] = {};
+    if (a.dx)
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const int64_t at = 8 * (int64_t)(lane + k * R);
+        store8<TY, WHOLE>(a.dx + (row * a.d + at) * Elem<TY>::kBytes, zero, (int)(a.d - at));
+      }
+  };
   if constexpr (kAhead) load(t);
   for (; t < a.T; t += step) {
     if constexpr (!kAhead) load(t);
     char* out = a.dx ? a.dx + t * a.d * Elem<TY>::kBytes : nullptr;
     const float m = mean, r = rstd;
+    const bool valid = there;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int p = lane + k * R, n = (int)(a.d - 8 * (int64_t)p);
@@ -122,6 +137,10 @@ __global__ __launch_bounds__(RowTeam<R>::kThreads, K > 1 && R == 64 ? 3 : 4) voi
       settle8<TY, WHOLE>(gr[k], n, p > 0);
     }
     if constexpr (kAhead) load(t + step);  // the next row, while this one is worked on
+    if (R > 64 && !valid) {
+      clear(t);
+      continue;
+    }
     auto weights = [&](int k) {
       if constexpr (kLds) {
 #pragma unroll
@@ -166,6 +185,18 @@ __global__ __launch_bounds__(RowTeam<R>::kThreads, K > 1 && R == 64 ? 3 : 4) voi
       for (int i = 0; i < 8; ++i) g[i] = r * fmaf(-h[i], c1, g[i] * w[k][i] - c0);
       store8<TY, WHOLE>(out + at * Elem<TY>::kBytes, g, (int)(a.d - at));
     }
+  }
+  if constexpr (R <= 64) {  // the row's weights are among those of the wave's lanes
+    uint32_t top = 0;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      if constexpr (K > 1)
+        if (a.w) load_any(a.w, a.wtype, a.d, lane + k * R, w[k]);
+      top = max(top, top8(w[k]));
+    }
+    if (__any(top >= 0x7f800000u))
+      for (t = (int64_t)blockIdx.x * Team::kRows + Team::slot(); t < a.T; t += step)
+        if (!row_valid(a.mask, t)) clear(t);
   }
   if (!a.dw && !a.db) return;
   // one partial row of each sum per workgroup; waves that hold a row each are added up first

@@ -163,3 +163,20 @@ def test_offsets_beyond_32_bits():
         ys, ms, rs, _ = kd.layer_norm_forward(p, w)
         assert torch.equal(ys, y[a:a + 64]) and torch.equal(ms, mean[a:a + 64])
         assert torch.equal(kd.layer_norm_backward(p, p, w, None, ms, rs)[0], dx[a:a + 64])
+
+
+@pytest.mark.parametrize("kept", [None, "int8"])
+@pytest.mark.parametrize("d", [72, 1000, 2048, 9216, 16385])
+def test_masked_rows_get_no_gradient_whatever_the_weight_holds(d, kept):
+    T = 9
+    for dtype in R.TYPES:
+        say(f"layer norm {dtype} d={d} kept={kept}")
+        x, mask = R.make_rows(T, d, dtype, d, masked=0.4)
+        x, mask = x.cuda(), mask.cuda()
+        w = torch.ones(d, dtype=dtype, device="cuda")
+        w[d // 2], w[d - 1] = float("inf"), float("nan")
+        y, mean, rstd, k = kd.layer_norm_forward(x, w, None, mask, checkpoint=kept)
+        dx, dw, db = kd.layer_norm_backward(torch.randn(T, d, device="cuda").to(dtype), None if k else x, w, mask, mean, rstd, k)
+        off = mask == 0
+        assert bool((y[off] == 0).all()) and bool((dx[off] == 0).all())
+        assert bool(dx[~off].isnan().all()) and bool(dw.isfinite().all()) and bool(db.isfinite().all())
