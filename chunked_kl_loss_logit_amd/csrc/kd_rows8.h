@@ -46,7 +46,11 @@ struct Scale8 {
 // The quotient by 127 or 448 is rounded correctly: the residual of the first
 // product is exact, the correction's own error is 2^-24 of an ulp, and a
 // 24-bit number over 127 or 7 is never nearer than 1/254 ulp to the middle of
-// two numbers.
+// two numbers.  But for scales below the normal range, whose steps are wider:
+// 448 of them are as many whole steps as 24 bits hold, so a largest value can lie
+// 224 of float32's smallest steps from both neighbours, and its even one is
+// taken.  (Only float32 values: those of 16 bits are multiples of 2^16 such steps.
+// Over 127, no value lies in the middle.)
 template <int KIND, bool SHORT>
 __device__ inline Scale8 scale8(uint32_t top) {
   constexpr float most = KIND == kRowsInt8 ? 127.f : 448.f, part = 1.f / most;
@@ -54,6 +58,11 @@ __device__ inline Scale8 scale8(uint32_t top) {
   Scale8 r;
   const float q = x * part;
   r.scale = fmaf(fmaf(-q, most, x), part, q);
+  if constexpr (KIND == kRowsE4m3 && !SHORT) {
+    const float left = fmaf(-r.scale, most, x);
+    const uint32_t u = __float_as_uint(r.scale);
+    if (fabsf(left) == 0x1.cp-142f && (u & 1)) r.scale = __uint_as_float(left > 0.f ? u + 1 : u - 1);
+  }
   r.lift = r.scale < 0x1p-90f ? 0x1p60f : 1.f;
   r.s = r.scale * r.lift;
   r.even = false;

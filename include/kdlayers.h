@@ -70,8 +70,9 @@ kd_status kd_embedding_bwd(const void* grad, const int32_t* tokens, const uint8_
  *   KD_ROWS_E4M3   scale = max |x| / 448, q = x / scale to the nearest value
  *                  of the 8-bit format with 4 exponent and 3 significand bits
  *                  (largest 448, no infinities)
- * The scale is rounded to float32; q is the nearest to the exact quotient of x
- * and that scale, ties to even.  A group of zeros, or one whose scale rounds
+ * The scale is rounded to float32, ties to even, also below its normal range;
+ * q is the nearest to the exact quotient of x and that scale, ties to even, but
+ * no larger than 127 or 448 (where such a scale was rounded down).  A group of zeros, or one whose scale rounds
  * to 0, has scale 0 and q 0.  A group with an infinity or a NaN has scale NaN
  * and q 0: it comes back as NaN. */
 typedef enum kd_rows_kind { KD_ROWS_NONE = 0, KD_ROWS_INT8 = 1, KD_ROWS_E4M3 = 2, KD_ROWS_KIND_MAX_ENUM = 0x7fffffff } kd_rows_kind;

@@ -101,6 +101,20 @@ def test_small_large_and_not_finite(kind, group):
     compare(x.to(torch.bfloat16), kind, group)
 
 
+@pytest.mark.parametrize("group", [0, 32])
+def test_scales_below_the_normal_range(group):
+    """448 j + 224 smallest steps of float32: a scale in the middle of two, whose even one it has to be."""
+    j = torch.cat([torch.arange(0, 40), torch.randint(0, 1 << 16, (200,), generator=R.gen(1)), torch.arange((1 << 23) - 9, (1 << 23) + 9)])
+    k = (448 * j + 224).double()
+    k = torch.cat([k, k + 1, k - 1, k + 224])
+    k = k[k == k.float().double()]
+    say(f"rows e4m3 group={group}: {len(k)} scales")
+    x = (k[:, None] * torch.linspace(1, -1, 32, dtype=torch.float64) * 2.0 ** -149).float()
+    assert bool((x[:, 0].double() == k * 2.0 ** -149).all())
+    for kind in ("e4m3", "int8"):
+        compare(x, kind, group)
+
+
 def test_every_value_of_a_16_bit_type():
     """All finite bfloat16 and float16 values with a scale each."""
     for dtype in (torch.bfloat16, torch.float16):
