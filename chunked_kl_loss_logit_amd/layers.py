@@ -18,8 +18,11 @@ outputs and workspaces with torch.
 """
 from __future__ import annotations
 
+import contextlib
+
 import torch
 from torch.autograd.function import once_differentiable
+from torch.utils._python_dispatch import TorchDispatchMode
 
 from . import _layers_binding as B
 from .policy import _f32, _workspace
@@ -101,11 +104,63 @@ def _rows(x):
     return x.detach().contiguous().reshape(-1, x.shape[-1])
 
 
+def _capturing():
+    return torch.cuda.is_initialized() and torch.cuda.is_current_stream_capturing()
+
+
+class _NoDraws(TorchDispatchMode):
+    """Refuses operations that draw random numbers."""
+
+    def __torch_dispatch__(self, func, types, args=(), kwargs=None):
+        kwargs = kwargs or {}
+        if torch.Tag.nondeterministic_seeded in func.tags:
+            names = func._schema.arguments
+            given = {a.name: a.default_value for a in names} | dict(zip((a.name for a in names), args)) | kwargs
+            if given.get("dropout_p") != 0:  # (attention draws nothing then)
+                raise RuntimeError(f"fn must not draw random numbers ({func}) in a captured graph: its random states can be "
+                                   "neither read nor set, and the backward pass has to draw the same ones")
+        return func(*args, **kwargs)
+
+
+class _Surroundings:
+    """What fn's result hangs on beside its arguments, as it is before the forward pass: the random states."""
+
+    def __init__(self, others):
+        self.states = [] if _capturing() else self._states(
+            [torch.default_generator, *(torch.cuda.default_generators if torch.cuda.is_initialized() else ()),
+             *(g for g in others if isinstance(g, torch.Generator))])
+
+    @staticmethod
+    def _states(generators):
+        return [(g, g.get_state()) for g in generators]
+
+    @staticmethod
+    def _set(states):
+        for g, state in states:
+            g.set_state(state)
+
+    def first(self):
+        return _NoDraws() if _capturing() else contextlib.nullcontext()
+
+    @contextlib.contextmanager
+    def again(self):
+        """As it was then; afterwards as it is now."""
+        with contextlib.ExitStack() as stack:
+            if _capturing():
+                stack.enter_context(_NoDraws())
+            else:
+                stack.callback(self._set, self._states([g for g, _ in self.states]))
+                self._set(self.states)
+            yield
+
+
 class _Checkpoint(torch.autograd.Function):
     @staticmethod
     def forward(ctx, fn, kind, group, x, *others):
         before = [t._version for t in (x, *others) if isinstance(t, torch.Tensor)]
-        out = fn(x, *others)
+        ctx.surroundings = _Surroundings(others)
+        with ctx.surroundings.first():
+            out = fn(x, *others)
         if before != [t._version for t in (x, *others) if isinstance(t, torch.Tensor)]:
             raise RuntimeError("fn must not change its arguments in place: the backward pass runs it again on them")
         out = tuple(out) if isinstance(out, list) else out
@@ -128,7 +183,7 @@ class _Checkpoint(torch.autograd.Function):
         need = ctx.needs_input_grad[3:]
         args = [t.detach().requires_grad_(n) if isinstance(t, torch.Tensor) else p
                 for t, p, n in zip([x, *others], [None, *ctx.plain], need)]
-        with torch.enable_grad():
+        with torch.enable_grad(), ctx.surroundings.again():
             out = ctx.fn(*args)
         out = [out] if isinstance(out, torch.Tensor) else list(out)
         pairs = [(o, g) for o, g in zip(out, grads) if g is not None and isinstance(o, torch.Tensor) and o.requires_grad]
@@ -142,7 +197,8 @@ def checkpoint_8bit(fn, x, *others, kind="int8", group=128):
     of what fn computes: the backward pass runs fn again on what those 8 bits stand for, and its gradients are exactly
     the gradients there.  others (tensors or not) are kept as they are.  Tensors that fn takes from elsewhere get their
     .grad from backward(), as parameters do; torch.autograd.grad with respect to them needs them among the others.  fn
-    has to compute the same both times: random numbers and autocast belong inside it or not in it."""
+    has to compute the same both times: random numbers of torch's own generators and of generators among the others are
+    drawn again as they were (in a captured graph they are refused); others, such as numpy's, are not."""
     if not isinstance(x, torch.Tensor) or x.dim() == 0 or x.shape[-1] == 0:
         raise TypeError("x must be a tensor with a last axis of at least one element")
     if x.dtype not in B.TYPES:

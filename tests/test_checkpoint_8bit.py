@@ -1,0 +1,94 @@
+"""checkpoint_8bit's part that is torch alone, on the CPU: with the rounding to 8 bits left out, every gradient has to be
+that of the function itself."""
+import pytest
+import torch
+import torch.nn.functional as F
+
+kd = pytest.importorskip("chunked_kl_loss_logit_amd")
+L = kd.layers
+
+
+@pytest.fixture(autouse=True)
+def exact_rows(monkeypatch):
+    """x itself in the place of its 8 bits."""
+    monkeypatch.setattr(L, "quantize_rows", lambda x, kind, group: (x.clone(), torch.ones(1)))
+    monkeypatch.setattr(L, "dequantize_rows", lambda q, scale, group, dtype: q.clone())
+
+
+def leaves(*shapes):
+    g = torch.Generator().manual_seed(len(shapes))
+    return [torch.randn(*s, generator=g).requires_grad_(True) for s in shapes]
+
+
+# ------------------------------------------------------------------ random numbers
+@pytest.mark.parametrize("fn", [
+    lambda x: F.dropout(x, 0.5) * x,
+    lambda x: x * torch.rand(x.shape),
+    lambda x: [x * torch.bernoulli(torch.full(x.shape, 0.5)), x * 2][0],
+], ids=["dropout", "rand", "bernoulli"])
+def test_random_numbers_are_drawn_alike_again(fn):
+    (x,) = leaves((64, 32))
+    torch.manual_seed(3)
+    y = kd.checkpoint_8bit(fn, x)
+    after = torch.get_rng_state()
+    torch.rand(5)  # what is drawn between the two passes
+    between = torch.get_rng_state()
+    (dx,) = torch.autograd.grad(y.sum(), x)
+    assert torch.equal(torch.get_rng_state(), between), "the backward pass moved the random state"
+    torch.manual_seed(3)
+    want = fn(x)
+    assert torch.equal(y, want) and torch.equal(torch.get_rng_state(), after)
+    assert torch.equal(dx, torch.autograd.grad(want.sum(), x)[0])
+
+
+def test_random_numbers_drawn_aside_and_from_a_generator_of_its_own():
+    (x,) = leaves((64, 32))
+
+    def aside(x):  # the state is the same before and after
+        with torch.random.fork_rng(devices=[]):
+            return F.dropout(x, 0.5) * x
+
+    def own(x, g):
+        return x * x * torch.rand(x.shape, generator=g)
+
+    for fn, others in ((aside, ()), (own, (torch.Generator().manual_seed(7),))):
+        torch.manual_seed(3)
+        y = kd.checkpoint_8bit(fn, x, *others)
+        torch.rand(5)
+        for g in others:
+            torch.rand(5, generator=g)
+        (dx,) = torch.autograd.grad(y.sum(), x)
+        torch.manual_seed(3)
+        want = fn(x, *(g.manual_seed(7) for g in others))
+        assert torch.equal(y, want) and torch.equal(dx, torch.autograd.grad(want.sum(), x)[0])
+
+
+def test_random_state_comes_back_after_an_error():
+    (x,) = leaves((4, 8))
+    runs = []
+
+    def fn(x):
+        runs.append(torch.rand(()).item())
+        if len(runs) > 1:
+            raise KeyError("again")
+        return x * 2
+
+    y = kd.checkpoint_8bit(fn, x)
+    torch.rand(3)
+    state = torch.get_rng_state()
+    with pytest.raises(KeyError):
+        y.sum().backward()
+    assert runs[0] == runs[1] and torch.equal(torch.get_rng_state(), state)
+
+
+def test_random_numbers_in_a_captured_graph_are_refused(monkeypatch):
+    """The states of a graph under capture can be neither read nor set."""
+    x, q = leaves((4, 8), (1, 2, 4, 8))
+    monkeypatch.setattr(L, "_capturing", lambda: True)
+    for fn in (lambda x: F.dropout(x, 0.5), lambda x: x * torch.rand(x.shape), lambda x: x * torch.randn_like(x)):
+        with pytest.raises(RuntimeError, match="random numbers"):
+            kd.checkpoint_8bit(fn, x)
+    for fn, t in ((lambda x: torch.tanh(x) + F.dropout(x, 0.5, training=False), x),
+                  (lambda q: F.scaled_dot_product_attention(q, q, q, dropout_p=0.0), q)):
+        y = kd.checkpoint_8bit(fn, t)
+        assert torch.equal(torch.autograd.grad(y.sum(), t)[0], torch.autograd.grad(fn(t).sum(), t)[0])

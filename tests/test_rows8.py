@@ -201,3 +201,45 @@ def test_checkpoint_refuses_what_changed_since():
         y.sum().backward()
     with pytest.raises(TypeError, match="last axis"):
         kd.checkpoint_8bit(abs, torch.ones(3, 0))
+
+
+def test_checkpoint_draws_the_same_random_numbers_again():
+    x = torch.randn(64, 256, device="cuda", requires_grad=True)
+    fn = lambda x: torch.nn.functional.dropout(x, 0.5) * 3  # noqa: E731
+    torch.manual_seed(5)
+    y = kd.checkpoint_8bit(fn, x)
+    torch.rand(7, device="cuda")
+    state = torch.cuda.get_rng_state()
+    (dx,) = torch.autograd.grad(y.sum(), x)
+    assert torch.equal(torch.cuda.get_rng_state(), state)
+    assert torch.equal(dx != 0, y != 0) and 0.4 < (y != 0).float().mean() < 0.6
+
+
+def test_checkpoint_in_a_captured_graph():
+    """Forward and backward captured together; a function that draws random numbers is refused there."""
+    say("checkpoint_8bit captured")
+    x, up = torch.randn(64, 256, device="cuda"), torch.randn(64, 256, device="cuda")
+    fn = lambda x: torch.tanh(x) * x  # noqa: E731
+
+    def step():
+        leaf = x.detach().requires_grad_(True)
+        y = kd.checkpoint_8bit(fn, leaf, kind="e4m3", group=32)
+        return torch.autograd.grad(y, leaf, up)[0]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        with pytest.raises(RuntimeError, match="random numbers"):
+            kd.checkpoint_8bit(lambda x: torch.nn.functional.dropout(x, 0.5), x.detach().requires_grad_(True))
+        dx = step()
+    for _ in range(3):
+        x.normal_()
+        graph.replay()
+        got = dx.clone()
+        torch.cuda.synchronize()
+        assert torch.equal(got, step())
