@@ -123,9 +123,12 @@ class _NoDraws(TorchDispatchMode):
 
 
 class _Surroundings:
-    """What fn's result hangs on beside its arguments, as it is before the forward pass: the random states."""
+    """What fn's result hangs on beside its arguments, as it is before the forward pass: autocast and the random
+    states."""
 
-    def __init__(self, others):
+    def __init__(self, x, others):
+        self.autocast = [dict(device_type=d, dtype=torch.get_autocast_dtype(d), enabled=torch.is_autocast_enabled(d),
+                              cache_enabled=torch.is_autocast_cache_enabled()) for d in {x.device.type, "cpu"}]
         self.states = [] if _capturing() else self._states(
             [torch.default_generator, *(torch.cuda.default_generators if torch.cuda.is_initialized() else ()),
              *(g for g in others if isinstance(g, torch.Generator))])
@@ -139,13 +142,21 @@ class _Surroundings:
         for g, state in states:
             g.set_state(state)
 
-    def first(self):
-        return _NoDraws() if _capturing() else contextlib.nullcontext()
+    @staticmethod
+    @contextlib.contextmanager
+    def first():
+        try:
+            with _NoDraws() if _capturing() else contextlib.nullcontext():
+                yield
+        finally:  # casts that autocast remembers from here, where nothing is recorded, would have no gradient elsewhere
+            torch.clear_autocast_cache()
 
     @contextlib.contextmanager
     def again(self):
         """As it was then; afterwards as it is now."""
         with contextlib.ExitStack() as stack:
+            for settings in self.autocast:
+                stack.enter_context(torch.autocast(**settings))
             if _capturing():
                 stack.enter_context(_NoDraws())
             else:
@@ -158,7 +169,7 @@ class _Checkpoint(torch.autograd.Function):
     @staticmethod
     def forward(ctx, fn, kind, group, x, *others):
         before = [t._version for t in (x, *others) if isinstance(t, torch.Tensor)]
-        ctx.surroundings = _Surroundings(others)
+        ctx.surroundings = _Surroundings(x, others)
         with ctx.surroundings.first():
             out = fn(x, *others)
         if before != [t._version for t in (x, *others) if isinstance(t, torch.Tensor)]:
@@ -197,7 +208,7 @@ def checkpoint_8bit(fn, x, *others, kind="int8", group=128):
     of what fn computes: the backward pass runs fn again on what those 8 bits stand for, and its gradients are exactly
     the gradients there.  others (tensors or not) are kept as they are.  Tensors that fn takes from elsewhere get their
     .grad from backward(), as parameters do; torch.autograd.grad with respect to them needs them among the others.  fn
-    has to compute the same both times: random numbers of torch's own generators and of generators among the others are
+    has to compute the same both times: it runs under the autocast of the forward pass again, and random numbers of torch's own generators and of generators among the others are
     drawn again as they were (in a captured graph they are refused); others, such as numpy's, are not."""
     if not isinstance(x, torch.Tensor) or x.dim() == 0 or x.shape[-1] == 0:
         raise TypeError("x must be a tensor with a last axis of at least one element")

@@ -92,3 +92,56 @@ def test_random_numbers_in_a_captured_graph_are_refused(monkeypatch):
                   (lambda q: F.scaled_dot_product_attention(q, q, q, dropout_p=0.0), q)):
         y = kd.checkpoint_8bit(fn, t)
         assert torch.equal(torch.autograd.grad(y.sum(), t)[0], torch.autograd.grad(fn(t).sum(), t)[0])
+
+
+# ------------------------------------------------------------------ autocast
+def seen(into):
+    def fn(x, w):
+        y = x @ w
+        into.append((y.dtype, torch.is_autocast_enabled("cpu"), torch.is_autocast_cache_enabled()))
+        return y
+    return fn
+
+
+@pytest.mark.parametrize("inside", [True, False], ids=["backward inside", "backward outside"])
+@pytest.mark.parametrize("cache", [True, False])
+def test_autocast_is_the_same_both_times(inside, cache):
+    x, w = leaves((4, 8), (8, 8))
+    types = []
+    with torch.autocast("cpu", torch.bfloat16, cache_enabled=cache):
+        y = kd.checkpoint_8bit(seen(types), x, w)
+        if inside:
+            got = torch.autograd.grad(y.float().sum(), (x, w))
+        want = torch.autograd.grad((x @ w).float().sum(), (x, w))
+    if not inside:
+        got = torch.autograd.grad(y.float().sum(), (x, w))
+    assert types == [(torch.bfloat16, True, cache)] * 2
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_autocast_of_the_backward_pass_is_not_the_functions():
+    x, w = leaves((4, 8), (8, 8))
+    types = []
+    y = kd.checkpoint_8bit(seen(types), x, w)
+    with torch.autocast("cpu", torch.bfloat16):
+        y.sum().backward()
+    assert [t[:2] for t in types] == [(torch.float32, False)] * 2
+
+
+@pytest.mark.parametrize("around", [True, False])
+def test_a_weight_used_before_and_behind_under_autocast_keeps_its_gradient(around):
+    """Autocast remembers the casts of leaves: one made while nothing is recorded has no gradient."""
+    g = torch.Generator().manual_seed(1)  # small whole numbers: nothing is rounded
+    x, w = (torch.randint(-3, 4, s, generator=g).float().requires_grad_(True) for s in ((4, 8), (8, 8)))
+
+    def fn(x):
+        with torch.autocast("cpu", torch.bfloat16):
+            return x @ w
+
+    with torch.autocast("cpu", torch.bfloat16, enabled=around):
+        y = kd.checkpoint_8bit(fn, x)
+        with torch.autocast("cpu", torch.bfloat16):
+            z = x @ w
+        (y.float().sum() + 2 * z.float().sum()).backward()
+        dx, dw = torch.autograd.grad(3 * fn(x).float().sum(), (x, w))
+    assert torch.equal(w.grad, dw) and torch.equal(x.grad, dx)

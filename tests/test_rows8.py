@@ -243,3 +243,17 @@ def test_checkpoint_in_a_captured_graph():
         got = dx.clone()
         torch.cuda.synchronize()
         assert torch.equal(got, step())
+
+
+def test_checkpoint_runs_again_under_the_same_autocast():
+    x, w = (torch.randn(64, 64, device="cuda", requires_grad=True) for _ in range(2))
+    types = []
+
+    def fn(x):
+        types.append((x @ w).dtype)
+        return x @ w
+
+    with torch.autocast("cuda", torch.bfloat16):
+        y = kd.checkpoint_8bit(fn, x, kind="e4m3", group=32)
+    y.float().sum().backward()
+    assert types == [torch.bfloat16] * 2 and x.grad.dtype == w.grad.dtype == torch.float32
