@@ -165,6 +165,40 @@ class _Surroundings:
             yield
 
 
+def _graph(nodes):
+    """The nodes that lie behind some of autograd's."""
+    stack, seen = list(nodes), set()
+    while stack:
+        node = stack.pop()
+        if node is not None and node not in seen:
+            seen.add(node)
+            stack += [n for n, _ in node.next_functions]
+    return seen
+
+
+def _runs(node):
+    """Whether the running backward pass comes to a node; None if torch.autograd.grad asks for that leaf's gradient."""
+    try:
+        return torch._C._will_engine_execute_node(node)
+    except RuntimeError:
+        return None
+
+
+def _check_asked(ctx, out, own):
+    """Under torch.autograd.grad and backward(inputs=...): fn's tensors from elsewhere must not be among those asked for,
+    whose gradients would lack fn's share."""
+    leaf = "torch::autograd::AccumulateGrad"
+    edge = torch.autograd.graph.get_gradient_edge
+    nodes = _graph(edge(o).node for o in out) - {edge(t).node for t in own}
+    asked = any(_runs(n) is not False for n in nodes)
+    if not asked and any(n.name() == leaf for n in nodes):
+        # backward(inputs=...) does not say which leaves it is for unless its own graph leads to them
+        asked = any(n.name() == leaf and _runs(n) for n in _graph([ctx]))
+    if asked:
+        raise RuntimeError("fn takes a tensor from elsewhere whose gradient may be asked for: torch.autograd.grad and "
+                           "backward(inputs=...) reach x and the others alone, so it has to be among the others")
+
+
 class _Checkpoint(torch.autograd.Function):
     @staticmethod
     def forward(ctx, fn, kind, group, x, *others):
@@ -198,18 +232,33 @@ class _Checkpoint(torch.autograd.Function):
             out = ctx.fn(*args)
         out = [out] if isinstance(out, torch.Tensor) else list(out)
         pairs = [(o, g) for o, g in zip(out, grads) if g is not None and isinstance(o, torch.Tensor) and o.requires_grad]
+        own = [a for a, n in zip(args, need) if n]
+        got = [None] * len(own)
         if pairs:
-            torch.autograd.backward([o for o, _ in pairs], [g for _, g in pairs])
-        return (None, None, None, *(a.grad if isinstance(a, torch.Tensor) and n else None for a, n in zip(args, need)))
+            out, up = zip(*pairs)
+            if torch.autograd.Variable._execution_engine.is_checkpoint_valid():  # backward() for all leaves
+                torch.autograd.backward(out, up)
+                got = [a.grad for a in own]
+            else:
+                _check_asked(ctx, out, own)
+                got = torch.autograd.grad(out, own, up, allow_unused=True)
+        got = iter(got)
+        return (None, None, None, *(next(got) if n else None for n in need))
 
 
 def checkpoint_8bit(fn, x, *others, kind="int8", group=128):
     """fn(x, *others), keeping x in 8 bits for the backward pass (any shape, groups along the last axis) and nothing
     of what fn computes: the backward pass runs fn again on what those 8 bits stand for, and its gradients are exactly
-    the gradients there.  others (tensors or not) are kept as they are.  Tensors that fn takes from elsewhere get their
-    .grad from backward(), as parameters do; torch.autograd.grad with respect to them needs them among the others.  fn
-    has to compute the same both times: it runs under the autocast of the forward pass again, and random numbers of torch's own generators and of generators among the others are
-    drawn again as they were (in a captured graph they are refused); others, such as numpy's, are not."""
+    the gradients there.  others (tensors or not) are kept as they are.
+
+    Leaves that fn takes from elsewhere, such as a module's parameters, get their .grad from backward(); tensors that were
+    computed with a gradient belong among the others.  torch.autograd.grad and backward(inputs=...) reach x and the others
+    only, and are refused where they may have been asked for a tensor from elsewhere.  What fn takes from elsewhere must
+    not change in between.
+
+    fn has to compute the same both times: it runs under the autocast of the forward pass again, and random numbers of
+    torch's own generators and of generators among the others are drawn again as they were (in a captured graph they are
+    refused); others, such as numpy's, are not."""
     if not isinstance(x, torch.Tensor) or x.dim() == 0 or x.shape[-1] == 0:
         raise TypeError("x must be a tensor with a last axis of at least one element")
     if x.dtype not in B.TYPES:

@@ -145,3 +145,56 @@ def test_a_weight_used_before_and_behind_under_autocast_keeps_its_gradient(aroun
         (y.float().sum() + 2 * z.float().sum()).backward()
         dx, dw = torch.autograd.grad(3 * fn(x).float().sum(), (x, w))
     assert torch.equal(w.grad, dw) and torch.equal(x.grad, dx)
+
+
+# ------------------------------------------------------------------ tensors from elsewhere
+def test_gradients_asked_for_by_name_leave_the_others_alone():
+    x, w, v = leaves((4, 8), (8, 8), (8, 8))
+    fn = lambda x, v: torch.tanh(x @ w) @ v  # noqa: E731
+    y = kd.checkpoint_8bit(fn, x, v)
+    want = torch.autograd.grad(fn(x, v).sum(), (x, v, w))
+    got = torch.autograd.grad(y.sum(), (x, v), retain_graph=True)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert torch.equal(torch.autograd.grad(y.sum(), x, retain_graph=True)[0], want[0])
+    assert x.grad is None and v.grad is None and w.grad is None
+    y.sum().backward()
+    assert all(torch.equal(t.grad, g) for t, g in zip((x, v, w), want))
+
+
+def test_a_checkpoint_in_a_checkpoint():
+    x, w, v = leaves((4, 8), (8, 8), (8, 8))
+    inner = lambda x: torch.tanh(x @ w)  # noqa: E731
+    y = kd.checkpoint_8bit(lambda x, v: kd.checkpoint_8bit(inner, x @ v) @ v, x, v)
+    want = torch.autograd.grad((inner(x @ v) @ v).sum(), (x, v, w))
+    got = torch.autograd.grad(y.sum(), (x, v), retain_graph=True)
+    assert all(torch.equal(a, b) for a, b in zip(got, want)) and w.grad is None
+    y.sum().backward()
+    assert all(torch.equal(t.grad, g) for t, g in zip((x, v, w), want))
+
+
+def test_tensors_from_elsewhere_that_are_asked_for_are_refused():
+    x, w = leaves((4, 8), (8, 8))
+    y = kd.checkpoint_8bit(lambda x: x @ w, x)
+    for inputs in ([x, w], [x]):  # which of the two it is, the backward pass does not see
+        with pytest.raises(RuntimeError, match="among the others"):
+            y.sum().backward(inputs=inputs, retain_graph=True)
+    with pytest.raises(RuntimeError, match="among the others"):  # w also has a use that torch knows of
+        torch.autograd.grad(y.sum() + w.sum(), (x, w), retain_graph=True)
+    h = w * 2
+    z = kd.checkpoint_8bit(lambda x: x @ h, x)
+    with pytest.raises(RuntimeError, match="among the others"):
+        torch.autograd.grad(z.sum() + h.sum(), (x, h), retain_graph=True)
+    assert w.grad is None and x.grad is None
+    f = w.detach()
+    kd.checkpoint_8bit(lambda x: x @ f, x).sum().backward(inputs=[x])  # nothing else there
+    assert torch.equal(x.grad, torch.autograd.grad((x @ f).sum(), x)[0])
+
+
+def test_a_computed_tensor_among_the_others():
+    x, w = leaves((4, 8), (8, 8))
+    h = torch.tanh(w)
+    y = kd.checkpoint_8bit(lambda x, h: x @ h, x, h) + kd.checkpoint_8bit(lambda x, h: x * h[:4], x, h)
+    want = torch.autograd.grad((x @ h + x * h[:4]).sum() + (h * h).sum(), (x, w), retain_graph=True)
+    (y.sum() + (h * h).sum()).backward()
+    assert torch.equal(x.grad, want[0])
+    torch.testing.assert_close(w.grad, want[1], rtol=0, atol=16 * 2.0 ** -24 * 40)  # a sum of 3 shares below 40, in another order
