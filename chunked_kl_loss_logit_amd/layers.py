@@ -201,16 +201,18 @@ def _check_asked(ctx, out, own):
 
 class _Checkpoint(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, fn, kind, group, x, *others):
+    def forward(ctx, fn, kind, group, form, x, *others):
         before = [t._version for t in (x, *others) if isinstance(t, torch.Tensor)]
         ctx.surroundings = _Surroundings(x, others)
         with ctx.surroundings.first():
             out = fn(x, *others)
         if before != [t._version for t in (x, *others) if isinstance(t, torch.Tensor)]:
             raise RuntimeError("fn must not change its arguments in place: the backward pass runs it again on them")
-        out = tuple(out) if isinstance(out, list) else out
-        for o in out if isinstance(out, tuple) else (out,):
-            if isinstance(o, (tuple, list, dict, set)):  # what they hold would have no gradient
+        if isinstance(out, (tuple, list)):
+            form.append(tuple if isinstance(out, list) else getattr(out, "_make", type(out)))
+            out = tuple(out)
+        for o in out if form else (out,):
+            if not isinstance(o, (torch.Tensor, int, float, complex, str, type(None))):  # whose tensors would have no gradient
                 raise TypeError(f"fn must return a tensor, or a tuple or list of them, got a {type(o).__name__} in its place")
         q, scale = quantize_rows(_rows(x), kind, group)
         tensors = [t if isinstance(t, torch.Tensor) else None for t in others]
@@ -225,7 +227,7 @@ class _Checkpoint(torch.autograd.Function):
     def backward(ctx, *grads):
         q, scale, *others = ctx.saved_tensors
         x = dequantize_rows(q, scale, ctx.group, ctx.dtype).reshape(ctx.shape)
-        need = ctx.needs_input_grad[3:]
+        need = ctx.needs_input_grad[4:]
         args = [t.detach().requires_grad_(n) if isinstance(t, torch.Tensor) else p
                 for t, p, n in zip([x, *others], [None, *ctx.plain], need)]
         with torch.enable_grad(), ctx.surroundings.again():
@@ -243,7 +245,7 @@ class _Checkpoint(torch.autograd.Function):
                 _check_asked(ctx, out, own)
                 got = torch.autograd.grad(out, own, up, allow_unused=True)
         got = iter(got)
-        return (None, None, None, *(next(got) if n else None for n in need))
+        return (None, None, None, None, *(next(got) if n else None for n in need))
 
 
 def checkpoint_8bit(fn, x, *others, kind="int8", group=128):
@@ -266,7 +268,9 @@ def checkpoint_8bit(fn, x, *others, kind="int8", group=128):
     B._kind(kind, group)
     if not torch.is_grad_enabled() or not any(isinstance(t, torch.Tensor) and t.requires_grad for t in (x, *others)):
         return fn(x, *others)  # nothing of it is kept, or only what fn takes from elsewhere needs it
-    return _Checkpoint.apply(fn, kind, int(group), x, *others)
+    form = []  # of a tuple that fn returns, a named one for instance
+    out = _Checkpoint.apply(fn, kind, int(group), form, x, *others)
+    return form[0](out) if form else out
 
 
 # ---------------------------------------------------------------- layer norm

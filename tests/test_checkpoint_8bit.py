@@ -1,5 +1,8 @@
 """checkpoint_8bit's part that is torch alone, on the CPU: with the rounding to 8 bits left out, every gradient has to be
 that of the function itself."""
+import collections
+import dataclasses
+
 import pytest
 import torch
 import torch.nn.functional as F
@@ -198,3 +201,33 @@ def test_a_computed_tensor_among_the_others():
     (y.sum() + (h * h).sum()).backward()
     assert torch.equal(x.grad, want[0])
     torch.testing.assert_close(w.grad, want[1], rtol=0, atol=16 * 2.0 ** -24 * 40)  # a sum of 3 shares below 40, in another order
+
+
+# ------------------------------------------------------------------ what fn returns
+Pair = collections.namedtuple("Pair", "y z")
+
+
+@dataclasses.dataclass
+class Held:
+    y: torch.Tensor
+
+
+def test_outputs_that_hold_tensors_are_refused():
+    (x,) = leaves((4, 8))
+    for fn, name in ((lambda x: Held(x * 2), "Held"), (lambda x: (x, Held(x * 2)), "Held"), (lambda x: {"y": x}, "dict"),
+                     (lambda x: [x, (x * 2,)], "tuple"), (lambda x: Pair(x, {1: x}), "dict"), (lambda x: (x, object()), "object")):
+        with pytest.raises(TypeError, match=f"got a {name}"):
+            kd.checkpoint_8bit(fn, x)
+
+
+def test_outputs_come_back_as_what_they_are():
+    (x,) = leaves((4, 8))
+    y = kd.checkpoint_8bit(lambda x: Pair(x * 2, x.sum(0)), x)
+    assert type(y) is Pair and torch.equal(torch.autograd.grad(y.z.sum() + y.y.sum(), x)[0], torch.full((4, 8), 3.0))
+    y = kd.checkpoint_8bit(lambda x: torch.max(x, 1), x)
+    assert torch.equal(y.indices, x.argmax(1)) and y.values.requires_grad
+    assert torch.equal(torch.autograd.grad(y.values.sum(), x)[0].argmax(1), y.indices)
+    a, none, n, s, flag = kd.checkpoint_8bit(lambda x: (x * 2, None, 3, "s", True), x)
+    assert none is None and (n, s, flag) == (3, "s", True) and a.requires_grad
+    assert type(kd.checkpoint_8bit(lambda x: (x * 2, x), x)) is tuple
+    assert kd.checkpoint_8bit(lambda x: None, x) is None and kd.checkpoint_8bit(lambda x: 3.0, x) == 3.0
