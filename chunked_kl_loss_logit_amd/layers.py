@@ -214,13 +214,17 @@ class _Checkpoint(torch.autograd.Function):
         for o in out if form else (out,):
             if not isinstance(o, (torch.Tensor, int, float, complex, str, type(None))):  # whose tensors would have no gradient
                 raise TypeError(f"fn must return a tensor, or a tuple or list of them, got a {type(o).__name__} in its place")
+        # a tensor from elsewhere must not become this function's output itself
+        given = [t for t in (x, *others) if isinstance(t, torch.Tensor)]
+        own = [o.detach() if isinstance(o, torch.Tensor) and not any(o is t for t in given) else o
+               for o in (out if form else (out,))]
         q, scale = quantize_rows(_rows(x), kind, group)
         tensors = [t if isinstance(t, torch.Tensor) else None for t in others]
         ctx.save_for_backward(q, scale, *tensors)
         ctx.fn, ctx.group, ctx.shape, ctx.dtype = fn, group, x.shape, x.dtype
         ctx.plain = [None if isinstance(t, torch.Tensor) else t for t in others]
         ctx.set_materialize_grads(False)
-        return out
+        return tuple(own) if form else own[0]
 
     @staticmethod
     @once_differentiable

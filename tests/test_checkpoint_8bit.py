@@ -231,3 +231,19 @@ def test_outputs_come_back_as_what_they_are():
     assert none is None and (n, s, flag) == (3, "s", True) and a.requires_grad
     assert type(kd.checkpoint_8bit(lambda x: (x * 2, x), x)) is tuple
     assert kd.checkpoint_8bit(lambda x: None, x) is None and kd.checkpoint_8bit(lambda x: 3.0, x) == 3.0
+
+
+def test_tensors_from_elsewhere_that_are_returned_stay_what_they_are():
+    x, w = leaves((4, 8), (8, 8))
+    buffer, h = torch.ones(3), w * 2
+    y, a, b, c = kd.checkpoint_8bit(lambda x: (x @ w, w, buffer, h), x)
+    assert w.is_leaf and w.grad_fn is None and not buffer.requires_grad and h.grad_fn.name() == "MulBackward0"
+    assert torch.equal(a, w) and torch.equal(b, buffer) and torch.equal(c, h)
+    want = torch.autograd.grad((x @ w).sum() + (w * w).sum(), (x, w))
+    (y.sum() + (a * w.detach()).sum() * 2).backward()
+    assert torch.equal(x.grad, want[0])
+    torch.testing.assert_close(w.grad, want[1], rtol=2.0 ** -22, atol=2.0 ** -20)  # two shares below 16, added up once
+    x.grad = None
+    y, same = kd.checkpoint_8bit(lambda x: (x * 2, x), x)
+    (y.sum() + 3 * same.sum()).backward()
+    assert x.is_leaf and torch.equal(x.grad, torch.full((4, 8), 5.0))
