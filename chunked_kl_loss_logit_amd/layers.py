@@ -315,8 +315,7 @@ def layer_norm_backward(grad, x, weight, mask, mean, rstd, kept=None, group=128,
 class _LayerNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, bias, mask, eps, checkpoint, group):
-        need = any(ctx.needs_input_grad[:3])
-        y, mean, rstd, kept = layer_norm_forward(x, weight, bias, mask, eps, checkpoint if need else None, group)
+        y, mean, rstd, kept = layer_norm_forward(x, weight, bias, mask, eps, checkpoint, group)
         ctx.save_for_backward(x if kept is None else None, weight, mask, mean, rstd, *(kept or (None, None)))
         ctx.group, ctx.wtype = group, None if bias is None else bias.dtype
         return y
@@ -336,6 +335,9 @@ def layer_norm(x, weight=None, bias=None, mask=None, eps=1e-5, checkpoint=None, 
     from 8 bits, in groups of `group` values with a scale each, and x itself is not kept."""
     if checkpoint is not None:
         B._kind(checkpoint, group)
+        # (within apply, gradients count as on, and as needed wherever an input has one)
+        if not torch.is_grad_enabled() or not any(getattr(t, "requires_grad", False) for t in (x, weight, bias)):
+            checkpoint = None
     return _LayerNorm.apply(x, weight, bias, mask, float(eps), checkpoint, int(group))
 
 

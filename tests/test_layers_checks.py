@@ -156,3 +156,24 @@ def test_int8_matmul():
     ])
     gpu_only(lambda: kd.int8_matmul(a["x"], a["x_scale"], a["w"], a["w_scale"]))
     refused(lambda: kd.int8_matmul(z(T, 40, dtype=i8), z(T), z(V, 40, dtype=i8), z(V)), kd.KDError, "multiple of 16")
+
+
+def test_layer_norm_keeps_its_input_only_for_a_backward_pass(monkeypatch):
+    """The copy in 8 bits is a third of the forward's traffic."""
+    asked = []
+
+    def forward(x, weight, bias, mask, eps, checkpoint, group):
+        asked.append(checkpoint)
+        return x * 1, z(T), z(T), None if checkpoint is None else (x.to(i8), z(T, 1))
+
+    monkeypatch.setattr(kd.layers, "layer_norm_forward", forward)
+    x, w = z(T, D), z(D)
+    for grad, leaf, want in ((True, w, "int8"), (False, w, None), (True, x, "int8"), (False, x, None), (True, None, None)):
+        for t in (x, w):
+            t.requires_grad_(t is leaf)
+        with torch.set_grad_enabled(grad):
+            y = kd.layer_norm(x, w, checkpoint="int8")
+        assert asked.pop() == want and y.requires_grad == (want is not None)
+    with torch.inference_mode():
+        kd.layer_norm(x, w.requires_grad_(True), checkpoint="int8")
+    assert asked == [None]
