@@ -172,9 +172,6 @@ template <int D>
 __device__ inline float add_lane(float v) {
   return v + __uint_as_float(other_lane<D>(__float_as_uint(v)));
 }
-__device__ inline float wave_sum(float v) {
-  return add_lane<32>(add_lane<16>(add_lane<8>(add_lane<4>(add_lane<2>(add_lane<1>(v))))));
-}
 // the largest of each aligned run of `lanes` lanes (4 to 64)
 __device__ inline uint32_t wave_max(uint32_t v, int lanes = 64) {
   v = max(v, other_lane<1>(v));

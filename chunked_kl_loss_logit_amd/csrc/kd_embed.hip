@@ -191,7 +191,6 @@ __global__ __launch_bounds__(kTiedT) void embed_tied_kernel(EmbedArgs a, int blo
   __shared__ uint32_t seen[16 * 65], sums[16];
   __shared__ uint32_t order[kTiedT];
   __shared__ __attribute__((aligned(16))) Bits tile[kTiedT * kLd];
-  const int lane = threadIdx.x & 63, w = wave_id();
   const int logical = xcd_remap(blockIdx.x, gridDim.x);
   const int64_t t0 = (int64_t)(logical % blocks_t) * kTiedT, k0 = (int64_t)(logical / blocks_t) * ROWS;
   constexpr uint32_t kNone = 0xfffffffeu, kOutside = 0xffffffffu;  // masked or behind the last one; no such token
