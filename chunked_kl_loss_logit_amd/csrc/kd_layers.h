@@ -116,7 +116,8 @@ struct NormGradArgs {
 };
 int norm_grad_blocks(int64_t T, int64_t d);
 hipError_t launch_norm_grad(const NormGradArgs& a, hipStream_t st);
-hipError_t launch_norm_sum(const NormGradArgs& a, hipStream_t st);  // dw and db from the partials
+// dw and db from the partials, and masked rows of dx that weights which are not finite have spoilt
+hipError_t launch_norm_sum(const NormGradArgs& a, hipStream_t st);
 
 // ---------------------------------------------------------------- product of 8-bit integers
 struct Int8Args {

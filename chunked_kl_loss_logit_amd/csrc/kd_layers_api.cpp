@@ -364,7 +364,7 @@ kd_status kd_layer_norm_bwd(const void* grad, const void* x, const void* weight,
   a.blocks = kd::norm_grad_blocks(T, d);
   hipStream_t st = static_cast<hipStream_t>(stream);
   KD_LAUNCH("layer_norm_grad", st, kd::launch_norm_grad(a, st));
-  if (dweight || dbias) KD_LAUNCH("layer_norm_sum", st, kd::launch_norm_sum(a, st));
+  if (dweight || dbias || (dx && weight && mask)) KD_LAUNCH("layer_norm_sum", st, kd::launch_norm_sum(a, st));
   return KD_OK;
 }
 

@@ -96,9 +96,8 @@ __global__ __launch_bounds__(RowTeam<R>::kThreads, K > 1 && R == 64 ? 3 : 4) voi
   Input<TY, KIND> xr[K], xn[K];
   Raw8<TY> gr[K], gn[K];
   float mean = 0.f, rstd = 0.f;
-  bool there = false;
   auto load = [&](int64_t row) {  // masked rows and those behind the last one as zeros
-    there = row < a.T && row_valid(a.mask, row);
+    const bool there = row < a.T && row_valid(a.mask, row);
     mean = there ? a.mean[row] : 0.f;
     rstd = there ? a.rstd[row] : 0.f;
 #pragma unroll
@@ -109,25 +108,11 @@ __global__ __launch_bounds__(RowTeam<R>::kThreads, K > 1 && R == 64 ? 3 : 4) voi
       gn[k] = load8<TY, WHOLE>(a.grad + (row * a.d + 8 * (int64_t)p) * Elem<TY>::kBytes, n, p > 0);
     }
   };
-  // A masked row's dx: as its grad counts as 0, it comes out 0 by itself unless a weight is not finite.  Rows of
-  // several waves are cleared instead of worked on; where a workgroup has several rows, a branch in the loop took 130 ->
-  // 148 us (400000 x 136 bf16, a tenth masked; 120000 x 520 197 -> 208), so that they are cleared after it, for such
-  // weights only.
-  auto clear = [&](int64_t row) {
-    const float zero[8] = {};
-    if (a.dx)
-#pragma unroll
-      for (int k = 0; k < K; ++k) {
-        const int64_t at = 8 * (int64_t)(lane + k * R);
-        store8<TY, WHOLE>(a.dx + (row * a.d + at) * Elem<TY>::kBytes, zero, (int)(a.d - at));
-      }
-  };
   if constexpr (kAhead) load(t);
   for (; t < a.T; t += step) {
     if constexpr (!kAhead) load(t);
     char* out = a.dx ? a.dx + t * a.d * Elem<TY>::kBytes : nullptr;
     const float m = mean, r = rstd;
-    const bool valid = there;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int p = lane + k * R, n = (int)(a.d - 8 * (int64_t)p);
@@ -137,10 +122,6 @@ __global__ __launch_bounds__(RowTeam<R>::kThreads, K > 1 && R == 64 ? 3 : 4) voi
       settle8<TY, WHOLE>(gr[k], n, p > 0);
     }
     if constexpr (kAhead) load(t + step);  // the next row, while this one is worked on
-    if (R > 64 && !valid) {
-      clear(t);
-      continue;
-    }
     auto weights = [&](int k) {
       if constexpr (kLds) {
 #pragma unroll
@@ -185,18 +166,6 @@ __global__ __launch_bounds__(RowTeam<R>::kThreads, K > 1 && R == 64 ? 3 : 4) voi
       for (int i = 0; i < 8; ++i) g[i] = r * fmaf(-h[i], c1, g[i] * w[k][i] - c0);
       store8<TY, WHOLE>(out + at * Elem<TY>::kBytes, g, (int)(a.d - at));
     }
-  }
-  if constexpr (R <= 64) {  // the row's weights are among those of the wave's lanes
-    uint32_t top = 0;
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      if constexpr (K > 1)
-        if (a.w) load_any(a.w, a.wtype, a.d, lane + k * R, w[k]);
-      top = max(top, top8(w[k]));
-    }
-    if (__any(top >= 0x7f800000u))
-      for (t = (int64_t)blockIdx.x * Team::kRows + Team::slot(); t < a.T; t += step)
-        if (!row_valid(a.mask, t)) clear(t);
   }
   if (!a.dw && !a.db) return;
   // one partial row of each sum per workgroup; waves that hold a row each are added up first
@@ -296,12 +265,36 @@ __global__ __launch_bounds__(1024) void norm_grad_long_kernel(NormGradArgs a) {
   }
 }
 
+namespace {
+// A masked row's dx comes out of the kernel above as 0, since its grad counts as
+// 0, unless a weight is not finite: then the masked rows are cleared here.
+// (With the mask looked at for each row in that kernel, it took up to a tenth longer.)
+__device__ inline void clear_masked(const NormGradArgs& a) {
+  const int pieces = (int)((a.d + 7) / 8);
+  uint32_t top = 0;
+  for (int p = threadIdx.x; p < pieces; p += 1024) {
+    float w[8];
+    load_any(a.w, a.wtype, a.d, p, w);
+    top = max(top, top8(w));
+  }
+  if (!__syncthreads_or(top >= 0x7f800000u)) return;
+  const int bytes = a.type == kTypeF32 ? 4 : 2;
+  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+    if (row_valid(a.mask, t)) continue;
+    uint16_t* row = reinterpret_cast<uint16_t*>(a.dx + t * a.d * bytes);
+    for (int64_t i = threadIdx.x; i < a.d * bytes / 2; i += 1024) row[i] = 0;
+  }
+}
+}  // namespace
+
 // dw and db from the workgroups' partial rows: 64 columns a workgroup, the
 // partial rows dealt to 16 waves, eight loads of a wave in flight, and the
-// waves' sums added up through LDS.
-__global__ __launch_bounds__(1024) void norm_sum_kernel(NormGradArgs a) {
+// waves' sums added up through LDS.  first + blockIdx.y: dw, db, the masked rows.
+template <bool MASKED>
+__global__ __launch_bounds__(1024) void norm_sum_kernel(NormGradArgs a, int first) {
   __shared__ float col[16][64];
-  const int which = blockIdx.y;
+  const int which = first + blockIdx.y;
+  if (MASKED && which == 2) return clear_masked(a);
   const int64_t c = (int64_t)blockIdx.x * 64 + (threadIdx.x & 63);
   const int w = threadIdx.x >> 6;
   float v = 0.f;
@@ -355,7 +348,11 @@ hipError_t launch_norm_grad(const NormGradArgs& a, hipStream_t st) {
 }
 
 hipError_t launch_norm_sum(const NormGradArgs& a, hipStream_t st) {
-  hipLaunchKernelGGL(norm_sum_kernel, dim3((unsigned)((a.d + 63) / 64), 2), dim3(1024), 0, st, a);
+  const bool sums = a.dw || a.db, masked = a.dx && a.w && a.mask && a.d <= kRowMost;
+  if (!sums && !masked) return hipSuccess;
+  const dim3 grid((unsigned)((a.d + 63) / 64), 2 * sums + masked);
+  if (masked) hipLaunchKernelGGL((norm_sum_kernel<true>), grid, dim3(1024), 0, st, a, sums ? 0 : 2);
+  else hipLaunchKernelGGL((norm_sum_kernel<false>), grid, dim3(1024), 0, st, a, 0);
   return hipGetLastError();
 }
 

@@ -176,7 +176,10 @@ def test_masked_rows_get_no_gradient_whatever_the_weight_holds(d, kept):
         w = torch.ones(d, dtype=dtype, device="cuda")
         w[d // 2], w[d - 1] = float("inf"), float("nan")
         y, mean, rstd, k = kd.layer_norm_forward(x, w, None, mask, checkpoint=kept)
-        dx, dw, db = kd.layer_norm_backward(torch.randn(T, d, device="cuda").to(dtype), None if k else x, w, mask, mean, rstd, k)
+        args = (torch.randn(T, d, device="cuda").to(dtype), None if k else x, w, mask, mean, rstd, k)
+        dx, dw, db = kd.layer_norm_backward(*args)
         off = mask == 0
+        alone = kd.layer_norm_backward(*args, want=(True, False, False))[0]
+        assert torch.equal(alone[off], dx[off])
         assert bool((y[off] == 0).all()) and bool((dx[off] == 0).all())
         assert bool(dx[~off].isnan().all()) and bool(dw.isfinite().all()) and bool(db.isfinite().all())
