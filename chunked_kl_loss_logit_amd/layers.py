@@ -127,11 +127,15 @@ class _Surroundings:
     states."""
 
     def __init__(self, x, others):
-        self.autocast = [dict(device_type=d, dtype=torch.get_autocast_dtype(d), enabled=torch.is_autocast_enabled(d),
-                              cache_enabled=torch.is_autocast_cache_enabled()) for d in {x.device.type, "cpu"}]
+        self.autocast = [self._autocast(d) for d in {x.device.type, "cpu"}]
         self.states = [] if _capturing() else self._states(
             [torch.default_generator, *(torch.cuda.default_generators if torch.cuda.is_initialized() else ()),
              *(g for g in others if isinstance(g, torch.Generator))])
+
+    @staticmethod
+    def _autocast(device_type):
+        return dict(device_type=device_type, dtype=torch.get_autocast_dtype(device_type),
+                    enabled=torch.is_autocast_enabled(device_type), cache_enabled=torch.is_autocast_cache_enabled())
 
     @staticmethod
     def _states(generators):
@@ -156,7 +160,8 @@ class _Surroundings:
         """As it was then; afterwards as it is now."""
         with contextlib.ExitStack() as stack:
             for settings in self.autocast:
-                stack.enter_context(torch.autocast(**settings))
+                if settings != self._autocast(settings["device_type"]):
+                    stack.enter_context(torch.autocast(**settings))
             if _capturing():
                 stack.enter_context(_NoDraws())
             else:
