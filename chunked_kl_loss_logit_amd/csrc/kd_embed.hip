@@ -4,8 +4,8 @@
 //
 // Forward: a copy of rows, or for tied weights a gather of columns.  Bound by
 // memory: 16384 rows of 2048 bf16 from a table of 128256 17-28 us (134 MB); tied,
-// 4096 of 128256 columns of 2048 rows 35 us, cold 42 (some 236 MB of cache
-// lines for 17 MB of elements).
+// 4096 of 128256 columns of 2048 rows 37 us, from cold lines 44 (tokens as frequent
+// as in text: 212 MB of cache lines for 17 MB of elements; spread evenly 94, 459 MB).
 //
 // Backward: rows that meet in one token are added up without atomics.  The
 // positions are sorted by token (stable, so in ascending order within one);
@@ -179,7 +179,10 @@ __device__ inline uint32_t place_in_block(uint32_t digit, uint32_t* seen, uint32
 // The elements are turned in LDS and written in runs of ROWS, each to its
 // token's row.  Workgroups of the same rows of W run on one XCD.  Up to
 // kTiedFew tokens, 64 to a workgroup and unsorted, sorting costs more than it
-// saves.
+// saves.  us, unsorted / sorted, cold W, bf16: d 2048, V 128256, T 128 7 / 12, 512 12 /
+// 16, 700 16 / 18, 1024 21 / 21, 2048 42 / 37; V 32000, T 512 11 / 14, 1024 20 / 18,
+// 2048 34 / 29; d 512, V 32000, T 512 7 / 12, 2048 9 / 13.  (Between 512 and 1024 the
+// unsorted one would still be 2 us ahead, at small d beyond that too.)
 constexpr int kTiedT = 1024;
 constexpr int64_t kTiedFew = 512;
 
@@ -785,7 +788,11 @@ __global__ __launch_bounds__(256) void fill_table_kernel(char* p, int64_t bytes)
   if (tail < bytes) *reinterpret_cast<uint16_t*>(p + tail) = 0;
 }
 
-// Entries of a piece (up to as many tokens need no joining).
+// Entries of a piece (up to as many tokens need no joining): short ones while
+// there are few waves, long ones where the partial rows cost more.  us of the
+// gradient, 16 / 64, bf16: V 128256, d 2048, T 4096 117 / 122, 16384 138 / 136, 32768
+// 176 / 168, 131072 338 / 310; V 32000, d 512, T 4096 25 / 38, 16384 32 / 42, 32768 51 /
+// 57, 65536 92 / 88, 131072 124 / 106.
 int embed_piece(int64_t T) { return T <= 16384 ? 16 : 64; }
 
 namespace {

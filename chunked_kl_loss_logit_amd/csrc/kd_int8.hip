@@ -350,12 +350,13 @@ __global__ __launch_bounds__(64 * W) void int8_few_kernel(Int8Args a) {
 }
 
 // ------------------------------------------------------------------ launches
-// Rounds of the chip's 256 CUs: a tile takes 48 us at d = 4096, a workgroup of
+// Rounds of the chip's 256 CUs: a tile takes 46 us at d = 4096, a workgroup of
 // the other kernel with 128 rows 28 us, one of them a CU.  Either side, us at
-// d = 4096: V 32000, T 96 50 / 51, 128 50 / 59, 512 66 / 118; V 11008, T 128
-// 43 / 29, 192 43 / 50, 512 47 / 85; V 4096, T 512 45 / 28, 1024 48 / 55.  Up to
+// d = 4096: V 32000, T 96 45 / 51, 128 45 / 58, 512 68 / 222; V 11008, T 128
+// 44 / 30, 192 44 / 50, 512 48 / 85; V 4096, T 512 46 / 31, 1024 48 / 57.  Up to
 // 64 rows the other kernel has two or three workgroups a CU and waits for w
-// only: V 128256, T 32 149 / 123, 64 153 / 160.
+// only: T 32, V 32000 46 / 27, V 128256 143 / 123; T 64, V 11008 42 / 20, V 32000 45 /
+// 36, but V 128256 143 / 160: for the largest heads the border lies a little high.
 bool int8_tiles(int64_t T, int64_t d, int64_t V) {
   auto rounds = [](int64_t workgroups) { return (workgroups + 255) / 256; };
   const int64_t tile = rounds(((T + 255) / 256) * ((V + 255) / 256)), few = rounds(((T + 127) / 128) * ((V + 63) / 64));

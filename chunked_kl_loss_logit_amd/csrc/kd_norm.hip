@@ -7,11 +7,11 @@
 // from the load to the store, the variance is taken around the mean (not as a
 // difference of two moments, which loses everything where the mean is large),
 // and a workgroup goes over many rows, so that weight and bias are read once
-// per workgroup.  One piece of 8 elements a thread, so that there are enough
-// waves: 16384 x 4096 bf16 with two pieces took 51 us, so 46 (268 MB, 5.8 TB/s).
-// Beyond 4096 elements three or two, as 16 waves at one barrier cost more: 8192 x
-// 8192 bf16 with one 50 us, so 46, and with its copy in 8 bits 82 and 77 (335 MB);
-// 14563 x 4608 58 and 47, 119 and 85.  Narrow rows share a workgroup, by the
+// per workgroup.  Up to 4096 elements one piece of 8 a thread (16384 x 4096 bf16 in
+// turn from four inputs 51 us, 268 MB at 5.2 TB/s, with two pieces the same; with its
+// copy in 8 bits 67 both ways).  Beyond that three or two, as 16 waves at one
+// barrier cost more: 8192 x 8192 with one 55 us, so 51, and with the copy 77 and 73
+// (335 MB); 14563 x 4608 69 and 49, 95 and 81.  Narrow rows share a workgroup, by the
 // smallest shape that holds them: 67 M values in rows of 136 116 us in whole
 // waves, 67 in halves; of 520 in four waves 110, in two 67.
 #include <type_traits>
@@ -48,8 +48,8 @@ __device__ inline void keep_piece(const NormArgs& a, int64_t t, int64_t d, int p
 
 // ------------------------------------------------------------------ forward
 // The thread's weights and biases: in registers, or in LDS where the 8-bit copy
-// takes the registers: 8192 x 8192 bf16 with its copy in registers 168 us, in LDS
-// 82; without a copy LDS costs 46 -> 56.
+// takes the registers: with the copy, in registers / in LDS, 16384 x 4096 bf16 106 /
+// 67 us, 14563 x 4608 150 / 81, 8192 x 8192 74 / 73; without one 52 / 53, 49 / 58, 51 / 55.
 template <bool LDS, int N>
 struct Affine {
   float w[N][8], b[N][8];

@@ -39,7 +39,9 @@ extern "C" {
  * out[t] = scale E[tokens[t]], rounded once to the table's type dt.  The table
  * is E [V,d] (tied = 0), or the head W [d,V] of the losses (tied = 1), token
  * v's embedding then being its column v.  Masked rows get zeros.  A valid
- * token outside [0, V) gets a row of NaN.
+ * token outside [0, V) gets a row of NaN.  A vocabulary shard [v0, v0 + Vs)
+ * takes tokens - v0 and a mask of the rows whose tokens are its own; the shards'
+ * outputs add up to the whole head's, and the backward call needs the same two.
  * tokens [T] int32; out [T,d] of type dt. */
 kd_status kd_embedding_fwd(const int32_t* tokens, const void* table, const uint8_t* mask, float scale, int64_t T,
                            int64_t V, int64_t d, kd_dtype dt, int32_t tied, void* out, void* stream);
