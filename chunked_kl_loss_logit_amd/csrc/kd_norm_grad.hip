@@ -8,7 +8,7 @@
 // over rows for dw and db stay in the registers of the threads that own those
 // columns; each workgroup leaves one partial row of each, which a second
 // kernel adds up in a fixed order.  16384 x 4096 bf16: 77 us (403 MB, 5.2 TB/s;
-// a large copy reaches 5.1) and 5 us for the sums; 8192 x 8192 from 8 bits 76.
+// a large copy reaches 5.1) and 5 us for the sums; 8192 x 8192 from 8 bits 76-79.
 #include <type_traits>
 
 #include "kd_launch.h"

@@ -1,7 +1,7 @@
 // Rows in 8 bits and back (kd_rows8.h has the rounding).
 //
 // Bound by memory: 3 bytes a value of a 16-bit type each way (16384 x 4096 bf16
-// in groups of 128 35-40 us to int8, 30 back, part of it from the last-level cache).  A lane holds 8
+// in groups of 128 35-41 us to int8, 30 back, part of it from the last-level cache).  A lane holds 8
 // consecutive values; a group of 32 to 512 values is then 4 to 64 neighbouring
 // lanes of one wave, which find its largest by shuffles.  Where a row is one
 // group, it is held in registers as for layer norm.
